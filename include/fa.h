@@ -48,7 +48,9 @@ typedef enum fa_status {
   FA_ERR_BOUNDS = 6       /* device: a page id or sequence length was out of range */
 } fa_status;
 
-typedef enum fa_dtype { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2 } fa_dtype;
+/* FA_E4M3 is the element type of an 8-bit paged cache (fa_cache_append and the calls that read
+ * it); no other call takes it. */
+typedef enum fa_dtype { FA_BF16 = 0, FA_FP16 = 1, FA_FP32 = 2, FA_E4M3 = 3 } fa_dtype;
 
 /*
  * Dense attention (prefill of a query chunk against a KV cache), bf16.
@@ -354,6 +356,107 @@ int gated_delta_prefill(const gated_delta_args* args, void* stream);
 
 /* Workspace bytes gated_delta_prefill needs for these sizes (pointers are not read). */
 size_t gated_delta_workspace_size(const gated_delta_args* args);
+
+/*
+ * Rotary positions on the queries and keys of a step (either may be absent: Hq or Hk = 0).
+ * Pair i of a row, at angle theta_i = position * inv_freq[i]:
+ *     y_a = amplitude * (x_a cos theta_i - x_b sin theta_i)
+ *     y_b = amplitude * (x_b cos theta_i + x_a sin theta_i)
+ * with (a, b) = (i, rot_dim/2 + i), or (2i, 2i + 1) when interleaved; columns from rot_dim on
+ * are copied.  transpose = 1 applies the transposed map (the angle's sign turned), which is
+ * the gradient: dx = fa_rotary(dy) with transpose = 1.
+ *   q [B, Hq, T, D], k [B, Hk, T, D] in dtype (FA_BF16, FA_FP16, FA_FP32), any strides (in
+ *   elements: batch, head, token; the last dimension is contiguous) that are multiples of 16
+ *   bytes; q_out, k_out likewise, and may be the inputs themselves (same pointer and strides);
+ *   any other overlap is not allowed;
+ *   positions [B, T] int32;  inv_freq [rot_dim / 2] fp64 (scaled frequencies for long contexts
+ *   are the caller's table, their amplitude the argument): the angle is reduced exactly, so
+ *   positions may be as large as int32 holds.
+ *   D a multiple of 8; rot_dim a multiple of 16, at most min(D, 512).
+ * Computed in fp32, rounded once to dtype.
+ */
+typedef struct fa_rotary_args {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+  const int32_t* positions;
+  const double* inv_freq;
+  int B, T, Hq, Hk, D, rot_dim;
+  int interleaved, transpose;
+  float amplitude;
+  fa_dtype dtype;
+} fa_rotary_args;
+
+int fa_rotary(const fa_rotary_args* args, void* stream);
+
+/*
+ * Writes a step's keys and values into a paged cache (the layout of fa_decode_paged).
+ *   k, v [B, Hkv, T, D] in dtype, strides as in fa_rotary;
+ *   k_pages, v_pages [num_pages, Hkv, page_size, D] in cache_dtype;
+ *   page_table [B, max_pages] int32; seq_lens [B] int32: tokens of each sequence, the new ones
+ *   included; new_lens [B] int32 or NULL (= T each): sequence b's first new_lens[b] tokens go to
+ *   its positions seq_lens[b] - new_lens[b] and on, its other rows are not read.
+ * Every other slot of the pages is left as it was.  The slots written in one call have to be
+ * different ones: a page belongs to one sequence of the batch (one that two sequences write at
+ * the same slot holds parts of either row).
+ * cache_dtype = dtype (FA_BF16, FA_FP16): the values.  cache_dtype = FA_E4M3: a row (one token
+ * of one head) is stored as e4m3 values times 2^e, e the least integer >= -126 with
+ * max |x| <= 448 * 2^e over the row's finite elements, rounded to nearest even; the byte
+ * k_scales / v_scales [num_pages, Hkv, page_size] holds e + 127 (the scale as an 8-bit
+ * exponent).  An infinity is stored as +-448, a NaN as NaN.
+ * inv_freq given: the keys are rotated as fa_rotary does, at positions [B, T] (or, when NULL, at
+ * the position in the cache), in fp32, before their one rounding.
+ *   D in {64, 128, 256}; page_size a power of two; rot_dim a multiple of 16, at most D.
+ * A length or page id out of range sets FA_ERR_BOUNDS in the device status word; the token is
+ * then not written.
+ */
+typedef struct fa_cache_append_args {
+  const void* k;
+  const void* v;
+  int64_t k_strides[3], v_strides[3];
+  void* k_pages;
+  void* v_pages;
+  uint8_t* k_scales;
+  uint8_t* v_scales;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* new_lens;
+  const int32_t* positions;
+  const double* inv_freq;
+  int B, T, Hkv, D, page_size, max_pages, num_pages;
+  int rot_dim, interleaved;
+  float amplitude;
+  fa_dtype dtype;
+  fa_dtype cache_dtype;
+} fa_cache_append_args;
+
+int fa_cache_append(const fa_cache_append_args* args, void* stream);
+
+/*
+ * Reads a paged cache back as dense keys and values: k, v [B, Hkv, max_seq_len, D] in dtype
+ * (FA_BF16, FA_FP16, FA_FP32), contiguous; rows at and past seq_lens[b] are set to zero.
+ * cache_dtype FA_BF16, FA_FP16 or FA_E4M3 (then with the scales of fa_cache_append; value *
+ * 2^(byte - 127), rounded to dtype).  D in {64, 128, 256}; page_size a power of two.
+ * A length outside [0, max_seq_len] or a page id out of range sets FA_ERR_BOUNDS in the device
+ * status word; the rows concerned are then zero.
+ */
+typedef struct fa_cache_gather_args {
+  const void* k_pages;
+  const void* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  void* k;
+  void* v;
+  int B, Hkv, D, page_size, max_pages, num_pages, max_seq_len;
+  fa_dtype dtype;
+  fa_dtype cache_dtype;
+} fa_cache_gather_args;
+
+int fa_cache_gather(const fa_cache_gather_args* args, void* stream);
 
 /*
  * Merge of attention states over disjoint key sets (the split-KV combine):

@@ -10,10 +10,14 @@ Entry points (same names as the C ABI):
     fa_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len, scale)
     mla_decode_paged(q_nope, q_pe, ckv, kpe, page_table, seq_lens, max_seq_len, scale)
     fa_merge_states(o_parts, lse_parts, n_splits=None, out_dtype=torch.bfloat16)
+    fa_rotary(q, k, positions, inv_freq, ...)                rotary positions (and their gradient)
+    fa_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, ...)   16-bit or e4m3 pages
+    fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len, ...)
     fa_get_device_status()
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -26,7 +30,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libfa.so")
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_WORKSPACE, FA_ERR_CUDA, FA_ERR_TIMEOUT, \
     FA_ERR_BOUNDS = range(7)
-FA_BF16, FA_FP16, FA_FP32 = 0, 1, 2
+FA_BF16, FA_FP16, FA_FP32, FA_E4M3 = 0, 1, 2, 3
 _DT = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16, torch.float32: FA_FP32}
 
 # Every symbol include/fa.h declares.
@@ -40,6 +44,7 @@ EXPORTS = (
     "mla_decode_chunk_tokens", "mla_decode_paged_states", "mla_decode_paged_ex", "fa_merge_states",
     "fa_get_device_status", "fa_selftest_wait_timeout", "fa_last_error", "fa_version",
     "gated_delta_prefill", "gated_delta_workspace_size",
+    "fa_rotary", "fa_cache_append", "fa_cache_gather",
 )
 
 
@@ -112,6 +117,48 @@ class GatedDeltaArgs(ctypes.Structure):
     ]
 
 
+_Strides = ctypes.c_int64 * 3
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p), ("q_strides", _Strides), ("k_strides", _Strides),
+        ("q_out_strides", _Strides), ("k_out_strides", _Strides),
+        ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+        ("D", ctypes.c_int), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+        ("transpose", ctypes.c_int), ("amplitude", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_strides", _Strides),
+        ("v_strides", _Strides), ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float),
+        ("dtype", ctypes.c_int), ("cache_dtype", ctypes.c_int),
+    ]
+
+
+class CacheGatherArgs(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+        ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int), ("num_pages", ctypes.c_int),
+        ("max_seq_len", ctypes.c_int), ("dtype", ctypes.c_int), ("cache_dtype", ctypes.c_int),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -177,6 +224,12 @@ def load_library(path: str | None = None):
         lib.gated_delta_prefill.argtypes = [ctypes.POINTER(GatedDeltaArgs), _vp]
         lib.gated_delta_workspace_size.restype = _sz
         lib.gated_delta_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaArgs)]
+        lib.fa_rotary.restype = _i
+        lib.fa_rotary.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
+        lib.fa_cache_append.restype = _i
+        lib.fa_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs), _vp]
+        lib.fa_cache_gather.restype = _i
+        lib.fa_cache_gather.argtypes = [ctypes.POINTER(CacheGatherArgs), _vp]
         _lib = lib
         return lib
 
@@ -598,3 +651,203 @@ def gated_delta_prefill(q, k, v, g, beta, *, scale=None, initial_state=None, out
         a.workspace_bytes = ws.numel() * ws.element_size()
     _check(lib.gated_delta_prefill(ctypes.byref(a), _stream(stream)))
     return out, final_state
+
+
+# ------------------------------------------------------------------------------------------
+# The serving step around the paged cache.  These calls take strided inputs, run on the
+# tensors' own device whichever device is current, and allocate what they return (and any
+# workspace) on the stream they launch on.
+# ------------------------------------------------------------------------------------------
+_CACHE_DT = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16, torch.float8_e4m3fn: FA_E4M3}
+
+
+class _Scope:
+    """The device of a call's tensors and the stream it launches on, made current."""
+
+    def __init__(self, device, stream):
+        self.device = torch.cuda.device(device)
+        self.stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self.device.__enter__()
+        self.stream.__enter__()
+
+    def __exit__(self, *exc):
+        self.stream.__exit__(*exc)
+        self.device.__exit__(*exc)
+
+
+_here = contextlib.nullcontext()
+
+
+def _scope(device, stream):
+    if stream is None:
+        return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return _Scope(device, stream)
+
+
+def _current_stream(device):
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _check_side(device, contiguous=(), rows=()):
+    """Every tensor on `device`; `contiguous` ones whole, `rows` with a contiguous last
+    dimension (their other strides go to the call)."""
+    for t in contiguous:
+        if t is not None and (t.device != device or not t.is_contiguous()):
+            raise ValueError("tensors must be contiguous CUDA tensors on one device")
+    for t in rows:
+        if t is not None and (t.device != device or (t.stride(-1) != 1 and t.shape[-1] > 1)):
+            raise ValueError("tensors must be CUDA tensors on one device with a contiguous last "
+                             "dimension")
+
+
+def _shape(name, t, *want):
+    if t is not None and tuple(t.shape) != want:
+        raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
+
+
+def _cuda_device(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return t.device
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _row_strides(t):
+    # the stride of a dimension of one element is never used: torch may report anything there
+    s, n = t.stride(), t.shape
+    return _Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+
+
+_NO_STRIDES = _Strides(0, 0, 0)
+
+
+def fa_rotary(q, k, positions, inv_freq, *, amplitude: float = 1.0, interleaved: bool = False,
+              transpose: bool = False, q_out=None, k_out=None, stream=None):
+    """Rotary positions on q [B,Hq,T,D] and k [B,Hk,T,D] (k may be None), bf16, fp16 or fp32,
+    any strides with a contiguous last dimension; positions [B,T] int32; inv_freq [rot_dim/2]
+    fp64: the first rot_dim columns of each head are rotated, in the half layout or interleaved,
+    the rest copied.  transpose=True applies the transposed map, the gradient of the call.  q_out
+    and k_out may be q and k themselves.  Returns (q_out, k_out)."""
+    lib = load_library()
+    dev = _cuda_device(q)
+    B, Hq, T, D = q.shape
+    Hk = 0
+    _need_dtype(q.dtype, k, q_out, k_out)
+    _need_dtype(torch.int32, positions)
+    _need_dtype(torch.float64, inv_freq)
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    if k is not None:
+        Hk = k.shape[1]
+        _shape("k", k, B, Hk, T, D)
+        _shape("k_out", k_out, B, Hk, T, D)
+    _shape("q_out", q_out, B, Hq, T, D)
+    _shape("positions", positions, B, T)
+    _check_side(dev, (positions, inv_freq), (q, k, q_out, k_out))
+    with _scope(dev, stream):
+        if q_out is None:
+            q_out = torch.empty((B, Hq, T, D), dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty((B, Hk, T, D), dtype=q.dtype, device=dev)
+        a = RotaryArgs(q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), _row_strides(q),
+                       _NO_STRIDES if k is None else _row_strides(k), _row_strides(q_out),
+                       _NO_STRIDES if k is None else _row_strides(k_out), positions.data_ptr(),
+                       inv_freq.data_ptr(), B, T, Hq, Hk, D, 2 * inv_freq.numel(),
+                       interleaved, transpose, amplitude, _DT[q.dtype])
+        _check(lib.fa_rotary(ctypes.byref(a), _current_stream(dev)))
+    return q_out, k_out
+
+
+def _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B):
+    """(num_pages, Hkv, page_size, D) of a paged cache, its tensors checked."""
+    if k_pages.dtype not in _CACHE_DT:
+        raise ValueError(f"pages must be bfloat16, float16 or float8_e4m3fn, got {k_pages.dtype}")
+    _need_dtype(k_pages.dtype, v_pages)
+    _need_dtype(torch.int32, page_table)
+    shape = tuple(k_pages.shape)
+    if len(shape) != 4:
+        raise ValueError(f"pages must be [num_pages, Hkv, page_size, D], got {shape}")
+    _shape("v_pages", v_pages, *shape)
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(page_table.shape)}")
+    if k_pages.dtype == torch.float8_e4m3fn:
+        if k_scales is None or v_scales is None:
+            raise ValueError("an 8-bit cache needs k_scales and v_scales")
+        _need_dtype(torch.uint8, k_scales, v_scales)
+        _shape("k_scales", k_scales, *shape[:3])
+        _shape("v_scales", v_scales, *shape[:3])
+    elif k_scales is not None or v_scales is not None:
+        raise ValueError("scales belong to an 8-bit cache")
+    _check_side(dev, (k_pages, v_pages, k_scales, v_scales, page_table))
+    return shape
+
+
+def fa_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, *, new_lens=None, k_scales=None,
+                    v_scales=None, inv_freq=None, amplitude: float = 1.0,
+                    interleaved: bool = False, positions=None, stream=None) -> None:
+    """Write a step's k, v [B,Hkv,T,D] (any strides with a contiguous last dimension) into the
+    pages [num_pages,Hkv,page_size,D]: in k's 16-bit type, or quantised (float8_e4m3fn pages,
+    k_scales and v_scales [num_pages,Hkv,page_size] uint8).  seq_lens [B] int32 (device) counts
+    the new tokens; sequence b has new_lens[b] of them (default T), its first rows.  With inv_freq
+    [rot_dim/2] fp64 the keys are rotated on the way, at positions [B,T] int32 (default: the
+    position in the cache)."""
+    lib = load_library()
+    dev = _cuda_device(k)
+    B, Hkv, T, D = k.shape
+    if k.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {k.dtype}")
+    _need_dtype(k.dtype, v)
+    _need_dtype(torch.int32, seq_lens, new_lens, positions)
+    _need_dtype(torch.float64, inv_freq)
+    _shape("v", v, B, Hkv, T, D)
+    _shape("seq_lens", seq_lens, B)
+    _shape("new_lens", new_lens, B)
+    _shape("positions", positions, B, T)
+    P, _, ps, _ = _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B)
+    _shape("k_pages", k_pages, P, Hkv, ps, D)
+    _check_side(dev, (seq_lens, new_lens, positions, inv_freq), (k, v))
+    with _scope(dev, stream):
+        a = CacheAppendArgs(k.data_ptr(), v.data_ptr(), _row_strides(k), _row_strides(v),
+                            k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales),
+                            _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
+                            _addr(new_lens), _addr(positions), _addr(inv_freq), B, T, Hkv, D, ps,
+                            page_table.shape[1], P, 0 if inv_freq is None else 2 * inv_freq.numel(),
+                            interleaved, amplitude, _DT[k.dtype], _CACHE_DT[k_pages.dtype])
+        _check(lib.fa_cache_append(ctypes.byref(a), _current_stream(dev)))
+
+
+def fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len: int, *,
+                    dtype=torch.bfloat16, k_scales=None, v_scales=None, k=None, v=None,
+                    stream=None):
+    """Read a paged cache (bf16, fp16, or float8_e4m3fn with its scales) back as dense k, v
+    [B,Hkv,max_seq_len,D] in dtype; rows at and past seq_lens[b] are zero."""
+    lib = load_library()
+    dev = _cuda_device(k_pages)
+    B, L = seq_lens.shape[0], int(max_seq_len)
+    if dtype not in _DT:
+        raise TypeError(f"unsupported dtype {dtype}")
+    _need_dtype(dtype, k, v)
+    _need_dtype(torch.int32, seq_lens)
+    _shape("seq_lens", seq_lens, B)
+    P, Hkv, ps, D = _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B)
+    _shape("k", k, B, Hkv, L, D)
+    _shape("v", v, B, Hkv, L, D)
+    _check_side(dev, (seq_lens, k, v))
+    with _scope(dev, stream):
+        if k is None:
+            k = torch.empty((B, Hkv, L, D), dtype=dtype, device=dev)
+        if v is None:
+            v = torch.empty((B, Hkv, L, D), dtype=dtype, device=dev)
+        a = CacheGatherArgs(k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales),
+                            _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
+                            k.data_ptr(), v.data_ptr(), B, Hkv, D, ps, page_table.shape[1], P, L,
+                            _DT[dtype], _CACHE_DT[k_pages.dtype])
+        _check(lib.fa_cache_gather(ctypes.byref(a), _current_stream(dev)))
+    return k, v
