@@ -459,6 +459,62 @@ typedef struct fa_cache_gather_args {
 int fa_cache_gather(const fa_cache_gather_args* args, void* stream);
 
 /*
+ * Attention of a tree of drafted tokens over a paged cache, 16-bit or 8-bit (T = 1: decode over
+ * an 8-bit cache).  The drafted tokens are in the cache as each sequence's last n_b positions
+ * (n_b = draft_lens[b], or T); query i of sequence b, i < n_b, sees every earlier token of the
+ * sequence and the drafted token j, j < n_b, if bit j % 64 of
+ * tree_mask[b, i, j / 64] is set (a row without its own bit does not see itself):
+ *     s_j = scale * <q_i, k_j>,   out_i = sum_j softmax(s)_j v_j,   lse_i = ln sum_j e^{s_j}
+ *   q [B, Hq, T, D] in dtype (FA_BF16 or FA_FP16), strides (batch, head, token; elements, the
+ *     last dimension contiguous) positive multiples of 16 bytes
+ *   k_pages, v_pages [num_pages, Hkv, page_size, D] in cache_dtype: dtype, or FA_E4M3 with the
+ *     scales [num_pages, Hkv, page_size] that fa_cache_append writes (a value is e4m3 *
+ *     2^(byte - 127), byte <= 254, held in dtype: exact in bf16; in fp16 rounded to it, so
+ *     infinite beyond 65504)
+ *   page_table [B, max_pages] int32; seq_lens [B] int32, the drafted tokens included, each at
+ *     most max_seq_len (which sizes the KV split); draft_lens [B] int32 or NULL (= T each)
+ *   tree_mask [mask_batches, T, ceil(T / 64)] 64-bit words, mask_batches 1 or B; NULL = a
+ *     chain (query i sees the drafted tokens 0..i)
+ *   out [B, Hq, T, D] in dtype, lse [B, Hq, T] fp32 or NULL: contiguous.  A row that sees no
+ *     key, and the padding rows i >= n_b, get out = 0 and lse = -inf.
+ *   T <= 256; D in {64, 128, 256}; page_size a power of two in [8, 128] (at most 64 when
+ *   D = 256); Hq / Hkv <= 128.
+ * A drafted token takes no part in a row that does not see it, whatever it holds (infinities
+ * and NaN included).  num_splits: 0, or a forced KV split.
+ * workspace: fa_tree_workspace_size(args) bytes, 256-byte aligned (none when that is 0); calls
+ * that may overlap on the GPU need one each.
+ * A length outside [n_b, max_pages * page_size] (an empty sequence without draft_lens is none),
+ * an n_b outside [0, T] or a page id out of range sets FA_ERR_BOUNDS in the device status word;
+ * the sequence is then empty (of the page's keys, page 0's are read instead).
+ */
+typedef struct fa_tree_args {
+  const void* q;
+  int64_t q_strides[3];
+  const void* k_pages;
+  const void* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* draft_lens;
+  const uint64_t* tree_mask;
+  void* out;
+  float* lse;
+  int B, Hq, Hkv, T, D, page_size, max_pages, num_pages, max_seq_len, mask_batches;
+  int num_splits;
+  float scale;
+  fa_dtype dtype;
+  fa_dtype cache_dtype;
+  void* workspace;
+  size_t workspace_bytes;
+} fa_tree_args;
+
+int fa_tree_decode_paged(const fa_tree_args* args, void* stream);
+
+/* Workspace bytes of a call with these sizes on the current device (pointers are not read). */
+size_t fa_tree_workspace_size(const fa_tree_args* args);
+
+/*
  * Merge of attention states over disjoint key sets (the split-KV combine):
  *   lse = ln sum_s e^{lse_s},   out = sum_s e^{lse_s - lse} o_s
  *   o_parts [rows, max_splits, D] fp32 (normalised partial outputs), lse_parts

@@ -13,6 +13,7 @@ Entry points (same names as the C ABI):
     fa_rotary(q, k, positions, inv_freq, ...)                rotary positions (and their gradient)
     fa_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, ...)   16-bit or e4m3 pages
     fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len, ...)
+    fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len, tree_mask=...)
     fa_get_device_status()
 """
 from __future__ import annotations
@@ -45,6 +46,7 @@ EXPORTS = (
     "fa_get_device_status", "fa_selftest_wait_timeout", "fa_last_error", "fa_version",
     "gated_delta_prefill", "gated_delta_workspace_size",
     "fa_rotary", "fa_cache_append", "fa_cache_gather",
+    "fa_tree_decode_paged", "fa_tree_workspace_size",
 )
 
 
@@ -159,6 +161,23 @@ class CacheGatherArgs(ctypes.Structure):
     ]
 
 
+class TreeArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("q_strides", _Strides),
+        ("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p),
+        ("k_scales", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("draft_lens", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("T", ctypes.c_int),
+        ("D", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_seq_len", ctypes.c_int),
+        ("mask_batches", ctypes.c_int), ("num_splits", ctypes.c_int), ("scale", ctypes.c_float),
+        ("dtype", ctypes.c_int), ("cache_dtype", ctypes.c_int), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -230,6 +249,10 @@ def load_library(path: str | None = None):
         lib.fa_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs), _vp]
         lib.fa_cache_gather.restype = _i
         lib.fa_cache_gather.argtypes = [ctypes.POINTER(CacheGatherArgs), _vp]
+        lib.fa_tree_decode_paged.restype = _i
+        lib.fa_tree_decode_paged.argtypes = [ctypes.POINTER(TreeArgs), _vp]
+        lib.fa_tree_workspace_size.restype = _sz
+        lib.fa_tree_workspace_size.argtypes = [ctypes.POINTER(TreeArgs)]
         _lib = lib
         return lib
 
@@ -851,3 +874,54 @@ def fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len: int, *,
                             _DT[dtype], _CACHE_DT[k_pages.dtype])
         _check(lib.fa_cache_gather(ctypes.byref(a), _current_stream(dev)))
     return k, v
+
+
+def fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len: int, *,
+                         tree_mask=None, draft_lens=None, scale: float | None = None,
+                         k_scales=None, v_scales=None, num_splits: int = 0, out=None, lse=None,
+                         workspace=None, stream=None):
+    """Attention of a tree of drafted tokens, each sequence's last draft_lens[b] (default T)
+    tokens in the cache.  q [B,Hq,T,D] bf16 or fp16 (any strides with a contiguous last
+    dimension); pages [num_pages,Hkv,page_size,D] in q's dtype, or float8_e4m3fn with k_scales
+    and v_scales [num_pages,Hkv,page_size] uint8; seq_lens [B] int32 (device) counts the drafted
+    tokens; tree_mask [1 or B,T,ceil(T/64)] int64: bit j of row i = query i sees drafted token j
+    (None: a chain).  T = 1 is the decode of one token a sequence.  Returns (out [B,Hq,T,D], lse
+    [B,Hq,T] fp32)."""
+    lib = load_library()
+    dev = _cuda_device(q)
+    B, Hq, T, D = q.shape
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16, got {q.dtype}")
+    _need_dtype(q.dtype, out)
+    _need_dtype(torch.float32, lse)
+    _need_dtype(torch.int32, seq_lens, draft_lens)
+    _need_dtype(torch.int64, tree_mask)
+    _shape("seq_lens", seq_lens, B)
+    _shape("draft_lens", draft_lens, B)
+    _shape("out", out, B, Hq, T, D)
+    _shape("lse", lse, B, Hq, T)
+    P, Hkv, ps, Dk = _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B)
+    if Dk != D or (k_pages.dtype != q.dtype and k_scales is None):
+        raise ValueError(f"pages of {Dk} columns in {k_pages.dtype} do not go with q's {D} in {q.dtype}")
+    if tree_mask is not None and (tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, B) or
+                                  tuple(tree_mask.shape[1:]) != (T, -(-T // 64))):
+        raise ValueError(f"tree_mask must be [1 or {B}, {T}, {-(-T // 64)}], got {tuple(tree_mask.shape)}")
+    _check_side(dev, (seq_lens, draft_lens, tree_mask, out, lse, workspace), (q,))
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((B, Hq, T, D), dtype=q.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
+        a = TreeArgs(q.data_ptr(), _row_strides(q), k_pages.data_ptr(), v_pages.data_ptr(),
+                     _addr(k_scales), _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
+                     _addr(draft_lens), _addr(tree_mask), out.data_ptr(), lse.data_ptr(), B, Hq,
+                     Hkv, T, D, ps, page_table.shape[1], P, int(max_seq_len),
+                     0 if tree_mask is None else tree_mask.shape[0], int(num_splits),
+                     1.0 / math.sqrt(D) if scale is None else scale, _DT[q.dtype],
+                     _CACHE_DT[k_pages.dtype])
+        ws = _workspace(lib.fa_tree_workspace_size(ctypes.byref(a)), dev, workspace)
+        if ws is not None:
+            a.workspace = ws.data_ptr()
+            a.workspace_bytes = ws.numel() * ws.element_size()
+        _check(lib.fa_tree_decode_paged(ctypes.byref(a), _current_stream(dev)))
+    return out, lse

@@ -1,0 +1,1042 @@
+// tree.cu -- attention of a tree of drafted tokens over a paged cache, 16-bit or 8-bit, on the
+// tensor cores (one drafted token: decode over an 8-bit cache).
+//
+// Query i of a sequence sees every token of the context (all but the sequence's last n drafted
+// tokens) and the drafted tokens that bit j of its mask row names:
+//   s_j = scale <q_i, k_j>,  out_i = sum_j softmax(s)_j v_j over the seen j.
+// The mask touches only the KV tiles that overlap the last n tokens; every other tile runs the
+// unmasked softmax.
+//
+// One CTA takes one 128-row tile of packed (query head, query) rows of one kv head against one
+// range of KV tiles, as the paged prefill kernel does, and the two issuing threads, the three
+// S/P buffers in tensor memory and the lazy rescale are the same protocol.  What differs is
+// where a K or V stage comes from.  16-bit pages: TMA boxes straight into the stage.  8-bit
+// pages: TMA boxes of e4m3 rows into a raw ring, from which a warpgroup of converters writes
+// the 16-bit stage, one row a thread: each row's scale is a power of two, so value * 2^e is
+// exact in bf16 and the product with Q is the same as on the widened cache.  Converting on
+// the way costs shared-memory bandwidth (a row is written twice and read twice) but keeps the
+// 16-bit queries and weights whole, which 8-bit MMAs would not.
+//
+// Warp roles: 0-3 softmax + epilogue (thread t owns row t), 4 TMA producer, 5 P V issuer and
+// tensor-memory owner, 6 S issuer, and for 8-bit pages 8-11 converters (7 idle, so that the
+// converters are a warpgroup of their own).
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "../../include/fa.h"
+#include "cache.cuh"
+#include "internal.h"
+#include "prefill_common.cuh"
+#include "sm103.cuh"
+
+namespace fa {
+namespace {
+
+using prefill::kRows;
+constexpr int kNumS = 3;       // S/P buffers in tensor memory
+constexpr int kMaxTree = 256;  // drafted tokens
+
+struct TreeParams {
+  const void* k_pages;
+  const void* v_pages;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* page_table;
+  const int32_t* kv_lens;
+  const int32_t* draft_lens;    // or nullptr: T each
+  const uint64_t* mask;         // [mask_batches, T, words], or nullptr: a chain
+  void* out;                    // [B,Hq,T,D]
+  float* lse;                   // [B,Hq,T] or nullptr
+  float* o_part;                // split: [B*Hq*T, n_splits, D] fp32
+  float* lse_part;              // split: [B*Hq*T, n_splits]
+  int mask_batches, words;
+  int B, Hq, Hkv, G, T;
+  int q_per_tile, n_qtiles, n_splits;
+  int page_size, page_shift, max_pages, num_pages;
+  float scale_log2;
+  uint32_t* status;
+};
+
+template <int D, int BN, int STAGES, int RAW, bool Q8>
+struct Layout {
+  static constexpr int kThreads = Q8 ? 384 : 224;
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kKVBytes = BN * D * 2;   // one 16-bit K (or V) stage
+  static constexpr int kRawBytes = BN * D;      // one 8-bit K (or V) stage
+  static constexpr int kKOff = kQBytes;
+  static constexpr int kVOff = kKOff + STAGES * kKVBytes;
+  static constexpr int kRawKOff = kVOff + STAGES * kKVBytes;
+  static constexpr int kRawVOff = kRawKOff + (Q8 ? RAW * kRawBytes : 0);
+  static constexpr int kBarOff = kRawVOff + (Q8 ? RAW * kRawBytes : 0);
+  // q_full, {k,v}_full[S], {k,v}_empty[S], s_full[3], p_full[3], pv_done[3], pv_issuer_done,
+  // s_issuer_done, raw {k,v}_full[R], raw {k,v}_empty[R]
+  static constexpr int kNumBars = 1 + 4 * STAGES + 3 * kNumS + 2 + (Q8 ? 4 * RAW : 0);
+  static constexpr int kPoisonOff = kBarOff + kNumBars * 8 + 16;
+  static constexpr int kBytes = kPoisonOff + (kMaxTree / 32) * 4;
+  static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 bytes
+  static_assert(D + kNumS * BN <= 512, "tensor memory budget (O and the S/P buffers)");
+  static_assert(kAlloc <= 232448, "shared memory budget");
+};
+
+// ------------------------------------------------------------------------------------------
+// The mask of one query row over the drafted tokens.
+// ------------------------------------------------------------------------------------------
+struct TreeRow {
+  const uint64_t* words;  // the row's mask words, or nullptr: a chain (tokens 0..i)
+  int i, n;               // query, drafted tokens
+};
+
+__device__ __forceinline__ uint64_t row_word(const TreeRow& r, int w) {
+  const int left = r.n - 64 * w;  // drafted tokens from this word on
+  if (left <= 0) return 0;
+  uint64_t v = ~0ull;
+  if (r.words) {
+    v = __ldg(reinterpret_cast<const unsigned long long*>(r.words + w));
+  } else {
+    const int c = r.i + 1 - 64 * w;
+    v = c >= 64 ? ~0ull : c > 0 ? (1ull << c) - 1 : 0ull;
+  }
+  return left >= 64 ? v : v & ((1ull << left) - 1);
+}
+
+// Visibility of the 32 keys from drafted offset `off` on (negative: still in the context).
+__device__ __forceinline__ uint32_t row_bits(const TreeRow& r, int off) {
+  if (off <= -32) return ~0u;
+  if (off < 0) return (static_cast<uint32_t>(row_word(r, 0)) << -off) | ((1u << -off) - 1);
+  const int w = off >> 6, s = off & 63;
+  uint64_t v = row_word(r, w) >> s;
+  if (s > 32) v |= row_word(r, w + 1) << (64 - s);
+  return static_cast<uint32_t>(v);
+}
+
+__device__ __forceinline__ bool row_sees(const TreeRow& r, int d) {
+  return (row_word(r, d >> 6) >> (d & 63)) & 1;
+}
+
+// ------------------------------------------------------------------------------------------
+// One KV tile of the online softmax for one row (prefill::softmax_tile with a bit mask in
+// place of the key limit and the additive mask).  raw: the S row; hidden keys already hold
+// -inf.  a: the factor into log2 units (positive).
+//
+// fp16 weights are held 2^7 times larger, as are their sums: the stale maximum lets a weight grow
+// to 2^8, so they still fit (2^15), and the small ones, whose rounding is absolute below 2^-14,
+// keep seven more bits.
+// ------------------------------------------------------------------------------------------
+template <bool BF16>
+constexpr float kWeightLog2 = BF16 ? 0.f : 7.f;
+
+template <int BN, bool BF16>
+__device__ __forceinline__ bool softmax_step(const uint32_t (&raw)[BN], float a, float& m, float& l,
+                                             float& alpha, uint32_t (&pk)[BN / 2]) {
+  float mx[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    mx[e] = prefill::fmax3(__uint_as_float(raw[e]), __uint_as_float(raw[e + 8]), -INFINITY);
+#pragma unroll
+  for (int c = 16; c < BN; c += 16) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      mx[e] = prefill::fmax3(mx[e], __uint_as_float(raw[c + e]), __uint_as_float(raw[c + 8 + e]));
+  }
+  const float row_max = a * prefill::fmax3(prefill::fmax3(mx[0], mx[1], mx[2]),
+                                           prefill::fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+  const float m_new = fmaxf(m, row_max);
+  const bool need = m_new > m + prefill::kRescaleLog2;
+  alpha = 1.f;
+  if (need) {
+    alpha = exp2_approx(m - m_new);  // 0 when m is -inf
+    m = m_new;
+    l *= alpha;
+  }
+  const float m_use = (m == -INFINITY) ? 0.f : m - kWeightLog2<BF16>;
+  const float2 a2 = make_float2(a, a), nm2 = make_float2(-m_use, -m_use);
+  float2 sum2[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) sum2[e] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < BN / 2; ++c) {
+    const float2 t = __ffma2_rn(
+        make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])), a2, nm2);
+    const float p0 = exp2_approx(t.x);
+    const float p1 = exp2_approx(t.y);
+    sum2[c & 3] = __fadd2_rn(sum2[c & 3], make_float2(p0, p1));
+    pk[c] = BF16 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
+  }
+  const float2 s01 = __fadd2_rn(sum2[0], sum2[1]), s23 = __fadd2_rn(sum2[2], sum2[3]);
+  l += (s01.x + s01.y) + (s23.x + s23.y);
+  return need;
+}
+
+// ------------------------------------------------------------------------------------------
+// e4m3 -> 16 bits with the row's scale.  bf16: the byte's exponent and mantissa placed in a
+// bf16 are the value times 2^-120 (subnormals included), so one product with 2^(120 + e) is
+// the exact result; exponents above 7 leave bf16's range there and take a second product.  fp16:
+// the hardware conversion, then the scale in two products of which only the last can round.
+// ------------------------------------------------------------------------------------------
+struct RowScale {
+  uint32_t f1, f2;  // packed pairs; f2 is used where `two`
+  bool two;
+};
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ RowScale row_scale(uint32_t byte) {
+  RowScale s;
+  const int e = static_cast<int>(byte) - 127;  // [-127, 128]
+  if constexpr (BF16) {
+    const int e1 = min(e, 7);
+    const uint32_t f1 = static_cast<uint32_t>(e1 + 120 + 127) << 7;  // exponent field in [120, 254]
+    const int e2 = e - e1;                                           // [0, 121]
+    const uint32_t f2 = static_cast<uint32_t>(e2 + 127) << 7;
+    s.f1 = f1 | (f1 << 16);
+    s.f2 = f2 | (f2 << 16);
+    s.two = e2 > 0;
+  } else {
+    // first factor in [2^-14, 2^15] (exact: an e4m3 value is a multiple of 2^-9), then the rest
+    const int e1 = max(-14, min(e, 15));
+    const int e2 = max(-24, min(e - e1, 15));
+    const uint32_t f1 = static_cast<uint32_t>(e1 + 15) << 10;
+    const uint32_t f1n = e1 == -14 ? 0x0400u : f1;
+    const uint32_t f2 = e2 >= -14 ? static_cast<uint32_t>(e2 + 15) << 10 : 1u << (e2 + 24);
+    s.f1 = f1n | (f1n << 16);
+    s.f2 = f2 | (f2 << 16);
+    s.two = e != e1;
+  }
+  return s;
+}
+
+// Four e4m3 codes -> two packed pairs, scaled.
+template <bool BF16>
+__device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& lo, uint32_t& hi) {
+  if constexpr (BF16) {
+    const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
+    lo = mul_bf16x2(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), s.f1);
+    hi = mul_bf16x2(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), s.f1);
+    if (s.two) {
+      lo = mul_bf16x2(lo, s.f2);
+      hi = mul_bf16x2(hi, s.f2);
+    }
+  } else {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+    lo = mul_f16x2(static_cast<uint32_t>(a.x) | (static_cast<uint32_t>(a.y) << 16), s.f1);
+    hi = mul_f16x2(static_cast<uint32_t>(b.x) | (static_cast<uint32_t>(b.y) << 16), s.f1);
+    if (s.two) {
+      lo = mul_f16x2(lo, s.f2);
+      hi = mul_f16x2(hi, s.f2);
+    }
+  }
+}
+
+// A NaN code (0x7f or 0xff) turns its sign bit over when one is added to every byte; a carry
+// out of 0xff can only add further marks.  Sign bits of the result: some byte is NaN.
+__device__ __forceinline__ uint32_t nan_mark(uint32_t acc, uint32_t w) {
+  return acc | ((w + 0x01010101u) ^ w);
+}
+
+__device__ __forceinline__ bool nonfinite16(uint32_t h, bool bf16) {
+  return bf16 ? (h & 0x7f80u) == 0x7f80u : (h & 0x7c00u) == 0x7c00u;
+}
+
+// Value of V at drafted token d, column c, if it is not finite (else 0): the slow path of a row
+// that sees a drafted token with such a value.
+template <int D, bool BF16, bool Q8>
+__device__ __noinline__ float nonfinite_v(const TreeParams& p, int b, int hk, int key, int c) {
+  const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + (key >> p.page_shift)];
+  if (page < 0 || page >= p.num_pages) return 0.f;
+  const int64_t at = ((static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1))) * D + c;
+  if constexpr (Q8) {
+    const uint32_t v = static_cast<const uint8_t*>(p.v_pages)[at];
+    return (v & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : 0.f;
+  } else {
+    const uint16_t h = static_cast<const uint16_t*>(p.v_pages)[at];
+    if (!nonfinite16(h, BF16)) return 0.f;
+    return BF16 ? __uint_as_float(static_cast<uint32_t>(h) << 16)
+                : __half2float(__ushort_as_half(h));
+  }
+}
+
+template <int D, int BN, int STAGES, int RAW, bool BF16, bool Q8, bool SPLIT>
+__global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
+    tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
+  using L = Layout<D, BN, STAGES, RAW, Q8>;
+  constexpr int kThreads = L::kThreads;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t s_base = smem_addr(smem);
+  const uint32_t sQ = s_base, sK = s_base + L::kKOff, sV = s_base + L::kVOff;
+  const uint32_t bars = s_base + L::kBarOff;
+  const uint32_t bar_q = bars;
+  auto bar_k = [&](int s) { return bars + 8u * (1 + s); };
+  auto bar_v = [&](int s) { return bars + 8u * (1 + STAGES + s); };
+  auto bar_ke = [&](int s) { return bars + 8u * (1 + 2 * STAGES + s); };
+  auto bar_ve = [&](int s) { return bars + 8u * (1 + 3 * STAGES + s); };
+  // per S/P buffer b (tile j with j % 3 == b): S_j computed, P_j written, P_j V_j finished
+  auto bar_s = [&](int b) { return bars + 8u * (1 + 4 * STAGES + b); };
+  auto bar_p = [&](int b) { return bars + 8u * (1 + 4 * STAGES + kNumS + b); };
+  auto bar_pv = [&](int b) { return bars + 8u * (1 + 4 * STAGES + 2 * kNumS + b); };
+  const uint32_t bar_done = bars + 8u * (1 + 4 * STAGES + 3 * kNumS);
+  const uint32_t bar_sdone = bar_done + 8u;
+  const uint32_t bar_raw = bar_done + 16u;
+  // 8-bit pages: raw K, V landed (TMA) and read (converters)
+  auto bar_rk = [&](int s) { return bar_raw + 8u * s; };
+  auto bar_rv = [&](int s) { return bar_raw + 8u * (RAW + s); };
+  auto bar_rke = [&](int s) { return bar_raw + 8u * (2 * RAW + s); };
+  auto bar_rve = [&](int s) { return bar_raw + 8u * (3 * RAW + s); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBarOff + L::kNumBars * 8);
+  // drafted tokens whose V row holds a value that is not finite (see the V clearing below)
+  uint32_t* poison = reinterpret_cast<uint32_t*>(smem + L::kPoisonOff);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // A 16-bit stage holds BN rows x D columns as 1024-byte SW128 atoms (8 rows x 64 columns), the
+  // D/64 atoms of an 8-row group side by side, group after group (a page is whole groups).
+  constexpr uint32_t kCB = 1024u;                // column-block stride
+  constexpr uint32_t kRG = (D / 64) * 1024u;     // 8-row-group stride
+
+  // ---- work item: (query tile, split) x kv head x sequence, longest sequences first ----
+  const int split = blockIdx.x % p.n_splits;
+  const int qt = static_cast<int>(blockIdx.x) / p.n_splits;
+  const int hk = blockIdx.y;
+  int b = blockIdx.z;
+  {
+    __shared__ int lpt_seq;
+    if (p.B <= kThreads) {
+      if (threadIdx.x < p.B) {
+        const int li = p.kv_lens[threadIdx.x];
+        int rank = 0;
+        for (int j = 0; j < p.B; ++j) {
+          const int lj = p.kv_lens[j];
+          rank += (lj > li || (lj == li && j < static_cast<int>(threadIdx.x))) ? 1 : 0;
+        }
+        if (rank == static_cast<int>(blockIdx.z)) lpt_seq = threadIdx.x;
+      }
+      __syncthreads();
+      b = lpt_seq;
+    }
+  }
+  int Lkv = p.kv_lens[b];
+  int n_draft = p.draft_lens ? p.draft_lens[b] : p.T;
+  if (Lkv < 0 || static_cast<int64_t>(Lkv) > static_cast<int64_t>(p.max_pages) * p.page_size ||
+      n_draft < 0 || n_draft > p.T || n_draft > Lkv) {
+    // an empty sequence without draft_lens is no error: its rows are empty
+    if (threadIdx.x == 0 && !(Lkv == 0 && !p.draft_lens)) record_error(p.status, kDevBounds);
+    Lkv = 0;
+    n_draft = 0;
+  }
+  const int ctx = Lkv - n_draft;
+  const int q0 = qt * p.q_per_tile;
+  // a tile of padding rows alone has nothing to attend
+  const int n_kv_tiles = q0 < n_draft ? (Lkv + BN - 1) / BN : 0;
+  const int per_split = (n_kv_tiles + p.n_splits - 1) / p.n_splits;
+  const int t_begin = min(n_kv_tiles, split * per_split);
+  const int n = min(n_kv_tiles, t_begin + per_split) - t_begin;
+  // rows are packed head-major: r = g * q_per_tile + (i - q0); warps past them have no work
+  const int rows_used = p.q_per_tile * p.G;
+  const int live_warps = (rows_used + 31) / 32;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q, 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(bar_k(s), Q8 ? 128 : 1);
+      mbar_init(bar_v(s), Q8 ? 128 : 1);
+      mbar_init(bar_ke(s), 1);
+      mbar_init(bar_ve(s), 1);
+    }
+    for (int i = 0; i < kNumS; ++i) {
+      mbar_init(bar_s(i), 1);
+      mbar_init(bar_p(i), live_warps * 32);
+      mbar_init(bar_pv(i), 1);
+    }
+    mbar_init(bar_done, 1);
+    mbar_init(bar_sdone, 1);
+    if constexpr (Q8) {
+      for (int s = 0; s < RAW; ++s) {
+        mbar_init(bar_rk(s), 1);
+        mbar_init(bar_rv(s), 1);
+        mbar_init(bar_rke(s), 128);
+        mbar_init(bar_rve(s), 128);
+      }
+    }
+    fence_barrier_init();
+  }
+  if (threadIdx.x < kMaxTree / 32) poison[threadIdx.x] = 0;
+  if (warp == 5) {
+    tmem_alloc(smem_addr(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t tm_o = tmem;           // O: columns [0, D)
+  const uint32_t tm_s0 = tmem + D;      // S/P buffer b: columns [D + b*BN, D + (b+1)*BN)
+
+  if (warp == 4) {
+    // ------------------------------- TMA producer ---------------------------------------
+    if (n > 0) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+        mbar_arrive_expect_tx(bar_q, static_cast<uint32_t>(D * 2 * p.q_per_tile * p.G));
+        for (int kb = 0; kb < D / 64; ++kb)
+          tma_load_4d(sQ + kb * (kRows * 128), &tm_q, bar_q, kb * 64, q0, hk * p.G, b);
+      }
+      // A KV tile is BN / page_size pages, each one TMA box.  Lane i holds the page id of page i
+      // of a tile, loaded one tile ahead, and issues that page's box itself.
+      const int ps = p.page_size, tp = BN / ps;
+      const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+      auto tile_page = [&](int jj) {
+        int id = 0;  // pages past the sequence's end read page 0; those keys are hidden
+        if (lane < tp) {
+          const int lp = (t_begin + jj) * tp + lane;
+          if (static_cast<int64_t>(lp) * ps < Lkv) {
+            const int v = __ldg(table + lp);
+            if (v >= 0 && v < p.num_pages) id = v;
+            else record_error(p.status, kDevBounds);
+          }
+        }
+        return id;
+      };
+      constexpr int kRing = Q8 ? RAW : STAGES;
+      constexpr uint32_t kBytes = Q8 ? L::kRawBytes : L::kKVBytes;
+      const uint32_t dst_k = Q8 ? s_base + L::kRawKOff : sK, dst_v = Q8 ? s_base + L::kRawVOff : sV;
+      auto full_k = [&](int s) { return Q8 ? bar_rk(s) : bar_k(s); };
+      auto full_v = [&](int s) { return Q8 ? bar_rv(s) : bar_v(s); };
+      auto empty_k = [&](int s) { return Q8 ? bar_rke(s) : bar_ke(s); };
+      auto empty_v = [&](int s) { return Q8 ? bar_rve(s) : bar_ve(s); };
+      auto load_pages = [&](uint32_t dst, const CUtensorMap* map, uint32_t bar, int id) {
+        if (lane < tp) {
+          const uint32_t to = dst + lane * ps * (kBytes / BN);
+          if constexpr (Q8) tma_load_4d(to, map, bar, 0, 0, 0, id * p.Hkv + hk);
+          else tma_load_5d(to, map, bar, 0, 0, 0, 0, id * p.Hkv + hk);
+        }
+      };
+      int k_issued = 0, v_issued = 0;
+      int ids_next = tile_page(0);
+      for (int jj = 0; jj < n; ++jj) {
+        const int ids = ids_next;
+        if (jj + 1 < n) ids_next = tile_page(jj + 1);
+        const int stage = jj % kRing;
+        const uint32_t par = ((jj / kRing) - 1) & 1;
+        bool okw = jj < kRing || mbar_wait(empty_k(stage), par, p.status);
+        if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
+        if (lane == 0) mbar_arrive_expect_tx(full_k(stage), kBytes);
+        __syncwarp();
+        load_pages(dst_k + stage * kBytes, &tm_k, full_k(stage), ids);
+        k_issued = jj + 1;
+        okw = jj < kRing || mbar_wait(empty_v(stage), par, p.status);
+        if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
+        if (lane == 0) mbar_arrive_expect_tx(full_v(stage), kBytes);
+        __syncwarp();
+        load_pages(dst_v + stage * kBytes, &tm_v, full_v(stage), ids);
+        v_issued = jj + 1;
+      }
+      if (lane == 0 && v_issued < n) {
+        // A wait ran out: let the copies in flight land before the CTA exits.  Each of these is
+        // the last one issued to its stage, so its parity wait is exact.
+        mbar_wait(bar_q, 0, nullptr);
+        for (int jj = max(0, k_issued - kRing); jj < k_issued; ++jj)
+          mbar_wait(full_k(jj % kRing), (jj / kRing) & 1, nullptr);
+        for (int jj = max(0, v_issued - kRing); jj < v_issued; ++jj)
+          mbar_wait(full_v(jj % kRing), (jj / kRing) & 1, nullptr);
+      }
+    }
+  } else if (warp == 5) {
+    // ------------------------------- P V issuer -----------------------------------------
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_o = idesc_f16(BF16, kRows, D, false, true);
+      const uint64_t v_desc = sdesc_sw128(sV, kCB, kRG);
+      bool ok = true;
+      for (int jj = 0; ok && jj < n; ++jj) {
+        const int stage = jj % STAGES, buf = jj % kNumS;
+        if (!(ok = mbar_wait(bar_p(buf), (jj / kNumS) & 1, p.status))) break;
+        if (!(ok = mbar_wait(bar_v(stage), (jj / STAGES) & 1, p.status))) break;
+        tc_fence_after();
+        const uint64_t vd = sdesc_add(v_desc, stage * L::kKVBytes);
+        const uint32_t a_p = tm_s0 + buf * BN;
+#pragma unroll
+        for (int kk = 0; kk < BN / 16; ++kk)
+          mma_ts(tm_o, a_p + kk * 8, sdesc_add(vd, kk * (2 * kRG)), idesc_o,
+                 (jj > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(bar_pv(buf));
+        tc_commit(bar_ve(stage));
+      }
+      // Every MMA this thread issued must finish before tensor memory is released.
+      tc_commit(bar_done);
+      mbar_wait(bar_done, 0, nullptr);
+    }
+  } else if (warp == 6) {
+    // --------------------------------- S issuer -----------------------------------------
+    if (lane == 0 && n > 0) {
+      constexpr uint32_t idesc_s = idesc_f16(BF16, kRows, BN, false, false);
+      const uint64_t k_desc = sdesc_sw128(sK, 16, kRG);
+      const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024);
+      bool ok = mbar_wait(bar_q, 0, p.status);
+      for (int jj = 0; ok && jj < n; ++jj) {
+        const int stage = jj % STAGES, buf = jj % kNumS;
+        if (!(ok = mbar_wait(bar_k(stage), (jj / STAGES) & 1, p.status))) break;
+        if (jj >= kNumS && !(ok = mbar_wait(bar_pv(buf), ((jj - kNumS) / kNumS) & 1, p.status))) break;
+        tc_fence_after();
+        const uint64_t kd = sdesc_add(k_desc, stage * L::kKVBytes);
+        const uint32_t d_s = tm_s0 + buf * BN;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk % 4) * 32;
+          mma_ss(d_s, sdesc_add(q_desc, (kk / 4) * (kRows * 128) + off),
+                 sdesc_add(kd, (kk / 4) * kCB + off), idesc_s, kk > 0 ? 1u : 0u);
+        }
+        tc_commit(bar_s(buf));
+        tc_commit(bar_ke(stage));
+      }
+      tc_commit(bar_sdone);
+      mbar_wait(bar_sdone, 0, nullptr);
+    }
+  } else if (Q8 && warp >= 8) {
+    // -------------------------------- converters ----------------------------------------
+    // Thread t takes row t % BN of a tile (for BN = 64 half its columns): its page and scale
+    // bytes are loaded a tile ahead, each 16-byte chunk of the raw row becomes two of the
+    // stage's.  Rows past the sequence's end become zeros.
+    if constexpr (Q8) {
+      constexpr int kParts = 128 / BN, kIn = D < 128 ? D : 128;
+      const int ct = threadIdx.x - 256, row = ct % BN, part = ct / BN;
+      const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+      auto scale_row = [&](int jj) {  // index of the row's scales, or -1
+        const int key = (t_begin + jj) * BN + row;
+        if (jj >= n || key >= Lkv) return static_cast<int64_t>(-1);
+        const int v = __ldg(table + (key >> p.page_shift));
+        const int page = v >= 0 && v < p.num_pages ? v : 0;
+        return (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1));
+      };
+      // raw row: BN / page_size pages of page_size rows, columns in blocks of kIn bytes
+      const int pg = row >> p.page_shift, rr = row & (p.page_size - 1);
+      const uint32_t raw_row = (pg << p.page_shift) * D + rr * kIn;
+      const uint32_t raw_blk = (kIn << p.page_shift);
+      const uint32_t raw_swz = D >= 128 ? rr & 7 : (rr >> 1) & 3;
+      const uint32_t out_row = (row / 8) * kRG + (row % 8) * 128;
+      auto convert = [&](const uint8_t* raw, uint8_t* dst, uint32_t byte, bool inside, int draft) {
+        const RowScale s = row_scale<BF16>(byte);
+        uint32_t marks = 0;
+        constexpr int kChunks = D / 16 / kParts;
+#pragma unroll
+        for (int c8 = 0; c8 < kChunks; ++c8) {
+          const int c = part * kChunks + c8;        // 16 columns from 16c on
+          const int blk = c / (kIn / 16), ci = c % (kIn / 16);
+          uint4 w = *reinterpret_cast<const uint4*>(raw + raw_row + blk * raw_blk + ((ci ^ raw_swz) * 16));
+          if (!inside) w = make_uint4(0, 0, 0, 0);
+          uint4 x, y;
+          widen4<BF16>(w.x, s, x.x, x.y);
+          widen4<BF16>(w.y, s, x.z, x.w);
+          widen4<BF16>(w.z, s, y.x, y.y);
+          widen4<BF16>(w.w, s, y.z, y.w);
+          marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w.x), w.y), w.z), w.w);
+          uint8_t* d = dst + out_row + (c / 4) * kCB;
+          const int ch = (c % 4) * 2;
+          *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) * 16)) = x;
+          *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) * 16)) = y;
+        }
+        if (marks & 0x80808080u) {
+          // NaN codes (rare): put NaN where they are, or, in a drafted token's V, zero, and note
+          // the token: a weight of 0 would still carry a NaN into rows that do not see it
+          for (int c8 = 0; c8 < kChunks; ++c8) {
+            const int c = part * kChunks + c8;
+            const int blk = c / (kIn / 16), ci = c % (kIn / 16);
+            const uint8_t* w = raw + raw_row + blk * raw_blk + ((ci ^ raw_swz) * 16);
+            uint8_t* d = dst + out_row + (c / 4) * kCB;
+            for (int e = 0; e < 16; ++e) {
+              if ((w[e] & 0x7f) != 0x7f) continue;
+              const int ch = (c % 4) * 2 + e / 8;
+              *reinterpret_cast<uint16_t*>(d + ((ch ^ (row & 7)) * 16) + (e % 8) * 2) =
+                  draft >= 0 ? 0 : 0x7fff;
+              if (draft >= 0) atomicOr(&poison[draft >> 5], 1u << (draft & 31));
+            }
+          }
+        }
+      };
+      int64_t at = scale_row(0);
+      uint32_t kb = at >= 0 ? p.k_scales[at] : 127, vb = at >= 0 ? p.v_scales[at] : 127;
+      for (int jj = 0; jj < n; ++jj) {
+        const int rs = jj % RAW, stage = jj % STAGES;
+        const int key = (t_begin + jj) * BN + row;
+        const bool inside = key < Lkv;
+        const uint32_t kbyte = kb, vbyte = vb;
+        at = scale_row(jj + 1);
+        if (at >= 0) {
+          kb = p.k_scales[at];
+          vb = p.v_scales[at];
+        }
+        if (!mbar_wait(bar_rk(rs), (jj / RAW) & 1, p.status)) break;
+        if (jj >= STAGES && !mbar_wait(bar_ke(stage), ((jj / STAGES) - 1) & 1, p.status)) break;
+        convert(smem + L::kRawKOff + rs * L::kRawBytes, smem + L::kKOff + stage * L::kKVBytes, kbyte,
+                inside, -1);
+        mbar_arrive(bar_rke(rs));
+        fence_proxy_async_smem();
+        mbar_arrive(bar_k(stage));
+        if (!mbar_wait(bar_rv(rs), (jj / RAW) & 1, p.status)) break;
+        if (jj >= STAGES && !mbar_wait(bar_ve(stage), ((jj / STAGES) - 1) & 1, p.status)) break;
+        convert(smem + L::kRawVOff + rs * L::kRawBytes, smem + L::kVOff + stage * L::kKVBytes, vbyte,
+                inside, inside && key >= ctx ? key - ctx : -1);
+        mbar_arrive(bar_rve(rs));
+        fence_proxy_async_smem();
+        mbar_arrive(bar_v(stage));
+      }
+    }
+  } else if (warp < live_warps) {
+    // ------------------------- softmax + epilogue (row per thread) ----------------------
+    const int r = threadIdx.x;
+    const int g = r / p.q_per_tile, i = q0 + r % p.q_per_tile;
+    const bool valid = g < p.G && i < p.T;   // a row of the output
+    const bool active = valid && i < n_draft;  // a query of this sequence (else an empty row)
+    const int64_t flat = (static_cast<int64_t>(b) * p.Hq + hk * p.G + g) * p.T + i;
+    TreeRow row;
+    row.i = i;
+    row.n = active ? n_draft : 0;
+    row.words = nullptr;
+    if (p.mask && active)
+      row.words = p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words;
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    float m_run = -INFINITY, l_run = 0.f;
+    // a > 0 goes into the exponential's argument; otherwise the scores are scaled first
+    const bool pre = !(p.scale_log2 > 0.f);
+    const float a = pre ? 1.f : p.scale_log2;
+    bool ok = true;
+    for (int jj = 0; ok && jj < n; ++jj) {
+      const int buf = jj % kNumS;
+      const uint32_t t_s = tm_s0 + lane_off + buf * BN;
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_s(buf), (jj / kNumS) & 1, p.status));
+      if (!ok) break;
+      tc_fence_after();
+      uint32_t raw[BN];
+      prefill::load_s<BN>(t_s, raw);
+      const int key0 = (t_begin + jj) * BN;
+      if (pre) {
+#pragma unroll
+        for (int c = 0; c < BN; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * p.scale_log2);
+      }
+      if (key0 + BN > ctx) {
+#pragma unroll
+        for (int w = 0; w < BN / 32; ++w) {
+          const uint32_t bits = row_bits(row, key0 + 32 * w - ctx);
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (!((bits >> c) & 1)) raw[32 * w + c] = 0xff800000u;  // -inf
+        }
+      }
+      float alpha;
+      uint32_t pk[BN / 2];
+      const bool need = softmax_step<BN, BF16>(raw, a, m_run, l_run, alpha, pk);
+      // O is rescaled only once every earlier P V product is in it; a tile with no rescale
+      // does not wait (S_j itself needed P_{j-3} V_{j-3} finished)
+      const bool rescale = jj > 0 && __any_sync(0xffffffffu, need);
+      if (rescale) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((jj - 1) % kNumS), ((jj - 1) / kNumS) & 1, p.status));
+        if (!ok) break;
+        tc_fence_after();
+        prefill::rescale_o<D>(tm_o + lane_off, alpha);
+      }
+      prefill::store_p<BN>(t_s, pk);
+      tmem_st_wait();
+      if (!Q8 && key0 + BN > ctx) {
+        // The stage holds rows of drafted tokens, which some queries do not see, or rows past
+        // the sequence's end.  Their weight is 0, but 0 times a V that is not finite would
+        // still poison O: rows past the end are cleared, and such values of drafted tokens are
+        // cleared and their token noted (the epilogue gives them to the rows that see it).
+        // The parity wait for V_j is exact only once V_{j-STAGES} has landed: P_{j-1} V_{j-1}
+        // finishing makes sure of it.
+        const int stage = jj % STAGES;
+        if (jj > 0 && !rescale)
+          ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((jj - 1) % kNumS), ((jj - 1) / kNumS) & 1, p.status));
+        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_v(stage), (jj / STAGES) & 1, p.status));
+        if (!ok) break;
+        uint8_t* vst = smem + L::kVOff + stage * L::kKVBytes;
+        const int r0 = max(0, ctx - key0);
+        constexpr int kChunks = D / 8;  // 16-byte chunks a row
+        for (int u = threadIdx.x; u < (BN - r0) * kChunks; u += live_warps * 32) {
+          const int vr = r0 + u / kChunks, c = u % kChunks;
+          uint4* at = reinterpret_cast<uint4*>(vst + (vr / 8) * kRG + (c / 8) * kCB + (vr % 8) * 128 +
+                                               (c % 8) * 16);
+          const int d = key0 + vr - ctx;
+          if (d >= n_draft) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+          }
+          const uint4 v = *at;
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (nonfinite16(w[e], BF16)) w[e] &= 0xffff0000u, bad = true;
+            if (nonfinite16(w[e] >> 16, BF16)) w[e] &= 0x0000ffffu, bad = true;
+          }
+          if (bad) {
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            atomicOr(&poison[d >> 5], 1u << (d & 31));
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(bar_p(buf));
+    }
+    if (ok && n > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((n - 1) % kNumS), ((n - 1) / kNumS) & 1, p.status));
+      tc_fence_after();
+    }
+    if (ok) {
+      // O / l, a row's slab of columns at a time: staged in this warp's part of the K ring (free:
+      // every MMA has finished) with 16-byte chunks swizzled by the row, then written out as
+      // whole 128-byte runs, eight lanes a row.
+      const bool have = active && n > 0 && !(l_run == 0.f);  // a NaN sum stays NaN
+      const float inv_l = 1.f / l_run;
+      bool any_poison = false;
+      if (n > 0) {
+        for (int w = 0; w < kMaxTree / 32; ++w) any_poison |= poison[w] != 0;
+      }
+      uint8_t* stage = smem + L::kKOff + warp * 4096;
+      constexpr int kCols = SPLIT ? 32 : 64;  // columns of a 128-byte run
+      const int64_t my_row = SPLIT ? flat * p.n_splits + split : flat;
+#pragma unroll 1
+      for (int c0 = 0; c0 < D; c0 += kCols) {
+#pragma unroll
+        for (int h = 0; h < kCols / 32; ++h) {
+          uint32_t o[32];
+          if (n > 0) {
+            tmem_ld32(tm_o + lane_off + c0 + 32 * h, o);
+            tmem_ld_wait();
+          }
+          if (any_poison && active) {
+            for (int d = 0; d < n_draft; ++d) {
+              if (!((poison[d >> 5] >> (d & 31)) & 1) || !row_sees(row, d)) continue;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                o[e] = __float_as_uint(__uint_as_float(o[e]) +
+                                       nonfinite_v<D, BF16, Q8>(p, b, hk, ctx + d, c0 + 32 * h + e));
+            }
+          }
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = have ? __uint_as_float(o[e]) * inv_l : 0.f;
+#pragma unroll
+          for (int ch = 0; ch < (SPLIT ? 8 : 4); ++ch) {
+            uint4 w;
+            if constexpr (SPLIT) {
+              w = make_uint4(__float_as_uint(v[4 * ch]), __float_as_uint(v[4 * ch + 1]),
+                             __float_as_uint(v[4 * ch + 2]), __float_as_uint(v[4 * ch + 3]));
+            } else {
+              uint32_t u[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                u[e] = BF16 ? pack_bf16x2(v[8 * ch + 2 * e], v[8 * ch + 2 * e + 1])
+                            : pack_f16x2(v[8 * ch + 2 * e], v[8 * ch + 2 * e + 1]);
+              w = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+            const int at = SPLIT ? ch : 4 * h + ch;
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((at ^ (lane & 7)) * 16)) = w;
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          const int rr = 4 * s + lane / 8, ch = lane % 8;
+          const int64_t to = __shfl_sync(0xffffffffu, my_row, rr);
+          const bool st = __shfl_sync(0xffffffffu, valid ? 1 : 0, rr);
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          if (st) {
+            if constexpr (SPLIT)
+              *reinterpret_cast<uint4*>(p.o_part + to * D + c0 + ch * 4) = w;
+            else
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + to * D + c0 + ch * 8) = w;
+          }
+        }
+        __syncwarp();
+      }
+      if (valid) {
+        const float lse = have ? (m_run - kWeightLog2<BF16> + log2f(l_run)) * prefill::kLn2 : -INFINITY;
+        // the merge takes a part of weight +inf as not a number, which a NaN part would not be
+        if constexpr (SPLIT) p.lse_part[my_row] = lse != lse ? INFINITY : lse;
+        else if (p.lse) p.lse[my_row] = lse;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 5) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Host side
+// ------------------------------------------------------------------------------------------
+int bad(int code, const char* msg) { return set_error(code, msg); }
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+struct TreePlan {
+  int G, q_per_tile, n_qtiles, n_splits;
+  size_t off_lse, total;
+};
+
+// KV tile of a head dimension: as the prefill kernels', what tensor memory holds beside O.
+int block_n(int D) { return D == 256 ? 64 : 128; }
+
+TreePlan plan_tree(const fa_tree_args* a) {
+  TreePlan pl{};
+  pl.G = a->Hq / a->Hkv;
+  // equal query tiles, so that their rows are packed without gaps
+  const int most = 128 / pl.G;
+  pl.n_qtiles = (a->T + most - 1) / most;
+  pl.q_per_tile = (a->T + pl.n_qtiles - 1) / pl.n_qtiles;
+  pl.n_qtiles = (a->T + pl.q_per_tile - 1) / pl.q_per_tile;
+  const int bn = block_n(a->D);
+  const int kv_tiles = (a->max_seq_len + bn - 1) / bn;
+  int s = 1;
+  if (a->num_splits > 0) {
+    s = a->num_splits;
+  } else if (kv_tiles > 0) {
+    // as the prefill plan: split only when the tiles cover less than half the SMs
+    const long tiles = static_cast<long>(pl.n_qtiles) * a->Hkv * a->B;
+    const int sms = num_sms() > 0 ? num_sms() : 152;
+    if (tiles * 2 <= sms) {
+      s = static_cast<int>(sms / tiles);
+      const int cap = kv_tiles / 4 > 1 ? kv_tiles / 4 : 1;
+      if (s > cap) s = cap;
+    }
+  }
+  if (s > kv_tiles) s = kv_tiles;
+  if (s < 1) s = 1;
+  pl.n_splits = s;
+  if (s > 1) {
+    const size_t rows = static_cast<size_t>(a->B) * a->Hq * a->T;
+    pl.off_lse = (rows * s * a->D * sizeof(float) + 255) / 256 * 256;
+    pl.total = pl.off_lse + (rows * s * sizeof(float) + 255) / 256 * 256;
+  }
+  return pl;
+}
+
+int check_tree(const fa_tree_args* a, bool pointers) {
+  char msg[200];
+  if (!a) return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: null argument struct");
+  if (a->B < 0 || a->T < 0 || a->Hq <= 0 || a->Hkv <= 0 || a->Hq % a->Hkv != 0 || a->max_pages < 0 ||
+      a->num_pages < 0 || a->max_seq_len < 0 || a->num_splits < 0)
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: need B, T, max_pages, num_pages, max_seq_len, "
+                                   "num_splits >= 0, Hq, Hkv > 0, Hq % Hkv == 0");
+  if (a->Hq / a->Hkv > 128)
+    return bad(FA_ERR_UNSUPPORTED, "fa_tree_decode_paged: query heads per kv head must be <= 128");
+  if (a->D != 64 && a->D != 128 && a->D != 256) {
+    snprintf(msg, sizeof msg, "fa_tree_decode_paged: D must be 64, 128 or 256 (got %d)", a->D);
+    return bad(FA_ERR_UNSUPPORTED, msg);
+  }
+  if (a->T > kMaxTree) {
+    snprintf(msg, sizeof msg, "fa_tree_decode_paged: T must be <= %d (got %d)", kMaxTree, a->T);
+    return bad(FA_ERR_UNSUPPORTED, msg);
+  }
+  if (a->dtype != FA_BF16 && a->dtype != FA_FP16)
+    return bad(FA_ERR_UNSUPPORTED, "fa_tree_decode_paged: dtype must be FA_BF16 or FA_FP16");
+  if (a->cache_dtype != FA_E4M3 && a->cache_dtype != a->dtype)
+    return bad(FA_ERR_UNSUPPORTED, "fa_tree_decode_paged: cache_dtype must be FA_E4M3 or dtype");
+  const int bn = block_n(a->D);
+  if (a->page_size < 8 || a->page_size > bn || (a->page_size & (a->page_size - 1)) != 0) {
+    snprintf(msg, sizeof msg, "fa_tree_decode_paged: page_size must be a power of two in [8, %d] (got %d)",
+             bn, a->page_size);
+    return bad(FA_ERR_UNSUPPORTED, msg);
+  }
+  if (a->B > 65535 || a->Hkv > 65535)
+    return bad(FA_ERR_UNSUPPORTED, "fa_tree_decode_paged: B and Hkv must be <= 65535");
+  if (static_cast<int64_t>(a->num_pages) * a->Hkv > 2147483647LL ||
+      static_cast<int64_t>(a->max_pages) * a->page_size > 2147483647LL - 256)  // a tile past the end
+    return bad(FA_ERR_UNSUPPORTED, "fa_tree_decode_paged: num_pages * Hkv must fit in int32, and "
+               "max_pages * page_size + 256");
+  if (static_cast<int64_t>(a->B) * a->Hq * a->T > 2147483647LL)
+    return bad(FA_ERR_UNSUPPORTED, "fa_tree_decode_paged: B * Hq * T must fit in int32");
+  if (a->max_seq_len > static_cast<int64_t>(a->max_pages) * a->page_size)
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: max_seq_len exceeds max_pages * page_size");
+  if (!(a->scale == a->scale) || isinf(a->scale))
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: scale must be finite");
+  if (a->tree_mask && a->mask_batches != 1 && a->mask_batches != a->B)
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: mask_batches must be 1 or B");
+  if (!pointers || a->B == 0 || a->T == 0) return FA_OK;
+  if (!a->q || !a->out || !a->seq_lens ||
+      (a->max_seq_len > 0 && (!a->k_pages || !a->v_pages || !a->page_table || a->num_pages == 0)))
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: null pointer or no pages");
+  if (a->max_seq_len > 0 && a->cache_dtype == FA_E4M3 && (!a->k_scales || !a->v_scales))
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: an 8-bit cache needs k_scales and v_scales");
+  if (!aligned(a->q, 16) || !aligned(a->k_pages, 16) || !aligned(a->v_pages, 16) || !aligned(a->out, 16) ||
+      !aligned(a->tree_mask, 8) || !aligned(a->seq_lens, 4) || !aligned(a->draft_lens, 4) ||
+      !aligned(a->page_table, 4) || !aligned(a->lse, 4))
+    return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: q, the pages and out must be 16-byte aligned, "
+                                   "tree_mask 8-byte aligned");
+  // a tensor map takes strides of a multiple of 16 bytes, positive, below 2^40 bytes
+  const int n[3] = {a->B, a->Hq, a->T};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (a->q_strides[i] % 8 != 0 || a->q_strides[i] <= 0 || a->q_strides[i] >= (1LL << 39)))
+      return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: q's strides must be positive multiples of 16 bytes");
+  return FA_OK;
+}
+
+template <int D, int BN, int STAGES, int RAW, bool BF16, bool Q8>
+cudaError_t launch_impl(const fa_tree_args* a, const TreeParams& p, cudaStream_t st) {
+  using L = Layout<D, BN, STAGES, RAW, Q8>;
+  const CUtensorMapDataType dt = BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap tq, tk, tv;
+  {
+    // (column, query, head, sequence); the stride of a dimension of one is never used
+    const uint64_t dims[4] = {static_cast<uint64_t>(D), static_cast<uint64_t>(p.T),
+                              static_cast<uint64_t>(p.Hq), static_cast<uint64_t>(p.B)};
+    const uint64_t str[3] = {p.T > 1 ? static_cast<uint64_t>(a->q_strides[2]) * 2 : D * 2ull,
+                             p.Hq > 1 ? static_cast<uint64_t>(a->q_strides[1]) * 2 : D * 2ull,
+                             p.B > 1 ? static_cast<uint64_t>(a->q_strides[0]) * 2 : D * 2ull};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(p.q_per_tile), static_cast<uint32_t>(p.G), 1};
+    if (!encode_tiled(&tq, dt, 4, a->q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  const uint64_t ps = static_cast<uint64_t>(p.page_size), pages = static_cast<uint64_t>(p.num_pages) * p.Hkv;
+  if constexpr (Q8) {
+    // a page of one head: page_size rows of D bytes as (column, row, block of 128 columns)
+    constexpr uint64_t in = D < 128 ? D : 128;
+    const uint64_t dims[4] = {in, ps, D / in, pages}, str[3] = {D, in, ps * D};
+    const uint32_t box[4] = {static_cast<uint32_t>(in), static_cast<uint32_t>(ps), static_cast<uint32_t>(D / in), 1};
+    const CUtensorMapSwizzle swz = D < 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a->k_pages, dims, str, box, swz) ||
+        !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, a->v_pages, dims, str, box, swz))
+      return cudaErrorInvalidValue;
+  } else {
+    const uint64_t row = static_cast<uint64_t>(D) * 2;
+    const uint64_t dims[5] = {64, 8, static_cast<uint64_t>(D) / 64, ps / 8, pages};
+    const uint64_t str[4] = {row, 128, 8 * row, ps * row};
+    const uint32_t box[5] = {64, 8, static_cast<uint32_t>(D) / 64, static_cast<uint32_t>(ps) / 8, 1};
+    if (!encode_tiled(&tk, dt, 5, a->k_pages, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_tiled(&tv, dt, 5, a->v_pages, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  auto kern = p.n_splits > 1 ? tree_kernel<D, BN, STAGES, RAW, BF16, Q8, true>
+                             : tree_kernel<D, BN, STAGES, RAW, BF16, Q8, false>;
+  cudaError_t e = ensure_smem_limit(kern, L::kAlloc);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.n_qtiles * p.n_splits, p.Hkv, p.B);
+  kern<<<grid, L::kThreads, L::kAlloc, st>>>(tq, tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_tree(const fa_tree_args* a, const TreeParams& p, cudaStream_t st) {
+  if (a->cache_dtype == FA_E4M3) {
+    switch (a->D) {
+      case 64: return launch_impl<64, 128, 3, 3, BF16, true>(a, p, st);
+      case 128: return launch_impl<128, 128, 2, 2, BF16, true>(a, p, st);
+      default: return launch_impl<256, 64, 2, 1, BF16, true>(a, p, st);
+    }
+  }
+  switch (a->D) {
+    case 64: return launch_impl<64, 128, 5, 1, BF16, false>(a, p, st);
+    case 128: return launch_impl<128, 128, 3, 1, BF16, false>(a, p, st);
+    default: return launch_impl<256, 64, 2, 1, BF16, false>(a, p, st);
+  }
+}
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_tree_workspace_size(const fa_tree_args* a) {
+  if (check_tree(a, false) != FA_OK || a->B == 0 || a->T == 0) return 0;
+  return plan_tree(a).total;
+}
+
+int fa_tree_decode_paged(const fa_tree_args* a, void* stream) {
+  int rc = check_tree(a, true);
+  if (rc != FA_OK || a->B == 0 || a->T == 0) return rc;
+  const TreePlan pl = plan_tree(a);
+  char msg[200];
+  if (pl.total > 0) {
+    if (!a->workspace || a->workspace_bytes < pl.total) {
+      snprintf(msg, sizeof msg, "fa_tree_decode_paged: workspace of %zu bytes needed (got %zu)", pl.total,
+               a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
+      return bad(FA_ERR_WORKSPACE, msg);
+    }
+    if (!aligned(a->workspace, 256))
+      return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: workspace must be 256-byte aligned");
+  }
+  uint32_t* status = device_status_ptr();
+  if (!status) return bad(FA_ERR_CUDA, "fa_tree_decode_paged: no usable CUDA device");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  MergeParams m{};
+  m.out = a->out;
+  m.lse = a->lse;
+  m.rows = a->B * a->Hq * a->T;
+  m.D = a->D;
+  m.max_splits = pl.n_splits;
+  m.out_dtype = static_cast<Dtype>(a->dtype);
+  cudaError_t e;
+  if (a->max_seq_len == 0) {  // no key anywhere: the merge alone writes the empty rows
+    m.max_splits = 0;
+    e = launch_merge(m, st);
+    if (e != cudaSuccess) return bad(FA_ERR_CUDA, cudaGetErrorString(e));
+    return FA_OK;
+  }
+  TreeParams p{};
+  p.k_pages = a->k_pages;
+  p.v_pages = a->v_pages;
+  p.k_scales = a->k_scales;
+  p.v_scales = a->v_scales;
+  p.page_table = a->page_table;
+  p.kv_lens = a->seq_lens;
+  p.draft_lens = a->draft_lens;
+  p.mask = a->tree_mask;
+  p.out = a->out;
+  p.lse = a->lse;
+  p.mask_batches = a->mask_batches;
+  p.words = (a->T + 63) / 64;
+  p.B = a->B;
+  p.Hq = a->Hq;
+  p.Hkv = a->Hkv;
+  p.G = pl.G;
+  p.T = a->T;
+  p.q_per_tile = pl.q_per_tile;
+  p.n_qtiles = pl.n_qtiles;
+  p.n_splits = pl.n_splits;
+  p.page_size = a->page_size;
+  while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
+  p.max_pages = a->max_pages;
+  p.num_pages = a->num_pages;
+  p.scale_log2 = a->scale * 1.44269504088896340736f;
+  p.status = status;
+  if (pl.n_splits > 1) {
+    p.o_part = static_cast<float*>(a->workspace);
+    p.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + pl.off_lse);
+  }
+  e = a->dtype == FA_BF16 ? launch_tree<true>(a, p, st) : launch_tree<false>(a, p, st);
+  if (e != cudaSuccess) {
+    snprintf(msg, sizeof msg, "fa_tree_decode_paged (attention kernel): %s", cudaGetErrorString(e));
+    return bad(FA_ERR_CUDA, msg);
+  }
+  if (pl.n_splits > 1) {
+    m.o_part = p.o_part;
+    m.lse_part = p.lse_part;
+    e = launch_merge(m, st);
+    if (e != cudaSuccess) {
+      snprintf(msg, sizeof msg, "fa_tree_decode_paged (merge kernel): %s", cudaGetErrorString(e));
+      return bad(FA_ERR_CUDA, msg);
+    }
+  }
+  return FA_OK;
+}
+
+}  // extern "C"

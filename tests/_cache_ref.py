@@ -99,27 +99,63 @@ def rows_of(pages, table, b, n):
 
 def tree_attention(q, k_rows, v_rows, draft_lens, mask, scale):
     """q [B,Hq,T,D]; k_rows, v_rows: per sequence [len,Hkv,D] fp64; mask: per sequence a boolean
-    [n,n] (query, drafted token) or None for a chain.  Returns out, lse in fp64; hidden keys
-    take no part at all, whatever they hold."""
+    [n,n] (query, drafted token) or None for a chain.  Returns, in fp64, out, lse, and what the
+    error bounds need: sum_j w_j |v_j| (as out), the largest scale sum_d |q_d k_d| of a row (as lse) and sum_j |v_j|.  Hidden keys take no part at all, whatever they hold."""
     B, Hq, T, D = q.shape
     out = torch.zeros(B, Hq, T, D, dtype=torch.float64)
     lse = torch.full((B, Hq, T), -math.inf, dtype=torch.float64)
+    mean_abs, sum_abs = torch.zeros_like(out), torch.zeros_like(out)
+    reach = torch.zeros(B, Hq, T, dtype=torch.float64)
     for b in range(B):
         n, L = draft_lens[b], k_rows[b].shape[0]
-        G = Hq // k_rows[b].shape[1] if L else 1
+        G = Hq // k_rows[b].shape[1]
         for i in range(n):
             seen = torch.ones(L, dtype=torch.bool)
-            tail = torch.arange(n) <= i if mask is None else mask[b][i, :n]
-            seen[L - n:] = tail
+            seen[L - n:] = torch.arange(n) <= i if mask is None else mask[b][i, :n]
             if not seen.any():
                 continue
             k, v = k_rows[b][seen], v_rows[b][seen]
             for h in range(Hq):
-                s = (k[:, h // G] @ q[b, h, i].double().cpu()) * scale
+                x = q[b, h, i].double().cpu()
+                s = (k[:, h // G] @ x) * scale
                 m = s.max()
                 if m == -math.inf:
                     continue
                 w = (s - m).exp()
                 out[b, h, i] = (w[:, None] * v[:, h // G]).sum(0) / w.sum()
                 lse[b, h, i] = m + w.sum().log()
-    return out, lse
+                mean_abs[b, h, i] = (w[:, None] * v[:, h // G].abs()).sum(0) / w.sum()
+                sum_abs[b, h, i] = v[:, h // G].abs().sum(0)
+                reach[b, h, i] = (k[:, h // G].abs() @ x.abs()).max() * abs(scale)
+    return out, lse, mean_abs, reach, sum_abs
+
+
+def check_tree(out, lse, want, dtype, D, what=""):
+    """The kernel's out and lse against tree_attention's.
+
+    A score is a sum of D products of 16-bit values in fp32, in the tensor core's own order and
+    with its own truncation: each of the D additions is off by at most 2^-23 of the running
+    sum, which sum |q_d k_d| bounds; times the scale, minus the maximum, through 2^x (2^-22):
+    delta below bounds the relative error of a weight, once in the numerator and once in the
+    sum.  A weight is rounded to dtype on its way into the second product (half a step), the
+    output once at its end.  An fp16 weight below 2^-14 has an absolute rounding, 2^-25, of a
+    weight held 2^7 times larger, where the row's largest is at least 1 (and so the sum by
+    which it is divided): 2^-32 sum_j |v_j| in all."""
+    o, l, mean_abs, reach, sum_abs = want
+    out, lse = out.double().cpu(), lse.double().cpu()
+    half = torch.finfo(dtype).eps / 2
+    delta = (D + 8) * 2.0 ** -23 * reach + 2.0 ** -20
+    tiny = torch.finfo(dtype).tiny
+    bound = (half + 2 * delta[..., None]) * mean_abs + half * o.abs() + tiny
+    if dtype == torch.float16:
+        bound = bound + 2.0 ** -32 * sum_abs
+    empty = l == -math.inf
+    assert torch.equal(empty, lse == -math.inf), f"{what}: other rows are empty"
+    assert (out[empty] == 0).all(), f"{what}: empty rows"
+    fin = torch.isfinite(o)
+    assert torch.equal(torch.isnan(o), torch.isnan(out)), f"{what}: NaN elsewhere"
+    bad = ((out - o).abs() > bound) & fin
+    assert not bad.any(), f"{what}: {int(bad.sum())} off, {((out - o).abs() / bound)[fin].max():.2f} of the bound"
+    dl = (lse - l).abs()[~empty & torch.isfinite(l)]
+    bl = (delta + 2.0 ** -21 * l.abs())[~empty & torch.isfinite(l)]
+    assert (dl <= bl).all(), f"{what}: lse off by {(dl / bl).max():.2f} of the bound"
