@@ -22,6 +22,7 @@ import contextlib
 import ctypes
 import math
 import os
+import struct
 import threading
 
 import torch
@@ -244,15 +245,15 @@ def load_library(path: str | None = None):
         lib.gated_delta_workspace_size.restype = _sz
         lib.gated_delta_workspace_size.argtypes = [ctypes.POINTER(GatedDeltaArgs)]
         lib.fa_rotary.restype = _i
-        lib.fa_rotary.argtypes = [ctypes.POINTER(RotaryArgs), _vp]
+        lib.fa_rotary.argtypes = [_vp, _vp]
         lib.fa_cache_append.restype = _i
-        lib.fa_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs), _vp]
+        lib.fa_cache_append.argtypes = [_vp, _vp]
         lib.fa_cache_gather.restype = _i
-        lib.fa_cache_gather.argtypes = [ctypes.POINTER(CacheGatherArgs), _vp]
+        lib.fa_cache_gather.argtypes = [_vp, _vp]
         lib.fa_tree_decode_paged.restype = _i
-        lib.fa_tree_decode_paged.argtypes = [ctypes.POINTER(TreeArgs), _vp]
+        lib.fa_tree_decode_paged.argtypes = [_vp, _vp]
         lib.fa_tree_workspace_size.restype = _sz
-        lib.fa_tree_workspace_size.argtypes = [ctypes.POINTER(TreeArgs)]
+        lib.fa_tree_workspace_size.argtypes = [_vp]
         _lib = lib
         return lib
 
@@ -682,13 +683,31 @@ def gated_delta_prefill(q, k, v, g, beta, *, scale=None, initial_state=None, out
 # workspace) on the stream they launch on.
 # ------------------------------------------------------------------------------------------
 _CACHE_DT = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16, torch.float8_e4m3fn: FA_E4M3}
+_STRUCT_CODE = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_size_t: "N",
+                _Strides: "3q"}
+
+
+def _packer(cls):
+    """pack() of a structure's fields in order (arrays flattened): about a third of the time of
+    filling a ctypes structure, which a decode step of a few microseconds feels."""
+    st = struct.Struct("@" + "".join(_STRUCT_CODE[t] for _, t in cls._fields_))
+    assert st.size <= ctypes.sizeof(cls) < st.size + 8  # C pads the end, struct does not
+    pad = bytes(ctypes.sizeof(cls) - st.size)
+    return (lambda *a: st.pack(*a) + pad) if pad else st.pack
+
+
+_pack_rotary, _pack_append, _pack_gather, _pack_tree = map(
+    _packer, (RotaryArgs, CacheAppendArgs, CacheGatherArgs, TreeArgs))
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
+    torch._C, "_cuda_getCurrentRawStream") else (
+        lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 class _Scope:
     """The device of a call's tensors and the stream it launches on, made current."""
 
-    def __init__(self, device, stream):
-        self.device = torch.cuda.device(device)
+    def __init__(self, dev, stream):
+        self.device = torch.cuda.device(dev)
         self.stream = torch.cuda.stream(stream)
 
     def __enter__(self):
@@ -703,52 +722,44 @@ class _Scope:
 _here = contextlib.nullcontext()
 
 
-def _scope(device, stream):
+def _scope(dev, stream):
     if stream is None:
-        return _here if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    return _Scope(device, stream)
+        return _here if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{dev}")
+    return _Scope(dev, stream)
 
 
-def _current_stream(device):
-    return torch.cuda.current_stream(device).cuda_stream
+def _cuda_index(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    return t.get_device()
 
 
-def _check_side(device, contiguous=(), rows=()):
-    """Every tensor on `device`; `contiguous` ones whole, `rows` with a contiguous last
-    dimension (their other strides go to the call)."""
-    for t in contiguous:
-        if t is not None and (t.device != device or not t.is_contiguous()):
+def _on(dev, *ts):
+    """Contiguous tensors on device `dev` (None passes)."""
+    for t in ts:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             raise ValueError("tensors must be contiguous CUDA tensors on one device")
-    for t in rows:
-        if t is not None and (t.device != device or (t.stride(-1) != 1 and t.shape[-1] > 1)):
-            raise ValueError("tensors must be CUDA tensors on one device with a contiguous last "
-                             "dimension")
+
+
+def _strides_on(dev, t):
+    """(batch, head, token) strides of a 4-D tensor on `dev` with a contiguous last dimension; 0
+    for a dimension of one element, where torch may report anything."""
+    s, n = t.stride(), t.shape
+    if t.get_device() != dev or (s[3] != 1 and n[3] > 1):
+        raise ValueError("tensors must be CUDA tensors on one device with a contiguous last "
+                         "dimension")
+    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
 
 
 def _shape(name, t, *want):
-    if t is not None and tuple(t.shape) != want:
+    if t is not None and t.shape != want:
         raise ValueError(f"{name} must have shape {want}, got {tuple(t.shape)}")
 
 
-def _cuda_device(t):
-    if not t.is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    return t.device
-
-
 def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _row_strides(t):
-    # the stride of a dimension of one element is never used: torch may report anything there
-    s, n = t.stride(), t.shape
-    return _Strides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
-
-
-_NO_STRIDES = _Strides(0, 0, 0)
+    return 0 if t is None else t.data_ptr()
 
 
 def fa_rotary(q, k, positions, inv_freq, *, amplitude: float = 1.0, interleaved: bool = False,
@@ -759,48 +770,49 @@ def fa_rotary(q, k, positions, inv_freq, *, amplitude: float = 1.0, interleaved:
     the rest copied.  transpose=True applies the transposed map, the gradient of the call.  q_out
     and k_out may be q and k themselves.  Returns (q_out, k_out)."""
     lib = load_library()
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     B, Hq, T, D = q.shape
-    Hk = 0
+    Hk = 0 if k is None else k.shape[1]
     _need_dtype(q.dtype, k, q_out, k_out)
     _need_dtype(torch.int32, positions)
     _need_dtype(torch.float64, inv_freq)
     if q.dtype not in _DT:
         raise TypeError(f"unsupported dtype {q.dtype}")
-    if k is not None:
-        Hk = k.shape[1]
-        _shape("k", k, B, Hk, T, D)
-        _shape("k_out", k_out, B, Hk, T, D)
+    _shape("k", k, B, Hk, T, D)
     _shape("q_out", q_out, B, Hq, T, D)
+    _shape("k_out", k_out, B, Hk, T, D)
     _shape("positions", positions, B, T)
-    _check_side(dev, (positions, inv_freq), (q, k, q_out, k_out))
+    _on(dev, positions, inv_freq)
+    none = (0, 0, 0)
     with _scope(dev, stream):
         if q_out is None:
-            q_out = torch.empty((B, Hq, T, D), dtype=q.dtype, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty((B, Hk, T, D), dtype=q.dtype, device=dev)
-        a = RotaryArgs(q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out), _row_strides(q),
-                       _NO_STRIDES if k is None else _row_strides(k), _row_strides(q_out),
-                       _NO_STRIDES if k is None else _row_strides(k_out), positions.data_ptr(),
-                       inv_freq.data_ptr(), B, T, Hq, Hk, D, 2 * inv_freq.numel(),
-                       interleaved, transpose, amplitude, _DT[q.dtype])
-        _check(lib.fa_rotary(ctypes.byref(a), _current_stream(dev)))
+            q_out = torch.empty((B, Hq, T, D), dtype=q.dtype, device=q.device)
+        if k is None:
+            k_out = None
+        elif k_out is None:
+            k_out = torch.empty((B, Hk, T, D), dtype=q.dtype, device=q.device)
+        a = _pack_rotary(q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
+                         *_strides_on(dev, q), *(none if k is None else _strides_on(dev, k)),
+                         *_strides_on(dev, q_out), *(none if k is None else _strides_on(dev, k_out)),
+                         positions.data_ptr(), inv_freq.data_ptr(), B, T, Hq, Hk, D,
+                         2 * inv_freq.numel(), interleaved, transpose, amplitude, _DT[q.dtype])
+        _check(lib.fa_rotary(a, _raw_stream(dev)))
     return q_out, k_out
 
 
 def _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B):
     """(num_pages, Hkv, page_size, D) of a paged cache, its tensors checked."""
-    if k_pages.dtype not in _CACHE_DT:
-        raise ValueError(f"pages must be bfloat16, float16 or float8_e4m3fn, got {k_pages.dtype}")
-    _need_dtype(k_pages.dtype, v_pages)
+    dtype, shape = k_pages.dtype, k_pages.shape
+    if dtype not in _CACHE_DT:
+        raise ValueError(f"pages must be bfloat16, float16 or float8_e4m3fn, got {dtype}")
+    _need_dtype(dtype, v_pages)
     _need_dtype(torch.int32, page_table)
-    shape = tuple(k_pages.shape)
     if len(shape) != 4:
-        raise ValueError(f"pages must be [num_pages, Hkv, page_size, D], got {shape}")
+        raise ValueError(f"pages must be [num_pages, Hkv, page_size, D], got {tuple(shape)}")
     _shape("v_pages", v_pages, *shape)
     if page_table.dim() != 2 or page_table.shape[0] != B:
         raise ValueError(f"page_table must be [{B}, max_pages], got {tuple(page_table.shape)}")
-    if k_pages.dtype == torch.float8_e4m3fn:
+    if dtype == torch.float8_e4m3fn:
         if k_scales is None or v_scales is None:
             raise ValueError("an 8-bit cache needs k_scales and v_scales")
         _need_dtype(torch.uint8, k_scales, v_scales)
@@ -808,7 +820,7 @@ def _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B):
         _shape("v_scales", v_scales, *shape[:3])
     elif k_scales is not None or v_scales is not None:
         raise ValueError("scales belong to an 8-bit cache")
-    _check_side(dev, (k_pages, v_pages, k_scales, v_scales, page_table))
+    _on(dev, k_pages, v_pages, k_scales, v_scales, page_table)
     return shape
 
 
@@ -822,7 +834,7 @@ def fa_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, *, new_lens=No
     [rot_dim/2] fp64 the keys are rotated on the way, at positions [B,T] int32 (default: the
     position in the cache)."""
     lib = load_library()
-    dev = _cuda_device(k)
+    dev = _cuda_index(k)
     B, Hkv, T, D = k.shape
     if k.dtype not in _DT:
         raise TypeError(f"unsupported dtype {k.dtype}")
@@ -835,15 +847,15 @@ def fa_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, *, new_lens=No
     _shape("positions", positions, B, T)
     P, _, ps, _ = _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B)
     _shape("k_pages", k_pages, P, Hkv, ps, D)
-    _check_side(dev, (seq_lens, new_lens, positions, inv_freq), (k, v))
+    _on(dev, seq_lens, new_lens, positions, inv_freq)
+    a = _pack_append(k.data_ptr(), v.data_ptr(), *_strides_on(dev, k), *_strides_on(dev, v),
+                     k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales), _addr(v_scales),
+                     page_table.data_ptr(), seq_lens.data_ptr(), _addr(new_lens), _addr(positions),
+                     _addr(inv_freq), B, T, Hkv, D, ps, page_table.shape[1], P,
+                     0 if inv_freq is None else 2 * inv_freq.numel(), interleaved, amplitude,
+                     _DT[k.dtype], _CACHE_DT[k_pages.dtype])
     with _scope(dev, stream):
-        a = CacheAppendArgs(k.data_ptr(), v.data_ptr(), _row_strides(k), _row_strides(v),
-                            k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales),
-                            _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
-                            _addr(new_lens), _addr(positions), _addr(inv_freq), B, T, Hkv, D, ps,
-                            page_table.shape[1], P, 0 if inv_freq is None else 2 * inv_freq.numel(),
-                            interleaved, amplitude, _DT[k.dtype], _CACHE_DT[k_pages.dtype])
-        _check(lib.fa_cache_append(ctypes.byref(a), _current_stream(dev)))
+        _check(lib.fa_cache_append(a, _raw_stream(dev)))
 
 
 def fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len: int, *,
@@ -852,7 +864,7 @@ def fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len: int, *,
     """Read a paged cache (bf16, fp16, or float8_e4m3fn with its scales) back as dense k, v
     [B,Hkv,max_seq_len,D] in dtype; rows at and past seq_lens[b] are zero."""
     lib = load_library()
-    dev = _cuda_device(k_pages)
+    dev = _cuda_index(k_pages)
     B, L = seq_lens.shape[0], int(max_seq_len)
     if dtype not in _DT:
         raise TypeError(f"unsupported dtype {dtype}")
@@ -862,17 +874,17 @@ def fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len: int, *,
     P, Hkv, ps, D = _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B)
     _shape("k", k, B, Hkv, L, D)
     _shape("v", v, B, Hkv, L, D)
-    _check_side(dev, (seq_lens, k, v))
+    _on(dev, seq_lens, k, v)
     with _scope(dev, stream):
         if k is None:
-            k = torch.empty((B, Hkv, L, D), dtype=dtype, device=dev)
+            k = torch.empty((B, Hkv, L, D), dtype=dtype, device=k_pages.device)
         if v is None:
-            v = torch.empty((B, Hkv, L, D), dtype=dtype, device=dev)
-        a = CacheGatherArgs(k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales),
-                            _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
-                            k.data_ptr(), v.data_ptr(), B, Hkv, D, ps, page_table.shape[1], P, L,
-                            _DT[dtype], _CACHE_DT[k_pages.dtype])
-        _check(lib.fa_cache_gather(ctypes.byref(a), _current_stream(dev)))
+            v = torch.empty((B, Hkv, L, D), dtype=dtype, device=k_pages.device)
+        a = _pack_gather(k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scales), _addr(v_scales),
+                         page_table.data_ptr(), seq_lens.data_ptr(), k.data_ptr(), v.data_ptr(), B,
+                         Hkv, D, ps, page_table.shape[1], P, L, _DT[dtype],
+                         _CACHE_DT[k_pages.dtype])
+        _check(lib.fa_cache_gather(a, _raw_stream(dev)))
     return k, v
 
 
@@ -888,7 +900,7 @@ def fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len:
     (None: a chain).  T = 1 is the decode of one token a sequence.  Returns (out [B,Hq,T,D], lse
     [B,Hq,T] fp32)."""
     lib = load_library()
-    dev = _cuda_device(q)
+    dev = _cuda_index(q)
     B, Hq, T, D = q.shape
     if q.dtype not in (torch.bfloat16, torch.float16):
         raise ValueError(f"expected bfloat16 or float16, got {q.dtype}")
@@ -901,27 +913,29 @@ def fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len:
     _shape("out", out, B, Hq, T, D)
     _shape("lse", lse, B, Hq, T)
     P, Hkv, ps, Dk = _check_cache(dev, k_pages, v_pages, k_scales, v_scales, page_table, B)
-    if Dk != D or (k_pages.dtype != q.dtype and k_scales is None):
+    if Dk != D or (k_scales is None and k_pages.dtype != q.dtype):
         raise ValueError(f"pages of {Dk} columns in {k_pages.dtype} do not go with q's {D} in {q.dtype}")
-    if tree_mask is not None and (tree_mask.dim() != 3 or tree_mask.shape[0] not in (1, B) or
-                                  tuple(tree_mask.shape[1:]) != (T, -(-T // 64))):
-        raise ValueError(f"tree_mask must be [1 or {B}, {T}, {-(-T // 64)}], got {tuple(tree_mask.shape)}")
-    _check_side(dev, (seq_lens, draft_lens, tree_mask, out, lse, workspace), (q,))
+    masks = 0
+    if tree_mask is not None:
+        masks = tree_mask.shape[0]
+        if masks not in (1, B) or tree_mask.shape[1:] != (T, -(-T // 64)):
+            raise ValueError(f"tree_mask must be [1 or {B}, {T}, {-(-T // 64)}], got {tuple(tree_mask.shape)}")
+    _on(dev, seq_lens, draft_lens, tree_mask, out, lse, workspace)
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((B, Hq, T, D), dtype=q.dtype, device=dev)
+            out = torch.empty((B, Hq, T, D), dtype=q.dtype, device=q.device)
         if lse is None:
-            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=dev)
-        a = TreeArgs(q.data_ptr(), _row_strides(q), k_pages.data_ptr(), v_pages.data_ptr(),
-                     _addr(k_scales), _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
-                     _addr(draft_lens), _addr(tree_mask), out.data_ptr(), lse.data_ptr(), B, Hq,
-                     Hkv, T, D, ps, page_table.shape[1], P, int(max_seq_len),
-                     0 if tree_mask is None else tree_mask.shape[0], int(num_splits),
-                     1.0 / math.sqrt(D) if scale is None else scale, _DT[q.dtype],
-                     _CACHE_DT[k_pages.dtype])
-        ws = _workspace(lib.fa_tree_workspace_size(ctypes.byref(a)), dev, workspace)
-        if ws is not None:
-            a.workspace = ws.data_ptr()
-            a.workspace_bytes = ws.numel() * ws.element_size()
-        _check(lib.fa_tree_decode_paged(ctypes.byref(a), _current_stream(dev)))
+            lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        fields = (q.data_ptr(), *_strides_on(dev, q), k_pages.data_ptr(), v_pages.data_ptr(),
+                  _addr(k_scales), _addr(v_scales), page_table.data_ptr(), seq_lens.data_ptr(),
+                  _addr(draft_lens), _addr(tree_mask), out.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
+                  T, D, ps, page_table.shape[1], P, int(max_seq_len), masks, int(num_splits),
+                  1.0 / math.sqrt(D) if scale is None else scale, _DT[q.dtype],
+                  _CACHE_DT[k_pages.dtype])
+        a = _pack_tree(*fields, 0, 0)
+        need = lib.fa_tree_workspace_size(a)
+        if need:
+            ws = _workspace(need, q.device, workspace)
+            a = _pack_tree(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
+        _check(lib.fa_tree_decode_paged(a, _raw_stream(dev)))
     return out, lse

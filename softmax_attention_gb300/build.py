@@ -13,9 +13,9 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfa.so")
 SOURCES = ["abi.cu", "prefill.cu", "decode.cu", "decode_noalloc.cu", "mla.cu", "merge.cu",
            "selftest.cu", "gated_delta.cu", "prefill_f32.cu", "cache.cu",
-           "tree.cu"]
+           "tree.cu", "tree_rows.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "sm103.cuh", "prefill_common.cuh",
-                                            "cache.cuh")] + [
+                                            "cache.cuh", "tree.cuh")] + [
     os.path.join(ROOT, "include", "fa.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")

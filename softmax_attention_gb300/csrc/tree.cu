@@ -24,39 +24,20 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <type_traits>
+
 #include "../../include/fa.h"
 #include "cache.cuh"
 #include "internal.h"
 #include "prefill_common.cuh"
 #include "sm103.cuh"
+#include "tree.cuh"
 
 namespace fa {
 namespace {
 
 using prefill::kRows;
-constexpr int kNumS = 3;       // S/P buffers in tensor memory
-constexpr int kMaxTree = 256;  // drafted tokens
-
-struct TreeParams {
-  const void* k_pages;
-  const void* v_pages;
-  const uint8_t* k_scales;
-  const uint8_t* v_scales;
-  const int32_t* page_table;
-  const int32_t* kv_lens;
-  const int32_t* draft_lens;    // or nullptr: T each
-  const uint64_t* mask;         // [mask_batches, T, words], or nullptr: a chain
-  void* out;                    // [B,Hq,T,D]
-  float* lse;                   // [B,Hq,T] or nullptr
-  float* o_part;                // split: [B*Hq*T, n_splits, D] fp32
-  float* lse_part;              // split: [B*Hq*T, n_splits]
-  int mask_batches, words;
-  int B, Hq, Hkv, G, T;
-  int q_per_tile, n_qtiles, n_splits;
-  int page_size, page_shift, max_pages, num_pages;
-  float scale_log2;
-  uint32_t* status;
-};
+constexpr int kNumS = 3;  // S/P buffers in tensor memory
 
 template <int D, int BN, int STAGES, int RAW, bool Q8>
 struct Layout {
@@ -78,41 +59,6 @@ struct Layout {
   static_assert(D + kNumS * BN <= 512, "tensor memory budget (O and the S/P buffers)");
   static_assert(kAlloc <= 232448, "shared memory budget");
 };
-
-// ------------------------------------------------------------------------------------------
-// The mask of one query row over the drafted tokens.
-// ------------------------------------------------------------------------------------------
-struct TreeRow {
-  const uint64_t* words;  // the row's mask words, or nullptr: a chain (tokens 0..i)
-  int i, n;               // query, drafted tokens
-};
-
-__device__ __forceinline__ uint64_t row_word(const TreeRow& r, int w) {
-  const int left = r.n - 64 * w;  // drafted tokens from this word on
-  if (left <= 0) return 0;
-  uint64_t v = ~0ull;
-  if (r.words) {
-    v = __ldg(reinterpret_cast<const unsigned long long*>(r.words + w));
-  } else {
-    const int c = r.i + 1 - 64 * w;
-    v = c >= 64 ? ~0ull : c > 0 ? (1ull << c) - 1 : 0ull;
-  }
-  return left >= 64 ? v : v & ((1ull << left) - 1);
-}
-
-// Visibility of the 32 keys from drafted offset `off` on (negative: still in the context).
-__device__ __forceinline__ uint32_t row_bits(const TreeRow& r, int off) {
-  if (off <= -32) return ~0u;
-  if (off < 0) return (static_cast<uint32_t>(row_word(r, 0)) << -off) | ((1u << -off) - 1);
-  const int w = off >> 6, s = off & 63;
-  uint64_t v = row_word(r, w) >> s;
-  if (s > 32) v |= row_word(r, w + 1) << (64 - s);
-  return static_cast<uint32_t>(v);
-}
-
-__device__ __forceinline__ bool row_sees(const TreeRow& r, int d) {
-  return (row_word(r, d >> 6) >> (d & 63)) & 1;
-}
 
 // ------------------------------------------------------------------------------------------
 // One KV tile of the online softmax for one row (prefill::softmax_tile with a bit mask in
@@ -216,14 +162,14 @@ __device__ __forceinline__ RowScale row_scale(uint32_t byte) {
   return s;
 }
 
-// Four e4m3 codes -> two packed pairs, scaled.
-template <bool BF16>
+// Four e4m3 codes -> two packed pairs, scaled (TWO: by both factors).
+template <bool BF16, bool TWO>
 __device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& lo, uint32_t& hi) {
   if constexpr (BF16) {
     const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
     lo = mul_bf16x2(((a >> 4) & 0x07f007f0u) | (a & 0x80008000u), s.f1);
     hi = mul_bf16x2(((b >> 4) & 0x07f007f0u) | (b & 0x80008000u), s.f1);
-    if (s.two) {
+    if constexpr (TWO) {
       lo = mul_bf16x2(lo, s.f2);
       hi = mul_bf16x2(hi, s.f2);
     }
@@ -232,38 +178,10 @@ __device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& 
     const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
     lo = mul_f16x2(static_cast<uint32_t>(a.x) | (static_cast<uint32_t>(a.y) << 16), s.f1);
     hi = mul_f16x2(static_cast<uint32_t>(b.x) | (static_cast<uint32_t>(b.y) << 16), s.f1);
-    if (s.two) {
+    if constexpr (TWO) {
       lo = mul_f16x2(lo, s.f2);
       hi = mul_f16x2(hi, s.f2);
     }
-  }
-}
-
-// A NaN code (0x7f or 0xff) turns its sign bit over when one is added to every byte; a carry
-// out of 0xff can only add further marks.  Sign bits of the result: some byte is NaN.
-__device__ __forceinline__ uint32_t nan_mark(uint32_t acc, uint32_t w) {
-  return acc | ((w + 0x01010101u) ^ w);
-}
-
-__device__ __forceinline__ bool nonfinite16(uint32_t h, bool bf16) {
-  return bf16 ? (h & 0x7f80u) == 0x7f80u : (h & 0x7c00u) == 0x7c00u;
-}
-
-// Value of V at drafted token d, column c, if it is not finite (else 0): the slow path of a row
-// that sees a drafted token with such a value.
-template <int D, bool BF16, bool Q8>
-__device__ __noinline__ float nonfinite_v(const TreeParams& p, int b, int hk, int key, int c) {
-  const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + (key >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) return 0.f;
-  const int64_t at = ((static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1))) * D + c;
-  if constexpr (Q8) {
-    const uint32_t v = static_cast<const uint8_t*>(p.v_pages)[at];
-    return (v & 0x7fu) == 0x7fu ? __uint_as_float(0x7fc00000u) : 0.f;
-  } else {
-    const uint16_t h = static_cast<const uint16_t*>(p.v_pages)[at];
-    if (!nonfinite16(h, BF16)) return 0.f;
-    return BF16 ? __uint_as_float(static_cast<uint32_t>(h) << 16)
-                : __half2float(__ushort_as_half(h));
   }
 }
 
@@ -531,23 +449,29 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         const RowScale s = row_scale<BF16>(byte);
         uint32_t marks = 0;
         constexpr int kChunks = D / 16 / kParts;
+        auto widen = [&](auto two_c) {
+          constexpr bool TWO = decltype(two_c)::value;
 #pragma unroll
-        for (int c8 = 0; c8 < kChunks; ++c8) {
-          const int c = part * kChunks + c8;        // 16 columns from 16c on
-          const int blk = c / (kIn / 16), ci = c % (kIn / 16);
-          uint4 w = *reinterpret_cast<const uint4*>(raw + raw_row + blk * raw_blk + ((ci ^ raw_swz) * 16));
-          if (!inside) w = make_uint4(0, 0, 0, 0);
-          uint4 x, y;
-          widen4<BF16>(w.x, s, x.x, x.y);
-          widen4<BF16>(w.y, s, x.z, x.w);
-          widen4<BF16>(w.z, s, y.x, y.y);
-          widen4<BF16>(w.w, s, y.z, y.w);
-          marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w.x), w.y), w.z), w.w);
-          uint8_t* d = dst + out_row + (c / 4) * kCB;
-          const int ch = (c % 4) * 2;
-          *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) * 16)) = x;
-          *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) * 16)) = y;
-        }
+          for (int c8 = 0; c8 < kChunks; ++c8) {
+            const int c = part * kChunks + c8;        // 16 columns from 16c on
+            const int blk = c / (kIn / 16), ci = c % (kIn / 16);
+            uint4 w = *reinterpret_cast<const uint4*>(raw + raw_row + blk * raw_blk + ((ci ^ raw_swz) * 16));
+            if (!inside) w = make_uint4(0, 0, 0, 0);
+            uint4 x, y;
+            widen4<BF16, TWO>(w.x, s, x.x, x.y);
+            widen4<BF16, TWO>(w.y, s, x.z, x.w);
+            widen4<BF16, TWO>(w.z, s, y.x, y.y);
+            widen4<BF16, TWO>(w.w, s, y.z, y.w);
+            marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w.x), w.y), w.z), w.w);
+            uint8_t* d = dst + out_row + (c / 4) * kCB;
+            const int ch = (c % 4) * 2;
+            *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) * 16)) = x;
+            *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) * 16)) = y;
+          }
+        };
+        // a warp whose scales all stay within one factor (the usual case) takes one product
+        if (__any_sync(0xffffffffu, s.two)) widen(std::true_type{});
+        else widen(std::false_type{});
         if (marks & 0x80808080u) {
           // NaN codes (rare): put NaN where they are, or, in a drafted token's V, zero, and note
           // the token: a weight of 0 would still carry a NaN into rows that do not see it
@@ -788,8 +712,11 @@ bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) 
 
 struct TreePlan {
   int G, q_per_tile, n_qtiles, n_splits;
+  bool few_rows;  // the kernel of tree_rows.cu
   size_t off_lse, total;
 };
+
+constexpr int kFewRowsTokens = 256;  // least tokens of a part in the kernel for few rows
 
 // KV tile of a head dimension: as the prefill kernels', what tensor memory holds beside O.
 int block_n(int D) { return D == 256 ? 64 : 128; }
@@ -802,11 +729,19 @@ TreePlan plan_tree(const fa_tree_args* a) {
   pl.n_qtiles = (a->T + most - 1) / most;
   pl.q_per_tile = (a->T + pl.n_qtiles - 1) / pl.n_qtiles;
   pl.n_qtiles = (a->T + pl.q_per_tile - 1) / pl.q_per_tile;
-  const int bn = block_n(a->D);
+  const int rows = pl.G * a->T;
+  pl.few_rows = a->cache_dtype == FA_E4M3 && tree_rows_takes(rows, a->D);
+  const int bn = pl.few_rows ? kFewRowsTokens : block_n(a->D);
   const int kv_tiles = (a->max_seq_len + bn - 1) / bn;
   int s = 1;
   if (a->num_splits > 0) {
     s = a->num_splits;
+  } else if (pl.few_rows) {
+    // its CTAs are small and several share an SM: split while the units leave half of them free,
+    // down to kFewRowsTokens tokens a part
+    const long units = static_cast<long>(a->Hkv) * a->B;
+    const int slots = tree_rows_slots(rows, a->D);
+    if (units > 0 && units * 2 <= slots) s = static_cast<int>(slots / units);
   } else if (kv_tiles > 0) {
     // as the prefill plan: split only when the tiles cover less than half the SMs
     const long tiles = static_cast<long>(pl.n_qtiles) * a->Hkv * a->B;
@@ -821,9 +756,9 @@ TreePlan plan_tree(const fa_tree_args* a) {
   if (s < 1) s = 1;
   pl.n_splits = s;
   if (s > 1) {
-    const size_t rows = static_cast<size_t>(a->B) * a->Hq * a->T;
-    pl.off_lse = (rows * s * a->D * sizeof(float) + 255) / 256 * 256;
-    pl.total = pl.off_lse + (rows * s * sizeof(float) + 255) / 256 * 256;
+    const size_t all = static_cast<size_t>(a->B) * a->Hq * a->T;
+    pl.off_lse = (all * s * a->D * sizeof(float) + 255) / 256 * 256;
+    pl.total = pl.off_lse + (all * s * sizeof(float) + 255) / 256 * 256;
   }
   return pl;
 }
@@ -1022,7 +957,15 @@ int fa_tree_decode_paged(const fa_tree_args* a, void* stream) {
     p.o_part = static_cast<float*>(a->workspace);
     p.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + pl.off_lse);
   }
-  e = a->dtype == FA_BF16 ? launch_tree<true>(a, p, st) : launch_tree<false>(a, p, st);
+  if (pl.few_rows) {
+    p.q = a->q;
+    p.q_strides[0] = a->B > 1 ? a->q_strides[0] : 0;
+    p.q_strides[1] = a->Hq > 1 ? a->q_strides[1] : 0;
+    p.q_strides[2] = a->T > 1 ? a->q_strides[2] : 0;
+    e = launch_tree_rows(p, a->D, a->dtype == FA_BF16, st);
+  } else {
+    e = a->dtype == FA_BF16 ? launch_tree<true>(a, p, st) : launch_tree<false>(a, p, st);
+  }
   if (e != cudaSuccess) {
     snprintf(msg, sizeof msg, "fa_tree_decode_paged (attention kernel): %s", cudaGetErrorString(e));
     return bad(FA_ERR_CUDA, msg);
