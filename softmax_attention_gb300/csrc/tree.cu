@@ -18,8 +18,9 @@
 // 16-bit queries and weights whole, which 8-bit MMAs would not.
 //
 // Warp roles: 0-3 softmax + epilogue (thread t owns row t), 4 TMA producer, 5 P V issuer and
-// tensor-memory owner, 6 S issuer, and for 8-bit pages 8-11 converters (7 idle, so that the
-// converters are a warpgroup of their own).
+// tensor-memory owner, 6 S issuer, and for 8-bit pages 8-11 converters of K, 12-15 of V (7
+// idle).  With 512 threads a thread has 128 registers, so there the softmax reads its row of
+// scores in two halves.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -41,7 +42,7 @@ constexpr int kNumS = 3;  // S/P buffers in tensor memory
 
 template <int D, int BN, int STAGES, int RAW, bool Q8>
 struct Layout {
-  static constexpr int kThreads = Q8 ? 384 : 224;
+  static constexpr int kThreads = Q8 ? 512 : 224;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKVBytes = BN * D * 2;   // one 16-bit K (or V) stage
   static constexpr int kRawBytes = BN * D;      // one 8-bit K (or V) stage
@@ -61,9 +62,9 @@ struct Layout {
 };
 
 // ------------------------------------------------------------------------------------------
-// One KV tile of the online softmax for one row (prefill::softmax_tile with a bit mask in
-// place of the key limit and the additive mask).  raw: the S row; hidden keys already hold
-// -inf.  a: the factor into log2 units (positive).
+// One KV tile of the online softmax for one row, in the steps of prefill::softmax_tile but with
+// a bit mask in place of the key limit and the additive mask.  raw: scores of a run of keys,
+// hidden ones -inf.  a: the factor into log2 units (positive).
 //
 // fp16 weights are held 2^7 times larger, as are their sums: the stale maximum lets a weight grow
 // to 2^8, so they still fit (2^15), and the small ones, whose rounding is absolute below 2^-14,
@@ -72,21 +73,26 @@ struct Layout {
 template <bool BF16>
 constexpr float kWeightLog2 = BF16 ? 0.f : 7.f;
 
-template <int BN, bool BF16>
-__device__ __forceinline__ bool softmax_step(const uint32_t (&raw)[BN], float a, float& m, float& l,
-                                             float& alpha, uint32_t (&pk)[BN / 2]) {
+// The largest of CH scores.
+template <int CH>
+__device__ __forceinline__ float chunk_max(const uint32_t (&raw)[CH]) {
   float mx[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     mx[e] = prefill::fmax3(__uint_as_float(raw[e]), __uint_as_float(raw[e + 8]), -INFINITY);
 #pragma unroll
-  for (int c = 16; c < BN; c += 16) {
+  for (int c = 16; c < CH; c += 16) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       mx[e] = prefill::fmax3(mx[e], __uint_as_float(raw[c + e]), __uint_as_float(raw[c + 8 + e]));
   }
-  const float row_max = a * prefill::fmax3(prefill::fmax3(mx[0], mx[1], mx[2]),
-                                           prefill::fmax3(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
+  return prefill::fmax3(prefill::fmax3(mx[0], mx[1], mx[2]), prefill::fmax3(mx[3], mx[4], mx[5]),
+                        fmaxf(mx[6], mx[7]));
+}
+
+// Moves the running maximum to a tile's (log2 units) if that is far enough above it; returns
+// whether O must then be rescaled by alpha.
+__device__ __forceinline__ bool raise_max(float row_max, float& m, float& l, float& alpha) {
   const float m_new = fmaxf(m, row_max);
   const bool need = m_new > m + prefill::kRescaleLog2;
   alpha = 1.f;
@@ -95,13 +101,20 @@ __device__ __forceinline__ bool softmax_step(const uint32_t (&raw)[BN], float a,
     m = m_new;
     l *= alpha;
   }
+  return need;
+}
+
+// Weights of CH scores against the maximum m: packed pairs, and their sum added to l.
+template <int CH, bool BF16>
+__device__ __forceinline__ void chunk_weights(const uint32_t (&raw)[CH], float a, float m, float& l,
+                                              uint32_t (&pk)[CH / 2]) {
   const float m_use = (m == -INFINITY) ? 0.f : m - kWeightLog2<BF16>;
   const float2 a2 = make_float2(a, a), nm2 = make_float2(-m_use, -m_use);
   float2 sum2[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum2[e] = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int c = 0; c < BN / 2; ++c) {
+  for (int c = 0; c < CH / 2; ++c) {
     const float2 t = __ffma2_rn(
         make_float2(__uint_as_float(raw[2 * c]), __uint_as_float(raw[2 * c + 1])), a2, nm2);
     const float p0 = exp2_approx(t.x);
@@ -111,7 +124,6 @@ __device__ __forceinline__ bool softmax_step(const uint32_t (&raw)[BN], float a,
   }
   const float2 s01 = __fadd2_rn(sum2[0], sum2[1]), s23 = __fadd2_rn(sum2[2], sum2[3]);
   l += (s01.x + s01.y) + (s23.x + s23.y);
-  return need;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -185,12 +197,112 @@ __device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& 
   }
 }
 
+// ------------------------------------------------------------------------------------------
+// Converters of K or of V: one warpgroup, thread t taking row t % BN of a tile (for BN = 64 half
+// its columns).  The row's page id is loaded two tiles ahead and its scale byte one tile ahead;
+// each 16-byte chunk of the raw row becomes two of the stage's.  Rows past the sequence's end
+// become zeros.  full/empty: the raw ring's barriers; out_full/out_empty: the 16-bit ring's.
+// ------------------------------------------------------------------------------------------
+// NaN codes of a raw row (rare): NaN in the stage, or, in a drafted token's V, zero, the token
+// noted: a weight of 0 would still carry a NaN into rows that do not see the token.
+template <int D, int kParts>
+__device__ __noinline__ void patch_nan(const uint8_t* raw, uint32_t raw_blk, uint32_t raw_swz, uint8_t* dst,
+                                       int row, int part, int draft, uint32_t* poison) {
+  constexpr int kIn = D < 128 ? D : 128, kChunks = D / 16 / kParts;
+  for (int c = part * kChunks; c < (part + 1) * kChunks; ++c) {
+    const int blk = c / (kIn / 16), ci = c % (kIn / 16);
+    const uint8_t* w = raw + blk * raw_blk + ((ci ^ raw_swz) * 16);
+    for (int e = 0; e < 16; ++e) {
+      if ((w[e] & 0x7f) != 0x7f) continue;
+      const int ch = (c % 4) * 2 + e / 8;
+      *reinterpret_cast<uint16_t*>(dst + (c / 4) * 1024 + ((ch ^ (row & 7)) * 16) + (e % 8) * 2) =
+          draft >= 0 ? 0 : 0x7fff;
+      if (draft >= 0) atomicOr(&poison[draft >> 5], 1u << (draft & 31));
+    }
+  }
+}
+
+template <int D, int BN, int STAGES, int RAW, bool BF16, bool V>
+__device__ __forceinline__ void convert_tiles(const TreeParams& p, const uint8_t* raw_ring, uint8_t* out_ring,
+                                              uint32_t full, uint32_t empty, uint32_t out_full,
+                                              uint32_t out_empty, uint32_t* poison, int b, int hk,
+                                              int t_begin, int n, int Lkv, int ctx) {
+  constexpr int kParts = 128 / BN, kIn = D < 128 ? D : 128, kChunks = D / 16 / kParts;
+  constexpr int kRawBytes = BN * D, kOutBytes = BN * D * 2;
+  constexpr uint32_t kCB = 1024u, kRG = (D / 64) * 1024u;
+  const int ct = threadIdx.x % 128, row = ct % BN, part = ct / BN;
+  const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+  const uint8_t* scales = V ? p.v_scales : p.k_scales;
+  auto page_of = [&](int jj) {
+    const int key = (t_begin + jj) * BN + row;
+    if (jj >= n || key >= Lkv) return 0;
+    const int v = __ldg(table + (key >> p.page_shift));
+    return v >= 0 && v < p.num_pages ? v : 0;  // the producer records a bad id
+  };
+  auto byte_of = [&](int jj, int page) -> uint32_t {
+    const int key = (t_begin + jj) * BN + row;
+    if (jj >= n || key >= Lkv) return 127;
+    return __ldg(scales + (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1)));
+  };
+  // raw row: BN / page_size pages of page_size rows, columns in blocks of kIn bytes
+  const int pg = row >> p.page_shift, rr = row & (p.page_size - 1);
+  const uint32_t raw_row = (pg << p.page_shift) * D + rr * kIn;
+  const uint32_t raw_blk = kIn << p.page_shift;
+  const uint32_t raw_swz = D >= 128 ? rr & 7 : (rr >> 1) & 3;
+  const uint32_t out_row = (row / 8) * kRG + (row % 8) * 128;
+  uint32_t byte = byte_of(0, page_of(0));
+  int page = page_of(1);
+  for (int jj = 0; jj < n; ++jj) {
+    const int rs = jj % RAW, stage = jj % STAGES;
+    const int key = (t_begin + jj) * BN + row;
+    const bool inside = key < Lkv;
+    const RowScale s = row_scale<BF16>(byte);
+    byte = byte_of(jj + 1, page);
+    page = page_of(jj + 2);
+    if (!mbar_wait(full + 8u * rs, (jj / RAW) & 1, p.status)) break;
+    if (jj >= STAGES && !mbar_wait(out_empty + 8u * stage, ((jj / STAGES) - 1) & 1, p.status)) break;
+    const uint8_t* raw = raw_ring + rs * kRawBytes + raw_row;
+    uint8_t* dst = out_ring + stage * kOutBytes + out_row;
+    uint32_t marks = 0;
+    auto widen = [&](auto two_c) {
+      constexpr bool TWO = decltype(two_c)::value;
+#pragma unroll 4
+      for (int c8 = 0; c8 < kChunks; ++c8) {
+        const int c = part * kChunks + c8;  // 16 columns from 16c on
+        const int blk = c / (kIn / 16), ci = c % (kIn / 16);
+        uint4 w = *reinterpret_cast<const uint4*>(raw + blk * raw_blk + ((ci ^ raw_swz) * 16));
+        if (!inside) w = make_uint4(0, 0, 0, 0);
+        uint4 x, y;
+        widen4<BF16, TWO>(w.x, s, x.x, x.y);
+        widen4<BF16, TWO>(w.y, s, x.z, x.w);
+        widen4<BF16, TWO>(w.z, s, y.x, y.y);
+        widen4<BF16, TWO>(w.w, s, y.z, y.w);
+        marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w.x), w.y), w.z), w.w);
+        uint8_t* d = dst + (c / 4) * kCB;
+        const int ch = (c % 4) * 2;
+        *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) * 16)) = x;
+        *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) * 16)) = y;
+      }
+    };
+    // a warp whose scales all stay within one factor (the usual case) takes one product
+    if (__any_sync(0xffffffffu, s.two)) widen(std::true_type{});
+    else widen(std::false_type{});
+    if (marks & 0x80808080u)
+      patch_nan<D, kParts>(raw, raw_blk, raw_swz, dst, row, part, V && key >= ctx ? key - ctx : -1, poison);
+    mbar_arrive(empty + 8u * rs);
+    fence_proxy_async_smem();
+    mbar_arrive(out_full + 8u * stage);
+  }
+}
+
 template <int D, int BN, int STAGES, int RAW, bool BF16, bool Q8, bool SPLIT>
-__global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
+__global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
   using L = Layout<D, BN, STAGES, RAW, Q8>;
   constexpr int kThreads = L::kThreads;
+  constexpr int CH = Q8 ? 64 : BN;  // scores a softmax thread holds at a time
+  constexpr int kPOff = CH < BN ? BN / 2 : 0;  // columns of P in an S/P buffer
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -385,7 +497,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         if (!(ok = mbar_wait(bar_v(stage), (jj / STAGES) & 1, p.status))) break;
         tc_fence_after();
         const uint64_t vd = sdesc_add(v_desc, stage * L::kKVBytes);
-        const uint32_t a_p = tm_s0 + buf * BN;
+        const uint32_t a_p = tm_s0 + buf * BN + kPOff;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
           mma_ts(tm_o, a_p + kk * 8, sdesc_add(vd, kk * (2 * kRG)), idesc_o,
@@ -425,98 +537,15 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
     }
   } else if (Q8 && warp >= 8) {
     // -------------------------------- converters ----------------------------------------
-    // Thread t takes row t % BN of a tile (for BN = 64 half its columns): its page and scale
-    // bytes are loaded a tile ahead, each 16-byte chunk of the raw row becomes two of the
-    // stage's.  Rows past the sequence's end become zeros.
     if constexpr (Q8) {
-      constexpr int kParts = 128 / BN, kIn = D < 128 ? D : 128;
-      const int ct = threadIdx.x - 256, row = ct % BN, part = ct / BN;
-      const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-      auto scale_row = [&](int jj) {  // index of the row's scales, or -1
-        const int key = (t_begin + jj) * BN + row;
-        if (jj >= n || key >= Lkv) return static_cast<int64_t>(-1);
-        const int v = __ldg(table + (key >> p.page_shift));
-        const int page = v >= 0 && v < p.num_pages ? v : 0;
-        return (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1));
-      };
-      // raw row: BN / page_size pages of page_size rows, columns in blocks of kIn bytes
-      const int pg = row >> p.page_shift, rr = row & (p.page_size - 1);
-      const uint32_t raw_row = (pg << p.page_shift) * D + rr * kIn;
-      const uint32_t raw_blk = (kIn << p.page_shift);
-      const uint32_t raw_swz = D >= 128 ? rr & 7 : (rr >> 1) & 3;
-      const uint32_t out_row = (row / 8) * kRG + (row % 8) * 128;
-      auto convert = [&](const uint8_t* raw, uint8_t* dst, uint32_t byte, bool inside, int draft) {
-        const RowScale s = row_scale<BF16>(byte);
-        uint32_t marks = 0;
-        constexpr int kChunks = D / 16 / kParts;
-        auto widen = [&](auto two_c) {
-          constexpr bool TWO = decltype(two_c)::value;
-#pragma unroll
-          for (int c8 = 0; c8 < kChunks; ++c8) {
-            const int c = part * kChunks + c8;        // 16 columns from 16c on
-            const int blk = c / (kIn / 16), ci = c % (kIn / 16);
-            uint4 w = *reinterpret_cast<const uint4*>(raw + raw_row + blk * raw_blk + ((ci ^ raw_swz) * 16));
-            if (!inside) w = make_uint4(0, 0, 0, 0);
-            uint4 x, y;
-            widen4<BF16, TWO>(w.x, s, x.x, x.y);
-            widen4<BF16, TWO>(w.y, s, x.z, x.w);
-            widen4<BF16, TWO>(w.z, s, y.x, y.y);
-            widen4<BF16, TWO>(w.w, s, y.z, y.w);
-            marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w.x), w.y), w.z), w.w);
-            uint8_t* d = dst + out_row + (c / 4) * kCB;
-            const int ch = (c % 4) * 2;
-            *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) * 16)) = x;
-            *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) * 16)) = y;
-          }
-        };
-        // a warp whose scales all stay within one factor (the usual case) takes one product
-        if (__any_sync(0xffffffffu, s.two)) widen(std::true_type{});
-        else widen(std::false_type{});
-        if (marks & 0x80808080u) {
-          // NaN codes (rare): put NaN where they are, or, in a drafted token's V, zero, and note
-          // the token: a weight of 0 would still carry a NaN into rows that do not see it
-          for (int c8 = 0; c8 < kChunks; ++c8) {
-            const int c = part * kChunks + c8;
-            const int blk = c / (kIn / 16), ci = c % (kIn / 16);
-            const uint8_t* w = raw + raw_row + blk * raw_blk + ((ci ^ raw_swz) * 16);
-            uint8_t* d = dst + out_row + (c / 4) * kCB;
-            for (int e = 0; e < 16; ++e) {
-              if ((w[e] & 0x7f) != 0x7f) continue;
-              const int ch = (c % 4) * 2 + e / 8;
-              *reinterpret_cast<uint16_t*>(d + ((ch ^ (row & 7)) * 16) + (e % 8) * 2) =
-                  draft >= 0 ? 0 : 0x7fff;
-              if (draft >= 0) atomicOr(&poison[draft >> 5], 1u << (draft & 31));
-            }
-          }
-        }
-      };
-      int64_t at = scale_row(0);
-      uint32_t kb = at >= 0 ? p.k_scales[at] : 127, vb = at >= 0 ? p.v_scales[at] : 127;
-      for (int jj = 0; jj < n; ++jj) {
-        const int rs = jj % RAW, stage = jj % STAGES;
-        const int key = (t_begin + jj) * BN + row;
-        const bool inside = key < Lkv;
-        const uint32_t kbyte = kb, vbyte = vb;
-        at = scale_row(jj + 1);
-        if (at >= 0) {
-          kb = p.k_scales[at];
-          vb = p.v_scales[at];
-        }
-        if (!mbar_wait(bar_rk(rs), (jj / RAW) & 1, p.status)) break;
-        if (jj >= STAGES && !mbar_wait(bar_ke(stage), ((jj / STAGES) - 1) & 1, p.status)) break;
-        convert(smem + L::kRawKOff + rs * L::kRawBytes, smem + L::kKOff + stage * L::kKVBytes, kbyte,
-                inside, -1);
-        mbar_arrive(bar_rke(rs));
-        fence_proxy_async_smem();
-        mbar_arrive(bar_k(stage));
-        if (!mbar_wait(bar_rv(rs), (jj / RAW) & 1, p.status)) break;
-        if (jj >= STAGES && !mbar_wait(bar_ve(stage), ((jj / STAGES) - 1) & 1, p.status)) break;
-        convert(smem + L::kRawVOff + rs * L::kRawBytes, smem + L::kVOff + stage * L::kKVBytes, vbyte,
-                inside, inside && key >= ctx ? key - ctx : -1);
-        mbar_arrive(bar_rve(rs));
-        fence_proxy_async_smem();
-        mbar_arrive(bar_v(stage));
-      }
+      if (warp < 12)
+        convert_tiles<D, BN, STAGES, RAW, BF16, false>(
+            p, smem + L::kRawKOff, smem + L::kKOff, bar_rk(0), bar_rke(0), bar_k(0), bar_ke(0), poison, b,
+            hk, t_begin, n, Lkv, ctx);
+      else
+        convert_tiles<D, BN, STAGES, RAW, BF16, true>(
+            p, smem + L::kRawVOff, smem + L::kVOff, bar_rv(0), bar_rve(0), bar_v(0), bar_ve(0), poison, b,
+            hk, t_begin, n, Lkv, ctx);
     }
   } else if (warp < live_warps) {
     // ------------------------- softmax + epilogue (row per thread) ----------------------
@@ -543,25 +572,35 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(bar_s(buf), (jj / kNumS) & 1, p.status));
       if (!ok) break;
       tc_fence_after();
-      uint32_t raw[BN];
-      prefill::load_s<BN>(t_s, raw);
       const int key0 = (t_begin + jj) * BN;
-      if (pre) {
+      // Scores are read CH at a time: all of them at once where the registers allow, else in
+      // two halves, read again after the maximum is known (tensor-memory loads are cheap next
+      // to the exponentials).
+      auto read = [&](int c0, uint32_t (&raw)[CH]) {
+        prefill::load_s<CH>(t_s + c0, raw);
+        if (pre) {
 #pragma unroll
-        for (int c = 0; c < BN; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * p.scale_log2);
-      }
-      if (key0 + BN > ctx) {
-#pragma unroll
-        for (int w = 0; w < BN / 32; ++w) {
-          const uint32_t bits = row_bits(row, key0 + 32 * w - ctx);
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (!((bits >> c) & 1)) raw[32 * w + c] = 0xff800000u;  // -inf
+          for (int c = 0; c < CH; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * p.scale_log2);
         }
+        if (key0 + BN > ctx) {
+#pragma unroll
+          for (int w = 0; w < CH / 32; ++w) {
+            const uint32_t bits = row_bits(row, key0 + c0 + 32 * w - ctx);
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((bits >> c) & 1)) raw[32 * w + c] = 0xff800000u;  // -inf
+          }
+        }
+      };
+      uint32_t raw[CH];
+      float row_max = -INFINITY;
+#pragma unroll
+      for (int c0 = 0; c0 < BN; c0 += CH) {
+        read(c0, raw);
+        row_max = fmaxf(row_max, chunk_max(raw));
       }
       float alpha;
-      uint32_t pk[BN / 2];
-      const bool need = softmax_step<BN, BF16>(raw, a, m_run, l_run, alpha, pk);
+      const bool need = raise_max(a * row_max, m_run, l_run, alpha);
       // O is rescaled only once every earlier P V product is in it; a tile with no rescale
       // does not wait (S_j itself needed P_{j-3} V_{j-3} finished)
       const bool rescale = jj > 0 && __any_sync(0xffffffffu, need);
@@ -571,7 +610,16 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         tc_fence_after();
         prefill::rescale_o<D>(tm_o + lane_off, alpha);
       }
-      prefill::store_p<BN>(t_s, pk);
+      // P_j (16-bit pairs) goes over BN / 2 columns of S_j: the first ones, or with two halves the
+      // last, the second half first: its own scores are then in registers already, and the
+      // first half's are not written over before they are read again
+#pragma unroll
+      for (int c0 = BN - CH; c0 >= 0; c0 -= CH) {
+        if (CH < BN) read(c0, raw);
+        uint32_t pk[CH / 2];
+        chunk_weights<CH, BF16>(raw, a, m_run, l_run, pk);
+        prefill::store_p<CH>(t_s + kPOff + c0 / 2, pk);
+      }
       tmem_st_wait();
       if (!Q8 && key0 + BN > ctx) {
         // The stage holds rows of drafted tokens, which some queries do not see, or rows past

@@ -202,10 +202,14 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   };
   auto k_stage = [&](int s) { return ring + s * 2 * L::kStage; };
   auto v_stage = [&](int s) { return ring + (s * 2 + 1) * L::kStage; };
-  for (int k = 0; k < NS && k < n; ++k) {
-    const int id = token_page(k);
-    copy(&tm_k, k_stage(k), bar_k(k), k, id);
-    copy(&tm_v, v_stage(k), bar_v(k), k, id);
+  int ids[NS + 1];
+#pragma unroll
+  for (int k = 0; k <= NS; ++k) ids[k] = token_page(k);
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    if (k >= n) break;
+    copy(&tm_k, k_stage(k), bar_k(k), k, ids[k]);
+    copy(&tm_v, v_stage(k), bar_v(k), k, ids[k]);
   }
 
   // ---- q: rows r = head * T + query, scaled and laid out as the fragments of its k steps ----
@@ -466,18 +470,23 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
     return true;
   };
 
-  // ---- the loop: page ids NS slices ahead, scale bytes one slice ahead ----
-  auto scale_bytes = [&](int k) {
+  // ---- the loop: page ids are loaded a slice before their copies are issued, scale bytes a
+  // slice before they are used ----
+  auto scale_bytes = [&](int k, int id) {
     if (k >= n || lane >= SL || (s_begin + k * kWarps) * SL + lane >= Lkv) return 0x7f7fu;
-    const int64_t at = token_row(k, token_page(k));
+    const int64_t at = token_row(k, id);
     return static_cast<uint32_t>(__ldg(p.k_scales + at)) | (static_cast<uint32_t>(__ldg(p.v_scales + at)) << 8);
   };
   int k = 0;
   bool ok = true;
-  uint32_t bytes = scale_bytes(0);
+  uint32_t bytes = scale_bytes(0, ids[0]);
   for (; ok && k < n; ++k) {
-    const int next_id = token_page(k + NS);
-    const uint32_t next_bytes = scale_bytes(k + 1);
+    // ids[j] is slice k + j's here
+    const uint32_t next_bytes = scale_bytes(k + 1, ids[1]);
+    const int next_id = ids[NS];
+#pragma unroll
+    for (int j = 0; j < NS; ++j) ids[j] = ids[j + 1];
+    ids[NS] = token_page(k + NS + 1);
     if ((s_begin + k * kWarps) * SL + SL > ctx) ok = slice(std::true_type{}, k, bytes, next_id);
     else ok = slice(std::false_type{}, k, bytes, next_id);
     bytes = next_bytes;
