@@ -17,10 +17,17 @@
 // the way costs shared-memory bandwidth (a row is written twice and read twice) but keeps the
 // 16-bit queries and weights whole, which 8-bit MMAs would not.
 //
+// fp16 operands for bf16 queries.  e4m3 converts to fp16 in one instruction a pair, to bf16 only
+// by placing bits (five, and a test for NaN codes); at 64 drafted tokens the conversion's
+// instructions are what bounds the kernel.  So a CTA looks at the scale bytes of its keys
+// first: if all lie in [113, 134], every value * 2^e is exact in fp16 too, the rows of Q are
+// scaled by powers of two into fp16 (exact down to 2^-32 of a row's maximum, undone in the
+// scores), and both products run in fp16.  Otherwise they run in bf16, which holds any scale.
+//
 // Warp roles: 0-3 softmax + epilogue (thread t owns row t), 4 TMA producer, 5 P V issuer and
-// tensor-memory owner, 6 S issuer, and for 8-bit pages 8-11 converters of K, 12-15 of V (7
-// idle).  With 512 threads a thread has 128 registers, so there the softmax reads its row of
-// scores in two halves.
+// tensor-memory owner, 6 S issuer, and for 8-bit pages 8-11 converters (7 idle).  With 384
+// threads a thread has 168 registers, so there the softmax reads its row of scores in two
+// halves.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -42,7 +49,7 @@ constexpr int kNumS = 3;  // S/P buffers in tensor memory
 
 template <int D, int BN, int STAGES, int RAW, bool Q8>
 struct Layout {
-  static constexpr int kThreads = Q8 ? 512 : 224;
+  static constexpr int kThreads = Q8 ? 384 : 224;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKVBytes = BN * D * 2;   // one 16-bit K (or V) stage
   static constexpr int kRawBytes = BN * D;      // one 8-bit K (or V) stage
@@ -52,8 +59,8 @@ struct Layout {
   static constexpr int kRawVOff = kRawKOff + (Q8 ? RAW * kRawBytes : 0);
   static constexpr int kBarOff = kRawVOff + (Q8 ? RAW * kRawBytes : 0);
   // q_full, {k,v}_full[S], {k,v}_empty[S], s_full[3], p_full[3], pv_done[3], pv_issuer_done,
-  // s_issuer_done, raw {k,v}_full[R], raw {k,v}_empty[R]
-  static constexpr int kNumBars = 1 + 4 * STAGES + 3 * kNumS + 2 + (Q8 ? 4 * RAW : 0);
+  // s_issuer_done, raw {k,v}_full[R], raw {k,v}_empty[R], q_ready
+  static constexpr int kNumBars = 1 + 4 * STAGES + 3 * kNumS + 2 + (Q8 ? 4 * RAW + 1 : 0);
   static constexpr int kPoisonOff = kBarOff + kNumBars * 8 + 16;
   static constexpr int kBytes = kPoisonOff + (kMaxTree / 32) * 4;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 bytes
@@ -70,8 +77,7 @@ struct Layout {
 // to 2^8, so they still fit (2^15), and the small ones, whose rounding is absolute below 2^-14,
 // keep seven more bits.
 // ------------------------------------------------------------------------------------------
-template <bool BF16>
-constexpr float kWeightLog2 = BF16 ? 0.f : 7.f;
+constexpr float kWeightLog2F16 = 7.f;
 
 // The largest of CH scores.
 template <int CH>
@@ -108,7 +114,7 @@ __device__ __forceinline__ bool raise_max(float row_max, float& m, float& l, flo
 template <int CH, bool BF16>
 __device__ __forceinline__ void chunk_weights(const uint32_t (&raw)[CH], float a, float m, float& l,
                                               uint32_t (&pk)[CH / 2]) {
-  const float m_use = (m == -INFINITY) ? 0.f : m - kWeightLog2<BF16>;
+  const float m_use = (m == -INFINITY) ? 0.f : m - (BF16 ? 0.f : kWeightLog2F16);
   const float2 a2 = make_float2(a, a), nm2 = make_float2(-m_use, -m_use);
   float2 sum2[4];
 #pragma unroll
@@ -186,10 +192,8 @@ __device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& 
       hi = mul_bf16x2(hi, s.f2);
     }
   } else {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
-    lo = mul_f16x2(static_cast<uint32_t>(a.x) | (static_cast<uint32_t>(a.y) << 16), s.f1);
-    hi = mul_f16x2(static_cast<uint32_t>(b.x) | (static_cast<uint32_t>(b.y) << 16), s.f1);
+    lo = mul_f16x2(widen2(w), s.f1);
+    hi = mul_f16x2(widen2_hi(w), s.f1);
     if constexpr (TWO) {
       lo = mul_f16x2(lo, s.f2);
       hi = mul_f16x2(hi, s.f2);
@@ -198,51 +202,153 @@ __device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& 
 }
 
 // ------------------------------------------------------------------------------------------
-// Converters of K or of V: one warpgroup, thread t taking row t % BN of a tile (for BN = 64 half
-// its columns).  The row's page id is loaded two tiles ahead and its scale byte one tile ahead;
+// Converters: one warpgroup, thread t taking row t % BN of a tile (for BN = 64 half its columns), K
+// then V.  The row's page id is loaded two tiles ahead and its scale bytes one tile ahead;
 // each 16-byte chunk of the raw row becomes two of the stage's.  Rows past the sequence's end
-// become zeros.  full/empty: the raw ring's barriers; out_full/out_empty: the 16-bit ring's.
+// become zeros.
 // ------------------------------------------------------------------------------------------
+// Whether some scale byte of keys [first, last) lies outside [113, 134], where every e4m3 value
+// times the scale is exact in fp16 (a multiple of 2^-23, at most 448 * 2^7).  Each thread of
+// the block looks at whole pages.
+template <int THREADS>
+__device__ __forceinline__ bool scales_leave_fp16(const TreeParams& p, int b, int hk, int first, int last) {
+  const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+  const int pages = last > first ? ((last - 1) >> p.page_shift) - (first >> p.page_shift) + 1 : 0;
+  bool outside = false;
+  for (int i = threadIdx.x; i < pages; i += THREADS) {
+    const int lp = (first >> p.page_shift) + i;
+    const int page = __ldg(table + lp);
+    if (page < 0 || page >= p.num_pages) continue;
+    const int64_t at = (static_cast<int64_t>(page) * p.Hkv + hk) << p.page_shift;
+    const int count = min(p.page_size, last - (lp << p.page_shift));
+    for (int t = 0; t < count; t += 8) {  // a page holds a multiple of eight tokens
+      const uint2 k = *reinterpret_cast<const uint2*>(p.k_scales + at + t);
+      const uint2 v = *reinterpret_cast<const uint2*>(p.v_scales + at + t);
+      const uint32_t w[4] = {k.x, k.y, v.x, v.y};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t byte = (w[j / 4] >> (8 * (j % 4))) & 0xffu;
+        outside |= t + j % 8 < count && byte - 113u > 21u;
+      }
+    }
+  }
+  return outside;
+}
+
+// Row r of the swizzled Q tile (64-column blocks of 128 rows x 128 bytes), bf16 to fp16: times
+// 2^-eq such that its largest finite element lies in [2^14, 2^15).  Returns 2^eq.
+template <int D>
+__device__ __forceinline__ float q_row_to_fp16(uint32_t tile, int r) {
+  float amax = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 v = lds128(tile + (c / 8) * (kRows * 128) + r * 128 + (((c % 8) ^ (r & 7)) * 16));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      unpack2<__nv_bfloat16>(w[e], lo, hi);
+      amax = fmaxf(amax, fmaxf(finite_abs(lo), finite_abs(hi)));
+    }
+  }
+  const int eq = amax > 0.f ? max(-112, static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14) : 0;
+  const float f = __uint_as_float(static_cast<uint32_t>(127 - eq) << 23);
+#pragma unroll 1
+  for (int c = 0; c < D / 8; ++c) {
+    const uint32_t at = tile + (c / 8) * (kRows * 128) + r * 128 + (((c % 8) ^ (r & 7)) * 16);
+    const uint4 v = lds128(at);
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      unpack2<__nv_bfloat16>(w[e], lo, hi);
+      w[e] = pack_f16x2(lo * f, hi * f);
+    }
+    sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  return __uint_as_float(static_cast<uint32_t>(127 + eq) << 23);
+}
+
 // NaN codes of a raw row (rare): NaN in the stage, or, in a drafted token's V, zero, the token
 // noted: a weight of 0 would still carry a NaN into rows that do not see the token.
 template <int D, int kParts>
-__device__ __noinline__ void patch_nan(const uint8_t* raw, uint32_t raw_blk, uint32_t raw_swz, uint8_t* dst,
+__device__ __noinline__ void patch_nan(uint32_t raw, uint32_t raw_blk, uint32_t raw_swz, uint32_t dst,
                                        int row, int part, int draft, uint32_t* poison) {
   constexpr int kIn = D < 128 ? D : 128, kChunks = D / 16 / kParts;
   for (int c = part * kChunks; c < (part + 1) * kChunks; ++c) {
     const int blk = c / (kIn / 16), ci = c % (kIn / 16);
-    const uint8_t* w = raw + blk * raw_blk + ((ci ^ raw_swz) * 16);
+    const uint4 x = lds128(raw + blk * raw_blk + ((ci ^ raw_swz) * 16));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    if (!(nan_mark(nan_mark(nan_mark(nan_mark(0, x.x), x.y), x.z), x.w) & 0x80808080u)) continue;
+#pragma unroll
     for (int e = 0; e < 16; ++e) {
-      if ((w[e] & 0x7f) != 0x7f) continue;
+      if (((w[e / 4] >> (8 * (e % 4))) & 0x7fu) != 0x7fu) continue;
       const int ch = (c % 4) * 2 + e / 8;
-      *reinterpret_cast<uint16_t*>(dst + (c / 4) * 1024 + ((ch ^ (row & 7)) * 16) + (e % 8) * 2) =
-          draft >= 0 ? 0 : 0x7fff;
+      sts16(dst + (c / 4) * 1024 + ((ch ^ (row & 7)) * 16) + (e % 8) * 2, draft >= 0 ? 0 : 0x7fff);
       if (draft >= 0) atomicOr(&poison[draft >> 5], 1u << (draft & 31));
     }
   }
 }
 
-template <int D, int BN, int STAGES, int RAW, bool BF16, bool V>
-__device__ __forceinline__ void convert_tiles(const TreeParams& p, const uint8_t* raw_ring, uint8_t* out_ring,
-                                              uint32_t full, uint32_t empty, uint32_t out_full,
-                                              uint32_t out_empty, uint32_t* poison, int b, int hk,
+// This thread's part of one raw row into the stage.  Returns marks of NaN codes (bf16 only: the
+// conversion to fp16 keeps them).
+template <int D, int kParts, bool BF16, bool TWO>
+__device__ __forceinline__ uint32_t widen_row(uint32_t raw, uint32_t raw_blk, uint32_t raw_swz,
+                                              uint32_t dst, int row, int part, const RowScale& s) {
+  constexpr int kIn = D < 128 ? D : 128, kChunks = D / 16 / kParts;
+  uint32_t marks = 0;
+  // both rows start at a multiple of their swizzled run (kIn and 128 bytes), so a chunk's address
+  // is the row's, its swizzle included, with the chunk's number flipped in
+  const uint32_t from = raw + raw_swz * 16, to = dst + (row & 7) * 16;
+  constexpr int kBatch = 4;  // chunks whose loads are issued together
+#pragma unroll(BF16 ? 1 : 2)
+  for (int c0 = 0; c0 < kChunks; c0 += kBatch) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int c = part * kChunks + c0 + u;  // 16 columns from 16c on
+      w[u] = lds128((from ^ ((c % (kIn / 16)) * 16)) + (c / (kIn / 16)) * raw_blk);
+    }
+    const uint32_t block = to + (part * kChunks + c0) / 4 * 1024;  // 64 columns
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      uint4 x, y;
+      widen4<BF16, TWO>(w[u].x, s, x.x, x.y);
+      widen4<BF16, TWO>(w[u].y, s, x.z, x.w);
+      widen4<BF16, TWO>(w[u].z, s, y.x, y.y);
+      widen4<BF16, TWO>(w[u].w, s, y.z, y.w);
+      if constexpr (BF16) marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w[u].x), w[u].y), w[u].z), w[u].w);
+      sts128(block ^ (2 * u * 16), x);
+      sts128(block ^ ((2 * u + 1) * 16), y);
+    }
+  }
+  return marks;
+}
+
+// The barriers and rings of K or of V: raw ring (full, empty) and 16-bit ring.
+struct Rings {
+  uint32_t raw, full, empty, out, out_full, out_empty;
+};
+
+template <int D, int BN, int STAGES, int RAW>
+__device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, const Rings& k_rings,
+                                              const Rings& v_rings, uint32_t* poison, int b, int hk,
                                               int t_begin, int n, int Lkv, int ctx) {
-  constexpr int kParts = 128 / BN, kIn = D < 128 ? D : 128, kChunks = D / 16 / kParts;
+  constexpr int kParts = 128 / BN, kIn = D < 128 ? D : 128;
   constexpr int kRawBytes = BN * D, kOutBytes = BN * D * 2;
-  constexpr uint32_t kCB = 1024u, kRG = (D / 64) * 1024u;
+  constexpr uint32_t kRG = (D / 64) * 1024u;
   const int ct = threadIdx.x % 128, row = ct % BN, part = ct / BN;
   const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  const uint8_t* scales = V ? p.v_scales : p.k_scales;
   auto page_of = [&](int jj) {
     const int key = (t_begin + jj) * BN + row;
-    if (jj >= n || key >= Lkv) return 0;
-    const int v = __ldg(table + (key >> p.page_shift));
-    return v >= 0 && v < p.num_pages ? v : 0;  // the producer records a bad id
+    return jj < n && key < Lkv ? __ldg(table + (key >> p.page_shift)) : 0;
   };
-  auto byte_of = [&](int jj, int page) -> uint32_t {
+  auto bytes_of = [&](int jj, int page) -> uint32_t {  // the row's scale bytes: K, V
     const int key = (t_begin + jj) * BN + row;
-    if (jj >= n || key >= Lkv) return 127;
-    return __ldg(scales + (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1)));
+    if (jj >= n || key >= Lkv) return 0x7f7fu;
+    if (page < 0 || page >= p.num_pages) page = 0;  // the producer records a bad id
+    const int64_t at = (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1));
+    return __ldg(p.k_scales + at) | (static_cast<uint32_t>(__ldg(p.v_scales + at)) << 8);
   };
   // raw row: BN / page_size pages of page_size rows, columns in blocks of kIn bytes
   const int pg = row >> p.page_shift, rr = row & (p.page_size - 1);
@@ -250,53 +356,47 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, const uint8_t
   const uint32_t raw_blk = kIn << p.page_shift;
   const uint32_t raw_swz = D >= 128 ? rr & 7 : (rr >> 1) & 3;
   const uint32_t out_row = (row / 8) * kRG + (row % 8) * 128;
-  uint32_t byte = byte_of(0, page_of(0));
+  uint32_t bytes = bytes_of(0, page_of(0));
   int page = page_of(1);
   for (int jj = 0; jj < n; ++jj) {
     const int rs = jj % RAW, stage = jj % STAGES;
     const int key = (t_begin + jj) * BN + row;
-    const bool inside = key < Lkv;
-    const RowScale s = row_scale<BF16>(byte);
-    byte = byte_of(jj + 1, page);
+    const uint32_t now = bytes;
+    bytes = bytes_of(jj + 1, page);
     page = page_of(jj + 2);
-    if (!mbar_wait(full + 8u * rs, (jj / RAW) & 1, p.status)) break;
-    if (jj >= STAGES && !mbar_wait(out_empty + 8u * stage, ((jj / STAGES) - 1) & 1, p.status)) break;
-    const uint8_t* raw = raw_ring + rs * kRawBytes + raw_row;
-    uint8_t* dst = out_ring + stage * kOutBytes + out_row;
-    uint32_t marks = 0;
-    auto widen = [&](auto two_c) {
-      constexpr bool TWO = decltype(two_c)::value;
-#pragma unroll 4
-      for (int c8 = 0; c8 < kChunks; ++c8) {
-        const int c = part * kChunks + c8;  // 16 columns from 16c on
-        const int blk = c / (kIn / 16), ci = c % (kIn / 16);
-        uint4 w = *reinterpret_cast<const uint4*>(raw + blk * raw_blk + ((ci ^ raw_swz) * 16));
-        if (!inside) w = make_uint4(0, 0, 0, 0);
-        uint4 x, y;
-        widen4<BF16, TWO>(w.x, s, x.x, x.y);
-        widen4<BF16, TWO>(w.y, s, x.z, x.w);
-        widen4<BF16, TWO>(w.z, s, y.x, y.y);
-        widen4<BF16, TWO>(w.w, s, y.z, y.w);
-        marks = nan_mark(nan_mark(nan_mark(nan_mark(marks, w.x), w.y), w.z), w.w);
-        uint8_t* d = dst + (c / 4) * kCB;
-        const int ch = (c % 4) * 2;
-        *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) * 16)) = x;
-        *reinterpret_cast<uint4*>(d + (((ch + 1) ^ (row & 7)) * 16)) = y;
+#pragma unroll 1
+    for (int v = 0; v < 2; ++v) {
+      const Rings& g = v ? v_rings : k_rings;
+      const uint32_t byte = v ? now >> 8 : now & 0xffu;
+      const RowScale s = f16 ? row_scale<false>(byte) : row_scale<true>(byte);
+      if (!mbar_wait(g.full + 8u * rs, (jj / RAW) & 1, p.status)) return;
+      if (jj >= STAGES && !mbar_wait(g.out_empty + 8u * stage, ((jj / STAGES) - 1) & 1, p.status)) return;
+      const uint32_t raw = g.raw + rs * kRawBytes + raw_row;
+      const uint32_t dst = g.out + stage * kOutBytes + out_row;
+      if (key >= Lkv) {
+        // past the sequence's end: zeros, whatever the page holds
+        for (int c = part * (D / 8 / kParts); c < (part + 1) * (D / 8 / kParts); ++c)
+          sts128(dst + (c / 8) * 1024 + (((c % 8) ^ (row & 7)) * 16), make_uint4(0, 0, 0, 0));
+      } else {
+        const int draft = v && key >= ctx ? key - ctx : -1;
+        // nearly always one factor holds the scale (in fp16 mode of bf16 queries always)
+        uint32_t marks;
+        if (f16) marks = s.two ? widen_row<D, kParts, false, true>(raw, raw_blk, raw_swz, dst, row, part, s)
+                               : widen_row<D, kParts, false, false>(raw, raw_blk, raw_swz, dst, row, part, s);
+        else marks = s.two ? widen_row<D, kParts, true, true>(raw, raw_blk, raw_swz, dst, row, part, s)
+                           : widen_row<D, kParts, true, false>(raw, raw_blk, raw_swz, dst, row, part, s);
+        if ((marks & 0x80808080u) || draft >= 0)
+          patch_nan<D, kParts>(raw, raw_blk, raw_swz, dst, row, part, draft, poison);
       }
-    };
-    // a warp whose scales all stay within one factor (the usual case) takes one product
-    if (__any_sync(0xffffffffu, s.two)) widen(std::true_type{});
-    else widen(std::false_type{});
-    if (marks & 0x80808080u)
-      patch_nan<D, kParts>(raw, raw_blk, raw_swz, dst, row, part, V && key >= ctx ? key - ctx : -1, poison);
-    mbar_arrive(empty + 8u * rs);
-    fence_proxy_async_smem();
-    mbar_arrive(out_full + 8u * stage);
+      fence_proxy_async_smem();
+      mbar_arrive(g.empty + 8u * rs);
+      mbar_arrive(g.out_full + 8u * stage);
+    }
   }
 }
 
 template <int D, int BN, int STAGES, int RAW, bool BF16, bool Q8, bool SPLIT>
-__global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
+__global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
   using L = Layout<D, BN, STAGES, RAW, Q8>;
@@ -326,6 +426,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
   auto bar_rv = [&](int s) { return bar_raw + 8u * (RAW + s); };
   auto bar_rke = [&](int s) { return bar_raw + 8u * (2 * RAW + s); };
   auto bar_rve = [&](int s) { return bar_raw + 8u * (3 * RAW + s); };
+  const uint32_t bar_qr = bar_raw + 8u * (4 * RAW);  // Q in the operand type
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kBarOff + L::kNumBars * 8);
   // drafted tokens whose V row holds a value that is not finite (see the V clearing below)
   uint32_t* poison = reinterpret_cast<uint32_t*>(smem + L::kPoisonOff);
@@ -399,6 +500,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
         mbar_init(bar_rke(s), 128);
         mbar_init(bar_rve(s), 128);
       }
+      mbar_init(bar_qr, live_warps * 32);
     }
     fence_barrier_init();
   }
@@ -407,8 +509,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
     tmem_alloc(smem_addr(tmem_slot), 512);
     tmem_relinquish();
   }
+  // Operand type of both products: the queries', or fp16 where bf16 queries meet 8-bit keys and
+  // values that fp16 holds exactly.
+  bool f16 = !BF16;
   tc_fence_before();
-  __syncthreads();
+  if constexpr (Q8 && BF16) {
+    const int last = min(Lkv, (t_begin + n) * BN);
+    f16 = !__syncthreads_or(scales_leave_fp16<kThreads>(p, b, hk, t_begin * BN, last) ? 1 : 0);
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_o = tmem;           // O: columns [0, D)
@@ -429,17 +539,14 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
       // of a tile, loaded one tile ahead, and issues that page's box itself.
       const int ps = p.page_size, tp = BN / ps;
       const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-      auto tile_page = [&](int jj) {
-        int id = 0;  // pages past the sequence's end read page 0; those keys are hidden
-        if (lane < tp) {
-          const int lp = (t_begin + jj) * tp + lane;
-          if (static_cast<int64_t>(lp) * ps < Lkv) {
-            const int v = __ldg(table + lp);
-            if (v >= 0 && v < p.num_pages) id = v;
-            else record_error(p.status, kDevBounds);
-          }
-        }
-        return id;
+      auto tile_page = [&](int jj) {  // pages past the sequence's end read page 0, keys hidden
+        const int lp = (t_begin + jj) * tp + lane;
+        return lane < tp && static_cast<int64_t>(lp) * ps < Lkv ? __ldg(table + lp) : 0;
+      };
+      auto checked = [&](int id) {  // where an id is used, so that nothing waits for its load
+        if (id >= 0 && id < p.num_pages) return id;
+        record_error(p.status, kDevBounds);
+        return 0;
       };
       constexpr int kRing = Q8 ? RAW : STAGES;
       constexpr uint32_t kBytes = Q8 ? L::kRawBytes : L::kKVBytes;
@@ -458,7 +565,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
       int k_issued = 0, v_issued = 0;
       int ids_next = tile_page(0);
       for (int jj = 0; jj < n; ++jj) {
-        const int ids = ids_next;
+        const int ids = checked(ids_next);
         if (jj + 1 < n) ids_next = tile_page(jj + 1);
         const int stage = jj % kRing;
         const uint32_t par = ((jj / kRing) - 1) & 1;
@@ -488,7 +595,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
   } else if (warp == 5) {
     // ------------------------------- P V issuer -----------------------------------------
     if (lane == 0 && n > 0) {
-      constexpr uint32_t idesc_o = idesc_f16(BF16, kRows, D, false, true);
+      const uint32_t idesc_o = idesc_f16(!f16, kRows, D, false, true);
       const uint64_t v_desc = sdesc_sw128(sV, kCB, kRG);
       bool ok = true;
       for (int jj = 0; ok && jj < n; ++jj) {
@@ -512,10 +619,10 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
   } else if (warp == 6) {
     // --------------------------------- S issuer -----------------------------------------
     if (lane == 0 && n > 0) {
-      constexpr uint32_t idesc_s = idesc_f16(BF16, kRows, BN, false, false);
+      const uint32_t idesc_s = idesc_f16(!f16, kRows, BN, false, false);
       const uint64_t k_desc = sdesc_sw128(sK, 16, kRG);
       const uint64_t q_desc = sdesc_sw128(sQ, 16, 1024);
-      bool ok = mbar_wait(bar_q, 0, p.status);
+      bool ok = mbar_wait(Q8 && BF16 && f16 ? bar_qr : bar_q, 0, p.status);
       for (int jj = 0; ok && jj < n; ++jj) {
         const int stage = jj % STAGES, buf = jj % kNumS;
         if (!(ok = mbar_wait(bar_k(stage), (jj / STAGES) & 1, p.status))) break;
@@ -538,14 +645,9 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
   } else if (Q8 && warp >= 8) {
     // -------------------------------- converters ----------------------------------------
     if constexpr (Q8) {
-      if (warp < 12)
-        convert_tiles<D, BN, STAGES, RAW, BF16, false>(
-            p, smem + L::kRawKOff, smem + L::kKOff, bar_rk(0), bar_rke(0), bar_k(0), bar_ke(0), poison, b,
-            hk, t_begin, n, Lkv, ctx);
-      else
-        convert_tiles<D, BN, STAGES, RAW, BF16, true>(
-            p, smem + L::kRawVOff, smem + L::kVOff, bar_rv(0), bar_rve(0), bar_v(0), bar_ve(0), poison, b,
-            hk, t_begin, n, Lkv, ctx);
+      const Rings k{s_base + L::kRawKOff, bar_rk(0), bar_rke(0), sK, bar_k(0), bar_ke(0)};
+      const Rings v{s_base + L::kRawVOff, bar_rv(0), bar_rve(0), sV, bar_v(0), bar_ve(0)};
+      convert_tiles<D, BN, STAGES, RAW>(p, f16, k, v, poison, b, hk, t_begin, n, Lkv, ctx);
     }
   } else if (warp < live_warps) {
     // ------------------------- softmax + epilogue (row per thread) ----------------------
@@ -564,8 +666,20 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
     float m_run = -INFINITY, l_run = 0.f;
     // a > 0 goes into the exponential's argument; otherwise the scores are scaled first
     const bool pre = !(p.scale_log2 > 0.f);
-    const float a = pre ? 1.f : p.scale_log2;
+    float to_log2 = p.scale_log2;
     bool ok = true;
+    if constexpr (Q8 && BF16) {
+      if (f16 && n > 0) {
+        // this thread's row of Q, bf16 to fp16 times 2^-eq, in place in its swizzled tile
+        ok = __all_sync(0xffffffffu, mbar_wait(bar_q, 0, p.status));
+        if (ok) {
+          to_log2 *= q_row_to_fp16<D>(sQ, r);
+          fence_proxy_async_smem();
+          mbar_arrive(bar_qr);
+        }
+      }
+    }
+    const float a = pre ? 1.f : to_log2;
     for (int jj = 0; ok && jj < n; ++jj) {
       const int buf = jj % kNumS;
       const uint32_t t_s = tm_s0 + lane_off + buf * BN;
@@ -580,7 +694,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
         prefill::load_s<CH>(t_s + c0, raw);
         if (pre) {
 #pragma unroll
-          for (int c = 0; c < CH; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * p.scale_log2);
+          for (int c = 0; c < CH; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * to_log2);
         }
         if (key0 + BN > ctx) {
 #pragma unroll
@@ -594,7 +708,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
       };
       uint32_t raw[CH];
       float row_max = -INFINITY;
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < BN; c0 += CH) {
         read(c0, raw);
         row_max = fmaxf(row_max, chunk_max(raw));
@@ -613,11 +727,16 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
       // P_j (16-bit pairs) goes over BN / 2 columns of S_j: the first ones, or with two halves the
       // last, the second half first: its own scores are then in registers already, and the
       // first half's are not written over before they are read again
-#pragma unroll
+#pragma unroll 1
       for (int c0 = BN - CH; c0 >= 0; c0 -= CH) {
         if (CH < BN) read(c0, raw);
         uint32_t pk[CH / 2];
-        chunk_weights<CH, BF16>(raw, a, m_run, l_run, pk);
+        if constexpr (Q8 && BF16) {
+          if (f16) chunk_weights<CH, false>(raw, a, m_run, l_run, pk);
+          else chunk_weights<CH, true>(raw, a, m_run, l_run, pk);
+        } else {
+          chunk_weights<CH, BF16>(raw, a, m_run, l_run, pk);
+        }
         prefill::store_p<CH>(t_s + kPOff + c0 / 2, pk);
       }
       tmem_st_wait();
@@ -633,19 +752,18 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((jj - 1) % kNumS), ((jj - 1) / kNumS) & 1, p.status));
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_v(stage), (jj / STAGES) & 1, p.status));
         if (!ok) break;
-        uint8_t* vst = smem + L::kVOff + stage * L::kKVBytes;
+        const uint32_t vst = sV + stage * L::kKVBytes;
         const int r0 = max(0, ctx - key0);
         constexpr int kChunks = D / 8;  // 16-byte chunks a row
         for (int u = threadIdx.x; u < (BN - r0) * kChunks; u += live_warps * 32) {
           const int vr = r0 + u / kChunks, c = u % kChunks;
-          uint4* at = reinterpret_cast<uint4*>(vst + (vr / 8) * kRG + (c / 8) * kCB + (vr % 8) * 128 +
-                                               (c % 8) * 16);
+          const uint32_t at = vst + (vr / 8) * kRG + (c / 8) * kCB + (vr % 8) * 128 + (c % 8) * 16;
           const int d = key0 + vr - ctx;
           if (d >= n_draft) {
-            *at = make_uint4(0, 0, 0, 0);
+            sts128(at, make_uint4(0, 0, 0, 0));
             continue;
           }
-          const uint4 v = *at;
+          const uint4 v = lds128(at);
           uint32_t w[4] = {v.x, v.y, v.z, v.w};
           bool bad = false;
 #pragma unroll
@@ -654,7 +772,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
             if (nonfinite16(w[e] >> 16, BF16)) w[e] &= 0x0000ffffu, bad = true;
           }
           if (bad) {
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
+            sts128(at, make_uint4(w[0], w[1], w[2], w[3]));
             atomicOr(&poison[d >> 5], 1u << (d & 31));
           }
         }
@@ -677,7 +795,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
       if (n > 0) {
         for (int w = 0; w < kMaxTree / 32; ++w) any_poison |= poison[w] != 0;
       }
-      uint8_t* stage = smem + L::kKOff + warp * 4096;
+      const uint32_t stage = sK + warp * 4096;
       constexpr int kCols = SPLIT ? 32 : 64;  // columns of a 128-byte run
       const int64_t my_row = SPLIT ? flat * p.n_splits + split : flat;
 #pragma unroll 1
@@ -716,7 +834,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
               w = make_uint4(u[0], u[1], u[2], u[3]);
             }
             const int at = SPLIT ? ch : 4 * h + ch;
-            *reinterpret_cast<uint4*>(stage + lane * 128 + ((at ^ (lane & 7)) * 16)) = w;
+            sts128(stage + lane * 128 + ((at ^ (lane & 7)) * 16), w);
           }
         }
         __syncwarp();
@@ -725,7 +843,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
           const int rr = 4 * s + lane / 8, ch = lane % 8;
           const int64_t to = __shfl_sync(0xffffffffu, my_row, rr);
           const bool st = __shfl_sync(0xffffffffu, valid ? 1 : 0, rr);
-          const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
+          const uint4 w = lds128(stage + rr * 128 + ((ch ^ (rr & 7)) * 16));
           if (st) {
             if constexpr (SPLIT)
               *reinterpret_cast<uint4*>(p.o_part + to * D + c0 + ch * 4) = w;
@@ -736,7 +854,7 @@ __global__ void __launch_bounds__(Q8 ? 512 : 224, 1)
         __syncwarp();
       }
       if (valid) {
-        const float lse = have ? (m_run - kWeightLog2<BF16> + log2f(l_run)) * prefill::kLn2 : -INFINITY;
+        const float lse = have ? (m_run - (f16 ? kWeightLog2F16 : 0.f) + log2f(l_run)) * prefill::kLn2 : -INFINITY;
         // the merge takes a part of weight +inf as not a number, which a NaN part would not be
         if constexpr (SPLIT) p.lse_part[my_row] = lse != lse ? INFINITY : lse;
         else if (p.lse) p.lse[my_row] = lse;
@@ -860,9 +978,9 @@ int check_tree(const fa_tree_args* a, bool pointers) {
     return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: an 8-bit cache needs k_scales and v_scales");
   if (!aligned(a->q, 16) || !aligned(a->k_pages, 16) || !aligned(a->v_pages, 16) || !aligned(a->out, 16) ||
       !aligned(a->tree_mask, 8) || !aligned(a->seq_lens, 4) || !aligned(a->draft_lens, 4) ||
-      !aligned(a->page_table, 4) || !aligned(a->lse, 4))
+      !aligned(a->page_table, 4) || !aligned(a->lse, 4) || !aligned(a->k_scales, 8) || !aligned(a->v_scales, 8))
     return bad(FA_ERR_INVALID_ARG, "fa_tree_decode_paged: q, the pages and out must be 16-byte aligned, "
-                                   "tree_mask 8-byte aligned");
+                                   "tree_mask and the scales 8-byte aligned");
   // a tensor map takes strides of a multiple of 16 bytes, positive, below 2^40 bytes
   const int n[3] = {a->B, a->Hq, a->T};
   for (int i = 0; i < 3; ++i)

@@ -97,6 +97,36 @@ __device__ __noinline__ float nonfinite_v(const TreeParams& p, int b, int hk, in
   }
 }
 
+// Shared memory by its 32-bit address.  (A pointer rounded up to the swizzle's alignment is a
+// generic one to the compiler, whose loads and stores take several times as long.)
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+               ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(static_cast<uint16_t>(v)) : "memory");
+}
+
+// Two e4m3 codes (the low or the high 16 bits) -> fp16 pair, exact.
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r) : "r"(codes));
+  return r;
+}
+__device__ __forceinline__ uint32_t widen2_hi(uint32_t codes) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+      : "=r"(r) : "r"(codes));
+  return r;
+}
+
 // The kernel for few rows over 8-bit pages (tree_rows.cu): takes a call if tree_rows_takes says
 // so (rows = query heads per kv head times T); tree_rows_slots is the number of its CTAs that
 // the current device holds at once.

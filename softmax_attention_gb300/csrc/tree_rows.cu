@@ -55,20 +55,6 @@ struct RowsLayout {
   static_assert(kCtas * (kAlloc + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
-// Two e4m3 codes (the low 16 bits) -> fp16 pair, exact.
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
-      : "=r"(r) : "r"(codes));
-  return r;
-}
-__device__ __forceinline__ uint32_t widen2_hi(uint32_t codes) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
-      : "=r"(r) : "r"(codes));
-  return r;
-}
-
 // C (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  With g = lane / 4, t = lane % 4:
 // a0 (row g, k 2t..), a1 (g + 8, 2t..), a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..); b0 (k 2t.., column
 // g), b1 (k 2t + 8..); c0, c1 (row g, columns 2t, 2t + 1), c2, c3 (row g + 8).
@@ -85,13 +71,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t
 __device__ __forceinline__ void ldmatrix4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
 }
 
 // Four elements of q in fp32.
@@ -178,15 +157,16 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   // ---- copies: lane i of a slice stands for token i; the lane of a box's first token issues it
   const int box = min(p.page_size, SL), box_shift = 31 - __clz(box);
   const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  auto token_page = [&](int k) {  // page of token `lane` of this warp's slice k (0 past the end)
-    int id = 0;
+  // Page id of token `lane` of this warp's slice k (0 past the end), as the table has it; checked
+  // where it is first used, so that nothing waits for the load.
+  auto token_page = [&](int k) {
     const int key = (s_begin + k * kWarps) * SL + lane;
-    if (lane < SL && k < n && key < Lkv) {
-      const int v = __ldg(table + (key >> p.page_shift));
-      if (v >= 0 && v < p.num_pages) id = v;
-      else record_error(p.status, kDevBounds);
-    }
-    return id;
+    return lane < SL && k < n && key < Lkv ? __ldg(table + (key >> p.page_shift)) : 0;
+  };
+  auto checked = [&](int id) {
+    if (id >= 0 && id < p.num_pages) return id;
+    record_error(p.status, kDevBounds);
+    return 0;
   };
   auto token_row = [&](int k, int id) {
     const int key = (s_begin + k * kWarps) * SL + lane;
@@ -205,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   int ids[NS + 1];
 #pragma unroll
   for (int k = 0; k <= NS; ++k) ids[k] = token_page(k);
+#pragma unroll
+  for (int k = 0; k < NS; ++k) ids[k] = checked(ids[k]);
 #pragma unroll
   for (int k = 0; k < NS; ++k) {
     if (k >= n) break;
@@ -481,11 +463,12 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   bool ok = true;
   uint32_t bytes = scale_bytes(0, ids[0]);
   for (; ok && k < n; ++k) {
-    // ids[j] is slice k + j's here
+    // ids[j] is slice k + j's here, the last one not yet checked
     const uint32_t next_bytes = scale_bytes(k + 1, ids[1]);
-    const int next_id = ids[NS];
+    const int next_id = checked(ids[NS]);
 #pragma unroll
-    for (int j = 0; j < NS; ++j) ids[j] = ids[j + 1];
+    for (int j = 0; j < NS - 1; ++j) ids[j] = ids[j + 1];
+    ids[NS - 1] = next_id;
     ids[NS] = token_page(k + NS + 1);
     if ((s_begin + k * kWarps) * SL + SL > ctx) ok = slice(std::true_type{}, k, bytes, next_id);
     else ok = slice(std::false_type{}, k, bytes, next_id);
