@@ -25,9 +25,9 @@
 // scores), and both products run in fp16.  Otherwise they run in bf16, which holds any scale.
 //
 // Warp roles: 0-3 softmax + epilogue (thread t owns row t), 4 TMA producer, 5 P V issuer and
-// tensor-memory owner, 6 S issuer, and for 8-bit pages 8-11 converters (7 idle).  With 384
-// threads a thread has 168 registers, so there the softmax reads its row of scores in two
-// halves.
+// tensor-memory owner, 6 S issuer, and for 8-bit pages 7 second TMA producer, 8-11 converters.
+// With 384 threads a thread has 168 registers, so there the softmax reads its row of scores in
+// two halves.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -343,12 +343,14 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
     const int key = (t_begin + jj) * BN + row;
     return jj < n && key < Lkv ? __ldg(table + (key >> p.page_shift)) : 0;
   };
-  auto bytes_of = [&](int jj, int page) -> uint32_t {  // the row's scale bytes: K, V
+  // The row's scale bytes; nothing is computed from a load before the tile that uses it.
+  auto load_bytes = [&](int jj, int page, uint32_t& kb, uint32_t& vb) {
     const int key = (t_begin + jj) * BN + row;
-    if (jj >= n || key >= Lkv) return 0x7f7fu;
+    if (jj >= n || key >= Lkv) return;
     if (page < 0 || page >= p.num_pages) page = 0;  // the producer records a bad id
     const int64_t at = (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1));
-    return __ldg(p.k_scales + at) | (static_cast<uint32_t>(__ldg(p.v_scales + at)) << 8);
+    kb = __ldg(p.k_scales + at);
+    vb = __ldg(p.v_scales + at);
   };
   // raw row: BN / page_size pages of page_size rows, columns in blocks of kIn bytes
   const int pg = row >> p.page_shift, rr = row & (p.page_size - 1);
@@ -356,18 +358,19 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
   const uint32_t raw_blk = kIn << p.page_shift;
   const uint32_t raw_swz = D >= 128 ? rr & 7 : (rr >> 1) & 3;
   const uint32_t out_row = (row / 8) * kRG + (row % 8) * 128;
-  uint32_t bytes = bytes_of(0, page_of(0));
+  uint32_t kb = 127, vb = 127;
+  load_bytes(0, page_of(0), kb, vb);
   int page = page_of(1);
   for (int jj = 0; jj < n; ++jj) {
     const int rs = jj % RAW, stage = jj % STAGES;
     const int key = (t_begin + jj) * BN + row;
-    const uint32_t now = bytes;
-    bytes = bytes_of(jj + 1, page);
+    const uint32_t k_byte = kb, v_byte = vb;
+    load_bytes(jj + 1, page, kb, vb);
     page = page_of(jj + 2);
 #pragma unroll 1
     for (int v = 0; v < 2; ++v) {
       const Rings& g = v ? v_rings : k_rings;
-      const uint32_t byte = v ? now >> 8 : now & 0xffu;
+      const uint32_t byte = v ? v_byte : k_byte;
       const RowScale s = f16 ? row_scale<false>(byte) : row_scale<true>(byte);
       if (!mbar_wait(g.full + 8u * rs, (jj / RAW) & 1, p.status)) return;
       if (jj >= STAGES && !mbar_wait(g.out_empty + 8u * stage, ((jj / STAGES) - 1) & 1, p.status)) return;
@@ -524,10 +527,13 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
   const uint32_t tm_o = tmem;           // O: columns [0, D)
   const uint32_t tm_s0 = tmem + D;      // S/P buffer b: columns [D + b*BN, D + (b+1)*BN)
 
-  if (warp == 4) {
+  if (warp == 4 || (Q8 && warp == 7)) {
     // ------------------------------- TMA producer ---------------------------------------
+    // 8-bit pages: warp 4 copies K, warp 7 V (a box takes some 80 clocks to issue, and a tile has
+    // BN / page_size of each); 16-bit pages: warp 4 copies both.
+    const bool do_k = warp == 4, do_v = !Q8 || warp == 7;
     if (n > 0) {
-      if (lane == 0) {
+      if (do_k && lane == 0) {
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
         tma_prefetch_desc(&tm_v);
@@ -569,23 +575,27 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         if (jj + 1 < n) ids_next = tile_page(jj + 1);
         const int stage = jj % kRing;
         const uint32_t par = ((jj / kRing) - 1) & 1;
-        bool okw = jj < kRing || mbar_wait(empty_k(stage), par, p.status);
-        if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
-        if (lane == 0) mbar_arrive_expect_tx(full_k(stage), kBytes);
-        __syncwarp();
-        load_pages(dst_k + stage * kBytes, &tm_k, full_k(stage), ids);
-        k_issued = jj + 1;
-        okw = jj < kRing || mbar_wait(empty_v(stage), par, p.status);
-        if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
-        if (lane == 0) mbar_arrive_expect_tx(full_v(stage), kBytes);
-        __syncwarp();
-        load_pages(dst_v + stage * kBytes, &tm_v, full_v(stage), ids);
-        v_issued = jj + 1;
+        if (do_k) {
+          const bool okw = jj < kRing || mbar_wait(empty_k(stage), par, p.status);
+          if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
+          if (lane == 0) mbar_arrive_expect_tx(full_k(stage), kBytes);
+          __syncwarp();
+          load_pages(dst_k + stage * kBytes, &tm_k, full_k(stage), ids);
+          k_issued = jj + 1;
+        }
+        if (do_v) {
+          const bool okw = jj < kRing || mbar_wait(empty_v(stage), par, p.status);
+          if (!__shfl_sync(0xffffffffu, okw ? 1 : 0, 0)) break;
+          if (lane == 0) mbar_arrive_expect_tx(full_v(stage), kBytes);
+          __syncwarp();
+          load_pages(dst_v + stage * kBytes, &tm_v, full_v(stage), ids);
+          v_issued = jj + 1;
+        }
       }
-      if (lane == 0 && v_issued < n) {
+      if (lane == 0 && ((do_k && k_issued < n) || (do_v && v_issued < n))) {
         // A wait ran out: let the copies in flight land before the CTA exits.  Each of these is
         // the last one issued to its stage, so its parity wait is exact.
-        mbar_wait(bar_q, 0, nullptr);
+        if (do_k) mbar_wait(bar_q, 0, nullptr);
         for (int jj = max(0, k_issued - kRing); jj < k_issued; ++jj)
           mbar_wait(full_k(jj % kRing), (jj / kRing) & 1, nullptr);
         for (int jj = max(0, v_issued - kRing); jj < v_issued; ++jj)

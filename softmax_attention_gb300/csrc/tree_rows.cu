@@ -454,17 +454,20 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
 
   // ---- the loop: page ids are loaded a slice before their copies are issued, scale bytes a
   // slice before they are used ----
-  auto scale_bytes = [&](int k, int id) {
-    if (k >= n || lane >= SL || (s_begin + k * kWarps) * SL + lane >= Lkv) return 0x7f7fu;
+  auto load_bytes = [&](int k, int id, uint32_t& kb, uint32_t& vb) {
+    if (k >= n || lane >= SL || (s_begin + k * kWarps) * SL + lane >= Lkv) return;
     const int64_t at = token_row(k, id);
-    return static_cast<uint32_t>(__ldg(p.k_scales + at)) | (static_cast<uint32_t>(__ldg(p.v_scales + at)) << 8);
+    kb = __ldg(p.k_scales + at);
+    vb = __ldg(p.v_scales + at);
   };
   int k = 0;
   bool ok = true;
-  uint32_t bytes = scale_bytes(0, ids[0]);
+  uint32_t kb = 127, vb = 127;
+  load_bytes(0, ids[0], kb, vb);
   for (; ok && k < n; ++k) {
     // ids[j] is slice k + j's here, the last one not yet checked
-    const uint32_t next_bytes = scale_bytes(k + 1, ids[1]);
+    const uint32_t bytes = kb | (vb << 8);
+    load_bytes(k + 1, ids[1], kb, vb);
     const int next_id = checked(ids[NS]);
 #pragma unroll
     for (int j = 0; j < NS - 1; ++j) ids[j] = ids[j + 1];
@@ -472,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
     ids[NS] = token_page(k + NS + 1);
     if ((s_begin + k * kWarps) * SL + SL > ctx) ok = slice(std::true_type{}, k, bytes, next_id);
     else ok = slice(std::false_type{}, k, bytes, next_id);
-    bytes = next_bytes;
   }
   if (!ok) {
     // a wait ran out: let the copies in flight land (each stage's last one) before the CTA ends
