@@ -24,10 +24,9 @@
 // scaled by powers of two into fp16 (exact down to 2^-32 of a row's maximum, undone in the
 // scores), and both products run in fp16.  Otherwise they run in bf16, which holds any scale.
 //
-// Warp roles: 0-3 softmax + epilogue (thread t owns row t), 4 TMA producer, 5 P V issuer and
-// tensor-memory owner, 6 S issuer, and for 8-bit pages 7 second TMA producer, 8-11 converters.
-// With 384 threads a thread has 168 registers, so there the softmax reads its row of scores in
-// two halves.
+// Warp roles: 0-3 and the last four softmax + epilogue (a row of scores is shared by two
+// threads), 4 TMA producer, 5 P V issuer and tensor-memory owner, 6 S issuer, and for 8-bit pages 7
+// second TMA producer, 8-11 converters.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -49,7 +48,10 @@ constexpr int kNumS = 3;  // S/P buffers in tensor memory
 
 template <int D, int BN, int STAGES, int RAW, bool Q8>
 struct Layout {
-  static constexpr int kThreads = Q8 ? 384 : 224;
+  static constexpr int kHalves = 2;                    // softmax warps a row of scores
+  static constexpr int kConvertWarp = 8;               // first converter
+  static constexpr int kHalfWarp = Q8 ? 12 : 8;        // first softmax warp of the second halves
+  static constexpr int kThreads = (kHalfWarp + 4) * 32;
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kKVBytes = BN * D * 2;   // one 16-bit K (or V) stage
   static constexpr int kRawBytes = BN * D;      // one 8-bit K (or V) stage
@@ -62,7 +64,9 @@ struct Layout {
   // s_issuer_done, raw {k,v}_full[R], raw {k,v}_empty[R], q_ready
   static constexpr int kNumBars = 1 + 4 * STAGES + 3 * kNumS + 2 + (Q8 ? 4 * RAW + 1 : 0);
   static constexpr int kPoisonOff = kBarOff + kNumBars * 8 + 16;
-  static constexpr int kBytes = kPoisonOff + (kMaxTree / 32) * 4;
+  // what two halves of a row exchange (a maximum or a sum each), and the power of two of the row of Q
+  static constexpr int kRowOff = kPoisonOff + (kMaxTree / 32) * 4;
+  static constexpr int kBytes = kRowOff + 3 * kRows * 4;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 bytes
   static_assert(D + kNumS * BN <= 512, "tensor memory budget (O and the S/P buffers)");
   static_assert(kAlloc <= 232448, "shared memory budget");
@@ -96,18 +100,19 @@ __device__ __forceinline__ float chunk_max(const uint32_t (&raw)[CH]) {
                         fmaxf(mx[6], mx[7]));
 }
 
-// Moves the running maximum to a tile's (log2 units) if that is far enough above it; returns
-// whether O must then be rescaled by alpha.
-__device__ __forceinline__ bool raise_max(float row_max, float& m, float& l, float& alpha) {
-  const float m_new = fmaxf(m, row_max);
-  const bool need = m_new > m + prefill::kRescaleLog2;
-  alpha = 1.f;
-  if (need) {
-    alpha = exp2_approx(m - m_new);  // 0 when m is -inf
-    m = m_new;
-    l *= alpha;
-  }
-  return need;
+// Whether `x` holds for any thread of the named barrier's `threads`; all of them must call.
+__device__ __forceinline__ bool barrier_any(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"(id), "r"(threads), "r"(x ? 1u : 0u) : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void barrier_sync(int id, int threads) {
+  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Weights of CH scores against the maximum m: packed pairs, and their sum added to l.
@@ -399,13 +404,15 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
 }
 
 template <int D, int BN, int STAGES, int RAW, bool BF16, bool Q8, bool SPLIT>
-__global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
+__global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
   using L = Layout<D, BN, STAGES, RAW, Q8>;
   constexpr int kThreads = L::kThreads;
-  constexpr int CH = Q8 ? 64 : BN;  // scores a softmax thread holds at a time
-  constexpr int kPOff = CH < BN ? BN / 2 : 0;  // columns of P in an S/P buffer
+  constexpr int H = L::kHalves, CH = BN / H;  // scores of a tile that a softmax thread takes
+  // P (16-bit pairs) takes BN / 2 columns of S: the last ones, so that a half's weights only ever go
+  // over scores of the second half, which both halves' votes show to be in registers
+  constexpr int kPOff = BN / 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -491,7 +498,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
     }
     for (int i = 0; i < kNumS; ++i) {
       mbar_init(bar_s(i), 1);
-      mbar_init(bar_p(i), live_warps * 32);
+      mbar_init(bar_p(i), H * live_warps * 32);
       mbar_init(bar_pv(i), 1);
     }
     mbar_init(bar_done, 1);
@@ -652,56 +659,65 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
       tc_commit(bar_sdone);
       mbar_wait(bar_sdone, 0, nullptr);
     }
-  } else if (Q8 && warp >= 8) {
+  } else if (Q8 && warp >= L::kConvertWarp && warp < L::kHalfWarp) {
     // -------------------------------- converters ----------------------------------------
     if constexpr (Q8) {
       const Rings k{s_base + L::kRawKOff, bar_rk(0), bar_rke(0), sK, bar_k(0), bar_ke(0)};
       const Rings v{s_base + L::kRawVOff, bar_rv(0), bar_rve(0), sV, bar_v(0), bar_ve(0)};
       convert_tiles<D, BN, STAGES, RAW>(p, f16, k, v, poison, b, hk, t_begin, n, Lkv, ctx);
     }
-  } else if (warp < live_warps) {
-    // ------------------------- softmax + epilogue (row per thread) ----------------------
-    const int r = threadIdx.x;
+  } else if ((warp < 4 || warp >= L::kHalfWarp) && warp % 4 < live_warps) {
+    // --------------------------- softmax + epilogue -------------------------------------
+    // Row r = 32 (warp % 4) + lane, of which warps 0-3 take the first CH scores of a tile and warps
+    // kHalfWarp.. the last CH: two warps a sub-partition, so that one's latencies hide behind
+    // the other's.  They share the row's running maximum without exchanging it: each votes on
+    // whether its scores are far enough above it, and only a tile where some row's are (the
+    // first, and few others) trades maxima through shared memory.
+    const int half = warp >= L::kHalfWarp ? 1 : 0, wq = warp % 4;
+    const int r = wq * 32 + lane, team = H * live_warps * 32;
     const int g = r / p.q_per_tile, i = q0 + r % p.q_per_tile;
     const bool valid = g < p.G && i < p.T;   // a row of the output
     const bool active = valid && i < n_draft;  // a query of this sequence (else an empty row)
     const int64_t flat = (static_cast<int64_t>(b) * p.Hq + hk * p.G + g) * p.T + i;
+    float* row_mem = reinterpret_cast<float*>(smem + L::kRowOff) + r;
+    auto shared = [&](int h) -> float& { return row_mem[h * kRows]; };
+    float& q_factor = row_mem[2 * kRows];
     TreeRow row;
     row.i = i;
     row.n = active ? n_draft : 0;
     row.words = nullptr;
     if (p.mask && active)
       row.words = p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words;
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     float m_run = -INFINITY, l_run = 0.f;
     // a > 0 goes into the exponential's argument; otherwise the scores are scaled first
     const bool pre = !(p.scale_log2 > 0.f);
     float to_log2 = p.scale_log2;
+    // A wait that runs out leaves ok false: no more work, but every barrier is still met.
     bool ok = true;
     if constexpr (Q8 && BF16) {
-      if (f16 && n > 0) {
+      if (f16 && n > 0 && half == 0) {
         // this thread's row of Q, bf16 to fp16 times 2^-eq, in place in its swizzled tile
         ok = __all_sync(0xffffffffu, mbar_wait(bar_q, 0, p.status));
         if (ok) {
-          to_log2 *= q_row_to_fp16<D>(sQ, r);
+          q_factor = q_row_to_fp16<D>(sQ, r);
           fence_proxy_async_smem();
           mbar_arrive(bar_qr);
         }
       }
     }
-    const float a = pre ? 1.f : to_log2;
-    for (int jj = 0; ok && jj < n; ++jj) {
+    for (int jj = 0; jj < n; ++jj) {
       const int buf = jj % kNumS;
       const uint32_t t_s = tm_s0 + lane_off + buf * BN;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_s(buf), (jj / kNumS) & 1, p.status));
-      if (!ok) break;
-      tc_fence_after();
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_s(buf), (jj / kNumS) & 1, p.status));
+      if (Q8 && BF16 && f16 && jj == 0) to_log2 *= q_factor;  // written before S_0 could be issued
+      const float a = pre ? 1.f : to_log2;
       const int key0 = (t_begin + jj) * BN;
-      // Scores are read CH at a time: all of them at once where the registers allow, else in
-      // two halves, read again after the maximum is known (tensor-memory loads are cheap next
-      // to the exponentials).
-      auto read = [&](int c0, uint32_t (&raw)[CH]) {
-        prefill::load_s<CH>(t_s + c0, raw);
+      uint32_t raw[CH];
+      float row_max = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        prefill::load_s<CH>(t_s + half * CH, raw);
         if (pre) {
 #pragma unroll
           for (int c = 0; c < CH; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * to_log2);
@@ -709,37 +725,39 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         if (key0 + BN > ctx) {
 #pragma unroll
           for (int w = 0; w < CH / 32; ++w) {
-            const uint32_t bits = row_bits(row, key0 + c0 + 32 * w - ctx);
+            const uint32_t bits = row_bits(row, key0 + half * CH + 32 * w - ctx);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((bits >> c) & 1)) raw[32 * w + c] = 0xff800000u;  // -inf
           }
         }
-      };
-      uint32_t raw[CH];
-      float row_max = -INFINITY;
-#pragma unroll 1
-      for (int c0 = 0; c0 < BN; c0 += CH) {
-        read(c0, raw);
-        row_max = fmaxf(row_max, chunk_max(raw));
+        row_max = a * chunk_max(raw);
+        tc_fence_before();  // the loads, before the other half's stores over these columns
       }
-      float alpha;
-      const bool need = raise_max(a * row_max, m_run, l_run, alpha);
-      // O is rescaled only once every earlier P V product is in it; a tile with no rescale
-      // does not wait (S_j itself needed P_{j-3} V_{j-3} finished)
-      const bool rescale = jj > 0 && __any_sync(0xffffffffu, need);
-      if (rescale) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((jj - 1) % kNumS), ((jj - 1) / kNumS) & 1, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        prefill::rescale_o<D>(tm_o + lane_off, alpha);
+      const bool raise = barrier_any(1, team, ok && row_max > m_run + prefill::kRescaleLog2);
+      if (raise) {
+        shared(half) = row_max;
+        barrier_sync(2, team);
+        const float m_new = fmaxf(m_run, fmaxf(row_max, shared(1 - half)));
+        float alpha = 1.f;
+        if (m_new > m_run + prefill::kRescaleLog2) {
+          alpha = exp2_approx(m_run - m_new);  // 0 when m_run is -inf
+          m_run = m_new;
+          l_run *= alpha;
+        }
+        if (jj > 0) {
+          // O is rescaled, half its columns each, once every earlier P V product is in it; a
+          // tile with no rescale does not wait (S_j itself needed P_{j-3} V_{j-3} finished)
+          if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((jj - 1) % kNumS), ((jj - 1) / kNumS) & 1, p.status));
+          if (ok) {
+            tc_fence_after();
+            prefill::rescale_o<D / H>(tm_o + lane_off + half * (D / H), alpha);
+          }
+        }
       }
-      // P_j (16-bit pairs) goes over BN / 2 columns of S_j: the first ones, or with two halves the
-      // last, the second half first: its own scores are then in registers already, and the
-      // first half's are not written over before they are read again
-#pragma unroll 1
-      for (int c0 = BN - CH; c0 >= 0; c0 -= CH) {
-        if (CH < BN) read(c0, raw);
+      if (!ok) continue;
+      tc_fence_after();
+      {
         uint32_t pk[CH / 2];
         if constexpr (Q8 && BF16) {
           if (f16) chunk_weights<CH, false>(raw, a, m_run, l_run, pk);
@@ -747,7 +765,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         } else {
           chunk_weights<CH, BF16>(raw, a, m_run, l_run, pk);
         }
-        prefill::store_p<CH>(t_s + kPOff + c0 / 2, pk);
+        prefill::store_p<CH>(t_s + kPOff + half * (CH / 2), pk);
       }
       tmem_st_wait();
       if (!Q8 && key0 + BN > ctx) {
@@ -758,14 +776,14 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         // The parity wait for V_j is exact only once V_{j-STAGES} has landed: P_{j-1} V_{j-1}
         // finishing makes sure of it.
         const int stage = jj % STAGES;
-        if (jj > 0 && !rescale)
+        if (jj > 0 && !raise)
           ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((jj - 1) % kNumS), ((jj - 1) / kNumS) & 1, p.status));
         if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_v(stage), (jj / STAGES) & 1, p.status));
-        if (!ok) break;
+        if (!ok) continue;
         const uint32_t vst = sV + stage * L::kKVBytes;
         const int r0 = max(0, ctx - key0);
         constexpr int kChunks = D / 8;  // 16-byte chunks a row
-        for (int u = threadIdx.x; u < (BN - r0) * kChunks; u += live_warps * 32) {
+        for (int u = (half * live_warps + wq) * 32 + lane; u < (BN - r0) * kChunks; u += team) {
           const int vr = r0 + u / kChunks, c = u % kChunks;
           const uint32_t at = vst + (vr / 8) * kRG + (c / 8) * kCB + (vr % 8) * 128 + (c % 8) * 16;
           const int d = key0 + vr - ctx;
@@ -795,21 +813,26 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
       ok = __all_sync(0xffffffffu, mbar_wait(bar_pv((n - 1) % kNumS), ((n - 1) / kNumS) & 1, p.status));
       tc_fence_after();
     }
+    // the row's sum over both halves (their maxima are one)
+    barrier_sync(2, team);  // the last maxima have been read
+    shared(half) = l_run;
+    barrier_sync(2, team);
+    l_run = shared(0) + shared(1);
     if (ok) {
-      // O / l, a row's slab of columns at a time: staged in this warp's part of the K ring (free:
-      // every MMA has finished) with 16-byte chunks swizzled by the row, then written out as
-      // whole 128-byte runs, eight lanes a row.
+      // O / l, a row's slab of columns at a time, the halves in turn: staged in this warp's part of
+      // the K ring (free: every MMA has finished) with 16-byte chunks swizzled by the row, then
+      // written out as whole 128-byte runs, eight lanes a row.
       const bool have = active && n > 0 && !(l_run == 0.f);  // a NaN sum stays NaN
       const float inv_l = 1.f / l_run;
       bool any_poison = false;
       if (n > 0) {
         for (int w = 0; w < kMaxTree / 32; ++w) any_poison |= poison[w] != 0;
       }
-      const uint32_t stage = sK + warp * 4096;
+      const uint32_t stage = sK + (half * 4 + wq) * 4096;
       constexpr int kCols = SPLIT ? 32 : 64;  // columns of a 128-byte run
       const int64_t my_row = SPLIT ? flat * p.n_splits + split : flat;
 #pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += kCols) {
+      for (int c0 = half * kCols; c0 < D; c0 += H * kCols) {
 #pragma unroll
         for (int h = 0; h < kCols / 32; ++h) {
           uint32_t o[32];
@@ -863,7 +886,7 @@ __global__ void __launch_bounds__(Q8 ? 384 : 224, 1)
         }
         __syncwarp();
       }
-      if (valid) {
+      if (valid && half == 0) {
         const float lse = have ? (m_run - (f16 ? kWeightLog2F16 : 0.f) + log2f(l_run)) * prefill::kLn2 : -INFINITY;
         // the merge takes a part of weight +inf as not a number, which a NaN part would not be
         if constexpr (SPLIT) p.lse_part[my_row] = lse != lse ? INFINITY : lse;
