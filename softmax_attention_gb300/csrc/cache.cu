@@ -28,19 +28,36 @@ constexpr int kMaxRot = 512;
 // ------------------------------------------------------------------------------------------
 // Sixteen-bit and fp32 rows in registers: eight elements.
 // ------------------------------------------------------------------------------------------
+// As loaded (so that a batch of loads in flight holds no more registers than its bytes).
+template <typename T>
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T* src) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) r.v[i] = reinterpret_cast<const uint4*>(src)[i];
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void expand8(const Raw8<T>& r, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t w[8] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w, r.v[1].x, r.v[1].y, r.v[1].z, r.v[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
+  } else {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack2<T>(w[i], x[2 * i], x[2 * i + 1]);
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* src, float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(src);
-    const float4 b = *reinterpret_cast<const float4*>(src + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 w = *reinterpret_cast<const uint4*>(src);
-    const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) unpack2<T>(r[i], x[2 * i], x[2 * i + 1]);
-  }
+  expand8<T>(load_raw8<T>(src), x);
 }
 
 template <typename T>
@@ -126,21 +143,21 @@ struct RotaryParams {
   int transpose;
   int T, D, half, units, rot_units;
   int heads_per_thread, head_groups;
-  int64_t tokens;  // B * T
+  uint32_t tokens;  // B * T; tokens * units * head_groups is below 2^31
 };
 
 template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryParams p) {
   __shared__ int64_t steps[kMaxRot / 2];
   fill_steps(steps, p.inv_freq, p.half);
-  const int64_t per_group = p.tokens * p.units;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t group = idx / per_group;
-  if (group >= p.head_groups) return;
-  const int64_t rem = idx - group * per_group;
-  const int64_t token = rem / p.units;
+  const uint32_t per_group = p.tokens * p.units;
+  const uint32_t idx = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t group = idx / per_group;
+  if (group >= static_cast<uint32_t>(p.head_groups)) return;
+  const uint32_t rem = idx - group * per_group;
+  const uint32_t token = rem / p.units;
   const int u = static_cast<int>(rem - token * p.units);
-  const int64_t b = token / p.T, t = token - b * p.T;
+  const uint32_t b = token / p.T, t = token - b * p.T;
   Turn turn;
   const bool rotated = u < p.rot_units;
   if (rotated)
@@ -151,25 +168,31 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryParams p) 
   const bool second = c1 < p.D;
   const int h0 = static_cast<int>(group) * p.heads_per_thread;
   const int h1 = min(h0 + p.heads_per_thread, p.H[0] + p.H[1]);
-  constexpr int kBatch = 4;  // heads whose loads are issued together
+  // this token's row of head 0 in q, k and their outputs
+  const T* x0 = static_cast<const T*>(p.x[0]) + b * p.xs[0][0] + t * p.xs[0][2];
+  const T* x1 = static_cast<const T*>(p.x[1]) + b * p.xs[1][0] + t * p.xs[1][2];
+  T* y0 = static_cast<T*>(p.y[0]) + b * p.ys[0][0] + t * p.ys[0][2];
+  T* y1 = static_cast<T*>(p.y[1]) + b * p.ys[1][0] + t * p.ys[1][2];
+  constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;  // heads whose loads are issued together
   for (int h = h0; h < h1; h += kBatch) {
-    float a[kBatch][8], c[kBatch][8];
+    Raw8<T> ra[kBatch], rc[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (h + j >= h1) break;
-      const int w = h + j >= p.H[0], hh = h + j - (w ? p.H[0] : 0);
-      const T* src = static_cast<const T*>(p.x[w]) + b * p.xs[w][0] + hh * p.xs[w][1] + t * p.xs[w][2];
-      load8(src + c0, a[j]);
-      if (second) load8(src + c1, c[j]);
+      const T* src = h + j < p.H[0] ? x0 + (h + j) * p.xs[0][1] : x1 + (h + j - p.H[0]) * p.xs[1][1];
+      ra[j] = load_raw8<T>(src + c0);
+      if (second) rc[j] = load_raw8<T>(src + c1);
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (h + j >= h1) break;
-      const int w = h + j >= p.H[0], hh = h + j - (w ? p.H[0] : 0);
-      if (rotated) rotate<INTERLEAVED>(turn, a[j], c[j]);
-      T* dst = static_cast<T*>(p.y[w]) + b * p.ys[w][0] + hh * p.ys[w][1] + t * p.ys[w][2];
-      store8(dst + c0, a[j]);
-      if (second) store8(dst + c1, c[j]);
+      float a[8], c[8];
+      expand8<T>(ra[j], a);
+      expand8<T>(rc[j], c);
+      if (rotated) rotate<INTERLEAVED>(turn, a, c);
+      T* dst = h + j < p.H[0] ? y0 + (h + j) * p.ys[0][1] : y1 + (h + j - p.H[0]) * p.ys[1][1];
+      store8(dst + c0, a);
+      if (second) store8(dst + c1, c);
     }
   }
 }
@@ -191,7 +214,7 @@ struct AppendParams {
   float amplitude;
   int T, D, Hkv, half, rot_units, page_size, page_shift, max_pages, num_pages;
   int heads_per_thread, head_groups;
-  int64_t tokens;
+  uint32_t tokens;  // B * T; tokens * units * head_groups is below 2^31
   uint32_t* status;
 };
 
@@ -236,16 +259,16 @@ template <typename T, bool Q8, int UNITS, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
   __shared__ int64_t steps[128];  // D <= 256
   if (p.inv_freq) fill_steps(steps, p.inv_freq, p.half);
-  const int64_t per_group = p.tokens * UNITS;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t group = idx / per_group;
+  const uint32_t per_group = p.tokens * UNITS;
+  const uint32_t idx = blockIdx.x * kThreads + threadIdx.x;
+  const uint32_t group = idx / per_group;
   // a row's threads stand or fall together (UNITS divides the warp); the shuffles need them all
-  bool live = group < p.head_groups;
-  const int64_t rem = live ? idx - group * per_group : 0;
-  const int64_t token = rem / UNITS;
+  bool live = group < static_cast<uint32_t>(p.head_groups);
+  const uint32_t rem = live ? idx - group * per_group : 0;
+  const uint32_t token = rem / UNITS;
   const int u = static_cast<int>(rem % UNITS);
   const int64_t b = token / p.T;
-  const int t = static_cast<int>(token - b * p.T);
+  const int t = static_cast<int>(token - static_cast<uint32_t>(b) * p.T);
   int64_t slot_row = 0;  // (page * Hkv) * page_size + slot, for head 0
   int pos = 0;
   if (live) {
@@ -293,7 +316,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 
 // ------------------------------------------------------------------------------------------
 // Cache read: dense [B,Hkv,L,D] from the pages, zeros past each sequence.  A thread keeps its
-// eight columns and walks down the tokens of its block, kBatch of them in flight.
+// eight columns and walks down the tokens of its block: kGatherSteps batches of kGatherBatch loads
+// in flight.
 // ------------------------------------------------------------------------------------------
 struct GatherParams {
   const void* pages[2];
@@ -305,55 +329,71 @@ struct GatherParams {
   uint32_t* status;
 };
 
-constexpr int kGatherBatch = 4;
-
-template <typename TIn, typename TOut, bool Q8>
+template <typename TIn, typename TOut, bool Q8, int kGatherBatch, int kGatherSteps>
 __global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
   const int lanes = p.D / 8;                // threads a row
   const int rows = kThreads / lanes;        // rows a step
   const int c = (threadIdx.x % lanes) * 8, r = threadIdx.x / lanes;
   const int b = blockIdx.z >> 1, w = blockIdx.z & 1;
   const int h = blockIdx.y;
+  const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
+  const int t0 = blockIdx.x * rows * kGatherBatch * kGatherSteps + r;
+  // Page ids of all rows, before anything is waited for: the length, the ids and the data would
+  // otherwise be three memory latencies one after another.  Entries past max_seq_len's pages are
+  // not read; those past the sequence's end are read and not used.
+  const int last_page = (p.L - 1) >> p.page_shift;
   int len = p.seq_lens[b];
+  int id[kGatherBatch * kGatherSteps];
+#pragma unroll
+  for (int j = 0; j < kGatherBatch * kGatherSteps; ++j)
+    id[j] = __ldg(table + min((t0 + j * rows) >> p.page_shift, last_page));
   if (len < 0 || len > p.L || static_cast<int64_t>(len) > static_cast<int64_t>(p.max_pages) * p.page_size) {
     if (threadIdx.x == 0) record_error(p.status, kDevBounds);
     len = 0;
   }
-  const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  TOut* out = static_cast<TOut*>(p.out[w]) + (static_cast<int64_t>(b) * p.Hkv + h) * p.L * p.D;
-  const int t0 = blockIdx.x * rows * kGatherBatch + r;
-  int64_t row[kGatherBatch];
+  // selected, not indexed: a kernel parameter indexed at run time is copied to local memory
+  TOut* out = static_cast<TOut*>(w ? p.out[1] : p.out[0]) + (static_cast<int64_t>(b) * p.Hkv + h) * p.L * p.D;
+  const void* pages = w ? p.pages[1] : p.pages[0];
+  const uint8_t* scales = w ? p.scales[1] : p.scales[0];
 #pragma unroll
-  for (int j = 0; j < kGatherBatch; ++j) {
-    const int t = t0 + j * rows;
-    row[j] = -1;
-    if (t < len) {
-      const int page = __ldg(table + (t >> p.page_shift));
-      if (page >= 0 && page < p.num_pages)
-        row[j] = (static_cast<int64_t>(page) * p.Hkv + h) * p.page_size + (t & (p.page_size - 1));
-      else
+  for (int s = 0; s < kGatherSteps; ++s) {
+    uint2 q[kGatherBatch];
+    uint32_t byte[kGatherBatch];
+    Raw8<uint16_t> raw[kGatherBatch];
+#pragma unroll
+    for (int j = 0; j < kGatherBatch; ++j) {
+      const int t = t0 + (s * kGatherBatch + j) * rows, page = id[s * kGatherBatch + j];
+      q[j] = make_uint2(0, 0);
+      byte[j] = 127;
+      raw[j].v[0] = make_uint4(0, 0, 0, 0);
+      if (t >= len) continue;
+      if (page < 0 || page >= p.num_pages) {
         record_error(p.status, kDevBounds);
+        continue;
+      }
+      const int64_t row = (static_cast<int64_t>(page) * p.Hkv + h) * p.page_size + (t & (p.page_size - 1));
+      if constexpr (Q8) {
+        q[j] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(pages) + row * p.D + c);
+        byte[j] = __ldg(scales + row);
+      } else {
+        raw[j] = load_raw8(static_cast<const uint16_t*>(pages) + row * p.D + c);
+      }
     }
-  }
-  float x[kGatherBatch][8];
 #pragma unroll
-  for (int j = 0; j < kGatherBatch; ++j) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[j][i] = 0.f;
-    if (row[j] < 0) continue;
-    if constexpr (Q8) {
-      const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.pages[w]) + row[j] * p.D + c);
-      const float s = scale_of_byte(p.scales[w][row[j]]);
-      dequant4(q.x, s, x[j][0], x[j][1], x[j][2], x[j][3]);
-      dequant4(q.y, s, x[j][4], x[j][5], x[j][6], x[j][7]);
-    } else {
-      load8(static_cast<const TIn*>(p.pages[w]) + row[j] * p.D + c, x[j]);
+    for (int j = 0; j < kGatherBatch; ++j) {
+      const int t = t0 + (s * kGatherBatch + j) * rows;
+      float x[8];
+      if constexpr (Q8) {
+        const float f = scale_of_byte(byte[j]);
+        dequant4(q[j].x, f, x[0], x[1], x[2], x[3]);
+        dequant4(q[j].y, f, x[4], x[5], x[6], x[7]);
+      } else {
+        Raw8<TIn> e;
+        e.v[0] = raw[j].v[0];
+        expand8<TIn>(e, x);
+      }
+      if (t < p.L) store8(out + static_cast<int64_t>(t) * p.D + c, x);
     }
-  }
-#pragma unroll
-  for (int j = 0; j < kGatherBatch; ++j) {
-    const int t = t0 + j * rows;
-    if (t < p.L) store8(out + static_cast<int64_t>(t) * p.D + c, x[j]);
   }
 }
 
@@ -381,19 +421,19 @@ int check_rot(const char* who, int rot_dim, int D) {
   return FA_OK;
 }
 
-// Heads a thread takes: as many as eight (the angles of a token are then computed once for
-// them), but no more than leave every SM its 2048 threads.
+// Heads a thread takes: as many as eight (the eight angles of a unit cost as much as several rows,
+// and are then computed once for them), but no more than leave every SM 512 threads.
 int heads_per_thread(int64_t unit_tokens, int H) {
   const int sms = num_sms() > 0 ? num_sms() : 152;
   int hpt = 8;
-  while (hpt > 1 && unit_tokens * ((H + hpt - 1) / hpt) < 2048LL * sms) hpt /= 2;
+  while (hpt > 1 && unit_tokens * ((H + hpt - 1) / hpt) < 512LL * sms) hpt /= 2;
   return hpt < H ? hpt : H;
 }
 
 template <typename T>
 cudaError_t run_rotary(const RotaryParams& p, bool interleaved, cudaStream_t st) {
-  const int64_t threads = p.tokens * p.units * p.head_groups;
-  const unsigned grid = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+  const uint32_t threads = p.tokens * p.units * p.head_groups;
+  const unsigned grid = (threads + kThreads - 1) / kThreads;
   if (interleaved) rotary_kernel<T, true><<<grid, kThreads, 0, st>>>(p);
   else rotary_kernel<T, false><<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
@@ -401,8 +441,8 @@ cudaError_t run_rotary(const RotaryParams& p, bool interleaved, cudaStream_t st)
 
 template <typename T, bool Q8, int UNITS>
 cudaError_t run_append(const AppendParams& p, bool interleaved, cudaStream_t st) {
-  const int64_t threads = p.tokens * UNITS * p.head_groups;
-  const unsigned grid = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+  const uint32_t threads = p.tokens * UNITS * p.head_groups;
+  const unsigned grid = (threads + kThreads - 1) / kThreads;
   if (interleaved) append_kernel<T, Q8, UNITS, true><<<grid, kThreads, 0, st>>>(p);
   else append_kernel<T, Q8, UNITS, false><<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
@@ -417,14 +457,29 @@ cudaError_t run_append_d(const AppendParams& p, bool interleaved, cudaStream_t s
   }
 }
 
+template <typename TIn, typename TOut, bool Q8, int BATCH, int STEPS>
+cudaError_t run_gather_as(const GatherParams& p, cudaStream_t st) {
+  const int rows = kThreads / (p.D / 8) * BATCH * STEPS;
+  const dim3 grid((p.L + rows - 1) / rows, p.Hkv, 2 * p.B);
+  gather_kernel<TIn, TOut, Q8, BATCH, STEPS><<<grid, kThreads, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+// Sixteen rows a thread, eight in flight, hide the memory's latency best (8 sequences of up to
+// 8192 tokens: 61 us, against 78 with four rows a thread); two a thread give a small read more
+// blocks (1021 tokens of two heads: 6 us against 10).  Sixteen once they fill every SM.
+template <typename TIn, typename TOut, bool Q8>
+cudaError_t run_gather_to(const GatherParams& p, cudaStream_t st) {
+  const int sms = num_sms() > 0 ? num_sms() : 152;
+  const int64_t blocks = static_cast<int64_t>(p.L) * (p.D / 8) / (kThreads * 16) * p.Hkv * 2 * p.B;
+  return blocks >= 2 * sms ? run_gather_as<TIn, TOut, Q8, 8, 2>(p, st) : run_gather_as<TIn, TOut, Q8, 2, 1>(p, st);
+}
+
 template <typename TIn, bool Q8>
 cudaError_t run_gather(const GatherParams& p, fa_dtype out, cudaStream_t st) {
-  const int rows = kThreads / (p.D / 8) * kGatherBatch;
-  const dim3 grid((p.L + rows - 1) / rows, p.Hkv, 2 * p.B);
-  if (out == FA_BF16) gather_kernel<TIn, __nv_bfloat16, Q8><<<grid, kThreads, 0, st>>>(p);
-  else if (out == FA_FP16) gather_kernel<TIn, __half, Q8><<<grid, kThreads, 0, st>>>(p);
-  else gather_kernel<TIn, float, Q8><<<grid, kThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  if (out == FA_BF16) return run_gather_to<TIn, __nv_bfloat16, Q8>(p, st);
+  if (out == FA_FP16) return run_gather_to<TIn, __half, Q8>(p, st);
+  return run_gather_to<TIn, float, Q8>(p, st);
 }
 
 int log2_of(int x) {
@@ -510,11 +565,12 @@ int fa_rotary(const fa_rotary_args* a, void* stream) {
   p.half = a->rot_dim / 2;
   p.rot_units = a->rot_dim / 16;
   p.units = p.rot_units + (a->D - a->rot_dim + 15) / 16;
-  p.tokens = static_cast<int64_t>(a->B) * a->T;
+  const int64_t tokens = static_cast<int64_t>(a->B) * a->T;
   const int H = a->Hq + a->Hk;
-  p.heads_per_thread = heads_per_thread(p.tokens * p.units, H);
+  p.tokens = static_cast<uint32_t>(tokens);
+  p.heads_per_thread = heads_per_thread(tokens * p.units, H);
   p.head_groups = (H + p.heads_per_thread - 1) / p.heads_per_thread;
-  if (p.tokens * p.units * p.head_groups > 2147483647LL * kThreads)
+  if (tokens > 2147483647LL / p.units / p.head_groups - kThreads)
     return bad(FA_ERR_UNSUPPORTED, "fa_rotary: too many rows for one launch");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = a->dtype == FA_BF16   ? run_rotary<__nv_bfloat16>(p, a->interleaved != 0, st)
@@ -576,12 +632,13 @@ int fa_cache_append(const fa_cache_append_args* a, void* stream) {
   p.page_shift = log2_of(a->page_size);
   p.max_pages = a->max_pages;
   p.num_pages = a->num_pages;
-  p.tokens = static_cast<int64_t>(a->B) * a->T;
+  const int64_t tokens = static_cast<int64_t>(a->B) * a->T;
+  p.tokens = static_cast<uint32_t>(tokens);
   p.status = status;
   // without a rotation a thread has nothing to share between heads
-  p.heads_per_thread = a->inv_freq ? heads_per_thread(p.tokens * (a->D / 16), a->Hkv) : 1;
+  p.heads_per_thread = a->inv_freq ? heads_per_thread(tokens * (a->D / 16), a->Hkv) : 1;
   p.head_groups = (a->Hkv + p.heads_per_thread - 1) / p.heads_per_thread;
-  if (p.tokens * (a->D / 16) * p.head_groups > 2147483647LL * kThreads)
+  if (tokens > 2147483647LL / (a->D / 16) / p.head_groups - kThreads)
     return bad(FA_ERR_UNSUPPORTED, "fa_cache_append: too many rows for one launch");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool il = a->interleaved != 0;
