@@ -335,7 +335,8 @@ struct Rings {
   uint32_t raw, full, empty, out, out_full, out_empty;
 };
 
-template <int D, int BN, int STAGES, int RAW>
+// BF16: the queries' type.
+template <int D, int BN, int STAGES, int RAW, bool BF16>
 __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, const Rings& k_rings,
                                               const Rings& v_rings, uint32_t* poison, int b, int hk,
                                               int t_begin, int n, int Lkv, int ctx) {
@@ -343,32 +344,34 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
   constexpr int kRawBytes = BN * D, kOutBytes = BN * D * 2;
   constexpr uint32_t kRG = (D / 64) * 1024u;
   const int ct = threadIdx.x % 128, row = ct % BN, part = ct / BN;
-  const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
-  auto page_of = [&](int jj) {
-    const int key = (t_begin + jj) * BN + row;
-    return jj < n && key < Lkv ? __ldg(table + (key >> p.page_shift)) : 0;
-  };
-  // The row's scale bytes; nothing is computed from a load before the tile that uses it.
-  auto load_bytes = [&](int jj, int page, uint32_t& kb, uint32_t& vb) {
-    const int key = (t_begin + jj) * BN + row;
-    if (jj >= n || key >= Lkv) return;
-    if (page < 0 || page >= p.num_pages) page = 0;  // the producer records a bad id
-    const int64_t at = (static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1));
-    kb = __ldg(p.k_scales + at);
-    vb = __ldg(p.v_scales + at);
-  };
-  // raw row: BN / page_size pages of page_size rows, columns in blocks of kIn bytes
+  // this row's slot in its page is the same in every tile (BN is a multiple of the page size)
   const int pg = row >> p.page_shift, rr = row & (p.page_size - 1);
+  const int64_t slot = static_cast<int64_t>(hk) * p.page_size + rr;
+  const uint8_t *k_scales = p.k_scales + slot, *v_scales = p.v_scales + slot;
+  const int page_stride = p.Hkv * p.page_size;
+  const int32_t* entry = p.page_table + static_cast<int64_t>(b) * p.max_pages +
+                         ((t_begin * BN) >> p.page_shift) + pg;
+  const int tile_pages = BN >> p.page_shift;
+  const int last = Lkv - t_begin * BN - row;  // tiles jj with jj * BN < last hold a token here
+  // Page ids two tiles ahead, scale bytes one: nothing is computed from a load before then.
+  auto page_of = [&](int jj) { return jj < n && jj * BN < last ? __ldg(entry + jj * tile_pages) : 0; };
+  auto load_bytes = [&](int jj, int page, uint32_t& kb, uint32_t& vb) {
+    if (jj >= n || jj * BN >= last) return;
+    if (static_cast<uint32_t>(page) >= static_cast<uint32_t>(p.num_pages)) page = 0;  // the producer records it
+    const int64_t at = static_cast<int64_t>(page) * page_stride;
+    kb = __ldg(k_scales + at);
+    vb = __ldg(v_scales + at);
+  };
   const uint32_t raw_row = (pg << p.page_shift) * D + rr * kIn;
   const uint32_t raw_blk = kIn << p.page_shift;
   const uint32_t raw_swz = D >= 128 ? rr & 7 : (rr >> 1) & 3;
-  const uint32_t out_row = (row / 8) * kRG + (row % 8) * 128;
+  const uint32_t dst_row = (row / 8) * kRG + (row % 8) * 128;
   uint32_t kb = 127, vb = 127;
   load_bytes(0, page_of(0), kb, vb);
   int page = page_of(1);
+  int rs = 0, stage = 0;  // raw and 16-bit slots, their phases
+  uint32_t raw_phase = 0, out_phase = 1;
   for (int jj = 0; jj < n; ++jj) {
-    const int rs = jj % RAW, stage = jj % STAGES;
-    const int key = (t_begin + jj) * BN + row;
     const uint32_t k_byte = kb, v_byte = vb;
     load_bytes(jj + 1, page, kb, vb);
     page = page_of(jj + 2);
@@ -376,23 +379,27 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
     for (int v = 0; v < 2; ++v) {
       const Rings& g = v ? v_rings : k_rings;
       const uint32_t byte = v ? v_byte : k_byte;
-      const RowScale s = f16 ? row_scale<false>(byte) : row_scale<true>(byte);
-      if (!mbar_wait(g.full + 8u * rs, (jj / RAW) & 1, p.status)) return;
-      if (jj >= STAGES && !mbar_wait(g.out_empty + 8u * stage, ((jj / STAGES) - 1) & 1, p.status)) return;
-      const uint32_t raw = g.raw + rs * kRawBytes + raw_row;
-      const uint32_t dst = g.out + stage * kOutBytes + out_row;
-      if (key >= Lkv) {
+      if (!mbar_wait(g.full + 8u * rs, raw_phase, p.status)) return;
+      if (jj >= STAGES && !mbar_wait(g.out_empty + 8u * stage, out_phase, p.status)) return;
+      const uint32_t raw = g.raw + rs * kRawBytes + raw_row, dst = g.out + stage * kOutBytes + dst_row;
+      if (jj * BN >= last) {
         // past the sequence's end: zeros, whatever the page holds
         for (int c = part * (D / 8 / kParts); c < (part + 1) * (D / 8 / kParts); ++c)
           sts128(dst + (c / 8) * 1024 + (((c % 8) ^ (row & 7)) * 16), make_uint4(0, 0, 0, 0));
       } else {
+        const int key = (t_begin + jj) * BN + row;
         const int draft = v && key >= ctx ? key - ctx : -1;
-        // nearly always one factor holds the scale (in fp16 mode of bf16 queries always)
         uint32_t marks;
-        if (f16) marks = s.two ? widen_row<D, kParts, false, true>(raw, raw_blk, raw_swz, dst, row, part, s)
-                               : widen_row<D, kParts, false, false>(raw, raw_blk, raw_swz, dst, row, part, s);
-        else marks = s.two ? widen_row<D, kParts, true, true>(raw, raw_blk, raw_swz, dst, row, part, s)
-                           : widen_row<D, kParts, true, false>(raw, raw_blk, raw_swz, dst, row, part, s);
+        if (f16) {
+          const RowScale s = row_scale<false>(byte);
+          // fp16 stands in for bf16 only where one factor holds every scale
+          if (!BF16 && s.two) marks = widen_row<D, kParts, false, true>(raw, raw_blk, raw_swz, dst, row, part, s);
+          else marks = widen_row<D, kParts, false, false>(raw, raw_blk, raw_swz, dst, row, part, s);
+        } else {
+          const RowScale s = row_scale<true>(byte);
+          if (s.two) marks = widen_row<D, kParts, true, true>(raw, raw_blk, raw_swz, dst, row, part, s);
+          else marks = widen_row<D, kParts, true, false>(raw, raw_blk, raw_swz, dst, row, part, s);
+        }
         if ((marks & 0x80808080u) || draft >= 0)
           patch_nan<D, kParts>(raw, raw_blk, raw_swz, dst, row, part, draft, poison);
       }
@@ -400,6 +407,8 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
       mbar_arrive(g.empty + 8u * rs);
       mbar_arrive(g.out_full + 8u * stage);
     }
+    if (++rs == RAW) rs = 0, raw_phase ^= 1;
+    if (++stage == STAGES) stage = 0, out_phase ^= 1;
   }
 }
 
@@ -410,9 +419,7 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
   using L = Layout<D, BN, STAGES, RAW, Q8>;
   constexpr int kThreads = L::kThreads;
   constexpr int H = L::kHalves, CH = BN / H;  // scores of a tile that a softmax thread takes
-  // P (16-bit pairs) takes BN / 2 columns of S: the last ones, so that a half's weights only ever go
-  // over scores of the second half, which both halves' votes show to be in registers
-  constexpr int kPOff = BN / 2;
+  constexpr int CR = CH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -621,10 +628,11 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
         if (!(ok = mbar_wait(bar_v(stage), (jj / STAGES) & 1, p.status))) break;
         tc_fence_after();
         const uint64_t vd = sdesc_add(v_desc, stage * L::kKVBytes);
-        const uint32_t a_p = tm_s0 + buf * BN + kPOff;
+        const uint32_t a_p = tm_s0 + buf * BN;
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          mma_ts(tm_o, a_p + kk * 8, sdesc_add(vd, kk * (2 * kRG)), idesc_o,
+          // P (16-bit pairs) of each half lies over the first columns of its own scores
+          mma_ts(tm_o, a_p + kk * 8 + (kk / (CH / 16)) * (CH / 2), sdesc_add(vd, kk * (2 * kRG)), idesc_o,
                  (jj > 0 || kk > 0) ? 1u : 0u);
         tc_commit(bar_pv(buf));
         tc_commit(bar_ve(stage));
@@ -664,7 +672,7 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
     if constexpr (Q8) {
       const Rings k{s_base + L::kRawKOff, bar_rk(0), bar_rke(0), sK, bar_k(0), bar_ke(0)};
       const Rings v{s_base + L::kRawVOff, bar_rv(0), bar_rve(0), sV, bar_v(0), bar_ve(0)};
-      convert_tiles<D, BN, STAGES, RAW>(p, f16, k, v, poison, b, hk, t_begin, n, Lkv, ctx);
+      convert_tiles<D, BN, STAGES, RAW, BF16>(p, f16, k, v, poison, b, hk, t_begin, n, Lkv, ctx);
     }
   } else if ((warp < 4 || warp >= L::kHalfWarp) && warp % 4 < live_warps) {
     // --------------------------- softmax + epilogue -------------------------------------
@@ -713,26 +721,32 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
       if (Q8 && BF16 && f16 && jj == 0) to_log2 *= q_factor;  // written before S_0 could be issued
       const float a = pre ? 1.f : to_log2;
       const int key0 = (t_begin + jj) * BN;
-      uint32_t raw[CH];
-      float row_max = -INFINITY;
-      if (ok) {
-        tc_fence_after();
-        prefill::load_s<CH>(t_s + half * CH, raw);
+      auto read = [&](int c0, uint32_t (&raw)[CR]) {
+        prefill::load_s<CR>(t_s + half * CH + c0, raw);
         if (pre) {
 #pragma unroll
-          for (int c = 0; c < CH; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * to_log2);
+          for (int c = 0; c < CR; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * to_log2);
         }
         if (key0 + BN > ctx) {
 #pragma unroll
-          for (int w = 0; w < CH / 32; ++w) {
-            const uint32_t bits = row_bits(row, key0 + half * CH + 32 * w - ctx);
+          for (int w = 0; w < CR / 32; ++w) {
+            const uint32_t bits = row_bits(row, key0 + half * CH + c0 + 32 * w - ctx);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((bits >> c) & 1)) raw[32 * w + c] = 0xff800000u;  // -inf
           }
         }
-        row_max = a * chunk_max(raw);
-        tc_fence_before();  // the loads, before the other half's stores over these columns
+      };
+      uint32_t raw[CR];
+      float row_max = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c0 = 0; c0 < CH; c0 += CR) {
+          read(c0, raw);
+          row_max = fmaxf(row_max, chunk_max(raw));
+        }
+        row_max *= a;
       }
       const bool raise = barrier_any(1, team, ok && row_max > m_run + prefill::kRescaleLog2);
       if (raise) {
@@ -756,16 +770,17 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
         }
       }
       if (!ok) continue;
-      tc_fence_after();
-      {
-        uint32_t pk[CH / 2];
+#pragma unroll 1
+      for (int c0 = 0; c0 < CH; c0 += CR) {
+        if (CR < CH) read(c0, raw);
+        uint32_t pk[CR / 2];
         if constexpr (Q8 && BF16) {
-          if (f16) chunk_weights<CH, false>(raw, a, m_run, l_run, pk);
-          else chunk_weights<CH, true>(raw, a, m_run, l_run, pk);
+          if (f16) chunk_weights<CR, false>(raw, a, m_run, l_run, pk);
+          else chunk_weights<CR, true>(raw, a, m_run, l_run, pk);
         } else {
-          chunk_weights<CH, BF16>(raw, a, m_run, l_run, pk);
+          chunk_weights<CR, BF16>(raw, a, m_run, l_run, pk);
         }
-        prefill::store_p<CH>(t_s + kPOff + half * (CH / 2), pk);
+        prefill::store_p<CR>(t_s + half * CH + c0 / 2, pk);
       }
       tmem_st_wait();
       if (!Q8 && key0 + BN > ctx) {
