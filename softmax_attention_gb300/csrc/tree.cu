@@ -65,7 +65,7 @@ struct Layout {
   static constexpr int kNumBars = 1 + 4 * STAGES + 3 * kNumS + 2 + (Q8 ? 4 * RAW + 1 : 0);
   static constexpr int kPoisonOff = kBarOff + kNumBars * 8 + 16;
   // what two halves of a row exchange (a maximum or a sum each), and the power of two of the row of Q
-  static constexpr int kRowOff = kPoisonOff + (kMaxTree / 32) * 4;
+  static constexpr int kRowOff = (kPoisonOff + (kMaxTree / 32) * 4 + 15) / 16 * 16;
   static constexpr int kBytes = kRowOff + 3 * kRows * 4;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 bytes
   static_assert(D + kNumS * BN <= 512, "tensor memory budget (O and the S/P buffers)");
@@ -458,23 +458,8 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
   const int split = blockIdx.x % p.n_splits;
   const int qt = static_cast<int>(blockIdx.x) / p.n_splits;
   const int hk = blockIdx.y;
-  int b = blockIdx.z;
-  {
-    __shared__ int lpt_seq;
-    if (p.B <= kThreads) {
-      if (threadIdx.x < p.B) {
-        const int li = p.kv_lens[threadIdx.x];
-        int rank = 0;
-        for (int j = 0; j < p.B; ++j) {
-          const int lj = p.kv_lens[j];
-          rank += (lj > li || (lj == li && j < static_cast<int>(threadIdx.x))) ? 1 : 0;
-        }
-        if (rank == static_cast<int>(blockIdx.z)) lpt_seq = threadIdx.x;
-      }
-      __syncthreads();
-      b = lpt_seq;
-    }
-  }
+  static_assert(3 * kRows * 4 >= (kMaxRanked + 4) * 4, "the rows' exchange serves as scratch first");
+  const int b = sequence_of_rank<kThreads>(p, blockIdx.z, reinterpret_cast<int*>(smem + L::kRowOff));
   int Lkv = p.kv_lens[b];
   int n_draft = p.draft_lens ? p.draft_lens[b] : p.T;
   if (Lkv < 0 || static_cast<int64_t>(Lkv) > static_cast<int64_t>(p.max_pages) * p.page_size ||
@@ -944,7 +929,7 @@ TreePlan plan_tree(const fa_tree_args* a) {
   pl.q_per_tile = (a->T + pl.n_qtiles - 1) / pl.n_qtiles;
   pl.n_qtiles = (a->T + pl.q_per_tile - 1) / pl.q_per_tile;
   const int rows = pl.G * a->T;
-  pl.few_rows = a->cache_dtype == FA_E4M3 && tree_rows_takes(rows, a->D);
+  pl.few_rows = a->cache_dtype == FA_E4M3 && tree_rows_takes(rows);
   const int bn = pl.few_rows ? kFewRowsTokens : block_n(a->D);
   const int kv_tiles = (a->max_seq_len + bn - 1) / bn;
   int s = 1;
@@ -954,7 +939,7 @@ TreePlan plan_tree(const fa_tree_args* a) {
     // its CTAs are small and several share an SM: split while the units leave half of them free,
     // down to kFewRowsTokens tokens a part
     const long units = static_cast<long>(a->Hkv) * a->B;
-    const int slots = tree_rows_slots(rows, a->D);
+    const int slots = tree_rows_slots(a->D);
     if (units > 0 && units * 2 <= slots) s = static_cast<int>(slots / units);
   } else if (kv_tiles > 0) {
     // as the prefill plan: split only when the tiles cover less than half the SMs

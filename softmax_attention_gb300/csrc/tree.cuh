@@ -2,6 +2,7 @@
 // over the drafted tokens, and the values of V that are not finite.
 #pragma once
 
+#include <limits.h>
 #include <stdint.h>
 
 #include "cache.cuh"
@@ -127,11 +128,36 @@ __device__ __forceinline__ uint32_t widen2_hi(uint32_t codes) {
   return r;
 }
 
+// The sequence that is `rank`-th in decreasing length (ties by index), so that the last blocks to
+// start are short ones; past kMaxRanked sequences the rank is the sequence.  All threads of the
+// block must call; scratch: kMaxRanked + 4 words of shared memory, 16-byte aligned.
+constexpr int kMaxRanked = 256;
+
+template <int THREADS>
+__device__ __forceinline__ int sequence_of_rank(const TreeParams& p, int rank, int* scratch) {
+  if (p.B > kMaxRanked) return rank;
+  const int rounded = (p.B + 3) / 4 * 4;
+  for (int t = threadIdx.x; t < rounded; t += THREADS) scratch[t] = t < p.B ? p.kv_lens[t] : INT_MIN;
+  __syncthreads();
+  for (int t = threadIdx.x; t < p.B; t += THREADS) {
+    const int mine = scratch[t];
+    int before = 0;
+    for (int j = 0; j < rounded; j += 4) {
+      const int4 l = *reinterpret_cast<const int4*>(scratch + j);
+      before += (l.x > mine || (l.x == mine && j < t)) + (l.y > mine || (l.y == mine && j + 1 < t)) +
+                (l.z > mine || (l.z == mine && j + 2 < t)) + (l.w > mine || (l.w == mine && j + 3 < t));
+    }
+    if (before == rank) scratch[kMaxRanked] = t;
+  }
+  __syncthreads();
+  return scratch[kMaxRanked];
+}
+
 // The kernel for few rows over 8-bit pages (tree_rows.cu): takes a call if tree_rows_takes says
 // so (rows = query heads per kv head times T); tree_rows_slots is the number of its CTAs that
 // the current device holds at once.
-bool tree_rows_takes(int rows, int D);
-int tree_rows_slots(int rows, int D);
+bool tree_rows_takes(int rows);
+int tree_rows_slots(int D);
 cudaError_t launch_tree_rows(const TreeParams& p, int D, bool bf16, cudaStream_t stream);
 
 }  // namespace fa

@@ -1,12 +1,14 @@
 // tree_rows.cu -- tree attention over an 8-bit paged cache for few rows (query heads of a kv head
 // times drafted tokens): the decode step, where the cache's bytes are all the time there is.
 //
-// With 16 or 32 rows the products fit the warp-level matrix instruction (m16n8k16), whose operands
-// are registers: e4m3 codes go from shared memory to registers, are converted there (one
-// instruction a pair) and multiplied, so a cache byte is written to shared memory once by TMA
-// and read once.  The 128-row tile of the tcgen05 kernel would pass each byte through shared
-// memory five times (raw in, out, widened in, out to the MMA) and spend its tensor time on empty
-// rows; there the 8-bit cache is no faster than a 16-bit one.
+// Up to 16 rows fill one tile of the warp-level matrix instruction (m16n8k16), whose operands are
+// registers: e4m3 codes go from shared memory to registers, are converted there (one instruction
+// a pair) and multiplied, so a cache byte is written to shared memory once by TMA and read once.
+// The 128-row tile of the tcgen05 kernel passes each byte through shared memory six times (raw in
+// and out, widened twice its size in and out) and spends its tensor time on empty rows: there
+// the 8-bit cache is read at 3.2 TB/s whatever the rows, here at 5.5 TB/s (57 sequences of 4096
+// tokens, 8 kv heads, D = 128; 0.83 of a copy), bound by the latencies and issue slots of the
+// twelve warps that an SM's registers hold.
 //
 // Each warp runs alone: its own ring of slices (SL tokens of K and of V), its own barriers, its
 // own online softmax; four warps of a CTA take the slices of a (sequence, kv head, part) in turn
@@ -25,11 +27,13 @@
 #include <type_traits>
 
 #include "internal.h"
+#include "prefill_common.cuh"
 #include "tree.cuh"
 
 namespace fa {
 namespace {
 
+constexpr int kTileRows = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kShift = 7.f;       // weights times 2^7
@@ -37,22 +41,22 @@ constexpr float kStale = 8.f;       // O is rescaled when a maximum grows by mor
 constexpr float kUnset = -3e38f;    // a maximum before the first score
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int D, int MT>
+template <int D>
 struct RowsLayout {
-  static constexpr int kSlice = D == 256 ? 16 : 32;              // tokens a step
-  static constexpr int kStage = kSlice * D;                      // bytes of K (or V) a slice
-  static constexpr int kCtas = D == 256 || MT == 2 ? 2 : 3;      // CTAs an SM
+  static constexpr int kSlice = D == 256 ? 16 : 32;  // tokens a step
+  static constexpr int kStage = kSlice * D;          // bytes of K (or V) a slice
+  static constexpr int kCtas = D == 256 ? 2 : 3;     // CTAs an SM
   static constexpr int kStages = D == 64 ? 4 : kCtas == 2 ? 3 : 2;
-  static constexpr int kRing = kStages * 2 * kStage;             // a warp's ring
+  static constexpr int kRing = kStages * 2 * kStage;  // a warp's ring
   static constexpr int kQOff = kWarps * kRing;
-  static constexpr int kQBytes = MT * (D / 16) * 512;            // fp16 fragments of q
+  static constexpr int kQBytes = (D / 16) * 512;  // fp16 fragments of q
   static constexpr int kBarOff = kQOff + kQBytes;
   static constexpr int kStatOff = kBarOff + kWarps * kStages * 2 * 8;
-  static constexpr int kPoisonOff = kStatOff + kWarps * 16 * MT * 3 * 4;
+  static constexpr int kPoisonOff = kStatOff + kWarps * kTileRows * 3 * 4;
   static constexpr int kBytes = kPoisonOff + kMaxTree / 32 * 4 + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(16 * MT * D * 4 <= kRing, "a warp's O goes into its ring at the end");
-  static_assert(kCtas * (kAlloc + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kTileRows * D * 4 <= kRing, "a warp's O goes into its ring at the end");
+  static_assert(kCtas * (kAlloc + 1024 + (kMaxRanked + 4 + kTileRows) * 4) <= 228 * 1024, "shared memory of an SM");
 };
 
 // C (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  With g = lane / 4, t = lane % 4:
@@ -86,11 +90,11 @@ __device__ __forceinline__ void load_q4(const void* q, int64_t at, float (&x)[4]
   }
 }
 
-template <int D, int MT, bool BF16, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
+template <int D, bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
     tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const TreeParams p) {
-  using L = RowsLayout<D, MT>;
+  using L = RowsLayout<D>;
   constexpr int SL = L::kSlice, NS = L::kStages;
   constexpr int kSteps = D / 16;      // k steps of S, and 16-column chunks of V
   constexpr int kTiles = SL / 8;      // 8-token tiles of S
@@ -107,23 +111,8 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   // ---- work item: part x kv head x sequence, longest sequences first ----
   const int split = blockIdx.x % p.n_splits;
   const int hk = blockIdx.y;
-  int b = blockIdx.z;
-  {
-    __shared__ int lpt_seq;
-    if (p.B <= kThreads) {
-      if (threadIdx.x < p.B) {
-        const int li = p.kv_lens[threadIdx.x];
-        int rank = 0;
-        for (int j = 0; j < p.B; ++j) {
-          const int lj = p.kv_lens[j];
-          rank += (lj > li || (lj == li && j < static_cast<int>(threadIdx.x))) ? 1 : 0;
-        }
-        if (rank == static_cast<int>(blockIdx.z)) lpt_seq = threadIdx.x;
-      }
-      __syncthreads();
-      b = lpt_seq;
-    }
-  }
+  __shared__ __align__(16) int rank_scratch[kMaxRanked + 4];
+  const int b = sequence_of_rank<kThreads>(p, blockIdx.z, rank_scratch);
   int Lkv = p.kv_lens[b];
   int n_draft = p.draft_lens ? p.draft_lens[b] : p.T;
   if (Lkv < 0 || static_cast<int64_t>(Lkv) > static_cast<int64_t>(p.max_pages) * p.page_size ||
@@ -198,8 +187,8 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   // A lane of four holds columns [kLaneBytes t, kLaneBytes (t + 1)) of each 128-column block of a
   // token; k step kk takes four of them, in both operands (the order of k does not matter).
   const int rows = p.G * p.T;
-  __shared__ float q_scale[16 * MT];  // scale_log2 times the row's power of two
-  for (int r = warp * 4 + lane / 8; r < 16 * MT; r += kWarps * 4) {
+  __shared__ float q_scale[kTileRows];  // scale_log2 times the row's power of two
+  for (int r = warp * 4 + lane / 8; r < kTileRows; r += kWarps * 4) {
     // eight lanes a row: lane c takes columns 4c, 4c + 32, ...
     const int c = lane % 8;
     const bool have = r < rows;
@@ -225,39 +214,35 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
       const int col = 4 * c + 32 * u, blk = col / kIn, in = col % kIn;
       const int t = in / kLaneBytes, kk = blk * (kIn / 16) + (in % kLaneBytes) / 4;
       // fragment words of lane (r % 8) * 4 + t: a0/a2 for rows 0-7 of the tile, a1/a3 for 8-15
-      uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::kQOff + ((r / 16) * kSteps + kk) * 512 +
-                                                  ((r % 8) * 4 + t) * 16) + (r % 16) / 8;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::kQOff + kk * 512 +
+                                                  ((r % 8) * 4 + t) * 16) + r / 8;
       dst[0] = pack_f16x2(x[u][0] * f, x[u][1] * f);
       dst[2] = pack_f16x2(x[u][2] * f, x[u][3] * f);
     }
   }
   __syncthreads();
 
-  // ---- this lane's rows: g and g + 8 of each 16-row tile ----
-  float a_row[MT][2], mx[MT][2], mo[MT][2], l[MT][2];
-  TreeRow row[MT][2];
+  // ---- this lane's rows: g and g + 8 ----
+  float a_row[2], mx[2], mo[2];
+  float2 l[2];  // two partial sums a row and lane
+  TreeRow row[2];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = 16 * m + 8 * h + g, i = r < rows ? r % p.T : 0;
-      const bool active = r < rows && i < n_draft;
-      a_row[m][h] = q_scale[r];
-      mx[m][h] = mo[m][h] = kUnset;
-      l[m][h] = 0.f;
-      row[m][h].i = i;
-      row[m][h].n = active ? n_draft : 0;
-      row[m][h].words = p.mask && active
-          ? p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words : nullptr;
-    }
+  for (int h = 0; h < 2; ++h) {
+    const int r = 8 * h + g, i = r < rows ? r % p.T : 0;
+    const bool active = r < rows && i < n_draft;
+    a_row[h] = q_scale[r];
+    mx[h] = mo[h] = kUnset;
+    l[h] = make_float2(0.f, 0.f);
+    row[h].i = i;
+    row[h].n = active ? n_draft : 0;
+    row[h].words = p.mask && active
+        ? p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words : nullptr;
   }
-  float o[MT][2 * kSteps][4];
+  float o[2 * kSteps][4];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+  for (int c = 0; c < 2 * kSteps; ++c)
 #pragma unroll
-    for (int c = 0; c < 2 * kSteps; ++c)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[m][c][e] = 0.f;
+    for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
 
   // shared-memory offsets inside a stage (a box holds [128-column block][token][128 bytes], 16-byte
   // chunks swizzled by the token)
@@ -270,18 +255,17 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   const uint32_t v_swz = D < 128 ? (v_tok >> 1) & 3 : v_tok & 7;
 
   // ---- one slice ----
-  auto slice = [&](auto tail_c, int k, uint32_t bytes, int next_id) -> bool {
+  // scales: of token `lane`, 2^ek in bf16 above ev in bf16 (both exact)
+  auto slice = [&](auto tail_c, int k, uint32_t scales, int next_id) -> bool {
     constexpr bool TAIL = decltype(tail_c)::value;
     const int st = k % NS, key0 = (s_begin + k * kWarps) * SL;
     if (!__all_sync(0xffffffffu, mbar_wait(bar_k(st), (k / NS) & 1, p.status))) return false;
     // S = Q K^T, a 128-column block at a time
-    float s[MT][kTiles][4];
+    float s[kTiles][4];
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int j = 0; j < kTiles; ++j)
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[m][j][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
 #pragma unroll
     for (int blk = 0; blk < D / kIn; ++blk) {
       uint32_t w[kTiles][kIn / 16];
@@ -303,101 +287,98 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
       }
 #pragma unroll
       for (int kk = 0; kk < kIn / 16; ++kk) {
-        uint4 a[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          a[m] = lds128(s_base + L::kQOff + (m * kSteps + blk * (kIn / 16) + kk) * 512 + lane * 16);
+        uint4 a;
+          a = lds128(s_base + L::kQOff + (blk * (kIn / 16) + kk) * 512 + lane * 16);
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
           const uint32_t b0 = widen2(w[j][kk]), b1 = widen2_hi(w[j][kk]);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) mma16816(s[m][j], a[m], b0, b1);
+          mma16816(s[j], a, b0, b1);
         }
       }
     }
-    // the scales of this lane's tokens 8j + 2t, + 1
-    float kf[kTiles][2], ev[kTiles][2];
+    // the scales of this lane's tokens 8j + 2t, + 1: 2^ek as it multiplies, ev as it is added
+    float2 kf[kTiles], ev[kTiles];
 #pragma unroll
     for (int j = 0; j < kTiles; ++j) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t by = __shfl_sync(0xffffffffu, bytes, 8 * j + 2 * t4 + e);
-        kf[j][e] = __uint_as_float((by & 0xffu) << 23);
-        ev[j][e] = static_cast<float>(static_cast<int>(by >> 8) - 127);
-      }
+      const uint32_t w0 = __shfl_sync(0xffffffffu, scales, 8 * j + 2 * t4);
+      const uint32_t w1 = __shfl_sync(0xffffffffu, scales, 8 * j + 2 * t4 + 1);
+      kf[j] = make_float2(__uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 & 0xffff0000u));
+      ev[j] = make_float2(__uint_as_float(w0 << 16), __uint_as_float(w1 << 16));
     }
     // scores in log2 units; hidden tokens get -inf
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int h = 0; h < 2; ++h) {
+      uint32_t bits = ~0u;
+      if constexpr (TAIL) bits = row_bits(row[h], key0 - ctx) >> (2 * t4);
+      const float2 a = make_float2(a_row[h], a_row[h]);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t bits = ~0u;
-        if constexpr (TAIL) bits = row_bits(row[m][h], key0 - ctx);
-#pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float& x = s[m][j][2 * h + e];
-            x = x * a_row[m][h] * kf[j][e];
-            if (TAIL && !((bits >> (8 * j + 2 * t4 + e)) & 1)) x = -INFINITY;
-          }
-        }
+      for (int j = 0; j < kTiles; ++j) {
+        float2 x = __fmul2_rn(__fmul2_rn(make_float2(s[j][2 * h], s[j][2 * h + 1]), a), kf[j]);
+        if (TAIL && !((bits >> (8 * j)) & 1)) x.x = -INFINITY;
+        if (TAIL && !((bits >> (8 * j + 1)) & 1)) x.y = -INFINITY;
+        s[j][2 * h] = x.x;
+        s[j][2 * h + 1] = x.y;
       }
     }
-    // how far the scores are above the running maxima; mostly not far enough to move them
-    float over = -INFINITY;
+    // exponents of the sums' terms (y1 = x - mx) and of the weights (y2 = x + ev - mo + kShift)
+    float2 y1[2][kTiles], y2[2][kTiles];
+    auto exponents = [&]() {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int h = 0; h < 2; ++h) {
+        const float down = -mx[h], up = kShift - mo[h];
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+          const float2 x = make_float2(s[j][2 * h], s[j][2 * h + 1]);
+          y1[h][j] = __fadd2_rn(x, make_float2(down, down));
+          y2[h][j] = __fadd2_rn(x, __fadd2_rn(ev[j], make_float2(up, up)));
+        }
+      }
+    };
+    exponents();
+    // how far the scores are above the running maxima; mostly not far enough to move them
+    float over1 = -INFINITY, over2 = -INFINITY;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = s[m][j][2 * h + e];
-            over = fmaxf(over, fmaxf(x - mx[m][h], x + ev[j][e] - mo[m][h]));
-          }
-    if (__any_sync(0xffffffffu, over > kStale)) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float x1 = mx[m][h], x2 = mo[m][h];
-#pragma unroll
-          for (int j = 0; j < kTiles; ++j)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              x1 = fmaxf(x1, s[m][j][2 * h + e]);
-              x2 = fmaxf(x2, s[m][j][2 * h + e] + ev[j][e]);
-            }
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-          x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 1));
-          x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-          x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 2));
-          l[m][h] *= exp2_approx(mx[m][h] - x1);
-          const float alpha = exp2_approx(mo[m][h] - x2);
-          mx[m][h] = x1;
-          mo[m][h] = x2;
-#pragma unroll
-          for (int c = 0; c < 2 * kSteps; ++c) {
-            o[m][c][2 * h] *= alpha;
-            o[m][c][2 * h + 1] *= alpha;
-          }
+        for (int j = 0; j < kTiles; ++j) {
+          over1 = prefill::fmax3(over1, y1[h][j].x, y1[h][j].y);
+          over2 = prefill::fmax3(over2, y2[h][j].x, y2[h][j].y);
         }
-      }
-    }
-    uint32_t pk[MT][kTiles][2];  // weights: rows g, g + 8
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    if (__any_sync(0xffffffffu, over1 > kStale || over2 > kStale + kShift)) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const float up = kShift - mo[m][h];
+        float x1 = mx[h], x2 = mo[h];
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
-          const float x0 = s[m][j][2 * h], x1 = s[m][j][2 * h + 1];
-          l[m][h] += exp2_approx(x0 - mx[m][h]) + exp2_approx(x1 - mx[m][h]);
-          pk[m][j][h] = pack_f16x2(exp2_approx(x0 + (ev[j][0] + up)), exp2_approx(x1 + (ev[j][1] + up)));
+          x1 = prefill::fmax3(x1, s[j][2 * h], s[j][2 * h + 1]);
+          x2 = prefill::fmax3(x2, s[j][2 * h] + ev[j].x, s[j][2 * h + 1] + ev[j].y);
         }
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 2));
+        const float alpha1 = exp2_approx(mx[h] - x1), alpha2 = exp2_approx(mo[h] - x2);
+        l[h].x *= alpha1;
+        l[h].y *= alpha1;
+        mx[h] = x1;
+        mo[h] = x2;
+#pragma unroll
+        for (int c = 0; c < 2 * kSteps; ++c) {
+          o[c][2 * h] *= alpha2;
+          o[c][2 * h + 1] *= alpha2;
+        }
+      }
+      exponents();
+    }
+    uint32_t pk[kTiles][2];  // weights: rows g, g + 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < kTiles; ++j) {
+        const float2 e1 = y1[h][j], e2 = y2[h][j];
+        l[h] = __fadd2_rn(l[h], make_float2(exp2_approx(e1.x), exp2_approx(e1.y)));
+        pk[j][h] = pack_f16x2(exp2_approx(e2.x), exp2_approx(e2.y));
       }
     }
     // O += P V: 16 tokens x 32 columns of V codes a load, transposed so that a register holds two
@@ -438,12 +419,9 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
         for (int cc = 0; cc < 2; ++cc) {
           const uint32_t u0 = __byte_perm(r[2 * cc], 0, 0x3120), u1 = __byte_perm(r[2 * cc + 1], 0, 0x3120);
           const uint32_t e0 = widen2(u0), e1 = widen2(u1), d0 = widen2_hi(u0), d1 = widen2_hi(u1);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            const uint4 a = make_uint4(pk[m][2 * kt][0], pk[m][2 * kt][1], pk[m][2 * kt + 1][0], pk[m][2 * kt + 1][1]);
-            mma16816(o[m][2 * (c + cc)], a, e0, e1);
-            mma16816(o[m][2 * (c + cc) + 1], a, d0, d1);
-          }
+          const uint4 a = make_uint4(pk[2 * kt][0], pk[2 * kt][1], pk[2 * kt + 1][0], pk[2 * kt + 1][1]);
+          mma16816(o[2 * (c + cc)], a, e0, e1);
+          mma16816(o[2 * (c + cc) + 1], a, d0, d1);
         }
       }
     }
@@ -466,15 +444,16 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   load_bytes(0, ids[0], kb, vb);
   for (; ok && k < n; ++k) {
     // ids[j] is slice k + j's here, the last one not yet checked
-    const uint32_t bytes = kb | (vb << 8);
+    const float ev = static_cast<float>(static_cast<int>(vb) - 127);
+    const uint32_t scales = (kb << 23) | (__float_as_uint(ev) >> 16);
     load_bytes(k + 1, ids[1], kb, vb);
     const int next_id = checked(ids[NS]);
 #pragma unroll
     for (int j = 0; j < NS - 1; ++j) ids[j] = ids[j + 1];
     ids[NS - 1] = next_id;
     ids[NS] = token_page(k + NS + 1);
-    if ((s_begin + k * kWarps) * SL + SL > ctx) ok = slice(std::true_type{}, k, bytes, next_id);
-    else ok = slice(std::false_type{}, k, bytes, next_id);
+    if ((s_begin + k * kWarps) * SL + SL > ctx) ok = slice(std::true_type{}, k, scales, next_id);
+    else ok = slice(std::false_type{}, k, scales, next_id);
   }
   if (!ok) {
     // a wait ran out: let the copies in flight land (each stage's last one) before the CTA ends
@@ -494,26 +473,23 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   float* stat = reinterpret_cast<float*>(smem + L::kStatOff);  // [warp][row][mx, mo, l]
   float* part = reinterpret_cast<float*>(smem + warp * L::kRing);
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float sum = l[m][h];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int r = 16 * m + 8 * h + g;
-      if (t4 == 0) {
-        float* at = stat + (warp * 16 * MT + r) * 3;
-        at[0] = mx[m][h];
-        at[1] = mo[m][h];
-        at[2] = sum;
-      }
-      // columns 16c + 4t .. + 3 of row r, chunks of four swizzled by the row
-#pragma unroll
-      for (int c = 0; c < kSteps; ++c)
-        *reinterpret_cast<float4*>(part + r * D + (((4 * c + t4) ^ (r & 7)) * 4)) =
-            make_float4(o[m][2 * c][2 * h], o[m][2 * c + 1][2 * h], o[m][2 * c][2 * h + 1],
-                        o[m][2 * c + 1][2 * h + 1]);
+  for (int h = 0; h < 2; ++h) {
+    float sum = l[h].x + l[h].y;
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    const int r = 8 * h + g;
+    if (t4 == 0) {
+      float* at = stat + (warp * kTileRows + r) * 3;
+      at[0] = mx[h];
+      at[1] = mo[h];
+      at[2] = sum;
     }
+    // columns 16c + 4t .. + 3 of row r, chunks of four swizzled by the row
+#pragma unroll
+    for (int c = 0; c < kSteps; ++c)
+      *reinterpret_cast<float4*>(part + r * D + (((4 * c + t4) ^ (r & 7)) * 4)) =
+          make_float4(o[2 * c][2 * h], o[2 * c + 1][2 * h], o[2 * c][2 * h + 1],
+                      o[2 * c + 1][2 * h + 1]);
   }
   __syncthreads();
   if (failed) return;
@@ -525,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
     float M = kUnset, Mo = kUnset;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float* at = stat + (w * 16 * MT + r) * 3;
+      const float* at = stat + (w * kTileRows + r) * 3;
       M = fmaxf(M, at[0]);
       Mo = fmaxf(Mo, at[1]);
     }
@@ -533,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float* at = stat + (w * 16 * MT + r) * 3;
+      const float* at = stat + (w * kTileRows + r) * 3;
       const float fo = exp2_approx(at[1] - Mo);
       sum += at[2] * exp2_approx(at[0] - M);
       const float4 x = *reinterpret_cast<const float4*>(
@@ -583,9 +559,9 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, MT>::kCtas)
   }
 }
 
-template <int D, int MT, bool BF16>
+template <int D, bool BF16>
 cudaError_t launch_impl(const TreeParams& p, cudaStream_t st) {
-  using L = RowsLayout<D, MT>;
+  using L = RowsLayout<D>;
   CUtensorMap tk, tv;
   const uint64_t ps = static_cast<uint64_t>(p.page_size), pages = static_cast<uint64_t>(p.num_pages) * p.Hkv;
   // a page of one head: page_size rows of D bytes as (column, row, block of 128 columns)
@@ -597,7 +573,7 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t st) {
   if (!encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_pages, dims, str, box, swz) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_pages, dims, str, box, swz))
     return cudaErrorInvalidValue;
-  auto kern = p.n_splits > 1 ? tree_rows_kernel<D, MT, BF16, true> : tree_rows_kernel<D, MT, BF16, false>;
+  auto kern = p.n_splits > 1 ? tree_rows_kernel<D, BF16, true> : tree_rows_kernel<D, BF16, false>;
   cudaError_t e = ensure_smem_limit(kern, L::kAlloc);
   if (e != cudaSuccess) return e;
   kern<<<dim3(p.n_splits, p.Hkv, p.B), kThreads, L::kAlloc, st>>>(tk, tv, p);
@@ -606,21 +582,22 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t st) {
 
 template <bool BF16>
 cudaError_t launch_d(const TreeParams& p, int D, cudaStream_t st) {
-  const bool two = p.G * p.T > 16;
   switch (D) {
-    case 64: return two ? launch_impl<64, 2, BF16>(p, st) : launch_impl<64, 1, BF16>(p, st);
-    case 128: return two ? launch_impl<128, 2, BF16>(p, st) : launch_impl<128, 1, BF16>(p, st);
-    default: return launch_impl<256, 1, BF16>(p, st);
+    case 64: return launch_impl<64, BF16>(p, st);
+    case 128: return launch_impl<128, BF16>(p, st);
+    default: return launch_impl<256, BF16>(p, st);
   }
 }
 
 }  // namespace
 
-bool tree_rows_takes(int rows, int D) { return rows <= (D == 256 ? 16 : 32); }
+// One 16-row tile.  With two (17 to 32 rows, D = 128) a warp's registers spill and the loop is bound by
+// its arithmetic: 38 sequences of 4096 tokens take 105 to 137 us, the 128-row kernel 100 us.
+bool tree_rows_takes(int rows) { return rows <= kTileRows; }
 
-int tree_rows_slots(int rows, int D) {
+int tree_rows_slots(int D) {
   const int sms = num_sms() > 0 ? num_sms() : 152;
-  return sms * (D == 256 || rows > 16 ? 2 : 3);
+  return sms * (D == 256 ? 2 : 3);
 }
 
 cudaError_t launch_tree_rows(const TreeParams& p, int D, bool bf16, cudaStream_t stream) {
