@@ -65,7 +65,7 @@ struct Layout {
   static constexpr int kNumBars = 1 + 4 * STAGES + 3 * kNumS + 2 + (Q8 ? 4 * RAW + 1 : 0);
   static constexpr int kPoisonOff = kBarOff + kNumBars * 8 + 16;
   // what two halves of a row exchange (a maximum or a sum each), and the power of two of the row of Q
-  static constexpr int kRowOff = (kPoisonOff + (kMaxTree / 32) * 4 + 15) / 16 * 16;
+  static constexpr int kRowOff = kPoisonOff + (kMaxTree / 32) * 4;
   static constexpr int kBytes = kRowOff + 3 * kRows * 4;
   static constexpr int kAlloc = kBytes + 1024;  // room to align the base to 1024 bytes
   static_assert(D + kNumS * BN <= 512, "tensor memory budget (O and the S/P buffers)");
@@ -458,8 +458,7 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
   const int split = blockIdx.x % p.n_splits;
   const int qt = static_cast<int>(blockIdx.x) / p.n_splits;
   const int hk = blockIdx.y;
-  static_assert(3 * kRows * 4 >= (kMaxRanked + 4) * 4, "the rows' exchange serves as scratch first");
-  const int b = sequence_of_rank<kThreads>(p, blockIdx.z, reinterpret_cast<int*>(smem + L::kRowOff));
+  const int b = sequence_of_rank<kThreads>(p, blockIdx.z);
   int Lkv = p.kv_lens[b];
   int n_draft = p.draft_lens ? p.draft_lens[b] : p.T;
   if (Lkv < 0 || static_cast<int64_t>(Lkv) > static_cast<int64_t>(p.max_pages) * p.page_size ||

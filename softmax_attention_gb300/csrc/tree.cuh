@@ -2,7 +2,6 @@
 // over the drafted tokens, and the values of V that are not finite.
 #pragma once
 
-#include <limits.h>
 #include <stdint.h>
 
 #include "cache.cuh"
@@ -129,28 +128,23 @@ __device__ __forceinline__ uint32_t widen2_hi(uint32_t codes) {
 }
 
 // The sequence that is `rank`-th in decreasing length (ties by index), so that the last blocks to
-// start are short ones; past kMaxRanked sequences the rank is the sequence.  All threads of the
-// block must call; scratch: kMaxRanked + 4 words of shared memory, 16-byte aligned.
-constexpr int kMaxRanked = 256;
-
+// start are short ones; past THREADS sequences the rank is the sequence.  All threads of the
+// block must call.
 template <int THREADS>
-__device__ __forceinline__ int sequence_of_rank(const TreeParams& p, int rank, int* scratch) {
-  if (p.B > kMaxRanked) return rank;
-  const int rounded = (p.B + 3) / 4 * 4;
-  for (int t = threadIdx.x; t < rounded; t += THREADS) scratch[t] = t < p.B ? p.kv_lens[t] : INT_MIN;
-  __syncthreads();
-  for (int t = threadIdx.x; t < p.B; t += THREADS) {
-    const int mine = scratch[t];
+__device__ __forceinline__ int sequence_of_rank(const TreeParams& p, int rank) {
+  __shared__ int found;
+  if (p.B > THREADS) return rank;
+  if (threadIdx.x < p.B) {
+    const int mine = p.kv_lens[threadIdx.x];
     int before = 0;
-    for (int j = 0; j < rounded; j += 4) {
-      const int4 l = *reinterpret_cast<const int4*>(scratch + j);
-      before += (l.x > mine || (l.x == mine && j < t)) + (l.y > mine || (l.y == mine && j + 1 < t)) +
-                (l.z > mine || (l.z == mine && j + 2 < t)) + (l.w > mine || (l.w == mine && j + 3 < t));
+    for (int j = 0; j < p.B; ++j) {
+      const int other = p.kv_lens[j];
+      before += (other > mine || (other == mine && j < static_cast<int>(threadIdx.x))) ? 1 : 0;
     }
-    if (before == rank) scratch[kMaxRanked] = t;
+    if (before == rank) found = threadIdx.x;
   }
   __syncthreads();
-  return scratch[kMaxRanked];
+  return found;
 }
 
 // The kernel for few rows over 8-bit pages (tree_rows.cu): takes a call if tree_rows_takes says

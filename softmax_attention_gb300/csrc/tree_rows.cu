@@ -56,7 +56,7 @@ struct RowsLayout {
   static constexpr int kBytes = kPoisonOff + kMaxTree / 32 * 4 + 16;
   static constexpr int kAlloc = kBytes + 1024;
   static_assert(kTileRows * D * 4 <= kRing, "a warp's O goes into its ring at the end");
-  static_assert(kCtas * (kAlloc + 1024 + (kMaxRanked + 4 + kTileRows) * 4) <= 228 * 1024, "shared memory of an SM");
+  static_assert(kCtas * (kAlloc + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // C (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  With g = lane / 4, t = lane % 4:
@@ -111,8 +111,7 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
   // ---- work item: part x kv head x sequence, longest sequences first ----
   const int split = blockIdx.x % p.n_splits;
   const int hk = blockIdx.y;
-  __shared__ __align__(16) int rank_scratch[kMaxRanked + 4];
-  const int b = sequence_of_rank<kThreads>(p, blockIdx.z, rank_scratch);
+  const int b = sequence_of_rank<kThreads>(p, blockIdx.z);
   int Lkv = p.kv_lens[b];
   int n_draft = p.draft_lens ? p.draft_lens[b] : p.T;
   if (Lkv < 0 || static_cast<int64_t>(Lkv) > static_cast<int64_t>(p.max_pages) * p.page_size ||
