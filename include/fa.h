@@ -391,6 +391,31 @@ typedef struct fa_rotary_args {
 
 int fa_rotary(const fa_rotary_args* args, void* stream);
 
+/* Host: the table of fa_rotary for a model's rotary settings.  inv_freq[i] = base^(-2i/rot_dim),
+ * i < rot_dim / 2, then scaled for contexts `factor` times longer than the training length
+ * original_len:
+ *   FA_ROTARY_PLAIN     as they are (factor and original_len are not read)
+ *   FA_ROTARY_LINEAR    inv_freq / factor (position interpolation)
+ *   FA_ROTARY_BASE      base * factor^(rot_dim / (rot_dim - 2)) in place of base: the longest
+ *                       wavelength is stretched by factor, the shortest kept
+ *   FA_ROTARY_BY_PARTS  YaRN (Peng, Quesnelle, Fan, Shippole, 2023): a pair that turns r =
+ *                       original_len * inv_freq / 2 pi times over the training length keeps its
+ *                       frequency if r >= fast, is interpolated if r <= slow, and is blended
+ *                       linearly in r between; amplitude 0.1 ln(factor) + 1
+ * *amplitude is 1 otherwise.  inv_freq and amplitude are host pointers.  Returns FA_OK or
+ * FA_ERR_INVALID_ARG (rot_dim odd or < 2, base <= 1, factor < 1, original_len <= 0, slow < 0,
+ * fast <= slow, an unknown scaling; FA_ROTARY_BASE needs rot_dim > 2). */
+typedef enum fa_rotary_scaling {
+  FA_ROTARY_PLAIN = 0,
+  FA_ROTARY_LINEAR = 1,
+  FA_ROTARY_BASE = 2,
+  FA_ROTARY_BY_PARTS = 3
+} fa_rotary_scaling;
+
+int fa_rotary_frequencies(int rot_dim, double base, fa_rotary_scaling scaling, double factor,
+                          double original_len, double fast, double slow, double* inv_freq,
+                          float* amplitude);
+
 /*
  * Writes a step's keys and values into a paged cache (the layout of fa_decode_paged).
  *   k, v [B, Hkv, T, D] in dtype, strides as in fa_rotary;
@@ -469,8 +494,8 @@ int fa_cache_gather(const fa_cache_gather_args* args, void* stream);
  *     last dimension contiguous) positive multiples of 16 bytes
  *   k_pages, v_pages [num_pages, Hkv, page_size, D] in cache_dtype: dtype, or FA_E4M3 with the
  *     scales [num_pages, Hkv, page_size] that fa_cache_append writes (a value is e4m3 *
- *     2^(byte - 127), byte <= 254, held in dtype: exact in bf16; in fp16 rounded to it, so
- *     infinite beyond 65504)
+ *     2^(byte - 127), bytes 1 to 254; with bf16 queries exact; with fp16 queries a value
+ *     beyond 65504 may become infinite and one below 2^-14 may be rounded to fp16)
  *   page_table [B, max_pages] int32; seq_lens [B] int32, the drafted tokens included, each at
  *     most max_seq_len (which sizes the KV split); draft_lens [B] int32 or NULL (= T each)
  *   tree_mask [mask_batches, T, ceil(T / 64)] 64-bit words, mask_batches 1 or B; NULL = a
@@ -510,6 +535,11 @@ typedef struct fa_tree_args {
 } fa_tree_args;
 
 int fa_tree_decode_paged(const fa_tree_args* args, void* stream);
+
+/* Host: the mask words of a tree given by each token's parent: parents[i] in [0, i) is the
+ * drafted token before token i, -1 the context; every token sees its ancestors and itself.
+ * words [T, ceil(T / 64)], T <= 256; both host pointers. */
+int fa_tree_mask(const int32_t* parents, int T, uint64_t* words);
 
 /* Workspace bytes of a call with these sizes on the current device (pointers are not read). */
 size_t fa_tree_workspace_size(const fa_tree_args* args);

@@ -10,9 +10,11 @@ Entry points (same names as the C ABI):
     fa_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len, scale)
     mla_decode_paged(q_nope, q_pe, ckv, kpe, page_table, seq_lens, max_seq_len, scale)
     fa_merge_states(o_parts, lse_parts, n_splits=None, out_dtype=torch.bfloat16)
+    rotary_frequencies(rot_dim, base, scaling, factor, ...)  a table for the next two, on the host
     fa_rotary(q, k, positions, inv_freq, ...)                rotary positions (and their gradient)
     fa_cache_append(k, v, k_pages, v_pages, page_table, seq_lens, ...)   16-bit or e4m3 pages
     fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len, ...)
+    tree_mask(parents)                                       a mask for the next one, on the host
     fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len, tree_mask=...)
     fa_get_device_status()
 """
@@ -46,8 +48,8 @@ EXPORTS = (
     "mla_decode_chunk_tokens", "mla_decode_paged_states", "mla_decode_paged_ex", "fa_merge_states",
     "fa_get_device_status", "fa_selftest_wait_timeout", "fa_last_error", "fa_version",
     "gated_delta_prefill", "gated_delta_workspace_size",
-    "fa_rotary", "fa_cache_append", "fa_cache_gather",
-    "fa_tree_decode_paged", "fa_tree_workspace_size",
+    "fa_rotary", "fa_rotary_frequencies", "fa_cache_append", "fa_cache_gather",
+    "fa_tree_decode_paged", "fa_tree_workspace_size", "fa_tree_mask",
 )
 
 
@@ -182,6 +184,7 @@ class TreeArgs(ctypes.Structure):
 _lock = threading.Lock()
 _lib = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_d = ctypes.c_double
 
 
 def load_library(path: str | None = None):
@@ -250,6 +253,10 @@ def load_library(path: str | None = None):
         lib.fa_cache_append.argtypes = [_vp, _vp]
         lib.fa_cache_gather.restype = _i
         lib.fa_cache_gather.argtypes = [_vp, _vp]
+        lib.fa_rotary_frequencies.restype = _i
+        lib.fa_rotary_frequencies.argtypes = [_i, _d, _i, _d, _d, _d, _d, _vp, _vp]
+        lib.fa_tree_mask.restype = _i
+        lib.fa_tree_mask.argtypes = [_vp, _i, _vp]
         lib.fa_tree_decode_paged.restype = _i
         lib.fa_tree_decode_paged.argtypes = [_vp, _vp]
         lib.fa_tree_workspace_size.restype = _sz
@@ -760,6 +767,38 @@ def _shape(name, t, *want):
 
 def _addr(t):
     return 0 if t is None else t.data_ptr()
+
+
+_ROTARY_SCALING = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}  # fa_rotary_scaling
+
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain",
+                       factor: float = 1.0, original_len: float = 0.0, fast: float = 32.0,
+                       slow: float = 1.0, device=None):
+    """Table and amplitude of fa_rotary (and of fa_cache_append's rotation): (inv_freq [rot_dim/2]
+    fp64 on `device`, amplitude).  scaling: "plain", "linear" (positions interpolated), "base" (the
+    base raised), "by_parts" (YaRN; original_len is the training length)."""
+    if scaling not in _ROTARY_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY_SCALING)}, got {scaling!r}")
+    table = torch.empty(max(rot_dim // 2, 0), dtype=torch.float64)
+    amplitude = ctypes.c_float()
+    lib = load_library()
+    _check(lib.fa_rotary_frequencies(rot_dim, base, _ROTARY_SCALING[scaling], factor, original_len,
+                                     fast, slow, table.data_ptr() or None, ctypes.byref(amplitude)))
+    return (table if device is None else table.to(device)), amplitude.value
+
+
+def tree_mask(parents, device=None):
+    """fa_tree_decode_paged's mask of trees given by parents: [T] or [B,T] ints, parents[i] < i the
+    drafted token before token i, -1 the context.  Returns int64 [1 or B,T,ceil(T/64)]."""
+    p = torch.as_tensor(parents, dtype=torch.int32, device="cpu")
+    p = (p if p.dim() == 2 else p.unsqueeze(0)).contiguous()
+    B, T = p.shape
+    words = torch.empty(B, T, -(-T // 64), dtype=torch.int64)
+    lib = load_library()
+    for b in range(B):
+        _check(lib.fa_tree_mask(p[b].data_ptr(), T, words[b].data_ptr()))
+    return words if device is None else words.to(device)
 
 
 def fa_rotary(q, k, positions, inv_freq, *, amplitude: float = 1.0, interleaved: bool = False,

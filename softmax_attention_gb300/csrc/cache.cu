@@ -580,6 +580,44 @@ int fa_rotary(const fa_rotary_args* a, void* stream) {
   return FA_OK;
 }
 
+int fa_rotary_frequencies(int rot_dim, double base, fa_rotary_scaling scaling, double factor,
+                          double original_len, double fast, double slow, double* inv_freq,
+                          float* amplitude) {
+  if (rot_dim < 2 || rot_dim % 2 != 0 || !(base > 1.0) || isinf(base) || !inv_freq || !amplitude)
+    return bad(FA_ERR_INVALID_ARG, "fa_rotary_frequencies: need an even rot_dim >= 2, base > 1 and both outputs");
+  if (scaling != FA_ROTARY_PLAIN && (!(factor >= 1.0) || isinf(factor)))
+    return bad(FA_ERR_INVALID_ARG, "fa_rotary_frequencies: factor must be >= 1");
+  float a = 1.f;
+  switch (scaling) {
+    case FA_ROTARY_PLAIN:
+    case FA_ROTARY_LINEAR:
+      break;
+    case FA_ROTARY_BASE:
+      if (rot_dim <= 2) return bad(FA_ERR_INVALID_ARG, "fa_rotary_frequencies: FA_ROTARY_BASE needs rot_dim > 2");
+      base *= pow(factor, static_cast<double>(rot_dim) / (rot_dim - 2));
+      break;
+    case FA_ROTARY_BY_PARTS:
+      if (!(original_len > 0.0) || !(slow >= 0.0) || !(fast > slow))
+        return bad(FA_ERR_INVALID_ARG, "fa_rotary_frequencies: need original_len > 0 and fast > slow >= 0");
+      a = static_cast<float>(0.1 * log(factor) + 1.0);
+      break;
+    default:
+      return bad(FA_ERR_INVALID_ARG, "fa_rotary_frequencies: unknown scaling");
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == FA_ROTARY_LINEAR) f /= factor;
+    if (scaling == FA_ROTARY_BY_PARTS) {
+      const double turns = original_len * f / 6.283185307179586477;
+      const double keep = fmin(1.0, fmax(0.0, (turns - slow) / (fast - slow)));
+      f = (1.0 - keep) * f / factor + keep * f;
+    }
+    inv_freq[i] = f;
+  }
+  *amplitude = a;
+  return FA_OK;
+}
+
 int fa_cache_append(const fa_cache_append_args* a, void* stream) {
   if (!a) return bad(FA_ERR_INVALID_ARG, "fa_cache_append: null argument struct");
   if (a->T < 0) return bad(FA_ERR_INVALID_ARG, "fa_cache_append: T must be >= 0");

@@ -1088,6 +1088,19 @@ using namespace fa;
 
 extern "C" {
 
+int fa_tree_mask(const int32_t* parents, int T, uint64_t* words) {
+  if (T < 0 || T > kMaxTree) return bad(FA_ERR_INVALID_ARG, "fa_tree_mask: T must be in [0, 256]");
+  if (T > 0 && (!parents || !words)) return bad(FA_ERR_INVALID_ARG, "fa_tree_mask: null pointer");
+  const int W = (T + 63) / 64;
+  for (int i = 0; i < T; ++i) {
+    const int up = parents[i];
+    if (up < -1 || up >= i) return bad(FA_ERR_INVALID_ARG, "fa_tree_mask: a parent must come before its child, or be -1");
+    for (int w = 0; w < W; ++w) words[i * W + w] = up >= 0 ? words[up * W + w] : 0;
+    words[i * W + i / 64] |= 1ull << (i % 64);
+  }
+  return FA_OK;
+}
+
 size_t fa_tree_workspace_size(const fa_tree_args* a) {
   if (check_tree(a, false) != FA_OK || a->B == 0 || a->T == 0) return 0;
   return plan_tree(a).total;

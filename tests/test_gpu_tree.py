@@ -104,6 +104,12 @@ CASES = [
     (3, 4, 2, 4, 256, 8, [70, 4, 9], [4, 0, 2], True, 0),       # a sequence without a query
     (1, 128, 1, 2, 64, 16, [90], None, True, 0),                # one query a tile
     (1, 7, 1, 3, 128, 128, [1100], None, True, 0),              # split by the library
+    (2, 4, 4, 3, 64, 128, [700, 3], None, True, 0),             # few rows, pages of four slices
+    (1, 16, 1, 1, 256, 8, [515], None, False, 0),               # sixteen rows, two pages a slice
+    (2, 8, 2, 4, 128, 64, [129, 70], [2, 4], True, 2),          # sixteen rows, split, padding
+    (3, 2, 1, 1, 128, 32, [1, 32, 33], None, False, 0),         # lengths around a slice
+    (2, 8, 8, 1, 64, 8, [0, 700], None, False, 0),              # an empty sequence
+    (1, 6, 2, 5, 256, 32, [1000], None, True, 5),               # fifteen rows, D = 256, split
 ]
 
 
@@ -286,6 +292,65 @@ def test_matches_paged_decode_and_prefill():
     o2, l2 = fa.fa_decode_paged(q[:, :, -1].contiguous(), k, v, table, lens, L)
     assert torch.allclose(lse[..., 0], l2, atol=1e-5)
     assert (out[:, :, 0].float() - o2.float()).abs().max() <= 2 ** -7
+
+
+@pytest.mark.parametrize("cache", [E4M3, BF16])
+def test_no_key_at_all(cache):
+    """max_seq_len 0: only empty rows; and nothing to do."""
+    q = torch.randn(2, 4, 3, 64, device="cuda").to(BF16)
+    pages = torch.zeros(1, 2, 16, 64, device="cuda").to(cache)
+    kw = {}
+    if cache == E4M3:
+        kw = dict(k_scales=torch.full((1, 2, 16), 127, dtype=torch.uint8, device="cuda"))
+        kw["v_scales"] = kw["k_scales"]
+    table = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    out, lse = fa.fa_tree_decode_paged(q, pages, pages, table, lens, 0, **kw)
+    assert not out.any() and (lse == -math.inf).all()
+    out, lse = fa.fa_tree_decode_paged(q[:, :, :0], pages, pages, table, lens, 16, **kw)
+    assert out.shape == (2, 4, 0, 64) and lse.shape == (2, 4, 0)
+
+
+@pytest.mark.parametrize("cache", [E4M3, BF16])
+@pytest.mark.parametrize("T", [2, 40])
+def test_padding_queries_hold_anything(cache, T):
+    """NaN in the queries of padding rows (at and past draft_lens) stays there: those rows are
+    empty, every other row as without it."""
+    pr = Problem(2, 8, 2, T, 128, 16, BF16, cache, [300, 77])
+    (q, *rest), kw = pr.gpu()
+    drafts = torch.tensor([1, T - 1], dtype=torch.int32, device="cuda")
+    good = fa.fa_tree_decode_paged(q, *rest, draft_lens=drafts, **kw)
+    q[0, :, 1:] = math.nan
+    q[1, :, T - 1:] = math.inf
+    out, lse = fa.fa_tree_decode_paged(q, *rest, draft_lens=drafts, **kw)
+    assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+    assert not out[0, :, 1:].any() and (lse[0, :, 1:] == -math.inf).all()
+
+
+def test_a_cache_past_four_gigabytes():
+    """Pages whose byte offsets pass 32 bits: written, read back and attended there."""
+    Hkv, ps, D, T = 8, 64, 128, 20
+    P = (1 << 32) // (Hkv * ps * D) + 40
+    kp = torch.empty(P, Hkv, ps, D, dtype=torch.uint8, device="cuda").view(E4M3)
+    vp = torch.empty(P, Hkv, ps, D, dtype=torch.uint8, device="cuda").view(E4M3)
+    ks = torch.empty(P, Hkv, ps, dtype=torch.uint8, device="cuda")
+    vs = torch.empty(P, Hkv, ps, dtype=torch.uint8, device="cuda")
+    g = torch.Generator().manual_seed(5)
+    n = 200
+    table = torch.tensor([[P - 1, 3, P - 30, P - 2]], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    x = torch.randn(2, 1, Hkv, n, D, generator=g).to(BF16)
+    fa.fa_cache_append(x[0].cuda(), x[1].cuda(), kp, vp, table, lens, k_scales=ks, v_scales=vs)
+    k, v = fa.fa_cache_gather(kp, vp, table, lens, n, dtype=torch.float32, k_scales=ks, v_scales=vs)
+    for got, src in ((k, x[0]), (v, x[1])):
+        want = ref.dequantise(*ref.quantise(src.float()))
+        assert torch.equal(got.cpu().double(), want)
+    rows = [[t[0].double().cpu().transpose(0, 1)] for t in (k, v)]
+    for t in (1, T):  # the kernel for few rows, and the 128-row one
+        q = torch.randn(1, 8, t, D, generator=g).to(BF16)
+        out, lse = fa.fa_tree_decode_paged(q.cuda(), kp, vp, table, lens, n, k_scales=ks, v_scales=vs)
+        want = ref.tree_attention(q, rows[0], rows[1], [t], None, D ** -0.5)
+        ref.check_tree(out, lse, want, BF16, D)
 
 
 def test_bad_lengths_and_pages():
