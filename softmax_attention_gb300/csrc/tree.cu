@@ -46,6 +46,18 @@ namespace {
 using prefill::kRows;
 constexpr int kNumS = 3;  // S/P buffers in tensor memory
 
+// 5-D tiled TMA load (a 16-bit page).
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t c0, int32_t c1, int32_t c2, int32_t c3,
+                                            int32_t c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4),
+      "r"(bar)
+      : "memory");
+}
+
 template <int D, int BN, int STAGES, int RAW, bool Q8>
 struct Layout {
   static constexpr int kHalves = 2;                    // softmax warps a row of scores
