@@ -679,6 +679,7 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
     // first, and few others) trades maxima through shared memory.
     const int half = warp >= L::kHalfWarp ? 1 : 0, wq = warp % 4;
     const int r = wq * 32 + lane, team = H * live_warps * 32;
+    const int vote = 1 + wq, trade = 5 + wq;  // barriers of the two warps that share these rows
     const int g = r / p.q_per_tile, i = q0 + r % p.q_per_tile;
     const bool valid = g < p.G && i < p.T;   // a row of the output
     const bool active = valid && i < n_draft;  // a query of this sequence (else an empty row)
@@ -744,10 +745,10 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
         }
         row_max *= a;
       }
-      const bool raise = barrier_any(1, team, ok && row_max > m_run + prefill::kRescaleLog2);
+      const bool raise = barrier_any(vote, H * 32, ok && row_max > m_run + prefill::kRescaleLog2);
       if (raise) {
         shared(half) = row_max;
-        barrier_sync(2, team);
+        barrier_sync(trade, H * 32);
         const float m_new = fmaxf(m_run, fmaxf(row_max, shared(1 - half)));
         float alpha = 1.f;
         if (m_new > m_run + prefill::kRescaleLog2) {
@@ -825,9 +826,9 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
       tc_fence_after();
     }
     // the row's sum over both halves (their maxima are one)
-    barrier_sync(2, team);  // the last maxima have been read
+    barrier_sync(trade, H * 32);  // the last maxima have been read
     shared(half) = l_run;
-    barrier_sync(2, team);
+    barrier_sync(trade, H * 32);
     l_run = shared(0) + shared(1);
     if (ok) {
       // O / l, a row's slab of columns at a time, the halves in turn: staged in this warp's part of
