@@ -431,7 +431,6 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
   using L = Layout<D, BN, STAGES, RAW, Q8>;
   constexpr int kThreads = L::kThreads;
   constexpr int H = L::kHalves, CH = BN / H;  // scores of a tile that a softmax thread takes
-  constexpr int CR = CH;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -718,32 +717,25 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
       if (Q8 && BF16 && f16 && jj == 0) to_log2 *= q_factor;  // written before S_0 could be issued
       const float a = pre ? 1.f : to_log2;
       const int key0 = (t_begin + jj) * BN;
-      auto read = [&](int c0, uint32_t (&raw)[CR]) {
-        prefill::load_s<CR>(t_s + half * CH + c0, raw);
+      uint32_t raw[CH];
+      float row_max = -INFINITY;
+      if (ok) {
+        tc_fence_after();
+        prefill::load_s<CH>(t_s + half * CH, raw);
         if (pre) {
 #pragma unroll
-          for (int c = 0; c < CR; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * to_log2);
+          for (int c = 0; c < CH; ++c) raw[c] = __float_as_uint(__uint_as_float(raw[c]) * to_log2);
         }
         if (key0 + BN > ctx) {
 #pragma unroll
-          for (int w = 0; w < CR / 32; ++w) {
-            const uint32_t bits = row_bits(row, key0 + half * CH + c0 + 32 * w - ctx);
+          for (int w = 0; w < CH / 32; ++w) {
+            const uint32_t bits = row_bits(row, key0 + half * CH + 32 * w - ctx);
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (!((bits >> c) & 1)) raw[32 * w + c] = 0xff800000u;  // -inf
           }
         }
-      };
-      uint32_t raw[CR];
-      float row_max = -INFINITY;
-      if (ok) {
-        tc_fence_after();
-#pragma unroll 1
-        for (int c0 = 0; c0 < CH; c0 += CR) {
-          read(c0, raw);
-          row_max = fmaxf(row_max, chunk_max(raw));
-        }
-        row_max *= a;
+        row_max = a * chunk_max(raw);
       }
       const bool raise = barrier_any(vote, H * 32, ok && row_max > m_run + prefill::kRescaleLog2);
       if (raise) {
@@ -767,18 +759,14 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
         }
       }
       if (!ok) continue;
-#pragma unroll 1
-      for (int c0 = 0; c0 < CH; c0 += CR) {
-        if (CR < CH) read(c0, raw);
-        uint32_t pk[CR / 2];
-        if constexpr (Q8 && BF16) {
-          if (f16) chunk_weights<CR, false>(raw, a, m_run, l_run, pk);
-          else chunk_weights<CR, true>(raw, a, m_run, l_run, pk);
-        } else {
-          chunk_weights<CR, BF16>(raw, a, m_run, l_run, pk);
-        }
-        prefill::store_p<CR>(t_s + half * CH + c0 / 2, pk);
+      uint32_t pk[CH / 2];
+      if constexpr (Q8 && BF16) {
+        if (f16) chunk_weights<CH, false>(raw, a, m_run, l_run, pk);
+        else chunk_weights<CH, true>(raw, a, m_run, l_run, pk);
+      } else {
+        chunk_weights<CH, BF16>(raw, a, m_run, l_run, pk);
       }
+      prefill::store_p<CH>(t_s + half * CH, pk);
       tmem_st_wait();
       if (!Q8 && key0 + BN > ctx) {
         // The stage holds rows of drafted tokens, which some queries do not see, or rows past
