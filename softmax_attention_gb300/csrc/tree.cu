@@ -225,14 +225,15 @@ __device__ __forceinline__ void widen4(uint32_t w, const RowScale& s, uint32_t& 
 // become zeros.
 // ------------------------------------------------------------------------------------------
 // Whether some scale byte of keys [first, last) lies outside [113, 134], where every e4m3 value
-// times the scale is exact in fp16 (a multiple of 2^-23, at most 448 * 2^7).  Each thread of
-// the block looks at whole pages.
+// times the scale is exact in fp16 (a multiple of 2^-23, at most 448 * 2^7).  Each of
+// THREADS threads, this one `looker`, looks at whole pages.
 template <int THREADS>
-__device__ __forceinline__ bool scales_leave_fp16(const TreeParams& p, int b, int hk, int first, int last) {
+__device__ __forceinline__ bool scales_leave_fp16(const TreeParams& p, int looker, int b, int hk, int first,
+                                                  int last) {
   const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
   const int pages = last > first ? ((last - 1) >> p.page_shift) - (first >> p.page_shift) + 1 : 0;
   bool outside = false;
-  for (int i = threadIdx.x; i < pages; i += THREADS) {
+  for (int i = looker; i < pages; i += THREADS) {
     const int lp = (first >> p.page_shift) + i;
     const int page = __ldg(table + lp);
     if (page < 0 || page >= p.num_pages) continue;
@@ -525,13 +526,18 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
   // values that fp16 holds exactly.
   bool f16 = !BF16;
   tc_fence_before();
-  if constexpr (Q8 && BF16) {
-    const int last = min(Lkv, (t_begin + n) * BN);
-    f16 = !__syncthreads_or(scales_leave_fp16<kThreads>(p, b, hk, t_begin * BN, last) ? 1 : 0);
-  } else {
-    __syncthreads();
-  }
+  __syncthreads();
   tc_fence_after();
+  if constexpr (Q8 && BF16) {
+    // every warp but the two that copy, which have begun meanwhile
+    if (warp != 4 && warp != 7) {
+      constexpr int kLookers = kThreads - 64;
+      const int looker = threadIdx.x - (warp > 7 ? 64 : warp > 4 ? 32 : 0);
+      const int last = min(Lkv, (t_begin + n) * BN);
+      f16 = !barrier_any(9, kLookers,
+                         scales_leave_fp16<kLookers>(p, looker, b, hk, t_begin * BN, last));
+    }
+  }
   const uint32_t tmem = *tmem_slot;
   const uint32_t tm_o = tmem;           // O: columns [0, D)
   const uint32_t tm_s0 = tmem + D;      // S/P buffer b: columns [D + b*BN, D + (b+1)*BN)

@@ -133,7 +133,7 @@ __device__ __forceinline__ uint32_t widen2_hi(uint32_t codes) {
 template <int THREADS>
 __device__ __forceinline__ int sequence_of_rank(const TreeParams& p, int rank) {
   __shared__ int found;
-  if (p.B > THREADS) return rank;
+  if (p.B == 1 || p.B > THREADS) return rank;
   if (threadIdx.x < p.B) {
     const int mine = p.kv_lens[threadIdx.x];
     int before = 0;
