@@ -148,10 +148,10 @@ __device__ __forceinline__ int sequence_of_rank(const TreeParams& p, int rank) {
 }
 
 // The kernel for few rows over 8-bit pages (tree_rows.cu): takes a call if tree_rows_takes says
-// so (rows = query heads per kv head times T); tree_rows_slots is the number of its CTAs that
-// the current device holds at once.
+// so (rows = query heads per kv head times T); tree_rows_ctas is the number of its CTAs that an SM
+// holds at once.
 bool tree_rows_takes(int rows);
-int tree_rows_slots(int D);
+int tree_rows_ctas(int D, int rows);
 cudaError_t launch_tree_rows(const TreeParams& p, int D, bool bf16, cudaStream_t stream);
 
 }  // namespace fa

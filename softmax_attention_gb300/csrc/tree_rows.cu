@@ -1,14 +1,18 @@
 // tree_rows.cu -- tree attention over an 8-bit paged cache for few rows (query heads of a kv head
 // times drafted tokens): the decode step, where the cache's bytes are all the time there is.
 //
-// Up to 16 rows fill one tile of the warp-level matrix instruction (m16n8k16), whose operands are
-// registers: e4m3 codes go from shared memory to registers, are converted there (one instruction
-// a pair) and multiplied, so a cache byte is written to shared memory once by TMA and read once.
-// The 128-row tile of the tcgen05 kernel passes each byte through shared memory six times (raw in
-// and out, widened twice its size in and out) and spends its tensor time on empty rows: there
-// the 8-bit cache is read at 3.2 TB/s whatever the rows, here at 5.5 TB/s (57 sequences of 4096
-// tokens, 8 kv heads, D = 128; 0.83 of a copy), bound by the latencies and issue slots of the
-// twelve warps that an SM's registers hold.
+// The warp-level matrix instruction (m16n8k16) takes its operands from registers: e4m3 codes go
+// from shared memory to registers, are converted there (one instruction a pair) and multiplied,
+// so a cache byte is written to shared memory once by TMA and read once.  (The 128-row tile of the
+// tcgen05 kernel passes each byte through shared memory six times and spends its tensor time on
+// empty rows: there 57 sequences of 4096 tokens, 8 kv heads, D = 128, are read at 3.2 TB/s.)
+// Codes are the 16-row operand and q's rows the 8-column one, in both products: S^T = K Q^T and
+// O^T += V^T P^T.  Eight rows or fewer, the decode step of up to eight query heads a kv head, then
+// fill their tile; nine to sixteen take two (NT).  With q as the 16-row operand a decode step's
+// matrix, exponential and O instructions were half empty: 718 instructions a warp and 32 tokens
+// and three CTAs of 166 registers an SM, where this takes 126 registers and four CTAs (128
+// sequences of 1K to 4K tokens: 135 -> 110 us, 6.0 TB/s or 0.88 of a copy; the 57 even ones 87 ->
+// 83 us).  Two tiles lose one or two per cent to the transposition of the weights.
 //
 // Each warp runs alone: its own ring of slices (SL tokens of K and of V), its own barriers, its
 // own online softmax; four warps of a CTA take the slices of a (sequence, kv head, part) in turn
@@ -33,7 +37,7 @@
 namespace fa {
 namespace {
 
-constexpr int kTileRows = 16;
+constexpr int kMaxRows = 16;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr float kShift = 7.f;       // weights times 2^7
@@ -41,33 +45,46 @@ constexpr float kStale = 8.f;       // O is rescaled when a maximum grows by mor
 constexpr float kUnset = -3e38f;    // a maximum before the first score
 constexpr float kLn2 = 0.69314718055994530942f;
 
-template <int D>
+template <int D, int NT>
 struct RowsLayout {
-  static constexpr int kSlice = D == 256 ? 16 : 32;  // tokens a step
+  static constexpr int kRows = 8 * NT;
+  // Tokens a step, CTAs an SM and stages: what fits registers and shared memory, measured.  One
+  // tile at D = 128 with slices of 32, three CTAs and two stages: 122 us where these take 110; two
+  // tiles with slices of 16 and four stages: 155 for 148 (sequences of 1K to 4K tokens).  D = 64
+  // with slices of 16: 150 us for 118; D = 256 with three CTAs of two stages: 115 for 113.
+  static constexpr int kSlice = D == 256 || (D == 128 && NT == 1) ? 16 : 32;
   static constexpr int kStage = kSlice * D;          // bytes of K (or V) a slice
-  static constexpr int kCtas = D == 256 ? 2 : 3;     // CTAs an SM
-  static constexpr int kStages = D == 64 ? 4 : kCtas == 2 ? 3 : 2;
+  static constexpr int kCtas = D == 256 ? 2 : NT == 1 ? 4 : 3;
+  static constexpr int kStages = D == 256 || NT == 1 ? 3 : D == 64 ? 4 : 2;
   static constexpr int kRing = kStages * 2 * kStage;  // a warp's ring
   static constexpr int kQOff = kWarps * kRing;
-  static constexpr int kQBytes = (D / 16) * 512;  // fp16 fragments of q
+  static constexpr int kQBytes = (D / 16) * NT * 256;  // fp16 fragments of q
   static constexpr int kBarOff = kQOff + kQBytes;
   static constexpr int kStatOff = kBarOff + kWarps * kStages * 2 * 8;
-  static constexpr int kPoisonOff = kStatOff + kWarps * kTileRows * 3 * 4;
+  static constexpr int kPoisonOff = kStatOff + kWarps * kRows * 3 * 4;
   static constexpr int kBytes = kPoisonOff + kMaxTree / 32 * 4 + 16;
   static constexpr int kAlloc = kBytes + 1024;
-  static_assert(kTileRows * D * 4 <= kRing, "a warp's O goes into its ring at the end");
+  static_assert(kRows * D * 4 <= kRing, "a warp's O goes into its ring at the end");
   static_assert(kCtas * (kAlloc + 1024) <= 228 * 1024, "shared memory of an SM");
 };
 
 // C (16 x 8, fp32) += A (16 x 16, fp16) B (16 x 8, fp16).  With g = lane / 4, t = lane % 4:
 // a0 (row g, k 2t..), a1 (g + 8, 2t..), a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..); b0 (k 2t.., column
 // g), b1 (k 2t + 8..); c0, c1 (row g, columns 2t, 2t + 1), c2, c3 (row g + 8).
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint2 b) {
   asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
+}
+
+// An 8x8 matrix of 16-bit elements, transposed (lane: row g, elements 2t, 2t + 1, in and out).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 // Four 8x8 matrices of 16-bit units, transposed: register i of lane l holds units (row 2t, row
@@ -90,14 +107,15 @@ __device__ __forceinline__ void load_q4(const void* q, int64_t at, float (&x)[4]
   }
 }
 
-template <int D, bool BF16, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
+// NT tiles of eight rows.
+template <int D, int NT, bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, RowsLayout<D, NT>::kCtas)
     tree_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const TreeParams p) {
-  using L = RowsLayout<D>;
+  using L = RowsLayout<D, NT>;
   constexpr int SL = L::kSlice, NS = L::kStages;
   constexpr int kSteps = D / 16;      // k steps of S, and 16-column chunks of V
-  constexpr int kTiles = SL / 8;      // 8-token tiles of S
+  constexpr int kGroups = SL / 8;     // 8-token groups of S
   constexpr int kIn = D < 128 ? D : 128;
   constexpr int kLaneBytes = kIn / 4;  // bytes of a token's block that a lane of four holds
   extern __shared__ uint8_t smem_raw[];
@@ -186,11 +204,11 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
   // A lane of four holds columns [kLaneBytes t, kLaneBytes (t + 1)) of each 128-column block of a
   // token; k step kk takes four of them, in both operands (the order of k does not matter).
   const int rows = p.G * p.T;
-  __shared__ float q_scale[kTileRows];  // scale_log2 times the row's power of two
-  for (int r = warp * 4 + lane / 8; r < kTileRows; r += kWarps * 4) {
+  __shared__ float q_scale[L::kRows];  // scale_log2 times the row's power of two
+  for (int r = warp * 4 + lane / 8; r < L::kRows; r += kWarps * 4) {
     // eight lanes a row: lane c takes columns 4c, 4c + 32, ...
     const int c = lane % 8;
-    const bool have = r < rows;
+    const bool have = r < rows && r % p.T < n_draft;  // padding rows: 0, whatever q has there
     const int head = hk * p.G + (have ? r / p.T : 0), i = have ? r % p.T : 0;
     const int64_t at = b * p.q_strides[0] + head * p.q_strides[1] + i * p.q_strides[2];
     float x[D / 32][4];
@@ -212,36 +230,40 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
     for (int u = 0; u < D / 32; ++u) {
       const int col = 4 * c + 32 * u, blk = col / kIn, in = col % kIn;
       const int t = in / kLaneBytes, kk = blk * (kIn / 16) + (in % kLaneBytes) / 4;
-      // fragment words of lane (r % 8) * 4 + t: a0/a2 for rows 0-7 of the tile, a1/a3 for 8-15
-      uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::kQOff + kk * 512 +
-                                                  ((r % 8) * 4 + t) * 16) + r / 8;
+      // fragment of lane (r % 8) * 4 + t
+      const int frag = kk * NT + r / 8;  // two to a 16-byte read
+      uint32_t* dst = reinterpret_cast<uint32_t*>(smem + L::kQOff + frag / 2 * 512 +
+                                                  ((r % 8) * 4 + t) * 16 + frag % 2 * 8);
       dst[0] = pack_f16x2(x[u][0] * f, x[u][1] * f);
-      dst[2] = pack_f16x2(x[u][2] * f, x[u][3] * f);
+      dst[1] = pack_f16x2(x[u][2] * f, x[u][3] * f);
     }
   }
   __syncthreads();
 
-  // ---- this lane's rows: g and g + 8 ----
-  float a_row[2], mx[2], mo[2];
-  float2 l[2];  // two partial sums a row and lane
-  TreeRow row[2];
+  // ---- this lane's rows: 8m + 2t and 8m + 2t + 1 of each tile m, a pair in every float2 ----
+  float2 mx[NT], mo[NT], l[NT];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 8 * h + g, i = r < rows ? r % p.T : 0;
-    const bool active = r < rows && i < n_draft;
-    a_row[h] = q_scale[r];
-    mx[h] = mo[h] = kUnset;
-    l[h] = make_float2(0.f, 0.f);
-    row[h].i = i;
-    row[h].n = active ? n_draft : 0;
-    row[h].words = p.mask && active
-        ? p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words : nullptr;
+  for (int m = 0; m < NT; ++m) {
+    mx[m] = mo[m] = make_float2(kUnset, kUnset);
+    l[m] = make_float2(0.f, 0.f);
   }
-  float o[2 * kSteps][4];
+  // drafted tokens of the 32 from key0 on that row r sees
+  auto seen = [&](int r, int off) {
+    const int i = r < rows ? r % p.T : 0;
+    TreeRow row;
+    row.i = i;
+    row.n = r < rows && i < n_draft ? n_draft : 0;
+    row.words = p.mask && row.n
+        ? p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words : nullptr;
+    return row_bits(row, off);
+  };
+  float o[NT][kSteps][4];  // columns 16c + 2g (elements 0, 1: the two rows) and 16c + 2g + 1 (2, 3)
 #pragma unroll
-  for (int c = 0; c < 2 * kSteps; ++c)
+  for (int m = 0; m < NT; ++m)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
+    for (int c = 0; c < kSteps; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[m][c][e] = 0.f;
 
   // shared-memory offsets inside a stage (a box holds [128-column block][token][128 bytes], 16-byte
   // chunks swizzled by the token)
@@ -259,17 +281,20 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
     constexpr bool TAIL = decltype(tail_c)::value;
     const int st = k % NS, key0 = (s_begin + k * kWarps) * SL;
     if (!__all_sync(0xffffffffu, mbar_wait(bar_k(st), (k / NS) & 1, p.status))) return false;
-    // S = Q K^T, a 128-column block at a time
-    float s[kTiles][4];
+    // S^T = K Q^T, a 128-column block at a time: s[.][i] are tokens 8i + g
+    float2 s[NT][kGroups];
+    float acc[NT][kGroups / 2][4];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+      for (int j = 0; j < kGroups / 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
 #pragma unroll
     for (int blk = 0; blk < D / kIn; ++blk) {
-      uint32_t w[kTiles][kIn / 16];
+      uint32_t w[kGroups][kIn / 16];
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
+      for (int j = 0; j < kGroups; ++j) {
         const uint32_t at = k_stage(st) + token_off(8 * j + g) + blk * blk_off;
 #pragma unroll
         for (int u = 0; u < kLaneBytes / 16; ++u) {
@@ -284,53 +309,59 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
         __syncwarp();  // every lane has read the stage
         if (k + NS < n) copy(&tm_k, k_stage(st), bar_k(st), k + NS, next_id);
       }
+      uint4 qf;
 #pragma unroll
       for (int kk = 0; kk < kIn / 16; ++kk) {
-        uint4 a;
-          a = lds128(s_base + L::kQOff + (blk * (kIn / 16) + kk) * 512 + lane * 16);
+        const int frag = (blk * (kIn / 16) + kk) * NT;
+        if (frag % 2 == 0) qf = lds128(s_base + L::kQOff + frag / 2 * 512 + lane * 16);
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          const uint32_t b0 = widen2(w[j][kk]), b1 = widen2_hi(w[j][kk]);
+        for (int j = 0; j < kGroups / 2; ++j) {
+          const uint32_t a0 = widen2(w[2 * j][kk]), a2 = widen2_hi(w[2 * j][kk]);
+          const uint32_t a1 = widen2(w[2 * j + 1][kk]), a3 = widen2_hi(w[2 * j + 1][kk]);
 #pragma unroll
-          mma16816(s[j], a, b0, b1);
+          for (int m = 0; m < NT; ++m)
+            mma16816(acc[m][j], a0, a1, a2, a3,
+                     (frag + m) % 2 ? make_uint2(qf.z, qf.w) : make_uint2(qf.x, qf.y));
         }
       }
     }
-    // the scales of this lane's tokens 8j + 2t, + 1: 2^ek as it multiplies, ev as it is added
-    float2 kf[kTiles], ev[kTiles];
+    // the scales of this lane's tokens: 2^ek as it multiplies, ev as it is added
+    float kf[kGroups], ev[kGroups];
 #pragma unroll
-    for (int j = 0; j < kTiles; ++j) {
-      const uint32_t w0 = __shfl_sync(0xffffffffu, scales, 8 * j + 2 * t4);
-      const uint32_t w1 = __shfl_sync(0xffffffffu, scales, 8 * j + 2 * t4 + 1);
-      kf[j] = make_float2(__uint_as_float(w0 & 0xffff0000u), __uint_as_float(w1 & 0xffff0000u));
-      ev[j] = make_float2(__uint_as_float(w0 << 16), __uint_as_float(w1 << 16));
+    for (int i = 0; i < kGroups; ++i) {
+      const uint32_t w = __shfl_sync(0xffffffffu, scales, 8 * i + g);
+      kf[i] = __uint_as_float(w & 0xffff0000u);
+      ev[i] = __uint_as_float(w << 16);
     }
     // scores in log2 units; hidden tokens get -inf
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t bits = ~0u;
-      if constexpr (TAIL) bits = row_bits(row[h], key0 - ctx) >> (2 * t4);
-      const float2 a = make_float2(a_row[h], a_row[h]);
+    for (int m = 0; m < NT; ++m) {
+      const float2 a = make_float2(q_scale[8 * m + 2 * t4], q_scale[8 * m + 2 * t4 + 1]);
+      uint32_t b0 = ~0u, b1 = ~0u;
+      if constexpr (TAIL) {
+        b0 = seen(8 * m + 2 * t4, key0 - ctx) >> g;
+        b1 = seen(8 * m + 2 * t4 + 1, key0 - ctx) >> g;
+      }
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
-        float2 x = __fmul2_rn(__fmul2_rn(make_float2(s[j][2 * h], s[j][2 * h + 1]), a), kf[j]);
-        if (TAIL && !((bits >> (8 * j)) & 1)) x.x = -INFINITY;
-        if (TAIL && !((bits >> (8 * j + 1)) & 1)) x.y = -INFINITY;
-        s[j][2 * h] = x.x;
-        s[j][2 * h + 1] = x.y;
+      for (int i = 0; i < kGroups; ++i) {
+        float2 x = make_float2(acc[m][i / 2][2 * (i & 1)], acc[m][i / 2][2 * (i & 1) + 1]);
+        x = __fmul2_rn(__fmul2_rn(x, a), make_float2(kf[i], kf[i]));
+        if (TAIL && !((b0 >> (8 * i)) & 1)) x.x = -INFINITY;
+        if (TAIL && !((b1 >> (8 * i)) & 1)) x.y = -INFINITY;
+        s[m][i] = x;
       }
     }
     // exponents of the sums' terms (y1 = x - mx) and of the weights (y2 = x + ev - mo + kShift)
-    float2 y1[2][kTiles], y2[2][kTiles];
+    float2 y1[NT][kGroups], y2[NT][kGroups];
     auto exponents = [&]() {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float down = -mx[h], up = kShift - mo[h];
+      for (int m = 0; m < NT; ++m) {
+        const float2 down = make_float2(-mx[m].x, -mx[m].y);
+        const float2 up = make_float2(kShift - mo[m].x, kShift - mo[m].y);
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          const float2 x = make_float2(s[j][2 * h], s[j][2 * h + 1]);
-          y1[h][j] = __fadd2_rn(x, make_float2(down, down));
-          y2[h][j] = __fadd2_rn(x, __fadd2_rn(ev[j], make_float2(up, up)));
+        for (int i = 0; i < kGroups; ++i) {
+          y1[m][i] = __fadd2_rn(s[m][i], down);
+          y2[m][i] = __fadd2_rn(s[m][i], __fadd2_rn(make_float2(ev[i], ev[i]), up));
         }
       }
     };
@@ -338,51 +369,58 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
     // how far the scores are above the running maxima; mostly not far enough to move them
     float over1 = -INFINITY, over2 = -INFINITY;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          over1 = prefill::fmax3(over1, y1[h][j].x, y1[h][j].y);
-          over2 = prefill::fmax3(over2, y2[h][j].x, y2[h][j].y);
-        }
+      for (int i = 0; i < kGroups; ++i) {
+        over1 = prefill::fmax3(over1, y1[m][i].x, y1[m][i].y);
+        over2 = prefill::fmax3(over2, y2[m][i].x, y2[m][i].y);
+      }
     if (__any_sync(0xffffffffu, over1 > kStale || over2 > kStale + kShift)) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x1 = mx[h], x2 = mo[h];
+      for (int m = 0; m < NT; ++m) {
+        float2 x1 = mx[m], x2 = mo[m];
 #pragma unroll
-        for (int j = 0; j < kTiles; ++j) {
-          x1 = prefill::fmax3(x1, s[j][2 * h], s[j][2 * h + 1]);
-          x2 = prefill::fmax3(x2, s[j][2 * h] + ev[j].x, s[j][2 * h + 1] + ev[j].y);
+        for (int i = 0; i < kGroups; ++i) {
+          x1.x = fmaxf(x1.x, s[m][i].x);
+          x1.y = fmaxf(x1.y, s[m][i].y);
+          x2.x = fmaxf(x2.x, s[m][i].x + ev[i]);
+          x2.y = fmaxf(x2.y, s[m][i].y + ev[i]);
         }
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
-        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 1));
-        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
-        x2 = fmaxf(x2, __shfl_xor_sync(0xffffffffu, x2, 2));
-        const float alpha1 = exp2_approx(mx[h] - x1), alpha2 = exp2_approx(mo[h] - x2);
-        l[h].x *= alpha1;
-        l[h].y *= alpha1;
-        mx[h] = x1;
-        mo[h] = x2;
 #pragma unroll
-        for (int c = 0; c < 2 * kSteps; ++c) {
-          o[c][2 * h] *= alpha2;
-          o[c][2 * h + 1] *= alpha2;
+        for (int d = 4; d <= 16; d *= 2) {
+          x1.x = fmaxf(x1.x, __shfl_xor_sync(0xffffffffu, x1.x, d));
+          x1.y = fmaxf(x1.y, __shfl_xor_sync(0xffffffffu, x1.y, d));
+          x2.x = fmaxf(x2.x, __shfl_xor_sync(0xffffffffu, x2.x, d));
+          x2.y = fmaxf(x2.y, __shfl_xor_sync(0xffffffffu, x2.y, d));
+        }
+        l[m].x *= exp2_approx(mx[m].x - x1.x);
+        l[m].y *= exp2_approx(mx[m].y - x1.y);
+        const float2 alpha = make_float2(exp2_approx(mo[m].x - x2.x), exp2_approx(mo[m].y - x2.y));
+        mx[m] = x1;
+        mo[m] = x2;
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) {
+          o[m][c][0] *= alpha.x;
+          o[m][c][1] *= alpha.y;
+          o[m][c][2] *= alpha.x;
+          o[m][c][3] *= alpha.y;
         }
       }
       exponents();
     }
-    uint32_t pk[kTiles][2];  // weights: rows g, g + 8
+    // weights: (token, two rows) turned to (row, two tokens), the MMA's B
+    uint32_t pk[NT][kGroups];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int m = 0; m < NT; ++m)
 #pragma unroll
-      for (int j = 0; j < kTiles; ++j) {
-        const float2 e1 = y1[h][j], e2 = y2[h][j];
-        l[h] = __fadd2_rn(l[h], make_float2(exp2_approx(e1.x), exp2_approx(e1.y)));
-        pk[j][h] = pack_f16x2(exp2_approx(e2.x), exp2_approx(e2.y));
+      for (int i = 0; i < kGroups; ++i) {
+        const float2 e1 = y1[m][i], e2 = y2[m][i];
+        l[m] = __fadd2_rn(l[m], make_float2(exp2_approx(e1.x), exp2_approx(e1.y)));
+        pk[m][i] = transpose8x8(pack_f16x2(exp2_approx(e2.x), exp2_approx(e2.y)));
       }
-    }
-    // O += P V: 16 tokens x 32 columns of V codes a load, transposed so that a register holds two
-    // neighbouring columns of two tokens; regrouped by column they are the pairs the MMA wants.
-    // Of a 16-column chunk, accumulators 2c and 2c + 1 hold the even and the odd columns.
+    // O^T += V^T P^T: 16 tokens x 32 columns of V codes a load, transposed so that a register holds
+    // two neighbouring columns of two tokens; regrouped by column they are the pairs the MMA wants.
+    // Of a 16-column chunk, the A rows 0-7 are the even columns and 8-15 the odd ones.
     if (!__all_sync(0xffffffffu, mbar_wait(bar_v(st), (k / NS) & 1, p.status))) return false;
 #pragma unroll
     for (int kt = 0; kt < SL / 16; ++kt) {
@@ -418,9 +456,9 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
         for (int cc = 0; cc < 2; ++cc) {
           const uint32_t u0 = __byte_perm(r[2 * cc], 0, 0x3120), u1 = __byte_perm(r[2 * cc + 1], 0, 0x3120);
           const uint32_t e0 = widen2(u0), e1 = widen2(u1), d0 = widen2_hi(u0), d1 = widen2_hi(u1);
-          const uint4 a = make_uint4(pk[2 * kt][0], pk[2 * kt][1], pk[2 * kt + 1][0], pk[2 * kt + 1][1]);
-          mma16816(o[2 * (c + cc)], a, e0, e1);
-          mma16816(o[2 * (c + cc) + 1], a, d0, d1);
+#pragma unroll
+          for (int m = 0; m < NT; ++m)
+            mma16816(o[m][c + cc], e0, d0, e1, d1, make_uint2(pk[m][2 * kt], pk[m][2 * kt + 1]));
         }
       }
     }
@@ -472,24 +510,25 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
   float* stat = reinterpret_cast<float*>(smem + L::kStatOff);  // [warp][row][mx, mo, l]
   float* part = reinterpret_cast<float*>(smem + warp * L::kRing);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    float sum = l[h].x + l[h].y;
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    const int r = 8 * h + g;
-    if (t4 == 0) {
-      float* at = stat + (warp * kTileRows + r) * 3;
-      at[0] = mx[h];
-      at[1] = mo[h];
-      at[2] = sum;
-    }
-    // columns 16c + 4t .. + 3 of row r, chunks of four swizzled by the row
+  for (int m = 0; m < NT; ++m)
 #pragma unroll
-    for (int c = 0; c < kSteps; ++c)
-      *reinterpret_cast<float4*>(part + r * D + (((4 * c + t4) ^ (r & 7)) * 4)) =
-          make_float4(o[2 * c][2 * h], o[2 * c + 1][2 * h], o[2 * c][2 * h + 1],
-                      o[2 * c + 1][2 * h + 1]);
-  }
+    for (int h = 0; h < 2; ++h) {
+      float sum = h ? l[m].y : l[m].x;
+#pragma unroll
+      for (int d = 4; d <= 16; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      const int r = 8 * m + 2 * t4 + h;
+      if (g == 0) {
+        float* at = stat + (warp * L::kRows + r) * 3;
+        at[0] = h ? mx[m].y : mx[m].x;
+        at[1] = h ? mo[m].y : mo[m].x;
+        at[2] = sum;
+      }
+      // columns 16c + 2g, + 1 of row r, chunks of four swizzled by the row
+#pragma unroll
+      for (int c = 0; c < kSteps; ++c)
+        *reinterpret_cast<float2*>(part + r * D + ((4 * c + g / 2) ^ (r & 7)) * 4 + (g & 1) * 2) =
+            make_float2(o[m][c][h], o[m][c][2 + h]);
+    }
   __syncthreads();
   if (failed) return;
   bool any_poison = false;
@@ -500,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
     float M = kUnset, Mo = kUnset;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float* at = stat + (w * kTileRows + r) * 3;
+      const float* at = stat + (w * L::kRows + r) * 3;
       M = fmaxf(M, at[0]);
       Mo = fmaxf(Mo, at[1]);
     }
@@ -508,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float* at = stat + (w * kTileRows + r) * 3;
+      const float* at = stat + (w * L::kRows + r) * 3;
       const float fo = exp2_approx(at[1] - Mo);
       sum += at[2] * exp2_approx(at[0] - M);
       const float4 x = *reinterpret_cast<const float4*>(
@@ -558,9 +597,9 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D>::kCtas)
   }
 }
 
-template <int D, bool BF16>
+template <int D, int NT, bool BF16>
 cudaError_t launch_impl(const TreeParams& p, cudaStream_t st) {
-  using L = RowsLayout<D>;
+  using L = RowsLayout<D, NT>;
   CUtensorMap tk, tv;
   const uint64_t ps = static_cast<uint64_t>(p.page_size), pages = static_cast<uint64_t>(p.num_pages) * p.Hkv;
   // a page of one head: page_size rows of D bytes as (column, row, block of 128 columns)
@@ -572,35 +611,40 @@ cudaError_t launch_impl(const TreeParams& p, cudaStream_t st) {
   if (!encode_tiled(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.k_pages, dims, str, box, swz) ||
       !encode_tiled(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.v_pages, dims, str, box, swz))
     return cudaErrorInvalidValue;
-  auto kern = p.n_splits > 1 ? tree_rows_kernel<D, BF16, true> : tree_rows_kernel<D, BF16, false>;
+  auto kern = p.n_splits > 1 ? tree_rows_kernel<D, NT, BF16, true> : tree_rows_kernel<D, NT, BF16, false>;
   cudaError_t e = ensure_smem_limit(kern, L::kAlloc);
   if (e != cudaSuccess) return e;
   kern<<<dim3(p.n_splits, p.Hkv, p.B), kThreads, L::kAlloc, st>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
-template <bool BF16>
+template <int NT, bool BF16>
 cudaError_t launch_d(const TreeParams& p, int D, cudaStream_t st) {
   switch (D) {
-    case 64: return launch_impl<64, BF16>(p, st);
-    case 128: return launch_impl<128, BF16>(p, st);
-    default: return launch_impl<256, BF16>(p, st);
+    case 64: return launch_impl<64, NT, BF16>(p, st);
+    case 128: return launch_impl<128, NT, BF16>(p, st);
+    default: return launch_impl<256, NT, BF16>(p, st);
   }
 }
 
 }  // namespace
 
-// One 16-row tile.  With two (17 to 32 rows, D = 128) a warp's registers spill and the loop is bound by
-// its arithmetic: 38 sequences of 4096 tokens take 105 to 137 us, the 128-row kernel 100 us.
-bool tree_rows_takes(int rows) { return rows <= kTileRows; }
+// At most two tiles.  With four (17 to 32 rows, D = 128) a warp's registers spill and the loop is
+// bound by its arithmetic: 38 sequences of 4096 tokens take 105 to 137 us, the 128-row kernel 100 us.
+bool tree_rows_takes(int rows) { return rows <= kMaxRows; }
 
-int tree_rows_slots(int D) {
-  const int sms = num_sms() > 0 ? num_sms() : 152;
-  return sms * (D == 256 ? 2 : 3);
+int tree_rows_ctas(int D, int rows) {
+  const bool one = rows <= 8;
+  switch (D) {
+    case 64: return one ? RowsLayout<64, 1>::kCtas : RowsLayout<64, 2>::kCtas;
+    case 128: return one ? RowsLayout<128, 1>::kCtas : RowsLayout<128, 2>::kCtas;
+    default: return one ? RowsLayout<256, 1>::kCtas : RowsLayout<256, 2>::kCtas;
+  }
 }
 
 cudaError_t launch_tree_rows(const TreeParams& p, int D, bool bf16, cudaStream_t stream) {
-  return bf16 ? launch_d<true>(p, D, stream) : launch_d<false>(p, D, stream);
+  if (p.G * p.T <= 8) return bf16 ? launch_d<1, true>(p, D, stream) : launch_d<1, false>(p, D, stream);
+  return bf16 ? launch_d<2, true>(p, D, stream) : launch_d<2, false>(p, D, stream);
 }
 
 }  // namespace fa
