@@ -651,11 +651,16 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
         tc_fence_after();
         const uint64_t vd = sdesc_add(v_desc, stage * L::kKVBytes);
         const uint32_t a_p = tm_s0 + buf * BN;
+        const int left = Lkv - (t_begin + jj) * BN;  // tokens from this tile's first on
 #pragma unroll
         for (int kk = 0; kk < BN / 16; ++kk)
-          // P (16-bit pairs) of each half lies over the first columns of its own scores
-          mma_ts(tm_o, a_p + kk * 8 + (kk / (CH / 16)) * (CH / 2), sdesc_add(vd, kk * (2 * kRG)), idesc_o,
-                 (jj > 0 || kk > 0) ? 1u : 0u);
+          // P (16-bit pairs) of each half lies over the first columns of its own scores.  16-bit
+          // pages: steps past the sequence's end are left out, so that nothing has to clear their
+          // V (92 sequences of two tokens, 8 kv heads: 43 -> 31 us with the mask's prefetch and
+          // no ranking); converters write zeros there at no cost, and a branch a step costs 2 %
+          if (Q8 || kk * 16 < left)
+            mma_ts(tm_o, a_p + kk * 8 + (kk / (CH / 16)) * (CH / 2), sdesc_add(vd, kk * (2 * kRG)), idesc_o,
+                   (jj > 0 || kk > 0) ? 1u : 0u);
         tc_commit(bar_pv(buf));
         tc_commit(bar_ve(stage));
       }
@@ -719,6 +724,7 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
     row.words = nullptr;
     if (p.mask && active)
       row.words = p.mask + (static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T + i) * p.words;
+    if (row.words) prefetch_l1(row.words);
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     float m_run = -INFINITY, l_run = 0.f;
     // a > 0 goes into the exponential's argument; otherwise the scores are scaled first
@@ -811,7 +817,8 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
         const uint32_t vst = sV + stage * L::kKVBytes;
         const int r0 = max(0, ctx - key0);
         constexpr int kChunks = D / 8;  // 16-byte chunks a row
-        for (int u = (half * live_warps + wq) * 32 + lane; u < (BN - r0) * kChunks; u += team) {
+        const int r1 = min(BN, (Lkv - key0 + 15) & ~15);  // rows that P V reads
+        for (int u = (half * live_warps + wq) * 32 + lane; u < (r1 - r0) * kChunks; u += team) {
           const int vr = r0 + u / kChunks, c = u % kChunks;
           const uint32_t at = vst + (vr / 8) * kRG + (c / 8) * kCB + (vr % 8) * 128 + (c % 8) * 16;
           const int d = key0 + vr - ctx;
@@ -1210,6 +1217,11 @@ int fa_tree_decode_paged(const fa_tree_args* a, void* stream) {
   p.num_pages = a->num_pages;
   p.scale_log2 = a->scale * 1.44269504088896340736f;
   p.status = status;
+  // the order matters where blocks wait for others to end and their lengths can differ by much
+  const long units = static_cast<long>(pl.n_splits) * (pl.few_rows ? 1 : pl.n_qtiles) * a->Hkv * a->B;
+  const long places = static_cast<long>(num_sms() > 0 ? num_sms() : 152) *
+                      (pl.few_rows ? tree_rows_ctas(a->D, pl.G * a->T) : 1);
+  p.ranked = units > places && a->max_seq_len > 512;
   if (pl.n_splits > 1) {
     p.o_part = static_cast<float*>(a->workspace);
     p.lse_part = reinterpret_cast<float*>(static_cast<uint8_t*>(a->workspace) + pl.off_lse);

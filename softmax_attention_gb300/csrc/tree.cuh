@@ -30,6 +30,7 @@ struct TreeParams {
   int B, Hq, Hkv, G, T;
   int q_per_tile, n_qtiles, n_splits;
   int page_size, page_shift, max_pages, num_pages;
+  int ranked;                   // blocks take the sequences in decreasing length
   float scale_log2;
   uint32_t* status;
 };
@@ -127,13 +128,18 @@ __device__ __forceinline__ uint32_t widen2_hi(uint32_t codes) {
   return r;
 }
 
+// Starts a row's mask words on their way to L1: the tiles that look at them come last.
+__device__ __forceinline__ void prefetch_l1(const void* at) {
+  asm volatile("prefetch.global.L1 [%0];" ::"l"(at));
+}
+
 // The sequence that is `rank`-th in decreasing length (ties by index), so that the last blocks to
-// start are short ones; past THREADS sequences the rank is the sequence.  All threads of the
-// block must call.
+// start are short ones; past THREADS sequences, and where the order cannot matter (!p.ranked), the
+// rank is the sequence.  All threads of the block must call.
 template <int THREADS>
 __device__ __forceinline__ int sequence_of_rank(const TreeParams& p, int rank) {
   __shared__ int found;
-  if (p.B == 1 || p.B > THREADS) return rank;
+  if (!p.ranked || p.B == 1 || p.B > THREADS) return rank;
   if (threadIdx.x < p.B) {
     const int mine = p.kv_lens[threadIdx.x];
     int before = 0;

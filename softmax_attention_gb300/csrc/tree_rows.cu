@@ -140,6 +140,10 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, NT>::kCtas)
     n_draft = 0;
   }
   const int ctx = Lkv - n_draft;
+  if (p.mask && n_draft > 0) {
+    const uint64_t* words = p.mask + static_cast<int64_t>(p.mask_batches == 1 ? 0 : b) * p.T * p.words;
+    for (int i = threadIdx.x * 16; i < p.T * p.words; i += kThreads * 16) prefetch_l1(words + i);
+  }
   const int n_slices = n_draft > 0 ? (Lkv + SL - 1) / SL : 0;
   const int per_split = (n_slices + p.n_splits - 1) / p.n_splits;
   const int s_begin = min(n_slices, split * per_split) + warp;
