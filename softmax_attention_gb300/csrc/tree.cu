@@ -24,6 +24,12 @@
 // scaled by powers of two into fp16 (exact down to 2^-32 of a row's maximum, undone in the
 // scores), and both products run in fp16.  Otherwise they run in bf16, which holds any scale.
 //
+// Measured (D = 128, 8 kv heads of four query heads, even sequences of 8192 tokens, 16-token
+// pages): 16-bit cache, 32 drafted tokens of 19 sequences 103 us, 6.2 TB/s, bound by memory; 64 of
+// them, two tiles a sequence, 141 us.  8-bit cache 96 and 182 us: a KV tile takes some 2450 clocks
+// of converters (730 for K, 780 for V and the waits between) and softmax warps (2000 of them) side
+// by side at half of the issue slots.
+//
 // Warp roles: 0-3 and the last four softmax + epilogue (a row of scores is shared by two
 // threads), 4 TMA producer, 5 P V issuer and tensor-memory owner, 6 S issuer, and for 8-bit pages 7
 // second TMA producer, 8-11 converters.

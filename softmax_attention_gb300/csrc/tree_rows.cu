@@ -11,7 +11,7 @@
 // fill their tile; nine to sixteen take two (NT).  With q as the 16-row operand a decode step's
 // matrix, exponential and O instructions were half empty: 718 instructions a warp and 32 tokens
 // and three CTAs of 166 registers an SM, where this takes 126 registers and four CTAs (128
-// sequences of 1K to 4K tokens: 135 -> 110 us, 6.0 TB/s or 0.88 of a copy; the 57 even ones 87 ->
+// sequences of 1K to 4K tokens: 135 -> 110 us, 6.2 TB/s or 0.92 of a copy; the 57 even ones 87 ->
 // 83 us).  Two tiles lose one or two per cent to the transposition of the weights.
 //
 // Each warp runs alone: its own ring of slices (SL tokens of K and of V), its own barriers, its
