@@ -455,3 +455,52 @@ def test_graph_replay_and_two_streams():
     torch.cuda.synchronize()
     for a, b in got:
         assert torch.equal(a[0], eager[0]) and torch.equal(b[0], want2[0])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,T", [(8, 1), (9, 1), (4, 2), (3, 3), (16, 1), (5, 3), (17, 1)])
+def test_eight_rows_and_the_next(D, G, T):
+    """Rows (query heads of a kv head times drafted tokens) around one and two tiles of eight,
+    lengths around a slice, long enough for several slices a warp."""
+    lens = [T, 33, 300, 16 + T]
+    pr = Problem(len(lens), 2 * G, 2, T, D, 16, BF16, E4M3, lens, scales=(100, 140))
+    masks = [random_tree(T, random.Random(G + b)) for b in range(len(lens))]
+    args, kw = pr.gpu()
+    for splits in (1, 2):
+        out, lse = fa.fa_tree_decode_paged(*args, tree_mask=pack(masks, T).cuda(), num_splits=splits, **kw)
+        ref.check_tree(out, lse, pr.want([T] * len(lens), masks, D ** -0.5), BF16, D, f"G={G} T={T} {splits}")
+
+
+@pytest.mark.parametrize("D,G,T", [(128, 2, 3), (128, 4, 4), (64, 3, 5), (256, 4, 2), (256, 5, 3)])
+def test_padding_queries_of_few_rows(D, G, T):
+    """What the queries of padding rows hold (NaN, infinities, the largest values) changes no bit
+    of the other rows, whose weights share their blocks' arithmetic."""
+    pr = Problem(2, 2 * G, 2, T, D, 16, BF16, E4M3, [700, 77])
+    (q, *rest), kw = pr.gpu()
+    drafts = torch.tensor([1, T - 1], dtype=torch.int32, device="cuda")
+    good = fa.fa_tree_decode_paged(q, *rest, draft_lens=drafts, num_splits=1, **kw)
+    for bad in (math.nan, math.inf, 3e38, 0.0):
+        q[0, :, 1:] = bad
+        q[1, :, T - 1:] = bad
+        out, lse = fa.fa_tree_decode_paged(q, *rest, draft_lens=drafts, num_splits=1, **kw)
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (FP16, FP16), (BF16, E4M3)])
+@pytest.mark.parametrize("D,G,T,ps", [(128, 5, 1, 32), (128, 4, 2, 8), (64, 2, 1, 8), (256, 4, 1, 64), (128, 4, 9, 16), (64, 33, 1, 16)])
+def test_short_sequences(dtype, cache, D, G, T, ps):
+    """Lengths around every step of 16 tokens and a tile; NaN in every slot past a sequence's end
+    and in pages that no sequence has."""
+    lens = [n for n in (1, 2, 15, 16, 17, 31, 33, 48, 63, 64, 65, 127, 128, 129, 145) if n >= T]
+    pr = Problem(len(lens), 2 * G, 2, T, D, ps, dtype, cache, lens)
+    used = torch.zeros(pr.k.shape[0], ps, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for j in range(n):
+            used[pr.table[b, j // ps], j % ps] = True
+    nan = 0x7f if cache == E4M3 else math.nan
+    past = (~used)[:, None, :, None].expand(pr.k.shape)
+    pr.k[past], pr.v[past] = nan, nan
+    masks = [random_tree(T, random.Random(b)) for b in range(len(lens))]
+    args, kw = pr.gpu()
+    out, lse = fa.fa_tree_decode_paged(*args, tree_mask=pack(masks, T).cuda(), **kw)
+    ref.check_tree(out, lse, pr.want([T] * len(lens), masks, D ** -0.5), dtype, D)
