@@ -494,8 +494,10 @@ int fa_cache_gather(const fa_cache_gather_args* args, void* stream);
  *     last dimension contiguous) positive multiples of 16 bytes
  *   k_pages, v_pages [num_pages, Hkv, page_size, D] in cache_dtype: dtype, or FA_E4M3 with the
  *     scales [num_pages, Hkv, page_size] that fa_cache_append writes (a value is e4m3 *
- *     2^(byte - 127), bytes 1 to 254; with bf16 queries exact; with fp16 queries a value
- *     beyond 65504 may become infinite and one below 2^-14 may be rounded to fp16)
+ *     2^(byte - 127), bytes 1 to 254).  Up to 16 rows (Hq / Hkv * T) take every value as it is.
+ *     More rows: with bf16 queries a value of 2^128 or more is taken as bf16's largest and one
+ *     is rounded below 2^-133; with fp16 queries a value beyond 131008 is taken as 131008, and
+ *     values of a row of scale below 2^-14 are rounded to multiples of 2^-23
  *   page_table [B, max_pages] int32; seq_lens [B] int32, the drafted tokens included, each at
  *     most max_seq_len (which sizes the KV split); draft_lens [B] int32 or NULL (= T each)
  *   tree_mask [mask_batches, T, ceil(T / 64)] 64-bit words, mask_batches 1 or B; NULL = a

@@ -24,6 +24,12 @@
 // scaled by powers of two into fp16 (exact down to 2^-32 of a row's maximum, undone in the
 // scores), and both products run in fp16.  Otherwise they run in bf16, which holds any scale.
 //
+// Values beyond the operand type.  fp16 queries meet K and V at half their size (undone in the
+// scores and in the sum that O is divided by): all that fp16 rows are ever stored as, up to 65536 =
+// 256 * 2^8, then fits, and a row of scale 2^-14 or more is exact.  What does not fit (fp16 from
+// scale byte 136 on, bf16 at 2^128) is held at the operand's largest value, never as an infinity,
+// which a weight of 0 would turn into NaN in rows that do not see the token.
+//
 // Measured (D = 128, 8 kv heads of four query heads, even sequences of 8192 tokens, 16-token
 // pages): 16-bit cache, 32 drafted tokens of 19 sequences 103 us, 6.2 TB/s, bound by memory; 64 of
 // them, two tiles a sequence, 141 us.  8-bit cache 96 and 182 us: a KV tile takes some 2450 clocks
@@ -314,23 +320,34 @@ __device__ __forceinline__ float q_row_to_fp16(uint32_t tile, int r) {
   return __uint_as_float(static_cast<uint32_t>(127 + eq) << 23);
 }
 
+// Least scale byte of a row whose widened values can overflow the operand type: 448 times the scale
+// is 448 * 2^8 in fp16 (fp16 queries, at half size; for bf16 ones every byte is below), 1.75 * 2^128 in
+// bf16.
+__device__ __forceinline__ uint32_t overflow_byte(bool f16) { return f16 ? 136 : 247; }
+
 // NaN codes of a raw row (rare): NaN in the stage, or, in a drafted token's V, zero, the token
-// noted: a weight of 0 would still carry a NaN into rows that do not see the token.
+// noted: a weight of 0 would still carry a NaN into rows that do not see the token.  Where the row
+// can have overflowed (`over`), its infinities become the operand type's largest value.
 template <int D, int kParts>
-__device__ __noinline__ void patch_nan(uint32_t raw, uint32_t raw_blk, uint32_t raw_swz, uint32_t dst,
-                                       int row, int part, int draft, uint32_t* poison) {
+__device__ __noinline__ void patch_row(uint32_t raw, uint32_t raw_blk, uint32_t raw_swz, uint32_t dst,
+                                       int row, int part, int draft, uint32_t* poison, bool over, bool f16) {
   constexpr int kIn = D < 128 ? D : 128, kChunks = D / 16 / kParts;
   for (int c = part * kChunks; c < (part + 1) * kChunks; ++c) {
     const int blk = c / (kIn / 16), ci = c % (kIn / 16);
     const uint4 x = lds128(raw + blk * raw_blk + ((ci ^ raw_swz) * 16));
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    if (!(nan_mark(nan_mark(nan_mark(nan_mark(0, x.x), x.y), x.z), x.w) & 0x80808080u)) continue;
+    if (!over && !(nan_mark(nan_mark(nan_mark(nan_mark(0, x.x), x.y), x.z), x.w) & 0x80808080u)) continue;
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      if (((w[e / 4] >> (8 * (e % 4))) & 0x7fu) != 0x7fu) continue;
       const int ch = (c % 4) * 2 + e / 8;
-      sts16(dst + (c / 4) * 1024 + ((ch ^ (row & 7)) * 16) + (e % 8) * 2, draft >= 0 ? 0 : 0x7fff);
-      if (draft >= 0) atomicOr(&poison[draft >> 5], 1u << (draft & 31));
+      const uint32_t at = dst + (c / 4) * 1024 + ((ch ^ (row & 7)) * 16) + (e % 8) * 2;
+      if (((w[e / 4] >> (8 * (e % 4))) & 0x7fu) == 0x7fu) {
+        sts16(at, draft >= 0 ? 0 : 0x7fff);
+        if (draft >= 0) atomicOr(&poison[draft >> 5], 1u << (draft & 31));
+      } else if (over) {
+        const uint32_t h = lds16(at);
+        if (nonfinite16(h, !f16)) sts16(at, (h & 0x8000u) | (f16 ? 0x7bffu : 0x7f7fu));
+      }
     }
   }
 }
@@ -431,7 +448,7 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
         const int draft = v && key >= ctx ? key - ctx : -1;
         uint32_t marks;
         if (f16) {
-          const RowScale s = row_scale<false>(byte);
+          const RowScale s = row_scale<false>(BF16 ? byte : byte - 1);  // fp16 queries: half size
           // fp16 stands in for bf16 only where one factor holds every scale
           if (!BF16 && s.two) marks = widen_row<D, kParts, false, true>(raw, raw_blk, raw_swz, dst, row, part, s);
           else marks = widen_row<D, kParts, false, false>(raw, raw_blk, raw_swz, dst, row, part, s);
@@ -440,8 +457,9 @@ __device__ __forceinline__ void convert_tiles(const TreeParams& p, bool f16, con
           if (s.two) marks = widen_row<D, kParts, true, true>(raw, raw_blk, raw_swz, dst, row, part, s);
           else marks = widen_row<D, kParts, true, false>(raw, raw_blk, raw_swz, dst, row, part, s);
         }
-        if ((marks & 0x80808080u) || draft >= 0)
-          patch_nan<D, kParts>(raw, raw_blk, raw_swz, dst, row, part, draft, poison);
+        const bool over = byte >= overflow_byte(f16);
+        if ((marks & 0x80808080u) || draft >= 0 || over)
+          patch_row<D, kParts>(raw, raw_blk, raw_swz, dst, row, part, draft, poison, over, f16);
       }
       fence_proxy_async_smem();
       mbar_arrive(g.empty + 8u * rs);
@@ -735,7 +753,9 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
     float m_run = -INFINITY, l_run = 0.f;
     // a > 0 goes into the exponential's argument; otherwise the scores are scaled first
     const bool pre = !(p.scale_log2 > 0.f);
-    float to_log2 = p.scale_log2;
+    // K and V at half size (see convert_tiles)
+    constexpr float kUnhalve = Q8 && !BF16 ? 2.f : 1.f;
+    float to_log2 = p.scale_log2 * kUnhalve;
     // A wait that runs out leaves ok false: no more work, but every barrier is still met.
     bool ok = true;
     if constexpr (Q8 && BF16) {
@@ -864,7 +884,7 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
       // the K ring (free: every MMA has finished) with 16-byte chunks swizzled by the row, then
       // written out as whole 128-byte runs, eight lanes a row.
       const bool have = active && n > 0 && !(l_run == 0.f);  // a NaN sum stays NaN
-      const float inv_l = 1.f / l_run;
+      const float inv_l = kUnhalve / l_run;
       bool any_poison = false;
       if (n > 0) {
         for (int w = 0; w < kMaxTree / 32; ++w) any_poison |= poison[w] != 0;

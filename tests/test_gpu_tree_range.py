@@ -1,0 +1,110 @@
+"""GPU checks of the tree attention at the ends of its ranges: cache values beyond the operand
+type's, against the 64-bit evaluation of tests/_cache_ref.py."""
+import math
+import random
+
+import pytest
+import torch
+
+import softmax_attention_gb300 as fa
+from tests import _cache_ref as ref
+from tests.test_gpu_tree import BF16, E4M3, FP16, Problem, pack, random_tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    fa.load_library()
+    yield
+    assert fa.fa_get_device_status() == fa.FA_OK, fa.fa_last_error()
+
+
+def rows_at(x, i):
+    return tuple(t[:, :, i] for t in x)
+
+
+@pytest.mark.parametrize("dtype,byte", [(FP16, 135), (FP16, 150), (FP16, 254), (BF16, 247), (BF16, 254)])
+@pytest.mark.parametrize("T,splits", [(4, 1), (24, 1), (24, 3), (70, 1)])
+@pytest.mark.parametrize("chain", [True, False])
+def test_hidden_values_beyond_the_operand_type(dtype, byte, T, splits, chain):
+    """A drafted token whose V (code 448 times its scale) is beyond fp16, or beyond bf16: rows
+    that do not see it are bit for bit what they are with its codes at zero."""
+    pr = Problem(1, 4, 2, T, 128, 16, dtype, E4M3, [300])
+    mask = torch.ones(T, T, dtype=torch.bool).tril() if chain else random_tree(T, random.Random(T))
+    if not chain:
+        mask[:, 2] = False
+        mask[2, 2] = mask[T - 1, 2] = True
+    hidden = ~mask[:, 2]
+    at = 300 - T + 2
+    pg, sl = int(pr.table[0, at // 16]), at % 16
+    pr.vs[pg, :, sl] = byte
+    pr.v[pg, :, sl] = 0
+    words = None if chain else pack([mask], T).cuda()
+
+    def call():
+        args, kw = pr.gpu()
+        return fa.fa_tree_decode_paged(*args, tree_mask=words, num_splits=splits, **kw)
+
+    without = call()
+    want = pr.want([T], [mask], 128 ** -0.5)
+    pr.v[pg, :, sl, ::2] = 0x7E  # 448
+    pr.v[pg, :, sl, 1::2] = 0xFE
+    out, lse = call()
+    i = hidden.cuda()
+    assert torch.equal(out[:, :, i], without[0][:, :, i]) and torch.equal(lse, without[1])
+    ref.check_tree(out[:, :, i], lse[:, :, i], rows_at(want, hidden), dtype, 128)
+
+
+@pytest.mark.parametrize("T", [4, 24])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_the_largest_fp16_keys_and_values(T, D):
+    """fp16's largest value in K and V, written by the library (stored as 256 * 2^8 = 65536):
+    finite results, whether the token's weight counts, is negligible or is hidden."""
+    g = torch.Generator().manual_seed(T + D)
+    Hq, Hkv, ps, n = 4, 2, 16, 200
+    P = -(-n // ps)
+    k, v = (torch.randn(1, Hkv, n, D, generator=g) * 0.5 for _ in range(2))
+    q = torch.randn(1, Hq, T, D, generator=g) * 0.5
+    q[..., 3] = (torch.rand(1, Hq, T, generator=g) - 0.5) * 2.0 ** -10
+    q[..., 5] = 4.0
+    k[0, :, 11, 3] = 65504.0            # a key whose score is moderate
+    v[0, :, 20] = 65504.0               # a value that counts
+    k[0, :, 30, 5] = -40.0 * math.sqrt(D)   # a weight of about e^-160, with such a value
+    v[0, :, 30, ::2] = -65504.0
+    v[0, :, n - T + 1, 1::2] = 65504.0  # a drafted one, which row 0 does not see
+    k[0, :, n - T + 1, 5] = -2.0 * math.sqrt(D)
+    q, k, v = q.to(FP16), k.to(FP16), v.to(FP16)
+    table = ref.make_table([n], ps, P, g).cuda()
+    lens = torch.tensor([n], dtype=torch.int32).cuda()
+    kp = torch.zeros(P, Hkv, ps, D, dtype=torch.uint8, device="cuda").view(E4M3)
+    ks = torch.zeros(P, Hkv, ps, dtype=torch.uint8, device="cuda")
+    vp, vs = kp.clone(), ks.clone()
+    fa.fa_cache_append(k.cuda(), v.cuda(), kp, vp, table, lens, k_scales=ks, v_scales=vs)
+    dk, dv = fa.fa_cache_gather(kp, vp, table, lens, n, dtype=torch.float32, k_scales=ks, v_scales=vs)
+    assert dk.abs().max() == 65536 and dv.abs().max() == 65536
+    out, lse = fa.fa_tree_decode_paged(q.cuda(), kp, vp, table, lens, n, k_scales=ks, v_scales=vs)
+    rows = [[t[0].double().cpu().transpose(0, 1)] for t in (dk, dv)]
+    want = ref.tree_attention(q, rows[0], rows[1], [T], None, D ** -0.5)
+    assert want[0].abs().max() < 65504
+    ref.check_tree(out, lse, want, FP16, D)
+
+
+def test_seen_values_beyond_the_operand_type():
+    """Seen by a row, a value beyond the fp16 operand counts as the operand's largest, 131008, in
+    the 128-row kernel and as itself in the kernel for few rows."""
+    for T, most in ((4, math.inf), (24, 131008.0)):
+        pr = Problem(1, 4, 2, T, 128, 16, FP16, E4M3, [300])
+        for t in (7, 299):  # of the context, and the last drafted token
+            pg, sl = int(pr.table[0, t // 16]), t % 16
+            pr.vs[pg, :, sl] = 139
+            pr.v[pg, :, sl, ::2] = 0x7E   # 448 * 2^12
+            pr.v[pg, :, sl, 1::2] = 0xC0  # -2 * 2^12
+            pr.ks[pg, :, sl] = 127
+            pr.k[pg, :, sl] = 0           # a weight of some 1 / 300
+        args, kw = pr.gpu()
+        out, lse = fa.fa_tree_decode_paged(*args, **kw)
+        k, v = pr.rows(0)
+        want = ref.tree_attention(pr.q, [k], [v.clamp(-most, most)], [T], None, 128 ** -0.5)
+        assert want[0].abs().max() < 65504
+        ref.check_tree(out, lse, want, FP16, 128, f"T={T}")
