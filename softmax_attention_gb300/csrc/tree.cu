@@ -261,7 +261,8 @@ __device__ __forceinline__ bool scales_leave_fp16(const TreeParams& p, int looke
     for (int u = 0; u < kBatch; ++u) {
       const int key = key0 + u * THREADS * 8;
       k[u] = v[u] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      const bool take = static_cast<uint32_t>(page[u]) < static_cast<uint32_t>(p.num_pages);
+      const bool take = key < last;
+      if (static_cast<uint32_t>(page[u]) >= static_cast<uint32_t>(p.num_pages)) page[u] = 0;  // as it is read
       const int64_t at = ((static_cast<int64_t>(page[u]) * p.Hkv + hk) << p.page_shift) + (key & (p.page_size - 1));
       if (take) k[u] = __ldg(reinterpret_cast<const uint2*>(p.k_scales + at));
       if (take) v[u] = __ldg(reinterpret_cast<const uint2*>(p.v_scales + at));

@@ -84,8 +84,8 @@ __device__ __forceinline__ bool nonfinite16(uint32_t h, bool bf16) {
 // that sees a drafted token with such a value.
 template <int D, bool BF16, bool Q8>
 __device__ __noinline__ float nonfinite_v(const TreeParams& p, int b, int hk, int key, int c) {
-  const int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + (key >> p.page_shift)];
-  if (page < 0 || page >= p.num_pages) return 0.f;
+  int page = p.page_table[static_cast<int64_t>(b) * p.max_pages + (key >> p.page_shift)];
+  if (page < 0 || page >= p.num_pages) page = 0;  // as the copies read it
   const int64_t at = ((static_cast<int64_t>(page) * p.Hkv + hk) * p.page_size + (key & (p.page_size - 1))) * D + c;
   if constexpr (Q8) {
     const uint32_t v = static_cast<const uint8_t*>(p.v_pages)[at];

@@ -1,5 +1,5 @@
 """GPU checks of the tree attention at the ends of its ranges: cache values beyond the operand
-type's, against the 64-bit evaluation of tests/_cache_ref.py."""
+type's, lengths and page ids out of range; against the 64-bit evaluation of tests/_cache_ref.py."""
 import math
 import random
 
@@ -108,3 +108,46 @@ def test_seen_values_beyond_the_operand_type():
         want = ref.tree_attention(pr.q, [k], [v.clamp(-most, most)], [T], None, 128 ** -0.5)
         assert want[0].abs().max() < 65504
         ref.check_tree(out, lse, want, FP16, 128, f"T={T}")
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, E4M3), (FP16, E4M3), (BF16, BF16)])
+@pytest.mark.parametrize("T", [3, 20])
+def test_bad_lengths_and_pages_of_both_kernels(dtype, cache, T):
+    """Lengths and page ids out of range in the kernel for few rows and the 128-row one: the
+    status is set, the sequences with a bad length are empty, a bad page stands for page 0 with
+    its own scales (here outside what fp16 operands take for bf16 queries), the rest is as it was."""
+    pr = Problem(4, 4, 2, T, 64, 16, dtype, cache, [40, 40, 40, 40])
+    spare = next(i for i in range(1, pr.k.shape[0]) if not (pr.table == i).any())
+    pr.table[pr.table == 0] = spare  # no sequence has page 0
+    pr.v[0, :, (40 - T // 2) % 16, 3] = 0x7F if cache == E4M3 else math.nan  # of a drafted token, too
+    if cache == E4M3:
+        pr.vs[0, :, ::2] = 105
+        if dtype == BF16:
+            pr.vs[0, :, 1::2] = 150
+    scale = 0.125
+    (q, k, v, table, lens, L), kw = pr.gpu()
+    good, _ = fa.fa_tree_decode_paged(q, k, v, table, lens, L, **kw)
+    lens2 = lens.clone()
+    lens2[1], lens2[2] = T - 1, 10 ** 6
+    out, lse = fa.fa_tree_decode_paged(q, k, v, table, lens2, L, **kw)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BOUNDS
+    assert not out[1:3].any() and (lse[1:3] == -math.inf).all()
+    assert torch.equal(out[0], good[0]) and torch.equal(out[3], good[3])
+    lens2[1], lens2[2] = -1, -2 ** 31
+    out, lse = fa.fa_tree_decode_paged(q, k, v, table, lens2, L, **kw)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BOUNDS
+    assert not out[1:3].any() and torch.equal(out[0], good[0]) and torch.equal(out[3], good[3])
+    drafts = torch.tensor([T, T + 1, -1, 0], dtype=torch.int32).cuda()
+    out, lse = fa.fa_tree_decode_paged(q, k, v, table, lens, L, draft_lens=drafts, **kw)
+    assert fa.fa_get_device_status() == fa.FA_ERR_BOUNDS
+    assert torch.equal(out[0], good[0]) and not out[1:].any() and (lse[1:] == -math.inf).all()
+    for bad in (10 ** 6, -5, pr.k.shape[0]):
+        table2 = table.clone()
+        table2[1, 1] = table2[2, 2] = bad
+        out, lse = fa.fa_tree_decode_paged(q, k, v, table2, lens, L, **kw)
+        assert fa.fa_get_device_status() == fa.FA_ERR_BOUNDS
+        assert torch.equal(out[0], good[0]) and torch.equal(out[3], good[3])
+        keep = pr.table.clone()
+        pr.table[1, 1] = pr.table[2, 2] = 0
+        ref.check_tree(out, lse, pr.want([T] * 4, None, scale), dtype, 64, f"page {bad}")
+        pr.table = keep
