@@ -39,6 +39,7 @@
 // Warp roles: 0-3 and the last four softmax + epilogue (a row of scores is shared by two
 // threads), 4 TMA producer, 5 P V issuer and tensor-memory owner, 6 S issuer, and for 8-bit pages 7
 // second TMA producer, 8-11 converters.
+#include <float.h>
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -775,7 +776,11 @@ __global__ void __launch_bounds__(Layout<D, BN, STAGES, RAW, Q8>::kThreads, 1)
       const int buf = jj % kNumS;
       const uint32_t t_s = tm_s0 + lane_off + buf * BN;
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_s(buf), (jj / kNumS) & 1, p.status));
-      if (Q8 && BF16 && f16 && jj == 0) to_log2 *= q_factor;  // written before S_0 could be issued
+      if (Q8 && BF16 && f16 && jj == 0) {
+        to_log2 *= q_factor;  // written before S_0 could be issued
+        // never 0, which a hidden score's -inf would turn into NaN; scores are below 2^39 here
+        if (!pre) to_log2 = fmaxf(to_log2, FLT_MIN);
+      }
       const float a = pre ? 1.f : to_log2;
       const int key0 = (t_begin + jj) * BN;
       uint32_t raw[CH];

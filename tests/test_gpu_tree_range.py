@@ -1,5 +1,6 @@
 """GPU checks of the tree attention at the ends of its ranges: cache values beyond the operand
-type's, lengths and page ids out of range; against the 64-bit evaluation of tests/_cache_ref.py."""
+type's, lengths and page ids out of range, scores that vanish; against the 64-bit evaluation of
+tests/_cache_ref.py."""
 import math
 import random
 
@@ -151,3 +152,18 @@ def test_bad_lengths_and_pages_of_both_kernels(dtype, cache, T):
         pr.table[1, 1] = pr.table[2, 2] = 0
         ref.check_tree(out, lse, pr.want([T] * 4, None, scale), dtype, 64, f"page {bad}")
         pr.table = keep
+
+
+@pytest.mark.parametrize("T", [3, 20])
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+def test_tiny_queries_and_score_scale(T, dtype):
+    """Scores that vanish (q near 2^-105, or fp16's least, times a scale of 2^-45): every seen token
+    weighs the same, hidden ones nothing."""
+    pr = Problem(1, 4, 2, T, 128, 16, dtype, E4M3, [300])
+    if dtype == BF16:
+        pr.q = (pr.q.float() * 2.0 ** -105).to(BF16)
+    else:
+        pr.q = (pr.q.float() * 2.0 ** -20).to(FP16)
+    args, kw = pr.gpu()
+    out, lse = fa.fa_tree_decode_paged(*args, scale=2.0 ** -45, **kw)
+    ref.check_tree(out, lse, pr.want([T], None, 2.0 ** -45), dtype, 128)
