@@ -249,20 +249,22 @@ __device__ __forceinline__ bool scales_leave_fp16(const TreeParams& p, int looke
   constexpr int kBatch = 4;
   const int32_t* table = p.page_table + static_cast<int64_t>(b) * p.max_pages;
   bool outside = false;
-  for (int key0 = first + looker * 8; key0 < last; key0 += THREADS * 8 * kBatch) {
+  // unsigned: the last step's keys may pass 2^31
+  const uint32_t end = static_cast<uint32_t>(last);
+  for (uint32_t key0 = static_cast<uint32_t>(first + looker * 8); key0 < end; key0 += THREADS * 8 * kBatch) {
     int page[kBatch];
     uint2 k[kBatch], v[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int key = key0 + u * THREADS * 8;
-      page[u] = key < last ? __ldg(table + (key >> p.page_shift)) : -1;
+      const uint32_t key = key0 + u * THREADS * 8;
+      page[u] = key < end ? __ldg(table + (key >> p.page_shift)) : -1;
     }
     asm volatile("" : "+r"(page[0]), "+r"(page[1]), "+r"(page[2]), "+r"(page[3]));
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int key = key0 + u * THREADS * 8;
+      const uint32_t key = key0 + u * THREADS * 8;
       k[u] = v[u] = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);
-      const bool take = key < last;
+      const bool take = key < end;
       if (static_cast<uint32_t>(page[u]) >= static_cast<uint32_t>(p.num_pages)) page[u] = 0;  // as it is read
       const int64_t at = ((static_cast<int64_t>(page[u]) * p.Hkv + hk) << p.page_shift) + (key & (p.page_size - 1));
       if (take) k[u] = __ldg(reinterpret_cast<const uint2*>(p.k_scales + at));
@@ -273,7 +275,7 @@ __device__ __forceinline__ bool scales_leave_fp16(const TreeParams& p, int looke
       asm volatile("" : "+r"(k[u].x), "+r"(k[u].y), "+r"(v[u].x), "+r"(v[u].y));
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int left = last - (key0 + u * THREADS * 8);  // tokens from this step's first on
+      const int left = static_cast<int>(end - (key0 + u * THREADS * 8));  // tokens from this step's first on
       const uint32_t w[4] = {k[u].x, k[u].y, v[u].x, v[u].y};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {

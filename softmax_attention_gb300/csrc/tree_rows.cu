@@ -170,8 +170,9 @@ __global__ void __launch_bounds__(kThreads, RowsLayout<D, NT>::kCtas)
   // Page id of token `lane` of this warp's slice k (0 past the end), as the table has it; checked
   // where it is first used, so that nothing waits for the load.
   auto token_page = [&](int k) {
+    if (lane >= SL || k >= n) return 0;  // (a slice past the last one may pass 2^31)
     const int key = (s_begin + k * kWarps) * SL + lane;
-    return lane < SL && k < n && key < Lkv ? __ldg(table + (key >> p.page_shift)) : 0;
+    return key < Lkv ? __ldg(table + (key >> p.page_shift)) : 0;
   };
   auto checked = [&](int id) {
     if (id >= 0 && id < p.num_pages) return id;

@@ -1,6 +1,6 @@
 """GPU checks of the tree attention at the ends of its ranges: cache values beyond the operand
-type's, lengths and page ids out of range, scores that vanish; against the 64-bit evaluation of
-tests/_cache_ref.py."""
+type's, lengths and page ids out of range, scores that vanish, the longest sequence; against
+the 64-bit evaluation of tests/_cache_ref.py."""
 import math
 import random
 
@@ -167,3 +167,25 @@ def test_tiny_queries_and_score_scale(T, dtype):
     args, kw = pr.gpu()
     out, lse = fa.fa_tree_decode_paged(*args, scale=2.0 ** -45, **kw)
     ref.check_tree(out, lse, pr.want([T], None, 2.0 ** -45), dtype, 128)
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_the_longest_sequence(T):
+    """max_pages * page_size as large as the call takes, over four pages that the table repeats:
+    token counts next to 2^31 in both 8-bit kernels.  Keys of 0, so that every token weighs the same;
+    V is 1, 2, 3 or 4 throughout a page.  Sums of such values are exact in fp32 here (a step of 16
+    tokens adds a multiple of 2^11 below 2^33), so the output is the mean, rounded once after a
+    merge of up to 608 parts (each of whose weights is off by 2^-19, its lse being near 2^4)."""
+    ps, D = 64, 64
+    pages = (2 ** 31 - 257) // ps
+    n = pages * ps
+    kp = torch.zeros(4, 1, ps, D, dtype=torch.uint8, device="cuda").view(E4M3)
+    vp = torch.arange(1, 5, device="cuda").view(4, 1, 1, 1).expand(4, 1, ps, D).to(torch.float32).to(E4M3).contiguous()
+    ks = torch.full((4, 1, ps), 127, dtype=torch.uint8, device="cuda")
+    table = (torch.arange(pages, dtype=torch.int32, device="cuda") % 4)[None].contiguous()
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 1, T, D, device="cuda").to(BF16)
+    out, lse = fa.fa_tree_decode_paged(q, kp, vp, table, lens, n, k_scales=ks, v_scales=ks)
+    torch.cuda.synchronize()
+    assert (out.float() - 2.5).abs().max() <= 2.5 * (2.0 ** -8 + 2.0 ** -17)
+    assert (lse.double() - math.log(n)).abs().max() <= 2.0 ** -17
