@@ -368,7 +368,8 @@ size_t gated_delta_workspace_size(const gated_delta_args* args);
  *   q [B, Hq, T, D], k [B, Hk, T, D] in dtype (FA_BF16, FA_FP16, FA_FP32), any strides (in
  *   elements: batch, head, token; the last dimension is contiguous) that are multiples of 16
  *   bytes; q_out, k_out likewise, and may be the inputs themselves (same pointer and strides);
- *   any other overlap is not allowed;
+ *   any other overlap is not allowed (inputs may be broadcast, with strides of 0; an output
+ *   may not);
  *   positions [B, T] int32;  inv_freq [rot_dim / 2] fp64 (scaled frequencies for long contexts
  *   are the caller's table, their amplitude the argument): the angle is reduced exactly, so
  *   positions may be as large as int32 holds.

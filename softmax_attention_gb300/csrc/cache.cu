@@ -412,6 +412,14 @@ bool strides_ok(const int64_t* s, fa_dtype t) {
   return s[0] % m == 0 && s[1] % m == 0 && s[2] % m == 0;
 }
 
+// Whether rows of an output [n0, n1, n2, D] are written over one another: neighbours closer than D.
+bool rows_overlap(const int64_t* s, int n0, int n1, int n2, int D) {
+  const int n[3] = {n0, n1, n2};
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && s[i] < D && s[i] > -D) return true;
+  return false;
+}
+
 int check_rot(const char* who, int rot_dim, int D) {
   char msg[200];
   if (rot_dim <= 0 || rot_dim % 16 != 0 || rot_dim > D || rot_dim > kMaxRot) {
@@ -545,6 +553,9 @@ int fa_rotary(const fa_rotary_args* a, void* stream) {
   if (!strides_ok(a->q_strides, a->dtype) || !strides_ok(a->k_strides, a->dtype) ||
       !strides_ok(a->q_out_strides, a->dtype) || !strides_ok(a->k_out_strides, a->dtype))
     return bad(FA_ERR_INVALID_ARG, "fa_rotary: strides must be multiples of 16 bytes");
+  if ((a->Hq > 0 && rows_overlap(a->q_out_strides, a->B, a->Hq, a->T, a->D)) ||
+      (a->Hk > 0 && rows_overlap(a->k_out_strides, a->B, a->Hk, a->T, a->D)))
+    return bad(FA_ERR_INVALID_ARG, "fa_rotary: rows of an output overlap (a broadcast tensor cannot be one)");
   if (!device_status_ptr()) return bad(FA_ERR_CUDA, "fa_rotary: no usable CUDA device");
   RotaryParams p{};
   p.x[0] = a->q;
