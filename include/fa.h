@@ -402,7 +402,9 @@ int fa_rotary(const fa_rotary_args* args, void* stream);
  *   FA_ROTARY_BY_PARTS  YaRN (Peng, Quesnelle, Fan, Shippole, 2023): a pair that turns r =
  *                       original_len * inv_freq / 2 pi times over the training length keeps its
  *                       frequency if r >= fast, is interpolated if r <= slow, and is blended
- *                       linearly in r between; amplitude 0.1 ln(factor) + 1
+ *                       linearly in r between; amplitude 0.1 ln(factor) + 1.  (A model served
+ *                       with a blend that is linear in the pair's index, between rounded bounds,
+ *                       needs a table of its own.)
  * *amplitude is 1 otherwise.  inv_freq and amplitude are host pointers.  Returns FA_OK or
  * FA_ERR_INVALID_ARG (rot_dim odd or < 2, base <= 1, factor < 1, original_len <= 0, slow < 0,
  * fast <= slow, an unknown scaling; FA_ROTARY_BASE needs rot_dim > 2). */
@@ -495,7 +497,10 @@ int fa_cache_gather(const fa_cache_gather_args* args, void* stream);
  *     last dimension contiguous) positive multiples of 16 bytes
  *   k_pages, v_pages [num_pages, Hkv, page_size, D] in cache_dtype: dtype, or FA_E4M3 with the
  *     scales [num_pages, Hkv, page_size] that fa_cache_append writes (a value is e4m3 *
- *     2^(byte - 127), bytes 1 to 254).  Up to 16 rows (Hq / Hkv * T) take every value as it is.
+ *     2^(byte - 127), bytes 1 to 254).  Up to 16 rows (Hq / Hkv * T) take every value as it is;
+ *     there a weight is held as a product with V's scale, next to the row's largest such product
+ *     P: one below 2^-21 P keeps fewer bits (an error of 2^-32 P a unit of code), which shows in
+ *     columns where the tokens of large scale are 0.
  *     More rows: with bf16 queries a value of 2^128 or more is taken as bf16's largest and one
  *     is rounded below 2^-133; with fp16 queries a value beyond 131008 is taken as 131008, and
  *     values of a row of scale below 2^-14 are rounded to multiples of 2^-23
@@ -508,7 +513,9 @@ int fa_cache_gather(const fa_cache_gather_args* args, void* stream);
  *   T <= 256; D in {64, 128, 256}; page_size a power of two in [8, 128] (at most 64 when
  *   D = 256); Hq / Hkv <= 128.
  * A drafted token takes no part in a row that does not see it, whatever it holds (infinities
- * and NaN included).  num_splits: 0, or a forced KV split.
+ * and NaN included; over an 8-bit cache with more than 16 rows the scales of all of a sequence's
+ * tokens together choose whether bf16 queries are met in fp16 or bf16, a matter of rounding).
+ * num_splits: 0, or a forced KV split.
  * workspace: fa_tree_workspace_size(args) bytes, 256-byte aligned (none when that is 0); calls
  * that may overlap on the GPU need one each.
  * A length outside [n_b, max_pages * page_size] (an empty sequence without draft_lens is none),

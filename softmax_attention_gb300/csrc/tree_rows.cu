@@ -10,7 +10,7 @@
 // O^T += V^T P^T.  Eight rows or fewer, the decode step of up to eight query heads a kv head, then
 // fill their tile; nine to sixteen take two (NT).  With q as the 16-row operand a decode step's
 // matrix, exponential and O instructions were half empty: 718 instructions a warp and 32 tokens
-// and three CTAs of 166 registers an SM, where this takes 126 registers and four CTAs (128
+// and three CTAs of 166 registers an SM, where this takes 128 registers and four CTAs (128
 // sequences of 1K to 4K tokens: 135 -> 110 us, 6.2 TB/s or 0.92 of a copy; the 57 even ones 87 ->
 // 83 us).  Two tiles lose one or two per cent to the transposition of the weights.
 //
@@ -19,14 +19,16 @@
 // and are combined once at the end.  Nothing in the loop waits for another warp.
 //
 // Numbers.  K codes are exact in fp16.  A row of q is scaled by a power of two so that its
-// largest element is in [2^14, 2^15), which makes bf16's (or fp16's) bits exact in fp16 down to
-// 2^-32 of the row's maximum.  S = q k accumulates in fp32; the scales of q's row, of the token's
+// largest element is in [2^14, 2^15), which makes its elements exact in fp16 down to 2^-31 of the row's
+// maximum for bf16 (whose eight bits end above 2^-24 from 2^-17 on) and 2^-28 for fp16.  S = q k accumulates in fp32; the scales of q's row, of the token's
 // K and the softmax scale multiply it there.  V's scale 2^ev goes into the weight: with x the
 // score in log2 units, O += 2^(x + ev - mo) v over the codes v, mo a running maximum of x + ev,
 // while l += 2^(x - mx) with mx that of x.  (One maximum would not do: a token with a large V
 // scale and no weight would push the others' weights out of fp16's range.)  The weights are
 // rounded to fp16, 2^7 times larger than 1 at the maximum, which may be stale by up to 2^8: at
-// most 2^15.  O and l are fp32.
+// most 2^15.  Below 2^-14, which is 2^-21 of the row's largest product of weight and scale, they lose
+// bits: an error of 2^-32 of that product a unit of code.  It is nothing next to the row's largest
+// term, but shows in a column where the tokens of large scale are 0.  O and l are fp32.
 #include <math.h>
 #include <type_traits>
 

@@ -189,3 +189,38 @@ def test_the_longest_sequence(T):
     torch.cuda.synchronize()
     assert (out.float() - 2.5).abs().max() <= 2.5 * (2.0 ** -8 + 2.0 ** -17)
     assert (lse.double() - math.log(n)).abs().max() <= 2.0 ** -17
+
+
+def test_values_of_one_column_above_the_rest():
+    """The kernel for few rows holds a weight times V's scale in fp16, relative to the row's largest
+    such product.  A token of scale 2^9, zero but in one column, next to tokens of scale 2^-21 to
+    2^-13: their columns keep an absolute error of 2^-32 of that product a unit of code.
+
+    With w the weights, s the scales, c the codes, 2^ev = s: the running maximum of w s is at most
+    the row's largest, and the fp16 weight of that maximum is 2^7, so the rounding (2^-11 of a
+    weight, or 2^-25 where it is below 2^-14) is at most 2^-11 w_j s_j + 2^-32 max(w s)."""
+    T, D, dtype = 2, 128, FP16
+    pr = Problem(1, 4, 2, T, D, 16, dtype, E4M3, [300], scales=(106, 115))
+    pr.ks[:] = 120
+    pg, sl = int(pr.table[0, 2]), 5
+    pr.vs[pg, :, sl] = 136
+    pr.v[pg, :, sl] = 0
+    pr.v[pg, :, sl, 9] = 0x38  # 1
+    args, kw = pr.gpu()
+    out, lse = fa.fa_tree_decode_paged(*args, num_splits=1, **kw)
+    want = pr.want([T], None, D ** -0.5)
+    o, l, mean_abs, reach, _ = want
+    k, v = pr.rows(0)
+    scales = torch.pow(2.0, ref.rows_of(pr.vs, pr.table, 0, 300).double() - 127.0)
+    codes = (v / scales[..., None]).abs()
+    half = 2.0 ** -11
+    got = out.double().cpu()
+    for h in range(4):
+        for i in range(T):
+            n = 300 - T + i + 1
+            w = torch.softmax(k[:n, h // 2] @ pr.q[0, h, i].double() * D ** -0.5, 0)
+            top = (w * scales[:n, h // 2]).max()
+            delta = (D + 8) * 2.0 ** -23 * reach[0, h, i] + 2.0 ** -20
+            bound = (half + 2 * delta) * mean_abs[0, h, i] + half * o[0, h, i].abs() + 2.0 ** -25 \
+                + 2.0 ** -32 * top * codes[:n, h // 2].sum(0)
+            assert ((got[0, h, i] - o[0, h, i]).abs() <= bound).all()
