@@ -78,6 +78,9 @@ KERNEL_SOURCES = {
     "decode": ("decode.cu", "sm103.cuh", "internal.h"),
     "mla": ("mla.cu", "sm103.cuh", "internal.h"),
     "gated_delta": ("gated_delta.cu", "sm103.cuh", "internal.h"),
+    "cache": ("cache.cu", "cache.cuh", "sm103.cuh", "internal.h"),
+    "tree": ("tree.cu", "tree_rows.cu", "tree.cuh", "cache.cuh", "prefill_common.cuh", "sm103.cuh",
+             "internal.h"),
 }
 
 

@@ -433,7 +433,8 @@ int fa_rotary_frequencies(int rot_dim, double base, fa_rotary_scaling scaling, d
  * of one head) is stored as e4m3 values times 2^e, e the least integer >= -126 with
  * max |x| <= 448 * 2^e over the row's finite elements, rounded to nearest even; the byte
  * k_scales / v_scales [num_pages, Hkv, page_size] holds e + 127 (the scale as an 8-bit
- * exponent).  An infinity is stored as +-448, a NaN as NaN.
+ * exponent).  An infinity is stored as +-448, a NaN as NaN.  (A magnitude of 248 * 2^120 or more
+ * is rounded to 2^128 or above, which reads back as an infinity.)
  * inv_freq given: the keys are rotated as fa_rotary does, at positions [B, T] (or, when NULL, at
  * the position in the cache), in fp32, before their one rounding.
  *   D in {64, 128, 256}; page_size a power of two; rot_dim a multiple of 16, at most D.

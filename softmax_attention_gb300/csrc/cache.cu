@@ -131,8 +131,10 @@ __device__ __forceinline__ void rotate(const Turn& t, float (&a)[8], float (&b)[
 // ------------------------------------------------------------------------------------------
 // Rotary positions on q and k.  Thread = (unit, token, group of heads); q's heads come first,
 // then k's.  16,384 tokens of 40 heads, D = 128, half of each rotated, bf16: 60 us, 5.6 TB/s or
-// 0.83 of a copy, bound by the memory's latency: 24 warps an SM (80 registers) with four heads'
-// loads in flight.  Two waves of blocks or fewer pay for their tables and sines instead.
+// 0.83 of a copy, bound by the memory's latency: 24 warps an SM (80 registers, for which the
+// half-layout and the 16-bit kernels spill 12 to 24 bytes a thread) with four heads' loads in
+// flight.  Two waves of blocks or fewer pay for their tables and sines instead: the fp32 gradient of
+// 3,686 tokens of 32 heads, D = 64, 461 blocks where 456 fit at once, 14.4 us.
 // ------------------------------------------------------------------------------------------
 struct RotaryParams {
   const void* x[2];
@@ -202,8 +204,10 @@ __global__ void __launch_bounds__(kThreads, 3) rotary_kernel(const RotaryParams 
 // ------------------------------------------------------------------------------------------
 // Cache write.  Thread = (unit, token, group of heads); the D/16 threads of a row sit side by
 // side in a warp and share the row's largest magnitude by shuffles.  512 tokens of eight sequences,
-// 8 kv heads, D = 128, to e4m3: 8.5 us, 2.9 TB/s; two waves of blocks, each of which loads,
-// reduces and stores in turn (10.3 us when the rows' loads waited for the page id).
+// 8 kv heads, D = 128, to e4m3: 8.4 us, 3.0 TB/s (10.3 us when the rows' loads waited for the page
+// id); 1024 blocks of 80 registers, 456 at once, each of which loads, reduces and stores in turn.
+// (The registers are the angles', which this call has none of.)  Twenty calls a graph: 6.5 us each,
+// 8.8 with the rotation; one token of each of 128 sequences 2.7 and 3.6 us.
 // ------------------------------------------------------------------------------------------
 struct AppendParams {
   const void* x[2];            // k, v

@@ -21,7 +21,7 @@
 // by placing bits (five, and a test for NaN codes); at 64 drafted tokens the conversion's
 // instructions are what bounds the kernel.  So a CTA looks at the scale bytes of its keys
 // first: if all lie in [113, 134], every value * 2^e is exact in fp16 too, the rows of Q are
-// scaled by powers of two into fp16 (exact down to 2^-32 of a row's maximum, undone in the
+// scaled by powers of two into fp16 (exact down to 2^-31 of a row's maximum, undone in the
 // scores), and both products run in fp16.  Otherwise they run in bf16, which holds any scale.
 //
 // Values beyond the operand type.  fp16 queries meet K and V at half their size (undone in the
@@ -32,9 +32,12 @@
 //
 // Measured (D = 128, 8 kv heads of four query heads, even sequences of 8192 tokens, 16-token
 // pages): 16-bit cache, 32 drafted tokens of 19 sequences 103 us, 6.2 TB/s, bound by memory; 64 of
-// them, two tiles a sequence, 141 us.  8-bit cache 96 and 182 us: a KV tile takes some 2450 clocks
+// them, two tiles a sequence, 144 us.  8-bit cache 95 and 180 us: a KV tile takes some 2450 clocks
 // of converters (730 for K, 780 for V and the waits between) and softmax warps (2000 of them) side
-// by side at half of the issue slots.
+// by side at half of the issue slots.  One row of each sequence with a scale byte outside [113, 134]
+// moves its blocks to bf16 operands: 1.5 times as long (replayed twenty a graph, 88 -> 131 and 173
+// -> 260 us; D = 64 238 -> 281, D = 256 190 -> 249).  fp16 queries: 83 and 163 us, 91 and 179 with
+// one row a sequence that can overflow.
 //
 // Warp roles: 0-3 and the last four softmax + epilogue (a row of scores is shared by two
 // threads), 4 TMA producer, 5 P V issuer and tensor-memory owner, 6 S issuer, and for 8-bit pages 7
