@@ -190,7 +190,7 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 template <bool BF16>
 __device__ __forceinline__ RowScale row_scale(uint32_t byte) {
   RowScale s;
-  const int e = static_cast<int>(byte) - 127;  // [-127, 128]
+  const int e = static_cast<int>(byte) - 127;  // [-127, 128], and -128 of fp16 at half size
   if constexpr (BF16) {
     const int e1 = min(e, 7);
     const uint32_t f1 = static_cast<uint32_t>(e1 + 120 + 127) << 7;  // exponent field in [120, 254]
