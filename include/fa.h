@@ -358,6 +358,43 @@ int gated_delta_prefill(const gated_delta_args* args, void* stream);
 size_t gated_delta_workspace_size(const gated_delta_args* args);
 
 /*
+ * The same recurrence token by token, on a pool of states: a decode step (T = 1), or a few drafted
+ * tokens.  Sequence b's state is read from slot read_index[b] of the pool (NULL: slot b), taken
+ * through its first new_lens[b] tokens (NULL: T) and written to slot write_index[b] (NULL: where
+ * it was read).  With two slots a sequence the state before drafted tokens is kept.
+ *   q, k [B, Hk, T, 128], v, out [B, Hv, T, 128] in dtype (FA_BF16 or FA_FP16), strides (batch,
+ *     head, token; in elements, multiples of 16 bytes; the last dimension contiguous; inputs may be
+ *     broadcast, with strides of 0)
+ *   g (log decay), beta [B, Hv, T] fp32 by their strides
+ *   states [num_states, Hv, 128, 128] fp32 (value row, key column: the states of
+ *     gated_delta_prefill), contiguous
+ *   read_index, write_index, new_lens [B] int32 (device) or NULL.
+ * Rows t >= new_lens[b] of out are set to 0; a sequence of no tokens has its state copied.  Slots
+ * written in one call have to be different ones, and none may be read by another sequence.  Sums
+ * and states are fp32, out is rounded once.
+ * A slot outside the pool or a new_lens[b] outside [0, T] sets FA_ERR_BOUNDS in the device status
+ * word; the sequence's out is then 0 and no state is written for it.
+ */
+typedef struct gated_delta_step_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* g;
+  const float* beta;
+  float* states;
+  const int32_t* read_index;
+  const int32_t* write_index;
+  const int32_t* new_lens;
+  void* out;
+  int64_t q_strides[3], k_strides[3], v_strides[3], g_strides[3], beta_strides[3], out_strides[3];
+  int B, T, Hk, Hv, dk, dv, num_states;
+  float scale;
+  fa_dtype dtype;
+} gated_delta_step_args;
+
+int gated_delta_step(const gated_delta_step_args* args, void* stream);
+
+/*
  * Rotary positions on the queries and keys of a step (either may be absent: Hq or Hk = 0).
  * Pair i of a row, at angle theta_i = position * inv_freq[i]:
  *     y_a = amplitude * (x_a cos theta_i - x_b sin theta_i)
@@ -418,6 +455,70 @@ typedef enum fa_rotary_scaling {
 int fa_rotary_frequencies(int rot_dim, double base, fa_rotary_scaling scaling, double factor,
                           double original_len, double fast, double slow, double* inv_freq,
                           float* amplitude);
+
+/*
+ * RMS norms of the queries and keys of a step for each head, and rotary positions on the result, in
+ * one pass (either tensor may be absent: Hq or Hk = 0).  Of a row x of D columns:
+ *     n = x / sqrt(mean(x^2) + eps),   y = fa_rotary's map of n * weight
+ *   q, k, q_out, k_out, positions, inv_freq, interleaved, amplitude: as in fa_rotary (rot_dim = 0:
+ *   norms alone, positions and inv_freq are not read);
+ *   q_weight, k_weight [D] in weight_dtype (dtype or FA_FP32), shared by all heads, or NULL (ones).
+ *   D a multiple of 16 up to 512; rot_dim a multiple of 16, at most D.
+ * Computed in fp32, rounded once to dtype.  q_out and k_out may be q and k themselves (same pointer
+ * and strides).
+ */
+typedef struct fa_norm_rotary_args {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_strides[3], k_strides[3], q_out_strides[3], k_out_strides[3];
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* positions;
+  const double* inv_freq;
+  int B, T, Hq, Hk, D, rot_dim;
+  int interleaved;
+  float amplitude, eps;
+  fa_dtype dtype, weight_dtype;
+} fa_norm_rotary_args;
+
+int fa_qk_norm_rotary(const fa_norm_rotary_args* args, void* stream);
+
+/*
+ * Its gradient: of dq_out and dk_out (the gradients of the outputs) and the inputs q and k of the
+ * forward call, dq and dk in dtype and the weights' gradients dq_weight, dk_weight [D] fp32 (NULL: not
+ * wanted), summed over all rows in a fixed order.  dq and dk may be dq_out and dk_out, or q and k,
+ * themselves (same pointer and strides).
+ * workspace: fa_qk_norm_rotary_backward_workspace_size(args) bytes, 256-byte aligned; calls that may
+ * overlap on the GPU need one each.
+ */
+typedef struct fa_norm_rotary_backward_args {
+  const void* dq_out;
+  const void* dk_out;
+  const void* q;
+  const void* k;
+  void* dq;
+  void* dk;
+  float* dq_weight;
+  float* dk_weight;
+  int64_t dq_out_strides[3], dk_out_strides[3], q_strides[3], k_strides[3], dq_strides[3], dk_strides[3];
+  const void* q_weight;
+  const void* k_weight;
+  const int32_t* positions;
+  const double* inv_freq;
+  int B, T, Hq, Hk, D, rot_dim;
+  int interleaved;
+  float amplitude, eps;
+  fa_dtype dtype, weight_dtype;
+  void* workspace;
+  size_t workspace_bytes;
+} fa_norm_rotary_backward_args;
+
+int fa_qk_norm_rotary_backward(const fa_norm_rotary_backward_args* args, void* stream);
+
+/* Workspace bytes of a call with these sizes on the current device (pointers are not read). */
+size_t fa_qk_norm_rotary_backward_workspace_size(const fa_norm_rotary_backward_args* args);
 
 /*
  * Writes a step's keys and values into a paged cache (the layout of fa_decode_paged).
@@ -554,6 +655,82 @@ int fa_tree_mask(const int32_t* parents, int T, uint64_t* words);
 
 /* Workspace bytes of a call with these sizes on the current device (pointers are not read). */
 size_t fa_tree_workspace_size(const fa_tree_args* args);
+
+/*
+ * Attention over packed prompts: B sequences of different lengths behind one another in one
+ * tensor.  Sequence b's queries are the rows cu_seqlens_q[b] .. cu_seqlens_q[b+1] - 1 of q, its
+ * keys the rows cu_seqlens_k[b] .. cu_seqlens_k[b+1] - 1 of k and v (n_q and n_k of them; for
+ * whole prompts both arrays are the same).  Query i sees the keys j < n_k, and with causal = 1
+ * those with j <= i + n_k - n_q (the queries are the last positions):
+ *     s_j = scale * <q_i, k_j>,   out_i = sum_j softmax(s)_j v_j,   lse_i = ln sum_j e^{s_j}
+ *   q [total_q, Hq, D], k, v [total_k, Hkv, D], out [total_q, Hq, D] in dtype (FA_BF16 or
+ *     FA_FP16), each with its strides (token, head; in elements, multiples of 16 bytes and at
+ *     least D; the last dimension contiguous); lse [total_q, Hq] fp32 contiguous, or NULL
+ *   cu_seqlens_q, cu_seqlens_k [B + 1] int32 (device), not decreasing
+ *   D in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 128.
+ * A row that sees no key gets out = 0 and lse = -inf.  Rows of out and lse in front of the first
+ * sequence and behind the last are left as they were, and what q, k and v hold there, or in other
+ * sequences, takes no part.  (Within a sequence a value of v that is not finite may reach
+ * rows that do not see it, as 0 times it.)
+ * Sequences whose offsets decrease or reach out of the tensor set FA_ERR_BOUNDS in the device
+ * status word and are taken as empty.  No workspace; one launch.
+ */
+typedef struct fa_packed_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  float* lse;
+  int64_t q_strides[2], k_strides[2], v_strides[2], out_strides[2];
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int B, Hq, Hkv, D, total_q, total_k;
+  int causal;
+  float scale;
+  fa_dtype dtype;
+} fa_packed_args;
+
+int fa_prefill_packed(const fa_packed_args* args, void* stream);
+
+/*
+ * The gradients of fa_prefill_packed's out (lse is taken as having none).  With P the softmax
+ * weights, dP_ij = <dout_i, v_j>, delta_i = <dout_i, out_i> and dS = P (dP - delta):
+ *     dq_i = scale sum_j dS_ij k_j,  dk_j = scale sum_i dS_ij q_i,  dv_j = sum_i P_ij dout_i
+ * the sums over i running over the query heads of the kv head as well.
+ *   q, k, v, out, lse, cu_seqlens_*: as in the forward call, out and lse what it returned; dout
+ *   [total_q, Hq, D]; dq [total_q, Hq, D], dk, dv [total_k, Hkv, D]; all in dtype, with strides as
+ *   above.
+ * Every row of dq, dk and dv that belongs to a sequence is written (zeros where nothing is seen),
+ * no other row.  No atomics: the same call gives the same bits.
+ * workspace: fa_packed_backward_workspace_size(args) bytes, 256-byte aligned; calls that may
+ * overlap on the GPU need one each.
+ */
+typedef struct fa_packed_backward_args {
+  const void* dout;
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* out;
+  const float* lse;
+  void* dq;
+  void* dk;
+  void* dv;
+  int64_t dout_strides[2], q_strides[2], k_strides[2], v_strides[2], out_strides[2], dq_strides[2],
+      dk_strides[2], dv_strides[2];
+  const int32_t* cu_seqlens_q;
+  const int32_t* cu_seqlens_k;
+  int B, Hq, Hkv, D, total_q, total_k;
+  int causal;
+  float scale;
+  fa_dtype dtype;
+  void* workspace;
+  size_t workspace_bytes;
+} fa_packed_backward_args;
+
+int fa_prefill_packed_backward(const fa_packed_backward_args* args, void* stream);
+
+/* Workspace bytes of a call with these sizes (pointers are not read). */
+size_t fa_packed_backward_workspace_size(const fa_packed_backward_args* args);
 
 /*
  * Merge of attention states over disjoint key sets (the split-KV combine):

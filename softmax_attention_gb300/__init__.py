@@ -16,6 +16,9 @@ Entry points (same names as the C ABI):
     fa_cache_gather(k_pages, v_pages, page_table, seq_lens, max_seq_len, ...)
     tree_mask(parents)                                       a mask for the next one, on the host
     fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len, tree_mask=...)
+    fa_qk_norm_rotary(q, k, positions, inv_freq, q_weight, k_weight, ...)   and its _backward
+    fa_prefill_packed(q, k, v, cu_seqlens_q, ...)            prompts behind one another, and its _backward
+    gated_delta_step(q, k, v, g, beta, states, ...)          the gated delta rule token by token
     fa_get_device_status()
 """
 from __future__ import annotations
@@ -50,6 +53,9 @@ EXPORTS = (
     "gated_delta_prefill", "gated_delta_workspace_size",
     "fa_rotary", "fa_rotary_frequencies", "fa_cache_append", "fa_cache_gather",
     "fa_tree_decode_paged", "fa_tree_workspace_size", "fa_tree_mask",
+    "fa_qk_norm_rotary", "fa_qk_norm_rotary_backward", "fa_qk_norm_rotary_backward_workspace_size",
+    "fa_prefill_packed", "fa_prefill_packed_backward", "fa_packed_backward_workspace_size",
+    "gated_delta_step",
 )
 
 
@@ -181,6 +187,77 @@ class TreeArgs(ctypes.Structure):
     ]
 
 
+_Strides2 = ctypes.c_int64 * 2
+_NORM_FIELDS = [
+    ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+    ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p),
+    ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hq", ctypes.c_int), ("Hk", ctypes.c_int),
+    ("D", ctypes.c_int), ("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+    ("amplitude", ctypes.c_float), ("eps", ctypes.c_float), ("dtype", ctypes.c_int),
+    ("weight_dtype", ctypes.c_int),
+]
+
+
+class NormRotaryArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+        ("k_out", ctypes.c_void_p), ("q_strides", _Strides), ("k_strides", _Strides),
+        ("q_out_strides", _Strides), ("k_out_strides", _Strides),
+    ] + _NORM_FIELDS
+
+
+class NormRotaryBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("dq_out", ctypes.c_void_p), ("dk_out", ctypes.c_void_p), ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
+        ("dq_weight", ctypes.c_void_p), ("dk_weight", ctypes.c_void_p),
+        ("dq_out_strides", _Strides), ("dk_out_strides", _Strides), ("q_strides", _Strides),
+        ("k_strides", _Strides), ("dq_strides", _Strides), ("dk_strides", _Strides),
+    ] + _NORM_FIELDS + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+_PACKED_FIELDS = [
+    ("cu_seqlens_q", ctypes.c_void_p), ("cu_seqlens_k", ctypes.c_void_p),
+    ("B", ctypes.c_int), ("Hq", ctypes.c_int), ("Hkv", ctypes.c_int), ("D", ctypes.c_int),
+    ("total_q", ctypes.c_int), ("total_k", ctypes.c_int), ("causal", ctypes.c_int),
+    ("scale", ctypes.c_float), ("dtype", ctypes.c_int),
+]
+
+
+class PackedArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("q_strides", _Strides2), ("k_strides", _Strides2), ("v_strides", _Strides2),
+        ("out_strides", _Strides2),
+    ] + _PACKED_FIELDS
+
+
+class PackedBackwardArgs(ctypes.Structure):
+    _fields_ = [
+        ("dout", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p), ("dv", ctypes.c_void_p),
+        ("dout_strides", _Strides2), ("q_strides", _Strides2), ("k_strides", _Strides2),
+        ("v_strides", _Strides2), ("out_strides", _Strides2), ("dq_strides", _Strides2),
+        ("dk_strides", _Strides2), ("dv_strides", _Strides2),
+    ] + _PACKED_FIELDS + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class GatedDeltaStepArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("g", ctypes.c_void_p), ("beta", ctypes.c_void_p), ("states", ctypes.c_void_p),
+        ("read_index", ctypes.c_void_p), ("write_index", ctypes.c_void_p),
+        ("new_lens", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("q_strides", _Strides), ("k_strides", _Strides), ("v_strides", _Strides),
+        ("g_strides", _Strides), ("beta_strides", _Strides), ("out_strides", _Strides),
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hk", ctypes.c_int), ("Hv", ctypes.c_int),
+        ("dk", ctypes.c_int), ("dv", ctypes.c_int), ("num_states", ctypes.c_int),
+        ("scale", ctypes.c_float), ("dtype", ctypes.c_int),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -261,6 +338,14 @@ def load_library(path: str | None = None):
         lib.fa_tree_decode_paged.argtypes = [_vp, _vp]
         lib.fa_tree_workspace_size.restype = _sz
         lib.fa_tree_workspace_size.argtypes = [_vp]
+        for name in ("fa_qk_norm_rotary", "fa_qk_norm_rotary_backward", "fa_prefill_packed",
+                     "fa_prefill_packed_backward", "gated_delta_step"):
+            getattr(lib, name).restype = _i
+            getattr(lib, name).argtypes = [_vp, _vp]
+        for name in ("fa_qk_norm_rotary_backward_workspace_size",
+                     "fa_packed_backward_workspace_size"):
+            getattr(lib, name).restype = _sz
+            getattr(lib, name).argtypes = [_vp]
         _lib = lib
         return lib
 
@@ -691,7 +776,7 @@ def gated_delta_prefill(q, k, v, g, beta, *, scale=None, initial_state=None, out
 # ------------------------------------------------------------------------------------------
 _CACHE_DT = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16, torch.float8_e4m3fn: FA_E4M3}
 _STRUCT_CODE = {ctypes.c_void_p: "P", ctypes.c_int: "i", ctypes.c_float: "f", ctypes.c_size_t: "N",
-                _Strides: "3q"}
+                _Strides: "3q", _Strides2: "2q"}
 
 
 def _packer(cls):
@@ -705,6 +790,9 @@ def _packer(cls):
 
 _pack_rotary, _pack_append, _pack_gather, _pack_tree = map(
     _packer, (RotaryArgs, CacheAppendArgs, CacheGatherArgs, TreeArgs))
+_pack_norm, _pack_norm_backward, _pack_packed, _pack_packed_backward, _pack_step = map(
+    _packer, (NormRotaryArgs, NormRotaryBackwardArgs, PackedArgs, PackedBackwardArgs,
+              GatedDeltaStepArgs))
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(
     torch._C, "_cuda_getCurrentRawStream") else (
         lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -978,3 +1066,247 @@ def fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len:
             a = _pack_tree(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
         _check(lib.fa_tree_decode_paged(a, _raw_stream(dev)))
     return out, lse
+
+
+# ------------------------------------------------------------------------------------------
+# Packed prompts, forward and backward; norms of queries and keys; the recurrent gated-delta step.
+# As above: strided inputs, the tensors' own device, allocations on the launching stream.
+# ------------------------------------------------------------------------------------------
+def _norm_fields(dev, q, k, positions, inv_freq, q_weight, k_weight, amplitude, interleaved, eps):
+    """The checked fields that fa_qk_norm_rotary and its backward share."""
+    B, Hq, T, D = q.shape
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype}")
+    weights = {w.dtype for w in (q_weight, k_weight) if w is not None}
+    if len(weights) > 1 or not weights <= {q.dtype, torch.float32}:
+        raise ValueError(f"the weights must both be {q.dtype} or float32, got {sorted(map(str, weights))}")
+    _need_dtype(q.dtype, k)
+    _need_dtype(torch.int32, positions)
+    _need_dtype(torch.float64, inv_freq)
+    _shape("k", k, B, 0 if k is None else k.shape[1], T, D)
+    _shape("q_weight", q_weight, D)
+    _shape("k_weight", k_weight, D)
+    _shape("positions", positions, B, T)
+    _on(dev, positions, inv_freq, q_weight, k_weight)
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq go together")
+    return (_addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), B, T, Hq,
+            0 if k is None else k.shape[1], D, 0 if inv_freq is None else 2 * inv_freq.numel(),
+            interleaved, amplitude, eps, _DT[q.dtype], _DT[weights.pop() if weights else q.dtype])
+
+
+_none3 = (0, 0, 0)
+
+
+def fa_qk_norm_rotary(q, k, positions, inv_freq, q_weight, k_weight=None, *, eps: float = 1e-6,
+                      amplitude: float = 1.0, interleaved: bool = False, q_out=None, k_out=None,
+                      stream=None):
+    """RMS norms of q [B,Hq,T,D] and k [B,Hk,T,D] (k may be None) for each head, times q_weight and
+    k_weight [D] (q's dtype or fp32; None: ones), then fa_rotary's rotation, in one pass.  bf16,
+    fp16 or fp32, any strides with a contiguous last dimension; positions [B,T] int32 and inv_freq
+    [rot_dim/2] fp64, or None for both: norms alone.  q_out and k_out may be q and k themselves.
+    Returns (q_out, k_out)."""
+    lib = load_library()
+    dev = _cuda_index(q)
+    _need_dtype(q.dtype, q_out, k_out)
+    _shape("q_out", q_out, *q.shape)
+    if k is not None:
+        _shape("k_out", k_out, *k.shape)
+    fields = _norm_fields(dev, q, k, positions, inv_freq, q_weight, k_weight, amplitude,
+                          interleaved, eps)
+    with _scope(dev, stream):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is None:
+            k_out = None
+        elif k_out is None:
+            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        a = _pack_norm(q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
+                       *_strides_on(dev, q), *(_none3 if k is None else _strides_on(dev, k)),
+                       *_strides_on(dev, q_out), *(_none3 if k is None else _strides_on(dev, k_out)),
+                       *fields)
+        _check(lib.fa_qk_norm_rotary(a, _raw_stream(dev)))
+    return q_out, k_out
+
+
+def fa_qk_norm_rotary_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weight, k_weight=None, *,
+                               eps: float = 1e-6, amplitude: float = 1.0, interleaved: bool = False,
+                               dq=None, dk=None, workspace=None, stream=None):
+    """Gradient of fa_qk_norm_rotary: of the outputs' gradients dq_out, dk_out and the call's
+    inputs.  dq and dk may be dq_out and dk_out, or q and k, themselves.  Returns (dq, dk, dq_weight,
+    dk_weight): the last two [D] fp32, None where there is no weight."""
+    lib = load_library()
+    dev = _cuda_index(q)
+    _need_dtype(q.dtype, dq_out, dk_out, dq, dk)
+    _shape("dq_out", dq_out, *q.shape)
+    _shape("dq", dq, *q.shape)
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    if k is not None:
+        _shape("dk_out", dk_out, *k.shape)
+        _shape("dk", dk, *k.shape)
+    fields = _norm_fields(dev, q, k, positions, inv_freq, q_weight, k_weight, amplitude,
+                          interleaved, eps)
+    _on(dev, workspace)
+    with _scope(dev, stream):
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k is None:
+            dk = None
+        elif dk is None:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        new = lambda w: None if w is None else torch.empty(q.shape[3], dtype=torch.float32, device=q.device)
+        dqw, dkw = new(q_weight), new(k_weight)
+        ks = (_none3,) * 3 if k is None else tuple(_strides_on(dev, t) for t in (dk_out, k, dk))
+        fields = (dq_out.data_ptr(), _addr(dk_out), q.data_ptr(), _addr(k), dq.data_ptr(), _addr(dk),
+                  _addr(dqw), _addr(dkw), *_strides_on(dev, dq_out), *ks[0], *_strides_on(dev, q),
+                  *ks[1], *_strides_on(dev, dq), *ks[2], *fields)
+        a = _pack_norm_backward(*fields, 0, 0)
+        need = lib.fa_qk_norm_rotary_backward_workspace_size(a)
+        if need:
+            ws = _workspace(need, q.device, workspace)
+            a = _pack_norm_backward(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
+        _check(lib.fa_qk_norm_rotary_backward(a, _raw_stream(dev)))
+    return dq, dk, dqw, dkw
+
+
+def _rows_on(dev, t):
+    """(token, head) strides of a 3-D tensor on `dev` with a contiguous last dimension; 0 for a
+    dimension of one element, where torch may report anything."""
+    s, n = t.stride(), t.shape
+    if t.get_device() != dev or (s[2] != 1 and n[2] > 1):
+        raise ValueError("tensors must be CUDA tensors on one device with a contiguous last "
+                         "dimension")
+    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+
+
+def _packed_fields(dev, q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale):
+    """The checked fields that fa_prefill_packed and its backward share."""
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16, got {q.dtype}")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, D]")
+    total_q, Hq, D = q.shape
+    total_k, Hkv, _ = k.shape
+    _need_dtype(q.dtype, k, v)
+    _shape("k", k, total_k, Hkv, D)
+    _shape("v", v, total_k, Hkv, D)
+    if cu_seqlens_k is None:
+        cu_seqlens_k = cu_seqlens_q
+        if total_k != total_q:
+            raise ValueError("without cu_seqlens_k the keys are the queries' tokens: "
+                             f"got {total_q} rows of q and {total_k} of k")
+    _need_dtype(torch.int32, cu_seqlens_q, cu_seqlens_k)
+    B = cu_seqlens_q.numel() - 1
+    if B < 0:
+        raise ValueError("cu_seqlens_q must hold one offset at least")
+    _shape("cu_seqlens_q", cu_seqlens_q, B + 1)
+    _shape("cu_seqlens_k", cu_seqlens_k, B + 1)
+    _on(dev, cu_seqlens_q, cu_seqlens_k)
+    return (cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv, D, total_q, total_k,
+            causal, 1.0 / math.sqrt(D) if scale is None else scale, _DT[q.dtype])
+
+
+def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool = True,
+                      scale: float | None = None, out=None, lse=None, stream=None):
+    """Attention over packed prompts: q [total_q,Hq,D], k, v [total_k,Hkv,D] bf16 or fp16 (any
+    token and head strides with a contiguous last dimension, as slices of one projection), the
+    sequences behind one another; cu_seqlens_q, cu_seqlens_k [B+1] int32 (device): first row of
+    each and the end of the last (cu_seqlens_k None: the same).  causal: a sequence's queries are
+    its last positions.  Rows outside the sequences are left as they were.  Returns (out
+    [total_q,Hq,D], lse [total_q,Hq] fp32)."""
+    lib = load_library()
+    dev = _cuda_index(q)
+    fields = _packed_fields(dev, q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale)
+    _need_dtype(q.dtype, out)
+    _need_dtype(torch.float32, lse)
+    _shape("out", out, *q.shape)
+    _shape("lse", lse, *q.shape[:2])
+    _on(dev, lse)
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        a = _pack_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                         *_rows_on(dev, q), *_rows_on(dev, k), *_rows_on(dev, v),
+                         *_rows_on(dev, out), *fields)
+        _check(lib.fa_prefill_packed(a, _raw_stream(dev)))
+    return out, lse
+
+
+def fa_prefill_packed_backward(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k=None, *,
+                               causal: bool = True, scale: float | None = None, dq=None, dk=None,
+                               dv=None, workspace=None, stream=None):
+    """Gradients of fa_prefill_packed's out: dout [total_q,Hq,D], the call's inputs, and the out and
+    lse that it returned.  Rows of dq, dk and dv outside the sequences are left as they were.
+    Returns (dq [total_q,Hq,D], dk, dv [total_k,Hkv,D])."""
+    lib = load_library()
+    dev = _cuda_index(q)
+    fields = _packed_fields(dev, q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale)
+    _need_dtype(q.dtype, dout, out, dq, dk, dv)
+    _need_dtype(torch.float32, lse)
+    for name, t in (("dout", dout), ("out", out), ("dq", dq)):
+        _shape(name, t, *q.shape)
+    _shape("dk", dk, *k.shape)
+    _shape("dv", dv, *k.shape)
+    _shape("lse", lse, *q.shape[:2])
+    _on(dev, lse, workspace)
+    with _scope(dev, stream):
+        if dq is None:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if dk is None:
+            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        if dv is None:
+            dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+        fields = (dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                  lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                  *(x for t in (dout, q, k, v, out, dq, dk, dv) for x in _rows_on(dev, t)), *fields)
+        a = _pack_packed_backward(*fields, 0, 0)
+        need = lib.fa_packed_backward_workspace_size(a)
+        if need:
+            ws = _workspace(need, q.device, workspace)
+            a = _pack_packed_backward(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
+        _check(lib.fa_prefill_packed_backward(a, _raw_stream(dev)))
+    return dq, dk, dv
+
+
+def gated_delta_step(q, k, v, g, beta, states, *, read_index=None, write_index=None, new_lens=None,
+                     scale: float | None = None, out=None, stream=None):
+    """The gated delta rule over the next T tokens of each sequence, one after another: q, k
+    [B,Hk,T,128], v [B,Hv,T,128] bf16 or fp16 (any strides with a contiguous last dimension); g
+    (log decay), beta [B,Hv,T] fp32, any strides; states [num_states,Hv,128,128] fp32, updated.
+    Sequence b's state is read from slot read_index[b] (default b) and written to write_index[b]
+    (default where it was read); it has new_lens[b] tokens (default T; int32, device, all three).
+    Returns out [B,Hv,T,128]."""
+    lib = load_library()
+    dev = _cuda_index(q)
+    if q.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"expected bfloat16 or float16, got {q.dtype}")
+    B, Hk, T, dk = q.shape
+    Hv, dv = v.shape[1], v.shape[3]
+    _need_dtype(q.dtype, k, v, out)
+    _need_dtype(torch.float32, g, beta, states)
+    _need_dtype(torch.int32, read_index, write_index, new_lens)
+    _shape("k", k, B, Hk, T, dk)
+    _shape("v", v, B, Hv, T, dv)
+    _shape("g", g, B, Hv, T)
+    _shape("beta", beta, B, Hv, T)
+    _shape("states", states, states.shape[0], Hv, dv, dk)
+    _shape("out", out, B, Hv, T, dv)
+    for name, t in (("read_index", read_index), ("write_index", write_index), ("new_lens", new_lens)):
+        _shape(name, t, B)
+    _on(dev, states, read_index, write_index, new_lens)
+    if g.get_device() != dev or beta.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors on one device")
+    with _scope(dev, stream):
+        if out is None:
+            out = torch.empty((B, Hv, T, dv), dtype=q.dtype, device=q.device)
+        a = _pack_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
+                       states.data_ptr(), _addr(read_index), _addr(write_index), _addr(new_lens),
+                       out.data_ptr(), *_strides_on(dev, q), *_strides_on(dev, k),
+                       *_strides_on(dev, v), *g.stride(), *beta.stride(), *_strides_on(dev, out), B,
+                       T, Hk, Hv, dk, dv, states.shape[0],
+                       1.0 / math.sqrt(dk) if scale is None else scale, _DT[q.dtype])
+        _check(lib.gated_delta_step(a, _raw_stream(dev)))
+    return out

@@ -13,9 +13,11 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libfa.so")
 SOURCES = ["abi.cu", "prefill.cu", "decode.cu", "decode_noalloc.cu", "mla.cu", "merge.cu",
            "selftest.cu", "gated_delta.cu", "prefill_f32.cu", "cache.cu",
-           "tree.cu", "tree_rows.cu"]
+           "tree.cu", "tree_rows.cu", "packed.cu", "packed_grad.cu",
+           "norm_rotary.cu", "delta_step.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "sm103.cuh", "prefill_common.cuh",
-                                            "cache.cuh", "tree.cuh")] + [
+                                            "cache.cuh", "tree.cuh", "packed.cuh",
+                                            "rotary.cuh")] + [
     os.path.join(ROOT, "include", "fa.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")
