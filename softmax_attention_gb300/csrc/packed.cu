@@ -49,8 +49,8 @@ struct Layout {
   static constexpr int kTile = kBlock * (D / 64);     // a Q tile, or a ring slot of K or V
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBars = kRing + kSlots * kTile;
-  // q[2], full[slots], empty[slots], tail, s[2], p[2], pv[2], done[2]
-  static constexpr int kNumBars = 2 * kSlots + 11;
+  // q[2], full[slots], empty[slots], tail, s[2], p[2], pv[2], done[2], turn[2]
+  static constexpr int kNumBars = 2 * kSlots + 13;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;  // room to align the base
   // tensor memory columns
   static constexpr bool kApart = D == 64;             // P beside S
@@ -73,14 +73,16 @@ __device__ __forceinline__ Tile make_tile(const Params& p, const Seq& s, int q0)
   return t;
 }
 
-// Thirty-two scores against the maximum m: exponentials packed, their sum added.
-template <bool BF16>
-__device__ __forceinline__ void weigh(const float (&x)[32], float a, float m, float2& sum, uint32_t* pk) {
+// Thirty-two scores against the maximum m: exponentials packed, their sum added; with MASK the
+// first `left` alone count.
+template <bool BF16, bool MASK>
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], int left, float a, float m, float2& sum, uint32_t* pk) {
   const float2 a2 = make_float2(a, a), nm = make_float2(-m, -m);
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
-    const float2 t = __ffma2_rn(make_float2(x[2 * c], x[2 * c + 1]), a2, nm);
-    const float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+    const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), a2, nm);
+    float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
+    if (MASK) e = make_float2(2 * c < left ? e.x : 0.f, 2 * c + 1 < left ? e.y : 0.f);
     sum = __fadd2_rn(sum, e);
     pk[c] = BF16 ? pack_bf16x2(e.x, e.y) : pack_f16x2(e.x, e.y);
   }
@@ -106,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar_p = [&](int x) { return bar_tail + 8u * (3 + x); };
   auto bar_pv = [&](int x) { return bar_tail + 8u * (5 + x); };
   auto bar_done = [&](int x) { return bar_tail + 8u * (7 + x); };
+  auto bar_turn = [&](int x) { return bar_tail + 8u * (9 + x); };
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int hk = blockIdx.x % p.Hkv;
@@ -131,6 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_p(x), 128);
       mbar_init(bar_pv(x), 1);
       mbar_init(bar_done(x), 1);
+      mbar_init(bar_turn(x), 1);
     }
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(bar_full(s), 1);
@@ -204,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp >= 9) {
       // ---------------------------------- issuers ---------------------------------------
-      const int x = warp - 9, nx = x ? tile_b.n : tile_a.n;
+      const int x = warp - 9, nx = x ? tile_b.n : tile_a.n, other_n = x ? tile_a.n : tile_b.n;
       if (lane == 0 && n > 0) {
         constexpr uint32_t idesc_s = idesc_f16(BF16, kRows, kKeys, false, false);
         constexpr uint32_t idesc_o = idesc_f16(BF16, kRows, D, false, true);
@@ -220,8 +224,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t off = (kk / 4) * L::kBlock + (kk % 4) * 32;
             mma_ss(tm_s, sdesc_add(q_desc, off), sdesc_add(kd, off), idesc_s, kk > 0 ? 1u : 0u);
           }
-          tc_commit(bar_s(x));
-          tc_commit(bar_empty(slot));
         };
         auto full = [&](int i) { return mbar_wait(bar_full(i % L::kSlots), (i / L::kSlots) & 1, p.status); };
         bool ok = true;
@@ -230,21 +232,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (ok) {
             tc_fence_after();
             issue_s(0);
+            tc_commit(bar_s(x));
+            tc_commit(bar_empty(0));
           }
         }
         for (int j = 0; ok && j < nx; ++j) {
           if (!(ok = mbar_wait(bar_p(x), j & 1, p.status))) break;
           if (!(ok = full(2 * j + 1))) break;
           if (j + 1 < nx && !(ok = full(2 * j + 2))) break;
+          // the other tile's turn before this one: its j-th pair of products for B, its (j-1)-th for A
+          const int theirs = x ? j : j - 1;
+          if (theirs >= 0 && theirs < other_n && !(ok = mbar_wait(bar_turn(1 - x), theirs & 1, p.status))) break;
           tc_fence_after();
           const int slot = (2 * j + 1) % L::kSlots;
           const uint64_t vd = sdesc_add(v_desc, slot * L::kTile);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
             mma_ts(tm_o, tm_p + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+          if (j + 1 < nx) issue_s(j + 1);
+          mbar_arrive(bar_turn(x));
           tc_commit(bar_pv(x));
           tc_commit(bar_empty(slot));
-          if (j + 1 < nx) issue_s(j + 1);
+          if (j + 1 < nx) {
+            tc_commit(bar_s(x));
+            tc_commit(bar_empty((2 * j + 2) % L::kSlots));
+          }
         }
         // tiles that only the other one sees: released as they land, phase by phase
         for (int i = 2 * nx; ok && i < 2 * n; ++i) {
@@ -288,15 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
             prefill::tmem_ld_wait_tied(cur);
             if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
-            float v[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(cur[e]);
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
 #pragma unroll
-              for (int f = 0; f < 4; ++f) mx[f] = prefill::fmax3(mx[f], v[e + f], v[e + 4 + f]);
+              for (int f = 0; f < 4; ++f)
+                mx[f] = prefill::fmax3(mx[f], __uint_as_float(cur[e + f]), __uint_as_float(cur[e + 4 + f]));
             }
-            weigh<BF16>(v, a, m, sum, &pk[c * 16]);
+            weigh<BF16, false>(cur, 32, a, m, sum, &pk[c * 16]);
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a;
           if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
@@ -311,16 +321,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!done) {
-          // masked keys, a first tile, or a maximum that grew: its maximum first, then its weights
+          // masked keys, a first tile, or a maximum that grew: its maximum first, then its weights.
+          // Thirty-two columns that a whole warp sees, or that none of its rows sees, need no look at
+          // each (a warp's rows are few query tokens, so that is most of them).
           float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t raw[32];
-            tmem_ld32(tm_s + c * 32, raw);
-            prefill::tmem_ld_wait_tied(raw);
-            const int left = key_lim - (key0 + c * 32);
+          uint32_t ra[32], rb[32];
+          tmem_ld32(tm_s, ra);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(raw[e]) * a : -INFINITY);
+          for (int c = 0; c < kKeys / 32; ++c) {
+            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+            prefill::tmem_ld_wait_tied(cur);
+            if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
+            const int left = key_lim - (key0 + c * 32);
+            if (__all_sync(0xffffffffu, left >= 32)) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                top = prefill::fmax3(top, __uint_as_float(cur[e]) * a, __uint_as_float(cur[e + 1]) * a);
+            } else if (__any_sync(0xffffffffu, left > 0)) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(cur[e]) * a : -INFINITY);
+            }
           }
           const float m_new = fmaxf(m, top);
           const bool need = valid && m_new > m + kRescaleLog2;
@@ -339,17 +360,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float m_use = m == -INFINITY ? 0.f : m;
           float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t raw[32], pk[16];
-            tmem_ld32(tm_s + c * 32, raw);
-            prefill::tmem_ld_wait_tied(raw);
-            const int left = key_lim - (key0 + c * 32);
-            float v[32];
+          tmem_ld32(tm_s, ra);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = e < left ? __uint_as_float(raw[e]) * a : -INFINITY;
-            weigh<BF16>(v, 1.f, m_use, sum, pk);
-            // (P over S: P's 32 columns so far are no more than the scores already read)
+          for (int c = 0; c < kKeys / 32; ++c) {
+            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+            uint32_t pk[16];
+            prefill::tmem_ld_wait_tied(cur);
+            if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
+            const int left = key_lim - (key0 + c * 32);
+            if (__any_sync(0xffffffffu, left > 0)) {
+              weigh<BF16, true>(cur, left, a, m_use, sum, pk);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) pk[e] = 0u;
+            }
+            // (P over S: P's columns so far are no more than the scores already in registers)
             tmem_st16(tm_p + c * 16, pk);
           }
           l += sum.x + sum.y;
