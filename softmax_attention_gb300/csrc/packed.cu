@@ -24,8 +24,12 @@
 // and the 64 registers of packed P are held, and the maximum is not in the way of the first
 // exponential.
 //
-// Warps (352 threads): 0-3 softmax A, 4-7 softmax B, 8 copies, 9 issuer A (and tensor memory), 10
-// issuer B.
+// A block stays for all of its work items: while one ends, the copies and the first scores of the
+// next are under way, so that only its first item pays for set-up and an empty pipe (packed.cuh
+// says how the items are dealt out).
+//
+// Warps (384 threads): 0-3 softmax A, 4-7 softmax B, 8 copies, 9 issuer A (and tensor memory), 10
+// issuer B, 11 finds the work items and clears what a last V tile holds past its sequence's end.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -40,7 +44,8 @@ namespace {
 using prefill::kLn2;
 using prefill::kRescaleLog2;
 
-constexpr int kThreads = 352;
+constexpr int kThreads = 384;
+constexpr int kItems = 4;  // work items on their way from the scheduling warp to the others
 
 template <int D>
 struct Layout {
@@ -49,8 +54,9 @@ struct Layout {
   static constexpr int kTile = kBlock * (D / 64);     // a Q tile, or a ring slot of K or V
   static constexpr int kRing = 2 * kTile;
   static constexpr int kBars = kRing + kSlots * kTile;
-  // q[2], full[slots], empty[slots], tail, s[2], p[2], pv[2], done[2], turn[2]
-  static constexpr int kNumBars = 2 * kSlots + 13;
+  // full[slots], empty[slots], tail, q[2], q_free[2], s[2], p[2], pv[2], o_free[2], done[2],
+  // item[items], item_read[items]
+  static constexpr int kNumBars = 2 * kSlots + 15 + 2 * kItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;  // room to align the base
   // tensor memory columns
   static constexpr bool kApart = D == 64;             // P beside S
@@ -60,15 +66,15 @@ struct Layout {
 };
 
 struct Tile {
-  int q0, n;  // first query of the tile in its sequence, KV tiles that it sees
+  int q0, end, n;  // first query in its sequence, keys that it sees, KV tiles
 };
 
 __device__ __forceinline__ Tile make_tile(const Params& p, const Seq& s, int q0) {
-  Tile t{q0, 0};
+  Tile t{q0, 0, 0};
   if (q0 < s.nq) {
     const int last = min(s.nq, q0 + p.q_per_tile) - 1;
-    const int end = p.causal ? min(s.nk, max(0, last + s.nk - s.nq + 1)) : s.nk;
-    t.n = (end + kKeys - 1) / kKeys;
+    t.end = p.causal ? min(s.nk, max(0, last + s.nk - s.nq + 1)) : s.nk;
+    t.n = (t.end + kKeys - 1) / kKeys;
   }
   return t;
 }
@@ -88,6 +94,151 @@ __device__ __forceinline__ void weigh(const uint32_t (&x)[32], int left, float a
   }
 }
 
+// The barriers, by their addresses.
+template <int D>
+struct Bars {
+  using L = Layout<D>;
+  uint32_t at;
+  __device__ __forceinline__ uint32_t one(int i) const { return at + 8u * i; }
+  __device__ __forceinline__ uint32_t full(int slot) const { return one(slot); }
+  __device__ __forceinline__ uint32_t empty(int slot) const { return one(L::kSlots + slot); }
+  __device__ __forceinline__ uint32_t tail() const { return one(2 * L::kSlots); }
+  __device__ __forceinline__ uint32_t q(int x) const { return one(2 * L::kSlots + 1 + x); }
+  __device__ __forceinline__ uint32_t q_free(int x) const { return one(2 * L::kSlots + 3 + x); }
+  __device__ __forceinline__ uint32_t s(int x) const { return one(2 * L::kSlots + 5 + x); }
+  __device__ __forceinline__ uint32_t p(int x) const { return one(2 * L::kSlots + 7 + x); }
+  __device__ __forceinline__ uint32_t pv(int x) const { return one(2 * L::kSlots + 9 + x); }
+  __device__ __forceinline__ uint32_t o_free(int x) const { return one(2 * L::kSlots + 11 + x); }
+  __device__ __forceinline__ uint32_t done(int x) const { return one(2 * L::kSlots + 13 + x); }
+  __device__ __forceinline__ uint32_t item(int i) const { return one(2 * L::kSlots + 15 + i); }
+  __device__ __forceinline__ uint32_t item_read(int i) const { return one(2 * L::kSlots + 15 + kItems + i); }
+};
+
+// The k-th item, copied from its place in shared memory; false: no more, or a wait ran out.
+template <int D>
+__device__ __forceinline__ bool next_item(const Bars<D>& bars, const Item* items, int k, Item& item, uint32_t* status) {
+  if (!mbar_wait(bars.item(k % kItems), (k / kItems) & 1, status)) return false;
+  item = items[k % kItems];
+  mbar_arrive(bars.item_read(k % kItems));
+  return item.at >= 0;
+}
+
+// The issuing warp of tile X.  All lanes wait, one issues; the order of the waits puts the last one to
+// come true, for P, in front of the products.
+template <int D, bool BF16, int X>
+__device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t bar_base, uint32_t tmem,
+                                      const Item* items, volatile int* turns) {
+  using L = Layout<D>;
+  const Bars<D> bars{bar_base};
+  tmem = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+  constexpr uint32_t idesc_s = idesc_f16(BF16, kRows, kKeys, false, false);
+  constexpr uint32_t idesc_o = idesc_f16(BF16, kRows, D, false, true);
+  const bool leader = (threadIdx.x & 31) == 0;
+  const uint64_t q_desc = sdesc_sw128(s_base + X * L::kTile, 16, 1024);
+  const uint64_t k_desc = sdesc_sw128(s_base + L::kRing, 16, 1024);
+  const uint64_t v_desc = sdesc_sw128(s_base + L::kRing, L::kBlock, 1024);
+  const uint32_t tm_o = tmem + X * D, tm_s = tmem + L::kS + X * kKeys, tm_p = tmem + L::kP + X * L::kPStep;
+  bool ok = true;
+  auto wait = [&](uint32_t bar, int phase) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
+    return ok;
+  };
+  auto issue_s = [&](int slot) {
+    const uint64_t kd = sdesc_add(k_desc, slot * L::kTile);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = (kk / 4) * L::kBlock + (kk % 4) * 32;
+      mma_ss(tm_s, sdesc_add(q_desc, off), sdesc_add(kd, off), idesc_s, kk > 0 ? 1u : 0u);
+    }
+  };
+  int slot = 0, lap = 0;  // the ring entry that comes next, and how often the ring has been gone through
+  auto next = [&]() {
+    if (++slot == L::kSlots) {
+      slot = 0;
+      ++lap;
+    }
+  };
+  int uses = 0, steps = 0, theirs = 0;  // items and KV tiles of this tile, KV tiles of the other
+  for (int k = 0; ok; ++k) {
+    Item got{};
+    bool more = false;
+    if (__all_sync(0xffffffffu, mbar_wait(bars.item(k % kItems), (k / kItems) & 1, p.status))) {
+      got = items[k % kItems];
+      __syncwarp();
+      if (leader) mbar_arrive(bars.item_read(k % kItems));
+      more = got.at >= 0;
+    }
+    if (!__any_sync(0xffffffffu, more)) break;
+    const Tile tile_a = make_tile(p, got.seq, got.at), tile_b = make_tile(p, got.seq, got.at + p.q_per_tile);
+    const int nx = uniform(X ? tile_b.n : tile_a.n), other_n = uniform(X ? tile_a.n : tile_b.n);
+    const int n = max(nx, other_n), end = uniform(X ? tile_b.end : tile_a.end);
+    if (nx > 0) {
+      if (!wait(bars.q(X), uses) || !wait(bars.full(slot), lap)) break;
+      tc_fence_after();
+      if (leader) {
+        issue_s(slot);
+        tc_commit(bars.s(X));
+        tc_commit(bars.empty(slot));
+        if (nx == 1) tc_commit(bars.q_free(X));
+      }
+      next();
+    }
+    for (int j = 0; j < nx; ++j) {
+      const int v_slot = slot, v_lap = lap;
+      next();
+      if (!wait(bars.full(v_slot), v_lap)) break;
+      if (j + 1 < nx && !wait(bars.full(slot), lap)) break;
+      // O of the item before has to be read before the first product overwrites it
+      if (j == 0 && uses > 0 && !wait(bars.o_free(X), uses - 1)) break;
+      // The other tile's turn first: its j-th pair of products before B's, its (j-1)-th before A's.  An
+      // order to keep the tiles out of step, nothing that a result depends on: so the wait may give up.
+      const int want = theirs + min(other_n, X ? j + 1 : j);
+      for (int spin = 0; spin < 4096 && turns[1 - X] < want; ++spin) {}
+      if (!wait(bars.p(X), steps + j)) break;
+      tc_fence_after();
+      if (leader) {
+        const uint64_t vd = sdesc_add(v_desc, v_slot * L::kTile);
+        // of the last tile, no more keys than the tile sees
+        const int ksteps = min(kKeys / 16, (end - j * kKeys + 15) / 16);
+        if (ksteps == kKeys / 16) {
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ts(tm_o, tm_p + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        } else {
+          for (int kk = 0; kk < ksteps; ++kk)
+            mma_ts(tm_o, tm_p + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
+        }
+        if (j + 1 < nx) issue_s(slot);
+        turns[X] = steps + j + 1;  // (before the commits: after them the store would wait for the products)
+        tc_commit(bars.pv(X));
+        tc_commit(bars.empty(v_slot));
+        if (j + 1 < nx) {
+          tc_commit(bars.s(X));
+          tc_commit(bars.empty(slot));
+          if (j + 2 == nx) tc_commit(bars.q_free(X));
+        }
+      }
+      __syncwarp();
+      if (j + 1 < nx) next();
+    }
+    if (!ok) break;
+    // tiles that only the other one sees: released as they land, phase by phase
+    for (int i = 2 * nx; i < 2 * n; ++i) {
+      if (!wait(bars.full(slot), lap)) break;
+      if (leader) mbar_arrive(bars.empty(slot));
+      next();
+    }
+    steps += nx;
+    theirs += other_n;
+    uses += nx > 0 ? 1 : 0;
+  }
+  // every product must finish before tensor memory and the ring are given up
+  if (leader) {
+    tc_commit(bars.done(X));
+    mbar_wait(bars.done(X), 0, nullptr);
+  }
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -97,50 +248,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ uint32_t tmem_slot;
-  __shared__ int item[2];
+  __shared__ Item items[kItems];
+  __shared__ int turns[2];  // pairs of products that each tile's issuer has put into the pipe
   const uint32_t s_base = smem_addr(smem);
-  const uint32_t bars = s_base + L::kBars;
-  auto bar_q = [&](int x) { return bars + 8u * x; };
-  auto bar_full = [&](int s) { return bars + 8u * (2 + s); };
-  auto bar_empty = [&](int s) { return bars + 8u * (2 + L::kSlots + s); };
-  const uint32_t bar_tail = bars + 8u * (2 + 2 * L::kSlots);
-  auto bar_s = [&](int x) { return bar_tail + 8u * (1 + x); };
-  auto bar_p = [&](int x) { return bar_tail + 8u * (3 + x); };
-  auto bar_pv = [&](int x) { return bar_tail + 8u * (5 + x); };
-  auto bar_done = [&](int x) { return bar_tail + 8u * (7 + x); };
-  auto bar_turn = [&](int x) { return bar_tail + 8u * (9 + x); };
-
+  const Bars<D> bars{s_base + L::kBars};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = blockIdx.x % p.Hkv;
-  if (warp == 0) {
-    const int width = 2 * p.q_per_tile;
-    int b, t;
-    find_item(p.B, blockIdx.x / p.Hkv, !p.causal, [&](int s, int& n, int& first) {
-      const Seq q = load_seq(p, s);
-      n = (q.nq + width - 1) / width;
-      first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / width;
-    }, b, t);
-    if (lane == 0) {
-      item[0] = b;
-      item[1] = t;
-    }
-  } else if (warp == 9) {
+  if (warp == 9) {
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   } else if (threadIdx.x == 8 * 32) {
     for (int x = 0; x < 2; ++x) {
-      mbar_init(bar_q(x), 1);
-      mbar_init(bar_s(x), 1);
-      mbar_init(bar_p(x), 128);
-      mbar_init(bar_pv(x), 1);
-      mbar_init(bar_done(x), 1);
-      mbar_init(bar_turn(x), 1);
+      mbar_init(bars.q(x), 1);
+      mbar_init(bars.q_free(x), 1);
+      mbar_init(bars.s(x), 1);
+      mbar_init(bars.p(x), 128);
+      mbar_init(bars.pv(x), 1);
+      mbar_init(bars.o_free(x), 128);
+      mbar_init(bars.done(x), 1);
+      turns[x] = 0;
     }
     for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 2);  // both tiles
+      mbar_init(bars.full(s), 1);
+      mbar_init(bars.empty(s), 2);  // both tiles
     }
-    mbar_init(bar_tail, 1);
+    mbar_init(bars.tail(), 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bars.item(i), 1);
+      mbar_init(bars.item_read(i), 256 + 3);  // softmax, issuers, copies
+    }
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_k);
@@ -150,140 +285,133 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int b = item[0];
-  if (b >= 0) {
-    const Seq seq = load_seq(p, b);
-    const int q0 = item[1] * 2 * p.q_per_tile;
-    const Tile tile_a = make_tile(p, seq, q0), tile_b = make_tile(p, seq, q0 + p.q_per_tile);
-    const int n = max(tile_a.n, tile_b.n);  // KV tiles through the ring
-    if (warp == 8) {
-      // ---------------------------------- copies ----------------------------------------
-      bool ok = true;
-      int issued = 0;
-      const bool tail = n > 0 && n * kKeys > seq.nk;  // the last V tile reaches past the sequence
-      if (lane == 0 && n > 0) {
-        for (int x = 0; x < 2; ++x) {
-          const Tile tile = x ? tile_b : tile_a;
-          if (tile.n == 0) continue;
-          mbar_arrive_expect_tx(bar_q(x), static_cast<uint32_t>(128 * (D / 64) * p.G * p.q_per_tile));
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(s_base + x * L::kTile + kb * L::kBlock, &tm_q, bar_q(x), kb * 64, hk * p.G,
-                        seq.q0 + tile.q0);
+  if (warp == 11) {
+    // ------------------------------ work items, V's last rows --------------------------------
+    const int width = 2 * p.q_per_tile;
+    auto pieces = [&](int s, int& n, int& first) {
+      const Seq q = load_seq(p, s);
+      n = (q.nq + width - 1) / width;
+      first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / width;
+    };
+    const Finder finder(p.B, !p.causal, pieces);
+    int entries = 0, tails = 0;     // ring entries of the items so far; V tiles cleared
+    int clear_at = -1, clear_row = 0;  // the item before: entry of its last V tile, first row to clear
+    bool ok = true, more = true;
+    for (int k = 0; ok && (more || clear_at >= 0); ++k) {
+      Item item{};
+      item.at = -1;
+      if (more) {
+        const int w = dealt(k);
+        int b, t;
+        finder.find(w / p.Hkv, pieces, b, t);
+        if (b >= 0) {
+          item.seq = load_seq(p, b);
+          item.at = t * width;
+          item.head = w % p.Hkv;
         }
-        for (int i = 0; i < 2 * n; ++i) {  // K_0, V_0, K_1, V_1, ...
-          const int slot = i % L::kSlots;
-          if (i >= L::kSlots && !(ok = mbar_wait(bar_empty(slot), (i / L::kSlots - 1) & 1, p.status))) break;
-          const uint32_t bar = tail && i == 2 * n - 1 ? bar_tail : bar_full(slot);
-          mbar_arrive_expect_tx(bar, L::kTile);
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(s_base + L::kRing + slot * L::kTile + kb * L::kBlock, (i & 1) ? &tm_v : &tm_k, bar,
-                        kb * 64, hk, seq.k0 + (i / 2) * kKeys);
-          issued = i + 1;
+        if (k >= kItems) ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read(k % kItems), (k / kItems - 1) & 1, p.status));
+        if (ok && lane == 0) {
+          items[k % kItems] = item;
+          mbar_arrive(bars.item(k % kItems));
         }
+        more = b >= 0;
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (ok && tail) {
-        // Rows past the sequence's end hold another sequence's values, or none: P is 0 there, but
-        // 0 times an infinity or NaN would spoil O.
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_tail, 0, p.status));
-        const int slot = (2 * n - 1) % L::kSlots, r0 = seq.nk - (n - 1) * kKeys;
-        uint8_t* v = smem + L::kRing + slot * L::kTile;
-        if (ok) {
-          for (int i = lane; i < (kKeys - r0) * 8 * (D / 64); i += 32) {
-            const int kb = i / ((kKeys - r0) * 8), at = i % ((kKeys - r0) * 8);
-            *reinterpret_cast<uint4*>(v + kb * L::kBlock + r0 * 128 + at * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
+      if (ok && clear_at >= 0) {
+        // Rows past the sequence's end hold another sequence's values, or none: P is 0 there, but 0
+        // times an infinity or NaN would spoil O.
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
+        ++tails;
+        uint8_t* v = smem + L::kRing + (clear_at % L::kSlots) * L::kTile;
+        const int per = (kKeys - clear_row) * 8;
+        if (ok)
+          for (int i = lane; i < per * (D / 64); i += 32)
+            *reinterpret_cast<uint4*>(v + (i / per) * L::kBlock + clear_row * 128 + (i % per) * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar_full(slot));
+        if (ok && lane == 0) mbar_arrive(bars.full(clear_at % L::kSlots));
+        clear_at = -1;
       }
-      if (lane == 0 && issued < 2 * n) {
-        // A wait ran out: let the copies in flight land before the CTA ends.  Each of these is the
-        // last copy into its slot, so its phase is the barrier's current one.
-        for (int x = 0; x < 2; ++x)
-          if ((x ? tile_b.n : tile_a.n) > 0) mbar_wait(bar_q(x), 0, nullptr);
-        for (int i = max(0, issued - L::kSlots); i < issued; ++i)
-          mbar_wait(bar_full(i % L::kSlots), (i / L::kSlots) & 1, nullptr);
+      if (item.at >= 0) {
+        const int n = max(make_tile(p, item.seq, item.at).n, make_tile(p, item.seq, item.at + p.q_per_tile).n);
+        entries += 2 * n;
+        if (n * kKeys > item.seq.nk && n > 0) {
+          clear_at = entries - 1;
+          clear_row = item.seq.nk - (n - 1) * kKeys;
+        }
       }
-    } else if (warp >= 9) {
-      // ---------------------------------- issuers ---------------------------------------
-      const int x = warp - 9, nx = x ? tile_b.n : tile_a.n, other_n = x ? tile_a.n : tile_b.n;
-      if (lane == 0 && n > 0) {
-        constexpr uint32_t idesc_s = idesc_f16(BF16, kRows, kKeys, false, false);
-        constexpr uint32_t idesc_o = idesc_f16(BF16, kRows, D, false, true);
-        const uint64_t q_desc = sdesc_sw128(s_base + x * L::kTile, 16, 1024);
-        const uint64_t k_desc = sdesc_sw128(s_base + L::kRing, 16, 1024);
-        const uint64_t v_desc = sdesc_sw128(s_base + L::kRing, L::kBlock, 1024);
-        const uint32_t tm_o = tmem + x * D, tm_s = tmem + L::kS + x * kKeys, tm_p = tmem + L::kP + x * L::kPStep;
-        auto issue_s = [&](int j) {
-          const int slot = (2 * j) % L::kSlots;
-          const uint64_t kd = sdesc_add(k_desc, slot * L::kTile);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk / 4) * L::kBlock + (kk % 4) * 32;
-            mma_ss(tm_s, sdesc_add(q_desc, off), sdesc_add(kd, off), idesc_s, kk > 0 ? 1u : 0u);
-          }
-        };
-        auto full = [&](int i) { return mbar_wait(bar_full(i % L::kSlots), (i / L::kSlots) & 1, p.status); };
-        bool ok = true;
-        if (nx > 0) {
-          ok = mbar_wait(bar_q(x), 0, p.status) && full(0);
-          if (ok) {
-            tc_fence_after();
-            issue_s(0);
-            tc_commit(bar_s(x));
-            tc_commit(bar_empty(0));
-          }
-        }
-        for (int j = 0; ok && j < nx; ++j) {
-          if (!(ok = mbar_wait(bar_p(x), j & 1, p.status))) break;
-          if (!(ok = full(2 * j + 1))) break;
-          if (j + 1 < nx && !(ok = full(2 * j + 2))) break;
-          // the other tile's turn before this one: its j-th pair of products for B, its (j-1)-th for A
-          const int theirs = x ? j : j - 1;
-          if (theirs >= 0 && theirs < other_n && !(ok = mbar_wait(bar_turn(1 - x), theirs & 1, p.status))) break;
-          tc_fence_after();
-          const int slot = (2 * j + 1) % L::kSlots;
-          const uint64_t vd = sdesc_add(v_desc, slot * L::kTile);
-#pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
-            mma_ts(tm_o, tm_p + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-          if (j + 1 < nx) issue_s(j + 1);
-          mbar_arrive(bar_turn(x));
-          tc_commit(bar_pv(x));
-          tc_commit(bar_empty(slot));
-          if (j + 1 < nx) {
-            tc_commit(bar_s(x));
-            tc_commit(bar_empty((2 * j + 2) % L::kSlots));
-          }
-        }
-        // tiles that only the other one sees: released as they land, phase by phase
-        for (int i = 2 * nx; ok && i < 2 * n; ++i) {
-          if (!(ok = full(i))) break;
-          mbar_arrive(bar_empty(i % L::kSlots));
-        }
-        // every product must finish before tensor memory and the ring are given up
-        tc_commit(bar_done(x));
-        mbar_wait(bar_done(x), 0, nullptr);
-      }
-    } else {
-      // --------------------------- softmax, epilogue: a row a thread ---------------------
-      const int x = warp / 4, r = threadIdx.x % 128;
-      const Tile tile = x ? tile_b : tile_a;
-      const int nx = tile.n;
-      const int i = tile.q0 + r / p.G, h = hk * p.G + r % p.G;
-      const bool valid = r < p.G * p.q_per_tile && i < seq.nq;
-      // a row of no query sees everything, so that it never asks for the slow path
-      const int key_lim = !valid ? 0x7fffffff : p.causal ? min(seq.nk, i + seq.nk - seq.nq + 1) : seq.nk;
-      const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-      const uint32_t tm_o = tmem + x * D + lanes, tm_s = tmem + L::kS + x * kKeys + lanes;
-      const uint32_t tm_p = tmem + L::kP + x * L::kPStep + lanes;
-      const float a = p.scale_log2;
-      float m = -INFINITY, l = 0.f;
+    }
+  } else if (warp == 8) {
+    // ---------------------------------- copies ----------------------------------------------
+    if (lane == 0) {
       bool ok = true;
-      for (int j = 0; j < nx; ++j) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s(x), j & 1, p.status));
+      int entry = 0, q_uses[2] = {0, 0};
+      int tail_at = -1, tails = 0;  // the last entry that lands on the tail's barrier; how many did
+      Item item;
+      for (int k = 0; ok && next_item(bars, items, k, item, p.status); ++k) {
+        const Tile tile_a = make_tile(p, item.seq, item.at), tile_b = make_tile(p, item.seq, item.at + p.q_per_tile);
+        const int n = max(tile_a.n, tile_b.n);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const Tile tile = x ? tile_b : tile_a;
+          if (!ok || tile.n == 0) continue;
+          if (q_uses[x] > 0 && !(ok = mbar_wait(bars.q_free(x), (q_uses[x] - 1) & 1, p.status))) continue;
+          mbar_arrive_expect_tx(bars.q(x), static_cast<uint32_t>(128 * (D / 64) * p.G * p.q_per_tile));
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(s_base + x * L::kTile + kb * L::kBlock, &tm_q, bars.q(x), kb * 64, item.head * p.G,
+                        item.seq.q0 + tile.q0);
+          ++q_uses[x];
+        }
+        const bool tail = n > 0 && n * kKeys > item.seq.nk;  // the last V tile reaches past the sequence
+        for (int i = 0; ok && i < 2 * n; ++i, ++entry) {      // K_0, V_0, K_1, V_1, ...
+          const int slot = entry % L::kSlots;
+          if (entry >= L::kSlots && !(ok = mbar_wait(bars.empty(slot), (entry / L::kSlots - 1) & 1, p.status))) break;
+          const bool to_tail = tail && i == 2 * n - 1;
+          const uint32_t bar = to_tail ? bars.tail() : bars.full(slot);
+          if (to_tail) {
+            tail_at = entry;
+            ++tails;
+          }
+          mbar_arrive_expect_tx(bar, L::kTile);
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(s_base + L::kRing + slot * L::kTile + kb * L::kBlock, (i & 1) ? &tm_v : &tm_k, bar, kb * 64,
+                        item.head, item.seq.k0 + (i / 2) * kKeys);
+        }
+      }
+      if (!ok) {
+        // A wait ran out: let the copies in flight land before the block ends
+        for (int x = 0; x < 2; ++x)
+          if (q_uses[x] > 0) mbar_wait(bars.q(x), (q_uses[x] - 1) & 1, nullptr);
+        for (int i = max(0, entry - L::kSlots); i < entry; ++i) {
+          if (i == tail_at) mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
+          else mbar_wait(bars.full(i % L::kSlots), (i / L::kSlots) & 1, nullptr);
+        }
+      }
+    }
+  } else if (warp == 9) {
+    issue<D, BF16, 0>(p, s_base, bars.at, tmem, items, turns);
+  } else if (warp == 10) {
+    issue<D, BF16, 1>(p, s_base, bars.at, tmem, items, turns);
+  } else {
+    // --------------------------- softmax, epilogue: a row a thread ---------------------------
+    const int x = warp / 4, r = threadIdx.x % 128;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tm_o = tmem + x * D + lanes, tm_s = tmem + L::kS + x * kKeys + lanes;
+    const uint32_t tm_p = tmem + L::kP + x * L::kPStep + lanes;
+    const float a = p.scale_log2;
+    const int row_token = r / p.G, row_head = r % p.G;
+    bool ok = true;
+    int steps = 0;  // KV tiles of this query tile so far
+    Item item;
+    for (int k = 0; ok && __all_sync(0xffffffffu, next_item(bars, items, k, item, p.status)); ++k) {
+      const Tile tile = make_tile(p, item.seq, item.at + x * p.q_per_tile);
+      const int nx = tile.n;
+      const int i = tile.q0 + row_token, h = item.head * p.G + row_head;
+      const bool valid = r < p.G * p.q_per_tile && i < item.seq.nq;
+      // a row of no query sees everything, so that it never asks for the slow path
+      const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nx; ++j, ++steps) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
         if (!ok) break;
         tc_fence_after();
         const int key0 = j * kKeys;
@@ -312,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
             l += sum.x + sum.y;
             if (L::kApart && j > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(bar_pv(x), (j - 1) & 1, p.status));
+              ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
               if (!ok) break;
               tc_fence_after();
             }
@@ -353,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j > 0) {
             // P_{j-1} V_{j-1} has to be in O before O is rescaled, and P_{j-1} read before P_j
-            ok = __all_sync(0xffffffffu, mbar_wait(bar_pv(x), (j - 1) & 1, p.status));
+            ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
             if (!ok) break;
             tc_fence_after();
             if (__any_sync(0xffffffffu, need)) prefill::rescale_o<D>(tm_o, alpha);
@@ -382,39 +510,42 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_p(x));
+        mbar_arrive(bars.p(x));
       }
       if (ok && nx > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_pv(x), (nx - 1) & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
         tc_fence_after();
       }
-      if (ok) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int64_t row = seq.q0 + i;
-        uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1];
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (nx > 0) {
-            tmem_ld32(tm_o + c * 32, o);
-            prefill::tmem_ld_wait_tied(o);
-          } else {
+      if (!ok) break;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const int64_t row = item.seq.q0 + i;
+      uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (nx > 0) {
+          tmem_ld32(tm_o + c * 32, o);
+          prefill::tmem_ld_wait_tied(o);
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            mbar_arrive(bars.o_free(x));
           }
-          if (!valid) continue;
-          uint32_t w[16];
+        } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float f = __uint_as_float(o[2 * e]) * inv, g = __uint_as_float(o[2 * e + 1]) * inv;
-            w[e] = BF16 ? pack_bf16x2(f, g) : pack_f16x2(f, g);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint4*>(dst + c * 32)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (valid && p.lse) p.lse[row * p.Hq + h] = prefill::row_lse(m, l);
+        if (!valid) continue;
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float f = __uint_as_float(o[2 * e]) * inv, g = __uint_as_float(o[2 * e + 1]) * inv;
+          w[e] = BF16 ? pack_bf16x2(f, g) : pack_f16x2(f, g);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<uint4*>(dst + c * 32)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
       }
+      if (valid && p.lse) p.lse[row * p.Hq + h] = prefill::row_lse(m, l);
     }
   }
   tc_fence_before();
@@ -432,7 +563,8 @@ cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tk
   auto kern = forward_kernel<D, BF16>;
   cudaError_t e = ensure_smem_limit(kern, Layout<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  kern<<<static_cast<unsigned>(items * p.Hkv), kThreads, Layout<D>::kAlloc, stream>>>(tq, tk, tv, p);
+  const int64_t work = items * p.Hkv, sms = num_sms() > 0 ? num_sms() : 152;
+  kern<<<static_cast<unsigned>(work < sms ? work : sms), kThreads, Layout<D>::kAlloc, stream>>>(tq, tk, tv, p);
   return cudaGetLastError();
 }
 
@@ -459,7 +591,7 @@ int check_sizes(const char* who, int B, int Hq, int Hkv, int D, int total_q, int
   if (!(scale == scale) || isinf(scale)) return fail(FA_ERR_INVALID_ARG, "%s: scale must be finite", who);
   const int64_t width = kRows / (Hq / Hkv);
   const int64_t most = most_items(total_q, B, width), keys = most_items(total_k, B, kKeys);
-  if ((most > keys ? most : keys) * Hkv > 2147483647LL)
+  if ((most > keys ? most : keys) * Hkv > (1LL << 30))
     return fail(FA_ERR_UNSUPPORTED, "%s: too many tiles for one launch", who);
   return FA_OK;
 }

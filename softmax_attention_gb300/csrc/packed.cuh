@@ -53,93 +53,115 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
 }
 
 // Work items.  Sequence s is cut into items(s) pieces, and a piece's work grows with its index t:
-// its level is first(s) + t, or first(s) for all pieces where `flat`.  Blocks take the pieces in
-// decreasing level over all sequences, so that the last blocks to start are short ones; nothing
-// but the order depends on it.  The piece of a rank is found by each block itself: a binary search
-// for the rank's level, a warp's lanes holding up to four sequences each (a few hundred clocks
-// beside the block's set-up; no list, no kernel before this one).  Past 128 sequences the pieces
-// are taken sequence by sequence.  One whole warp calls; b = -1 where the rank is past the end.
-template <typename Items>
-__device__ __forceinline__ void find_item(int B, int rank, bool flat, Items items, int& b, int& t) {
-  const int lane = threadIdx.x & 31;
-  b = -1;
-  t = 0;
-  if (B == 1) {
-    int n, first;
-    items(0, n, first);
-    if (rank < n) {
-      b = 0;
-      t = n - 1 - rank;
+// its level is first(s) + t, or first(s) for all pieces where `flat`.  The pieces are taken in
+// decreasing level over all sequences, dealt out to the blocks there and back (block i of n takes the
+// ranks i, 2n-1-i, 2n+i, ...), so that every block gets about the same work and the last pieces are
+// short ones; nothing but the order depends on it.  Each block finds its pieces by itself: a binary
+// search for a rank's level, a warp's lanes holding up to four sequences each, a few hundred
+// clocks in a warp with nothing else to do; no list, no kernel before this one.  Past 128 sequences
+// the pieces are taken sequence by sequence.
+class Finder {
+ public:
+  template <typename Items>
+  __device__ __forceinline__ Finder(int B, bool flat, Items items) : B_(B), flat_(flat), top_(0) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+      n_[i] = first_[i] = 0;
+      if (B <= 32 * kHeld && 32 * i + lane < B) items(32 * i + lane, n_[i], first_[i]);
+      if (n_[i] > 0) top_ = max(top_, flat ? first_[i] : first_[i] + n_[i] - 1);
     }
-    return;
+    top_ = __reduce_max_sync(0xffffffffu, top_);
   }
-  int before = 0;  // pieces in front of those looked at
-  constexpr int kHeld = 4;
-  if (B <= 32 * kHeld) {
-    int n[kHeld], first[kHeld], top = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      n[i] = first[i] = 0;
-      if (32 * i + lane < B) items(32 * i + lane, n[i], first[i]);
-      if (n[i] > 0) top = max(top, flat ? first[i] : first[i] + n[i] - 1);
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    auto at_least = [&](int level) {  // pieces of this level or above
-      int c = 0;
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i)
-        c += flat ? (first[i] >= level ? n[i] : 0) : min(n[i], max(0, first[i] + n[i] - level));
-      return __reduce_add_sync(0xffffffffu, c);
-    };
-    if (rank >= at_least(0)) return;
-    int low = 0, high = top + 1;  // at_least(low) > rank >= at_least(high)
-    while (high - low > 1) {
-      const int mid = (low + high) / 2;
-      if (at_least(mid) > rank) low = mid;
-      else high = mid;
-    }
-    rank -= at_least(high);
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-      const int here = flat ? (first[i] == low ? n[i] : 0) : (low >= first[i] && low < first[i] + n[i] ? 1 : 0);
-      int upto = here;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int other = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o) upto += other;
+
+  // The piece of a rank: sequence b and index t; b = -1 past the end.  The whole warp calls.
+  template <typename Items>
+  __device__ __forceinline__ void find(int rank, Items items, int& b, int& t) const {
+    const int lane = threadIdx.x & 31;
+    b = -1;
+    t = 0;
+    int before = 0;  // pieces in front of those looked at
+    if (B_ <= 32 * kHeld) {
+      if (rank >= at_least(0)) return;
+      int low = 0, high = top_ + 1;  // at_least(low) > rank >= at_least(high)
+      while (high - low > 1) {
+        const int mid = (low + high) / 2;
+        if (at_least(mid) > rank) low = mid;
+        else high = mid;
       }
-      const bool mine = rank >= before + upto - here && rank < before + upto;
-      const uint32_t who = __ballot_sync(0xffffffffu, mine);
-      if (who) {
-        const int src = __ffs(who) - 1;
-        b = 32 * i + src;
-        t = __shfl_sync(0xffffffffu, flat ? rank - (before + upto - here) : low - first[i], src);
+      rank -= at_least(high);
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i) {
+        const int here = flat_ ? (first_[i] == low ? n_[i] : 0) : (low >= first_[i] && low < first_[i] + n_[i] ? 1 : 0);
+        if (pick(rank, before, here, 32 * i, flat_, low - first_[i], b, t)) return;
+      }
+      return;
+    }
+    for (int base = 0; base < B_; base += 32) {
+      int n = 0, first = 0;
+      if (base + lane < B_) items(base + lane, n, first);
+      if (pick(rank, before, n, base, true, 0, b, t)) {
+        t = __shfl_sync(0xffffffffu, n, b - base) - 1 - t;  // the longest first
         return;
       }
-      before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    return;
   }
-  for (int base = 0; base < B; base += 32) {
-    int n = 0, first = 0;
-    if (base + lane < B) items(base + lane, n, first);
-    int upto = n;
+
+ private:
+  static constexpr int kHeld = 4;
+
+  __device__ __forceinline__ int at_least(int level) const {  // pieces of this level or above
+    int c = 0;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      c += flat_ ? (first_[i] >= level ? n_[i] : 0) : min(n_[i], max(0, first_[i] + n_[i] - level));
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+
+  // Lanes hold the counts `here` of 32 sequences from `base`; if the rank falls among them, its
+  // sequence and its place there (`count`), or that lane's `index`.
+  static __device__ __forceinline__ bool pick(int rank, int& before, int here, int base, bool count, int index, int& b,
+                                              int& t) {
+    const int lane = threadIdx.x & 31;
+    int upto = here;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int other = __shfl_up_sync(0xffffffffu, upto, o);
       if (lane >= o) upto += other;
     }
-    const bool mine = rank >= before + upto - n && rank < before + upto;
-    const uint32_t who = __ballot_sync(0xffffffffu, mine);
-    if (who) {
-      const int src = __ffs(who) - 1;
-      b = base + src;
-      t = __shfl_sync(0xffffffffu, n - 1 - (rank - (before + upto - n)), src);
-      return;
-    }
+    const int from = before + upto - here;
+    const uint32_t who = __ballot_sync(0xffffffffu, rank >= from && rank < from + here);
     before += __shfl_sync(0xffffffffu, upto, 31);
+    if (!who) return false;
+    const int src = __ffs(who) - 1;
+    b = base + src;
+    t = __shfl_sync(0xffffffffu, count ? rank - from : index, src);
+    return true;
   }
+
+  int B_;
+  bool flat_;
+  int top_;
+  int n_[kHeld], first_[kHeld];  // of sequences lane, lane + 32, ...
+};
+
+// The k-th rank of this block, of `blocks` that deal them out there and back.
+__device__ __forceinline__ int dealt(int k) {
+  const int n = gridDim.x, i = blockIdx.x;
+  return k * n + ((k & 1) ? n - 1 - i : i);
 }
+
+// One work item, as the scheduling warp hands it to the others through shared memory.
+struct Item {
+  Seq seq;
+  int at;    // first query, or key, of the piece in its sequence; -1: no more work
+  int head;  // kv head
+};
+
+// A value that is the same in every lane, in a form that the compiler knows to be: the operands of
+// tcgen05.mma are uniform registers, and what it cannot prove uniform is moved there before every
+// product, beside softmax warps that leave an issuing warp few slots.
+__device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // The most pieces of `width` rows that B sequences of `total` rows together can have.
 inline int64_t most_items(int64_t total, int64_t B, int64_t width) {

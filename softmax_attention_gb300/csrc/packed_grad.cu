@@ -149,11 +149,13 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   const int hk = blockIdx.x % p.Hkv;
   if (warp == 0) {
     int b, t;
-    find_item(p.B, blockIdx.x / p.Hkv, !p.causal, [&](int s, int& n, int& first) {
+    auto pieces = [&](int s, int& n, int& first) {
       const Seq q = load_seq(p, s);
       n = (q.nq + p.q_per_tile - 1) / p.q_per_tile;
       first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / p.q_per_tile;
-    }, b, t);
+    };
+    const Finder finder(p.B, !p.causal, pieces);
+    finder.find(blockIdx.x / p.Hkv, pieces, b, t);
     if (lane == 0) {
       item[0] = b;
       item[1] = t;
@@ -462,11 +464,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int used = p.G * p.q_per_tile;  // rows of a query tile
   if (warp == 0) {
     int b, t;
-    find_item(p.B, blockIdx.x / p.Hkv, !p.causal, [&](int s, int& n, int& first) {
+    auto pieces = [&](int s, int& n, int& first) {
       const Seq q = load_seq(p, s);
       n = (q.nk + kKeys - 1) / kKeys;
       first = p.causal ? 0 : q.nq / kKeys;
-    }, b, t);
+    };
+    const Finder finder(p.B, !p.causal, pieces);
+    finder.find(blockIdx.x / p.Hkv, pieces, b, t);
     if (lane == 0) {
       item[0] = b;
       item[1] = t;
