@@ -18,11 +18,10 @@
 // drain the pipe.  S_{j+1} may be issued behind P_j V_j although it overwrites P_j: products of
 // one thread and one shape run in order (D = 64, where the shapes differ, keeps P apart).
 //
-// The softmax works on a row 32 scores at a time against the maximum of the tiles before, and
-// looks for a larger one on the way; only if a row's maximum grew by more than 2^8 (or the tile
-// has masked keys, or is the first) is the tile done in two passes.  So no more than 32 scores
-// and the 64 registers of packed P are held, and the maximum is not in the way of the first
-// exponential.
+// The softmax works on a row 32 scores at a time against the maximum so far (of the first 32 scores
+// to begin with), and looks for a larger one on the way; only if a row's maximum turns out to be more
+// than 2^8 times larger is the tile done again in two passes.  So no more than 64 scores and the 64
+// registers of packed P are held, and the maximum is not in the way of the first exponential.
 //
 // A block stays for all of its work items: while one ends, the copies and the first scores of the
 // next are under way, so that only its first item pays for set-up and an empty pipe (packed.cuh
@@ -49,11 +48,12 @@ constexpr int kItems = 4;  // work items on their way from the scheduling warp t
 
 template <int D>
 struct Layout {
-  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kSlots = D == 128 ? 4 : 8;
   static constexpr int kBlock = kRows * 128;          // 128 rows x 64 columns of 16 bits
   static constexpr int kTile = kBlock * (D / 64);     // a Q tile, or a ring slot of K or V
   static constexpr int kRing = 2 * kTile;
-  static constexpr int kBars = kRing + kSlots * kTile;
+  static constexpr int kStage = kRing + kSlots * kTile;  // 32 rows x 64 columns of each softmax warp's output
+  static constexpr int kBars = kStage + 8 * 32 * 128;
   // full[slots], empty[slots], tail, q[2], q_free[2], s[2], p[2], pv[2], o_free[2], done[2],
   // item[items], item_read[items]
   static constexpr int kNumBars = 2 * kSlots + 15 + 2 * kItems;
@@ -79,16 +79,14 @@ __device__ __forceinline__ Tile make_tile(const Params& p, const Seq& s, int q0)
   return t;
 }
 
-// Thirty-two scores against the maximum m: exponentials packed, their sum added; with MASK the
-// first `left` alone count.
-template <bool BF16, bool MASK>
-__device__ __forceinline__ void weigh(const uint32_t (&x)[32], int left, float a, float m, float2& sum, uint32_t* pk) {
+// Thirty-two scores against the maximum m: exponentials packed, their sum added.
+template <bool BF16>
+__device__ __forceinline__ void weigh(const uint32_t (&x)[32], float a, float m, float2& sum, uint32_t* pk) {
   const float2 a2 = make_float2(a, a), nm = make_float2(-m, -m);
 #pragma unroll
   for (int c = 0; c < 16; ++c) {
     const float2 t = __ffma2_rn(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])), a2, nm);
-    float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
-    if (MASK) e = make_float2(2 * c < left ? e.x : 0.f, 2 * c + 1 < left ? e.y : 0.f);
+    const float2 e = make_float2(exp2_approx(t.x), exp2_approx(t.y));
     sum = __fadd2_rn(sum, e);
     pk[c] = BF16 ? pack_bf16x2(e.x, e.y) : pack_f16x2(e.x, e.y);
   }
@@ -205,6 +203,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
           for (int kk = 0; kk < kKeys / 16; ++kk)
             mma_ts(tm_o, tm_p + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         } else {
+#pragma unroll 1
           for (int kk = 0; kk < ksteps; ++kk)
             mma_ts(tm_o, tm_p + kk * 8, sdesc_add(vd, kk * 2048), idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
         }
@@ -414,9 +413,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
         if (!ok) break;
         tc_fence_after();
-        const int key0 = j * kKeys;
+        const int left = key_lim - j * kKeys;  // keys of the tile that the row sees
         bool done = false;
-        if (__all_sync(0xffffffffu, a > 0.f && key0 + kKeys <= key_lim && (m > -INFINITY || !valid))) {
+        if (a > 0.f) {
+          const bool masked = __any_sync(0xffffffffu, left < kKeys);
+          if (j == 0) {
+            // a first guess at the maximum: that of the first 32 scores
+            uint32_t raw[32];
+            tmem_ld32(tm_s, raw);
+            prefill::tmem_ld_wait_tied(raw);
+            float top = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(raw[e]) : -INFINITY);
+            m = top > -INFINITY ? top * a : 0.f;
+          }
           uint32_t pk[kKeys / 2];
           float2 sum = make_float2(0.f, 0.f);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -428,13 +438,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
             prefill::tmem_ld_wait_tied(cur);
             if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
+            if (masked) {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) cur[e] = 32 * c + e < left ? cur[e] : 0xff800000u;  // -inf
+            }
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
 #pragma unroll
               for (int f = 0; f < 4; ++f)
                 mx[f] = prefill::fmax3(mx[f], __uint_as_float(cur[e + f]), __uint_as_float(cur[e + 4 + f]));
             }
-            weigh<BF16, false>(cur, 32, a, m, sum, &pk[c * 16]);
+            weigh<BF16>(cur, a, m, sum, &pk[c * 16]);
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a;
           if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
@@ -449,33 +463,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!done) {
-          // masked keys, a first tile, or a maximum that grew: its maximum first, then its weights.
-          // Thirty-two columns that a whole warp sees, or that none of its rows sees, need no look at
-          // each (a warp's rows are few query tokens, so that is most of them).
+          // a maximum that grew (or a scale that is not positive): the maximum first, then the weights
           float top = -INFINITY;
-          uint32_t ra[32], rb[32];
-          tmem_ld32(tm_s, ra);
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t raw[32];
+            tmem_ld32(tm_s + c, raw);
+            prefill::tmem_ld_wait_tied(raw);
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
-            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
-            prefill::tmem_ld_wait_tied(cur);
-            if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
-            const int left = key_lim - (key0 + c * 32);
-            if (__all_sync(0xffffffffu, left >= 32)) {
-#pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                top = prefill::fmax3(top, __uint_as_float(cur[e]) * a, __uint_as_float(cur[e + 1]) * a);
-            } else if (__any_sync(0xffffffffu, left > 0)) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(cur[e]) * a : -INFINITY);
-            }
+            for (int e = 0; e < 32; ++e) top = fmaxf(top, c + e < left ? __uint_as_float(raw[e]) * a : -INFINITY);
           }
-          const float m_new = fmaxf(m, top);
-          const bool need = valid && m_new > m + kRescaleLog2;
+          const float before = l > 0.f ? m : -INFINITY;  // (a guess that nothing was added to is none)
+          const float m_new = fmaxf(before, top);
+          const bool need = valid && m_new > before + kRescaleLog2;
           float alpha = 1.f;
           if (need) {
-            alpha = exp2_approx(m - m_new);  // 0 when m is -inf
+            alpha = exp2_approx(before - m_new);  // 0 when nothing was added before
             m = m_new;
             l *= alpha;
           }
@@ -488,23 +491,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float m_use = m == -INFINITY ? 0.f : m;
           float2 sum = make_float2(0.f, 0.f);
-          tmem_ld32(tm_s, ra);
+#pragma unroll 1
+          for (int c = 0; c < kKeys; c += 32) {
+            uint32_t raw[32], pk[16];
+            tmem_ld32(tm_s + c, raw);
+            prefill::tmem_ld_wait_tied(raw);
 #pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
-            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
-            uint32_t pk[16];
-            prefill::tmem_ld_wait_tied(cur);
-            if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
-            const int left = key_lim - (key0 + c * 32);
-            if (__any_sync(0xffffffffu, left > 0)) {
-              weigh<BF16, true>(cur, left, a, m_use, sum, pk);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 16; ++e) pk[e] = 0u;
-            }
+            for (int e = 0; e < 32; ++e) raw[e] = c + e < left ? __float_as_uint(__uint_as_float(raw[e]) * a) : 0xff800000u;
+            weigh<BF16>(raw, 1.f, m_use, sum, pk);
             // (P over S: P's columns so far are no more than the scores already in registers)
-            tmem_st16(tm_p + c * 16, pk);
+            tmem_st16(tm_p + c / 2, pk);
           }
           l += sum.x + sum.y;
         }
@@ -519,31 +515,37 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       const float inv = l > 0.f ? 1.f / l : 0.f;
       const int64_t row = item.seq.q0 + i;
-      uint16_t* dst = static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1];
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+      uint16_t* dst = valid ? static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1] : nullptr;
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t oa[32], ob[32];
         if (nx > 0) {
-          tmem_ld32(tm_o + c * 32, o);
-          prefill::tmem_ld_wait_tied(o);
-          if (c == D / 32 - 1) {
+          tmem_ld32(tm_o + c * 64, oa);
+          tmem_ld32(tm_o + c * 64 + 32, ob);
+          prefill::tmem_ld_wait_tied(oa);
+          prefill::tmem_ld_wait_tied(ob);
+          if (c == D / 64 - 1) {
             tc_fence_before();
             mbar_arrive(bars.o_free(x));
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0u;
+          for (int e = 0; e < 32; ++e) oa[e] = ob[e] = 0u;
         }
-        if (!valid) continue;
-        uint32_t w[16];
+        // A thread's row would be written 16 bytes at a time, each of a warp's stores touching 32 rows: through
+        // shared memory (128-byte swizzle) a store writes four rows' 128 bytes.
+        uint8_t* mine = smem + L::kStage + warp * (32 * 128);
+        prefill::stage_slab16<BF16>(oa, inv, mine, lane, 0);
+        prefill::stage_slab16<BF16>(ob, inv, mine, lane, 1);
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float f = __uint_as_float(o[2 * e]) * inv, g = __uint_as_float(o[2 * e + 1]) * inv;
-          w[e] = BF16 ? pack_bf16x2(f, g) : pack_f16x2(f, g);
+        for (int e = 0; e < 8; ++e) {
+          const int rr = 4 * e + lane / 8;
+          const uint4 v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((lane % 8) ^ (rr & 7)) * 16);
+          uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
+          if (to) *reinterpret_cast<uint4*>(to + c * 64 + (lane % 8) * 8) = v;
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          reinterpret_cast<uint4*>(dst + c * 32)[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        __syncwarp();
       }
       if (valid && p.lse) p.lse[row * p.Hq + h] = prefill::row_lse(m, l);
     }
