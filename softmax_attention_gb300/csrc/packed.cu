@@ -92,6 +92,35 @@ __device__ __forceinline__ void weigh(const uint32_t (&x)[32], float a, float m,
   }
 }
 
+// One pass over a row's scores of a tile against the maximum m, with the next 32 on their way while 32
+// are worked on: exponentials packed, their sum added, the largest score returned.  With MASK the first
+// `left` alone count (apart, because the masks' branches would cost the common pass a quarter).
+template <bool BF16, bool MASK>
+__device__ __forceinline__ float sweep(uint32_t tm_s, int left, float a, float m, float2& sum, uint32_t (&pk)[kKeys / 2]) {
+  float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  uint32_t ra[32], rb[32];
+  tmem_ld32(tm_s, ra);
+#pragma unroll
+  for (int c = 0; c < kKeys / 32; ++c) {
+    uint32_t(&cur)[32] = (c & 1) ? rb : ra;
+    uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
+    prefill::tmem_ld_wait_tied(cur);
+    if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
+    if (MASK) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e) cur[e] = 32 * c + e < left ? cur[e] : 0xff800000u;  // -inf
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        mx[f] = prefill::fmax3(mx[f], __uint_as_float(cur[e + f]), __uint_as_float(cur[e + 4 + f]));
+    }
+    weigh<BF16>(cur, a, m, sum, &pk[c * 16]);
+  }
+  return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+}
+
 // The barriers, by their addresses.
 template <int D>
 struct Bars {
@@ -429,28 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           uint32_t pk[kKeys / 2];
           float2 sum = make_float2(0.f, 0.f);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          uint32_t ra[32], rb[32];
-          tmem_ld32(tm_s, ra);
-#pragma unroll
-          for (int c = 0; c < kKeys / 32; ++c) {
-            uint32_t(&cur)[32] = (c & 1) ? rb : ra;
-            uint32_t(&nxt)[32] = (c & 1) ? ra : rb;
-            prefill::tmem_ld_wait_tied(cur);
-            if (c + 1 < kKeys / 32) tmem_ld32(tm_s + (c + 1) * 32, nxt);
-            if (masked) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) cur[e] = 32 * c + e < left ? cur[e] : 0xff800000u;  // -inf
-            }
-#pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                mx[f] = prefill::fmax3(mx[f], __uint_as_float(cur[e + f]), __uint_as_float(cur[e + 4 + f]));
-            }
-            weigh<BF16>(cur, a, m, sum, &pk[c * 16]);
-          }
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a;
+          const float top = a * (masked ? sweep<BF16, true>(tm_s, left, a, m, sum, pk) : sweep<BF16, false>(tm_s, left, a, m, sum, pk));
           if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
             l += sum.x + sum.y;
             if (L::kApart && j > 0) {
