@@ -461,11 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float top = a * (masked ? sweep<BF16, true>(tm_s, left, a, m, sum, pk) : sweep<BF16, false>(tm_s, left, a, m, sum, pk));
           if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
             l += sum.x + sum.y;
-            if (L::kApart && j > 0) {
-              ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
-              if (!ok) break;
-              tc_fence_after();
-            }
+            // (P_{j-1} has been read: the commit that told of S_j covers P_{j-1} V_{j-1} before it)
             prefill::store_p<kKeys>(tm_p, pk);
             done = true;
           }

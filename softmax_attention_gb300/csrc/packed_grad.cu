@@ -4,19 +4,20 @@
 // dS = P (dP - delta):
 //     dq_i = scale sum_j dS_ij k_j,   dk_j = scale sum_i dS_ij q_i,   dv_j = sum_i P_ij dout_i
 //
-// Two kernels, each with the sums it owns resident in tensor memory, so that nothing is added by
-// atomics and the same call gives the same bits:
-//   - dq_kernel: a CTA holds a 128-row query tile (query tokens x heads of a kv head, as in
-//     packed.cu) and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K.  It also computes
-//     delta on its way in and leaves it for the second kernel.
-//   - dkv_kernel: a CTA holds a tile of 128 keys and walks over the query tiles that see it, all
+// Three kernels; the sums that a block owns stay in tensor memory, so that nothing is added by atomics
+// and the same call gives the same bits:
+//   - row_kernel: delta and -lse, in the form that the others use them, a pass over dout and out;
+//   - dq_kernel: a block holds a 128-row query tile (query tokens x heads of a kv head, as in
+//     packed.cu) and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K;
+//   - dkv_kernel: a block holds a tile of 128 keys and walks over the query tiles that see it, all
 //     heads of the group: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  With the
 //     products turned, P^T and dS^T have keys as rows and go back to tensor memory as the
 //     left operands of the second pair: neither ever passes through shared memory.
 // S and dP are computed in both, seven products for the five of a form that adds dq by atomics.
 //
 // Eight warps do the element-wise work, two a row, 64 columns each; P and dS, packed to 16 bits, are
-// written over the half of S or dP that the warp itself has read.
+// written over the half of S or dP that the warp itself has read.  Blocks stay for all of their work
+// items, and the products are issued by whole warps from uniform registers, as in packed.cu.
 //
 // fp16: dS is held times a power of two, f, so that the small values that gradients have keep their
 // bits (its smallest normal number is 2^-14): f brings the largest |dout| to [8, 16), of the row
@@ -46,7 +47,8 @@ struct GradParams {
   void* dk;
   void* dv;
   int64_t dq_strides[2], dk_strides[2], dv_strides[2];
-  float* delta;          // [total_q, Hq]
+  float2* rows;          // [total_q, Hq]: -lse log2 e (-inf where nothing is seen), delta
+  float* powers;         // fp16, [total_q, Hq]: f of the row
   uint32_t* dout_max;    // fp16: bits of the largest |dout|
 };
 
@@ -62,16 +64,28 @@ __device__ __forceinline__ uint32_t pack(float2 v) {
   return BF16 ? pack_bf16x2(v.x, v.y) : pack_f16x2(v.x, v.y);
 }
 
-// 32 accumulator columns times `f`, in 16 bits to global memory (16-byte aligned).
+// 32 accumulator columns of a warp's 32 rows, times f, in 16 bits to global memory; `dst`: where the
+// lane's row goes, or nullptr.  Through 2 KB of shared memory (16-byte pieces q of row r at q ^ (r / 2 % 4)),
+// so that each store writes eight rows' 64 bytes and not 16 bytes of 32 rows.
 template <bool BF16>
-__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&o)[32], float f) {
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&o)[32], float f, uint8_t* stage) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // the slab before has been read
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = pack<BF16>(make_float2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f));
-    reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(stage + lane * 64 + (q ^ ((lane >> 1) & 3)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int r = 8 * e + lane / 4, q = lane % 4;
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + (q ^ ((r >> 1) & 3)) * 16);
+    uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+    if (to) *reinterpret_cast<uint4*>(to + q * 8) = v;
   }
 }
 
@@ -103,28 +117,143 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t half
 }
 
 // ------------------------------------------------------------------------------------------
-// dq.  Warps (352 threads): 0-3 columns 0..63 of S, 4-7 columns 64..127, 8 copies, 9 issues S and dP
-// (and owns tensor memory), 10 issues dS K.  S is double-buffered: S_{j+1} is computed while the
-// weights of tile j are; dS_j is written over S_j.  dP has one buffer, given back as soon as it is
-// in registers.
+// delta and lse of each row.  D / 8 lanes a row, 16 bytes of dout and of out each, four rows in flight
+// a thread; bound by memory.
 // ------------------------------------------------------------------------------------------
-constexpr int kDqThreads = 352;
+constexpr int kRowThreads = 256;
+constexpr int kRowBatch = 4;
 
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
+  constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
+  const Params& p = g.f;
+  // rows in front of the first sequence and behind the last take no part
+  const int64_t from = max(0, __ldg(p.cu_q)) * static_cast<int64_t>(p.Hq);
+  const int64_t to = min(p.total_q, __ldg(p.cu_q + p.B)) * static_cast<int64_t>(p.Hq);
+  const int lane = threadIdx.x % kLanes;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kPerPass * kRowBatch + threadIdx.x / kLanes;
+  uint4 a[kRowBatch], c[kRowBatch];
+#pragma unroll
+  for (int i = 0; i < kRowBatch; ++i) {
+    const int64_t row = row0 + i * kPerPass;
+    a[i] = c[i] = make_uint4(0, 0, 0, 0);
+    if (row < from || row >= to) continue;
+    const int64_t token = row / p.Hq, h = row - token * p.Hq;
+    a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + token * g.dout_strides[0] + h * g.dout_strides[1]) + lane);
+    c[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.o) + token * g.o_strides[0] + h * g.o_strides[1]) + lane);
+  }
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < kRowBatch; ++i) {
+    const int64_t row = row0 + i * kPerPass;
+    const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wc[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+    float delta = 0.f, top = 0.f;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      float2 x, y;
+      if constexpr (BF16) {
+        x = make_float2(__uint_as_float(wa[f] << 16), __uint_as_float(wa[f] & 0xffff0000u));
+        y = make_float2(__uint_as_float(wc[f] << 16), __uint_as_float(wc[f] & 0xffff0000u));
+      } else {
+        x = __half22float2(*reinterpret_cast<const __half2*>(&wa[f]));
+        y = __half22float2(*reinterpret_cast<const __half2*>(&wc[f]));
+        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+      }
+      delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o >= 1; o >>= 1) {
+      delta += __shfl_xor_sync(0xffffffffu, delta, o);
+      if constexpr (!BF16) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    }
+    most = fmaxf(most, top);
+    if (lane == 0 && row >= from && row < to) {
+      const float lse = __ldg(g.lse + row);
+      g.rows[row] = make_float2(lse == -INFINITY ? -INFINITY : -lse * prefill::kLog2e, delta);
+      if constexpr (!BF16) g.powers[row] = power_for(top);
+    }
+  }
+  if constexpr (!BF16) {
+    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
+    if (threadIdx.x % 32 == 0 && bits > 0) atomicMax(g.dout_max, bits);  // a maximum: the order does not matter
+  }
+}
+
+// What the blocks of dq_kernel and dkv_kernel have in common: their scheduling warp's work items, and the
+// clearing of rows past a sequence's end that a sum would otherwise run over.
+constexpr int kThreads = 384;
+constexpr int kItems = 4;
+
+// The k-th item, copied from its place in shared memory; false: no more, or a wait ran out.
+__device__ __forceinline__ bool next_item(uint32_t bar_item, uint32_t bar_item_read, const Item* items, int k, Item& item,
+                                          uint32_t* status) {
+  if (!mbar_wait(bar_item + 8u * (k % kItems), (k / kItems) & 1, status)) return false;
+  item = items[k % kItems];
+  mbar_arrive(bar_item_read + 8u * (k % kItems));
+  return item.at >= 0;
+}
+
+// The same by a whole issuing warp, one arrival for all lanes.
+__device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_item_read, const Item* items, int k,
+                                               Item& item, uint32_t* status) {
+  if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8u * (k % kItems), (k / kItems) & 1, status))) return false;
+  item = items[k % kItems];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar_item_read + 8u * (k % kItems));
+  return __any_sync(0xffffffffu, item.at >= 0);
+}
+
+// ------------------------------------------------------------------------------------------
+// dq.  Warps: 0-3 columns 0..63 of S, 4-7 columns 64..127, 8 copies, 9 issues S and dP (and owns tensor
+// memory), 10 issues dS K, 11 finds the work items and clears what a last K tile holds past its
+// sequence's end.  S is double-buffered: S_{j+1} is computed while the weights of tile j are; dS_j is
+// written over S_j.  dP has one buffer, given back as soon as it is in registers.
+// ------------------------------------------------------------------------------------------
 template <int D>
 struct DqLayout {
-  static constexpr int kSlots = 5;
+  static constexpr int kPairs = D == 128 ? 2 : 4;  // ring: pairs of a K and a V tile
   static constexpr int kTile = kBlock * (D / 64);
   static constexpr int kQ = 0, kDo = kTile, kRing = 2 * kTile;
-  static constexpr int kBars = kRing + kSlots * kTile;
-  // q, full[slots], empty[slots], tail, s[2], dp, dp_read, ds[2], dq[2], done[2]
-  static constexpr int kNumBars = 2 * kSlots + 13;
+  static constexpr int kStage = kRing + 2 * kPairs * kTile;  // 2 KB for each of the eight warps
+  static constexpr int kBars = kStage + 8 * 2048;
+  static constexpr int kNumBars = 4 * kPairs + 16 + 2 * kItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;
   static constexpr int kS = D, kDp = D + 2 * kKeys;     // tensor memory: dQ, S[2], dP
   static_assert(kAlloc <= 232448 && kDp + kKeys <= 512, "memory budgets");
 };
 
+template <int D>
+struct DqBars {
+  using L = DqLayout<D>;
+  uint32_t at;
+  __device__ __forceinline__ uint32_t one(int i) const { return at + 8u * i; }
+  __device__ __forceinline__ uint32_t k_full(int pair) const { return one(pair); }
+  __device__ __forceinline__ uint32_t v_full(int pair) const { return one(L::kPairs + pair); }
+  __device__ __forceinline__ uint32_t k_empty(int pair) const { return one(2 * L::kPairs + pair); }
+  __device__ __forceinline__ uint32_t v_empty(int pair) const { return one(3 * L::kPairs + pair); }
+  __device__ __forceinline__ uint32_t tail() const { return one(4 * L::kPairs); }
+  __device__ __forceinline__ uint32_t q() const { return one(4 * L::kPairs + 1); }
+  __device__ __forceinline__ uint32_t q_free() const { return one(4 * L::kPairs + 2); }
+  __device__ __forceinline__ uint32_t s(int i) const { return one(4 * L::kPairs + 3 + i); }
+  __device__ __forceinline__ uint32_t dp() const { return one(4 * L::kPairs + 5); }
+  __device__ __forceinline__ uint32_t dp_read() const { return one(4 * L::kPairs + 6); }
+  __device__ __forceinline__ uint32_t ds(int i) const { return one(4 * L::kPairs + 7 + i); }
+  __device__ __forceinline__ uint32_t dq(int i) const { return one(4 * L::kPairs + 9 + i); }
+  __device__ __forceinline__ uint32_t o_free() const { return one(4 * L::kPairs + 11); }
+  __device__ __forceinline__ uint32_t done(int i) const { return one(4 * L::kPairs + 12 + i); }
+  __device__ __forceinline__ uint32_t item() const { return one(4 * L::kPairs + 14); }
+  __device__ __forceinline__ uint32_t item_read() const { return one(4 * L::kPairs + 14 + kItems); }
+};
+
+// Key tiles that a query tile sees.
+__device__ __forceinline__ int key_tiles(const Params& p, const Seq& s, int q0) {
+  const int last = min(s.nq, q0 + p.q_per_tile) - 1;
+  const int end = p.causal ? min(s.nk, max(0, last + s.nk - s.nq + 1)) : s.nk;
+  return (end + kKeys - 1) / kKeys;
+}
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kDqThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
               const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const GradParams gp) {
   using L = DqLayout<D>;
@@ -133,50 +262,35 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ uint32_t tmem_slot;
-  __shared__ int item[2];
-  const uint32_t s_base = smem_addr(smem), bars = s_base + L::kBars;
-  const uint32_t bar_q = bars;
-  auto bar_full = [&](int s) { return bars + 8u * (1 + s); };
-  auto bar_empty = [&](int s) { return bars + 8u * (1 + L::kSlots + s); };
-  const uint32_t bar_tail = bars + 8u * (1 + 2 * L::kSlots);
-  auto bar_s = [&](int i) { return bar_tail + 8u * (1 + i); };
-  const uint32_t bar_dp = bar_tail + 24u, bar_dp_read = bar_tail + 32u;
-  auto bar_ds = [&](int i) { return bar_tail + 8u * (5 + i); };
-  auto bar_dq = [&](int i) { return bar_tail + 8u * (7 + i); };
-  auto bar_done = [&](int i) { return bar_tail + 8u * (9 + i); };
-
+  __shared__ Item items[kItems];
+  const uint32_t s_base = smem_addr(smem);
+  const DqBars<D> bars{s_base + L::kBars};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = blockIdx.x % p.Hkv;
-  if (warp == 0) {
-    int b, t;
-    auto pieces = [&](int s, int& n, int& first) {
-      const Seq q = load_seq(p, s);
-      n = (q.nq + p.q_per_tile - 1) / p.q_per_tile;
-      first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / p.q_per_tile;
-    };
-    const Finder finder(p.B, !p.causal, pieces);
-    finder.find(blockIdx.x / p.Hkv, pieces, b, t);
-    if (lane == 0) {
-      item[0] = b;
-      item[1] = t;
-    }
-  } else if (warp == 9) {
+  if (warp == 9) {
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   } else if (threadIdx.x == 8 * 32) {
-    mbar_init(bar_q, 1);
-    for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 1);
+    for (int i = 0; i < L::kPairs; ++i) {
+      mbar_init(bars.k_full(i), 1);
+      mbar_init(bars.v_full(i), 1);
+      mbar_init(bars.k_empty(i), 1);
+      mbar_init(bars.v_empty(i), 1);
     }
-    mbar_init(bar_tail, 1);
-    mbar_init(bar_dp, 1);
-    mbar_init(bar_dp_read, 256);
+    mbar_init(bars.tail(), 1);
+    mbar_init(bars.q(), 1);
+    mbar_init(bars.q_free(), 1);
+    mbar_init(bars.dp(), 1);
+    mbar_init(bars.dp_read(), 256);
+    mbar_init(bars.o_free(), 256);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_s(i), 1);
-      mbar_init(bar_ds(i), 256);
-      mbar_init(bar_dq(i), 1);
-      mbar_init(bar_done(i), 1);
+      mbar_init(bars.s(i), 1);
+      mbar_init(bars.ds(i), 256);
+      mbar_init(bars.dq(i), 1);
+      mbar_init(bars.done(i), 1);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bars.item() + 8u * i, 1);
+      mbar_init(bars.item_read() + 8u * i, 256 + 3);  // weights, issuers, copies
     }
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
@@ -188,146 +302,208 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int b = item[0];
-  if (b >= 0) {
-    const Seq seq = load_seq(p, b);
-    const int q0 = item[1] * p.q_per_tile;
-    const int last = min(seq.nq, q0 + p.q_per_tile) - 1;
-    const int end = p.causal ? min(seq.nk, max(0, last + seq.nk - seq.nq + 1)) : seq.nk;
-    const int n = (end + kKeys - 1) / kKeys;
-    auto full = [&](int i) { return mbar_wait(bar_full(i % L::kSlots), (i / L::kSlots) & 1, p.status); };
-    if (warp == 8) {
-      // ---------------------------------- copies ----------------------------------------
-      bool ok = true;
-      int issued = 0;
-      const bool tail = n > 0 && n * kKeys > seq.nk;  // the last K tile reaches past the sequence
-      if (lane == 0 && n > 0) {
-        mbar_arrive_expect_tx(bar_q, static_cast<uint32_t>(2 * 128 * (D / 64) * p.G * p.q_per_tile));
-        for (int kb = 0; kb < D / 64; ++kb) {
-          tma_load_3d(s_base + L::kQ + kb * kBlock, &tm_q, bar_q, kb * 64, hk * p.G, seq.q0 + q0);
-          tma_load_3d(s_base + L::kDo + kb * kBlock, &tm_do, bar_q, kb * 64, hk * p.G, seq.q0 + q0);
+  if (warp == 11) {
+    // ------------------------------ work items, K's last rows --------------------------------
+    auto pieces = [&](int s, int& n, int& first) {
+      const Seq q = load_seq(p, s);
+      n = (q.nq + p.q_per_tile - 1) / p.q_per_tile;
+      first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / p.q_per_tile;
+    };
+    const Finder finder(p.B, !p.causal, pieces);
+    int tiles = 0, tails = 0;          // key tiles of the items so far; K tiles cleared
+    int clear_at = -1, clear_row = 0;  // the item before: its last key tile, first row to clear
+    bool ok = true, more = true;
+    for (int k = 0; ok && (more || clear_at >= 0); ++k) {
+      Item item{};
+      item.at = -1;
+      if (more) {
+        const int w = dealt(k);
+        int b, t;
+        finder.find(w / p.Hkv, pieces, b, t);
+        if (b >= 0) {
+          item.seq = load_seq(p, b);
+          item.at = t * p.q_per_tile;
+          item.head = w % p.Hkv;
         }
-        for (int i = 0; i < 2 * n; ++i) {  // K_0, V_0, K_1, V_1, ...
-          const int slot = i % L::kSlots;
-          if (i >= L::kSlots && !(ok = mbar_wait(bar_empty(slot), (i / L::kSlots - 1) & 1, p.status))) break;
-          const uint32_t bar = tail && i == 2 * n - 2 ? bar_tail : bar_full(slot);
-          mbar_arrive_expect_tx(bar, L::kTile);
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(s_base + L::kRing + slot * L::kTile + kb * kBlock, (i & 1) ? &tm_v : &tm_k, bar, kb * 64, hk,
-                        seq.k0 + (i / 2) * kKeys);
-          issued = i + 1;
+        if (k >= kItems)
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kItems), (k / kItems - 1) & 1, p.status));
+        if (ok && lane == 0) {
+          items[k % kItems] = item;
+          mbar_arrive(bars.item() + 8u * (k % kItems));
         }
+        more = b >= 0;
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (ok && tail) {
+      if (ok && clear_at >= 0) {
         // K rows past the sequence's end: dS is 0 there, but 0 times an infinity or NaN is not
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_tail, 0, p.status));
-        const int slot = (2 * n - 2) % L::kSlots;
-        if (ok) clear_rows<D>(smem + L::kRing + slot * L::kTile, seq.nk - (n - 1) * kKeys, lane, 32);
+        const int pair = clear_at % L::kPairs;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
+        ++tails;
+        if (ok) clear_rows<D>(smem + L::kRing + 2 * pair * L::kTile, clear_row, lane, 32);
         fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar_full(slot));
+        if (ok && lane == 0) mbar_arrive(bars.k_full(pair));
+        clear_at = -1;
       }
-      if (lane == 0 && issued < 2 * n) {
-        // A wait ran out: let the copies in flight land before the CTA ends
-        mbar_wait(bar_q, 0, nullptr);
-        for (int i = max(0, issued - L::kSlots); i < issued; ++i) {
-          const bool in_tail = tail && i == 2 * n - 2;
-          mbar_wait(in_tail ? bar_tail : bar_full(i % L::kSlots), in_tail ? 0 : (i / L::kSlots) & 1, nullptr);
+      if (item.at >= 0) {
+        const int n = key_tiles(p, item.seq, item.at);
+        tiles += n;
+        if (n > 0 && n * kKeys > item.seq.nk) {
+          clear_at = tiles - 1;
+          clear_row = item.seq.nk - (n - 1) * kKeys;
         }
       }
-    } else if (warp == 9) {
-      // ---------------------------------- S and dP --------------------------------------
-      if (lane == 0 && n > 0) {
-        constexpr uint32_t idesc = idesc_f16(BF16, kRows, kKeys, false, false);
-        const uint64_t q_desc = sdesc_sw128(s_base + L::kQ, 16, 1024), do_desc = sdesc_sw128(s_base + L::kDo, 16, 1024);
-        const uint64_t ring = sdesc_sw128(s_base + L::kRing, 16, 1024);
-        bool ok = mbar_wait(bar_q, 0, p.status);
-        for (int j = 0; ok && j < n; ++j) {
-          if (!(ok = full(2 * j))) break;
-          if (j >= 2 && !(ok = mbar_wait(bar_dq(j & 1), (j / 2 - 1) & 1, p.status))) break;
-          tc_fence_after();
-          product_ss<D>(tmem + L::kS + (j & 1) * kKeys, q_desc, sdesc_add(ring, ((2 * j) % L::kSlots) * L::kTile), idesc);
-          tc_commit(bar_s(j & 1));
-          if (!(ok = full(2 * j + 1))) break;
-          if (j >= 1 && !(ok = mbar_wait(bar_dp_read, (j - 1) & 1, p.status))) break;
-          tc_fence_after();
-          const int slot = (2 * j + 1) % L::kSlots;
-          product_ss<D>(tmem + L::kDp, do_desc, sdesc_add(ring, slot * L::kTile), idesc);
-          tc_commit(bar_dp);
-          tc_commit(bar_empty(slot));
+    }
+  } else if (warp == 8) {
+    // ---------------------------------- copies ----------------------------------------------
+    if (lane == 0) {
+      bool ok = true;
+      int tile = 0, uses = 0, tails = 0;  // key tiles; items with any; K tiles that land on the tail's barrier
+      int tail_at = -1, k_only = -1;
+      Item item;
+      for (int k = 0; ok && next_item(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+        const int n = key_tiles(p, item.seq, item.at);
+        if (n == 0) continue;
+        if (uses > 0 && !(ok = mbar_wait(bars.q_free(), (uses - 1) & 1, p.status))) break;
+        ++uses;
+        mbar_arrive_expect_tx(bars.q(), static_cast<uint32_t>(2 * 128 * (D / 64) * p.G * p.q_per_tile));
+        for (int kb = 0; kb < D / 64; ++kb) {
+          tma_load_3d(s_base + L::kQ + kb * kBlock, &tm_q, bars.q(), kb * 64, item.head * p.G, item.seq.q0 + item.at);
+          tma_load_3d(s_base + L::kDo + kb * kBlock, &tm_do, bars.q(), kb * 64, item.head * p.G, item.seq.q0 + item.at);
         }
-        tc_commit(bar_done(0));
-        mbar_wait(bar_done(0), 0, nullptr);
-      }
-    } else if (warp == 10) {
-      // ---------------------------------- dQ += dS K ------------------------------------
-      if (lane == 0 && n > 0) {
-        constexpr uint32_t idesc = idesc_f16(BF16, kRows, D, false, true);
-        const uint64_t ring = sdesc_sw128(s_base + L::kRing, kBlock, 1024);
-        bool ok = true;
-        for (int j = 0; ok && j < n; ++j) {
-          if (!(ok = full(2 * j))) break;
-          if (!(ok = mbar_wait(bar_ds(j & 1), (j / 2) & 1, p.status))) break;
-          tc_fence_after();
-          const int slot = (2 * j) % L::kSlots;
-          product_ts(tmem, tmem + L::kS + (j & 1) * kKeys, kHalf, sdesc_add(ring, slot * L::kTile), idesc, j == 0);
-          tc_commit(bar_dq(j & 1));
-          tc_commit(bar_empty(slot));
+        const bool tail = n * kKeys > item.seq.nk;  // the last K tile reaches past the sequence
+        for (int j = 0; j < n; ++j, ++tile) {
+          const int pair = tile % L::kPairs, lap = tile / L::kPairs;
+          const uint32_t to = s_base + L::kRing + 2 * pair * L::kTile;
+          if (lap > 0 && !(ok = mbar_wait(bars.k_empty(pair), (lap - 1) & 1, p.status))) break;
+          uint32_t bar = bars.k_full(pair);
+          if (tail && j == n - 1) {
+            bar = bars.tail();
+            tail_at = tile;
+            ++tails;
+          }
+          mbar_arrive_expect_tx(bar, L::kTile);
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(to + kb * kBlock, &tm_k, bar, kb * 64, item.head, item.seq.k0 + j * kKeys);
+          k_only = tile;
+          if (lap > 0 && !(ok = mbar_wait(bars.v_empty(pair), (lap - 1) & 1, p.status))) break;
+          mbar_arrive_expect_tx(bars.v_full(pair), L::kTile);
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(to + L::kTile + kb * kBlock, &tm_v, bars.v_full(pair), kb * 64, item.head, item.seq.k0 + j * kKeys);
+          k_only = -1;
         }
-        tc_commit(bar_done(1));
-        mbar_wait(bar_done(1), 0, nullptr);
       }
-    } else {
-      // ------------------------- weights: a row and 64 columns a thread -------------------
-      const int w = warp / 4, r = threadIdx.x % 128;  // half of the columns
-      const int i = q0 + r / p.G, h = hk * p.G + r % p.G;
-      const bool valid = r < p.G * p.q_per_tile && i < seq.nq;
-      const int64_t row = seq.q0 + i;
-      const int key_lim = !valid ? 0 : p.causal ? min(seq.nk, i + seq.nk - seq.nq + 1) : seq.nk;
-      const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-      // delta and the largest |dout| of the row, by both of its threads: the second finds the first's
-      // lines in L1, and no shared memory is left to trade halves in
-      float delta = 0.f, top = 0.f, lse = -INFINITY;
-      if (valid) {
-        const uint4* a = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gp.dout) + row * gp.dout_strides[0] +
-                                                        h * gp.dout_strides[1]);
-        const uint4* c = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(gp.o) + row * gp.o_strides[0] +
-                                                        h * gp.o_strides[1]);
-        lse = __ldg(gp.lse + row * p.Hq + h);
-#pragma unroll
-        for (int e = 0; e < D / 8; ++e) {
-          const uint4 va = __ldg(a + e), vc = __ldg(c + e);
-          const uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wc[4] = {vc.x, vc.y, vc.z, vc.w};
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            float2 x, y;
-            if constexpr (BF16) {
-              x = make_float2(__uint_as_float(wa[f] << 16), __uint_as_float(wa[f] & 0xffff0000u));
-              y = make_float2(__uint_as_float(wc[f] << 16), __uint_as_float(wc[f] & 0xffff0000u));
-            } else {
-              x = __half22float2(*reinterpret_cast<const __half2*>(&wa[f]));
-              y = __half22float2(*reinterpret_cast<const __half2*>(&wc[f]));
-              top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
-            }
-            delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
+      if (!ok) {
+        // A wait ran out: let the copies in flight land before the block ends.  (Each wait is for the last
+        // copy to its barrier.)
+        if (uses > 0) mbar_wait(bars.q(), (uses - 1) & 1, nullptr);
+        const int k_end = k_only >= 0 ? tile + 1 : tile;
+        for (int i = max(0, k_end - L::kPairs); i < k_end; ++i) {
+          if (i == tail_at) mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
+          else mbar_wait(bars.k_full(i % L::kPairs), (i / L::kPairs) & 1, nullptr);
+        }
+        for (int i = max(0, tile - L::kPairs); i < tile; ++i)
+          mbar_wait(bars.v_full(i % L::kPairs), (i / L::kPairs) & 1, nullptr);
+      }
+    }
+  } else if (warp == 9 || warp == 10) {
+    // ------------------- issuer 9: S = Q K^T and dP = dO V^T; issuer 10: dQ += dS K -------------------
+    const bool leader = lane == 0;
+    const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+    bool ok = true;
+    auto wait = [&](uint32_t bar, int phase) {
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
+      return ok;
+    };
+    int pair = 0, lap = 0, step = 0, uses = 0;
+    Item item;
+    if (warp == 9) {
+      constexpr uint32_t idesc = idesc_f16(BF16, kRows, kKeys, false, false);
+      const uint64_t q_desc = sdesc_sw128(s_base + L::kQ, 16, 1024), do_desc = sdesc_sw128(s_base + L::kDo, 16, 1024);
+      const uint64_t ring = sdesc_sw128(s_base + L::kRing, 16, 1024);
+      for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+        const int n = uniform(key_tiles(p, item.seq, item.at));
+        if (n == 0) continue;
+        if (!wait(bars.q(), uses++)) break;
+        for (int j = 0; j < n; ++j, ++step) {
+          const uint64_t kd = sdesc_add(ring, 2 * pair * L::kTile);
+          if (!wait(bars.k_full(pair), lap)) break;
+          if (step >= 2 && !wait(bars.dq(step & 1), step / 2 - 1)) break;  // dS_{step-2} read
+          tc_fence_after();
+          if (leader) {
+            product_ss<D>(tm + L::kS + (step & 1) * kKeys, q_desc, kd, idesc);
+            tc_commit(bars.s(step & 1));
+          }
+          __syncwarp();
+          if (!wait(bars.v_full(pair), lap)) break;
+          if (step >= 1 && !wait(bars.dp_read(), step - 1)) break;
+          tc_fence_after();
+          if (leader) {
+            product_ss<D>(tm + L::kDp, do_desc, sdesc_add(kd, L::kTile), idesc);
+            tc_commit(bars.dp());
+            tc_commit(bars.v_empty(pair));
+            if (j == n - 1) tc_commit(bars.q_free());
+          }
+          __syncwarp();
+          if (++pair == L::kPairs) {
+            pair = 0;
+            ++lap;
           }
         }
-        if (w == 0) gp.delta[row * p.Hq + h] = delta;
       }
-      float f = 1.f;
-      if constexpr (!BF16) {
-        f = power_for(top);
-        const uint32_t most = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        if (w == 0 && lane == 0 && most > 0) atomicMax(gp.dout_max, most);  // a maximum: any order
+    } else {
+      constexpr uint32_t idesc = idesc_f16(BF16, kRows, D, false, true);
+      const uint64_t ring = sdesc_sw128(s_base + L::kRing, kBlock, 1024);
+      for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+        const int n = uniform(key_tiles(p, item.seq, item.at));
+        if (n == 0) continue;
+        // dQ of the item before has to be read before the first product overwrites it
+        if (uses > 0 && !wait(bars.o_free(), uses - 1)) break;
+        ++uses;
+        for (int j = 0; j < n; ++j, ++step) {
+          if (!wait(bars.k_full(pair), lap)) break;
+          if (!wait(bars.ds(step & 1), step / 2)) break;
+          tc_fence_after();
+          if (leader) {
+            product_ts(tm, tm + L::kS + (step & 1) * kKeys, kHalf, sdesc_add(ring, 2 * pair * L::kTile), idesc, j == 0);
+            tc_commit(bars.dq(step & 1));
+            tc_commit(bars.k_empty(pair));
+          }
+          __syncwarp();
+          if (++pair == L::kPairs) {
+            pair = 0;
+            ++lap;
+          }
+        }
       }
-      const float nl = lse > -INFINITY ? -lse * prefill::kLog2e : -INFINITY;
-      const float2 a2 = make_float2(p.scale_log2, p.scale_log2), nl2 = make_float2(nl, nl);
-      const float2 f2 = make_float2(f, f), nd2 = make_float2(-delta * f, -delta * f);
-      bool ok = true;
-      for (int j = 0; j < n; ++j) {
-        const uint32_t tm_s = tmem + L::kS + (j & 1) * kKeys + w * kHalf + lanes;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_s(j & 1), (j / 2) & 1, p.status));
+    }
+    // every product must finish before tensor memory and the ring are given up
+    if (leader) {
+      tc_commit(bars.done(warp - 9));
+      mbar_wait(bars.done(warp - 9), 0, nullptr);
+    }
+  } else {
+    // ------------------------- weights: a row and 64 columns a thread -------------------------
+    const int w = warp / 4, r = threadIdx.x % 128;  // half of the columns
+    const int row_token = r / p.G, row_head = r % p.G;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const float2 a2 = make_float2(p.scale_log2, p.scale_log2);
+    const uint32_t tm_dp = tmem + L::kDp + w * kHalf + lanes;
+    bool ok = true;
+    int step = 0;
+    Item item;
+    for (int k = 0; ok && __all_sync(0xffffffffu, next_item(bars.item(), bars.item_read(), items, k, item, p.status)); ++k) {
+      const int n = key_tiles(p, item.seq, item.at);
+      const int i = item.at + row_token, h = item.head * p.G + row_head;
+      const bool valid = r < p.G * p.q_per_tile && i < item.seq.nq;
+      const int64_t row = item.seq.q0 + i;
+      const float2 rd = valid ? __ldg(gp.rows + row * p.Hq + h) : make_float2(-INFINITY, 0.f);
+      const float f = !BF16 && valid ? __ldg(gp.powers + row * p.Hq + h) : 1.f;
+      // (a row of no query is not looked at by anyone: it may see everything)
+      const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
+      const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(f, f), nd2 = make_float2(-rd.y * f, -rd.y * f);
+      for (int j = 0; j < n; ++j, ++step) {
+        const uint32_t tm_s = tmem + L::kS + (step & 1) * kKeys + w * kHalf + lanes;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.s(step & 1), (step / 2) & 1, p.status));
         if (!ok) break;
         tc_fence_after();
         const int left = key_lim - (j * kKeys + w * kHalf);  // columns that the row sees
@@ -344,15 +520,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
                                                   __uint_as_float(raw[c / 16][(2 * c) % 32 + 1])), a2, nl2);
           x[c] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
         }
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) x[c] = make_float2(2 * c < left ? x[c].x : 0.f, 2 * c + 1 < left ? x[c].y : 0.f);
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_dp, j & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.dp(), step & 1, p.status));
         if (!ok) break;
         tc_fence_after();
         uint32_t dp[2][32], ds[32];
-        const uint32_t tm_dp = tmem + L::kDp + w * kHalf + lanes;
         tmem_ld32(tm_dp, dp[0]);
         prefill::tmem_ld_wait_tied(dp[0]);
         tmem_ld32(tm_dp + 32, dp[1]);
@@ -361,42 +532,49 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           if (q == 1) {
             prefill::tmem_ld_wait_tied(dp[1]);
             tc_fence_before();
-            mbar_arrive(bar_dp_read);
+            mbar_arrive(bars.dp_read());
           }
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
             const float2 t = __ffma2_rn(make_float2(__uint_as_float(dp[q][2 * c]), __uint_as_float(dp[q][2 * c + 1])), f2, nd2);
-            float2 v = __fmul2_rn(x[16 * q + c], t);
-            // a hidden column's dP may be another sequence's, or no number: selected, not multiplied
-            if (!whole) v = make_float2(32 * q + 2 * c < left ? v.x : 0.f, 32 * q + 2 * c + 1 < left ? v.y : 0.f);
-            ds[16 * q + c] = pack<BF16>(v);
+            ds[16 * q + c] = pack<BF16>(__fmul2_rn(x[16 * q + c], t));
           }
+        }
+        if (!whole) {
+          // what a hidden column holds may be another sequence's, or no number: replaced, not multiplied
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            ds[c] &= (2 * c < left ? 0xffffu : 0u) | (2 * c + 1 < left ? 0xffff0000u : 0u);
         }
         tmem_st32(tm_s, ds);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_ds(j & 1));
+        mbar_arrive(bars.ds(step & 1));
       }
       if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_dq((n - 1) & 1), ((n - 1) / 2) & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.dq((step - 1) & 1), ((step - 1) / 2) & 1, p.status));
         tc_fence_after();
       }
-      if (ok) {
-        const float back = p.scale / f;
-        uint16_t* dst = static_cast<uint16_t*>(gp.dq) + row * gp.dq_strides[0] + h * gp.dq_strides[1] + w * (D / 2);
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld32(tmem + lanes + w * (D / 2) + c * 32, o);
-            prefill::tmem_ld_wait_tied(o);
-          } else {
+      if (!ok) break;
+      uint16_t* dst = valid ? static_cast<uint16_t*>(gp.dq) + row * gp.dq_strides[0] + h * gp.dq_strides[1] + w * (D / 2) : nullptr;
+      uint32_t o[D / 64][32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
-          }
-          if (valid) store32<BF16>(dst + c * 32, o, back);
+      for (int c = 0; c < D / 64; ++c) {
+        if (n > 0) {
+          tmem_ld32(tmem + lanes + w * (D / 2) + c * 32, o[c]);
+          prefill::tmem_ld_wait_tied(o[c]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[c][e] = 0u;
         }
       }
+      if (n > 0) {
+        tc_fence_before();
+        mbar_arrive(bars.o_free());
+      }
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        store32<BF16>(dst ? dst + c * 32 : nullptr, o[c], p.scale / f, smem + L::kStage + warp * 2048);
     }
   }
   tc_fence_before();
@@ -409,25 +587,24 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------
-// dk and dv.  Warps (384 threads): 0-3 query columns 0..63 of S^T, 4-7 columns 64..127, 8 copies, 9
-// issues dV and S^T (and owns tensor memory), 10 issues dK and dP^T, 11 brings each query row's lse
-// and delta.  Tensor memory is full at D = 128 (dV, dK, S^T, dP^T): P^T lies over S^T and dS^T over
-// dP^T, and issuer 9 puts S^T_{i+1} right behind dV_i (issuer 10 dP^T_{i+1} behind dK_i), which
-// reads what it overwrites: products of one thread and one shape run in order.  While the
-// element-wise warps work on S^T the tensor cores run dK and dP^T, and the other way round.  At
-// D = 64, where the shapes differ, P^T and dS^T have columns of their own.
+// dk and dv.  Warps: 0-3 query columns 0..63 of S^T, 4-7 columns 64..127, 8 copies, 9 issues dV and S^T
+// (and owns tensor memory), 10 issues dK and dP^T, 11 finds the work items, brings each query row's
+// lse and delta and clears query rows past a sequence's end.  Tensor memory is full at D = 128 (dV, dK,
+// S^T, dP^T): P^T lies over S^T and dS^T over dP^T, and issuer 9 puts S^T_{i+1} right behind dV_i
+// (issuer 10 dP^T_{i+1} behind dK_i), which reads what it overwrites: products of one thread and
+// one shape run in order.  While the element-wise warps work on S^T the tensor cores run dK and
+// dP^T, and the other way round.  At D = 64, where the shapes differ, P^T and dS^T have columns of
+// their own.
 // ------------------------------------------------------------------------------------------
-constexpr int kDkvThreads = 384;
-
 template <int D>
 struct DkvLayout {
-  static constexpr int kSlots = D == 128 ? 4 : 8;
+  static constexpr int kPairs = D == 128 ? 2 : 4;  // ring: pairs of a Q and a dO tile
   static constexpr int kTile = kBlock * (D / 64);
   static constexpr int kK = 0, kV = kTile, kRing = 2 * kTile;
-  static constexpr int kRowData = kRing + kSlots * kTile;  // [2][-lse, -delta][128] fp32
+  static constexpr int kStage = kRing + 2 * kPairs * kTile;  // 2 KB for each of the eight warps
+  static constexpr int kRowData = kStage + 8 * 2048;         // [2][-lse, -delta][128] fp32
   static constexpr int kBars = kRowData + 2 * 2 * kRows * 4;
-  // kv, full[slots], empty[slots], tail, rows_full[2], rows_empty[2], s, p, dp, ds, dv, dk, done[2]
-  static constexpr int kNumBars = 2 * kSlots + 14;
+  static constexpr int kNumBars = 4 * kPairs + 17 + 2 * kItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;
   static constexpr bool kApart = D == 64;
   static constexpr int kDv = 0, kDk = D, kS = 2 * D, kDp = kS + kRows;
@@ -436,66 +613,151 @@ struct DkvLayout {
   static_assert(kAlloc <= 232448 && kDs + kRows / 2 <= 512, "memory budgets");
 };
 
+template <int D>
+struct DkvBars {
+  using L = DkvLayout<D>;
+  uint32_t at;
+  __device__ __forceinline__ uint32_t one(int i) const { return at + 8u * i; }
+  // of Q (which = 0) or dO (1) of a pair
+  __device__ __forceinline__ uint32_t full(int pair, int which) const { return one(2 * pair + which); }
+  __device__ __forceinline__ uint32_t empty(int pair, int which) const { return one(2 * L::kPairs + 2 * pair + which); }
+  __device__ __forceinline__ uint32_t tail() const { return one(4 * L::kPairs); }
+  __device__ __forceinline__ uint32_t kv() const { return one(4 * L::kPairs + 1); }
+  __device__ __forceinline__ uint32_t kv_free() const { return one(4 * L::kPairs + 2); }
+  __device__ __forceinline__ uint32_t rows(int i) const { return one(4 * L::kPairs + 3 + i); }
+  __device__ __forceinline__ uint32_t rows_read(int i) const { return one(4 * L::kPairs + 5 + i); }
+  // x = 0: S^T, P^T, dV; 1: dP^T, dS^T, dK
+  __device__ __forceinline__ uint32_t first(int x) const { return one(4 * L::kPairs + 7 + x); }
+  __device__ __forceinline__ uint32_t packed(int x) const { return one(4 * L::kPairs + 9 + x); }
+  __device__ __forceinline__ uint32_t second(int x) const { return one(4 * L::kPairs + 11 + x); }
+  __device__ __forceinline__ uint32_t out_free(int x) const { return one(4 * L::kPairs + 13 + x); }
+  __device__ __forceinline__ uint32_t done(int x) const { return one(4 * L::kPairs + 15 + x); }
+  __device__ __forceinline__ uint32_t item() const { return one(4 * L::kPairs + 17); }
+  __device__ __forceinline__ uint32_t item_read() const { return one(4 * L::kPairs + 17 + kItems); }
+};
+
+// First query tile that sees a key of the tile at key0, and how many tiles from there on there are.
+__device__ __forceinline__ int query_tiles(const Params& p, const Seq& s, int key0, int& first) {
+  first = p.causal ? max(0, key0 - (s.nk - s.nq)) / p.q_per_tile : 0;
+  return max(0, (s.nq + p.q_per_tile - 1) / p.q_per_tile - first);
+}
+
+// The issuing warp of S^T and dV (X = 0) or of dP^T and dK (X = 1).  A tile's first product reads its own
+// ring entry (Q for S^T, dO for dP^T), its second the other's.
+template <int D, bool BF16, int X>
+__device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uint32_t bar_base, uint32_t tmem, const Item* items,
+                                           volatile int* turns) {
+  using L = DkvLayout<D>;
+  const DkvBars<D> bars{bar_base};
+  constexpr uint32_t idesc1 = idesc_f16(BF16, kRows, kRows, false, false);
+  constexpr uint32_t idesc2 = idesc_f16(BF16, kRows, D, false, true);
+  const bool leader = (threadIdx.x & 31) == 0;
+  tmem = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
+  const uint64_t left = sdesc_sw128(s_base + (X ? L::kV : L::kK), 16, 1024);
+  const uint64_t ring1 = sdesc_sw128(s_base + L::kRing + X * L::kTile, 16, 1024);
+  const uint64_t ring2 = sdesc_sw128(s_base + L::kRing + (1 - X) * L::kTile, kBlock, 1024);
+  const uint32_t tm1 = tmem + (X ? L::kDp : L::kS), tm2 = tmem + (X ? L::kDk : L::kDv), tm_a = tmem + (X ? L::kDs : L::kP);
+  bool ok = true;
+  auto wait = [&](uint32_t bar, int phase) {
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
+    return ok;
+  };
+  int pair = 0, lap = 0, step = 0, uses = 0;
+  Item item;
+  for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+    int first_tile;
+    const int n = uniform(query_tiles(p, item.seq, item.at, first_tile));
+    if (n == 0) continue;
+    if (!wait(bars.kv(), uses) || !wait(bars.full(pair, X), lap)) break;
+    tc_fence_after();
+    if (leader) {
+      product_ss<D>(tm1, left, sdesc_add(ring1, 2 * pair * L::kTile), idesc1);
+      tc_commit(bars.first(X));
+      tc_commit(bars.empty(pair, X));
+      if (n == 1) tc_commit(bars.kv_free());
+    }
+    __syncwarp();
+    for (int i = 0; i < n; ++i, ++step) {
+      const int at = pair;
+      if (!wait(bars.full(at, 1 - X), lap)) break;
+      if (++pair == L::kPairs) {
+        pair = 0;
+        ++lap;
+      }
+      if (i + 1 < n && !wait(bars.full(pair, X), lap)) break;
+      // the item before has to be read before the first product overwrites it
+      if (i == 0 && uses > 0 && !wait(bars.out_free(X), uses - 1)) break;
+      // The other pair's turn first (dV and S^T of a tile before dK and dP^T, these before the next): one
+      // pair's products are not to wait behind half of the other's.  Only an order: the wait may give up.
+      for (int spin = 0; spin < 4096 && turns[1 - X] < (X ? step + 1 : step); ++spin) {}
+      if (!wait(bars.packed(X), step)) break;
+      tc_fence_after();
+      if (leader) {
+        product_ts(tm2, tm_a, L::kStep, sdesc_add(ring2, 2 * at * L::kTile), idesc2, i == 0);
+        if (i + 1 < n) product_ss<D>(tm1, left, sdesc_add(ring1, 2 * pair * L::kTile), idesc1);
+        turns[X] = step + 1;  // (before the commits: after them the store would wait for the products)
+        tc_commit(bars.second(X));
+        tc_commit(bars.empty(at, 1 - X));
+        if (i + 1 < n) {
+          tc_commit(bars.first(X));
+          tc_commit(bars.empty(pair, X));
+          if (i + 2 == n) tc_commit(bars.kv_free());
+        }
+      }
+      __syncwarp();
+    }
+    ++uses;
+  }
+  // every product must finish before tensor memory and the ring are given up
+  if (leader) {
+    tc_commit(bars.done(X));
+    mbar_wait(bars.done(X), 0, nullptr);
+  }
+}
+
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kDkvThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const GradParams gp) {
   using L = DkvLayout<D>;
-  constexpr float kPower = BF16 ? 0.f : 7.f;  // P is held times 2^kPower
+  constexpr float kPower = BF16 ? 0.f : 7.f;             // P is held times 2^kPower
+  constexpr float kUnpower = BF16 ? 1.f : 0.0078125f;    // 2^-kPower
   const Params& p = gp.f;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ uint32_t tmem_slot;
-  __shared__ int item[2];
-  const uint32_t s_base = smem_addr(smem), bars = s_base + L::kBars;
-  const uint32_t bar_kv = bars;
-  auto bar_full = [&](int s) { return bars + 8u * (1 + s); };
-  auto bar_empty = [&](int s) { return bars + 8u * (1 + L::kSlots + s); };
-  const uint32_t bar_tail = bars + 8u * (1 + 2 * L::kSlots);
-  auto bar_rows = [&](int i) { return bar_tail + 8u * (1 + i); };
-  auto bar_rows_read = [&](int i) { return bar_tail + 8u * (3 + i); };
-  const uint32_t bar_s = bar_tail + 40u, bar_p = bar_tail + 48u, bar_dp = bar_tail + 56u, bar_ds = bar_tail + 64u;
-  const uint32_t bar_dv = bar_tail + 72u, bar_dk = bar_tail + 80u;
-  auto bar_done = [&](int i) { return bar_tail + 8u * (11 + i); };
-
+  __shared__ Item items[kItems];
+  __shared__ int turns[2];  // pairs of products that each issuer has put into the pipe
+  const uint32_t s_base = smem_addr(smem);
+  const DkvBars<D> bars{s_base + L::kBars};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int hk = blockIdx.x % p.Hkv;
   const int used = p.G * p.q_per_tile;  // rows of a query tile
-  if (warp == 0) {
-    int b, t;
-    auto pieces = [&](int s, int& n, int& first) {
-      const Seq q = load_seq(p, s);
-      n = (q.nk + kKeys - 1) / kKeys;
-      first = p.causal ? 0 : q.nq / kKeys;
-    };
-    const Finder finder(p.B, !p.causal, pieces);
-    finder.find(blockIdx.x / p.Hkv, pieces, b, t);
-    if (lane == 0) {
-      item[0] = b;
-      item[1] = t;
-    }
-  } else if (warp == 9) {
+  if (warp == 9) {
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   } else if (threadIdx.x == 8 * 32) {
-    mbar_init(bar_kv, 1);
-    for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(bar_full(s), 1);
-      mbar_init(bar_empty(s), 2);  // both issuers
+    for (int i = 0; i < 2 * L::kPairs; ++i) {
+      mbar_init(bars.full(i / 2, i % 2), 1);
+      mbar_init(bars.empty(i / 2, i % 2), 2);  // both issuers
     }
-    mbar_init(bar_tail, 1);
+    mbar_init(bars.tail(), 1);
+    mbar_init(bars.kv(), 1);
+    mbar_init(bars.kv_free(), 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar_rows(i), 32);
-      mbar_init(bar_rows_read(i), 256);
-      mbar_init(bar_done(i), 1);
+      mbar_init(bars.rows(i), 32);
+      mbar_init(bars.rows_read(i), 256);
+      mbar_init(bars.first(i), 1);
+      mbar_init(bars.packed(i), 256);
+      mbar_init(bars.second(i), 1);
+      mbar_init(bars.out_free(i), 128);
+      mbar_init(bars.done(i), 1);
+      turns[i] = 0;
     }
-    mbar_init(bar_s, 1);
-    mbar_init(bar_p, 256);
-    mbar_init(bar_dp, 1);
-    mbar_init(bar_ds, 256);
-    mbar_init(bar_dv, 1);
-    mbar_init(bar_dk, 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(bars.item() + 8u * i, 1);
+      mbar_init(bars.item_read() + 8u * i, 256 + 3);  // weights, issuers, copies
+    }
     fence_barrier_init();
     tma_prefetch_desc(&tm_q);
     tma_prefetch_desc(&tm_do);
@@ -504,154 +766,174 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   }
   if (used < kRows) {
     // Rows that no copy writes are summed over all the same: zero, once.
-    for (int s = 0; s < L::kSlots; ++s)
-      clear_rows<D>(smem + L::kRing + s * L::kTile, used, threadIdx.x, kDkvThreads);
+    for (int s = 0; s < 2 * L::kPairs; ++s)
+      clear_rows<D>(smem + L::kRing + s * L::kTile, used, threadIdx.x, kThreads);
     fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int b = item[0];
-  if (b >= 0) {
-    const Seq seq = load_seq(p, b);
-    const int off = seq.nk - seq.nq;
-    // the pieces' work grows with their index: the first keys, seen by most queries, come last
-    const int key0 = (p.causal ? (seq.nk + kKeys - 1) / kKeys - 1 - item[1] : item[1]) * kKeys;
-    const int it0 = p.causal ? max(0, key0 - off) / p.q_per_tile : 0;  // first query tile that sees a key
-    const int n = max(0, (seq.nq + p.q_per_tile - 1) / p.q_per_tile - it0);
-    auto full = [&](int i) { return mbar_wait(bar_full(i % L::kSlots), (i / L::kSlots) & 1, p.status); };
-    if (warp == 8) {
-      // ---------------------------------- copies ----------------------------------------
-      bool ok = true;
-      int issued = 0;
-      const int rows = n > 0 ? (seq.nq - (it0 + n - 1) * p.q_per_tile) * p.G : 0;  // of the last query tile
-      const bool tail = n > 0 && rows < used;
-      if (lane == 0 && n > 0) {
-        mbar_arrive_expect_tx(bar_kv, 2 * L::kTile);
-        for (int kb = 0; kb < D / 64; ++kb) {
-          tma_load_3d(s_base + L::kK + kb * kBlock, &tm_k, bar_kv, kb * 64, hk, seq.k0 + key0);
-          tma_load_3d(s_base + L::kV + kb * kBlock, &tm_v, bar_kv, kb * 64, hk, seq.k0 + key0);
-        }
-        const uint32_t bytes = static_cast<uint32_t>(128 * (D / 64) * used);
-        for (int i = 0; i < 2 * n; ++i) {  // Q_0, dO_0, Q_1, dO_1, ...
-          const int slot = i % L::kSlots;
-          if (i >= L::kSlots && !(ok = mbar_wait(bar_empty(slot), (i / L::kSlots - 1) & 1, p.status))) break;
-          const bool in_tail = tail && i >= 2 * n - 2;
-          const uint32_t bar = in_tail ? bar_tail : bar_full(slot);
-          // (the tail's barrier counts one arrival, for both of its copies)
-          if (!in_tail) mbar_arrive_expect_tx(bar, bytes);
-          else if (i == 2 * n - 2) mbar_arrive_expect_tx(bar, 2 * bytes);
-          for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(s_base + L::kRing + slot * L::kTile + kb * kBlock, (i & 1) ? &tm_do : &tm_q, bar, kb * 64,
-                        hk * p.G, seq.q0 + (it0 + i / 2) * p.q_per_tile);
-          issued = i + 1;
-        }
+  if (warp == 11) {
+    // --------------- work items; lse and delta of each query row; rows past the end ----------------
+    auto pieces = [&](int s, int& n, int& first) {
+      const Seq q = load_seq(p, s);
+      n = (q.nk + kKeys - 1) / kKeys;
+      first = p.causal ? 0 : q.nq / kKeys;
+    };
+    const Finder finder(p.B, !p.causal, pieces);
+    auto find = [&](int k) {
+      Item item{};
+      item.at = -1;
+      const int rank = dealt(k);
+      int b, t;
+      finder.find(rank / p.Hkv, pieces, b, t);
+      if (b >= 0) {
+        item.seq = load_seq(p, b);
+        // a piece's work grows with its index: the first keys, which most queries see, come last
+        item.at = (p.causal ? (item.seq.nk + kKeys - 1) / kKeys - 1 - t : t) * kKeys;
+        item.head = rank % p.Hkv;
       }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      if (ok && tail) {
-        // query rows past the sequence's end, which the sums over rows must not see
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_tail, 0, p.status));
-        for (int i = 2 * n - 2; ok && i < 2 * n; ++i)
-          clear_rows<D>(smem + L::kRing + (i % L::kSlots) * L::kTile, rows, lane, 32);
-        fence_proxy_async_smem();
-        __syncwarp();
-        for (int i = 2 * n - 2; ok && lane == 0 && i < 2 * n; ++i) mbar_arrive(bar_full(i % L::kSlots));
+      return item;
+    };
+    bool ok = true;
+    auto publish = [&](int k, const Item& item) {
+      if (k >= kItems)
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kItems), (k / kItems - 1) & 1, p.status));
+      if (ok && lane == 0) {
+        items[k % kItems] = item;
+        mbar_arrive(bars.item() + 8u * (k % kItems));
       }
-      if (lane == 0 && issued < 2 * n) {
-        // A wait ran out: let the copies in flight land before the CTA ends (of the tail's two the
-        // first alone may be on its way: its barrier then does not complete, and the wait's own
-        // limit, far longer than a copy takes, stands for it)
-        mbar_wait(bar_kv, 0, nullptr);
-        for (int i = max(0, issued - L::kSlots); i < issued; ++i) {
-          const bool in_tail = tail && i >= 2 * n - 2;
-          mbar_wait(in_tail ? bar_tail : bar_full(i % L::kSlots), in_tail ? 0 : (i / L::kSlots) & 1, nullptr);
-        }
-      }
-    } else if (warp == 9 || warp == 10) {
-      // --------------------- issuer 9: S^T and dV; issuer 10: dP^T and dK ----------------
-      // first = left . (ring tile of this role)^T, second += packed . (the other role's ring tile)
-      const int x = warp - 9;
-      if (lane == 0 && n > 0) {
-        constexpr uint32_t idesc1 = idesc_f16(BF16, kRows, kRows, false, false);
-        constexpr uint32_t idesc2 = idesc_f16(BF16, kRows, D, false, true);
-        const uint64_t left = sdesc_sw128(s_base + (x ? L::kV : L::kK), 16, 1024);
-        const uint64_t ring1 = sdesc_sw128(s_base + L::kRing, 16, 1024), ring2 = sdesc_sw128(s_base + L::kRing, kBlock, 1024);
-        const uint32_t tm1 = tmem + (x ? L::kDp : L::kS), tm2 = tmem + (x ? L::kDk : L::kDv), tm_a = tmem + (x ? L::kDs : L::kP);
-        const uint32_t bar1 = x ? bar_dp : bar_s, bar_a = x ? bar_ds : bar_p, bar2 = x ? bar_dk : bar_dv;
-        // Q_i is ring entry 2i, dO_i 2i + 1: S^T reads Q and dV dO; dP^T reads dO and dK Q
-        bool ok = mbar_wait(bar_kv, 0, p.status) && full(x);
-        if (ok) {
-          tc_fence_after();
-          product_ss<D>(tm1, left, sdesc_add(ring1, (x % L::kSlots) * L::kTile), idesc1);
-          tc_commit(bar1);
-          tc_commit(bar_empty(x % L::kSlots));
-        }
-        for (int i = 0; ok && i < n; ++i) {
-          const int mine = 2 * i + 2 + x, other = 2 * i + 1 - x;
-          if (!(ok = mbar_wait(bar_a, i & 1, p.status))) break;
-          if (!(ok = full(other))) break;
-          if (i + 1 < n && !(ok = full(mine))) break;
-          tc_fence_after();
-          product_ts(tm2, tm_a, L::kStep, sdesc_add(ring2, (other % L::kSlots) * L::kTile), idesc2, i == 0);
-          tc_commit(bar2);
-          tc_commit(bar_empty(other % L::kSlots));
-          if (i + 1 < n) {
-            product_ss<D>(tm1, left, sdesc_add(ring1, (mine % L::kSlots) * L::kTile), idesc1);
-            tc_commit(bar1);
-            tc_commit(bar_empty(mine % L::kSlots));
-          }
-        }
-        tc_commit(bar_done(x));
-        mbar_wait(bar_done(x), 0, nullptr);
-      }
-    } else if (warp == 11) {
-      // --------------------- lse and delta of each query row, ready for use ---------------
-      float f = 1.f;
-      if constexpr (!BF16) f = power_for(__uint_as_float(__ldcg(gp.dout_max))) * 0.0078125f;  // 2^-kPower
-      bool ok = true;
-      for (int i = 0; ok && i < n; ++i) {
-        const int q0 = (it0 + i) * p.q_per_tile;
+    };
+    float f = kUnpower;
+    if constexpr (!BF16) f *= power_for(__uint_as_float(__ldcg(gp.dout_max)));
+    int step = 0, tails = 0;
+    Item item = find(0);
+    publish(0, item);
+    for (int k = 0; ok && item.at >= 0; ++k) {
+      const Item ahead = find(k + 1);
+      publish(k + 1, ahead);
+      int first_tile;
+      const int n = query_tiles(p, item.seq, item.at, first_tile);
+      const int last_rows = n > 0 ? (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G : used;
+      for (int i = 0; ok && i < n; ++i, ++step) {
+        const int q0 = (first_tile + i) * p.q_per_tile;
         float nl[4], nd[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int r = lane * 4 + e, token = q0 + r / p.G;
-          nl[e] = -INFINITY;  // no query, or one that sees no key: P = 0
+          nl[e] = -INFINITY;  // no query: P = 0
           nd[e] = 0.f;
-          if (r < used && token < seq.nq) {
-            const int64_t at = static_cast<int64_t>(seq.q0 + token) * p.Hq + hk * p.G + r % p.G;
-            const float lse = __ldg(gp.lse + at);
-            if (!(lse == -INFINITY)) nl[e] = kPower - lse * prefill::kLog2e;
-            nd[e] = -f * __ldg(gp.delta + at);
+          if (r < used && token < item.seq.nq) {
+            const float2 rd = __ldg(gp.rows + static_cast<int64_t>(item.seq.q0 + token) * p.Hq + item.head * p.G + r % p.G);
+            nl[e] = rd.x + kPower;
+            nd[e] = -f * rd.y;
           }
         }
-        if (i >= 2) ok = __all_sync(0xffffffffu, mbar_wait(bar_rows_read(i & 1), (i / 2 - 1) & 1, p.status));
-        float* to = reinterpret_cast<float*>(smem + L::kRowData) + (i & 1) * 2 * kRows + lane * 4;
-        *reinterpret_cast<float4*>(to) = make_float4(nl[0], nl[1], nl[2], nl[3]);
-        *reinterpret_cast<float4*>(to + kRows) = make_float4(nd[0], nd[1], nd[2], nd[3]);
-        mbar_arrive(bar_rows(i & 1));
+        if (step >= 2)
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.rows_read(step & 1), (step / 2 - 1) & 1, p.status));
+        float* to = reinterpret_cast<float*>(smem + L::kRowData) + (step & 1) * 2 * kRows + lane * 4;
+        if (ok) {
+          *reinterpret_cast<float4*>(to) = make_float4(nl[0], nl[1], nl[2], nl[3]);
+          *reinterpret_cast<float4*>(to + kRows) = make_float4(nd[0], nd[1], nd[2], nd[3]);
+          mbar_arrive(bars.rows(step & 1));
+        }
+        if (ok && i == n - 1 && last_rows < used) {
+          // query rows past the sequence's end, which the sums over rows must not see
+          const int pair = step % L::kPairs;
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
+          ++tails;
+          for (int x = 0; ok && x < 2; ++x)
+            clear_rows<D>(smem + L::kRing + (2 * pair + x) * L::kTile, last_rows, lane, 32);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (ok && lane < 2) mbar_arrive(bars.full(pair, lane));
+        }
       }
-    } else {
-      // -------------------- weights: a key and 64 query columns a thread ------------------
-      const int w = warp / 4, r = threadIdx.x % 128;
-      const int key = key0 + r;
-      const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-      const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
-      const uint32_t tm_p = tmem + L::kP + w * L::kStep + lanes, tm_ds = tmem + L::kDs + w * L::kStep + lanes;
-      float f = 1.f;
-      if constexpr (!BF16) f = power_for(__uint_as_float(__ldcg(gp.dout_max)));
-      const float fs = BF16 ? 1.f : f * 0.0078125f;  // 2^-kPower
-      const float2 a2 = make_float2(p.scale_log2, p.scale_log2), f2 = make_float2(fs, fs);
+      item = ahead;
+    }
+  } else if (warp == 8) {
+    // ---------------------------------- copies ----------------------------------------------
+    if (lane == 0) {
       bool ok = true;
-      for (int i = 0; i < n; ++i) {
-        const float4* row_data = reinterpret_cast<const float4*>(smem + L::kRowData) + (i & 1) * 64 + w * 16;
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_rows(i & 1), (i / 2) & 1, p.status));
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bar_s, i & 1, p.status));
+      int step = 0, uses = 0, tails = 0, tail_at = -1;
+      const uint32_t bytes = static_cast<uint32_t>(128 * (D / 64) * used);
+      Item item;
+      for (int k = 0; ok && next_item(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+        int first_tile;
+        const int n = query_tiles(p, item.seq, item.at, first_tile);
+        if (n == 0) continue;
+        if (uses > 0 && !(ok = mbar_wait(bars.kv_free(), (uses - 1) & 1, p.status))) break;
+        ++uses;
+        mbar_arrive_expect_tx(bars.kv(), 2 * L::kTile);
+        for (int kb = 0; kb < D / 64; ++kb) {
+          tma_load_3d(s_base + L::kK + kb * kBlock, &tm_k, bars.kv(), kb * 64, item.head, item.seq.k0 + item.at);
+          tma_load_3d(s_base + L::kV + kb * kBlock, &tm_v, bars.kv(), kb * 64, item.head, item.seq.k0 + item.at);
+        }
+        const bool tail = (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G < used;
+        for (int i = 0; i < n; ++i, ++step) {
+          const int pair = step % L::kPairs, lap = step / L::kPairs;
+          const bool in_tail = tail && i == n - 1;
+          // Both copies of a pair wait for both of its places: on a failure none is left without the other.
+          if (lap > 0 && !((ok = mbar_wait(bars.empty(pair, 0), (lap - 1) & 1, p.status)) &&
+                           (ok = mbar_wait(bars.empty(pair, 1), (lap - 1) & 1, p.status))))
+            break;
+          if (in_tail) {
+            tail_at = step;
+            ++tails;
+            mbar_arrive_expect_tx(bars.tail(), 2 * bytes);
+          }
+          for (int x = 0; x < 2; ++x) {
+            const uint32_t bar = in_tail ? bars.tail() : bars.full(pair, x);
+            if (!in_tail) mbar_arrive_expect_tx(bar, bytes);
+            for (int kb = 0; kb < D / 64; ++kb)
+              tma_load_3d(s_base + L::kRing + (2 * pair + x) * L::kTile + kb * kBlock, x ? &tm_do : &tm_q, bar, kb * 64,
+                          item.head * p.G, item.seq.q0 + (first_tile + i) * p.q_per_tile);
+          }
+        }
+      }
+      if (!ok) {
+        // A wait ran out: let the copies in flight land before the block ends
+        if (uses > 0) mbar_wait(bars.kv(), (uses - 1) & 1, nullptr);
+        for (int i = max(0, step - L::kPairs); i < step; ++i) {
+          if (i == tail_at) {
+            mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
+          } else {
+            mbar_wait(bars.full(i % L::kPairs, 0), (i / L::kPairs) & 1, nullptr);
+            mbar_wait(bars.full(i % L::kPairs, 1), (i / L::kPairs) & 1, nullptr);
+          }
+        }
+      }
+    }
+  } else if (warp == 9) {
+    issue_pair<D, BF16, 0>(p, s_base, bars.at, tmem, items, turns);
+  } else if (warp == 10) {
+    issue_pair<D, BF16, 1>(p, s_base, bars.at, tmem, items, turns);
+  } else {
+    // -------------------- weights: a key and 64 query columns a thread ------------------------
+    const int w = warp / 4, r = threadIdx.x % 128;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
+    const uint32_t tm_p = tmem + L::kP + w * L::kStep + lanes, tm_ds = tmem + L::kDs + w * L::kStep + lanes;
+    float f = 1.f;
+    if constexpr (!BF16) f = power_for(__uint_as_float(__ldcg(gp.dout_max)));
+    const float2 a2 = make_float2(p.scale_log2, p.scale_log2), f2 = make_float2(f * kUnpower, f * kUnpower);
+    bool ok = true;
+    int step = 0;
+    Item item;
+    for (int k = 0; ok && __all_sync(0xffffffffu, next_item(bars.item(), bars.item_read(), items, k, item, p.status)); ++k) {
+      int first_tile;
+      const int n = query_tiles(p, item.seq, item.at, first_tile);
+      const int key = item.at + r;
+      // columns below `from` are queries in front of the key
+      int from = p.causal ? (key - (item.seq.nk - item.seq.nq) - first_tile * p.q_per_tile) * p.G - w * kHalf : 0;
+      for (int i = 0; i < n; ++i, ++step, from -= used) {
+        const float4* row_data = reinterpret_cast<const float4*>(smem + L::kRowData) + (step & 1) * 64 + w * 16;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.rows(step & 1), (step / 2) & 1, p.status));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.first(0), step & 1, p.status));
         if (!ok) break;
         tc_fence_after();
-        // columns below `from` are queries in front of the key
-        const int from = p.causal ? (key - off - (it0 + i) * p.q_per_tile) * p.G - w * kHalf : 0;
-        const bool whole = __all_sync(0xffffffffu, from <= 0);
+        const bool whole = !p.causal || __all_sync(0xffffffffu, from <= 0);
         uint32_t raw[2][32];
         tmem_ld32(tm_s, raw[0]);
         tmem_ld32(tm_s + 32, raw[1]);
@@ -675,16 +957,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         }
 #pragma unroll
         for (int c = 0; c < 32; ++c) pk[c] = pack<BF16>(x[c]);
-        if (L::kApart && i > 0) {  // P^T_{i-1} has to be read before P^T_i takes its place
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_dv, (i - 1) & 1, p.status));
-          if (!ok) break;
-          tc_fence_after();
-        }
+        // (P^T_{i-1} has been read: the commit that told of S^T_i covers dV_{i-1} before it)
         tmem_st32(tm_p, pk);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_p);
-        ok = __all_sync(0xffffffffu, mbar_wait(bar_dp, i & 1, p.status));
+        mbar_arrive(bars.packed(0));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.first(1), step & 1, p.status));
         if (!ok) break;
         tc_fence_after();
         uint32_t dp[2][32], ds[32];
@@ -705,40 +983,38 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
             ds[16 * q + 2 * c + 1] = pack<BF16>(__fmul2_rn(x[16 * q + 2 * c + 1], u));
           }
         }
-        mbar_arrive(bar_rows_read(i & 1));
-        if (L::kApart && i > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bar_dk, (i - 1) & 1, p.status));
-          if (!ok) break;
-          tc_fence_after();
-        }
+        mbar_arrive(bars.rows_read(step & 1));
         tmem_st32(tm_ds, ds);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar_ds);
+        mbar_arrive(bars.packed(1));
       }
       if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(w ? bar_dk : bar_dv, (n - 1) & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.second(w), (step - 1) & 1, p.status));
         tc_fence_after();
       }
-      if (ok) {
-        // dv by the first four warps, dk by the others
-        const bool valid = key < seq.nk;
-        const int64_t row = seq.k0 + key;
-        uint16_t* dst = w ? static_cast<uint16_t*>(gp.dk) + row * gp.dk_strides[0] + hk * gp.dk_strides[1]
-                          : static_cast<uint16_t*>(gp.dv) + row * gp.dv_strides[0] + hk * gp.dv_strides[1];
-        const float back = w ? p.scale / f : BF16 ? 1.f : 0.0078125f;
-#pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld32(tmem + (w ? L::kDk : L::kDv) + lanes + c * 32, o);
-            prefill::tmem_ld_wait_tied(o);
-          } else {
+      if (!ok) break;
+      // dv by the first four warps, dk by the others
+      const int64_t row = item.seq.k0 + key;
+      uint16_t* dst = w ? static_cast<uint16_t*>(gp.dk) + row * gp.dk_strides[0] + item.head * gp.dk_strides[1]
+                        : static_cast<uint16_t*>(gp.dv) + row * gp.dv_strides[0] + item.head * gp.dv_strides[1];
+      if (key >= item.seq.nk) dst = nullptr;
+      const float back = w ? p.scale / f : kUnpower;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0u;
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32(tmem + (w ? L::kDk : L::kDv) + lanes + c * 32, o);
+          prefill::tmem_ld_wait_tied(o);
+          if (c == D / 32 - 1) {
+            tc_fence_before();
+            mbar_arrive(bars.out_free(w));
           }
-          if (valid) store32<BF16>(dst + c * 32, o, back);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
+        store32<BF16>(dst ? dst + c * 32 : nullptr, o, back, smem + L::kStage + warp * 2048);
       }
     }
   }
@@ -759,17 +1035,26 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   if (e == cudaSuccess) e = ensure_smem_limit(kk, DkvLayout<D>::kAlloc);
   if (e == cudaSuccess && !BF16) e = cudaMemsetAsync(g.dout_max, 0, sizeof(uint32_t), st);
   if (e != cudaSuccess) return e;
-  if (q_items > 0)
-    kq<<<static_cast<unsigned>(q_items * g.f.Hkv), kDqThreads, DqLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
-  if (k_items > 0)
-    kk<<<static_cast<unsigned>(k_items * g.f.Hkv), kDkvThreads, DkvLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
+  const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+  auto blocks = [&](int64_t items) { return static_cast<unsigned>(items * g.f.Hkv < sms ? items * g.f.Hkv : sms); };
+  if (q_items > 0) {
+    constexpr int64_t kPer = kRowThreads / (D / 8) * kRowBatch;
+    const int64_t rows = static_cast<int64_t>(g.f.total_q) * g.f.Hq;
+    row_kernel<D, BF16><<<static_cast<unsigned>((rows + kPer - 1) / kPer), kRowThreads, 0, st>>>(g);
+    kq<<<blocks(q_items), kThreads, DqLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
+  }
+  if (k_items > 0) kk<<<blocks(k_items), kThreads, DkvLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
   return cudaGetLastError();
 }
 
-constexpr size_t kWordBytes = 256;  // in front of delta: the largest |dout|
+constexpr size_t kWordBytes = 256;  // in front: the largest |dout|
+
+size_t row_bytes(const fa_packed_backward_args* a) {
+  return (static_cast<size_t>(a->total_q) * a->Hq * sizeof(float2) + 255) / 256 * 256;
+}
 
 size_t workspace_bytes(const fa_packed_backward_args* a) {
-  return kWordBytes + (static_cast<size_t>(a->total_q) * a->Hq * sizeof(float) + 255) / 256 * 256;
+  return kWordBytes + row_bytes(a) + (a->dtype == FA_FP16 ? (row_bytes(a) / 2 + 255) / 256 * 256 : 0);
 }
 
 }  // namespace
@@ -846,7 +1131,8 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   memcpy(g.dv_strides, a->dv_strides, sizeof g.dv_strides);
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   g.dout_max = reinterpret_cast<uint32_t*>(ws);
-  g.delta = reinterpret_cast<float*>(ws + packed::kWordBytes);
+  g.rows = reinterpret_cast<float2*>(ws + packed::kWordBytes);
+  g.powers = reinterpret_cast<float*>(ws + packed::kWordBytes + packed::row_bytes(a));
   const bool bf16 = a->dtype == FA_BF16;
   // Maps of an empty side are read by nothing; they get the workspace as their address.
   const bool hq = a->total_q > 0, hk = a->total_k > 0;

@@ -140,8 +140,8 @@ def test_nothing_to_do(lib):
 
 def test_workspace_sizes(lib):
     size = lib.fa_packed_backward_workspace_size
-    assert size(ctypes.byref(_packed_backward())) == 256 + 256          # 9 * 4 fp32, and a word
-    assert size(ctypes.byref(_packed_backward(total_q=1000))) == 256 + 16128
+    assert size(ctypes.byref(_packed_backward())) == 256 + 512          # 9 * 4 pairs of fp32, and a word
+    assert size(ctypes.byref(_packed_backward(total_q=1000))) == 256 + 32000
     assert size(ctypes.byref(_packed_backward(B=0))) == 0
     assert size(ctypes.byref(_packed_backward(D=80))) == 0
     size = lib.fa_qk_norm_rotary_backward_workspace_size
