@@ -89,6 +89,19 @@ __device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&o)[32], 
   }
 }
 
+// The same, each lane its own row's 64 bytes: for a kernel that has no shared memory left.
+template <bool BF16>
+__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t (&o)[32], float f) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack<BF16>(make_float2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f));
+    reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 // Rows r0.. of a 128-row tile in shared memory set to zero by `n` threads.
 template <int D>
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int r0, int at, int n) {
@@ -598,14 +611,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------------------------------------
 template <int D>
 struct DkvLayout {
-  static constexpr int kPairs = D == 128 ? 2 : 4;  // ring: pairs of a Q and a dO tile
+  // Ring of Q and dO tiles by turns.  Q_{i+1} is needed as soon as dK_{i-1}, the last to read Q_{i-1}, is
+  // done: with two places for Q the load would be waited for every tile (D = 128: 3930 clocks a tile).
+  static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kTile = kBlock * (D / 64);
   static constexpr int kK = 0, kV = kTile, kRing = 2 * kTile;
-  static constexpr int kStage = kRing + 2 * kPairs * kTile;  // 2 KB for each of the eight warps
-  static constexpr int kRowData = kStage + 8 * 2048;         // [2][-lse, -delta][128] fp32
+  static constexpr int kRowData = kRing + kSlots * kTile;    // [2][-lse, -delta][128] fp32
   static constexpr int kBars = kRowData + 2 * 2 * kRows * 4;
-  static constexpr int kNumBars = 4 * kPairs + 17 + 2 * kItems;
-  static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;
+  static constexpr int kNumBars = 2 * kSlots + 17 + 2 * kItems;
+  static constexpr int kShared = kBars + kNumBars * 8;       // work items, turns, tensor memory's address
+  // No room is left to align the base by hand: the kernel has no static shared memory, and its dynamic
+  // one is declared with this alignment.
+  static constexpr int kAlloc = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;
   static constexpr bool kApart = D == 64;
   static constexpr int kDv = 0, kDk = D, kS = 2 * D, kDp = kS + kRows;
   static constexpr int kP = kApart ? kDp + kRows : kS, kDs = kApart ? kP + kRows / 2 : kDp;
@@ -618,22 +635,33 @@ struct DkvBars {
   using L = DkvLayout<D>;
   uint32_t at;
   __device__ __forceinline__ uint32_t one(int i) const { return at + 8u * i; }
-  // of Q (which = 0) or dO (1) of a pair
-  __device__ __forceinline__ uint32_t full(int pair, int which) const { return one(2 * pair + which); }
-  __device__ __forceinline__ uint32_t empty(int pair, int which) const { return one(2 * L::kPairs + 2 * pair + which); }
-  __device__ __forceinline__ uint32_t tail() const { return one(4 * L::kPairs); }
-  __device__ __forceinline__ uint32_t kv() const { return one(4 * L::kPairs + 1); }
-  __device__ __forceinline__ uint32_t kv_free() const { return one(4 * L::kPairs + 2); }
-  __device__ __forceinline__ uint32_t rows(int i) const { return one(4 * L::kPairs + 3 + i); }
-  __device__ __forceinline__ uint32_t rows_read(int i) const { return one(4 * L::kPairs + 5 + i); }
+  __device__ __forceinline__ uint32_t full(int slot) const { return one(slot); }
+  __device__ __forceinline__ uint32_t empty(int slot) const { return one(L::kSlots + slot); }
+  __device__ __forceinline__ uint32_t tail() const { return one(2 * L::kSlots); }
+  __device__ __forceinline__ uint32_t kv() const { return one(2 * L::kSlots + 1); }
+  __device__ __forceinline__ uint32_t kv_free() const { return one(2 * L::kSlots + 2); }
+  __device__ __forceinline__ uint32_t rows(int i) const { return one(2 * L::kSlots + 3 + i); }
+  __device__ __forceinline__ uint32_t rows_read(int i) const { return one(2 * L::kSlots + 5 + i); }
   // x = 0: S^T, P^T, dV; 1: dP^T, dS^T, dK
-  __device__ __forceinline__ uint32_t first(int x) const { return one(4 * L::kPairs + 7 + x); }
-  __device__ __forceinline__ uint32_t packed(int x) const { return one(4 * L::kPairs + 9 + x); }
-  __device__ __forceinline__ uint32_t second(int x) const { return one(4 * L::kPairs + 11 + x); }
-  __device__ __forceinline__ uint32_t out_free(int x) const { return one(4 * L::kPairs + 13 + x); }
-  __device__ __forceinline__ uint32_t done(int x) const { return one(4 * L::kPairs + 15 + x); }
-  __device__ __forceinline__ uint32_t item() const { return one(4 * L::kPairs + 17); }
-  __device__ __forceinline__ uint32_t item_read() const { return one(4 * L::kPairs + 17 + kItems); }
+  __device__ __forceinline__ uint32_t first(int x) const { return one(2 * L::kSlots + 7 + x); }
+  __device__ __forceinline__ uint32_t packed(int x) const { return one(2 * L::kSlots + 9 + x); }
+  __device__ __forceinline__ uint32_t second(int x) const { return one(2 * L::kSlots + 11 + x); }
+  __device__ __forceinline__ uint32_t out_free(int x) const { return one(2 * L::kSlots + 13 + x); }
+  __device__ __forceinline__ uint32_t done(int x) const { return one(2 * L::kSlots + 15 + x); }
+  __device__ __forceinline__ uint32_t item() const { return one(2 * L::kSlots + 17); }
+  __device__ __forceinline__ uint32_t item_read() const { return one(2 * L::kSlots + 17 + kItems); }
+};
+
+// A place in the ring, and how often the ring has been gone through before it.
+template <int SLOTS>
+struct Place {
+  int slot = 0, lap = 0;
+  __device__ __forceinline__ Place next() const {
+    Place n;
+    n.slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    n.lap = slot + 1 == SLOTS ? lap + 1 : lap;
+    return n;
+  }
 };
 
 // First query tile that sees a key of the tile at key0, and how many tiles from there on there are.
@@ -654,37 +682,36 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
   const bool leader = (threadIdx.x & 31) == 0;
   tmem = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
   const uint64_t left = sdesc_sw128(s_base + (X ? L::kV : L::kK), 16, 1024);
-  const uint64_t ring1 = sdesc_sw128(s_base + L::kRing + X * L::kTile, 16, 1024);
-  const uint64_t ring2 = sdesc_sw128(s_base + L::kRing + (1 - X) * L::kTile, kBlock, 1024);
+  const uint64_t ring1 = sdesc_sw128(s_base + L::kRing, 16, 1024), ring2 = sdesc_sw128(s_base + L::kRing, kBlock, 1024);
   const uint32_t tm1 = tmem + (X ? L::kDp : L::kS), tm2 = tmem + (X ? L::kDk : L::kDv), tm_a = tmem + (X ? L::kDs : L::kP);
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase) {
     ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
     return ok;
   };
-  int pair = 0, lap = 0, step = 0, uses = 0;
+  Place<L::kSlots> q;  // of the tile's Q; its dO is the next
+  int step = 0, uses = 0;
   Item item;
   for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
     int first_tile;
     const int n = uniform(query_tiles(p, item.seq, item.at, first_tile));
     if (n == 0) continue;
-    if (!wait(bars.kv(), uses) || !wait(bars.full(pair, X), lap)) break;
+    const Place<L::kSlots> start = X ? q.next() : q;
+    if (!wait(bars.kv(), uses) || !wait(bars.full(start.slot), start.lap)) break;
     tc_fence_after();
     if (leader) {
-      product_ss<D>(tm1, left, sdesc_add(ring1, 2 * pair * L::kTile), idesc1);
+      product_ss<D>(tm1, left, sdesc_add(ring1, start.slot * L::kTile), idesc1);
       tc_commit(bars.first(X));
-      tc_commit(bars.empty(pair, X));
+      tc_commit(bars.empty(start.slot));
       if (n == 1) tc_commit(bars.kv_free());
     }
     __syncwarp();
     for (int i = 0; i < n; ++i, ++step) {
-      const int at = pair;
-      if (!wait(bars.full(at, 1 - X), lap)) break;
-      if (++pair == L::kPairs) {
-        pair = 0;
-        ++lap;
-      }
-      if (i + 1 < n && !wait(bars.full(pair, X), lap)) break;
+      const Place<L::kSlots> d = q.next(), q2 = d.next();
+      const Place<L::kSlots> other = X ? q : d, mine = X ? q2.next() : q2;
+      q = q2;
+      if (!wait(bars.full(other.slot), other.lap)) break;
+      if (i + 1 < n && !wait(bars.full(mine.slot), mine.lap)) break;
       // the item before has to be read before the first product overwrites it
       if (i == 0 && uses > 0 && !wait(bars.out_free(X), uses - 1)) break;
       // The other pair's turn first (dV and S^T of a tile before dK and dP^T, these before the next): one
@@ -693,14 +720,14 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
       if (!wait(bars.packed(X), step)) break;
       tc_fence_after();
       if (leader) {
-        product_ts(tm2, tm_a, L::kStep, sdesc_add(ring2, 2 * at * L::kTile), idesc2, i == 0);
-        if (i + 1 < n) product_ss<D>(tm1, left, sdesc_add(ring1, 2 * pair * L::kTile), idesc1);
+        product_ts(tm2, tm_a, L::kStep, sdesc_add(ring2, other.slot * L::kTile), idesc2, i == 0);
+        if (i + 1 < n) product_ss<D>(tm1, left, sdesc_add(ring1, mine.slot * L::kTile), idesc1);
         turns[X] = step + 1;  // (before the commits: after them the store would wait for the products)
         tc_commit(bars.second(X));
-        tc_commit(bars.empty(at, 1 - X));
+        tc_commit(bars.empty(other.slot));
         if (i + 1 < n) {
           tc_commit(bars.first(X));
-          tc_commit(bars.empty(pair, X));
+          tc_commit(bars.empty(mine.slot));
           if (i + 2 == n) tc_commit(bars.kv_free());
         }
       }
@@ -723,12 +750,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr float kPower = BF16 ? 0.f : 7.f;             // P is held times 2^kPower
   constexpr float kUnpower = BF16 ? 1.f : 0.0078125f;    // 2^-kPower
   const Params& p = gp.f;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  __shared__ uint32_t tmem_slot;
-  __shared__ Item items[kItems];
-  __shared__ int turns[2];  // pairs of products that each issuer has put into the pipe
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Item* items = reinterpret_cast<Item*>(smem + L::kShared);
+  int* turns = reinterpret_cast<int*>(items + kItems);  // pairs of products that each issuer has put into the pipe
+  uint32_t& tmem_slot = reinterpret_cast<uint32_t*>(turns)[2];
   const uint32_t s_base = smem_addr(smem);
   const DkvBars<D> bars{s_base + L::kBars};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -737,9 +762,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   } else if (threadIdx.x == 8 * 32) {
-    for (int i = 0; i < 2 * L::kPairs; ++i) {
-      mbar_init(bars.full(i / 2, i % 2), 1);
-      mbar_init(bars.empty(i / 2, i % 2), 2);  // both issuers
+    for (int i = 0; i < L::kSlots; ++i) {
+      mbar_init(bars.full(i), 1);
+      mbar_init(bars.empty(i), 2);  // both issuers
     }
     mbar_init(bars.tail(), 1);
     mbar_init(bars.kv(), 1);
@@ -766,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (used < kRows) {
     // Rows that no copy writes are summed over all the same: zero, once.
-    for (int s = 0; s < 2 * L::kPairs; ++s)
+    for (int s = 0; s < L::kSlots; ++s)
       clear_rows<D>(smem + L::kRing + s * L::kTile, used, threadIdx.x, kThreads);
     fence_proxy_async_smem();
   }
@@ -840,14 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && i == n - 1 && last_rows < used) {
           // query rows past the sequence's end, which the sums over rows must not see
-          const int pair = step % L::kPairs;
           ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
           ++tails;
           for (int x = 0; ok && x < 2; ++x)
-            clear_rows<D>(smem + L::kRing + (2 * pair + x) * L::kTile, last_rows, lane, 32);
+            clear_rows<D>(smem + L::kRing + (2 * step + x) % L::kSlots * L::kTile, last_rows, lane, 32);
           fence_proxy_async_smem();
           __syncwarp();
-          if (ok && lane < 2) mbar_arrive(bars.full(pair, lane));
+          if (ok && lane < 2) mbar_arrive(bars.full((2 * step + lane) % L::kSlots));
         }
       }
       item = ahead;
@@ -856,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------- copies ----------------------------------------------
     if (lane == 0) {
       bool ok = true;
-      int step = 0, uses = 0, tails = 0, tail_at = -1;
+      int entry = 0, uses = 0, tails = 0, tail_at = -1;
       const uint32_t bytes = static_cast<uint32_t>(128 * (D / 64) * used);
       Item item;
       for (int k = 0; ok && next_item(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
@@ -871,37 +895,32 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(s_base + L::kV + kb * kBlock, &tm_v, bars.kv(), kb * 64, item.head, item.seq.k0 + item.at);
         }
         const bool tail = (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G < used;
-        for (int i = 0; i < n; ++i, ++step) {
-          const int pair = step % L::kPairs, lap = step / L::kPairs;
-          const bool in_tail = tail && i == n - 1;
-          // Both copies of a pair wait for both of its places: on a failure none is left without the other.
-          if (lap > 0 && !((ok = mbar_wait(bars.empty(pair, 0), (lap - 1) & 1, p.status)) &&
-                           (ok = mbar_wait(bars.empty(pair, 1), (lap - 1) & 1, p.status))))
-            break;
-          if (in_tail) {
-            tail_at = step;
+        for (int i = 0; ok && i < 2 * n; ++i, ++entry) {  // Q, dO, Q, dO, ...
+          const int slot = entry % L::kSlots, lap = entry / L::kSlots;
+          if (lap > 0 && !(ok = mbar_wait(bars.empty(slot), (lap - 1) & 1, p.status))) break;
+          const bool in_tail = tail && i >= 2 * n - 2;
+          const uint32_t bar = in_tail ? bars.tail() : bars.full(slot);
+          // (the tail's barrier counts one arrival, for both of its copies)
+          if (!in_tail) {
+            mbar_arrive_expect_tx(bar, bytes);
+          } else if (i == 2 * n - 2) {
+            tail_at = entry;
             ++tails;
-            mbar_arrive_expect_tx(bars.tail(), 2 * bytes);
+            mbar_arrive_expect_tx(bar, 2 * bytes);
           }
-          for (int x = 0; x < 2; ++x) {
-            const uint32_t bar = in_tail ? bars.tail() : bars.full(pair, x);
-            if (!in_tail) mbar_arrive_expect_tx(bar, bytes);
-            for (int kb = 0; kb < D / 64; ++kb)
-              tma_load_3d(s_base + L::kRing + (2 * pair + x) * L::kTile + kb * kBlock, x ? &tm_do : &tm_q, bar, kb * 64,
-                          item.head * p.G, item.seq.q0 + (first_tile + i) * p.q_per_tile);
-          }
+          for (int kb = 0; kb < D / 64; ++kb)
+            tma_load_3d(s_base + L::kRing + slot * L::kTile + kb * kBlock, (i & 1) ? &tm_do : &tm_q, bar, kb * 64,
+                        item.head * p.G, item.seq.q0 + (first_tile + i / 2) * p.q_per_tile);
         }
       }
       if (!ok) {
-        // A wait ran out: let the copies in flight land before the block ends
+        // A wait ran out: let the copies in flight land before the block ends.  (Of the tail's two the first
+        // alone may be on its way: its barrier then does not complete, and the wait's own limit, far longer
+        // than a copy takes, stands for it.)
         if (uses > 0) mbar_wait(bars.kv(), (uses - 1) & 1, nullptr);
-        for (int i = max(0, step - L::kPairs); i < step; ++i) {
-          if (i == tail_at) {
-            mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
-          } else {
-            mbar_wait(bars.full(i % L::kPairs, 0), (i / L::kPairs) & 1, nullptr);
-            mbar_wait(bars.full(i % L::kPairs, 1), (i / L::kPairs) & 1, nullptr);
-          }
+        for (int i = max(0, entry - L::kSlots); i < entry; ++i) {
+          if (tail_at >= 0 && (i == tail_at || i == tail_at + 1)) mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
+          else mbar_wait(bars.full(i % L::kSlots), (i / L::kSlots) & 1, nullptr);
         }
       }
     }
@@ -1014,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        store32<BF16>(dst ? dst + c * 32 : nullptr, o, back, smem + L::kStage + warp * 2048);
+        if (dst) store_row32<BF16>(dst + c * 32, o, back);
       }
     }
   }
