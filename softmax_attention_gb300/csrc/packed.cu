@@ -160,7 +160,6 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
   tmem = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
   constexpr uint32_t idesc_s = idesc_f16(BF16, kRows, kKeys, false, false);
   constexpr uint32_t idesc_o = idesc_f16(BF16, kRows, D, false, true);
-  const bool leader = (threadIdx.x & 31) == 0;
   const uint64_t q_desc = sdesc_sw128(s_base + X * L::kTile, 16, 1024);
   const uint64_t k_desc = sdesc_sw128(s_base + L::kRing, 16, 1024);
   const uint64_t v_desc = sdesc_sw128(s_base + L::kRing, L::kBlock, 1024);
@@ -192,7 +191,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
     if (__all_sync(0xffffffffu, mbar_wait(bars.item(k % kItems), (k / kItems) & 1, p.status))) {
       got = items[k % kItems];
       __syncwarp();
-      if (leader) mbar_arrive(bars.item_read(k % kItems));
+      if (elected()) mbar_arrive(bars.item_read(k % kItems));
       more = got.at >= 0;
     }
     if (!__any_sync(0xffffffffu, more)) break;
@@ -202,7 +201,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
     if (nx > 0) {
       if (!wait(bars.q(X), uses) || !wait(bars.full(slot), lap)) break;
       tc_fence_after();
-      if (leader) {
+      if (elected()) {
         issue_s(slot);
         tc_commit(bars.s(X));
         tc_commit(bars.empty(slot));
@@ -223,7 +222,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
       for (int spin = 0; spin < 4096 && turns[1 - X] < want; ++spin) {}
       if (!wait(bars.p(X), steps + j)) break;
       tc_fence_after();
-      if (leader) {
+      if (elected()) {
         const uint64_t vd = sdesc_add(v_desc, v_slot * L::kTile);
         // of the last tile, no more keys than the tile sees
         const int ksteps = min(kKeys / 16, (end - j * kKeys + 15) / 16);
@@ -253,7 +252,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
     // tiles that only the other one sees: released as they land, phase by phase
     for (int i = 2 * nx; i < 2 * n; ++i) {
       if (!wait(bars.full(slot), lap)) break;
-      if (leader) mbar_arrive(bars.empty(slot));
+      if (elected()) mbar_arrive(bars.empty(slot));
       next();
     }
     steps += nx;
@@ -261,7 +260,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
     uses += nx > 0 ? 1 : 0;
   }
   // every product must finish before tensor memory and the ring are given up
-  if (leader) {
+  if (elected()) {
     tc_commit(bars.done(X));
     mbar_wait(bars.done(X), 0, nullptr);
   }

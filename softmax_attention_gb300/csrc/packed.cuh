@@ -163,6 +163,14 @@ struct Item {
 // product, beside softmax warps that leave an issuing warp few slots.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
+// True in one lane of the warp, always the same.  (An election, not a lane's number: the compiler then
+// keeps the code behind it on uniform registers.)
+__device__ __forceinline__ bool elected() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
+
 // The most pieces of `width` rows that B sequences of `total` rows together can have.
 inline int64_t most_items(int64_t total, int64_t B, int64_t width) {
   return (total + B * (width - 1)) / width;

@@ -420,7 +420,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9 || warp == 10) {
     // ------------------- issuer 9: S = Q K^T and dP = dO V^T; issuer 10: dQ += dS K -------------------
-    const bool leader = lane == 0;
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     bool ok = true;
     auto wait = [&](uint32_t bar, int phase) {
@@ -442,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(bars.k_full(pair), lap)) break;
           if (step >= 2 && !wait(bars.dq(step & 1), step / 2 - 1)) break;  // dS_{step-2} read
           tc_fence_after();
-          if (leader) {
+          if (elected()) {
             product_ss<D>(tm + L::kS + (step & 1) * kKeys, q_desc, kd, idesc);
             tc_commit(bars.s(step & 1));
           }
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(bars.v_full(pair), lap)) break;
           if (step >= 1 && !wait(bars.dp_read(), step - 1)) break;
           tc_fence_after();
-          if (leader) {
+          if (elected()) {
             product_ss<D>(tm + L::kDp, do_desc, sdesc_add(kd, L::kTile), idesc);
             tc_commit(bars.dp());
             tc_commit(bars.v_empty(pair));
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!wait(bars.k_full(pair), lap)) break;
           if (!wait(bars.ds(step & 1), step / 2)) break;
           tc_fence_after();
-          if (leader) {
+          if (elected()) {
             product_ts(tm, tm + L::kS + (step & 1) * kKeys, kHalf, sdesc_add(ring, 2 * pair * L::kTile), idesc, j == 0);
             tc_commit(bars.dq(step & 1));
             tc_commit(bars.k_empty(pair));
@@ -490,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     // every product must finish before tensor memory and the ring are given up
-    if (leader) {
+    if (elected()) {
       tc_commit(bars.done(warp - 9));
       mbar_wait(bars.done(warp - 9), 0, nullptr);
     }
@@ -679,7 +678,6 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
   const DkvBars<D> bars{bar_base};
   constexpr uint32_t idesc1 = idesc_f16(BF16, kRows, kRows, false, false);
   constexpr uint32_t idesc2 = idesc_f16(BF16, kRows, D, false, true);
-  const bool leader = (threadIdx.x & 31) == 0;
   tmem = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
   const uint64_t left = sdesc_sw128(s_base + (X ? L::kV : L::kK), 16, 1024);
   const uint64_t ring1 = sdesc_sw128(s_base + L::kRing, 16, 1024), ring2 = sdesc_sw128(s_base + L::kRing, kBlock, 1024);
@@ -699,7 +697,7 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
     const Place<L::kSlots> start = X ? q.next() : q;
     if (!wait(bars.kv(), uses) || !wait(bars.full(start.slot), start.lap)) break;
     tc_fence_after();
-    if (leader) {
+    if (elected()) {
       product_ss<D>(tm1, left, sdesc_add(ring1, start.slot * L::kTile), idesc1);
       tc_commit(bars.first(X));
       tc_commit(bars.empty(start.slot));
@@ -719,7 +717,7 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
       for (int spin = 0; spin < 4096 && turns[1 - X] < (X ? step + 1 : step); ++spin) {}
       if (!wait(bars.packed(X), step)) break;
       tc_fence_after();
-      if (leader) {
+      if (elected()) {
         product_ts(tm2, tm_a, L::kStep, sdesc_add(ring2, other.slot * L::kTile), idesc2, i == 0);
         if (i + 1 < n) product_ss<D>(tm1, left, sdesc_add(ring1, mine.slot * L::kTile), idesc1);
         turns[X] = step + 1;  // (before the commits: after them the store would wait for the products)
@@ -736,7 +734,7 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
     ++uses;
   }
   // every product must finish before tensor memory and the ring are given up
-  if (leader) {
+  if (elected()) {
     tc_commit(bars.done(X));
     mbar_wait(bars.done(X), 0, nullptr);
   }
