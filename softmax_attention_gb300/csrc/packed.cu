@@ -428,129 +428,151 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_token = r / p.G, row_head = r % p.G;
     bool ok = true;
     int steps = 0;  // KV tiles of this query tile so far
-    Item item;
-    for (int k = 0; ok && __all_sync(0xffffffffu, next_item(bars, items, k, item, p.status)); ++k) {
+    // The item before, whose output is still in tensor memory: it is written when the first tile of the next
+    // has been dealt with, so that the wait for its last product, and the stores, have work beside them.
+    bool pending = false;
+    uint16_t* out_row = nullptr;
+    float* lse_row = nullptr;
+    float out_m = 0.f, out_l = 0.f;
+    int out_step = 0;
+    bool more = true;
+    for (int k = 0; ok && more; ++k) {
+      Item item{};
+      more = __all_sync(0xffffffffu, next_item(bars, items, k, item, p.status));
       const Tile tile = make_tile(p, item.seq, item.at + x * p.q_per_tile);
-      const int nx = tile.n;
+      const int nx = more ? tile.n : 0;
       const int i = tile.q0 + row_token, h = item.head * p.G + row_head;
-      const bool valid = r < p.G * p.q_per_tile && i < item.seq.nq;
+      const bool valid = more && r < p.G * p.q_per_tile && i < item.seq.nq;
       // a row of no query sees everything, so that it never asks for the slow path
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < nx; ++j, ++steps) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        const int left = key_lim - j * kKeys;  // keys of the tile that the row sees
-        bool done = false;
-        if (a > 0.f) {
-          const bool masked = __any_sync(0xffffffffu, left < kKeys);
-          if (j == 0) {
-            // a first guess at the maximum: that of the first 32 scores
-            uint32_t raw[32];
-            tmem_ld32(tm_s, raw);
-            prefill::tmem_ld_wait_tied(raw);
+      for (int j = 0; j < max(nx, 1); ++j) {
+        if (j < nx) {
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          const int left = key_lim - j * kKeys;  // keys of the tile that the row sees
+          bool done = false;
+          if (a > 0.f) {
+            const bool masked = __any_sync(0xffffffffu, left < kKeys);
+            if (j == 0) {
+              // a first guess at the maximum: that of the first 32 scores
+              uint32_t raw[32];
+              tmem_ld32(tm_s, raw);
+              prefill::tmem_ld_wait_tied(raw);
+              float top = -INFINITY;
+  #pragma unroll
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(raw[e]) : -INFINITY);
+              m = top > -INFINITY ? top * a : 0.f;
+            }
+            uint32_t pk[kKeys / 2];
+            float2 sum = make_float2(0.f, 0.f);
+            const float top = a * (masked ? sweep<BF16, true>(tm_s, left, a, m, sum, pk) : sweep<BF16, false>(tm_s, left, a, m, sum, pk));
+            if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
+              l += sum.x + sum.y;
+              // (P_{j-1} has been read: the commit that told of S_j covers P_{j-1} V_{j-1} before it)
+              prefill::store_p<kKeys>(tm_p, pk);
+              done = true;
+            }
+          }
+          if (!done) {
+            // a maximum that grew (or a scale that is not positive): the maximum first, then the weights
             float top = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(raw[e]) : -INFINITY);
-            m = top > -INFINITY ? top * a : 0.f;
-          }
-          uint32_t pk[kKeys / 2];
-          float2 sum = make_float2(0.f, 0.f);
-          const float top = a * (masked ? sweep<BF16, true>(tm_s, left, a, m, sum, pk) : sweep<BF16, false>(tm_s, left, a, m, sum, pk));
-          if (!__any_sync(0xffffffffu, valid && !(top <= m + kRescaleLog2))) {
+  #pragma unroll 1
+            for (int c = 0; c < kKeys; c += 32) {
+              uint32_t raw[32];
+              tmem_ld32(tm_s + c, raw);
+              prefill::tmem_ld_wait_tied(raw);
+  #pragma unroll
+              for (int e = 0; e < 32; ++e) top = fmaxf(top, c + e < left ? __uint_as_float(raw[e]) * a : -INFINITY);
+            }
+            const float before = l > 0.f ? m : -INFINITY;  // (a guess that nothing was added to is none)
+            const float m_new = fmaxf(before, top);
+            const bool need = valid && m_new > before + kRescaleLog2;
+            float alpha = 1.f;
+            if (need) {
+              alpha = exp2_approx(before - m_new);  // 0 when nothing was added before
+              m = m_new;
+              l *= alpha;
+            }
+            if (j > 0) {
+              // P_{j-1} V_{j-1} has to be in O before O is rescaled, and P_{j-1} read before P_j
+              ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
+              if (!ok) break;
+              tc_fence_after();
+              if (__any_sync(0xffffffffu, need)) prefill::rescale_o<D>(tm_o, alpha);
+            }
+            const float m_use = m == -INFINITY ? 0.f : m;
+            float2 sum = make_float2(0.f, 0.f);
+  #pragma unroll 1
+            for (int c = 0; c < kKeys; c += 32) {
+              uint32_t raw[32], pk[16];
+              tmem_ld32(tm_s + c, raw);
+              prefill::tmem_ld_wait_tied(raw);
+  #pragma unroll
+              for (int e = 0; e < 32; ++e) raw[e] = c + e < left ? __float_as_uint(__uint_as_float(raw[e]) * a) : 0xff800000u;
+              weigh<BF16>(raw, 1.f, m_use, sum, pk);
+              // (P over S: P's columns so far are no more than the scores already in registers)
+              tmem_st16(tm_p + c / 2, pk);
+            }
             l += sum.x + sum.y;
-            // (P_{j-1} has been read: the commit that told of S_j covers P_{j-1} V_{j-1} before it)
-            prefill::store_p<kKeys>(tm_p, pk);
-            done = true;
           }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bars.p(x));
+          ++steps;
         }
-        if (!done) {
-          // a maximum that grew (or a scale that is not positive): the maximum first, then the weights
-          float top = -INFINITY;
+        if (j == 0 && pending) {
+          pending = false;
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), out_step & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          const float inv = out_l > 0.f ? 1.f / out_l : 0.f;
 #pragma unroll 1
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t raw[32];
-            tmem_ld32(tm_s + c, raw);
-            prefill::tmem_ld_wait_tied(raw);
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t oa[32], ob[32];
+            tmem_ld32(tm_o + c * 64, oa);
+            tmem_ld32(tm_o + c * 64 + 32, ob);
+            prefill::tmem_ld_wait_tied(oa);
+            prefill::tmem_ld_wait_tied(ob);
+            if (c == D / 64 - 1) {
+              tc_fence_before();
+              mbar_arrive(bars.o_free(x));
+            }
+            // A thread's row would be written 16 bytes at a time, each of a warp's stores touching 32 rows:
+            // through shared memory (128-byte swizzle) a store writes four rows' 128 bytes.
+            uint8_t* mine = smem + L::kStage + warp * (32 * 128);
+            prefill::stage_slab16<BF16>(oa, inv, mine, lane, 0);
+            prefill::stage_slab16<BF16>(ob, inv, mine, lane, 1);
+            __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) top = fmaxf(top, c + e < left ? __uint_as_float(raw[e]) * a : -INFINITY);
+            for (int e = 0; e < 8; ++e) {
+              const int rr = 4 * e + lane / 8;
+              const uint4 v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((lane % 8) ^ (rr & 7)) * 16);
+              uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_row), rr));
+              if (to) *reinterpret_cast<uint4*>(to + c * 64 + (lane % 8) * 8) = v;
+            }
+            __syncwarp();
           }
-          const float before = l > 0.f ? m : -INFINITY;  // (a guess that nothing was added to is none)
-          const float m_new = fmaxf(before, top);
-          const bool need = valid && m_new > before + kRescaleLog2;
-          float alpha = 1.f;
-          if (need) {
-            alpha = exp2_approx(before - m_new);  // 0 when nothing was added before
-            m = m_new;
-            l *= alpha;
-          }
-          if (j > 0) {
-            // P_{j-1} V_{j-1} has to be in O before O is rescaled, and P_{j-1} read before P_j
-            ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
-            if (!ok) break;
-            tc_fence_after();
-            if (__any_sync(0xffffffffu, need)) prefill::rescale_o<D>(tm_o, alpha);
-          }
-          const float m_use = m == -INFINITY ? 0.f : m;
-          float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 1
-          for (int c = 0; c < kKeys; c += 32) {
-            uint32_t raw[32], pk[16];
-            tmem_ld32(tm_s + c, raw);
-            prefill::tmem_ld_wait_tied(raw);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) raw[e] = c + e < left ? __float_as_uint(__uint_as_float(raw[e]) * a) : 0xff800000u;
-            weigh<BF16>(raw, 1.f, m_use, sum, pk);
-            // (P over S: P's columns so far are no more than the scores already in registers)
-            tmem_st16(tm_p + c / 2, pk);
-          }
-          l += sum.x + sum.y;
+          if (lse_row) *lse_row = prefill::row_lse(out_m, out_l);
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bars.p(x));
       }
-      if (ok && nx > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
-        tc_fence_after();
-      }
-      if (!ok) break;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (!ok || !more) break;
       const int64_t row = item.seq.q0 + i;
       uint16_t* dst = valid ? static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1] : nullptr;
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t oa[32], ob[32];
-        if (nx > 0) {
-          tmem_ld32(tm_o + c * 64, oa);
-          tmem_ld32(tm_o + c * 64 + 32, ob);
-          prefill::tmem_ld_wait_tied(oa);
-          prefill::tmem_ld_wait_tied(ob);
-          if (c == D / 64 - 1) {
-            tc_fence_before();
-            mbar_arrive(bars.o_free(x));
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) oa[e] = ob[e] = 0u;
-        }
-        // A thread's row would be written 16 bytes at a time, each of a warp's stores touching 32 rows: through
-        // shared memory (128-byte swizzle) a store writes four rows' 128 bytes.
-        uint8_t* mine = smem + L::kStage + warp * (32 * 128);
-        prefill::stage_slab16<BF16>(oa, inv, mine, lane, 0);
-        prefill::stage_slab16<BF16>(ob, inv, mine, lane, 1);
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int rr = 4 * e + lane / 8;
-          const uint4 v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((lane % 8) ^ (rr & 7)) * 16);
-          uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), rr));
-          if (to) *reinterpret_cast<uint4*>(to + c * 64 + (lane % 8) * 8) = v;
-        }
-        __syncwarp();
+      float* dst_lse = valid && p.lse ? p.lse + row * p.Hq + h : nullptr;
+      if (nx > 0) {
+        pending = true;
+        out_row = dst;
+        lse_row = dst_lse;
+        out_m = m;
+        out_l = l;
+        out_step = steps - 1;
+      } else {  // rows that see no key
+        if (dst)
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+        if (dst_lse) *dst_lse = -INFINITY;
       }
-      if (valid && p.lse) p.lse[row * p.Hq + h] = prefill::row_lse(m, l);
     }
   }
   tc_fence_before();

@@ -65,40 +65,35 @@ __device__ __forceinline__ uint32_t pack(float2 v) {
 }
 
 // 32 accumulator columns of a warp's 32 rows, times f, in 16 bits to global memory; `dst`: where the
-// lane's row goes, or nullptr.  Through 2 KB of shared memory (16-byte pieces q of row r at q ^ (r / 2 % 4)),
-// so that each store writes eight rows' 64 bytes and not 16 bytes of 32 rows.
+// lane's row goes, or nullptr.  Four lanes trade their 16-byte pieces first, so that each store writes
+// eight rows' 64 bytes and not 16 bytes of 32 rows.
 template <bool BF16>
-__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&o)[32], float f, uint8_t* stage) {
-  const int lane = threadIdx.x & 31;
-  __syncwarp();  // the slab before has been read
+__device__ __forceinline__ void store32(uint16_t* dst, const uint32_t (&o)[32], float f) {
+  const int l = threadIdx.x & 3;
+  uint32_t w[4][4];  // [piece][word]; in the end [row of the four][word] of piece l
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w[4];
+  for (int q = 0; q < 4; ++q)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      w[e] = pack<BF16>(make_float2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f));
-    *reinterpret_cast<uint4*>(stage + lane * 64 + (q ^ ((lane >> 1) & 3)) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      w[q][e] = pack<BF16>(make_float2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f));
+#pragma unroll
+  for (int step = 1; step <= 2; ++step) {
+    const bool up = (l & step) != 0;
+#pragma unroll
+    for (int a = 0; a < 2; ++a) {
+      const int lo = step == 1 ? 2 * a : a, hi = lo + step;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? w[lo][e] : w[hi][e], step);
+        if (up) w[lo][e] = got;
+        else w[hi][e] = got;
+      }
+    }
   }
-  __syncwarp();
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const int r = 8 * e + lane / 4, q = lane % 4;
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + (q ^ ((r >> 1) & 3)) * 16);
-    uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
-    if (to) *reinterpret_cast<uint4*>(to + q * 8) = v;
-  }
-}
-
-// The same, each lane its own row's 64 bytes: for a kernel that has no shared memory left.
-template <bool BF16>
-__device__ __forceinline__ void store_row32(uint16_t* dst, const uint32_t (&o)[32], float f) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = pack<BF16>(make_float2(__uint_as_float(o[8 * q + 2 * e]) * f, __uint_as_float(o[8 * q + 2 * e + 1]) * f));
-    reinterpret_cast<uint4*>(dst)[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 4; ++i) {
+    const unsigned long long at = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), i, 4);
+    if (at) reinterpret_cast<uint4*>(at)[l] = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
   }
 }
 
@@ -224,12 +219,13 @@ __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_i
 // ------------------------------------------------------------------------------------------
 template <int D>
 struct DqLayout {
-  static constexpr int kPairs = D == 128 ? 2 : 4;  // ring: pairs of a K and a V tile
+  // K_{j+1} is needed for S while the weights of tile j are computed, when dQ_{j-1}, the last to read
+  // K_{j-1}, has only just been issued: three places.  V_j is given back as soon as dP_j is computed.
+  static constexpr int kKeep = D == 128 ? 3 : 4, kPass = D == 128 ? 2 : 4;
   static constexpr int kTile = kBlock * (D / 64);
-  static constexpr int kQ = 0, kDo = kTile, kRing = 2 * kTile;
-  static constexpr int kStage = kRing + 2 * kPairs * kTile;  // 2 KB for each of the eight warps
-  static constexpr int kBars = kStage + 8 * 2048;
-  static constexpr int kNumBars = 4 * kPairs + 16 + 2 * kItems;
+  static constexpr int kQ = 0, kDo = kTile, kK = 2 * kTile, kV = kK + kKeep * kTile;
+  static constexpr int kBars = kV + kPass * kTile;
+  static constexpr int kNumBars = 2 * kKeep + 2 * kPass + 14 + 2 * kItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;
   static constexpr int kS = D, kDp = D + 2 * kKeys;     // tensor memory: dQ, S[2], dP
   static_assert(kAlloc <= 232448 && kDp + kKeys <= 512, "memory budgets");
@@ -240,22 +236,35 @@ struct DqBars {
   using L = DqLayout<D>;
   uint32_t at;
   __device__ __forceinline__ uint32_t one(int i) const { return at + 8u * i; }
-  __device__ __forceinline__ uint32_t k_full(int pair) const { return one(pair); }
-  __device__ __forceinline__ uint32_t v_full(int pair) const { return one(L::kPairs + pair); }
-  __device__ __forceinline__ uint32_t k_empty(int pair) const { return one(2 * L::kPairs + pair); }
-  __device__ __forceinline__ uint32_t v_empty(int pair) const { return one(3 * L::kPairs + pair); }
-  __device__ __forceinline__ uint32_t tail() const { return one(4 * L::kPairs); }
-  __device__ __forceinline__ uint32_t q() const { return one(4 * L::kPairs + 1); }
-  __device__ __forceinline__ uint32_t q_free() const { return one(4 * L::kPairs + 2); }
-  __device__ __forceinline__ uint32_t s(int i) const { return one(4 * L::kPairs + 3 + i); }
-  __device__ __forceinline__ uint32_t dp() const { return one(4 * L::kPairs + 5); }
-  __device__ __forceinline__ uint32_t dp_read() const { return one(4 * L::kPairs + 6); }
-  __device__ __forceinline__ uint32_t ds(int i) const { return one(4 * L::kPairs + 7 + i); }
-  __device__ __forceinline__ uint32_t dq(int i) const { return one(4 * L::kPairs + 9 + i); }
-  __device__ __forceinline__ uint32_t o_free() const { return one(4 * L::kPairs + 11); }
-  __device__ __forceinline__ uint32_t done(int i) const { return one(4 * L::kPairs + 12 + i); }
-  __device__ __forceinline__ uint32_t item() const { return one(4 * L::kPairs + 14); }
-  __device__ __forceinline__ uint32_t item_read() const { return one(4 * L::kPairs + 14 + kItems); }
+  static constexpr int kRest = 2 * (L::kKeep + L::kPass);
+  __device__ __forceinline__ uint32_t k_full(int i) const { return one(i); }
+  __device__ __forceinline__ uint32_t k_empty(int i) const { return one(L::kKeep + i); }
+  __device__ __forceinline__ uint32_t v_full(int i) const { return one(2 * L::kKeep + i); }
+  __device__ __forceinline__ uint32_t v_empty(int i) const { return one(2 * L::kKeep + L::kPass + i); }
+  __device__ __forceinline__ uint32_t tail() const { return one(kRest); }
+  __device__ __forceinline__ uint32_t q() const { return one(kRest + 1); }
+  __device__ __forceinline__ uint32_t q_free() const { return one(kRest + 2); }
+  __device__ __forceinline__ uint32_t s(int i) const { return one(kRest + 3 + i); }
+  __device__ __forceinline__ uint32_t dp() const { return one(kRest + 5); }
+  __device__ __forceinline__ uint32_t dp_read() const { return one(kRest + 6); }
+  __device__ __forceinline__ uint32_t ds(int i) const { return one(kRest + 7 + i); }
+  __device__ __forceinline__ uint32_t dq(int i) const { return one(kRest + 9 + i); }
+  __device__ __forceinline__ uint32_t o_free() const { return one(kRest + 11); }
+  __device__ __forceinline__ uint32_t done(int i) const { return one(kRest + 12 + i); }
+  __device__ __forceinline__ uint32_t item() const { return one(kRest + 14); }
+  __device__ __forceinline__ uint32_t item_read() const { return one(kRest + 14 + kItems); }
+};
+
+// A place in a ring, and how often the ring has been gone through before it.
+template <int SLOTS>
+struct Place {
+  int slot = 0, lap = 0;
+  __device__ __forceinline__ Place next() const {
+    Place n;
+    n.slot = slot + 1 == SLOTS ? 0 : slot + 1;
+    n.lap = slot + 1 == SLOTS ? lap + 1 : lap;
+    return n;
+  }
 };
 
 // Key tiles that a query tile sees.
@@ -283,10 +292,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_addr(&tmem_slot), 512);
     tmem_relinquish();
   } else if (threadIdx.x == 8 * 32) {
-    for (int i = 0; i < L::kPairs; ++i) {
+    for (int i = 0; i < L::kKeep; ++i) {
       mbar_init(bars.k_full(i), 1);
-      mbar_init(bars.v_full(i), 1);
       mbar_init(bars.k_empty(i), 1);
+    }
+    for (int i = 0; i < L::kPass; ++i) {
+      mbar_init(bars.v_full(i), 1);
       mbar_init(bars.v_empty(i), 1);
     }
     mbar_init(bars.tail(), 1);
@@ -348,13 +359,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok && clear_at >= 0) {
         // K rows past the sequence's end: dS is 0 there, but 0 times an infinity or NaN is not
-        const int pair = clear_at % L::kPairs;
+        const int slot = clear_at % L::kKeep;
         ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
         ++tails;
-        if (ok) clear_rows<D>(smem + L::kRing + 2 * pair * L::kTile, clear_row, lane, 32);
+        if (ok) clear_rows<D>(smem + L::kK + slot * L::kTile, clear_row, lane, 32);
         fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bars.k_full(pair));
+        if (ok && lane == 0) mbar_arrive(bars.k_full(slot));
         clear_at = -1;
       }
       if (item.at >= 0) {
@@ -385,10 +396,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const bool tail = n * kKeys > item.seq.nk;  // the last K tile reaches past the sequence
         for (int j = 0; j < n; ++j, ++tile) {
-          const int pair = tile % L::kPairs, lap = tile / L::kPairs;
-          const uint32_t to = s_base + L::kRing + 2 * pair * L::kTile;
-          if (lap > 0 && !(ok = mbar_wait(bars.k_empty(pair), (lap - 1) & 1, p.status))) break;
-          uint32_t bar = bars.k_full(pair);
+          const int kp = tile % L::kKeep, vp = tile % L::kPass;
+          if (tile >= L::kKeep && !(ok = mbar_wait(bars.k_empty(kp), (tile / L::kKeep - 1) & 1, p.status))) break;
+          uint32_t bar = bars.k_full(kp);
           if (tail && j == n - 1) {
             bar = bars.tail();
             tail_at = tile;
@@ -396,12 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           mbar_arrive_expect_tx(bar, L::kTile);
           for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(to + kb * kBlock, &tm_k, bar, kb * 64, item.head, item.seq.k0 + j * kKeys);
+            tma_load_3d(s_base + L::kK + kp * L::kTile + kb * kBlock, &tm_k, bar, kb * 64, item.head, item.seq.k0 + j * kKeys);
           k_only = tile;
-          if (lap > 0 && !(ok = mbar_wait(bars.v_empty(pair), (lap - 1) & 1, p.status))) break;
-          mbar_arrive_expect_tx(bars.v_full(pair), L::kTile);
+          if (tile >= L::kPass && !(ok = mbar_wait(bars.v_empty(vp), (tile / L::kPass - 1) & 1, p.status))) break;
+          mbar_arrive_expect_tx(bars.v_full(vp), L::kTile);
           for (int kb = 0; kb < D / 64; ++kb)
-            tma_load_3d(to + L::kTile + kb * kBlock, &tm_v, bars.v_full(pair), kb * 64, item.head, item.seq.k0 + j * kKeys);
+            tma_load_3d(s_base + L::kV + vp * L::kTile + kb * kBlock, &tm_v, bars.v_full(vp), kb * 64, item.head,
+                        item.seq.k0 + j * kKeys);
           k_only = -1;
         }
       }
@@ -410,12 +421,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // copy to its barrier.)
         if (uses > 0) mbar_wait(bars.q(), (uses - 1) & 1, nullptr);
         const int k_end = k_only >= 0 ? tile + 1 : tile;
-        for (int i = max(0, k_end - L::kPairs); i < k_end; ++i) {
+        for (int i = max(0, k_end - L::kKeep); i < k_end; ++i) {
           if (i == tail_at) mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
-          else mbar_wait(bars.k_full(i % L::kPairs), (i / L::kPairs) & 1, nullptr);
+          else mbar_wait(bars.k_full(i % L::kKeep), (i / L::kKeep) & 1, nullptr);
         }
-        for (int i = max(0, tile - L::kPairs); i < tile; ++i)
-          mbar_wait(bars.v_full(i % L::kPairs), (i / L::kPairs) & 1, nullptr);
+        for (int i = max(0, tile - L::kPass); i < tile; ++i)
+          mbar_wait(bars.v_full(i % L::kPass), (i / L::kPass) & 1, nullptr);
       }
     }
   } else if (warp == 9 || warp == 10) {
@@ -426,45 +437,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
       return ok;
     };
-    int pair = 0, lap = 0, step = 0, uses = 0;
+    Place<L::kKeep> kp;
+    int step = 0, uses = 0;
     Item item;
     if (warp == 9) {
       constexpr uint32_t idesc = idesc_f16(BF16, kRows, kKeys, false, false);
       const uint64_t q_desc = sdesc_sw128(s_base + L::kQ, 16, 1024), do_desc = sdesc_sw128(s_base + L::kDo, 16, 1024);
-      const uint64_t ring = sdesc_sw128(s_base + L::kRing, 16, 1024);
+      const uint64_t k_desc = sdesc_sw128(s_base + L::kK, 16, 1024), v_desc = sdesc_sw128(s_base + L::kV, 16, 1024);
+      Place<L::kPass> vp;
       for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
         const int n = uniform(key_tiles(p, item.seq, item.at));
         if (n == 0) continue;
         if (!wait(bars.q(), uses++)) break;
         for (int j = 0; j < n; ++j, ++step) {
-          const uint64_t kd = sdesc_add(ring, 2 * pair * L::kTile);
-          if (!wait(bars.k_full(pair), lap)) break;
+          if (!wait(bars.k_full(kp.slot), kp.lap)) break;
           if (step >= 2 && !wait(bars.dq(step & 1), step / 2 - 1)) break;  // dS_{step-2} read
           tc_fence_after();
           if (elected()) {
-            product_ss<D>(tm + L::kS + (step & 1) * kKeys, q_desc, kd, idesc);
+            product_ss<D>(tm + L::kS + (step & 1) * kKeys, q_desc, sdesc_add(k_desc, kp.slot * L::kTile), idesc);
             tc_commit(bars.s(step & 1));
           }
           __syncwarp();
-          if (!wait(bars.v_full(pair), lap)) break;
+          if (!wait(bars.v_full(vp.slot), vp.lap)) break;
           if (step >= 1 && !wait(bars.dp_read(), step - 1)) break;
           tc_fence_after();
           if (elected()) {
-            product_ss<D>(tm + L::kDp, do_desc, sdesc_add(kd, L::kTile), idesc);
+            product_ss<D>(tm + L::kDp, do_desc, sdesc_add(v_desc, vp.slot * L::kTile), idesc);
             tc_commit(bars.dp());
-            tc_commit(bars.v_empty(pair));
+            tc_commit(bars.v_empty(vp.slot));
             if (j == n - 1) tc_commit(bars.q_free());
           }
           __syncwarp();
-          if (++pair == L::kPairs) {
-            pair = 0;
-            ++lap;
-          }
+          kp = kp.next();
+          vp = vp.next();
         }
       }
     } else {
       constexpr uint32_t idesc = idesc_f16(BF16, kRows, D, false, true);
-      const uint64_t ring = sdesc_sw128(s_base + L::kRing, kBlock, 1024);
+      const uint64_t k_desc = sdesc_sw128(s_base + L::kK, kBlock, 1024);
       for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
         const int n = uniform(key_tiles(p, item.seq, item.at));
         if (n == 0) continue;
@@ -472,19 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (uses > 0 && !wait(bars.o_free(), uses - 1)) break;
         ++uses;
         for (int j = 0; j < n; ++j, ++step) {
-          if (!wait(bars.k_full(pair), lap)) break;
+          if (!wait(bars.k_full(kp.slot), kp.lap)) break;
           if (!wait(bars.ds(step & 1), step / 2)) break;
           tc_fence_after();
           if (elected()) {
-            product_ts(tm, tm + L::kS + (step & 1) * kKeys, kHalf, sdesc_add(ring, 2 * pair * L::kTile), idesc, j == 0);
+            product_ts(tm, tm + L::kS + (step & 1) * kKeys, kHalf, sdesc_add(k_desc, kp.slot * L::kTile), idesc, j == 0);
             tc_commit(bars.dq(step & 1));
-            tc_commit(bars.k_empty(pair));
+            tc_commit(bars.k_empty(kp.slot));
           }
           __syncwarp();
-          if (++pair == L::kPairs) {
-            pair = 0;
-            ++lap;
-          }
+          kp = kp.next();
         }
       }
     }
@@ -502,91 +509,103 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_dp = tmem + L::kDp + w * kHalf + lanes;
     bool ok = true;
     int step = 0;
-    Item item;
-    for (int k = 0; ok && __all_sync(0xffffffffu, next_item(bars.item(), bars.item_read(), items, k, item, p.status)); ++k) {
-      const int n = key_tiles(p, item.seq, item.at);
+    // The item before, whose dQ is still in tensor memory: it is written when the first tile of the next has
+    // been dealt with, so that the wait for its last product, and the stores, have work beside them.
+    bool pending = false;
+    uint16_t* out_row = nullptr;
+    float out_scale = 0.f;
+    int out_step = 0;
+    bool more = true;
+    for (int k = 0; ok && more; ++k) {
+      Item item{};
+      more = __all_sync(0xffffffffu, next_item(bars.item(), bars.item_read(), items, k, item, p.status));
+      const int n = more ? key_tiles(p, item.seq, item.at) : 0;
       const int i = item.at + row_token, h = item.head * p.G + row_head;
-      const bool valid = r < p.G * p.q_per_tile && i < item.seq.nq;
+      const bool valid = more && r < p.G * p.q_per_tile && i < item.seq.nq;
       const int64_t row = item.seq.q0 + i;
       const float2 rd = valid ? __ldg(gp.rows + row * p.Hq + h) : make_float2(-INFINITY, 0.f);
       const float f = !BF16 && valid ? __ldg(gp.powers + row * p.Hq + h) : 1.f;
       // (a row of no query is not looked at by anyone: it may see everything)
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
       const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(f, f), nd2 = make_float2(-rd.y * f, -rd.y * f);
-      for (int j = 0; j < n; ++j, ++step) {
-        const uint32_t tm_s = tmem + L::kS + (step & 1) * kKeys + w * kHalf + lanes;
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.s(step & 1), (step / 2) & 1, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        const int left = key_lim - (j * kKeys + w * kHalf);  // columns that the row sees
-        uint32_t raw[2][32];
-        tmem_ld32(tm_s, raw[0]);
-        tmem_ld32(tm_s + 32, raw[1]);
-        prefill::tmem_ld_wait_tied(raw[0]);
-        prefill::tmem_ld_wait_tied(raw[1]);
-        float2 x[32];
-        const bool whole = __all_sync(0xffffffffu, left >= kHalf);
+      for (int j = 0; j < max(n, 1); ++j) {
+        if (j < n) {
+          const uint32_t tm_s = tmem + L::kS + (step & 1) * kKeys + w * kHalf + lanes;
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.s(step & 1), (step / 2) & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          const int left = key_lim - (j * kKeys + w * kHalf);  // columns that the row sees
+          uint32_t raw[2][32];
+          tmem_ld32(tm_s, raw[0]);
+          tmem_ld32(tm_s + 32, raw[1]);
+          prefill::tmem_ld_wait_tied(raw[0]);
+          prefill::tmem_ld_wait_tied(raw[1]);
+          float2 x[32];
+          const bool whole = __all_sync(0xffffffffu, left >= kHalf);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 t = __ffma2_rn(make_float2(__uint_as_float(raw[c / 16][(2 * c) % 32]),
-                                                  __uint_as_float(raw[c / 16][(2 * c) % 32 + 1])), a2, nl2);
-          x[c] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
-        }
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.dp(), step & 1, p.status));
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t dp[2][32], ds[32];
-        tmem_ld32(tm_dp, dp[0]);
-        prefill::tmem_ld_wait_tied(dp[0]);
-        tmem_ld32(tm_dp + 32, dp[1]);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q == 1) {
-            prefill::tmem_ld_wait_tied(dp[1]);
-            tc_fence_before();
-            mbar_arrive(bars.dp_read());
+          for (int c = 0; c < 32; ++c) {
+            const float2 t = __ffma2_rn(make_float2(__uint_as_float(raw[c / 16][(2 * c) % 32]),
+                                                    __uint_as_float(raw[c / 16][(2 * c) % 32 + 1])), a2, nl2);
+            x[c] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
           }
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.dp(), step & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t dp[2][32], ds[32];
+          tmem_ld32(tm_dp, dp[0]);
+          prefill::tmem_ld_wait_tied(dp[0]);
+          tmem_ld32(tm_dp + 32, dp[1]);
 #pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const float2 t = __ffma2_rn(make_float2(__uint_as_float(dp[q][2 * c]), __uint_as_float(dp[q][2 * c + 1])), f2, nd2);
-            ds[16 * q + c] = pack<BF16>(__fmul2_rn(x[16 * q + c], t));
+          for (int q = 0; q < 2; ++q) {
+            if (q == 1) {
+              prefill::tmem_ld_wait_tied(dp[1]);
+              tc_fence_before();
+              mbar_arrive(bars.dp_read());
+            }
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              const float2 t = __ffma2_rn(make_float2(__uint_as_float(dp[q][2 * c]), __uint_as_float(dp[q][2 * c + 1])), f2, nd2);
+              ds[16 * q + c] = pack<BF16>(__fmul2_rn(x[16 * q + c], t));
+            }
           }
-        }
-        if (!whole) {
-          // what a hidden column holds may be another sequence's, or no number: replaced, not multiplied
+          if (!whole) {
+            // what a hidden column holds may be another sequence's, or no number: replaced, not multiplied
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            ds[c] &= (2 * c < left ? 0xffffu : 0u) | (2 * c + 1 < left ? 0xffff0000u : 0u);
+            for (int c = 0; c < 32; ++c)
+              ds[c] &= (2 * c < left ? 0xffffu : 0u) | (2 * c + 1 < left ? 0xffff0000u : 0u);
+          }
+          tmem_st32(tm_s, ds);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bars.ds(step & 1));
+          ++step;
         }
-        tmem_st32(tm_s, ds);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bars.ds(step & 1));
+        if (j == 0 && pending) {
+          pending = false;
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.dq(out_step & 1), (out_step / 2) & 1, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t o[D / 64][32];
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) tmem_ld32(tmem + lanes + w * (D / 2) + c * 32, o[c]);
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) prefill::tmem_ld_wait_tied(o[c]);
+          tc_fence_before();
+          mbar_arrive(bars.o_free());
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) store32<BF16>(out_row ? out_row + c * 32 : nullptr, o[c], out_scale);
+        }
       }
-      if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.dq((step - 1) & 1), ((step - 1) / 2) & 1, p.status));
-        tc_fence_after();
-      }
-      if (!ok) break;
+      if (!ok || !more) break;
       uint16_t* dst = valid ? static_cast<uint16_t*>(gp.dq) + row * gp.dq_strides[0] + h * gp.dq_strides[1] + w * (D / 2) : nullptr;
-      uint32_t o[D / 64][32];
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        if (n > 0) {
-          tmem_ld32(tmem + lanes + w * (D / 2) + c * 32, o[c]);
-          prefill::tmem_ld_wait_tied(o[c]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[c][e] = 0u;
-        }
-      }
       if (n > 0) {
-        tc_fence_before();
-        mbar_arrive(bars.o_free());
+        pending = true;
+        out_row = dst;
+        out_scale = p.scale / f;
+        out_step = step - 1;
+      } else if (dst) {  // rows that see no key
+        for (int c = 0; c < D / 16; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
       }
-#pragma unroll
-      for (int c = 0; c < D / 64; ++c)
-        store32<BF16>(dst ? dst + c * 32 : nullptr, o[c], p.scale / f, smem + L::kStage + warp * 2048);
     }
   }
   tc_fence_before();
@@ -649,18 +668,6 @@ struct DkvBars {
   __device__ __forceinline__ uint32_t done(int x) const { return one(2 * L::kSlots + 15 + x); }
   __device__ __forceinline__ uint32_t item() const { return one(2 * L::kSlots + 17); }
   __device__ __forceinline__ uint32_t item_read() const { return one(2 * L::kSlots + 17 + kItems); }
-};
-
-// A place in the ring, and how often the ring has been gone through before it.
-template <int SLOTS>
-struct Place {
-  int slot = 0, lap = 0;
-  __device__ __forceinline__ Place next() const {
-    Place n;
-    n.slot = slot + 1 == SLOTS ? 0 : slot + 1;
-    n.lap = slot + 1 == SLOTS ? lap + 1 : lap;
-    return n;
-  }
 };
 
 // First query tile that sees a key of the tile at key0, and how many tiles from there on there are.
@@ -947,6 +954,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < n; ++i, ++step, from -= used) {
         const float4* row_data = reinterpret_cast<const float4*>(smem + L::kRowData) + (step & 1) * 64 + w * 16;
         ok = __all_sync(0xffffffffu, mbar_wait(bars.rows(step & 1), (step / 2) & 1, p.status));
+        // (read before S^T is waited for: beside the products, which take all of shared memory's bandwidth,
+        // these reads cost 250 clocks)
+        float4 nl[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) nl[c] = row_data[c];
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.first(0), step & 1, p.status));
         if (!ok) break;
         tc_fence_after();
@@ -960,11 +972,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t pk[32];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          const float4 nl = row_data[c];
           const float2 t = __ffma2_rn(make_float2(__uint_as_float(raw[c / 8][(4 * c) % 32]),
-                                                  __uint_as_float(raw[c / 8][(4 * c) % 32 + 1])), a2, make_float2(nl.x, nl.y));
+                                                  __uint_as_float(raw[c / 8][(4 * c) % 32 + 1])), a2, make_float2(nl[c].x, nl[c].y));
           const float2 u = __ffma2_rn(make_float2(__uint_as_float(raw[c / 8][(4 * c) % 32 + 2]),
-                                                  __uint_as_float(raw[c / 8][(4 * c) % 32 + 3])), a2, make_float2(nl.z, nl.w));
+                                                  __uint_as_float(raw[c / 8][(4 * c) % 32 + 3])), a2, make_float2(nl[c].z, nl[c].w));
           x[2 * c] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
           x[2 * c + 1] = make_float2(exp2_approx(u.x), exp2_approx(u.y));
         }
@@ -1031,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
         }
-        if (dst) store_row32<BF16>(dst + c * 32, o, back);
+        store32<BF16>(dst ? dst + c * 32 : nullptr, o, back);
       }
     }
   }
