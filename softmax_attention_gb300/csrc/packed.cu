@@ -428,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_token = r / p.G, row_head = r % p.G;
     bool ok = true;
     int steps = 0;  // KV tiles of this query tile so far
-    // The item before, whose output is still in tensor memory: it is written when the first tile of the next
-    // has been dealt with, so that the wait for its last product, and the stores, have work beside them.
+    // The item before, whose output is still in tensor memory: if the first scores of the next are there, they
+    // are dealt with first, so that the wait for its last product, and the stores, have work beside them.
     bool pending = false;
     uint16_t* out_row = nullptr;
     float* lse_row = nullptr;
@@ -446,8 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // a row of no query sees everything, so that it never asks for the slow path
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < max(nx, 1); ++j) {
-        if (j < nx) {
+      for (int j = -1; j < nx; ++j) {
+        if (j >= 0) {
           ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
           if (!ok) break;
           tc_fence_after();
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bars.p(x));
           ++steps;
         }
-        if (j == 0 && pending) {
+        if (pending && (j == 0 || nx == 0 || !__all_sync(0xffffffffu, mbar_test_wait(bars.s(x), steps & 1)))) {
           pending = false;
           ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), out_step & 1, p.status));
           if (!ok) break;

@@ -509,8 +509,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_dp = tmem + L::kDp + w * kHalf + lanes;
     bool ok = true;
     int step = 0;
-    // The item before, whose dQ is still in tensor memory: it is written when the first tile of the next has
-    // been dealt with, so that the wait for its last product, and the stores, have work beside them.
+    // The item before, whose dQ is still in tensor memory: if the first scores of the next are there, they are
+    // dealt with first, so that the wait for its last product, and the stores, have work beside them.
     bool pending = false;
     uint16_t* out_row = nullptr;
     float out_scale = 0.f;
@@ -528,8 +528,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // (a row of no query is not looked at by anyone: it may see everything)
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
       const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(f, f), nd2 = make_float2(-rd.y * f, -rd.y * f);
-      for (int j = 0; j < max(n, 1); ++j) {
-        if (j < n) {
+      for (int j = -1; j < n; ++j) {
+        if (j >= 0) {
           const uint32_t tm_s = tmem + L::kS + (step & 1) * kKeys + w * kHalf + lanes;
           ok = __all_sync(0xffffffffu, mbar_wait(bars.s(step & 1), (step / 2) & 1, p.status));
           if (!ok) break;
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(bars.ds(step & 1));
           ++step;
         }
-        if (j == 0 && pending) {
+        if (pending && (j == 0 || n == 0 || !__all_sync(0xffffffffu, mbar_test_wait(bars.s(step & 1), (step / 2) & 1)))) {
           pending = false;
           ok = __all_sync(0xffffffffu, mbar_wait(bars.dq(out_step & 1), (out_step / 2) & 1, p.status));
           if (!ok) break;
