@@ -80,67 +80,71 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // Forward.  LANES: lanes of a row, the least power of two that holds its units.
 template <typename T, int LANES, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 3) norm_rotary_kernel(const NormParams p) {
+__global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormParams p) {
   __shared__ int64_t steps[kMaxRot / 2];
   __shared__ float4 weights[2][kMaxD / 4];
   fill_weights<T, INTERLEAVED>(p, 0, weights[0]);
   fill_weights<T, INTERLEAVED>(p, 1, weights[1]);
   fill_steps(steps, p.inv_freq, p.half);
-  const int64_t slot = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / LANES;
-  const int u = threadIdx.x % LANES;
-  const int group = static_cast<int>(slot / p.tokens);
-  // every lane of a warp takes part in the shuffles, with nothing to load where it has no unit
-  const bool live = group < p.groups[0] + p.groups[1] && u < p.units;
-  const int64_t token = live ? slot - group * p.tokens : 0;
-  const int which = group < p.groups[0] ? 0 : 1;
-  const int h0 = (which ? group - p.groups[0] : group) * p.heads_per_thread;
-  const int h1 = live ? min(h0 + p.heads_per_thread, which ? p.H[1] : p.H[0]) : 0;
-  const int64_t b = token / p.T, t = token - b * p.T;
-  const bool rotated = u < p.rot_units;
-  Turn turn;
-  if (live && rotated) fill_turn(turn, steps, u, p.positions[token], p.amplitude, false);
+  constexpr int kSlots = kThreads / LANES;
+  const int u = threadIdx.x % LANES, slot = threadIdx.x / LANES;
+  const bool unit = u < p.units, rotated = u < p.rot_units;
   const int c0 = rotated && !INTERLEAVED ? 8 * u : 16 * u;
   const int c1 = rotated && !INTERLEAVED ? p.half + 8 * u : 16 * u + 8;
-  const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]);
-  T* y = static_cast<T*>(which ? p.y[1] : p.y[0]);
-  x += which ? b * p.xs[1][0] + t * p.xs[1][2] : b * p.xs[0][0] + t * p.xs[0][2];
-  y += which ? b * p.ys[1][0] + t * p.ys[1][2] : b * p.ys[0][0] + t * p.ys[0][2];
-  const int64_t xh = which ? p.xs[1][1] : p.xs[0][1], yh = which ? p.ys[1][1] : p.ys[0][1];
   const float inv_d = 1.f / p.D;
+  const int64_t tasks = p.tokens * (p.groups[0] + p.groups[1]), step = static_cast<int64_t>(gridDim.x) * kSlots;
   constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;  // heads whose loads are issued together
-  for (int j = 0; j < p.heads_per_thread; j += kBatch) {  // the same count for every lane: shuffles
-    Raw8<T> ra[kBatch], rb[kBatch];
+  for (int64_t base = static_cast<int64_t>(blockIdx.x) * kSlots; base < tasks; base += step) {
+    const int64_t task = base + slot;  // the loop's length is the block's: shuffles
+    // every lane of a warp takes part in the shuffles, with nothing to load where it has no unit
+    const bool live = unit && task < tasks;
+    const int group = live ? static_cast<int>(task / p.tokens) : 0;
+    const int64_t token = live ? task - group * p.tokens : 0;
+    const int which = group < p.groups[0] ? 0 : 1;
+    const int h0 = (which ? group - p.groups[0] : group) * p.heads_per_thread;
+    const int h1 = live ? min(h0 + p.heads_per_thread, which ? p.H[1] : p.H[0]) : 0;
+    const int64_t b = token / p.T, t = token - b * p.T;
+    Turn turn;
+    if (live && rotated) fill_turn(turn, steps, u, p.positions[token], p.amplitude, false);
+    const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]);
+    T* y = static_cast<T*>(which ? p.y[1] : p.y[0]);
+    x += which ? b * p.xs[1][0] + t * p.xs[1][2] : b * p.xs[0][0] + t * p.xs[0][2];
+    y += which ? b * p.ys[1][0] + t * p.ys[1][2] : b * p.ys[0][0] + t * p.ys[0][2];
+    const int64_t xh = which ? p.xs[1][1] : p.xs[0][1], yh = which ? p.ys[1][1] : p.ys[0][1];
+    for (int j = 0; j < p.heads_per_thread; j += kBatch) {  // the same count for every lane: shuffles
+      Raw8<T> ra[kBatch], rb[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      if (h0 + j + i >= h1) continue;
-      const T* src = x + (h0 + j + i) * xh;
-      ra[i] = load_raw8<T>(src + c0);
-      rb[i] = load_raw8<T>(src + c1);
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const bool ok = h0 + j + i < h1;
-      float a[8] = {}, c[8] = {};
-      if (ok) {
-        expand8<T>(ra[i], a);
-        expand8<T>(rb[i], c);
+      for (int i = 0; i < kBatch; ++i) {
+        if (h0 + j + i >= h1) continue;
+        const T* src = x + (h0 + j + i) * xh;
+        ra[i] = load_raw8<T>(src + c0);
+        rb[i] = load_raw8<T>(src + c1);
       }
-      float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], fmaf(c[e], c[e], sum));
-      const float r = rsqrtf(row_sum<LANES>(sum) * inv_d + p.eps);
-      if (!ok) continue;
-      float wa[8], wc[8];
-      read_weights(weights[which], p.units, u, wa, wc);
+      for (int i = 0; i < kBatch; ++i) {
+        const bool ok = h0 + j + i < h1;
+        float a[8] = {}, c[8] = {};
+        if (ok) {
+          expand8<T>(ra[i], a);
+          expand8<T>(rb[i], c);
+        }
+        float sum = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] *= r * wa[e];
-        c[e] *= r * wc[e];
+        for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], fmaf(c[e], c[e], sum));
+        const float r = rsqrtf(row_sum<LANES>(sum) * inv_d + p.eps);
+        if (!ok) continue;
+        float wa[8], wc[8];
+        read_weights(weights[which], p.units, u, wa, wc);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          a[e] *= r * wa[e];
+          c[e] *= r * wc[e];
+        }
+        if (rotated) rotate<INTERLEAVED>(turn, a, c);
+        T* dst = y + (h0 + j + i) * yh;
+        store8(dst + c0, a);
+        store8(dst + c1, c);
       }
-      if (rotated) rotate<INTERLEAVED>(turn, a, c);
-      T* dst = y + (h0 + j + i) * yh;
-      store8(dst + c0, a);
-      store8(dst + c1, c);
     }
   }
 }
@@ -380,8 +384,10 @@ cudaError_t launch(const NormParams& p, bool interleaved, bool grad, cudaStream_
     else norm_rotary_grad_kernel<T, LANES, false><<<n, kThreads, 0, st>>>(p);
     if (p.dw[0] || p.dw[1]) weight_sum_kernel<<<dim3((p.D + 31) / 32, 2), kSumThreads, 0, st>>>(p);
   } else {
-    const int64_t threads = p.tokens * (p.groups[0] + p.groups[1]) * LANES;
-    const unsigned n = static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+    // no more blocks than are resident at once: each fills its tables once
+    const int64_t threads = p.tokens * (p.groups[0] + p.groups[1]) * LANES, most = 2LL * sms();
+    const int64_t want = (threads + kThreads - 1) / kThreads;
+    const unsigned n = static_cast<unsigned>(want < most ? want : most);
     if (interleaved) norm_rotary_kernel<T, LANES, true><<<n, kThreads, 0, st>>>(p);
     else norm_rotary_kernel<T, LANES, false><<<n, kThreads, 0, st>>>(p);
   }
