@@ -17,7 +17,7 @@ SOURCES = ["abi.cu", "prefill.cu", "decode.cu", "decode_noalloc.cu", "mla.cu", "
            "norm_rotary.cu", "delta_step.cu"]
 HEADERS = [os.path.join(CSRC, h) for h in ("internal.h", "sm103.cuh", "prefill_common.cuh",
                                             "cache.cuh", "tree.cuh", "packed.cuh",
-                                            "rotary.cuh")] + [
+                                            "rotary.cuh", "dependent.cuh")] + [
     os.path.join(ROOT, "include", "fa.h")]
 
 NVCC = os.environ.get("NVCC", "nvcc")

@@ -14,6 +14,7 @@
 #include <string.h>
 
 #include "../../include/fa.h"
+#include "dependent.cuh"
 #include "internal.h"
 #include "rotary.cuh"
 #include "sm103.cuh"
@@ -154,6 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormPara
 // order, and weight_sum_kernel the blocks': no atomics.
 template <typename T, int LANES, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const NormParams p) {
+  let_next_start();
   __shared__ int64_t steps[kMaxRot / 2];
   __shared__ float4 weights[kMaxD / 4];
   constexpr int kSlots = kThreads / LANES;
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const Nor
 
 // The blocks' parts of the weights' gradients: block = (32 columns, tensor), eight threads a column.
 __global__ void __launch_bounds__(kSumThreads) weight_sum_kernel(const NormParams p) {
+  wait_for_previous();
   __shared__ float part[8][32];
   const int which = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x % 32, k = threadIdx.x / 32;
   const int n = which ? p.blocks[1] : p.blocks[0];
@@ -382,7 +385,9 @@ cudaError_t launch(const NormParams& p, bool interleaved, bool grad, cudaStream_
     const unsigned n = p.blocks[0] + p.blocks[1];
     if (interleaved) norm_rotary_grad_kernel<T, LANES, true><<<n, kThreads, 0, st>>>(p);
     else norm_rotary_grad_kernel<T, LANES, false><<<n, kThreads, 0, st>>>(p);
-    if (p.dw[0] || p.dw[1]) weight_sum_kernel<<<dim3((p.D + 31) / 32, 2), kSumThreads, 0, st>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || !(p.dw[0] || p.dw[1])) return e;
+    return launch_dependent(weight_sum_kernel, (p.D + 31) / 32, 2, kSumThreads, 0, st, p);
   } else {
     // no more blocks than are resident at once: each fills its tables once
     const int64_t threads = p.tokens * (p.groups[0] + p.groups[1]) * LANES, most = 2LL * sms();

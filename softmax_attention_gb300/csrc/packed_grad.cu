@@ -27,6 +27,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "dependent.cuh"
 #include "internal.h"
 #include "packed.cuh"
 
@@ -47,8 +48,9 @@ struct GradParams {
   void* dk;
   void* dv;
   int64_t dq_strides[2], dk_strides[2], dv_strides[2];
-  float2* rows;          // [total_q, Hq]: -lse log2 e (-inf where nothing is seen), delta
-  float* powers;         // fp16, [total_q, Hq]: f of the row
+  // A query tile's rows side by side: [Hkv, total_q, G]
+  float2* rows;          // -lse log2 e (-inf where nothing is seen), delta
+  float* powers;         // fp16: f of the row
   uint32_t* dout_max;    // fp16: bits of the largest |dout|
 };
 
@@ -135,20 +137,24 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
   const Params& p = g.f;
+  let_next_start();
   // rows in front of the first sequence and behind the last take no part
-  const int64_t from = max(0, __ldg(p.cu_q)) * static_cast<int64_t>(p.Hq);
-  const int64_t to = min(p.total_q, __ldg(p.cu_q + p.B)) * static_cast<int64_t>(p.Hq);
+  const int from = max(0, __ldg(p.cu_q)), to = min(p.total_q, __ldg(p.cu_q + p.B));
   const int lane = threadIdx.x % kLanes;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kPerPass * kRowBatch + threadIdx.x / kLanes;
+  const int64_t per_head = static_cast<int64_t>(p.total_q) * p.G;  // rows of a kv head
   uint4 a[kRowBatch], c[kRowBatch];
+  int token[kRowBatch], head[kRowBatch];
 #pragma unroll
   for (int i = 0; i < kRowBatch; ++i) {
-    const int64_t row = row0 + i * kPerPass;
+    const int64_t row = row0 + i * kPerPass, hk = row / per_head, rest = row - hk * per_head;
+    token[i] = static_cast<int>(rest / p.G);
+    head[i] = static_cast<int>(hk * p.G + rest % p.G);
     a[i] = c[i] = make_uint4(0, 0, 0, 0);
-    if (row < from || row >= to) continue;
-    const int64_t token = row / p.Hq, h = row - token * p.Hq;
-    a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + token * g.dout_strides[0] + h * g.dout_strides[1]) + lane);
-    c[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.o) + token * g.o_strides[0] + h * g.o_strides[1]) + lane);
+    if (hk >= p.Hkv || token[i] < from || token[i] >= to) token[i] = -1;
+    if (token[i] < 0) continue;
+    a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + token[i] * g.dout_strides[0] + head[i] * g.dout_strides[1]) + lane);
+    c[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.o) + token[i] * g.o_strides[0] + head[i] * g.o_strides[1]) + lane);
   }
   float most = 0.f;
 #pragma unroll
@@ -175,8 +181,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
       if constexpr (!BF16) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     }
     most = fmaxf(most, top);
-    if (lane == 0 && row >= from && row < to) {
-      const float lse = __ldg(g.lse + row);
+    if (lane == 0 && token[i] >= 0) {
+      const float lse = __ldg(g.lse + static_cast<int64_t>(token[i]) * p.Hq + head[i]);
       g.rows[row] = make_float2(lse == -INFINITY ? -INFINITY : -lse * prefill::kLog2e, delta);
       if constexpr (!BF16) g.powers[row] = power_for(top);
     }
@@ -507,6 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const float2 a2 = make_float2(p.scale_log2, p.scale_log2);
     const uint32_t tm_dp = tmem + L::kDp + w * kHalf + lanes;
+    wait_for_previous();  // row_kernel
+    if (threadIdx.x == 0) let_next_start();
     bool ok = true;
     int step = 0;
     // The item before, whose dQ is still in tensor memory: if the first scores of the next are there, they are
@@ -523,8 +531,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int i = item.at + row_token, h = item.head * p.G + row_head;
       const bool valid = more && r < p.G * p.q_per_tile && i < item.seq.nq;
       const int64_t row = item.seq.q0 + i;
-      const float2 rd = valid ? __ldg(gp.rows + row * p.Hq + h) : make_float2(-INFINITY, 0.f);
-      const float f = !BF16 && valid ? __ldg(gp.powers + row * p.Hq + h) : 1.f;
+      const int64_t at = (item.head * static_cast<int64_t>(p.total_q) + row) * p.G + row_head;
+      const float2 rd = valid ? gp.rows[at] : make_float2(-INFINITY, 0.f);
+      const float f = !BF16 && valid ? gp.powers[at] : 1.f;
       // (a row of no query is not looked at by anyone: it may see everything)
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
       const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(f, f), nd2 = make_float2(-rd.y * f, -rd.y * f);
@@ -836,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     float f = kUnpower;
-    if constexpr (!BF16) f *= power_for(__uint_as_float(__ldcg(gp.dout_max)));
+    if constexpr (!BF16) f *= power_for(__uint_as_float(*gp.dout_max));
     int step = 0, tails = 0;
     Item item = find(0);
     publish(0, item);
@@ -848,14 +857,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int last_rows = n > 0 ? (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G : used;
       for (int i = 0; ok && i < n; ++i, ++step) {
         const int q0 = (first_tile + i) * p.q_per_tile;
+        const int live = min(used, (item.seq.nq - q0) * p.G);  // rows of the tile that are a query's
+        const float2* src = gp.rows + (item.head * static_cast<int64_t>(p.total_q) + item.seq.q0 + q0) * p.G + lane * 4;
         float nl[4], nd[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int r = lane * 4 + e, token = q0 + r / p.G;
           nl[e] = -INFINITY;  // no query: P = 0
           nd[e] = 0.f;
-          if (r < used && token < item.seq.nq) {
-            const float2 rd = __ldg(gp.rows + static_cast<int64_t>(item.seq.q0 + token) * p.Hq + item.head * p.G + r % p.G);
+          if (lane * 4 + e < live) {
+            const float2 rd = src[e];
             nl[e] = rd.x + kPower;
             nd[e] = -f * rd.y;
           }
@@ -940,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
     const uint32_t tm_p = tmem + L::kP + w * L::kStep + lanes, tm_ds = tmem + L::kDs + w * L::kStep + lanes;
     float f = 1.f;
-    if constexpr (!BF16) f = power_for(__uint_as_float(__ldcg(gp.dout_max)));
+    if constexpr (!BF16) f = power_for(__uint_as_float(*gp.dout_max));
     const float2 a2 = make_float2(p.scale_log2, p.scale_log2), f2 = make_float2(f * kUnpower, f * kUnpower);
     bool ok = true;
     int step = 0;
@@ -1053,6 +1063,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  wait_for_previous();  // nothing of dq_kernel's is read here; but what follows this kernel counts on its end
 }
 
 template <int D, bool BF16>
@@ -1069,10 +1080,14 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
     constexpr int64_t kPer = kRowThreads / (D / 8) * kRowBatch;
     const int64_t rows = static_cast<int64_t>(g.f.total_q) * g.f.Hq;
     row_kernel<D, BF16><<<static_cast<unsigned>((rows + kPer - 1) / kPer), kRowThreads, 0, st>>>(g);
-    kq<<<blocks(q_items), kThreads, DqLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dependent(kq, blocks(q_items), 1, kThreads, DqLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
+    if (e != cudaSuccess) return e;
   }
-  if (k_items > 0) kk<<<blocks(k_items), kThreads, DkvLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
-  return cudaGetLastError();
+  if (k_items == 0) return cudaSuccess;
+  // dkv_kernel reads nothing of dq_kernel's, whose blocks let it start once row_kernel has ended: it takes
+  // each SM as dq_kernel leaves it.  (Without queries there is no kernel before it to wait for.)
+  return launch_dependent(kk, blocks(k_items), 1, kThreads, DkvLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
 }
 
 constexpr size_t kWordBytes = 256;  // in front: the largest |dout|
