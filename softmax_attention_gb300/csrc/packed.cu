@@ -616,6 +616,8 @@ int check_sizes(const char* who, int B, int Hq, int Hkv, int D, int total_q, int
   if (dtype != FA_BF16 && dtype != FA_FP16)
     return fail(FA_ERR_UNSUPPORTED, "%s: dtype must be FA_BF16 or FA_FP16 (got %ld)", who, (long)dtype);
   if (!(scale == scale) || isinf(scale)) return fail(FA_ERR_INVALID_ARG, "%s: scale must be finite", who);
+  if (Hkv > 65535 || static_cast<int64_t>(total_q) * Hq > 2147483647LL - 65536)
+    return fail(FA_ERR_UNSUPPORTED, "%s: Hkv must be <= 65535, and total_q * Hq fit in int32", who);
   const int64_t width = kRows / (Hq / Hkv);
   const int64_t most = most_items(total_q, B, width), keys = most_items(total_k, B, kKeys);
   if ((most > keys ? most : keys) * Hkv > (1LL << 30))

@@ -141,17 +141,17 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
   // rows in front of the first sequence and behind the last take no part
   const int from = max(0, __ldg(p.cu_q)), to = min(p.total_q, __ldg(p.cu_q + p.B));
   const int lane = threadIdx.x % kLanes;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kPerPass * kRowBatch + threadIdx.x / kLanes;
-  const int64_t per_head = static_cast<int64_t>(p.total_q) * p.G;  // rows of a kv head
+  const uint32_t row0 = blockIdx.x * (kPerPass * kRowBatch) + threadIdx.x / kLanes;  // of the kv head's
+  const int hk = blockIdx.y;
   uint4 a[kRowBatch], c[kRowBatch];
   int token[kRowBatch], head[kRowBatch];
 #pragma unroll
   for (int i = 0; i < kRowBatch; ++i) {
-    const int64_t row = row0 + i * kPerPass, hk = row / per_head, rest = row - hk * per_head;
-    token[i] = static_cast<int>(rest / p.G);
-    head[i] = static_cast<int>(hk * p.G + rest % p.G);
+    const uint32_t row = row0 + i * kPerPass;
+    token[i] = static_cast<int>(row / static_cast<uint32_t>(p.G));
+    head[i] = hk * p.G + static_cast<int>(row - token[i] * p.G);
     a[i] = c[i] = make_uint4(0, 0, 0, 0);
-    if (hk >= p.Hkv || token[i] < from || token[i] >= to) token[i] = -1;
+    if (token[i] < from || token[i] >= to) token[i] = -1;
     if (token[i] < 0) continue;
     a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + token[i] * g.dout_strides[0] + head[i] * g.dout_strides[1]) + lane);
     c[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.o) + token[i] * g.o_strides[0] + head[i] * g.o_strides[1]) + lane);
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
   float most = 0.f;
 #pragma unroll
   for (int i = 0; i < kRowBatch; ++i) {
-    const int64_t row = row0 + i * kPerPass;
+    const int64_t row = static_cast<int64_t>(hk) * p.total_q * p.G + row0 + i * kPerPass;
     const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wc[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
     float delta = 0.f, top = 0.f;
 #pragma unroll
@@ -1078,8 +1078,8 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   auto blocks = [&](int64_t items) { return static_cast<unsigned>(items * g.f.Hkv < sms ? items * g.f.Hkv : sms); };
   if (q_items > 0) {
     constexpr int64_t kPer = kRowThreads / (D / 8) * kRowBatch;
-    const int64_t rows = static_cast<int64_t>(g.f.total_q) * g.f.Hq;
-    row_kernel<D, BF16><<<static_cast<unsigned>((rows + kPer - 1) / kPer), kRowThreads, 0, st>>>(g);
+    const int64_t rows = static_cast<int64_t>(g.f.total_q) * g.f.G;
+    row_kernel<D, BF16><<<dim3(static_cast<unsigned>((rows + kPer - 1) / kPer), g.f.Hkv), kRowThreads, 0, st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = launch_dependent(kq, blocks(q_items), 1, kThreads, DqLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
     if (e != cudaSuccess) return e;
