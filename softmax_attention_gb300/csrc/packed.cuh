@@ -163,6 +163,13 @@ struct Item {
 // product, beside softmax warps that leave an issuing warp few slots.
 __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
+// Waits of a whole warp for two barriers.  A look at a barrier takes some 150 clocks even when it has come
+// true: both looks are on their way together.
+__device__ __forceinline__ bool warp_wait(uint32_t a, int phase_a, uint32_t b, int phase_b, uint32_t* status) {
+  const bool first = mbar_test_wait(a, phase_a & 1), second = mbar_test_wait(b, phase_b & 1);
+  return __all_sync(0xffffffffu, (first || mbar_wait(a, phase_a & 1, status)) && (second || mbar_wait(b, phase_b & 1, status)));
+}
+
 // True in one lane of the warp, always the same.  (An election, not a lane's number: the compiler then
 // keeps the code behind it on uniform registers.)
 __device__ __forceinline__ bool elected() {

@@ -15,8 +15,7 @@
 //     left operands of the second pair: neither ever passes through shared memory.
 // S and dP are computed in both, seven products for the five of a form that adds dq by atomics.
 //
-// Eight warps do the element-wise work, two a row, 64 columns each; P and dS, packed to 16 bits, are
-// written over the half of S or dP that the warp itself has read.  Blocks stay for all of their work
+// Eight warps do the element-wise work, two a row, 64 columns each.  Blocks stay for all of their work
 // items, and the products are issued by whole warps from uniform registers, as in packed.cu.
 //
 // fp16: dS is held times a power of two, f, so that the small values that gradients have keep their
@@ -220,8 +219,9 @@ __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_i
 // ------------------------------------------------------------------------------------------
 // dq.  Warps: 0-3 columns 0..63 of S, 4-7 columns 64..127, 8 copies, 9 issues S and dP (and owns tensor
 // memory), 10 issues dS K, 11 finds the work items and clears what a last K tile holds past its
-// sequence's end.  S is double-buffered: S_{j+1} is computed while the weights of tile j are; dS_j is
-// written over S_j.  dP has one buffer, given back as soon as it is in registers.
+// sequence's end.  S and dP are given back as soon as they are in registers, so that S_{j+1} and
+// dP_{j+1} are computed while the weights of tile j are; dS has two buffers of its own.  (With dS_j written
+// over one of two S buffers S_{j+1} had to wait for dQ_{j-1}.)
 // ------------------------------------------------------------------------------------------
 template <int D>
 struct DqLayout {
@@ -233,8 +233,8 @@ struct DqLayout {
   static constexpr int kBars = kV + kPass * kTile;
   static constexpr int kNumBars = 2 * kKeep + 2 * kPass + 14 + 2 * kItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;
-  static constexpr int kS = D, kDp = D + 2 * kKeys;     // tensor memory: dQ, S[2], dP
-  static_assert(kAlloc <= 232448 && kDp + kKeys <= 512, "memory budgets");
+  static constexpr int kS = D, kDp = D + kKeys, kDs = D + 2 * kKeys;  // tensor memory: dQ, S, dP, dS[2]
+  static_assert(kAlloc <= 232448 && kDs + kKeys <= 512, "memory budgets");
 };
 
 template <int D>
@@ -250,7 +250,8 @@ struct DqBars {
   __device__ __forceinline__ uint32_t tail() const { return one(kRest); }
   __device__ __forceinline__ uint32_t q() const { return one(kRest + 1); }
   __device__ __forceinline__ uint32_t q_free() const { return one(kRest + 2); }
-  __device__ __forceinline__ uint32_t s(int i) const { return one(kRest + 3 + i); }
+  __device__ __forceinline__ uint32_t s() const { return one(kRest + 3); }
+  __device__ __forceinline__ uint32_t s_read() const { return one(kRest + 4); }
   __device__ __forceinline__ uint32_t dp() const { return one(kRest + 5); }
   __device__ __forceinline__ uint32_t dp_read() const { return one(kRest + 6); }
   __device__ __forceinline__ uint32_t ds(int i) const { return one(kRest + 7 + i); }
@@ -309,11 +310,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bars.tail(), 1);
     mbar_init(bars.q(), 1);
     mbar_init(bars.q_free(), 1);
+    mbar_init(bars.s(), 1);
+    mbar_init(bars.s_read(), 256);
     mbar_init(bars.dp(), 1);
     mbar_init(bars.dp_read(), 256);
     mbar_init(bars.o_free(), 256);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bars.s(i), 1);
       mbar_init(bars.ds(i), 256);
       mbar_init(bars.dq(i), 1);
       mbar_init(bars.done(i), 1);
@@ -456,16 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n == 0) continue;
         if (!wait(bars.q(), uses++)) break;
         for (int j = 0; j < n; ++j, ++step) {
-          if (!wait(bars.k_full(kp.slot), kp.lap)) break;
-          if (step >= 2 && !wait(bars.dq(step & 1), step / 2 - 1)) break;  // dS_{step-2} read
+          ok = step == 0 ? wait(bars.k_full(kp.slot), kp.lap)
+                         : warp_wait(bars.k_full(kp.slot), kp.lap, bars.s_read(), step - 1, p.status);
+          if (!ok) break;
           tc_fence_after();
           if (elected()) {
-            product_ss<D>(tm + L::kS + (step & 1) * kKeys, q_desc, sdesc_add(k_desc, kp.slot * L::kTile), idesc);
-            tc_commit(bars.s(step & 1));
+            product_ss<D>(tm + L::kS, q_desc, sdesc_add(k_desc, kp.slot * L::kTile), idesc);
+            tc_commit(bars.s());
           }
           __syncwarp();
-          if (!wait(bars.v_full(vp.slot), vp.lap)) break;
-          if (step >= 1 && !wait(bars.dp_read(), step - 1)) break;
+          ok = step == 0 ? wait(bars.v_full(vp.slot), vp.lap)
+                         : warp_wait(bars.v_full(vp.slot), vp.lap, bars.dp_read(), step - 1, p.status);
+          if (!ok) break;
           tc_fence_after();
           if (elected()) {
             product_ss<D>(tm + L::kDp, do_desc, sdesc_add(v_desc, vp.slot * L::kTile), idesc);
@@ -488,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (uses > 0 && !wait(bars.o_free(), uses - 1)) break;
         ++uses;
         for (int j = 0; j < n; ++j, ++step) {
-          if (!wait(bars.k_full(kp.slot), kp.lap)) break;
-          if (!wait(bars.ds(step & 1), step / 2)) break;
+          ok = warp_wait(bars.k_full(kp.slot), kp.lap, bars.ds(step & 1), step / 2, p.status);
+          if (!ok) break;
           tc_fence_after();
           if (elected()) {
-            product_ts(tm, tm + L::kS + (step & 1) * kKeys, kHalf, sdesc_add(k_desc, kp.slot * L::kTile), idesc, j == 0);
+            product_ts(tm, tm + L::kDs + (step & 1) * (kKeys / 2), kHalf / 2, sdesc_add(k_desc, kp.slot * L::kTile), idesc, j == 0);
             tc_commit(bars.dq(step & 1));
             tc_commit(bars.k_empty(kp.slot));
           }
@@ -512,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row_token = r / p.G, row_head = r % p.G;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const float2 a2 = make_float2(p.scale_log2, p.scale_log2);
-    const uint32_t tm_dp = tmem + L::kDp + w * kHalf + lanes;
+    const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
     wait_for_previous();  // row_kernel
     if (threadIdx.x == 0) let_next_start();
     bool ok = true;
@@ -539,8 +543,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(f, f), nd2 = make_float2(-rd.y * f, -rd.y * f);
       for (int j = -1; j < n; ++j) {
         if (j >= 0) {
-          const uint32_t tm_s = tmem + L::kS + (step & 1) * kKeys + w * kHalf + lanes;
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.s(step & 1), (step / 2) & 1, p.status));
+          // S_step; and dS_{step-2} read, before dS_step takes its place
+          ok = step < 2 ? __all_sync(0xffffffffu, mbar_wait(bars.s(), step & 1, p.status))
+                        : warp_wait(bars.dq(step & 1), step / 2 - 1, bars.s(), step, p.status);
           if (!ok) break;
           tc_fence_after();
           const int left = key_lim - (j * kKeys + w * kHalf);  // columns that the row sees
@@ -549,6 +554,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(tm_s + 32, raw[1]);
           prefill::tmem_ld_wait_tied(raw[0]);
           prefill::tmem_ld_wait_tied(raw[1]);
+          tc_fence_before();
+          mbar_arrive(bars.s_read());
           float2 x[32];
           const bool whole = __all_sync(0xffffffffu, left >= kHalf);
 #pragma unroll
@@ -583,13 +590,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c)
               ds[c] &= (2 * c < left ? 0xffffu : 0u) | (2 * c + 1 < left ? 0xffff0000u : 0u);
           }
-          tmem_st32(tm_s, ds);
+          tmem_st32(tmem + L::kDs + (step & 1) * (kKeys / 2) + w * (kHalf / 2) + lanes, ds);
           tmem_st_wait();
           tc_fence_before();
           mbar_arrive(bars.ds(step & 1));
           ++step;
         }
-        if (pending && (j == 0 || n == 0 || !__all_sync(0xffffffffu, mbar_test_wait(bars.s(step & 1), (step / 2) & 1)))) {
+        if (pending && (j == 0 || n == 0 || !__all_sync(0xffffffffu, mbar_test_wait(bars.s(), step & 1)))) {
           pending = false;
           ok = __all_sync(0xffffffffu, mbar_wait(bars.dq(out_step & 1), (out_step / 2) & 1, p.status));
           if (!ok) break;
