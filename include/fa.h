@@ -667,7 +667,8 @@ size_t fa_tree_workspace_size(const fa_tree_args* args);
  *     FA_FP16), each with its strides (token, head; in elements, multiples of 16 bytes and at
  *     least D; the last dimension contiguous); lse [total_q, Hq] fp32 contiguous, or NULL
  *   cu_seqlens_q, cu_seqlens_k [B + 1] int32 (device), not decreasing
- *   D in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 128.
+ *   D in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 128, Hkv <= 65535; total_q * Hq and total_k * Hkv
+ *   below 2^31 - 2^16.  out must not overlap an input.
  * A row that sees no key gets out = 0 and lse = -inf.  Rows of out and lse in front of the first
  * sequence and behind the last are left as they were, and what q, k and v hold there, or in other
  * sequences, takes no part.  (Within a sequence a value of v that is not finite may reach
@@ -699,7 +700,12 @@ int fa_prefill_packed(const fa_packed_args* args, void* stream);
  * the sums over i running over the query heads of the kv head as well.
  *   q, k, v, out, lse, cu_seqlens_*: as in the forward call, out and lse what it returned; dout
  *   [total_q, Hq, D]; dq [total_q, Hq, D], dk, dv [total_k, Hkv, D]; all in dtype, with strides as
- *   above.
+ *   above, the results apart from each other and from the inputs.
+ * dS is rounded to dtype on its way to the products.  FA_FP16: it is held there times a power of two
+ * that brings the largest |dout| (of the row for dq, of all sequences for dk and dv) to [8, 16),
+ * so gradients far below 1 keep their bits; what is 2^-28 of that largest, or less, is lost.
+ * (Within a sequence values of q, k, v or dout that are not finite may reach gradients that they have
+ * no part in, as 0 times them.)
  * Every row of dq, dk and dv that belongs to a sequence is written (zeros where nothing is seen),
  * no other row.  No atomics: the same call gives the same bits.
  * workspace: fa_packed_backward_workspace_size(args) bytes, 256-byte aligned; calls that may

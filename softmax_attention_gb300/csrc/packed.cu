@@ -54,9 +54,9 @@ struct Layout {
   static constexpr int kRing = 2 * kTile;
   static constexpr int kStage = kRing + kSlots * kTile;  // 32 rows x 64 columns of each softmax warp's output
   static constexpr int kBars = kStage + 8 * 32 * 128;
-  // full[slots], empty[slots], tail, q[2], q_free[2], s[2], p[2], pv[2], o_free[2], done[2],
+  // full[slots], empty[slots], tail[slots], q[2], q_free[2], s[2], p[2], pv[2], o_free[2], done[2],
   // item[items], item_read[items]
-  static constexpr int kNumBars = 2 * kSlots + 15 + 2 * kItems;
+  static constexpr int kNumBars = 3 * kSlots + 14 + 2 * kItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;  // room to align the base
   // tensor memory columns
   static constexpr bool kApart = D == 64;             // P beside S
@@ -129,16 +129,17 @@ struct Bars {
   __device__ __forceinline__ uint32_t one(int i) const { return at + 8u * i; }
   __device__ __forceinline__ uint32_t full(int slot) const { return one(slot); }
   __device__ __forceinline__ uint32_t empty(int slot) const { return one(L::kSlots + slot); }
-  __device__ __forceinline__ uint32_t tail() const { return one(2 * L::kSlots); }
-  __device__ __forceinline__ uint32_t q(int x) const { return one(2 * L::kSlots + 1 + x); }
-  __device__ __forceinline__ uint32_t q_free(int x) const { return one(2 * L::kSlots + 3 + x); }
-  __device__ __forceinline__ uint32_t s(int x) const { return one(2 * L::kSlots + 5 + x); }
-  __device__ __forceinline__ uint32_t p(int x) const { return one(2 * L::kSlots + 7 + x); }
-  __device__ __forceinline__ uint32_t pv(int x) const { return one(2 * L::kSlots + 9 + x); }
-  __device__ __forceinline__ uint32_t o_free(int x) const { return one(2 * L::kSlots + 11 + x); }
-  __device__ __forceinline__ uint32_t done(int x) const { return one(2 * L::kSlots + 13 + x); }
-  __device__ __forceinline__ uint32_t item(int i) const { return one(2 * L::kSlots + 15 + i); }
-  __device__ __forceinline__ uint32_t item_read(int i) const { return one(2 * L::kSlots + 15 + kItems + i); }
+  // of a V tile that reaches past its sequence: it lands here, and is full when its last rows are cleared
+  __device__ __forceinline__ uint32_t tail(int slot) const { return one(2 * L::kSlots + slot); }
+  __device__ __forceinline__ uint32_t q(int x) const { return one(3 * L::kSlots + x); }
+  __device__ __forceinline__ uint32_t q_free(int x) const { return one(3 * L::kSlots + 2 + x); }
+  __device__ __forceinline__ uint32_t s(int x) const { return one(3 * L::kSlots + 4 + x); }
+  __device__ __forceinline__ uint32_t p(int x) const { return one(3 * L::kSlots + 6 + x); }
+  __device__ __forceinline__ uint32_t pv(int x) const { return one(3 * L::kSlots + 8 + x); }
+  __device__ __forceinline__ uint32_t o_free(int x) const { return one(3 * L::kSlots + 10 + x); }
+  __device__ __forceinline__ uint32_t done(int x) const { return one(3 * L::kSlots + 12 + x); }
+  __device__ __forceinline__ uint32_t item(int i) const { return one(3 * L::kSlots + 14 + i); }
+  __device__ __forceinline__ uint32_t item_read(int i) const { return one(3 * L::kSlots + 14 + kItems + i); }
 };
 
 // The k-th item, copied from its place in shared memory; false: no more, or a wait ran out.
@@ -300,8 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < L::kSlots; ++s) {
       mbar_init(bars.full(s), 1);
       mbar_init(bars.empty(s), 2);  // both tiles
+      mbar_init(bars.tail(s), 1);
     }
-    mbar_init(bars.tail(), 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(bars.item(i), 1);
       mbar_init(bars.item_read(i), 256 + 3);  // softmax, issuers, copies
@@ -324,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / width;
     };
     const Finder finder(p.B, !p.causal, pieces);
-    int entries = 0, tails = 0;     // ring entries of the items so far; V tiles cleared
+    int entries = 0;                // ring entries of the items so far
+    uint32_t tail_phase = 0;        // of each slot's tail barrier, a bit
     int clear_at = -1, clear_row = 0;  // the item before: entry of its last V tile, first row to clear
     bool ok = true, more = true;
     for (int k = 0; ok && (more || clear_at >= 0); ++k) {
@@ -349,16 +351,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && clear_at >= 0) {
         // Rows past the sequence's end hold another sequence's values, or none: P is 0 there, but 0
         // times an infinity or NaN would spoil O.
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
-        ++tails;
-        uint8_t* v = smem + L::kRing + (clear_at % L::kSlots) * L::kTile;
+        const int slot = clear_at % L::kSlots;
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(slot), (tail_phase >> slot) & 1, p.status));
+        tail_phase ^= 1u << slot;
+        uint8_t* v = smem + L::kRing + slot * L::kTile;
         const int per = (kKeys - clear_row) * 8;
         if (ok)
           for (int i = lane; i < per * (D / 64); i += 32)
             *reinterpret_cast<uint4*>(v + (i / per) * L::kBlock + clear_row * 128 + (i % per) * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bars.full(clear_at % L::kSlots));
+        if (ok && lane == 0) mbar_arrive(bars.full(slot));
         clear_at = -1;
       }
       if (item.at >= 0) {
@@ -375,7 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int entry = 0, q_uses[2] = {0, 0};
-      int tail_at = -1, tails = 0;  // the last entry that lands on the tail's barrier; how many did
+      // a bit for each slot: the phase of its tail barrier; whether its last copy was to that one.  (One for
+      // each slot: the last V of a short item may still be on its way when the next item's is copied.)
+      uint32_t tail_phase = 0, to_tail = 0;
       Item item;
       for (int k = 0; ok && next_item(bars, items, k, item, p.status); ++k) {
         const Tile tile_a = make_tile(p, item.seq, item.at), tile_b = make_tile(p, item.seq, item.at + p.q_per_tile);
@@ -395,11 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < 2 * n; ++i, ++entry) {      // K_0, V_0, K_1, V_1, ...
           const int slot = entry % L::kSlots;
           if (entry >= L::kSlots && !(ok = mbar_wait(bars.empty(slot), (entry / L::kSlots - 1) & 1, p.status))) break;
-          const bool to_tail = tail && i == 2 * n - 1;
-          const uint32_t bar = to_tail ? bars.tail() : bars.full(slot);
-          if (to_tail) {
-            tail_at = entry;
-            ++tails;
+          uint32_t bar = bars.full(slot);
+          to_tail &= ~(1u << slot);
+          if (tail && i == 2 * n - 1) {
+            bar = bars.tail(slot);
+            to_tail |= 1u << slot;
+            tail_phase ^= 1u << slot;
           }
           mbar_arrive_expect_tx(bar, L::kTile);
           for (int kb = 0; kb < D / 64; ++kb)
@@ -412,8 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 2; ++x)
           if (q_uses[x] > 0) mbar_wait(bars.q(x), (q_uses[x] - 1) & 1, nullptr);
         for (int i = max(0, entry - L::kSlots); i < entry; ++i) {
-          if (i == tail_at) mbar_wait(bars.tail(), (tails - 1) & 1, nullptr);
-          else mbar_wait(bars.full(i % L::kSlots), (i / L::kSlots) & 1, nullptr);
+          const int slot = i % L::kSlots;
+          if ((to_tail >> slot) & 1) mbar_wait(bars.tail(slot), ((tail_phase >> slot) & 1) ^ 1, nullptr);
+          else mbar_wait(bars.full(slot), (i / L::kSlots) & 1, nullptr);
         }
       }
     }
@@ -619,8 +626,9 @@ int check_sizes(const char* who, int B, int Hq, int Hkv, int D, int total_q, int
   if (dtype != FA_BF16 && dtype != FA_FP16)
     return fail(FA_ERR_UNSUPPORTED, "%s: dtype must be FA_BF16 or FA_FP16 (got %ld)", who, (long)dtype);
   if (!(scale == scale) || isinf(scale)) return fail(FA_ERR_INVALID_ARG, "%s: scale must be finite", who);
-  if (Hkv > 65535 || static_cast<int64_t>(total_q) * Hq > 2147483647LL - 65536)
-    return fail(FA_ERR_UNSUPPORTED, "%s: Hkv must be <= 65535, and total_q * Hq fit in int32", who);
+  if (Hkv > 65535 || static_cast<int64_t>(total_q) * Hq > 2147483647LL - 65536 ||
+      static_cast<int64_t>(total_k) * Hkv > 2147483647LL - 65536)
+    return fail(FA_ERR_UNSUPPORTED, "%s: Hkv must be <= 65535, total_q * Hq and total_k * Hkv below 2^31 - 2^16", who);
   const int64_t width = kRows / (Hq / Hkv);
   const int64_t most = most_items(total_q, B, width), keys = most_items(total_k, B, kKeys);
   if ((most > keys ? most : keys) * Hkv > (1LL << 30))

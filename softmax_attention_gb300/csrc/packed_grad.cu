@@ -193,7 +193,9 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
 }
 
 // What the blocks of dq_kernel and dkv_kernel have in common: their scheduling warp's work items, and the
-// clearing of rows past a sequence's end that a sum would otherwise run over.
+// clearing of rows past a sequence's end that a sum would otherwise run over.  (The copies that need it
+// land on a barrier of their own, and are full when they are cleared.  One such barrier is enough: the
+// next item's copies wait for the products that read this one's.)
 constexpr int kThreads = 384;
 constexpr int kItems = 4;
 
@@ -652,7 +654,7 @@ struct DkvLayout {
   static constexpr int kK = 0, kV = kTile, kRing = 2 * kTile;
   static constexpr int kRowData = kRing + kSlots * kTile;    // [2][-lse, -delta][128] fp32
   static constexpr int kBars = kRowData + 2 * 2 * kRows * 4;
-  static constexpr int kNumBars = 2 * kSlots + 17 + 2 * kItems;
+  static constexpr int kNumBars = 2 * kSlots + 15 + 2 * kItems;
   static constexpr int kShared = kBars + kNumBars * 8;       // work items, turns, tensor memory's address
   // No room is left to align the base by hand: the kernel has no static shared memory, and its dynamic
   // one is declared with this alignment.
@@ -680,10 +682,9 @@ struct DkvBars {
   __device__ __forceinline__ uint32_t first(int x) const { return one(2 * L::kSlots + 7 + x); }
   __device__ __forceinline__ uint32_t packed(int x) const { return one(2 * L::kSlots + 9 + x); }
   __device__ __forceinline__ uint32_t second(int x) const { return one(2 * L::kSlots + 11 + x); }
-  __device__ __forceinline__ uint32_t out_free(int x) const { return one(2 * L::kSlots + 13 + x); }
-  __device__ __forceinline__ uint32_t done(int x) const { return one(2 * L::kSlots + 15 + x); }
-  __device__ __forceinline__ uint32_t item() const { return one(2 * L::kSlots + 17); }
-  __device__ __forceinline__ uint32_t item_read() const { return one(2 * L::kSlots + 17 + kItems); }
+  __device__ __forceinline__ uint32_t done(int x) const { return one(2 * L::kSlots + 13 + x); }
+  __device__ __forceinline__ uint32_t item() const { return one(2 * L::kSlots + 15); }
+  __device__ __forceinline__ uint32_t item_read() const { return one(2 * L::kSlots + 15 + kItems); }
 };
 
 // First query tile that sees a key of the tile at key0, and how many tiles from there on there are.
@@ -733,8 +734,7 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
       q = q2;
       if (!wait(bars.full(other.slot), other.lap)) break;
       if (i + 1 < n && !wait(bars.full(mine.slot), mine.lap)) break;
-      // the item before has to be read before the first product overwrites it
-      if (i == 0 && uses > 0 && !wait(bars.out_free(X), uses - 1)) break;
+      // (the sums of the item before have been read: the weights of this one's first tile come after that)
       // The other pair's turn first (dV and S^T of a tile before dK and dP^T, these before the next): one
       // pair's products are not to wait behind half of the other's.  Only an order: the wait may give up.
       for (int spin = 0; spin < 4096 && turns[1 - X] < (X ? step + 1 : step); ++spin) {}
@@ -796,7 +796,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars.first(i), 1);
       mbar_init(bars.packed(i), 256);
       mbar_init(bars.second(i), 1);
-      mbar_init(bars.out_free(i), 128);
       mbar_init(bars.done(i), 1);
       turns[i] = 0;
     }
@@ -1051,10 +1050,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) {
           tmem_ld32(tmem + (w ? L::kDk : L::kDv) + lanes + c * 32, o);
           prefill::tmem_ld_wait_tied(o);
-          if (c == D / 32 - 1) {
-            tc_fence_before();
-            mbar_arrive(bars.out_free(w));
-          }
         } else {
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0u;
@@ -1092,8 +1087,12 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
     if (e != cudaSuccess) return e;
   }
   if (k_items == 0) return cudaSuccess;
+  if (q_items == 0) {  // what is ahead of it is not known here
+    kk<<<blocks(k_items), kThreads, DkvLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
+    return cudaGetLastError();
+  }
   // dkv_kernel reads nothing of dq_kernel's, whose blocks let it start once row_kernel has ended: it takes
-  // each SM as dq_kernel leaves it.  (Without queries there is no kernel before it to wait for.)
+  // each SM as dq_kernel leaves it.
   return launch_dependent(kk, blocks(k_items), 1, kThreads, DkvLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
 }
 

@@ -95,6 +95,14 @@ CASES = [
     ([40, 200, 3], [10, 0, 3], 4, 4, 64, HF, True),
     ([1] * 40, None, 4, 1, 64, BF, True),                   # more than a warp of sequences
     ([3, 140, 0] * 50, None, 2, 1, 64, BF, True),           # more than find their place by level
+    # several work items a block, one after another, ragged, with and without tiles that only half
+    # of a pair of query tiles sees
+    ([(37 * i) % 401 for i in range(24)], None, 8, 8, 64, BF, True),
+    ([(53 * i) % 401 for i in range(24)], None, 8, 8, 128, HF, True),
+    ([(61 * i) % 331 for i in range(20)], None, 24, 8, 128, BF, False),
+    ([(71 * i) % 211 for i in range(30)], [(29 * i) % 307 for i in range(30)], 24, 8, 64, HF, True),
+    ([(41 * i) % 211 for i in range(30)], [(83 * i) % 307 for i in range(30)], 24, 8, 128, BF, True),
+    ([200, 1, 77] * 60, None, 4, 2, 128, BF, True),         # and past what find their place by level
 ]
 
 
@@ -325,6 +333,34 @@ def test_no_rows():
     one = cu[:1]
     fa.fa_prefill_packed(kv, kv, kv, one)  # no sequence at all
     torch.cuda.synchronize()
+
+
+def test_long_sequences():
+    """Thousands of tokens: the forward pass against the dense call, the gradients by what holds for
+    any size: dv sums to dout's sum where every row sees a key (weights sum to 1), and <dq, q> and <dk, k>
+    to the same number."""
+    lens = [4100, 1, 2000, 6001]
+    c = Case(lens, 8, 2, 128, BF, seed=21)
+    q, k, v = c.gpu()
+    cu, _ = c.offsets()
+    out, lse = fa.fa_prefill_packed(q, k, v, cu)
+    do = c.do.cuda()
+    dq, dk, dv = fa.fa_prefill_packed_backward(do, q, k, v, out, lse, cu)
+    u = 2.0 ** -8
+    for a, b in zip(c.cu, c.cu[1:]):
+        dense = [x[a:b].transpose(0, 1)[None].contiguous() for x in (q, k, v)]
+        o2, l2 = fa.fa_prefill(*dense, causal=True)
+        # both round weights and results once: u each, of values of at most 1 in the mean
+        torch.testing.assert_close(out[a:b].float(), o2[0].transpose(0, 1).float(), rtol=2 * u, atol=2 * u)
+        torch.testing.assert_close(lse[a:b], l2[0].T, rtol=1e-6, atol=2e-5)
+        n = b - a
+        heads = lambda t: t[a:b].double().view(n, 2, -1, 128).sum((0, 2))  # noqa: E731
+        # n * 4 terms of size about 1, each good to a few u at random: 6 standard deviations
+        off = (dv[a:b].double().sum(0) - heads(do)).abs().max().item()
+        assert off <= 6 * 2 * u * (4 * n) ** 0.5, off
+        x, y = (dq[a:b].double() * q[a:b].double()).sum().item(), (dk[a:b].double() * k[a:b].double()).sum().item()
+        size = (dq[a:b].double() * q[a:b].double()).norm().item() + (dk[a:b].double() * k[a:b].double()).norm().item()
+        assert abs(x - y) <= 6 * 2 * u * size, (x, y, size)
 
 
 def test_large_offsets():
