@@ -1070,32 +1070,73 @@ def fa_tree_decode_paged(q, k_pages, v_pages, page_table, seq_lens, max_seq_len:
 
 # ------------------------------------------------------------------------------------------
 # Packed prompts, forward and backward; norms of queries and keys; the recurrent gated-delta step.
-# As above: strided inputs, the tensors' own device, allocations on the launching stream.
+# As above: strided inputs, the tensors' own device, allocations on the launching stream.  A call of
+# these on a few tokens takes the GPU about as long as Python takes to look at its arguments, so each
+# tensor is looked at once, and what is wrong is found out only where something is.
 # ------------------------------------------------------------------------------------------
-def _norm_fields(dev, q, k, positions, inv_freq, q_weight, k_weight, amplitude, interleaved, eps):
-    """The checked fields that fa_qk_norm_rotary and its backward share."""
-    B, Hq, T, D = q.shape
-    if q.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {q.dtype}")
-    weights = {w.dtype for w in (q_weight, k_weight) if w is not None}
-    if len(weights) > 1 or not weights <= {q.dtype, torch.float32}:
-        raise ValueError(f"the weights must both be {q.dtype} or float32, got {sorted(map(str, weights))}")
-    _need_dtype(q.dtype, k)
-    _need_dtype(torch.int32, positions)
-    _need_dtype(torch.float64, inv_freq)
-    _shape("k", k, B, 0 if k is None else k.shape[1], T, D)
-    _shape("q_weight", q_weight, D)
-    _shape("k_weight", k_weight, D)
-    _shape("positions", positions, B, T)
-    _on(dev, positions, inv_freq, q_weight, k_weight)
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq go together")
-    return (_addr(q_weight), _addr(k_weight), _addr(positions), _addr(inv_freq), B, T, Hq,
-            0 if k is None else k.shape[1], D, 0 if inv_freq is None else 2 * inv_freq.numel(),
-            interleaved, amplitude, eps, _DT[q.dtype], _DT[weights.pop() if weights else q.dtype])
-
-
+_HALF = {torch.bfloat16: FA_BF16, torch.float16: FA_FP16}
 _none3 = (0, 0, 0)
+_empty = torch.empty
+
+
+def _gpu(t):
+    """Device index of a CUDA tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return dev
+
+
+def _flat(dev, dtype, shape, name, t):
+    """Address of a contiguous tensor of this type and shape on the device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _need_dtype(dtype, t)
+        _shape(name, t, *shape)
+        _on(dev, t)
+    return t.data_ptr()
+
+
+def _strided(dev, dtype, shape, name, t):
+    """Strides but the last of a tensor of this type and shape (three or four dimensions) on the
+    device, contiguous in its last dimension; 0 for a dimension of one element, where torch may
+    report anything."""
+    s = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (s[-1] != 1 and shape[-1] > 1):
+        _need_dtype(dtype, t)
+        _shape(name, t, *shape)
+        raise ValueError("tensors must be CUDA tensors on one device with a contiguous last "
+                         "dimension")
+    if len(s) == 3:
+        return (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0)
+    return (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
+
+
+def _norm_fields(dev, shape, Hk, dtype, positions, inv_freq, q_weight, k_weight, amplitude,
+                 interleaved, eps):
+    """The checked fields that fa_qk_norm_rotary and its backward share."""
+    B, Hq, T, D = shape
+    code = _DT.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype}")
+    wq = wk = pos = freq = rot = 0
+    wcode = code
+    weight = k_weight if q_weight is None else q_weight
+    if weight is not None:
+        wtype = weight.dtype
+        wcode = _DT.get(wtype)
+        if wtype is not dtype and wtype is not torch.float32:
+            raise ValueError(f"the weights must be {dtype} or float32, got {wtype}")
+        if q_weight is not None:
+            wq = _flat(dev, wtype, (D,), "q_weight", q_weight)
+        if k_weight is not None:
+            wk = _flat(dev, wtype, (D,), "k_weight", k_weight)
+    if positions is not None and inv_freq is not None:
+        pos = _flat(dev, torch.int32, (B, T), "positions", positions)
+        freq = _flat(dev, torch.float64, inv_freq.shape, "inv_freq", inv_freq)
+        rot = 2 * inv_freq.numel()
+    elif positions is not None or inv_freq is not None:
+        raise ValueError("positions and inv_freq go together")
+    return wq, wk, pos, freq, B, T, Hq, Hk, D, rot, interleaved, amplitude, eps, code, wcode
 
 
 def fa_qk_norm_rotary(q, k, positions, inv_freq, q_weight, k_weight=None, *, eps: float = 1e-6,
@@ -1106,25 +1147,28 @@ def fa_qk_norm_rotary(q, k, positions, inv_freq, q_weight, k_weight=None, *, eps
     fp16 or fp32, any strides with a contiguous last dimension; positions [B,T] int32 and inv_freq
     [rot_dim/2] fp64, or None for both: norms alone.  q_out and k_out may be q and k themselves.
     Returns (q_out, k_out)."""
-    lib = load_library()
-    dev = _cuda_index(q)
-    _need_dtype(q.dtype, q_out, k_out)
-    _shape("q_out", q_out, *q.shape)
+    lib = _lib or load_library()
+    dev, dtype, qs = _gpu(q), q.dtype, q.shape
+    B, _, T, D = qs
+    q_in = _strided(dev, dtype, qs, "q", q)
+    ka, Hk, k_in, k_to = 0, 0, _none3, _none3
     if k is not None:
-        _shape("k_out", k_out, *k.shape)
-    fields = _norm_fields(dev, q, k, positions, inv_freq, q_weight, k_weight, amplitude,
+        Hk = k.shape[1]
+        ks = (B, Hk, T, D)
+        ka, k_in = k.data_ptr(), _strided(dev, dtype, ks, "k", k)
+    fields = _norm_fields(dev, qs, Hk, dtype, positions, inv_freq, q_weight, k_weight, amplitude,
                           interleaved, eps)
     with _scope(dev, stream):
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = _empty(qs, dtype=dtype, device=q.device)
         if k is None:
             k_out = None
-        elif k_out is None:
-            k_out = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        a = _pack_norm(q.data_ptr(), _addr(k), q_out.data_ptr(), _addr(k_out),
-                       *_strides_on(dev, q), *(_none3 if k is None else _strides_on(dev, k)),
-                       *_strides_on(dev, q_out), *(_none3 if k is None else _strides_on(dev, k_out)),
-                       *fields)
+        else:
+            if k_out is None:
+                k_out = _empty(ks, dtype=dtype, device=q.device)
+            k_to = _strided(dev, dtype, ks, "k_out", k_out)
+        a = _pack_norm(q.data_ptr(), ka, q_out.data_ptr(), 0 if k is None else k_out.data_ptr(), *q_in,
+                       *k_in, *_strided(dev, dtype, qs, "q_out", q_out), *k_to, *fields)
         _check(lib.fa_qk_norm_rotary(a, _raw_stream(dev)))
     return q_out, k_out
 
@@ -1135,76 +1179,65 @@ def fa_qk_norm_rotary_backward(dq_out, dk_out, q, k, positions, inv_freq, q_weig
     """Gradient of fa_qk_norm_rotary: of the outputs' gradients dq_out, dk_out and the call's
     inputs.  dq and dk may be dq_out and dk_out, or q and k, themselves.  Returns (dq, dk, dq_weight,
     dk_weight): the last two [D] fp32, None where there is no weight."""
-    lib = load_library()
-    dev = _cuda_index(q)
-    _need_dtype(q.dtype, dq_out, dk_out, dq, dk)
-    _shape("dq_out", dq_out, *q.shape)
-    _shape("dq", dq, *q.shape)
+    lib = _lib or load_library()
+    dev, dtype, qs = _gpu(q), q.dtype, q.shape
+    B, _, T, D = qs
     if (k is None) != (dk_out is None):
         raise ValueError("k and dk_out go together")
+    q_in = _strided(dev, dtype, qs, "q", q)
+    q_back = _strided(dev, dtype, qs, "dq_out", dq_out)
+    ka, ga, Hk, k_in, k_back, k_to = 0, 0, 0, _none3, _none3, _none3
     if k is not None:
-        _shape("dk_out", dk_out, *k.shape)
-        _shape("dk", dk, *k.shape)
-    fields = _norm_fields(dev, q, k, positions, inv_freq, q_weight, k_weight, amplitude,
+        Hk = k.shape[1]
+        ks = (B, Hk, T, D)
+        ka, k_in = k.data_ptr(), _strided(dev, dtype, ks, "k", k)
+        ga, k_back = dk_out.data_ptr(), _strided(dev, dtype, ks, "dk_out", dk_out)
+    fields = _norm_fields(dev, qs, Hk, dtype, positions, inv_freq, q_weight, k_weight, amplitude,
                           interleaved, eps)
-    _on(dev, workspace)
+    if workspace is not None:
+        _on(dev, workspace)
+    device = q.device
     with _scope(dev, stream):
         if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            dq = _empty(qs, dtype=dtype, device=device)
         if k is None:
             dk = None
-        elif dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        new = lambda w: None if w is None else torch.empty(q.shape[3], dtype=torch.float32, device=q.device)
-        dqw, dkw = new(q_weight), new(k_weight)
-        ks = (_none3,) * 3 if k is None else tuple(_strides_on(dev, t) for t in (dk_out, k, dk))
-        fields = (dq_out.data_ptr(), _addr(dk_out), q.data_ptr(), _addr(k), dq.data_ptr(), _addr(dk),
-                  _addr(dqw), _addr(dkw), *_strides_on(dev, dq_out), *ks[0], *_strides_on(dev, q),
-                  *ks[1], *_strides_on(dev, dq), *ks[2], *fields)
-        a = _pack_norm_backward(*fields, 0, 0)
-        need = lib.fa_qk_norm_rotary_backward_workspace_size(a)
-        if need:
-            ws = _workspace(need, q.device, workspace)
-            a = _pack_norm_backward(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
+        else:
+            if dk is None:
+                dk = _empty(ks, dtype=dtype, device=device)
+            k_to = _strided(dev, dtype, ks, "dk", dk)
+        dqw = None if q_weight is None else _empty((D,), dtype=torch.float32, device=device)
+        dkw = None if k_weight is None else _empty((D,), dtype=torch.float32, device=device)
+        fields = (dq_out.data_ptr(), ga, q.data_ptr(), ka, dq.data_ptr(), _addr(dk), _addr(dqw),
+                  _addr(dkw), *q_back, *k_back, *q_in, *k_in, *_strided(dev, dtype, qs, "dq", dq),
+                  *k_to, *fields)
+        need = lib.fa_qk_norm_rotary_backward_workspace_size(_pack_norm_backward(*fields, 0, 0))
+        ws = _workspace(need, device, workspace)
+        a = _pack_norm_backward(*fields, _addr(ws), 0 if ws is None else ws.numel() * ws.element_size())
         _check(lib.fa_qk_norm_rotary_backward(a, _raw_stream(dev)))
     return dq, dk, dqw, dkw
 
 
-def _rows_on(dev, t):
-    """(token, head) strides of a 3-D tensor on `dev` with a contiguous last dimension; 0 for a
-    dimension of one element, where torch may report anything."""
-    s, n = t.stride(), t.shape
-    if t.get_device() != dev or (s[2] != 1 and n[2] > 1):
-        raise ValueError("tensors must be CUDA tensors on one device with a contiguous last "
-                         "dimension")
-    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
-
-
-def _packed_fields(dev, q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale):
+def _packed_fields(dev, dtype, q, k, cu_seqlens_q, cu_seqlens_k, causal, scale):
     """The checked fields that fa_prefill_packed and its backward share."""
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"expected bfloat16 or float16, got {q.dtype}")
-    if q.dim() != 3 or k.dim() != 3:
+    code = _HALF.get(dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16 or float16, got {dtype}")
+    if len(q) != 3 or len(k) != 3:
         raise ValueError("q, k and v must be [tokens, heads, D]")
-    total_q, Hq, D = q.shape
-    total_k, Hkv, _ = k.shape
-    _need_dtype(q.dtype, k, v)
-    _shape("k", k, total_k, Hkv, D)
-    _shape("v", v, total_k, Hkv, D)
-    if cu_seqlens_k is None:
-        cu_seqlens_k = cu_seqlens_q
-        if total_k != total_q:
-            raise ValueError("without cu_seqlens_k the keys are the queries' tokens: "
-                             f"got {total_q} rows of q and {total_k} of k")
-    _need_dtype(torch.int32, cu_seqlens_q, cu_seqlens_k)
-    B = cu_seqlens_q.numel() - 1
-    if B < 0:
-        raise ValueError("cu_seqlens_q must hold one offset at least")
-    _shape("cu_seqlens_q", cu_seqlens_q, B + 1)
-    _shape("cu_seqlens_k", cu_seqlens_k, B + 1)
-    _on(dev, cu_seqlens_q, cu_seqlens_k)
-    return (cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), B, Hq, Hkv, D, total_q, total_k,
-            causal, 1.0 / math.sqrt(D) if scale is None else scale, _DT[q.dtype])
+    total_q, Hq, D = q
+    total_k, Hkv, _ = k
+    n = cu_seqlens_q.shape
+    if len(n) != 1 or n[0] < 1:
+        raise ValueError("cu_seqlens_q must be [B + 1]")
+    at_q = at_k = _flat(dev, torch.int32, n, "cu_seqlens_q", cu_seqlens_q)
+    if cu_seqlens_k is not None:
+        at_k = _flat(dev, torch.int32, n, "cu_seqlens_k", cu_seqlens_k)
+    elif total_k != total_q:
+        raise ValueError("without cu_seqlens_k the keys are the queries' tokens: "
+                         f"got {total_q} rows of q and {total_k} of k")
+    return (at_q, at_k, n[0] - 1, Hq, Hkv, D, total_q, total_k, causal,
+            1.0 / math.sqrt(D) if scale is None else scale, code)
 
 
 def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool = True,
@@ -1215,22 +1248,21 @@ def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool 
     each and the end of the last (cu_seqlens_k None: the same).  causal: a sequence's queries are
     its last positions.  Rows outside the sequences are left as they were.  Returns (out
     [total_q,Hq,D], lse [total_q,Hq] fp32)."""
-    lib = load_library()
-    dev = _cuda_index(q)
-    fields = _packed_fields(dev, q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale)
-    _need_dtype(q.dtype, out)
-    _need_dtype(torch.float32, lse)
-    _shape("out", out, *q.shape)
-    _shape("lse", lse, *q.shape[:2])
-    _on(dev, lse)
+    lib = _lib or load_library()
+    dev, dtype, qs, ks = _gpu(q), q.dtype, q.shape, k.shape
+    fields = _packed_fields(dev, dtype, qs, ks, cu_seqlens_q, cu_seqlens_k, causal, scale)
+    rows = qs[:2]
+    ks = (ks[0], ks[1], qs[2])
+    strides = (*_strided(dev, dtype, qs, "q", q), *_strided(dev, dtype, ks, "k", k),
+               *_strided(dev, dtype, ks, "v", v))
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            out = _empty(qs, dtype=dtype, device=q.device)
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        a = _pack_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                         *_rows_on(dev, q), *_rows_on(dev, k), *_rows_on(dev, v),
-                         *_rows_on(dev, out), *fields)
+            lse = _empty(rows, dtype=torch.float32, device=q.device)
+        a = _pack_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                         _flat(dev, torch.float32, rows, "lse", lse), *strides,
+                         *_strided(dev, dtype, qs, "out", out), *fields)
         _check(lib.fa_prefill_packed(a, _raw_stream(dev)))
     return out, lse
 
@@ -1241,32 +1273,31 @@ def fa_prefill_packed_backward(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens
     """Gradients of fa_prefill_packed's out: dout [total_q,Hq,D], the call's inputs, and the out and
     lse that it returned.  Rows of dq, dk and dv outside the sequences are left as they were.
     Returns (dq [total_q,Hq,D], dk, dv [total_k,Hkv,D])."""
-    lib = load_library()
-    dev = _cuda_index(q)
-    fields = _packed_fields(dev, q, k, v, cu_seqlens_q, cu_seqlens_k, causal, scale)
-    _need_dtype(q.dtype, dout, out, dq, dk, dv)
-    _need_dtype(torch.float32, lse)
-    for name, t in (("dout", dout), ("out", out), ("dq", dq)):
-        _shape(name, t, *q.shape)
-    _shape("dk", dk, *k.shape)
-    _shape("dv", dv, *k.shape)
-    _shape("lse", lse, *q.shape[:2])
-    _on(dev, lse, workspace)
+    lib = _lib or load_library()
+    dev, dtype, qs, ks = _gpu(q), q.dtype, q.shape, k.shape
+    fields = _packed_fields(dev, dtype, qs, ks, cu_seqlens_q, cu_seqlens_k, causal, scale)
+    ks = (ks[0], ks[1], qs[2])
+    strides = (*_strided(dev, dtype, qs, "dout", dout), *_strided(dev, dtype, qs, "q", q),
+               *_strided(dev, dtype, ks, "k", k), *_strided(dev, dtype, ks, "v", v),
+               *_strided(dev, dtype, qs, "out", out))
+    at_lse = _flat(dev, torch.float32, qs[:2], "lse", lse)
+    if workspace is not None:
+        _on(dev, workspace)
+    device = q.device
     with _scope(dev, stream):
         if dq is None:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            dq = _empty(qs, dtype=dtype, device=device)
         if dk is None:
-            dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+            dk = _empty(ks, dtype=dtype, device=device)
         if dv is None:
-            dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-        fields = (dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                  lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                  *(x for t in (dout, q, k, v, out, dq, dk, dv) for x in _rows_on(dev, t)), *fields)
-        a = _pack_packed_backward(*fields, 0, 0)
-        need = lib.fa_packed_backward_workspace_size(a)
-        if need:
-            ws = _workspace(need, q.device, workspace)
-            a = _pack_packed_backward(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
+            dv = _empty(ks, dtype=dtype, device=device)
+        fields = (dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), at_lse,
+                  dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *strides,
+                  *_strided(dev, dtype, qs, "dq", dq), *_strided(dev, dtype, ks, "dk", dk),
+                  *_strided(dev, dtype, ks, "dv", dv), *fields)
+        need = lib.fa_packed_backward_workspace_size(_pack_packed_backward(*fields, 0, 0))
+        ws = _workspace(need, device, workspace)
+        a = _pack_packed_backward(*fields, _addr(ws), 0 if ws is None else ws.numel() * ws.element_size())
         _check(lib.fa_prefill_packed_backward(a, _raw_stream(dev)))
     return dq, dk, dv
 
@@ -1279,34 +1310,32 @@ def gated_delta_step(q, k, v, g, beta, states, *, read_index=None, write_index=N
     Sequence b's state is read from slot read_index[b] (default b) and written to write_index[b]
     (default where it was read); it has new_lens[b] tokens (default T; int32, device, all three).
     Returns out [B,Hv,T,128]."""
-    lib = load_library()
-    dev = _cuda_index(q)
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"expected bfloat16 or float16, got {q.dtype}")
-    B, Hk, T, dk = q.shape
+    lib = _lib or load_library()
+    dev, dtype, qs = _gpu(q), q.dtype, q.shape
+    code = _HALF.get(dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16 or float16, got {dtype}")
+    B, Hk, T, dk = qs
     Hv, dv = v.shape[1], v.shape[3]
-    _need_dtype(q.dtype, k, v, out)
-    _need_dtype(torch.float32, g, beta, states)
-    _need_dtype(torch.int32, read_index, write_index, new_lens)
-    _shape("k", k, B, Hk, T, dk)
-    _shape("v", v, B, Hv, T, dv)
-    _shape("g", g, B, Hv, T)
-    _shape("beta", beta, B, Hv, T)
-    _shape("states", states, states.shape[0], Hv, dv, dk)
-    _shape("out", out, B, Hv, T, dv)
-    for name, t in (("read_index", read_index), ("write_index", write_index), ("new_lens", new_lens)):
-        _shape(name, t, B)
-    _on(dev, states, read_index, write_index, new_lens)
-    if g.get_device() != dev or beta.get_device() != dev:
-        raise ValueError("tensors must be CUDA tensors on one device")
+    vs, gate, n = (B, Hv, T, dv), (B, Hv, T), states.shape[0]
+    for name, t in (("g", g), ("beta", beta)):
+        if t.dtype is not torch.float32 or t.shape != gate or t.get_device() != dev:
+            _need_dtype(torch.float32, t)
+            _shape(name, t, *gate)
+            raise ValueError("tensors must be CUDA tensors on one device")
+    at_states = _flat(dev, torch.float32, (n, Hv, dv, dk), "states", states)
+    i32 = torch.int32
+    read = 0 if read_index is None else _flat(dev, i32, (B,), "read_index", read_index)
+    write = 0 if write_index is None else _flat(dev, i32, (B,), "write_index", write_index)
+    lens = 0 if new_lens is None else _flat(dev, i32, (B,), "new_lens", new_lens)
+    strides = (*_strided(dev, dtype, qs, "q", q), *_strided(dev, dtype, qs, "k", k),
+               *_strided(dev, dtype, vs, "v", v), *g.stride(), *beta.stride())
     with _scope(dev, stream):
         if out is None:
-            out = torch.empty((B, Hv, T, dv), dtype=q.dtype, device=q.device)
+            out = _empty(vs, dtype=dtype, device=q.device)
         a = _pack_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), beta.data_ptr(),
-                       states.data_ptr(), _addr(read_index), _addr(write_index), _addr(new_lens),
-                       out.data_ptr(), *_strides_on(dev, q), *_strides_on(dev, k),
-                       *_strides_on(dev, v), *g.stride(), *beta.stride(), *_strides_on(dev, out), B,
-                       T, Hk, Hv, dk, dv, states.shape[0],
-                       1.0 / math.sqrt(dk) if scale is None else scale, _DT[q.dtype])
+                       at_states, read, write, lens, out.data_ptr(), *strides,
+                       *_strided(dev, dtype, vs, "out", out), B, T, Hk, Hv, dk, dv, n,
+                       1.0 / math.sqrt(dk) if scale is None else scale, code)
         _check(lib.gated_delta_step(a, _raw_stream(dev)))
     return out
