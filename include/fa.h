@@ -674,7 +674,12 @@ size_t fa_tree_workspace_size(const fa_tree_args* args);
  * sequences, takes no part.  (Within a sequence a value of v that is not finite may reach
  * rows that do not see it, as 0 times it.)
  * Sequences whose offsets decrease or reach out of the tensor set FA_ERR_BOUNDS in the device
- * status word and are taken as empty.  No workspace; one launch.
+ * status word and are taken as empty.
+ * num_splits: parts that each sequence's keys are split into, 0 (the library's choice: more than one
+ * where few query tiles meet long sequences) or 1 to 32; the parts are joined by a second
+ * kernel.
+ * workspace: fa_packed_workspace_size(args) bytes, 256-byte aligned (none when that is 0); calls that
+ * may overlap on the GPU need one each.
  */
 typedef struct fa_packed_args {
   const void* q;
@@ -689,9 +694,15 @@ typedef struct fa_packed_args {
   int causal;
   float scale;
   fa_dtype dtype;
+  int num_splits;
+  void* workspace;
+  size_t workspace_bytes;
 } fa_packed_args;
 
 int fa_prefill_packed(const fa_packed_args* args, void* stream);
+
+/* Workspace bytes of a call with these sizes on the current device (pointers are not read). */
+size_t fa_packed_workspace_size(const fa_packed_args* args);
 
 /*
  * The gradients of fa_prefill_packed's out (lse is taken as having none).  With P the softmax

@@ -54,7 +54,8 @@ EXPORTS = (
     "fa_rotary", "fa_rotary_frequencies", "fa_cache_append", "fa_cache_gather",
     "fa_tree_decode_paged", "fa_tree_workspace_size", "fa_tree_mask",
     "fa_qk_norm_rotary", "fa_qk_norm_rotary_backward", "fa_qk_norm_rotary_backward_workspace_size",
-    "fa_prefill_packed", "fa_prefill_packed_backward", "fa_packed_backward_workspace_size",
+    "fa_prefill_packed", "fa_packed_workspace_size",
+    "fa_prefill_packed_backward", "fa_packed_backward_workspace_size",
     "gated_delta_step",
 )
 
@@ -230,7 +231,8 @@ class PackedArgs(ctypes.Structure):
         ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("q_strides", _Strides2), ("k_strides", _Strides2), ("v_strides", _Strides2),
         ("out_strides", _Strides2),
-    ] + _PACKED_FIELDS
+    ] + _PACKED_FIELDS + [("num_splits", ctypes.c_int), ("workspace", ctypes.c_void_p),
+                          ("workspace_bytes", ctypes.c_size_t)]
 
 
 class PackedBackwardArgs(ctypes.Structure):
@@ -342,7 +344,7 @@ def load_library(path: str | None = None):
                      "fa_prefill_packed_backward", "gated_delta_step"):
             getattr(lib, name).restype = _i
             getattr(lib, name).argtypes = [_vp, _vp]
-        for name in ("fa_qk_norm_rotary_backward_workspace_size",
+        for name in ("fa_qk_norm_rotary_backward_workspace_size", "fa_packed_workspace_size",
                      "fa_packed_backward_workspace_size"):
             getattr(lib, name).restype = _sz
             getattr(lib, name).argtypes = [_vp]
@@ -1241,13 +1243,15 @@ def _packed_fields(dev, dtype, q, k, cu_seqlens_q, cu_seqlens_k, causal, scale):
 
 
 def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool = True,
-                      scale: float | None = None, out=None, lse=None, stream=None):
+                      scale: float | None = None, num_splits: int = 0, out=None, lse=None,
+                      workspace=None, stream=None):
     """Attention over packed prompts: q [total_q,Hq,D], k, v [total_k,Hkv,D] bf16 or fp16 (any
     token and head strides with a contiguous last dimension, as slices of one projection), the
     sequences behind one another; cu_seqlens_q, cu_seqlens_k [B+1] int32 (device): first row of
     each and the end of the last (cu_seqlens_k None: the same).  causal: a sequence's queries are
-    its last positions.  Rows outside the sequences are left as they were.  Returns (out
-    [total_q,Hq,D], lse [total_q,Hq] fp32)."""
+    its last positions.  num_splits: parts of each sequence's keys (0: the library's choice).  Rows
+    outside the sequences are left as they were.  Returns (out [total_q,Hq,D], lse [total_q,Hq]
+    fp32)."""
     lib = _lib or load_library()
     dev, dtype, qs, ks = _gpu(q), q.dtype, q.shape, k.shape
     fields = _packed_fields(dev, dtype, qs, ks, cu_seqlens_q, cu_seqlens_k, causal, scale)
@@ -1260,9 +1264,16 @@ def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool 
             out = _empty(qs, dtype=dtype, device=q.device)
         if lse is None:
             lse = _empty(rows, dtype=torch.float32, device=q.device)
-        a = _pack_packed(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                         _flat(dev, torch.float32, rows, "lse", lse), *strides,
-                         *_strided(dev, dtype, qs, "out", out), *fields)
+        fields = (q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                  _flat(dev, torch.float32, rows, "lse", lse), *strides,
+                  *_strided(dev, dtype, qs, "out", out), *fields, num_splits)
+        a = _pack_packed(*fields, 0, 0)
+        need = lib.fa_packed_workspace_size(a)
+        if need:
+            if workspace is not None:
+                _on(dev, workspace)
+            ws = _workspace(need, q.device, workspace)
+            a = _pack_packed(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
         _check(lib.fa_prefill_packed(a, _raw_stream(dev)))
     return out, lse
 

@@ -33,6 +33,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include "dependent.cuh"
 #include "internal.h"
 #include "packed.cuh"
 
@@ -78,6 +79,30 @@ __device__ __forceinline__ Tile make_tile(const Params& p, const Seq& s, int q0)
   }
   return t;
 }
+
+// An item's two query tiles and the KV tiles that go through the ring for them: first, first + 1, ...; of
+// each tile's own, n counts from there.
+template <bool SPLIT>
+struct Work {
+  Tile a, b;
+  int first, n;
+  __device__ __forceinline__ Work(const Params& p, const Item& item) {
+    a = make_tile(p, item.seq, item.at);
+    b = make_tile(p, item.seq, item.at + p.q_per_tile);
+    first = 0;
+    n = max(a.n, b.n);
+    if (SPLIT) {
+      const int per = (n + p.splits - 1) / p.splits;
+      first = min(n, item.split * per);
+      const int last = min(n, first + per);
+      a.n = max(0, min(a.n, last) - first);
+      b.n = max(0, min(b.n, last) - first);
+      n = last - first;
+    }
+  }
+  // whether the last V tile reaches past the sequence
+  __device__ __forceinline__ bool tail(const Item& item) const { return n > 0 && (first + n) * kKeys > item.seq.nk; }
+};
 
 // Thirty-two scores against the maximum m: exponentials packed, their sum added.
 template <bool BF16>
@@ -153,7 +178,7 @@ __device__ __forceinline__ bool next_item(const Bars<D>& bars, const Item* items
 
 // The issuing warp of tile X.  All lanes wait, one issues; the order of the waits puts the last one to
 // come true, for P, in front of the products.
-template <int D, bool BF16, int X>
+template <int D, bool BF16, bool SPLIT, int X>
 __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t bar_base, uint32_t tmem,
                                       const Item* items, volatile int* turns) {
   using L = Layout<D>;
@@ -196,9 +221,9 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
       more = got.at >= 0;
     }
     if (!__any_sync(0xffffffffu, more)) break;
-    const Tile tile_a = make_tile(p, got.seq, got.at), tile_b = make_tile(p, got.seq, got.at + p.q_per_tile);
-    const int nx = uniform(X ? tile_b.n : tile_a.n), other_n = uniform(X ? tile_a.n : tile_b.n);
-    const int n = max(nx, other_n), end = uniform(X ? tile_b.end : tile_a.end);
+    const Work<SPLIT> work(p, got);
+    const int nx = uniform(X ? work.b.n : work.a.n), other_n = uniform(X ? work.a.n : work.b.n);
+    const int n = uniform(work.n), end = uniform((X ? work.b.end : work.a.end) - work.first * kKeys);
     if (nx > 0) {
       if (!wait(bars.q(X), uses) || !wait(bars.full(slot), lap)) break;
       tc_fence_after();
@@ -270,7 +295,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
   }
 }
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     forward_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const Params p) {
@@ -335,11 +360,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (more) {
         const int w = dealt(k);
         int b, t;
-        finder.find(w / p.Hkv, pieces, b, t);
+        finder.find(w / (SPLIT ? p.Hkv * p.splits : p.Hkv), pieces, b, t);
         if (b >= 0) {
           item.seq = load_seq(p, b);
           item.at = t * width;
-          item.head = w % p.Hkv;
+          item.head = SPLIT ? w / p.splits % p.Hkv : w % p.Hkv;
+          item.split = SPLIT ? w % p.splits : 0;
         }
         if (k >= kItems) ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read(k % kItems), (k / kItems - 1) & 1, p.status));
         if (ok && lane == 0) {
@@ -365,11 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         clear_at = -1;
       }
       if (item.at >= 0) {
-        const int n = max(make_tile(p, item.seq, item.at).n, make_tile(p, item.seq, item.at + p.q_per_tile).n);
-        entries += 2 * n;
-        if (n * kKeys > item.seq.nk && n > 0) {
+        const Work<SPLIT> work(p, item);
+        entries += 2 * work.n;
+        if (work.tail(item)) {
           clear_at = entries - 1;
-          clear_row = item.seq.nk - (n - 1) * kKeys;
+          clear_row = item.seq.nk - (work.first + work.n - 1) * kKeys;
         }
       }
     }
@@ -383,11 +409,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t tail_phase = 0, to_tail = 0;
       Item item;
       for (int k = 0; ok && next_item(bars, items, k, item, p.status); ++k) {
-        const Tile tile_a = make_tile(p, item.seq, item.at), tile_b = make_tile(p, item.seq, item.at + p.q_per_tile);
-        const int n = max(tile_a.n, tile_b.n);
+        const Work<SPLIT> work(p, item);
+        const int n = work.n;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const Tile tile = x ? tile_b : tile_a;
+          const Tile tile = x ? work.b : work.a;
           if (!ok || tile.n == 0) continue;
           if (q_uses[x] > 0 && !(ok = mbar_wait(bars.q_free(x), (q_uses[x] - 1) & 1, p.status))) continue;
           mbar_arrive_expect_tx(bars.q(x), static_cast<uint32_t>(128 * (D / 64) * p.G * p.q_per_tile));
@@ -396,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         item.seq.q0 + tile.q0);
           ++q_uses[x];
         }
-        const bool tail = n > 0 && n * kKeys > item.seq.nk;  // the last V tile reaches past the sequence
+        const bool tail = work.tail(item);
         for (int i = 0; ok && i < 2 * n; ++i, ++entry) {      // K_0, V_0, K_1, V_1, ...
           const int slot = entry % L::kSlots;
           if (entry >= L::kSlots && !(ok = mbar_wait(bars.empty(slot), (entry / L::kSlots - 1) & 1, p.status))) break;
@@ -410,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(bar, L::kTile);
           for (int kb = 0; kb < D / 64; ++kb)
             tma_load_3d(s_base + L::kRing + slot * L::kTile + kb * L::kBlock, (i & 1) ? &tm_v : &tm_k, bar, kb * 64,
-                        item.head, item.seq.k0 + (i / 2) * kKeys);
+                        item.head, item.seq.k0 + (work.first + i / 2) * kKeys);
         }
       }
       if (!ok) {
@@ -425,9 +451,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 9) {
-    issue<D, BF16, 0>(p, s_base, bars.at, tmem, items, turns);
+    issue<D, BF16, SPLIT, 0>(p, s_base, bars.at, tmem, items, turns);
   } else if (warp == 10) {
-    issue<D, BF16, 1>(p, s_base, bars.at, tmem, items, turns);
+    issue<D, BF16, SPLIT, 1>(p, s_base, bars.at, tmem, items, turns);
   } else {
     // --------------------------- softmax, epilogue: a row a thread ---------------------------
     const int x = warp / 4, r = threadIdx.x % 128;
@@ -441,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The item before, whose output is still in tensor memory: if the first scores of the next are there, they
     // are dealt with first, so that the wait for its last product, and the stores, have work beside them.
     bool pending = false;
-    uint16_t* out_row = nullptr;
+    uint8_t* out_row = nullptr;
     float* lse_row = nullptr;
     float out_m = 0.f, out_l = 0.f;
     int out_step = 0;
@@ -449,7 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && more; ++k) {
       Item item{};
       more = __all_sync(0xffffffffu, next_item(bars, items, k, item, p.status));
-      const Tile tile = make_tile(p, item.seq, item.at + x * p.q_per_tile);
+      int first = 0;
+      Tile tile;
+      if (SPLIT) {
+        const Work<SPLIT> work(p, item);
+        tile = x ? work.b : work.a;
+        first = work.first * kKeys;
+      } else {
+        tile = make_tile(p, item.seq, item.at + x * p.q_per_tile);
+      }
       const int nx = more ? tile.n : 0;
       const int i = tile.q0 + row_token, h = item.head * p.G + row_head;
       const bool valid = more && r < p.G * p.q_per_tile && i < item.seq.nq;
@@ -461,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
           if (!ok) break;
           tc_fence_after();
-          const int left = key_lim - j * kKeys;  // keys of the tile that the row sees
+          const int left = key_lim - first - j * kKeys;  // keys of the tile that the row sees
           bool done = false;
           if (a > 0.f) {
             const bool masked = __any_sync(0xffffffffu, left < kKeys);
@@ -538,29 +572,34 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const float inv = out_l > 0.f ? 1.f / out_l : 0.f;
+          // A thread's row would be written 16 bytes at a time, each of a warp's stores touching 32 rows:
+          // through shared memory (128-byte swizzle) a store writes four rows' 128 bytes.
+          uint8_t* mine = smem + L::kStage + warp * (32 * 128);
+          constexpr int kSlab = SPLIT ? 32 : 64;  // columns of 128 bytes
 #pragma unroll 1
-          for (int c = 0; c < D / 64; ++c) {
+          for (int c = 0; c < D / kSlab; ++c) {
             uint32_t oa[32], ob[32];
-            tmem_ld32(tm_o + c * 64, oa);
-            tmem_ld32(tm_o + c * 64 + 32, ob);
+            tmem_ld32(tm_o + c * kSlab, oa);
+            if (!SPLIT) tmem_ld32(tm_o + c * kSlab + 32, ob);
             prefill::tmem_ld_wait_tied(oa);
-            prefill::tmem_ld_wait_tied(ob);
-            if (c == D / 64 - 1) {
+            if (!SPLIT) prefill::tmem_ld_wait_tied(ob);
+            if (c == D / kSlab - 1) {
               tc_fence_before();
               mbar_arrive(bars.o_free(x));
             }
-            // A thread's row would be written 16 bytes at a time, each of a warp's stores touching 32 rows:
-            // through shared memory (128-byte swizzle) a store writes four rows' 128 bytes.
-            uint8_t* mine = smem + L::kStage + warp * (32 * 128);
-            prefill::stage_slab16<BF16>(oa, inv, mine, lane, 0);
-            prefill::stage_slab16<BF16>(ob, inv, mine, lane, 1);
+            if (SPLIT) {
+              prefill::stage_slab_f32(oa, inv, mine, lane);
+            } else {
+              prefill::stage_slab16<BF16>(oa, inv, mine, lane, 0);
+              prefill::stage_slab16<BF16>(ob, inv, mine, lane, 1);
+            }
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const int rr = 4 * e + lane / 8;
               const uint4 v = *reinterpret_cast<const uint4*>(mine + rr * 128 + ((lane % 8) ^ (rr & 7)) * 16);
-              uint16_t* to = reinterpret_cast<uint16_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_row), rr));
-              if (to) *reinterpret_cast<uint4*>(to + c * 64 + (lane % 8) * 8) = v;
+              uint8_t* to = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out_row), rr));
+              if (to) reinterpret_cast<uint4*>(to + c * 128)[lane % 8] = v;
             }
             __syncwarp();
           }
@@ -569,8 +608,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok || !more) break;
       const int64_t row = item.seq.q0 + i;
-      uint16_t* dst = valid ? static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1] : nullptr;
-      float* dst_lse = valid && p.lse ? p.lse + row * p.Hq + h : nullptr;
+      uint8_t* dst = nullptr;
+      float* dst_lse = nullptr;
+      if (valid && SPLIT) {
+        const int64_t at = (row * p.Hq + h) * p.splits + item.split;
+        dst = reinterpret_cast<uint8_t*>(p.o_part + at * D);
+        dst_lse = p.lse_part + at;
+      } else if (valid) {
+        dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + row * p.out_strides[0] + h * p.out_strides[1]);
+        if (p.lse) dst_lse = p.lse + row * p.Hq + h;
+      }
       if (nx > 0) {
         pending = true;
         out_row = dst;
@@ -580,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         out_step = steps - 1;
       } else {  // rows that see no key
         if (dst)
-          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < D / (SPLIT ? 4 : 8); ++c) reinterpret_cast<uint4*>(dst)[c] = make_uint4(0, 0, 0, 0);
         if (dst_lse) *dst_lse = -INFINITY;
       }
     }
@@ -594,15 +641,107 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Parts of the rows' keys joined: lse = ln sum_s e^{lse_s}, out = sum_s e^{lse_s - lse} o_s.  A block a
+// token, a warp a head at a time, eight parts on their way at once.
+constexpr int kJoinThreads = 256;
+constexpr int kMaxSplits = 32;
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
+  constexpr int kCols = D / 32;  // columns a lane
+  const int token = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // rows of no sequence are left as they were
+  bool mine = false;
+  for (int b = threadIdx.x; b < p.B; b += kJoinThreads) {
+    const int first = __ldg(p.cu_q + b), end = __ldg(p.cu_q + b + 1);
+    mine = mine || (first >= 0 && first <= token && token < end && end <= p.total_q);
+  }
+  if (!__syncthreads_or(mine)) return;
+  wait_for_previous();
+  for (int h = warp; h < p.Hq; h += kJoinThreads / 32) {
+    const int64_t row = static_cast<int64_t>(token) * p.Hq + h;
+    const float* o = p.o_part + row * p.splits * D + lane * kCols;
+    const float part = lane < p.splits ? p.lse_part[row * p.splits + lane] : -INFINITY;
+    float top = part;
+#pragma unroll
+    for (int i = 16; i >= 1; i >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+    const float m = top == -INFINITY ? 0.f : top;
+    const float e = exp2_approx((part - m) * prefill::kLog2e);
+    float total = 0.f, y[kCols] = {};
+    for (int s0 = 0; s0 < p.splits; s0 += 8) {
+      float x[8][kCols];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        if (s0 + s >= p.splits) break;
+        if constexpr (kCols == 4) {
+          const float4 v = *reinterpret_cast<const float4*>(o + (s0 + s) * D);
+          x[s][0] = v.x;
+          x[s][1] = v.y;
+          x[s][2] = v.z;
+          x[s][3] = v.w;
+        } else {
+          const float2 v = *reinterpret_cast<const float2*>(o + (s0 + s) * D);
+          x[s][0] = v.x;
+          x[s][1] = v.y;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        if (s0 + s >= p.splits) break;
+        const float w = __shfl_sync(0xffffffffu, e, s0 + s);
+        total += w;
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) y[c] = fmaf(w, x[s][c], y[c]);
+      }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;  // (a NaN stays one)
+    uint16_t* to = static_cast<uint16_t*>(p.out) + token * p.out_strides[0] + h * p.out_strides[1] + lane * kCols;
+    uint32_t w[kCols / 2];
+#pragma unroll
+    for (int c = 0; c < kCols / 2; ++c)
+      w[c] = BF16 ? pack_bf16x2(y[2 * c] * inv, y[2 * c + 1] * inv) : pack_f16x2(y[2 * c] * inv, y[2 * c + 1] * inv);
+    if constexpr (kCols == 4) *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(to) = w[0];
+    if (lane == 0 && p.lse) p.lse[row] = total == 0.f ? -INFINITY : m + logf(total);
+  }
+}
+
 template <int D, bool BF16>
 cudaError_t launch(const Params& p, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                    int64_t items, cudaStream_t stream) {
-  auto kern = forward_kernel<D, BF16>;
+  auto kern = p.splits > 1 ? forward_kernel<D, BF16, true> : forward_kernel<D, BF16, false>;
   cudaError_t e = ensure_smem_limit(kern, Layout<D>::kAlloc);
   if (e != cudaSuccess) return e;
-  const int64_t work = items * p.Hkv, sms = num_sms() > 0 ? num_sms() : 152;
+  const int64_t work = items * p.Hkv * p.splits, sms = num_sms() > 0 ? num_sms() : 152;
   kern<<<static_cast<unsigned>(work < sms ? work : sms), kThreads, Layout<D>::kAlloc, stream>>>(tq, tk, tv, p);
-  return cudaGetLastError();
+  if ((e = cudaGetLastError()) != cudaSuccess || p.splits == 1) return e;
+  return launch_dependent(join_kernel<D, BF16>, static_cast<unsigned>(p.total_q), 1, kJoinThreads, 0, stream, p);
+}
+
+// Parts that the keys are split into: as many as give no SM a second work item, each of eight KV tiles of a
+// mean sequence at least; so one from half as many items as SMs on.  Measured (bf16, D = 128; us): 16 queries of
+// 8 heads over 65,536 keys, 1 item: 637 whole, 88 in 8 parts, 32 in 32; 512 queries of 32 heads in 8 groups over
+// 32,768 keys, 64 items: 342 whole, 186 in 2, 253 in 3; two of 512 over 16,384 keys, 128 items: 180 whole, 201 in
+// 2; 1024 queries over their own keys, 64 items: 19 whole, 22 in 2 (four tiles each).
+int plan_splits(const fa_packed_args* a) {
+  if (a->num_splits > 0) return a->num_splits;
+  const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+  const int64_t width = 2 * (kRows / (a->Hq / a->Hkv));
+  const int64_t items = (a->total_q / width + (a->B + 1) / 2) * a->Hkv;  // a sequence's last one is half full
+  int64_t s = sms / items;
+  const int64_t most = a->total_k / (8LL * kKeys * a->B);
+  if (s > most) s = most;
+  if (s > kMaxSplits) s = kMaxSplits;
+  return s < 2 ? 1 : static_cast<int>(s);
+}
+
+size_t part_bytes(const fa_packed_args* a, int splits) {
+  return (static_cast<size_t>(a->total_q) * a->Hq * splits * a->D * sizeof(float) + 255) / 256 * 256;
+}
+
+size_t workspace_bytes(const fa_packed_args* a, int splits) {
+  if (splits == 1) return 0;
+  return part_bytes(a, splits) + (static_cast<size_t>(a->total_q) * a->Hq * splits * sizeof(float) + 255) / 256 * 256;
 }
 
 int fail(int code, const char* fmt, const char* who, long a = 0, long b = 0, long c = 0) {
@@ -672,11 +811,24 @@ bool encode_rows(CUtensorMap* map, bool bf16, const void* base, const int64_t* s
 
 using namespace fa;
 
+extern "C" size_t fa_packed_workspace_size(const fa_packed_args* a) {
+  if (!a || packed::check_sizes("fa_prefill_packed", a->B, a->Hq, a->Hkv, a->D, a->total_q, a->total_k, a->dtype,
+                                a->scale) != FA_OK)
+    return 0;
+  if (a->B == 0 || a->total_q == 0 || a->num_splits < 0 || a->num_splits > packed::kMaxSplits) return 0;
+  return packed::workspace_bytes(a, packed::plan_splits(a));
+}
+
 extern "C" int fa_prefill_packed(const fa_packed_args* a, void* stream) {
   const char* who = "fa_prefill_packed";
   if (!a) return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed: null argument struct");
   int rc = packed::check_sizes(who, a->B, a->Hq, a->Hkv, a->D, a->total_q, a->total_k, a->dtype, a->scale);
   if (rc != FA_OK || a->B == 0 || a->total_q == 0) return rc;
+  if (a->num_splits < 0 || a->num_splits > packed::kMaxSplits)
+    return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed: num_splits must be in [0, 32]");
+  if (a->num_splits > 1 && packed::most_items(a->total_q, a->B, 2 * (packed::kRows / (a->Hq / a->Hkv))) * a->Hkv *
+                                   a->num_splits > (1LL << 30))
+    return set_error(FA_ERR_UNSUPPORTED, "fa_prefill_packed: too many tiles for that many parts");
   if (!a->cu_seqlens_q || !a->cu_seqlens_k)
     return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed: null cu_seqlens pointer");
   if ((rc = packed::check_tensor(who, "q", a->q, a->q_strides, a->total_q, a->Hq, a->D)) != FA_OK) return rc;
@@ -685,6 +837,16 @@ extern "C" int fa_prefill_packed(const fa_packed_args* a, void* stream) {
       ((rc = packed::check_tensor(who, "k", a->k, a->k_strides, a->total_k, a->Hkv, a->D)) != FA_OK ||
        (rc = packed::check_tensor(who, "v", a->v, a->v_strides, a->total_k, a->Hkv, a->D)) != FA_OK))
     return rc;
+  const int splits = packed::plan_splits(a);
+  const size_t need = packed::workspace_bytes(a, splits);
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need)) {
+    char msg[160];
+    snprintf(msg, sizeof msg, "fa_prefill_packed: workspace of %zu bytes needed (got %zu)", need,
+             a->workspace ? a->workspace_bytes : static_cast<size_t>(0));
+    return set_error(FA_ERR_WORKSPACE, msg);
+  }
+  if (need > 0 && (reinterpret_cast<uintptr_t>(a->workspace) & 255u) != 0)
+    return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed: workspace must be 256-byte aligned");
   uint32_t* status = device_status_ptr();
   if (!status) return set_error(FA_ERR_CUDA, "fa_prefill_packed: no usable CUDA device");
   packed::Params p{};
@@ -704,6 +866,12 @@ extern "C" int fa_prefill_packed(const fa_packed_args* a, void* stream) {
   memcpy(p.out_strides, a->out_strides, sizeof p.out_strides);
   p.lse = a->lse;
   p.status = status;
+  p.splits = splits;
+  if (splits > 1) {
+    uint8_t* ws = static_cast<uint8_t*>(a->workspace);
+    p.o_part = reinterpret_cast<float*>(ws);
+    p.lse_part = reinterpret_cast<float*>(ws + packed::part_bytes(a, splits));
+  }
   const bool bf16 = a->dtype == FA_BF16;
   // without keys nothing reads the maps of K and V
   const void* k = a->total_k > 0 ? a->k : a->q;

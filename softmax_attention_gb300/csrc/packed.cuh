@@ -25,6 +25,10 @@ struct Params {
   void* out;             // forward: [total_q, Hq, D] by its strides (token, head; elements)
   int64_t out_strides[2];
   float* lse;            // [total_q, Hq]; forward: or nullptr
+  // forward, keys split: normalised partial outputs [total_q, Hq, splits, D] and their lse
+  int splits;
+  float* o_part;
+  float* lse_part;
   uint32_t* status;
 };
 
@@ -156,6 +160,7 @@ struct Item {
   Seq seq;
   int at;    // first query, or key, of the piece in its sequence; -1: no more work
   int head;  // kv head
+  int split; // forward: part of the keys
 };
 
 // A value that is the same in every lane, in a form that the compiler knows to be: the operands of

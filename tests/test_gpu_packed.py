@@ -122,6 +122,64 @@ def test_forward(lens, klens, Hq, Hkv, D, dtype, causal):
         assert (t[:c.cu[0]] == 7).all() and (t[c.cu[-1]:] == 7).all()
 
 
+@pytest.mark.parametrize("splits", [2, 3, 11, 32])
+@pytest.mark.parametrize("lens,klens,Hq,Hkv,D,dtype,causal", CASES)
+def test_forward_split(lens, klens, Hq, Hkv, D, dtype, causal, splits):
+    """Keys in parts: the same bounds (parts are joined in 32 bits); rows of no sequence as they were."""
+    c = Case(lens, Hq, Hkv, D, dtype, klens=klens, first=0 if klens else 3, behind=5, seed=D + Hq)
+    scale = 1.0 / math.sqrt(D)
+    q, k, v = c.gpu()
+    out = torch.full((q.shape[0], Hq + 1, D), 7.0, dtype=dtype, device="cuda")[:, :Hq]  # strided
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    ws = torch.full((32 * q.shape[0] * Hq * (D + 1) * 4 + 512,), 255, dtype=torch.uint8, device="cuda")  # NaN
+    fa.fa_prefill_packed(q, k, v, *c.offsets(), causal=causal, scale=scale, out=out, lse=lse,
+                         num_splits=splits, workspace=ws)
+    torch.cuda.synchronize()
+    for rows, _, want in c.want(causal, scale):
+        ref.check("out", out[rows], *want["out"])
+        ref.check("lse", lse[rows], *want["lse"])
+    outside = torch.ones(q.shape[0], dtype=torch.bool)
+    outside[c.cu[0]:c.cu[-1]] = False
+    assert (out[outside.cuda()] == 7).all() and (lse[outside.cuda()] == 7).all()
+
+
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF)])
+def test_forward_split_by_rule(D, dtype):
+    """A few tokens at the end of long contexts: the library's own choice of parts."""
+    c = Case([1, 70, 0, 33], 8, 2, D, dtype, klens=[9000, 7001, 300, 4096], seed=3)
+    scale = 1.0 / math.sqrt(D)
+    q, k, v = c.gpu()
+    out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), scale=scale)
+    one, _ = fa.fa_prefill_packed(q, k, v, *c.offsets(), scale=scale, num_splits=1)
+    torch.cuda.synchronize()
+    for rows, _, want in c.want(True, scale):
+        ref.check("out", out[rows], *want["out"])
+        ref.check("lse", lse[rows], *want["lse"])
+        ref.check("out", one[rows], *want["out"])
+
+
+def test_split_captured_and_replayed():
+    """A captured call whose workspace is the graph's own, replayed with other values."""
+    c = Case([5, 60], 8, 2, 128, BF, klens=[3000, 2500], seed=4)
+    d = Case([5, 60], 8, 2, 128, BF, klens=[3000, 2500], seed=5)
+    scale = 1.0 / math.sqrt(128)
+    q, k, v = (t.contiguous() for t in c.gpu())
+    offsets = c.offsets()
+    fa.fa_prefill_packed(q, k, v, *offsets, scale=scale, num_splits=5)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = fa.fa_prefill_packed(q, k, v, *offsets, scale=scale, num_splits=5)
+    for case in (c, d):
+        for to, src in zip((q, k, v), case.gpu()):
+            to.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        for rows, _, want in case.want(True, scale):
+            ref.check("out", out[rows], *want["out"])
+            ref.check("lse", lse[rows], *want["lse"])
+
+
 @pytest.mark.parametrize("lens,klens,Hq,Hkv,D,dtype,causal", CASES)
 def test_backward(lens, klens, Hq, Hkv, D, dtype, causal):
     c = Case(lens, Hq, Hkv, D, dtype, klens=klens, first=0 if klens else 3, behind=5, seed=D + Hq)

@@ -122,6 +122,27 @@ def test_refused(lib, name, make, kw, code):
     assert fa.fa_last_error()
 
 
+@pytest.mark.parametrize("kw,code", [
+    (dict(num_splits=-1), INV), (dict(num_splits=33), INV), (dict(num_splits=2), WS),
+    (dict(num_splits=2, workspace=P, workspace_bytes=2 * 9 * 4 * 128 * 4), WS),
+    (dict(num_splits=2, workspace=P + 16, workspace_bytes=1 << 20), INV),
+    # 2^14 sequences, 2^13 kv heads and 32 parts: 2^32 work items
+    (dict(num_splits=32, B=1 << 14, Hq=1 << 13, Hkv=1 << 13), UNS)])
+def test_parts_refused(lib, kw, code):
+    assert lib.fa_prefill_packed(ctypes.byref(_packed(**kw)), None) == code
+    assert fa.fa_last_error()
+
+
+def test_parts_workspace(lib):
+    size = lambda **kw: lib.fa_packed_workspace_size(ctypes.byref(_packed(**kw)))  # noqa: E731
+    assert size() == size(num_splits=1) == size(num_splits=33) == size(num_splits=2, total_q=0) == 0
+    assert size(num_splits=3) >= 3 * 9 * 4 * (128 + 1) * 4
+    # few query tiles and many keys: parts of eight tiles or more; many query tiles: none
+    assert size(B=1, total_q=16, total_k=16384) >= 16 * 16 * 4 * (128 + 1) * 4
+    assert size(B=1, total_q=16, total_k=2047) == size(B=1, total_q=16384, total_k=16384) == 0
+    assert lib.fa_packed_workspace_size(None) == 0
+
+
 @pytest.mark.parametrize("name", ["fa_prefill_packed", "fa_prefill_packed_backward", "fa_qk_norm_rotary",
                                   "fa_qk_norm_rotary_backward", "gated_delta_step"])
 def test_null_struct(lib, name):
