@@ -463,7 +463,7 @@ int fa_rotary_frequencies(int rot_dim, double base, fa_rotary_scaling scaling, d
  *   q, k, q_out, k_out, positions, inv_freq, interleaved, amplitude: as in fa_rotary (rot_dim = 0:
  *   norms alone, positions and inv_freq are not read);
  *   q_weight, k_weight [D] in weight_dtype (dtype or FA_FP32), shared by all heads, or NULL (ones).
- *   D a multiple of 16 up to 512; rot_dim a multiple of 16, at most D.
+ *   D a multiple of 16 up to 512; rot_dim a multiple of 16, at most D; Hq and Hk <= 65535.
  * Computed in fp32, rounded once to dtype.  q_out and k_out may be q and k themselves (same pointer
  * and strides).
  */

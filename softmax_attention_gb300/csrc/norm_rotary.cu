@@ -301,6 +301,8 @@ bool is_type(fa_dtype t) { return t == FA_BF16 || t == FA_FP16 || t == FA_FP32; 
 
 int check_call(const char* who, const NormCall& a) {
   if (a.B < 0 || a.T < 0 || a.Hq < 0 || a.Hk < 0) return bad(FA_ERR_INVALID_ARG, who, "need B, T, Hq, Hk >= 0");
+  if (a.Hq > 65535 || a.Hk > 65535 || static_cast<int64_t>(a.B) * a.T > (1LL << 40))
+    return bad(FA_ERR_UNSUPPORTED, who, "Hq and Hk must be <= 65535, B * T <= 2^40");
   if (a.D <= 0 || a.D % 16 != 0 || a.D > kMaxD)
     return bad(FA_ERR_UNSUPPORTED, who, "D must be a multiple of 16 in [16, 512]");
   if (a.rot_dim < 0 || a.rot_dim % 16 != 0 || a.rot_dim > a.D)

@@ -656,8 +656,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const Params p) {
     const int first = __ldg(p.cu_q + b), end = __ldg(p.cu_q + b + 1);
     mine = mine || (first >= 0 && first <= token && token < end && end <= p.total_q);
   }
+  wait_for_previous();  // (by every block: what follows this kernel counts on the end of the one before it)
   if (!__syncthreads_or(mine)) return;
-  wait_for_previous();
   for (int h = warp; h < p.Hq; h += kJoinThreads / 32) {
     const int64_t row = static_cast<int64_t>(token) * p.Hq + h;
     const float* o = p.o_part + row * p.splits * D + lane * kCols;

@@ -122,6 +122,15 @@ def test_refused(lib, name, make, kw, code):
     assert fa.fa_last_error()
 
 
+@pytest.mark.parametrize("name,make", [("fa_qk_norm_rotary", _norm), ("fa_qk_norm_rotary_backward", _norm_backward)])
+@pytest.mark.parametrize("kw", [dict(Hq=65536), dict(Hk=2**31 - 1), dict(Hq=2**31 - 1, Hk=2**31 - 1),
+                                dict(B=2**31 - 1, T=2**31 - 1)])
+def test_norm_too_many_rows(lib, name, make, kw):
+    """Counts whose sums or products would pass the integers that hold them."""
+    assert getattr(lib, name)(ctypes.byref(make(**kw)), None) == UNS
+    assert lib.fa_qk_norm_rotary_backward_workspace_size(ctypes.byref(_norm_backward(**kw))) == 0
+
+
 @pytest.mark.parametrize("kw,code", [
     (dict(num_splits=-1), INV), (dict(num_splits=33), INV), (dict(num_splits=2), WS),
     (dict(num_splits=2, workspace=P, workspace_bytes=2 * 9 * 4 * 128 * 4), WS),
