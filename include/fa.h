@@ -718,7 +718,7 @@ size_t fa_packed_workspace_size(const fa_packed_args* args);
  * (Within a sequence values of q, k, v or dout that are not finite may reach gradients that they have
  * no part in, as 0 times them.)
  * Every row of dq, dk and dv that belongs to a sequence is written (zeros where nothing is seen),
- * no other row.  No atomics: the same call gives the same bits.
+ * no other row.  No sum depends on an order of arrival: the same call gives the same bits.
  * workspace: fa_packed_backward_workspace_size(args) bytes, 256-byte aligned; calls that may
  * overlap on the GPU need one each.
  */

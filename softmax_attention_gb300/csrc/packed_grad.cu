@@ -7,12 +7,12 @@
 // Three kernels; the sums that a block owns stay in tensor memory, so that nothing is added by atomics
 // and the same call gives the same bits:
 //   - row_kernel: delta and -lse, in the form that the others use them, a pass over dout and out;
-//   - dq_kernel: a block holds a 128-row query tile (query tokens x heads of a kv head, as in
-//     packed.cu) and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K;
 //   - dkv_kernel: a block holds a tile of 128 keys and walks over the query tiles that see it, all
 //     heads of the group: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  With the
 //     products turned, P^T and dS^T have keys as rows and go back to tensor memory as the
-//     left operands of the second pair: neither ever passes through shared memory.
+//     left operands of the second pair: neither ever passes through shared memory;
+//   - dq_kernel: a block holds a 128-row query tile (query tokens x heads of a kv head, as in
+//     packed.cu) and walks over the keys: S = Q K^T, dP = dO V^T, dQ += dS K.
 // S and dP are computed in both, seven products for the five of a form that adds dq by atomics.
 //
 // Eight warps do the element-wise work, two a row, 64 columns each.  Blocks stay for all of their work
@@ -51,6 +51,7 @@ struct GradParams {
   float2* rows;          // -lse log2 e (-inf where nothing is seen), delta
   float* powers;         // fp16: f of the row
   uint32_t* dout_max;    // fp16: bits of the largest |dout|
+  int* taken;            // dq_kernel: work items taken so far, beyond each block's first
 };
 
 // The power of two that brings `top` to [8, 16); 1 for 0, an infinity or NaN.
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
   const Params& p = g.f;
   let_next_start();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *g.taken = 0;
   // rows in front of the first sequence and behind the last take no part
   const int from = max(0, __ldg(p.cu_q)), to = min(p.total_q, __ldg(p.cu_q + p.B));
   const int lane = threadIdx.x % kLanes;
@@ -199,22 +201,24 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
 constexpr int kThreads = 384;
 constexpr int kItems = 4;
 
-// The k-th item, copied from its place in shared memory; false: no more, or a wait ran out.
+// The k-th item, copied from its place (of PLACES) in shared memory; false: no more, or a wait ran out.
+template <int PLACES>
 __device__ __forceinline__ bool next_item(uint32_t bar_item, uint32_t bar_item_read, const Item* items, int k, Item& item,
                                           uint32_t* status) {
-  if (!mbar_wait(bar_item + 8u * (k % kItems), (k / kItems) & 1, status)) return false;
-  item = items[k % kItems];
-  mbar_arrive(bar_item_read + 8u * (k % kItems));
+  if (!mbar_wait(bar_item + 8u * (k % PLACES), (k / PLACES) & 1, status)) return false;
+  item = items[k % PLACES];
+  mbar_arrive(bar_item_read + 8u * (k % PLACES));
   return item.at >= 0;
 }
 
 // The same by a whole issuing warp, one arrival for all lanes.
+template <int PLACES>
 __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_item_read, const Item* items, int k,
                                                Item& item, uint32_t* status) {
-  if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8u * (k % kItems), (k / kItems) & 1, status))) return false;
-  item = items[k % kItems];
+  if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8u * (k % PLACES), (k / PLACES) & 1, status))) return false;
+  item = items[k % PLACES];
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(bar_item_read + 8u * (k % kItems));
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bar_item_read + 8u * (k % PLACES));
   return __any_sync(0xffffffffu, item.at >= 0);
 }
 
@@ -225,6 +229,13 @@ __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_i
 // dP_{j+1} are computed while the weights of tile j are; dS has two buffers of its own.  (With dS_j written
 // over one of two S buffers S_{j+1} had to wait for dQ_{j-1}.)
 // ------------------------------------------------------------------------------------------
+// Its work items are taken as blocks come free (a counter in the workspace; which block takes an item changes
+// nothing in it), and it runs after dkv_kernel, whose blocks end far apart where sequences are long (8192 tokens: a
+// key tile meets up to 256 query tiles, and the mean block 219): it fills what they leave.  dq first and both dealt
+// out ahead of time: 572 us for the 550 of this (16 heads in 4 groups, D = 128), 386 for 373 with samples of 512 to
+// 2048 tokens.  An item in one place is taken as late as can be; with 2, 3 and 4 places 561, 585 and 609 us.
+constexpr int kDqItems = 1;
+
 template <int D>
 struct DqLayout {
   // K_{j+1} is needed for S while the weights of tile j are computed, when dQ_{j-1}, the last to read
@@ -233,7 +244,7 @@ struct DqLayout {
   static constexpr int kTile = kBlock * (D / 64);
   static constexpr int kQ = 0, kDo = kTile, kK = 2 * kTile, kV = kK + kKeep * kTile;
   static constexpr int kBars = kV + kPass * kTile;
-  static constexpr int kNumBars = 2 * kKeep + 2 * kPass + 14 + 2 * kItems;
+  static constexpr int kNumBars = 2 * kKeep + 2 * kPass + 14 + 2 * kDqItems;
   static constexpr int kAlloc = kBars + kNumBars * 8 + 1024;
   static constexpr int kS = D, kDp = D + kKeys, kDs = D + 2 * kKeys;  // tensor memory: dQ, S, dP, dS[2]
   static_assert(kAlloc <= 232448 && kDs + kKeys <= 512, "memory budgets");
@@ -261,7 +272,7 @@ struct DqBars {
   __device__ __forceinline__ uint32_t o_free() const { return one(kRest + 11); }
   __device__ __forceinline__ uint32_t done(int i) const { return one(kRest + 12 + i); }
   __device__ __forceinline__ uint32_t item() const { return one(kRest + 14); }
-  __device__ __forceinline__ uint32_t item_read() const { return one(kRest + 14 + kItems); }
+  __device__ __forceinline__ uint32_t item_read() const { return one(kRest + 14 + kDqItems); }
 };
 
 // A place in a ring, and how often the ring has been gone through before it.
@@ -293,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   __shared__ uint32_t tmem_slot;
-  __shared__ Item items[kItems];
+  __shared__ Item items[kDqItems];
   const uint32_t s_base = smem_addr(smem);
   const DqBars<D> bars{s_base + L::kBars};
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bars.dq(i), 1);
       mbar_init(bars.done(i), 1);
     }
-    for (int i = 0; i < kItems; ++i) {
+    for (int i = 0; i < kDqItems; ++i) {
       mbar_init(bars.item() + 8u * i, 1);
       mbar_init(bars.item_read() + 8u * i, 256 + 3);  // weights, issuers, copies
     }
@@ -351,7 +362,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Item item{};
       item.at = -1;
       if (more) {
-        const int w = dealt(k);
+        int w = blockIdx.x;
+        if (k > 0) {
+          if (lane == 0) w = static_cast<int>(gridDim.x) + atomicAdd(gp.taken, 1);
+          w = __shfl_sync(0xffffffffu, w, 0);
+        }
         int b, t;
         finder.find(w / p.Hkv, pieces, b, t);
         if (b >= 0) {
@@ -359,11 +374,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           item.at = t * p.q_per_tile;
           item.head = w % p.Hkv;
         }
-        if (k >= kItems)
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kItems), (k / kItems - 1) & 1, p.status));
+        if (k >= kDqItems)
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kDqItems), (k / kDqItems - 1) & 1, p.status));
         if (ok && lane == 0) {
-          items[k % kItems] = item;
-          mbar_arrive(bars.item() + 8u * (k % kItems));
+          items[k % kDqItems] = item;
+          mbar_arrive(bars.item() + 8u * (k % kDqItems));
         }
         more = b >= 0;
       }
@@ -394,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tile = 0, uses = 0, tails = 0;  // key tiles; items with any; K tiles that land on the tail's barrier
       int tail_at = -1, k_only = -1;
       Item item;
-      for (int k = 0; ok && next_item(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
         const int n = key_tiles(p, item.seq, item.at);
         if (n == 0) continue;
         if (uses > 0 && !(ok = mbar_wait(bars.q_free(), (uses - 1) & 1, p.status))) break;
@@ -455,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = sdesc_sw128(s_base + L::kQ, 16, 1024), do_desc = sdesc_sw128(s_base + L::kDo, 16, 1024);
       const uint64_t k_desc = sdesc_sw128(s_base + L::kK, 16, 1024), v_desc = sdesc_sw128(s_base + L::kV, 16, 1024);
       Place<L::kPass> vp;
-      for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item_warp<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
         const int n = uniform(key_tiles(p, item.seq, item.at));
         if (n == 0) continue;
         if (!wait(bars.q(), uses++)) break;
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       constexpr uint32_t idesc = idesc_f16(BF16, kRows, D, false, true);
       const uint64_t k_desc = sdesc_sw128(s_base + L::kK, kBlock, 1024);
-      for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item_warp<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
         const int n = uniform(key_tiles(p, item.seq, item.at));
         if (n == 0) continue;
         // dQ of the item before has to be read before the first product overwrites it
@@ -519,8 +534,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const float2 a2 = make_float2(p.scale_log2, p.scale_log2);
     const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
-    wait_for_previous();  // row_kernel
-    if (threadIdx.x == 0) let_next_start();
     bool ok = true;
     int step = 0;
     // The item before, whose dQ is still in tensor memory: if the first scores of the next are there, they are
@@ -532,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = true;
     for (int k = 0; ok && more; ++k) {
       Item item{};
-      more = __all_sync(0xffffffffu, next_item(bars.item(), bars.item_read(), items, k, item, p.status));
+      more = __all_sync(0xffffffffu, next_item<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status));
       const int n = more ? key_tiles(p, item.seq, item.at) : 0;
       const int i = item.at + row_token, h = item.head * p.G + row_head;
       const bool valid = more && r < p.G * p.q_per_tile && i < item.seq.nq;
@@ -633,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  wait_for_previous();  // nothing of dkv_kernel's is read here; but what follows this kernel counts on its end
 }
 
 // ------------------------------------------------------------------------------------------
@@ -714,7 +728,7 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
   Place<L::kSlots> q;  // of the tile's Q; its dO is the next
   int step = 0, uses = 0;
   Item item;
-  for (int k = 0; ok && next_item_warp(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+  for (int k = 0; ok && next_item_warp<kItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
     int first_tile;
     const int n = uniform(query_tiles(p, item.seq, item.at, first_tile));
     if (n == 0) continue;
@@ -821,6 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   if (warp == 11) {
     // --------------- work items; lse and delta of each query row; rows past the end ----------------
+    wait_for_previous();  // row_kernel
+    if (lane == 0) let_next_start();
     auto pieces = [&](int s, int& n, int& first) {
       const Seq q = load_seq(p, s);
       n = (q.nk + kKeys - 1) / kKeys;
@@ -904,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int entry = 0, uses = 0, tails = 0, tail_at = -1;
       const uint32_t bytes = static_cast<uint32_t>(128 * (D / 64) * used);
       Item item;
-      for (int k = 0; ok && next_item(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item<kItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
         int first_tile;
         const int n = query_tiles(p, item.seq, item.at, first_tile);
         if (n == 0) continue;
@@ -956,12 +972,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
     const uint32_t tm_p = tmem + L::kP + w * L::kStep + lanes, tm_ds = tmem + L::kDs + w * L::kStep + lanes;
     float f = 1.f;
-    if constexpr (!BF16) f = power_for(__uint_as_float(*gp.dout_max));
+    if constexpr (!BF16) {
+      wait_for_previous();
+      f = power_for(__uint_as_float(*gp.dout_max));
+    }
     const float2 a2 = make_float2(p.scale_log2, p.scale_log2), f2 = make_float2(f * kUnpower, f * kUnpower);
     bool ok = true;
     int step = 0;
     Item item;
-    for (int k = 0; ok && __all_sync(0xffffffffu, next_item(bars.item(), bars.item_read(), items, k, item, p.status)); ++k) {
+    for (int k = 0; ok && __all_sync(0xffffffffu, next_item<kItems>(bars.item(), bars.item_read(), items, k, item, p.status)); ++k) {
       int first_tile;
       const int n = query_tiles(p, item.seq, item.at, first_tile);
       const int key = item.at + r;
@@ -1065,7 +1084,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  wait_for_previous();  // nothing of dq_kernel's is read here; but what follows this kernel counts on its end
 }
 
 template <int D, bool BF16>
@@ -1083,20 +1101,23 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
     const int64_t rows = static_cast<int64_t>(g.f.total_q) * g.f.G;
     row_kernel<D, BF16><<<dim3(static_cast<unsigned>((rows + kPer - 1) / kPer), g.f.Hkv), kRowThreads, 0, st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = launch_dependent(kq, blocks(q_items), 1, kThreads, DqLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
-    if (e != cudaSuccess) return e;
   }
-  if (k_items == 0) return cudaSuccess;
-  if (q_items == 0) {  // what is ahead of it is not known here
+  // dq_kernel reads nothing of dkv_kernel's, whose blocks let it start once row_kernel has ended: it takes
+  // each SM as dkv_kernel leaves it.  (Without the one ahead, what is ahead is not known: a plain launch.)
+  if (k_items > 0) {
+    if (q_items > 0) {
+      e = launch_dependent(kk, blocks(k_items), 1, kThreads, DkvLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
+      if (e != cudaSuccess) return e;
+      return launch_dependent(kq, blocks(q_items), 1, kThreads, DqLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
+    }
     kk<<<blocks(k_items), kThreads, DkvLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
-    return cudaGetLastError();
+  } else if (q_items > 0) {
+    kq<<<blocks(q_items), kThreads, DqLayout<D>::kAlloc, st>>>(maps[0], maps[1], maps[2], maps[3], g);
   }
-  // dkv_kernel reads nothing of dq_kernel's, whose blocks let it start once row_kernel has ended: it takes
-  // each SM as dq_kernel leaves it.
-  return launch_dependent(kk, blocks(k_items), 1, kThreads, DkvLayout<D>::kAlloc, st, maps[0], maps[1], maps[2], maps[3], g);
+  return cudaGetLastError();
 }
 
-constexpr size_t kWordBytes = 256;  // in front: the largest |dout|
+constexpr size_t kWordBytes = 256;  // in front: the largest |dout|, the items taken
 
 size_t row_bytes(const fa_packed_backward_args* a) {
   return (static_cast<size_t>(a->total_q) * a->Hq * sizeof(float2) + 255) / 256 * 256;
@@ -1180,6 +1201,7 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   memcpy(g.dv_strides, a->dv_strides, sizeof g.dv_strides);
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   g.dout_max = reinterpret_cast<uint32_t*>(ws);
+  g.taken = reinterpret_cast<int*>(ws + 128);
   g.rows = reinterpret_cast<float2*>(ws + packed::kWordBytes);
   g.powers = reinterpret_cast<float*>(ws + packed::kWordBytes + packed::row_bytes(a));
   const bool bf16 = a->dtype == FA_BF16;

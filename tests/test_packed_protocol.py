@@ -18,7 +18,7 @@ import pytest
 
 from tests._protomodel import Bar, Hazard, Sim, TensorPipe
 
-ITEMS = 4  # places for work items on their way to the other warps
+ITEMS = 4  # places for work items on their way to the other warps (dq_kernel: one)
 
 
 def check(cond, what):
@@ -29,13 +29,13 @@ def check(cond, what):
 class Block:
     """What the three kernels share: the items, the ring, the latencies."""
 
-    def __init__(self, seed, items, slots, readers, mutate):
+    def __init__(self, seed, items, slots, readers, mutate, places=ITEMS):
         self.rng = random.Random(seed)
         self.sim = Sim(self.rng)
-        self.items, self.slots, self.mutate = items, slots, mutate
-        self.bar_item = [Bar(f"item{i}", 1) for i in range(ITEMS)]
-        self.bar_read = [Bar(f"item_read{i}", readers) for i in range(ITEMS)]
-        self.place = [None] * ITEMS
+        self.items, self.slots, self.mutate, self.places = items, slots, mutate, places
+        self.bar_item = [Bar(f"item{i}", 1) for i in range(places)]
+        self.bar_read = [Bar(f"item_read{i}", readers) for i in range(places)]
+        self.place = [None] * places
         self.pace = {}
 
     def product(self, who):
@@ -51,18 +51,18 @@ class Block:
 
     def next_item(self, k):
         """A role's wait for item k; yields, then returns the item (None: no more)."""
-        yield self.wait(self.bar_item[k % ITEMS], k // ITEMS)
-        got = self.place[k % ITEMS]
+        yield self.wait(self.bar_item[k % self.places], k // self.places)
+        got = self.place[k % self.places]
         check(got[0] == k, "an item was overwritten")
         yield self.lat(0, 0.1)
-        self.bar_read[k % ITEMS].arrive()
+        self.bar_read[k % self.places].arrive()
         return got[1]
 
     def publish(self, k):
-        if k >= ITEMS:
-            yield self.wait(self.bar_read[k % ITEMS], k // ITEMS - 1)
-        self.place[k % ITEMS] = (k, self.items[k] if k < len(self.items) else None)
-        self.bar_item[k % ITEMS].arrive()
+        if k >= self.places:
+            yield self.wait(self.bar_read[k % self.places], k // self.places - 1)
+        self.place[k % self.places] = (k, self.items[k] if k < len(self.items) else None)
+        self.bar_item[k % self.places].arrive()
 
 
 class Ring:
@@ -314,7 +314,7 @@ def test_forward_reports(mutate):
 # ------------------------------------------------------------------------------------ dq
 def queries(items, keep, passing, seed, mutate=None):
     """dq_kernel.  items: (key tiles, whether the last K tile has rows to clear)."""
-    b = Block(seed, items, keep, 4, mutate)
+    b = Block(seed, items, keep, 4, mutate, places=1)
     sim, lat, wait = b.sim, b.lat, b.wait
     k_full, k_empty = ([Bar(f"{n}{i}", 1) for i in range(keep)] for n in ("k_full", "k_empty"))
     tail = Bar("tail", 1)
