@@ -8,11 +8,13 @@
 // One CTA takes two neighbouring 128-row query tiles A and B of one kv head (a tile is 128 / G
 // query tokens x the G heads of the kv head, token by token, so rows past a sequence's end are
 // the last ones) over all their keys.  K and V tiles of 128 keys go through one shared ring and
-// serve both tiles.  Each tile has its own softmax warpgroup and its own issuing thread; tensor
+// serve both tiles.  Each tile has its own softmax warpgroup and its own issuing warp; tensor
 // memory holds O and S of both, with P in 16 bits written over S (D = 128) or beside it (D = 64).
 //
 // Why two tiles: a tile's chain S_j -> softmax -> P_j V_j -> S_{j+1} leaves the tensor cores idle
-// while its softmax runs; the other tile's products fill that time.  An issuer waits for P_j, V_j
+// while its softmax runs; the other tile's products fill that time.  The issuers take turns, for the two
+// tiles' products mixed in the pipe take longer than one after the other (a 16K-token prompt of 16 heads in 4
+// groups: 995 us without turns, 761 with them, before the steps below).  An issuer waits for P_j, V_j
 // and K_{j+1} before it issues P_j V_j and S_{j+1} together: once a thread has committed products
 // its next look at shared memory is held until they finish, so a wait between the two would
 // drain the pipe.  S_{j+1} may be issued behind P_j V_j although it overwrites P_j: products of
@@ -26,6 +28,16 @@
 // A block stays for all of its work items: while one ends, the copies and the first scores of the
 // next are under way, so that only its first item pays for set-up and an empty pipe (packed.cuh
 // says how the items are dealt out).
+//
+// Bound by the tensor cores: that prompt takes 620 to 660 us, from board to board (1670 to 1770 TFLOP/s of its
+// unmasked half, 0.87 to 0.92 of the measured bf16 rate), three quarters of all clocks with a product in the pipe and
+// the exponentials' pipe busy in 38 % (counters of four sequences of 8192 tokens).  At D = 64 by the softmax instead,
+// which is the same per score for half the products (four sequences of 4096 tokens: 150 us, 920 TFLOP/s).  Short
+// sequences pay some 3.5 us a work item for its first and last tiles (512 to 2048 tokens: 180 us, 1100 TFLOP/s).
+// Registers stand in the way of more: the softmax warps use all of their 168, and each of these spilled: runs of 32
+// scores that no row of the warp sees skipped in a masked tile (180 -> 217 us), masks as words of 32 bits (293).
+// Issuing by one thread in a loop that is not unrolled 1012 us, by a warp's elected lane from uniform registers 689 ->
+// 650, the turn given after the commits instead of among the products 626.
 //
 // Warps (384 threads): 0-3 softmax A, 4-7 softmax B, 8 copies, 9 issuer A (and tensor memory), 10
 // issuer B, 11 finds the work items and clears what a last V tile holds past its sequence's end.
@@ -641,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Parts of the rows' keys joined: lse = ln sum_s e^{lse_s}, out = sum_s e^{lse_s - lse} o_s.  A block a
+// Parts of the rows' keys joined (in 16 bits, by out's strides, and only the rows of a sequence): lse = ln sum_s e^{lse_s}, out = sum_s e^{lse_s - lse} o_s.  A block a
 // token, a warp a head at a time, eight parts on their way at once.
 constexpr int kJoinThreads = 256;
 constexpr int kMaxSplits = 32;
