@@ -7,8 +7,8 @@
 // u = b (v - a <s, k>) its new value is a s + u k, and its output (a <s, q> + u <k, q>) scale, both
 // from the row before the token, in one pass.  So the state stays in registers from the read to the
 // write however many tokens there are; the state's bytes (64 KB a head, once each way, fp32) bound
-// the call: 128 sequences of 32 heads, one token each, take 80.8 us, 6.68 TB/s, the measured copy rate;
-// one sequence 4.3 us, a launch and one trip to memory.  Eight lanes hold a row, sixteen columns each (four 16-byte pieces 128 bytes apart, so
+// the call: 128 sequences of 32 heads, one token each, take 80.1 us, 6.74 TB/s, the measured copy rate;
+// one sequence of five tokens 4.2 us, a launch, one trip to memory and five dependent tokens.  Eight lanes hold a row, sixteen columns each (four 16-byte pieces 128 bytes apart, so
 // that a row's lanes read whole lines); two dot products a row and token go through three
 // shuffles each.
 #include <math.h>
@@ -142,7 +142,8 @@ int bad(int code, const char* msg) { return set_error(code, msg); }
 template <typename T>
 cudaError_t launch(const StepParams& p, int B, cudaStream_t st) {
   // A whole state a block where that gives every SM two blocks or more, else a quarter each: the
-  // loads of a few states then come from four times as many SMs.
+  // loads of a few states then come from four times as many SMs (one sequence of 32 heads: 4.2 us for 6.5; 128
+  // sequences: 80.1 us whole, 80.9 in quarters).
   const int sms = num_sms() > 0 ? num_sms() : 152;
   if (static_cast<int64_t>(B) * p.Hv >= 2LL * sms) step_kernel<T, 4><<<dim3(1, p.Hv, B), kThreads, 0, st>>>(p);
   else step_kernel<T, 1><<<dim3(4, p.Hv, B), kThreads, 0, st>>>(p);

@@ -6,12 +6,15 @@
 // Of dy, with g = R^T dy:
 //     dw = sum over rows of g n,   dx = r (g w - n mean(g w n)) = r (g w - x r^2 mean(g w x)).
 // Both are bound by memory: the forward pass reads each row once and writes it once, the gradient
-// reads two and writes one.  Measured: 16,384 tokens of 40 heads (bf16, D = 128) 61.5 us, 5.46 TB/s, 0.82 of the copy
-// rate; the gradient of the same size 104 us with cold caches, of 2 x 1843 tokens of 32 heads (fp32, D = 64) 25.6,
-// of which 2.7 are the weights' sums and some 5 the start: what is left of both is latency, with sixteen warps an
-// SM (the forward's registers and the gradient's sums leave no room for more).  A row's units (rotary.cuh) lie in neighbouring lanes of a warp, which
-// trade their sums by shuffles; a thread takes the same unit of several heads of one token, with
-// the loads of a batch of heads in flight, and its eight sines once for all of them.
+// reads two and writes one.  A row's units, each a lane's two 16-byte pieces (rotary.cuh describes them for
+// 16-bit rows; fp32 ones are half as wide), lie in neighbouring lanes of a warp, which trade their
+// sums by shuffles; a thread takes the same unit of several heads of one token, with the loads of a
+// batch of heads in flight, and its sines once for all of them.
+//
+// Measured: 16,384 tokens of 40 heads (bf16, D = 128) 61.3 us, 5.5 TB/s, 0.82 of the copy rate; their gradient 112,
+// 4.5 TB/s; the gradient of 2 x 1843 tokens of 32 heads (fp32, D = 64) 18.0, 5.0 TB/s, of which 2.7 are the weights'
+// sums.  What is left is latency, with sixteen warps an SM: the forward's loads in flight and the gradient's sums
+// leave no registers for more (the gradient of 16-bit rows spills 20 bytes as it is).
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -39,7 +42,7 @@ struct NormParams {
   const int32_t* positions;
   const double* inv_freq;
   float amplitude, eps;
-  int H[2], T, D, half, units, rot_units;
+  int H[2], T, D, half, units, rot_units, lanes;  // lanes: of a row
   int heads_per_thread, groups[2];  // head groups of q and of k: no group holds heads of both
   int64_t tokens;
   int blocks[2];           // gradient: blocks of q, then of k
@@ -47,13 +50,60 @@ struct NormParams {
   float* dw[2];
 };
 
-// The norms' weights in shared memory, as float4 [tensor][quarter of a unit][unit], so that
+// W elements of a row, as loaded (so that a batch of loads in flight holds no more registers than its bytes).
+template <typename T, int W>
+struct Raw {
+  static constexpr int kWords = W * static_cast<int>(sizeof(T)) / 4;
+  uint32_t v[kWords];
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void load(const T* src, Raw<T, W>& r) {
+  if constexpr (Raw<T, W>::kWords == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(src);
+    r.v[0] = x.x;
+    r.v[1] = x.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < Raw<T, W>::kWords / 4; ++i) {
+      const uint4 x = reinterpret_cast<const uint4*>(src)[i];
+      r.v[4 * i] = x.x;
+      r.v[4 * i + 1] = x.y;
+      r.v[4 * i + 2] = x.z;
+      r.v[4 * i + 3] = x.w;
+    }
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void expand(const Raw<T, W>& r, float (&x)[W]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) x[i] = __uint_as_float(r.v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) unpack2<T>(r.v[i], x[2 * i], x[2 * i + 1]);
+  }
+}
+
+template <typename T, int W>
+__device__ __forceinline__ void store(T* dst, const float (&x)[W]) {
+  if constexpr (sizeof(T) == 2 && W == 4) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]));
+  } else if constexpr (W == 4) {
+    *reinterpret_cast<float4*>(dst) = make_float4(x[0], x[1], x[2], x[3]);
+  } else {
+    store8(dst, x);
+  }
+}
+
+// The norms' weights in shared memory, as float4 [tensor][four elements of a unit][unit], so that
 // neighbouring lanes read neighbouring vectors.
-template <typename T, bool INTERLEAVED>
+template <typename T, int W, bool INTERLEAVED>
 __device__ __forceinline__ void fill_weights(const NormParams& p, int which, float4* w) {
   for (int i = threadIdx.x; i < p.D; i += kThreads) {
-    const int u = i / 16, e = i % 16;
-    const int col = u < p.rot_units && !INTERLEAVED ? (e < 8 ? 8 * u + e : p.half + 8 * u + e - 8) : i;
+    const int u = i / (2 * W), e = i % (2 * W);
+    const int col = u < p.rot_units && !INTERLEAVED ? (e < W ? W * u + e : p.half + W * u + e - W) : i;
     float v = 1.f;
     if (p.w[which]) {
       if (p.w_fp32) v = static_cast<const float*>(p.w[which])[col];
@@ -63,11 +113,12 @@ __device__ __forceinline__ void fill_weights(const NormParams& p, int which, flo
   }
 }
 
-__device__ __forceinline__ void read_weights(const float4* w, int units, int u, float (&a)[8], float (&b)[8]) {
+template <int W>
+__device__ __forceinline__ void read_weights(const float4* w, int units, int u, float (&a)[W], float (&b)[W]) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < W / 2; ++q) {
     const float4 v = w[q * units + u];
-    float* to = (q < 2 ? a : b) + (q & 1) * 4;
+    float* to = (q < W / 4 ? a : b) + (q % (W / 4)) * 4;
     to[0] = v.x;
     to[1] = v.y;
     to[2] = v.z;
@@ -84,21 +135,21 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // Forward.  LANES: lanes of a row, the least power of two that holds its units.  Two blocks an SM that stay: 61.5 us
 // for that prompt; a block a task, three an SM, 68; batches of eight heads 67.5, three blocks with batches of two 63.6.
-template <typename T, int LANES, bool INTERLEAVED>
+template <typename T, int W, int LANES, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormParams p) {
   __shared__ int64_t steps[kMaxRot / 2];
   __shared__ float4 weights[2][kMaxD / 4];
-  fill_weights<T, INTERLEAVED>(p, 0, weights[0]);
-  fill_weights<T, INTERLEAVED>(p, 1, weights[1]);
+  fill_weights<T, W, INTERLEAVED>(p, 0, weights[0]);
+  fill_weights<T, W, INTERLEAVED>(p, 1, weights[1]);
   fill_steps(steps, p.inv_freq, p.half);
   constexpr int kSlots = kThreads / LANES;
   const int u = threadIdx.x % LANES, slot = threadIdx.x / LANES;
   const bool unit = u < p.units, rotated = u < p.rot_units;
-  const int c0 = rotated && !INTERLEAVED ? 8 * u : 16 * u;
-  const int c1 = rotated && !INTERLEAVED ? p.half + 8 * u : 16 * u + 8;
+  const int c0 = rotated && !INTERLEAVED ? W * u : 2 * W * u;
+  const int c1 = rotated && !INTERLEAVED ? p.half + W * u : 2 * W * u + W;
   const float inv_d = 1.f / p.D;
   const int64_t tasks = p.tokens * (p.groups[0] + p.groups[1]), step = static_cast<int64_t>(gridDim.x) * kSlots;
-  constexpr int kBatch = sizeof(T) == 4 ? 2 : 4;  // heads whose loads are issued together
+  constexpr int kBatch = W * sizeof(T) == 16 ? 4 : 2;  // heads whose loads are issued together
   for (int64_t base = static_cast<int64_t>(blockIdx.x) * kSlots; base < tasks; base += step) {
     const int64_t task = base + slot;  // the loop's length is the block's: shuffles
     // every lane of a warp takes part in the shuffles, with nothing to load where it has no unit
@@ -109,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormPara
     const int h0 = (which ? group - p.groups[0] : group) * p.heads_per_thread;
     const int h1 = live ? min(h0 + p.heads_per_thread, which ? p.H[1] : p.H[0]) : 0;
     const int64_t b = token / p.T, t = token - b * p.T;
-    Turn turn;
+    Angles<W> turn;
     if (live && rotated) fill_turn(turn, steps, u, p.positions[token], p.amplitude, false);
     const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]);
     T* y = static_cast<T*>(which ? p.y[1] : p.y[0]);
@@ -117,38 +168,38 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormPara
     y += which ? b * p.ys[1][0] + t * p.ys[1][2] : b * p.ys[0][0] + t * p.ys[0][2];
     const int64_t xh = which ? p.xs[1][1] : p.xs[0][1], yh = which ? p.ys[1][1] : p.ys[0][1];
     for (int j = 0; j < p.heads_per_thread; j += kBatch) {  // the same count for every lane: shuffles
-      Raw8<T> ra[kBatch], rb[kBatch];
+      Raw<T, W> ra[kBatch], rb[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         if (h0 + j + i >= h1) continue;
         const T* src = x + (h0 + j + i) * xh;
-        ra[i] = load_raw8<T>(src + c0);
-        rb[i] = load_raw8<T>(src + c1);
+        load<T, W>(src + c0, ra[i]);
+        load<T, W>(src + c1, rb[i]);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const bool ok = h0 + j + i < h1;
-        float a[8] = {}, c[8] = {};
+        float a[W] = {}, c[W] = {};
         if (ok) {
-          expand8<T>(ra[i], a);
-          expand8<T>(rb[i], c);
+          expand<T, W>(ra[i], a);
+          expand<T, W>(rb[i], c);
         }
         float sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum = fmaf(a[e], a[e], fmaf(c[e], c[e], sum));
+        for (int e = 0; e < W; ++e) sum = fmaf(a[e], a[e], fmaf(c[e], c[e], sum));
         const float r = rsqrtf(row_sum<LANES>(sum) * inv_d + p.eps);
         if (!ok) continue;
-        float wa[8], wc[8];
-        read_weights(weights[which], p.units, u, wa, wc);
+        float wa[W], wc[W];
+        read_weights<W>(weights[which], p.units, u, wa, wc);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < W; ++e) {
           a[e] *= r * wa[e];
           c[e] *= r * wc[e];
         }
         if (rotated) rotate<INTERLEAVED>(turn, a, c);
         T* dst = y + (h0 + j + i) * yh;
-        store8(dst + c0, a);
-        store8(dst + c1, c);
+        store<T, W>(dst + c0, a);
+        store<T, W>(dst + c1, c);
       }
     }
   }
@@ -156,23 +207,23 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormPara
 
 // Gradient.  A block belongs to q or to k and walks over (token, head group) tasks; a thread adds
 // its columns' part of the weight's gradient in registers, the block its rows' parts in a fixed
-// order, and weight_sum_kernel the blocks': no atomics.  (The next batch's rows loaded ahead: 78 us for 25.6,
-// the registers spill.)
-template <typename T, int LANES, bool INTERLEAVED>
+// order, and weight_sum_kernel the blocks': no atomics.  (The next batch's rows loaded ahead made the registers
+// spill: three times as long.)
+template <typename T, int W, int LANES, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const NormParams p) {
   let_next_start();
   __shared__ int64_t steps[kMaxRot / 2];
   __shared__ float4 weights[kMaxD / 4];
   constexpr int kSlots = kThreads / LANES;
-  __shared__ float sums[kSlots * LANES * 16];  // [slot][unit's 16 columns]
+  __shared__ float sums[kSlots * LANES * 2 * W];  // [slot][unit's columns]
   const int which = static_cast<int>(blockIdx.x) < p.blocks[0] ? 0 : 1;
   const int block = which ? blockIdx.x - p.blocks[0] : blockIdx.x;
-  fill_weights<T, INTERLEAVED>(p, which, weights);
+  fill_weights<T, W, INTERLEAVED>(p, which, weights);
   fill_steps(steps, p.inv_freq, p.half);
   const int u = threadIdx.x % LANES, slot = threadIdx.x / LANES;
   const bool unit = u < p.units, rotated = u < p.rot_units;
-  const int c0 = rotated && !INTERLEAVED ? 8 * u : 16 * u;
-  const int c1 = rotated && !INTERLEAVED ? p.half + 8 * u : 16 * u + 8;
+  const int c0 = rotated && !INTERLEAVED ? W * u : 2 * W * u;
+  const int c1 = rotated && !INTERLEAVED ? p.half + W * u : 2 * W * u + W;
   const int H = which ? p.H[1] : p.H[0];
   const int64_t tasks = p.tokens * (which ? p.groups[1] : p.groups[0]);
   const int64_t step = static_cast<int64_t>(which ? p.blocks[1] : p.blocks[0]) * kSlots;
@@ -183,8 +234,8 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const Nor
   const int64_t db = which ? p.ds[1][0] : p.ds[0][0], dh = which ? p.ds[1][1] : p.ds[0][1], dt = which ? p.ds[1][2] : p.ds[0][2];
   const int64_t yb = which ? p.ys[1][0] : p.ys[0][0], yh = which ? p.ys[1][1] : p.ys[0][1], yt = which ? p.ys[1][2] : p.ys[0][2];
   const float inv_d = 1.f / p.D;
-  float dwa[8] = {}, dwc[8] = {};
-  constexpr int kBatch = sizeof(T) == 4 ? 1 : 2;  // heads whose loads are issued together
+  float dwa[W] = {}, dwc[W] = {};
+  constexpr int kBatch = W * sizeof(T) == 16 ? 2 : 1;  // heads whose loads are issued together
   for (int64_t base = static_cast<int64_t>(block) * kSlots; base < tasks; base += step) {
     const int64_t task = base + slot;  // the loop's length is the block's: shuffles
     const bool live = unit && task < tasks;
@@ -192,38 +243,38 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const Nor
     const int64_t token = live ? task - group * p.tokens : 0;
     const int64_t b = token / p.T, t = token - b * p.T;
     const int h0 = group * p.heads_per_thread, h1 = live ? min(h0 + p.heads_per_thread, H) : 0;
-    Turn turn;
+    Angles<W> turn;
     if (live && rotated) fill_turn(turn, steps, u, p.positions[token], p.amplitude, true);
     const T* x = x0 + b * xb + t * xt;
     const T* d = d0 + b * db + t * dt;
     T* y = y0 + b * yb + t * yt;
     for (int j = 0; j < p.heads_per_thread; j += kBatch) {
-      Raw8<T> ra[kBatch], rb[kBatch], rg[kBatch], rh[kBatch];
+      Raw<T, W> ra[kBatch], rb[kBatch], rg[kBatch], rh[kBatch];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + j + i;
         if (h >= h1) continue;
-        ra[i] = load_raw8<T>(x + h * xh + c0);
-        rb[i] = load_raw8<T>(x + h * xh + c1);
-        rg[i] = load_raw8<T>(d + h * dh + c0);
-        rh[i] = load_raw8<T>(d + h * dh + c1);
+        load<T, W>(x + h * xh + c0, ra[i]);
+        load<T, W>(x + h * xh + c1, rb[i]);
+        load<T, W>(d + h * dh + c0, rg[i]);
+        load<T, W>(d + h * dh + c1, rh[i]);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int h = h0 + j + i;
         const bool ok = h < h1;
-        float a[8] = {}, c[8] = {}, g[8] = {}, f[8] = {}, wa[8] = {}, wc[8] = {};
+        float a[W] = {}, c[W] = {}, g[W] = {}, f[W] = {}, wa[W] = {}, wc[W] = {};
         if (ok) {
-          expand8<T>(ra[i], a);
-          expand8<T>(rb[i], c);
-          expand8<T>(rg[i], g);
-          expand8<T>(rh[i], f);
+          expand<T, W>(ra[i], a);
+          expand<T, W>(rb[i], c);
+          expand<T, W>(rg[i], g);
+          expand<T, W>(rh[i], f);
           if (rotated) rotate<INTERLEAVED>(turn, g, f);
-          read_weights(weights, p.units, u, wa, wc);
+          read_weights<W>(weights, p.units, u, wa, wc);
         }
         float xx = 0.f, gx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < W; ++e) {
           xx = fmaf(a[e], a[e], fmaf(c[e], c[e], xx));
           gx = fmaf(g[e] * wa[e], a[e], fmaf(f[e] * wc[e], c[e], gx));
         }
@@ -233,29 +284,29 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const Nor
         const float r = rsqrtf(xx * inv_d + p.eps);
         const float back = r * r * gx * inv_d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < W; ++e) {
           dwa[e] = fmaf(g[e], a[e] * r, dwa[e]);
           dwc[e] = fmaf(f[e], c[e] * r, dwc[e]);
           a[e] = r * (g[e] * wa[e] - a[e] * back);
           c[e] = r * (f[e] * wc[e] - c[e] * back);
         }
-        store8(y + h * yh + c0, a);
-        store8(y + h * yh + c1, c);
+        store<T, W>(y + h * yh + c0, a);
+        store<T, W>(y + h * yh + c1, c);
       }
     }
   }
-  float* mine = sums + (slot * LANES + u) * 16;
+  float* mine = sums + (slot * LANES + u) * 2 * W;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < W; ++e) {
     mine[e] = dwa[e];
-    mine[8 + e] = dwc[e];
+    mine[W + e] = dwc[e];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < p.D; i += kThreads) {
-    const int un = i / 16, e = i % 16;
-    const int col = un < p.rot_units && !INTERLEAVED ? (e < 8 ? 8 * un + e : p.half + 8 * un + e - 8) : i;
+    const int un = i / (2 * W), e = i % (2 * W);
+    const int col = un < p.rot_units && !INTERLEAVED ? (e < W ? W * un + e : p.half + W * un + e - W) : i;
     float v = 0.f;
-    for (int s = 0; s < kSlots; ++s) v += sums[s * LANES * 16 + i];
+    for (int s = 0; s < kSlots; ++s) v += sums[s * LANES * 2 * W + i];
     p.partial[static_cast<int64_t>(blockIdx.x) * p.D + col] = v;
   }
 }
@@ -345,15 +396,22 @@ int check_tables(const char* who, const NormCall& a) {
 
 int sms() { return num_sms() > 0 ? num_sms() : 152; }
 
-int row_lanes(int D) {
+// Width of half a unit: 16 bytes, for fp32 rows that a warp holds that way.  (2 x 1843 tokens of 32 heads, D = 64: fp32
+// with eight 26.0 us for 18.0 with four, forward 14.7 for 11.0; 16,384 tokens of 40 heads, D = 128: bf16 with eight 112
+// for 117 with four, forward 64 for 68.)
+int width(const NormCall& a) { return a.dtype == FA_FP32 && a.D <= 256 ? 4 : 8; }
+
+int row_lanes(int D, int w) {
   int lanes = 1;
-  while (lanes * 16 < D) lanes *= 2;
+  while (lanes * 2 * w < D) lanes *= 2;
   return lanes;
 }
 
 // Heads a thread takes: as many as eight, so that its eight sines serve them all, but no more than leave every SM 512
-// threads (128 tokens of 40 heads: 4.9 us with one a thread; 16,384 tokens: 61.5 with eight, 63.8 with sixteen).
+// threads (128 tokens of 40 heads: 4.9 us with one a thread, 6.2 with eight; 16,384 tokens: 61.3 with eight, 67 with
+// four, 176 with one, 63.6 with sixteen).
 void fill_params(NormParams& p, const NormCall& a) {
+  const int w = width(a), lanes = row_lanes(a.D, w);
   p.w[0] = a.q_weight;
   p.w[1] = a.k_weight;
   p.w_fp32 = a.weight_dtype == FA_FP32;
@@ -366,11 +424,12 @@ void fill_params(NormParams& p, const NormCall& a) {
   p.T = a.T;
   p.D = a.D;
   p.half = a.rot_dim / 2;
-  p.units = a.D / 16;
-  p.rot_units = a.rot_dim / 16;
+  p.lanes = lanes;
+  p.units = a.D / (2 * w);
+  p.rot_units = a.rot_dim / (2 * w);
   p.tokens = static_cast<int64_t>(a.B) * a.T;
   int hpt = 8;
-  while (hpt > 1 && p.tokens * row_lanes(a.D) * ((a.Hq + a.Hk + hpt - 1) / hpt) < 512LL * sms()) hpt /= 2;
+  while (hpt > 1 && p.tokens * lanes * ((a.Hq + a.Hk + hpt - 1) / hpt) < 512LL * sms()) hpt /= 2;
   p.heads_per_thread = hpt;
   p.groups[0] = (a.Hq + hpt - 1) / hpt;
   p.groups[1] = (a.Hk + hpt - 1) / hpt;
@@ -378,7 +437,7 @@ void fill_params(NormParams& p, const NormCall& a) {
 
 // Blocks of the gradient for q and for k: two an SM at most, shared out by their rows.
 void grad_blocks(NormParams& p) {
-  const int64_t slots = kThreads / row_lanes(p.D);
+  const int64_t slots = kThreads / p.lanes;
   const int64_t want[2] = {(p.tokens * p.groups[0] + slots - 1) / slots, (p.tokens * p.groups[1] + slots - 1) / slots};
   const int64_t most = 2LL * sms();
   for (int i = 0; i < 2; ++i) {
@@ -388,12 +447,12 @@ void grad_blocks(NormParams& p) {
   }
 }
 
-template <typename T, int LANES>
+template <typename T, int W, int LANES>
 cudaError_t launch(const NormParams& p, bool interleaved, bool grad, cudaStream_t st) {
   if (grad) {
     const unsigned n = p.blocks[0] + p.blocks[1];
-    if (interleaved) norm_rotary_grad_kernel<T, LANES, true><<<n, kThreads, 0, st>>>(p);
-    else norm_rotary_grad_kernel<T, LANES, false><<<n, kThreads, 0, st>>>(p);
+    if (interleaved) norm_rotary_grad_kernel<T, W, LANES, true><<<n, kThreads, 0, st>>>(p);
+    else norm_rotary_grad_kernel<T, W, LANES, false><<<n, kThreads, 0, st>>>(p);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !(p.dw[0] || p.dw[1])) return e;
     return launch_dependent(weight_sum_kernel, (p.D + 31) / 32, 2, kSumThreads, 0, st, p);
@@ -402,32 +461,35 @@ cudaError_t launch(const NormParams& p, bool interleaved, bool grad, cudaStream_
     const int64_t threads = p.tokens * (p.groups[0] + p.groups[1]) * LANES, most = 2LL * sms();
     const int64_t want = (threads + kThreads - 1) / kThreads;
     const unsigned n = static_cast<unsigned>(want < most ? want : most);
-    if (interleaved) norm_rotary_kernel<T, LANES, true><<<n, kThreads, 0, st>>>(p);
-    else norm_rotary_kernel<T, LANES, false><<<n, kThreads, 0, st>>>(p);
+    if (interleaved) norm_rotary_kernel<T, W, LANES, true><<<n, kThreads, 0, st>>>(p);
+    else norm_rotary_kernel<T, W, LANES, false><<<n, kThreads, 0, st>>>(p);
   }
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, int W>
 cudaError_t launch_lanes(const NormParams& p, bool interleaved, bool grad, cudaStream_t st) {
-  switch (row_lanes(p.D)) {
-    case 1: return launch<T, 1>(p, interleaved, grad, st);
-    case 2: return launch<T, 2>(p, interleaved, grad, st);
-    case 4: return launch<T, 4>(p, interleaved, grad, st);
-    case 8: return launch<T, 8>(p, interleaved, grad, st);
-    case 16: return launch<T, 16>(p, interleaved, grad, st);
-    default: return launch<T, 32>(p, interleaved, grad, st);
+  if constexpr (W == 8 && sizeof(T) == 4) return launch<T, W, 32>(p, interleaved, grad, st);  // (D > 256 alone)
+  if constexpr (W == 8 && sizeof(T) == 2)
+    if (p.lanes == 1) return launch<T, W, 1>(p, interleaved, grad, st);  // (D = 16; of fp32 two lanes)
+  switch (p.lanes) {
+    case 2: return launch<T, W, 2>(p, interleaved, grad, st);
+    case 4: return launch<T, W, 4>(p, interleaved, grad, st);
+    case 8: return launch<T, W, 8>(p, interleaved, grad, st);
+    case 16: return launch<T, W, 16>(p, interleaved, grad, st);
+    default: return launch<T, W, 32>(p, interleaved, grad, st);
   }
 }
 
 int launch_type(const char* who, const NormParams& p, const NormCall& a, bool interleaved, bool grad, void* stream) {
-  if (p.tokens * (p.groups[0] + p.groups[1]) * row_lanes(p.D) > 2147483647LL * kThreads)
+  if (p.tokens * (p.groups[0] + p.groups[1]) * p.lanes > 2147483647LL * kThreads)
     return bad(FA_ERR_UNSUPPORTED, who, "too many rows for one launch");
   if (!device_status_ptr()) return bad(FA_ERR_CUDA, who, "no usable CUDA device");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a.dtype == FA_BF16   ? launch_lanes<__nv_bfloat16>(p, interleaved, grad, st)
-                        : a.dtype == FA_FP16 ? launch_lanes<__half>(p, interleaved, grad, st)
-                                             : launch_lanes<float>(p, interleaved, grad, st);
+  const cudaError_t e = a.dtype == FA_BF16   ? launch_lanes<__nv_bfloat16, 8>(p, interleaved, grad, st)
+                        : a.dtype == FA_FP16 ? launch_lanes<__half, 8>(p, interleaved, grad, st)
+                        : width(a) == 4      ? launch_lanes<float, 4>(p, interleaved, grad, st)
+                                             : launch_lanes<float, 8>(p, interleaved, grad, st);
   return e == cudaSuccess ? FA_OK : bad(FA_ERR_CUDA, who, cudaGetErrorString(e));
 }
 

@@ -85,30 +85,33 @@ __device__ __forceinline__ void fill_steps(int64_t* steps, const double* inv_fre
   __syncthreads();
 }
 
-// The eight angles of a thread's unit.
-struct Turn {
-  float c[8], s[8];
+// The angles of a thread's unit: W pairs, eight here (a kernel of its own may cut rows into smaller units).
+template <int W>
+struct Angles {
+  float c[W], s[W];
 };
+using Turn = Angles<8>;
 
-// Unit u of the rotated part: half layout pairs (8u + i, half + 8u + i), pair index 8u + i;
-// interleaved pairs (16u + 2i, 16u + 2i + 1), the same pair index.
-__device__ __forceinline__ void fill_turn(Turn& t, const int64_t* steps, int u, int pos,
+// Unit u of the rotated part: half layout pairs (W u + i, half + W u + i), pair index W u + i;
+// interleaved pairs (2 W u + 2i, 2 W u + 2i + 1), the same pair index.
+template <int W>
+__device__ __forceinline__ void fill_turn(Angles<W>& t, const int64_t* steps, int u, int pos,
                                           float amplitude, bool transpose) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    angle(steps[8 * u + i], pos, amplitude, t.c[i], t.s[i]);
+  for (int i = 0; i < W; ++i) {
+    angle(steps[W * u + i], pos, amplitude, t.c[i], t.s[i]);
     if (transpose) t.s[i] = -t.s[i];
   }
 }
 
-// Rotates a unit's 16 elements: half layout a = first members, b = second; interleaved a, b =
-// the 16 consecutive elements.
-template <bool INTERLEAVED>
-__device__ __forceinline__ void rotate(const Turn& t, float (&a)[8], float (&b)[8]) {
+// Rotates a unit's 2 W elements: half layout a = first members, b = second; interleaved a, b =
+// the 2 W consecutive elements.
+template <bool INTERLEAVED, int W>
+__device__ __forceinline__ void rotate(const Angles<W>& t, float (&a)[W], float (&b)[W]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float& x = INTERLEAVED ? (i < 4 ? a[(2 * i) & 7] : b[(2 * i) & 7]) : a[i];
-    float& y = INTERLEAVED ? (i < 4 ? a[(2 * i + 1) & 7] : b[(2 * i + 1) & 7]) : b[i];
+  for (int i = 0; i < W; ++i) {
+    float& x = INTERLEAVED ? (2 * i < W ? a[(2 * i) % W] : b[(2 * i) % W]) : a[i];
+    float& y = INTERLEAVED ? (2 * i < W ? a[(2 * i + 1) % W] : b[(2 * i + 1) % W]) : b[i];
     const float rx = x * t.c[i] - y * t.s[i];
     const float ry = y * t.c[i] + x * t.s[i];
     x = rx;
