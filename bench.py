@@ -78,9 +78,13 @@ KERNEL_SOURCES = {
     "decode": ("decode.cu", "sm103.cuh", "internal.h"),
     "mla": ("mla.cu", "sm103.cuh", "internal.h"),
     "gated_delta": ("gated_delta.cu", "sm103.cuh", "internal.h"),
-    "cache": ("cache.cu", "cache.cuh", "sm103.cuh", "internal.h"),
+    "cache": ("cache.cu", "cache.cuh", "rotary.cuh", "sm103.cuh", "internal.h"),
     "tree": ("tree.cu", "tree_rows.cu", "tree.cuh", "cache.cuh", "prefill_common.cuh", "sm103.cuh",
              "internal.h"),
+    "packed": ("packed.cu", "packed_grad.cu", "packed.cuh", "dependent.cuh", "prefill_common.cuh", "sm103.cuh",
+               "internal.h"),
+    "norm_rotary": ("norm_rotary.cu", "rotary.cuh", "cache.cuh", "dependent.cuh", "sm103.cuh", "internal.h"),
+    "delta_step": ("delta_step.cu", "cache.cuh", "sm103.cuh", "internal.h"),
 }
 
 
