@@ -76,6 +76,10 @@ CASES = [
     (1, 8, 8, 9, 32, 16, True, HF, HF, 7, 0.0),             # no epsilon
     (1, 40, 8, 700, 128, 128, False, BF, BF, 0, 1e-6),      # several heads a thread
     (2, 17, 3, 301, 64, 32, False, SF, SF, 5, 1e-6),
+    (1, 3, 2, 5, 256, 128, True, SF, SF, 77, 1e-6),         # fp32: the widest rows in units of eight columns
+    (1, 3, 2, 5, 272, 160, False, SF, SF, 77, 1e-6),        # and in units of sixteen
+    (2, 2, 1, 3, 512, 512, True, SF, SF, 1 << 16, 1e-6),
+    (1, 2, 3, 9, 16, 16, True, HF, HF, 11, 1e-6),           # a row a lane
 ]
 
 

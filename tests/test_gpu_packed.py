@@ -378,6 +378,55 @@ def test_broken_offsets_are_reported():
     assert fa.fa_get_device_status() == fa.FA_OK
 
 
+def test_broken_offsets_with_parts():
+    """Rows of a sequence that is taken as empty stay as they were, whatever the workspace holds."""
+    c = Case([64, 64], 2, 2, 64, BF, seed=17)
+    q, k, v = c.gpu()
+    for offsets, first, end in (([0, 64, 32], 0, 64), ([-5, 64, 128], 64, 128), ([0, 64, 129], 0, 64),
+                                ([0, 2 ** 31 - 1, 128], 0, 0)):
+        cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+        out = torch.full((128, 2, 64), 7.0, dtype=BF, device="cuda")
+        lse = torch.full((128, 2), 7.0, device="cuda")
+        ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")  # NaN
+        fa.fa_prefill_packed(q, k, v, cu, num_splits=2, out=out, lse=lse, workspace=ws)
+        assert fa.fa_get_device_status() == fa.FA_ERR_BOUNDS
+        left = torch.ones(128, dtype=torch.bool, device="cuda")
+        left[first:end] = False
+        assert (out[left] == 7).all() and (lse[left] == 7).all()
+        assert not (out[first:end] == 7).all() if end > first else True
+        assert out.isfinite().all() and lse.isfinite().all()
+    assert fa.fa_get_device_status() == fa.FA_OK
+
+
+def test_parts_on_two_streams_at_once():
+    """Two calls that overlap, a workspace each: the bits of the same calls alone."""
+    cases = [Case([40, 7], 8, 2, 128, BF, klens=[6000, 3000], seed=s) for s in (6, 7)]
+    ins = [(*c.gpu(), *c.offsets()) for c in cases]
+    alone = [fa.fa_prefill_packed(*x, num_splits=6) for x in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    for _ in range(3):
+        got = [fa.fa_prefill_packed(*x, num_splits=6, stream=s) for x, s in zip(ins, streams)]
+        torch.cuda.synchronize()
+        for (a, la), (b, lb) in zip(alone, got):
+            assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+def test_parts_and_causal_rows_in_front():
+    """Infinite scores and NaN in keys that a row's part does not see take no part."""
+    c = Case([300], 4, 2, 64, HF, klens=[900], seed=8)
+    q, k, v = c.gpu()
+    k, v = k.clone(), v.clone()
+    k[700:] = float("inf")  # seen by the rows from 100 on alone
+    out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), num_splits=7)
+    one, lone = fa.fa_prefill_packed(q, k, v, *c.offsets(), num_splits=1)
+    torch.cuda.synchronize()
+    ref_rows = next(c.want(True, 1.0 / 8.0))[2]
+    for got, l in ((out, lse), (one, lone)):
+        ref.check("out", got[:100], *(t[:100] for t in ref_rows["out"]))
+        ref.check("lse", l[:100], *(t[:100] for t in ref_rows["lse"]))
+
+
 def test_no_rows():
     empty = torch.empty(0, 4, 64, dtype=BF, device="cuda")
     cu = torch.zeros(3, dtype=torch.int32, device="cuda")
