@@ -11,10 +11,10 @@
 // sums by shuffles; a thread takes the same unit of several heads of one token, with the loads of a
 // batch of heads in flight, and its sines once for all of them.
 //
-// Measured: 16,384 tokens of 40 heads (bf16, D = 128) 61.3 us, 5.5 TB/s, 0.82 of the copy rate; their gradient 112,
-// 4.5 TB/s; the gradient of 2 x 1843 tokens of 32 heads (fp32, D = 64) 18.0, 5.0 TB/s, of which 2.7 are the weights'
+// Measured: 16,384 tokens of 40 heads (bf16, D = 128) 60.2 us, 5.6 TB/s, 0.83 of the copy rate; their gradient 108,
+// 4.6 TB/s; the gradient of 2 x 1843 tokens of 32 heads (fp32, D = 64) 17.9, 5.1 TB/s, of which 2.7 are the weights'
 // sums.  What is left is latency, with sixteen warps an SM: the forward's loads in flight and the gradient's sums
-// leave no registers for more (the gradient of 16-bit rows spills 20 bytes as it is).
+// leave no registers for more (the gradient of 16-bit rows spills a few bytes as it is).  Sums and products go two elements an instruction.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -126,6 +126,26 @@ __device__ __forceinline__ void read_weights(const float4* w, int units, int u, 
   }
 }
 
+// Two elements at a time.
+__device__ __forceinline__ float2 two(const float* x) { return make_float2(x[0], x[1]); }
+__device__ __forceinline__ void put(float* x, float2 v) {
+  x[0] = v.x;
+  x[1] = v.y;
+}
+
+// A unit turned, pairs (a[i], b[i]) of the half layout two at a time.  (In the forward pass over 16-bit rows alone: 16,384
+// tokens of 40 heads, D = 128, 60.2 us for 61.2; fp32 rows 116 for 106, the gradient of 16-bit ones, whose registers
+// spill, 127 for 108.)
+template <int W>
+__device__ __forceinline__ void turn_halves(const Angles<W>& t, float (&a)[W], float (&b)[W]) {
+#pragma unroll
+  for (int i = 0; i < W; i += 2) {
+    const float2 x = two(a + i), y = two(b + i), c = two(t.c + i), s = two(t.s + i);
+    put(a + i, __ffma2_rn(x, c, __fmul2_rn(y, make_float2(-s.x, -s.y))));
+    put(b + i, __ffma2_rn(y, c, __fmul2_rn(x, s)));
+  }
+}
+
 template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -184,19 +204,22 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_kernel(const NormPara
           expand<T, W>(ra[i], a);
           expand<T, W>(rb[i], c);
         }
-        float sum = 0.f;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < W; ++e) sum = fmaf(a[e], a[e], fmaf(c[e], c[e], sum));
-        const float r = rsqrtf(row_sum<LANES>(sum) * inv_d + p.eps);
+        for (int e = 0; e < W; e += 2) sum = __ffma2_rn(two(a + e), two(a + e), __ffma2_rn(two(c + e), two(c + e), sum));
+        const float r = rsqrtf(row_sum<LANES>(sum.x + sum.y) * inv_d + p.eps);
         if (!ok) continue;
         float wa[W], wc[W];
         read_weights<W>(weights[which], p.units, u, wa, wc);
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          a[e] *= r * wa[e];
-          c[e] *= r * wc[e];
+        for (int e = 0; e < W; e += 2) {
+          put(a + e, __fmul2_rn(two(a + e), __fmul2_rn(make_float2(r, r), two(wa + e))));
+          put(c + e, __fmul2_rn(two(c + e), __fmul2_rn(make_float2(r, r), two(wc + e))));
         }
-        if (rotated) rotate<INTERLEAVED>(turn, a, c);
+        if (rotated) {
+          if constexpr (!INTERLEAVED && sizeof(T) == 2) turn_halves(turn, a, c);
+          else rotate<INTERLEAVED>(turn, a, c);
+        }
         T* dst = y + (h0 + j + i) * yh;
         store<T, W>(dst + c0, a);
         store<T, W>(dst + c1, c);
@@ -272,23 +295,24 @@ __global__ void __launch_bounds__(kThreads, 2) norm_rotary_grad_kernel(const Nor
           if (rotated) rotate<INTERLEAVED>(turn, g, f);
           read_weights<W>(weights, p.units, u, wa, wc);
         }
-        float xx = 0.f, gx = 0.f;
+        float2 x2 = make_float2(0.f, 0.f), g2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          xx = fmaf(a[e], a[e], fmaf(c[e], c[e], xx));
-          gx = fmaf(g[e] * wa[e], a[e], fmaf(f[e] * wc[e], c[e], gx));
+        for (int e = 0; e < W; e += 2) {
+          x2 = __ffma2_rn(two(a + e), two(a + e), __ffma2_rn(two(c + e), two(c + e), x2));
+          g2 = __ffma2_rn(__fmul2_rn(two(g + e), two(wa + e)), two(a + e),
+                          __ffma2_rn(__fmul2_rn(two(f + e), two(wc + e)), two(c + e), g2));
         }
-        xx = row_sum<LANES>(xx);
-        gx = row_sum<LANES>(gx);
+        const float xx = row_sum<LANES>(x2.x + x2.y), gx = row_sum<LANES>(g2.x + g2.y);
         if (!ok) continue;
         const float r = rsqrtf(xx * inv_d + p.eps);
-        const float back = r * r * gx * inv_d;
+        const float back = -r * r * gx * inv_d;
+        const float2 r2 = make_float2(r, r), back2 = make_float2(back, back);
 #pragma unroll
-        for (int e = 0; e < W; ++e) {
-          dwa[e] = fmaf(g[e], a[e] * r, dwa[e]);
-          dwc[e] = fmaf(f[e], c[e] * r, dwc[e]);
-          a[e] = r * (g[e] * wa[e] - a[e] * back);
-          c[e] = r * (f[e] * wc[e] - c[e] * back);
+        for (int e = 0; e < W; e += 2) {
+          put(dwa + e, __ffma2_rn(two(g + e), __fmul2_rn(two(a + e), r2), two(dwa + e)));
+          put(dwc + e, __ffma2_rn(two(f + e), __fmul2_rn(two(c + e), r2), two(dwc + e)));
+          put(a + e, __fmul2_rn(r2, __ffma2_rn(two(a + e), back2, __fmul2_rn(two(g + e), two(wa + e)))));
+          put(c + e, __fmul2_rn(r2, __ffma2_rn(two(c + e), back2, __fmul2_rn(two(f + e), two(wc + e)))));
         }
         store<T, W>(y + h * yh + c0, a);
         store<T, W>(y + h * yh + c1, c);
