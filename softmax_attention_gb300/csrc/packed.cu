@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       n = (q.nq + width - 1) / width;
       first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / width;
     };
-    const Finder finder(p.B, !p.causal, pieces);
+    Finder finder(p.B, !p.causal, pieces);
     int entries = 0;                // ring entries of the items so far
     uint32_t tail_phase = 0;        // of each slot's tail barrier, a bit
     int clear_at = -1, clear_row = 0;  // the item before: entry of its last V tile, first row to clear

@@ -63,7 +63,7 @@ __device__ __forceinline__ Seq load_seq(const Params& p, int b) {
 // short ones; nothing but the order depends on it.  Each block finds its pieces by itself: a binary
 // search for a rank's level, a warp's lanes holding up to four sequences each, a few hundred
 // clocks in a warp with nothing else to do; no list, no kernel before this one.  Past 128 sequences
-// the pieces are taken sequence by sequence.
+// the pieces are taken sequence by sequence, each search going on where the block's last one ended.
 class Finder {
  public:
   template <typename Items>
@@ -78,9 +78,9 @@ class Finder {
     top_ = __reduce_max_sync(0xffffffffu, top_);
   }
 
-  // The piece of a rank: sequence b and index t; b = -1 past the end.  The whole warp calls.
+  // The piece of a rank, larger from call to call: sequence b and index t; b = -1 past the end.  The whole warp calls.
   template <typename Items>
-  __device__ __forceinline__ void find(int rank, Items items, int& b, int& t) const {
+  __device__ __forceinline__ void find(int rank, Items items, int& b, int& t) {
     const int lane = threadIdx.x & 31;
     b = -1;
     t = 0;
@@ -101,13 +101,15 @@ class Finder {
       }
       return;
     }
-    for (int base = 0; base < B_; base += 32) {
+    for (; base_ < B_; base_ += 32) {
       int n = 0, first = 0;
-      if (base + lane < B_) items(base + lane, n, first);
-      if (pick(rank, before, n, base, true, 0, b, t)) {
-        t = __shfl_sync(0xffffffffu, n, b - base) - 1 - t;  // the longest first
+      if (base_ + lane < B_) items(base_ + lane, n, first);
+      before = before_;
+      if (pick(rank, before, n, base_, true, 0, b, t)) {
+        t = __shfl_sync(0xffffffffu, n, b - base_) - 1 - t;  // the longest first
         return;
       }
+      before_ = before;
     }
   }
 
@@ -147,6 +149,7 @@ class Finder {
   bool flat_;
   int top_;
   int n_[kHeld], first_[kHeld];  // of sequences lane, lane + 32, ...
+  int base_ = 0, before_ = 0;    // more sequences than that: those looked at last, and the pieces in front of them
 };
 
 // The k-th rank of this block, of `blocks` that deal them out there and back.

@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       n = (q.nq + p.q_per_tile - 1) / p.q_per_tile;
       first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / p.q_per_tile;
     };
-    const Finder finder(p.B, !p.causal, pieces);
+    Finder finder(p.B, !p.causal, pieces);
     int tiles = 0, tails = 0;          // key tiles of the items so far; K tiles cleared
     int clear_at = -1, clear_row = 0;  // the item before: its last key tile, first row to clear
     bool ok = true, more = true;
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       n = (q.nk + kKeys - 1) / kKeys;
       first = p.causal ? 0 : q.nq / kKeys;
     };
-    const Finder finder(p.B, !p.causal, pieces);
+    Finder finder(p.B, !p.causal, pieces);
     auto find = [&](int k) {
       Item item{};
       item.at = -1;

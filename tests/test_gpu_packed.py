@@ -378,6 +378,22 @@ def test_broken_offsets_are_reported():
     assert fa.fa_get_device_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF)])
+def test_many_sequences(D, dtype):
+    """Seven hundred short samples: every block goes through many of them."""
+    c = Case([(13 * i) % 17 for i in range(700)], 4, 2, D, dtype, first=2, behind=3, seed=21)
+    scale = 1.0 / math.sqrt(D)
+    q, k, v = c.gpu()
+    cu, _ = c.offsets()
+    out, lse = fa.fa_prefill_packed(q, k, v, cu, scale=scale)
+    dq, dk, dv = fa.fa_prefill_packed_backward(c.do.cuda(), q, k, v, out, lse, cu, scale=scale)
+    torch.cuda.synchronize()
+    got = {"out": out, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+    for rows, _, want in c.want(True, scale, grad=True):
+        for name, (value, bound) in want.items():
+            ref.check(name, got[name][rows], value, bound)
+
+
 def test_broken_offsets_with_parts():
     """Rows of a sequence that is taken as empty stay as they were, whatever the workspace holds."""
     c = Case([64, 64], 2, 2, 64, BF, seed=17)
