@@ -1268,12 +1268,14 @@ def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool 
                   _flat(dev, torch.float32, rows, "lse", lse), *strides,
                   *_strided(dev, dtype, qs, "out", out), *fields, num_splits)
         a = _pack_packed(*fields, 0, 0)
-        need = lib.fa_packed_workspace_size(a)
-        if need:
-            if workspace is not None:
-                _on(dev, workspace)
-            ws = _workspace(need, q.device, workspace)
-            a = _pack_packed(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
+        # (keys of fewer than 2048 a sequence are in parts only where the caller asks for it)
+        if num_splits > 1 or (num_splits == 0 and ks[0] >= 2048 * (len(cu_seqlens_q) - 1)):
+            need = lib.fa_packed_workspace_size(a)
+            if need:
+                if workspace is not None:
+                    _on(dev, workspace)
+                ws = _workspace(need, q.device, workspace)
+                a = _pack_packed(*fields, ws.data_ptr(), ws.numel() * ws.element_size())
         _check(lib.fa_prefill_packed(a, _raw_stream(dev)))
     return out, lse
 
