@@ -56,7 +56,8 @@ struct GradParams {
   // A query tile's rows side by side: [Hkv, total_q, G]
   float2* rows;          // -lse log2 e (-inf where nothing is seen), delta
   float* powers;         // fp16: f of the row
-  uint32_t* dout_max;    // fp16: bits of the largest |dout|
+  float* maxima;         // fp16: the largest |dout| of each block of row_kernel (num_maxima of them)
+  int num_maxima;
   int* taken;            // dq_kernel: work items taken so far, beyond each block's first
 };
 
@@ -139,6 +140,12 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t half
 constexpr int kRowThreads = 256;
 constexpr int kRowBatch = 4;
 
+// Blocks for the rows of a kv head.
+unsigned row_blocks(int total_q, int G, int D) {
+  const int64_t per = kRowThreads / (D / 8) * kRowBatch;
+  return static_cast<unsigned>((static_cast<int64_t>(total_q) * G + per - 1) / per);
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
@@ -195,8 +202,16 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
     }
   }
   if constexpr (!BF16) {
+    // (a maximum a block, and not one for the call by an atomic, which something would have to set to 0 first: a
+    // launch of some 4 us)
+    __shared__ uint32_t tops[kRowThreads / 32];
     const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-    if (threadIdx.x % 32 == 0 && bits > 0) atomicMax(g.dout_max, bits);  // a maximum: the order does not matter
+    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = bits;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      const uint32_t all = __reduce_max_sync(0xffffffffu, threadIdx.x < kRowThreads / 32 ? tops[threadIdx.x] : 0u);
+      if (threadIdx.x == 0) g.maxima[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = __uint_as_float(all);
+    }
   }
 }
 
@@ -681,7 +696,8 @@ struct DkvLayout {
   static constexpr int kShared = kBars + kNumBars * 8;       // work items, turns, tensor memory's address
   // No room is left to align the base by hand: the kernel has no static shared memory, and its dynamic
   // one is declared with this alignment.
-  static constexpr int kAlloc = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;
+  static constexpr int kTops = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;  // fp16: largest |dout|, a warp each
+  static constexpr int kAlloc = kTops + kThreads / 32 * 4;
   static constexpr bool kApart = D == 64;
   static constexpr int kDv = 0, kDk = D, kS = 2 * D, kDp = kS + kRows;
   static constexpr int kP = kApart ? kDp + kRows : kS, kDs = kApart ? kP + kRows / 2 : kDp;
@@ -838,10 +854,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       clear_rows<D>(smem + L::kRing + s * L::kTile, used, threadIdx.x, kThreads);
     fence_proxy_async_smem();
   }
+  if constexpr (!BF16) {
+    wait_for_previous();  // row_kernel
+    uint32_t top = 0;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < gp.num_maxima; i += kThreads) top = max(top, __float_as_uint(gp.maxima[i]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::kTops)[warp] = top;
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  float power = 1.f;  // that dS is held times
+  if constexpr (!BF16) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kThreads / 32; ++i) top = max(top, reinterpret_cast<const uint32_t*>(smem + L::kTops)[i]);
+    power = power_for(__uint_as_float(top));
+  }
   if (warp == 11) {
     // --------------- work items; lse and delta of each query row; rows past the end ----------------
     wait_for_previous();  // row_kernel
@@ -875,8 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bars.item() + 8u * (k % kItems));
       }
     };
-    float f = kUnpower;
-    if constexpr (!BF16) f *= power_for(__uint_as_float(*gp.dout_max));
+    const float f = kUnpower * power;
     int step = 0, tails = 0;
     Item item = find(0);
     publish(0, item);
@@ -980,11 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
     const uint32_t tm_p = tmem + L::kP + w * L::kStep + lanes, tm_ds = tmem + L::kDs + w * L::kStep + lanes;
-    float f = 1.f;
-    if constexpr (!BF16) {
-      wait_for_previous();
-      f = power_for(__uint_as_float(*gp.dout_max));
-    }
+    const float f = power;
     const float2 a2 = make_float2(p.scale_log2, p.scale_log2), f2 = make_float2(f * kUnpower, f * kUnpower);
     bool ok = true;
     int step = 0;
@@ -1101,14 +1127,11 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   auto kk = dkv_kernel<D, BF16>;
   cudaError_t e = ensure_smem_limit(kq, DqLayout<D>::kAlloc);
   if (e == cudaSuccess) e = ensure_smem_limit(kk, DkvLayout<D>::kAlloc);
-  if (e == cudaSuccess && !BF16) e = cudaMemsetAsync(g.dout_max, 0, sizeof(uint32_t), st);
   if (e != cudaSuccess) return e;
   const int64_t sms = num_sms() > 0 ? num_sms() : 152;
   auto blocks = [&](int64_t items) { return static_cast<unsigned>(items * g.f.Hkv < sms ? items * g.f.Hkv : sms); };
   if (q_items > 0) {
-    constexpr int64_t kPer = kRowThreads / (D / 8) * kRowBatch;
-    const int64_t rows = static_cast<int64_t>(g.f.total_q) * g.f.G;
-    row_kernel<D, BF16><<<dim3(static_cast<unsigned>((rows + kPer - 1) / kPer), g.f.Hkv), kRowThreads, 0, st>>>(g);
+    row_kernel<D, BF16><<<dim3(row_blocks(g.f.total_q, g.f.G, D), g.f.Hkv), kRowThreads, 0, st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // dq_kernel reads nothing of dkv_kernel's, whose blocks let it start once row_kernel has ended: it takes
@@ -1126,14 +1149,21 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   return cudaGetLastError();
 }
 
-constexpr size_t kWordBytes = 256;  // in front: the largest |dout|, the items taken
+constexpr size_t kWordBytes = 256;  // in front: the items taken
+
+size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 size_t row_bytes(const fa_packed_backward_args* a) {
-  return (static_cast<size_t>(a->total_q) * a->Hq * sizeof(float2) + 255) / 256 * 256;
+  return round_up(static_cast<size_t>(a->total_q) * a->Hq * sizeof(float2));
+}
+
+size_t num_maxima(const fa_packed_backward_args* a) {
+  return static_cast<size_t>(row_blocks(a->total_q, a->Hq / a->Hkv, a->D)) * a->Hkv;
 }
 
 size_t workspace_bytes(const fa_packed_backward_args* a) {
-  return kWordBytes + row_bytes(a) + (a->dtype == FA_FP16 ? (row_bytes(a) / 2 + 255) / 256 * 256 : 0);
+  return kWordBytes + row_bytes(a) +
+         (a->dtype == FA_FP16 ? round_up(row_bytes(a) / 2) + round_up(num_maxima(a) * sizeof(float)) : 0);
 }
 
 }  // namespace
@@ -1209,10 +1239,13 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   memcpy(g.dk_strides, a->dk_strides, sizeof g.dk_strides);
   memcpy(g.dv_strides, a->dv_strides, sizeof g.dv_strides);
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
-  g.dout_max = reinterpret_cast<uint32_t*>(ws);
-  g.taken = reinterpret_cast<int*>(ws + 128);
+  g.taken = reinterpret_cast<int*>(ws);
   g.rows = reinterpret_cast<float2*>(ws + packed::kWordBytes);
   g.powers = reinterpret_cast<float*>(ws + packed::kWordBytes + packed::row_bytes(a));
+  if (a->dtype == FA_FP16) {
+    g.maxima = g.powers + packed::round_up(packed::row_bytes(a) / 2) / sizeof(float);
+    g.num_maxima = static_cast<int>(packed::num_maxima(a));
+  }
   const bool bf16 = a->dtype == FA_BF16;
   // Maps of an empty side are read by nothing; they get the workspace as their address.
   const bool hq = a->total_q > 0, hk = a->total_k > 0;
