@@ -712,6 +712,8 @@ size_t fa_packed_workspace_size(const fa_packed_args* args);
  *   q, k, v, out, lse, cu_seqlens_*: as in the forward call, out and lse what it returned; dout
  *   [total_q, Hq, D]; dq [total_q, Hq, D], dk, dv [total_k, Hkv, D]; all in dtype, with strides as
  *   above, the results apart from each other and from the inputs.
+ * Of a row that sees 16 keys or fewer delta is taken as sum_j P dP instead, free of out's rounding, which
+ * would show where dP and delta nearly cancel (of one that sees one key dq is 0).
  * dS is rounded to dtype on its way to the products.  FA_FP16: it is held there times a power of two
  * that brings the largest |dout| (of the row for dq, of all sequences for dk and dv) to [8, 16),
  * so gradients far below 1 keep their bits; what is 2^-28 of that largest, or less, is lost.

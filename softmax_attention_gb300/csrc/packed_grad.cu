@@ -6,7 +6,8 @@
 //
 // Three kernels; the sums that a block owns stay in tensor memory, so that nothing is added by atomics
 // and the same call gives the same bits:
-//   - row_kernel: delta and -lse, in the form that the others use them, a pass over dout and out;
+//   - row_kernel: delta and -lse, in the form that the others use them, a pass over dout and out (and, of rows that see
+//     few keys, the products themselves);
 //   - dkv_kernel: a block holds a tile of 128 keys and walks over the query tiles that see it, all
 //     heads of the group: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  With the
 //     products turned, P^T and dS^T have keys as rows and go back to tensor memory as the
@@ -16,8 +17,8 @@
 // S and dP are computed in both, seven products for the five of a form that adds dq by atomics.
 //
 // Bound by the tensor cores where sequences are long: 8192 tokens of 16 heads in 4 groups (bf16, D = 128, causal) take
-// 550 us, 1250 TFLOP/s counting five products and 1750 counting the seven, 0.91 of the measured bf16 rate.
-// Samples of 512 to 2048 tokens: 373 us (870 and 1220); there a work item's first tile, which waits for its loads
+// 555 us, 1240 TFLOP/s counting five products and 1740 counting the seven, 0.90 of the measured bf16 rate.
+// Samples of 512 to 2048 tokens: 380 us (850 and 1190); there a work item's first tile, which waits for its loads
 // and meets an empty pipe, costs some 3 us of the 7 to 20 that the item takes, and shared memory has no room to
 // hold the next item's Q and dO (K and V) beside this one's.  (Loading them to L2 ahead of time: no change.)
 //
@@ -48,6 +49,10 @@ struct GradParams {
   const void* dout;
   const void* o;         // the forward pass's out
   const float* lse;      // [total_q, Hq]
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_strides[2], k_strides[2], v_strides[2];
   int64_t dout_strides[2], o_strides[2];
   void* dq;
   void* dk;
@@ -56,6 +61,8 @@ struct GradParams {
   // A query tile's rows side by side: [Hkv, total_q, G]
   float2* rows;          // -lse log2 e (-inf where nothing is seen), delta
   float* powers;         // fp16: f of the row
+  float* few;            // delta of the rows that see few keys, likewise
+  int few_units, few_blocks;  // row_kernel: pieces of such rows of a sequence; blocks for them, in front
   float* maxima;         // fp16: the largest |dout| of each block of row_kernel (num_maxima of them)
   int num_maxima;
   int* taken;            // dq_kernel: work items taken so far, beyond each block's first
@@ -146,16 +153,128 @@ unsigned row_blocks(int total_q, int G, int D) {
   return static_cast<unsigned>((static_cast<int64_t>(total_q) * G + per - 1) / per);
 }
 
+// Where a row sees few keys, dP and delta are nearly alike, and the rounding of `out` in <dout, out> would show in
+// dS (sequences of two to eight tokens: gradients twice as far off as by dS's own rounding, of 32 a tenth).  There
+// delta is sum_j P_j dP_j / sum_j P_j, from the products themselves; and of a row that sees one key dS is 0,
+// exactly, which dq_kernel sees to for the row and dkv_kernel for a sequence's only key.  (Costs 1 us of 15 for three
+// short samples, 4 of 380 for samples of 512 to 2048 tokens.  Such rows' columns masked out of dS in dkv_kernel's loop:
+// 18 us of 555.  32 keys, two passes: 2 us more for the short ones, and registers that slow the others.)
+constexpr int kFew = 16;
+
+// C (16 x 8, fp32) += A (16 x 16) B (16 x 8).  With g = lane / 4, t = lane % 4: a0 (row g, k 2t..), a1 (g + 8, 2t..),
+// a2 (g, 2t + 8..), a3 (g + 8, 2t + 8..); b0 (k 2t.., column g), b1 (2t + 8.., g); c0, c1 (row g, columns 2t,
+// 2t + 1), c2, c3 (row g + 8).
+template <bool BF16>
+__device__ __forceinline__ void mma_warp(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// delta of a piece of the rows of sequence b that see 1 to kFew keys.  A warp takes 16 rows at a time;
+// which of a row's elements a product's k-th is does not matter as long as both sides agree, so a lane reads 16 bytes.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
+__device__ __forceinline__ void few_rows(const GradParams& g, int b, int piece, int hk) {
+  const Params& p = g.f;
+  const Seq s = load_seq(p, b);
+  int first = 0, n = 0;  // tokens
+  if (p.causal) {
+    first = max(0, s.nq - s.nk);
+    n = max(0, min(s.nq, s.nq - s.nk + kFew) - first);
+  } else if (s.nk > 0 && s.nk <= kFew) {
+    n = s.nq;
+  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gr = lane / 4, t = lane % 4;
+  constexpr int kPerBlock = kRowThreads / 32 * 16;
+  for (int64_t r0 = static_cast<int64_t>(piece) * kPerBlock + warp * 16; r0 < static_cast<int64_t>(n) * p.G;
+       r0 += static_cast<int64_t>(g.few_units) * kPerBlock) {
+    const uint16_t *q[2], *dout[2];
+    int sees[2];  // keys
+    float nl[2];
+    int64_t at[2];
+    const uint4 none = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int64_t r = r0 + gr + 8 * x;
+      const int token = static_cast<int>(r / p.G), h = hk * p.G + static_cast<int>(r - static_cast<int64_t>(token) * p.G);
+      const int i = first + token;
+      const int64_t row = s.q0 + i;
+      sees[x] = token >= n ? 0 : p.causal ? min(s.nk, i + s.nk - s.nq + 1) : s.nk;
+      at[x] = (hk * static_cast<int64_t>(p.total_q) + row) * p.G + (h - hk * p.G);
+      nl[x] = -INFINITY;
+      q[x] = dout[x] = nullptr;
+      if (sees[x] == 0) continue;
+      q[x] = static_cast<const uint16_t*>(g.q) + row * g.q_strides[0] + h * g.q_strides[1] + 8 * t;
+      dout[x] = static_cast<const uint16_t*>(g.dout) + row * g.dout_strides[0] + h * g.dout_strides[1] + 8 * t;
+      const float lse = __ldg(g.lse + row * p.Hq + h);
+      if (lse != -INFINITY) nl[x] = -lse * prefill::kLog2e;
+    }
+    float sum[2] = {0.f, 0.f}, dot[2] = {0.f, 0.f};
+    {
+      float sc[2][4] = {}, dp[2][4] = {};
+      const uint16_t *k[2], *v[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int key = 8 * x + gr;
+        k[x] = v[x] = nullptr;
+        if (key >= s.nk) continue;
+        k[x] = static_cast<const uint16_t*>(g.k) + (s.k0 + static_cast<int64_t>(key)) * g.k_strides[0] + hk * g.k_strides[1] + 8 * t;
+        v[x] = static_cast<const uint16_t*>(g.v) + (s.k0 + static_cast<int64_t>(key)) * g.v_strides[0] + hk * g.v_strides[1] + 8 * t;
+      }
+#pragma unroll
+      for (int c = 0; c < D; c += 32) {
+        auto part = [&](const uint16_t* from) { return from ? __ldg(reinterpret_cast<const uint4*>(from + c)) : none; };
+        const uint4 a0 = part(q[0]), a1 = part(q[1]), d0 = part(dout[0]), d1 = part(dout[1]);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const uint4 kb = part(k[x]), vb = part(v[x]);
+          mma_warp<BF16>(sc[x], a0.x, a1.x, a0.y, a1.y, kb.x, kb.y);
+          mma_warp<BF16>(sc[x], a0.z, a1.z, a0.w, a1.w, kb.z, kb.w);
+          mma_warp<BF16>(dp[x], d0.x, d1.x, d0.y, d1.y, vb.x, vb.y);
+          mma_warp<BF16>(dp[x], d0.z, d1.z, d0.w, d1.w, vb.z, vb.w);
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (8 * x + 2 * t + (e & 1) >= sees[e / 2]) continue;
+          const float w = nl[e / 2] == -INFINITY ? 0.f : exp2_approx(fmaf(sc[x][e], p.scale_log2, nl[e / 2]));
+          sum[e / 2] += w;
+          dot[e / 2] = fmaf(w, dp[x][e], dot[e / 2]);
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+#pragma unroll
+      for (int o = 1; o <= 2; o <<= 1) {
+        sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
+        dot[x] += __shfl_xor_sync(0xffffffffu, dot[x], o);
+      }
+      if (t == 0 && sees[x] > 0) g.few[at[x]] = sum[x] == 0.f ? 0.f : dot[x] / sum[x];
+    }
+  }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
   const Params& p = g.f;
   let_next_start();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *g.taken = 0;
+  const int few = g.few_blocks;  // (a sequence's piece each, or more in turn)
+  if (static_cast<int>(blockIdx.x) < few) {
+    for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * g.few_units; u += few)
+      few_rows<D, BF16>(g, static_cast<int>(u / g.few_units), static_cast<int>(u % g.few_units), blockIdx.y);
+    return;
+  }
   // rows in front of the first sequence and behind the last take no part
   const int from = max(0, __ldg(p.cu_q)), to = min(p.total_q, __ldg(p.cu_q + p.B));
   const int lane = threadIdx.x % kLanes;
-  const uint32_t row0 = blockIdx.x * (kPerPass * kRowBatch) + threadIdx.x / kLanes;  // of the kv head's
+  const uint32_t row0 = (blockIdx.x - few) * (kPerPass * kRowBatch) + threadIdx.x / kLanes;  // of the kv head's
   const int hk = blockIdx.y;
   uint4 a[kRowBatch], c[kRowBatch];
   int token[kRowBatch], head[kRowBatch];
@@ -210,7 +329,7 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const GradParams g) {
     __syncthreads();
     if (threadIdx.x < 32) {
       const uint32_t all = __reduce_max_sync(0xffffffffu, threadIdx.x < kRowThreads / 32 ? tops[threadIdx.x] : 0u);
-      if (threadIdx.x == 0) g.maxima[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = __uint_as_float(all);
+      if (threadIdx.x == 0) g.maxima[static_cast<int64_t>(blockIdx.y) * (gridDim.x - few) + blockIdx.x - few] = __uint_as_float(all);
     }
   }
 }
@@ -254,7 +373,7 @@ __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_i
 // Its work items are taken as blocks come free (a counter in the workspace; which block takes an item changes
 // nothing in it), and it runs after dkv_kernel, whose blocks end far apart where sequences are long (8192 tokens: a
 // key tile meets up to 256 query tiles, and the mean block 219): it fills what they leave.  dq first and both dealt
-// out ahead of time: 572 us for the 550 of this (16 heads in 4 groups, D = 128), 386 for 373 with samples of 512 to
+// out ahead of time: 572 us for 550 (16 heads in 4 groups, D = 128), 386 for 373 with samples of 512 to
 // 2048 tokens.  An item in one place is taken as late as can be; with 2, 3 and 4 places 561, 585 and 609 us.
 constexpr int kDqItems = 1;
 
@@ -577,7 +696,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float f = !BF16 && valid ? gp.powers[at] : 1.f;
       // (a row of no query is not looked at by anyone: it may see everything)
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
-      const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(f, f), nd2 = make_float2(-rd.y * f, -rd.y * f);
+      const float delta = key_lim >= 1 && key_lim <= kFew ? gp.few[at] : rd.y, fd = key_lim == 1 ? 0.f : f;
+      const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(fd, fd), nd2 = make_float2(-delta * fd, -delta * fd);
       for (int j = -1; j < n; ++j) {
         if (j >= 0) {
           // S_step; and dS_{step-2} read, before dS_step takes its place
@@ -908,6 +1028,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     const float f = kUnpower * power;
     int step = 0, tails = 0;
+    int token[4];  // of the tile's, of the lane's rows
+#pragma unroll
+    for (int e = 0; e < 4; ++e) token[e] = (lane * 4 + e) / p.G;
     Item item = find(0);
     publish(0, item);
     for (int k = 0; ok && item.at >= 0; ++k) {
@@ -919,16 +1042,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; ok && i < n; ++i, ++step) {
         const int q0 = (first_tile + i) * p.q_per_tile;
         const int live = min(used, (item.seq.nq - q0) * p.G);  // rows of the tile that are a query's
-        const float2* src = gp.rows + (item.head * static_cast<int64_t>(p.total_q) + item.seq.q0 + q0) * p.G + lane * 4;
+        const int64_t at = (item.head * static_cast<int64_t>(p.total_q) + item.seq.q0 + q0) * p.G + lane * 4;
         float nl[4], nd[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           nl[e] = -INFINITY;  // no query: P = 0
           nd[e] = 0.f;
           if (lane * 4 + e < live) {
-            const float2 rd = src[e];
+            const float2 rd = gp.rows[at + e];
+            const int sees = p.causal ? q0 + token[e] + item.seq.nk - item.seq.nq + 1 : item.seq.nk;
             nl[e] = rd.x + kPower;
-            nd[e] = -f * rd.y;
+            nd[e] = -f * (sees >= 1 && sees <= kFew ? gp.few[at + e] : rd.y);
           }
         }
         if (step >= 2)
@@ -1097,7 +1221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint16_t* dst = w ? static_cast<uint16_t*>(gp.dk) + row * gp.dk_strides[0] + item.head * gp.dk_strides[1]
                         : static_cast<uint16_t*>(gp.dv) + row * gp.dv_strides[0] + item.head * gp.dv_strides[1];
       if (key >= item.seq.nk) dst = nullptr;
-      const float back = w ? p.scale / f : kUnpower;
+      // (the only key of a sequence: no dS but 0)
+      const float back = w ? (item.seq.nk == 1 ? 0.f : p.scale / f) : kUnpower;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -1131,7 +1256,7 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   const int64_t sms = num_sms() > 0 ? num_sms() : 152;
   auto blocks = [&](int64_t items) { return static_cast<unsigned>(items * g.f.Hkv < sms ? items * g.f.Hkv : sms); };
   if (q_items > 0) {
-    row_kernel<D, BF16><<<dim3(row_blocks(g.f.total_q, g.f.G, D), g.f.Hkv), kRowThreads, 0, st>>>(g);
+    row_kernel<D, BF16><<<dim3(g.few_blocks + row_blocks(g.f.total_q, g.f.G, D), g.f.Hkv), kRowThreads, 0, st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // dq_kernel reads nothing of dkv_kernel's, whose blocks let it start once row_kernel has ended: it takes
@@ -1162,7 +1287,7 @@ size_t num_maxima(const fa_packed_backward_args* a) {
 }
 
 size_t workspace_bytes(const fa_packed_backward_args* a) {
-  return kWordBytes + row_bytes(a) +
+  return kWordBytes + row_bytes(a) + round_up(row_bytes(a) / 2) +
          (a->dtype == FA_FP16 ? round_up(row_bytes(a) / 2) + round_up(num_maxima(a) * sizeof(float)) : 0);
 }
 
@@ -1241,9 +1366,22 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   g.taken = reinterpret_cast<int*>(ws);
   g.rows = reinterpret_cast<float2*>(ws + packed::kWordBytes);
-  g.powers = reinterpret_cast<float*>(ws + packed::kWordBytes + packed::row_bytes(a));
+  const size_t one = packed::round_up(packed::row_bytes(a) / 2) / sizeof(float);  // a float a row
+  g.few = reinterpret_cast<float*>(ws + packed::kWordBytes + packed::row_bytes(a));
+  // pieces of 128 rows: causal, all that a sequence can have of few keys; else, the mean sequence's
+  const int64_t rows = p.causal ? static_cast<int64_t>(packed::kFew) * p.G : (static_cast<int64_t>(a->total_q) * p.G + a->B - 1) / a->B;
+  g.few_units = static_cast<int>((rows + 127) / 128 > 1 ? (rows + 127) / 128 : 1);
+  const int64_t few = static_cast<int64_t>(a->B) * g.few_units;
+  g.few_blocks = static_cast<int>(few < (1 << 20) ? few : 1 << 20);
+  g.q = a->q;
+  g.k = a->k;
+  g.v = a->v;
+  memcpy(g.q_strides, a->q_strides, sizeof g.q_strides);
+  memcpy(g.k_strides, a->k_strides, sizeof g.k_strides);
+  memcpy(g.v_strides, a->v_strides, sizeof g.v_strides);
   if (a->dtype == FA_FP16) {
-    g.maxima = g.powers + packed::round_up(packed::row_bytes(a) / 2) / sizeof(float);
+    g.powers = g.few + one;
+    g.maxima = g.powers + one;
     g.num_maxima = static_cast<int>(packed::num_maxima(a));
   }
   const bool bf16 = a->dtype == FA_BF16;

@@ -6,7 +6,8 @@ fp32.  What the bounds count:
   scores   D products summed in fp32 (2 D e of sum |q k| scale, to allow for sums that truncate),
            and a handful of roundings of the exponent itself (8 e of |s| + |lse| + 1)
   weights  P rounded once to 16 bits (u); the sums of its products in fp32 (2 n e)
-  dS       e_p of the weight, dP's and delta's errors times the weight, one rounding to 16 bits (u,
+  dS       0 where a row sees one key (in dk, where the sequence has one); else e_p of the weight, dP's and delta's errors times the weight (delta's with
+           out's rounding where a row sees more than 16 keys), one rounding to 16 bits (u,
            and in fp16 half the least subnormal over the power of two that it is held times)
   results  one rounding to 16 bits (u)
 """
@@ -78,11 +79,19 @@ def attention(q, k, v, causal, scale, dout=None, call_top=None, in_place_of=None
     ds = p * (dp - delta)
     e_dp = 2 * D * E * (do.abs() @ vv.abs().transpose(1, 2))
     e_delta = (do.abs() * (e_out + 2 * D * E * out.abs())).sum(-1, keepdim=True)
+    # of a row that sees 16 keys at most delta is sum p dp / sum p, without out's rounding: each weight off by ep, above
+    # and below, and each dp by e_dp; 16 sums and a division
+    e_few = (p * (e_dp + (2 * ep + 80 * E) * dp.abs())).sum(-1, keepdim=True)
+    count = seen.sum(-1, keepdim=True)
+    e_delta = torch.where(count <= 16, e_few, e_delta)
     half = t == torch.float16
     e_ds = (ep + u) * ds.abs() + p * (e_dp + e_delta) * (1 + u)
     hidden = torch.where(seen, 1.0, 0.0)
     e_q = e_ds + (hidden * (2.0 ** -25 / f_row)[..., None] if half else 0.0)
     e_k = e_ds + (hidden * (2.0 ** -25 / f_call) if half else 0.0)
+    # the only key's weight is 1: no gradient (exactly none in dq, and in dk if it is the sequence's only one)
+    ds, e_q = (torch.where(count == 1, 0.0, x) for x in (ds, e_q))
+    e_k = torch.zeros_like(e_k) if m == 1 else e_k
     e_p = (ep + u) * p + (hidden * 2.0 ** -25 / 128 if half else 0.0)
     heads = lambda x: x.view(Hkv, G, m, D).sum(1)  # noqa: E731  (a kv head's query heads)
     dq = ds @ kk * scale

@@ -378,6 +378,37 @@ def test_broken_offsets_are_reported():
     assert fa.fa_get_device_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("lens,klens,Hq,Hkv,D,dtype,causal", [
+    ([1, 1, 1], None, 4, 2, 64, BF, True),                   # one key each: dq and dk are 0
+    ([1, 2, 3, 4, 5, 8], None, 6, 2, 128, BF, True),
+    ([1, 2, 3, 4, 5, 8], None, 10, 2, 64, HF, True),
+    ([15, 16, 17, 31, 32, 33, 70], None, 8, 2, 128, HF, True),       # either side of what few means, and of twice it
+    ([31, 32, 33, 200], [15, 16, 17, 16], 8, 2, 64, BF, False),
+    ([300, 40], [1, 1], 4, 1, 128, BF, False),               # many queries of one key
+    ([90, 64], [40, 3], 12, 4, 64, BF, True),                # queries in front of every key, then the first of one
+    ([90, 64], [40, 3], 3, 3, 128, HF, True),
+    ([5, 40], None, 128, 1, 64, BF, True),                   # more rows of few keys than a block takes
+    ([1000], [13], 16, 1, 128, HF, False),
+])
+def test_rows_of_few_keys(lens, klens, Hq, Hkv, D, dtype, causal):
+    """Where dP and delta nearly cancel: bounds without the rounding of out, and zeros that are zeros."""
+    c = Case(lens, Hq, Hkv, D, dtype, klens=klens, first=0 if klens else 3, behind=5, seed=31 + D + Hq)
+    scale = 1.0 / math.sqrt(D)
+    q, k, v = c.gpu()
+    offsets = c.offsets()
+    out, lse = fa.fa_prefill_packed(q, k, v, *offsets, causal=causal, scale=scale)
+    ws = torch.full((1 << 24,), 255, dtype=torch.uint8, device="cuda")  # NaN
+    dq, dk, dv = fa.fa_prefill_packed_backward(c.do.cuda(), q, k, v, out, lse, *offsets, causal=causal,
+                                               scale=scale, workspace=ws)
+    torch.cuda.synchronize()
+    for rows, keys, want in c.want(causal, scale, grad=True):
+        for name, got, at in (("dq", dq, rows), ("dk", dk, keys), ("dv", dv, keys)):
+            if name in want:
+                ref.check(name, got[at], *want[name])
+    if lens == [1, 1, 1]:
+        assert not dq[c.cu[0]:c.cu[-1]].any() and not dk[c.cu[0]:c.cu[-1]].any()
+
+
 @pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF)])
 def test_many_sequences(D, dtype):
     """Seven hundred short samples: every block goes through many of them."""
