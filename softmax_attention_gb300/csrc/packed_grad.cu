@@ -142,7 +142,7 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t half
 
 // ------------------------------------------------------------------------------------------
 // delta and lse of each row.  D / 8 lanes a row, 16 bytes of dout and of out each, four rows in flight
-// a thread; bound by memory (32,768 tokens of 16 heads, D = 128: 46 us with cold caches, 278 MB, 0.9 of the copy rate).
+// a thread; bound by memory (32,768 tokens of 16 heads, D = 128: 48 us with cold caches, 279 MB, 0.87 of the copy rate).
 // ------------------------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 constexpr int kRowBatch = 4;
@@ -367,7 +367,7 @@ __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_i
 // memory), 10 issues dS K, 11 finds the work items and clears what a last K tile holds past its
 // sequence's end.  S and dP are given back as soon as they are in registers, so that S_{j+1} and
 // dP_{j+1} are computed while the weights of tile j are; dS has two buffers of its own.  (With dS_j written
-// over one of two S buffers S_{j+1} had to wait for dQ_{j-1}.)  Products are in the pipe in 77 % of all clocks
+// over one of two S buffers S_{j+1} had to wait for dQ_{j-1}.)  Products are in the pipe in 76 % of all clocks
 // (four sequences of 8192 tokens).
 // ------------------------------------------------------------------------------------------
 // Its work items are taken as blocks come free (a counter in the workspace; which block takes an item changes
@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // S^T, dP^T): P^T lies over S^T and dS^T over dP^T, and issuer 9 puts S^T_{i+1} right behind dV_i
 // (issuer 10 dP^T_{i+1} behind dK_i), which reads what it overwrites: products of one thread and
 // one shape run in order.  While the element-wise warps work on S^T the tensor cores run dK and
-// dP^T, and the other way round: products are in the pipe in 74 % of all clocks (four sequences of 8192 tokens).
+// dP^T, and the other way round: products are in the pipe in 75 % of all clocks (four sequences of 8192 tokens).
 // Without turns of the two issuers 604 us for 575 of the whole gradient (one of 8192 tokens, dq first), with the turn
 // given earlier 594, after the commits 602.  At D = 64, where the shapes differ, P^T and dS^T have columns of
 // their own.
