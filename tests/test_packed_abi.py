@@ -170,8 +170,12 @@ def test_nothing_to_do(lib):
 
 def test_workspace_sizes(lib):
     size = lib.fa_packed_backward_workspace_size
-    assert size(ctypes.byref(_packed_backward())) == 256 + 512          # 9 * 4 pairs of fp32, and a word
-    assert size(ctypes.byref(_packed_backward(total_q=1000))) == 256 + 32000
+    # a word; 9 * 4 pairs of fp32; as many deltas of rows that see few keys; in pieces of 256
+    assert size(ctypes.byref(_packed_backward())) == 256 + 512 + 256
+    assert size(ctypes.byref(_packed_backward(total_q=1000))) == 256 + 32000 + 16128
+    # fp16: a power of two a row, and a maximum for each 64 rows (D = 128) of a kv head
+    assert size(ctypes.byref(_packed_backward(dtype=fa.FA_FP16))) == 256 + 512 + 256 + 256 + 256
+    assert size(ctypes.byref(_packed_backward(total_q=1000, dtype=fa.FA_FP16))) == 256 + 32000 + 2 * 16128 + 256
     assert size(ctypes.byref(_packed_backward(B=0))) == 0
     assert size(ctypes.byref(_packed_backward(D=80))) == 0
     size = lib.fa_qk_norm_rotary_backward_workspace_size
