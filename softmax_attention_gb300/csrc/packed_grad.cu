@@ -1143,8 +1143,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       int first_tile;
       const int n = query_tiles(p, item.seq, item.at, first_tile);
       const int key = item.at + r;
-      // columns below `from` are queries in front of the key
-      int from = p.causal ? (key - (item.seq.nk - item.seq.nq) - first_tile * p.q_per_tile) * p.G - w * kHalf : 0;
+      // Columns below `from` are queries in front of the key.  (Held at 0 or more before the product: a context of more
+      // than 2^31 / G keys would pass 32 bits.  From there down it falls by the rows of a sequence, below 2^31, at most.)
+      int from = p.causal ? max(0, key - (item.seq.nk - item.seq.nq) - first_tile * p.q_per_tile) * p.G - w * kHalf : 0;
       for (int i = 0; i < n; ++i, ++step, from -= used) {
         const float4* row_data = reinterpret_cast<const float4*>(smem + L::kRowData) + (step & 1) * 64 + w * 16;
         ok = __all_sync(0xffffffffu, mbar_wait(bars.rows(step & 1), (step / 2) & 1, p.status));
