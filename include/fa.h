@@ -715,8 +715,9 @@ size_t fa_packed_workspace_size(const fa_packed_args* args);
  * Of a row that sees 16 keys or fewer delta is taken as sum_j P dP instead, free of out's rounding, which
  * would show where dP and delta nearly cancel (of one that sees one key dq is 0).
  * dS is rounded to dtype on its way to the products.  FA_FP16: it is held there times a power of two
- * that brings the largest |dout| (of the row for dq, of all sequences for dk and dv) to [8, 16),
- * so gradients far below 1 keep their bits; what is 2^-28 of that largest, or less, is lost.
+ * that brings sum_d |dout_id| max |v|, which no |dP_ij| passes, to [2^14, 2^15) (of the row for dq, the
+ * largest of all rows for dk and dv; max |v| over all keys), so that it stays in range whatever q, k, v and
+ * dout are, and gradients far below 1 keep their bits: what is 2^-39 of that bound, or less, is lost.
  * (Within a sequence values of q, k, v or dout that are not finite may reach gradients that they have
  * no part in, as 0 times them.)
  * Every row of dq, dk and dv that belongs to a sequence is written (zeros where nothing is seen),

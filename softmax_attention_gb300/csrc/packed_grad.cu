@@ -26,9 +26,11 @@
 // items, and the products are issued by whole warps from uniform registers, as in packed.cu.
 //
 // fp16: dS is held times a power of two, f, so that the small values that gradients have keep their
-// bits (its smallest normal number is 2^-14): f brings the largest |dout| to [8, 16), of the row
-// in dq_kernel, of the whole call in dkv_kernel, whose sums run over rows.  P is held times 2^7
-// there.  bf16 has fp32's exponents, and f = 1.
+// bits (its smallest normal number is 2^-14) and the large ones stay below its largest, 65504.  No |dP_ij| passes
+// b_i = sum_d |dout_id| max |v|, and no |dS_ij|, with delta_i a mean of dP_ij over j by P_ij, b_i / 2: f brings b_i to
+// [2^14, 2^15), of the row in dq_kernel, the largest of the whole call in dkv_kernel, whose sums run over rows.
+// (What |dout| alone would give, dS of values of 100 can pass.)  P is held times 2^7 there.  bf16 has fp32's
+// exponents, and f = 1.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
@@ -60,19 +62,22 @@ struct GradParams {
   int64_t dq_strides[2], dk_strides[2], dv_strides[2];
   // A query tile's rows side by side: [Hkv, total_q, G]
   float2* rows;          // -lse log2 e (-inf where nothing is seen), delta
-  float* powers;         // fp16: f of the row
+  float* norms;          // fp16: sum of |dout| of the row; 0 where that is no number, or infinite
   float* few;            // delta of the rows that see few keys, likewise
   int few_units, few_blocks;  // row_kernel: pieces of such rows of a sequence; blocks for them, in front
-  float* maxima;         // fp16: the largest |dout| of each block of row_kernel (num_maxima of them)
+  float* maxima;         // fp16: the largest of `norms` in each block of row_kernel (num_maxima of them)
   int num_maxima;
+  float* v_maxima;       // fp16: the largest finite |v| of each of its blocks for values (num_v_maxima of them)
+  int num_v_maxima;
+  int q_blocks;          // row_kernel: blocks for the rows of a kv head, behind which those for its values come
   int* taken;            // dq_kernel: work items taken so far, beyond each block's first
 };
 
-// The power of two that brings `top` to [8, 16); 1 for 0, an infinity or NaN.
-__device__ __forceinline__ float power_for(float top) {
-  if (!(top > 0.f) || top == INFINITY) return 1.f;
-  const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;  // of a subnormal: -127
-  return __uint_as_float(static_cast<uint32_t>(min(max(3 - e, -100), 100) + 127) << 23);
+// The power of two that brings `bound` to [2^14, 2^15); 1 for 0.
+__device__ __forceinline__ float power_for(float bound) {
+  if (!(bound > 0.f)) return 1.f;
+  const int e = static_cast<int>(__float_as_uint(bound) >> 23) - 127;  // (fp16's: -48 to 39)
+  return __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
 }
 
 template <bool BF16>
@@ -259,6 +264,38 @@ __device__ __forceinline__ void few_rows(const GradParams& g, int b, int piece, 
   }
 }
 
+// The largest of `v`, not negative, of a block's threads, in its first one.
+__device__ __forceinline__ float block_max(float v) {
+  __shared__ uint32_t tops[kRowThreads / 32];
+  const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(v));
+  if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = bits;
+  __syncthreads();
+  return __uint_as_float(threadIdx.x < 32 ? __reduce_max_sync(0xffffffffu, threadIdx.x < kRowThreads / 32 ? tops[threadIdx.x] : 0u) : 0u);
+}
+
+// fp16: the largest finite |v| of a block of keys of a kv head.  (With all that the bound takes: three
+// short samples 17.2 us for 16.3 without, 8 of 693 to 2005 tokens 405 for 395.)
+template <int D>
+__device__ __forceinline__ void value_rows(const GradParams& g, int block, int hk) {
+  constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
+  const int from = max(0, __ldg(g.f.cu_k)), to = min(g.f.total_k, __ldg(g.f.cu_k + g.f.B));
+  uint32_t most = 0;
+#pragma unroll
+  for (int i = 0; i < kRowBatch; ++i) {
+    const int64_t key = (static_cast<int64_t>(block) * kRowBatch + i) * kPerPass + threadIdx.x / kLanes;
+    if (key < from || key >= to) continue;
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.v) + key * g.v_strides[0] + hk * g.v_strides[1]) + threadIdx.x % kLanes);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;  // magnitudes: 0x7c00 and up are no numbers
+      most = max(most, max(lo < 0x7c00u ? lo : 0u, hi < 0x7c00u ? hi : 0u));
+    }
+  }
+  const float top = block_max(__half2float(__ushort_as_half(static_cast<unsigned short>(most))));
+  if (threadIdx.x == 0) g.v_maxima[static_cast<int64_t>(hk) * (gridDim.x - g.few_blocks - g.q_blocks) + block] = top;
+}
+
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
@@ -270,6 +307,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g)
     for (int64_t u = blockIdx.x; u < static_cast<int64_t>(p.B) * g.few_units; u += few)
       few_rows<D, BF16>(g, static_cast<int>(u / g.few_units), static_cast<int>(u % g.few_units), blockIdx.y);
     return;
+  }
+  if constexpr (!BF16) {
+    if (static_cast<int>(blockIdx.x) >= few + g.q_blocks) {
+      value_rows<D>(g, blockIdx.x - few - g.q_blocks, blockIdx.y);
+      return;
+    }
   }
   // rows in front of the first sequence and behind the last take no part
   const int from = max(0, __ldg(p.cu_q)), to = min(p.total_q, __ldg(p.cu_q + p.B));
@@ -294,7 +337,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g)
   for (int i = 0; i < kRowBatch; ++i) {
     const int64_t row = static_cast<int64_t>(hk) * p.total_q * p.G + row0 + i * kPerPass;
     const uint32_t wa[4] = {a[i].x, a[i].y, a[i].z, a[i].w}, wc[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-    float delta = 0.f, top = 0.f;
+    float delta = 0.f, norm = 0.f;
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       float2 x, y;
@@ -304,33 +347,28 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g)
       } else {
         x = __half22float2(*reinterpret_cast<const __half2*>(&wa[f]));
         y = __half22float2(*reinterpret_cast<const __half2*>(&wc[f]));
-        top = fmaxf(top, fmaxf(fabsf(x.x), fabsf(x.y)));
+        norm += fabsf(x.x) + fabsf(x.y);
       }
       delta = fmaf(x.x, y.x, fmaf(x.y, y.y, delta));
     }
 #pragma unroll
     for (int o = kLanes / 2; o >= 1; o >>= 1) {
       delta += __shfl_xor_sync(0xffffffffu, delta, o);
-      if constexpr (!BF16) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if constexpr (!BF16) norm += __shfl_xor_sync(0xffffffffu, norm, o);
     }
-    most = fmaxf(most, top);
+    if (!(norm < INFINITY)) norm = 0.f;
+    most = fmaxf(most, norm);
     if (lane == 0 && token[i] >= 0) {
       const float lse = __ldg(g.lse + static_cast<int64_t>(token[i]) * p.Hq + head[i]);
       g.rows[row] = make_float2(lse == -INFINITY ? -INFINITY : -lse * prefill::kLog2e, delta);
-      if constexpr (!BF16) g.powers[row] = power_for(top);
+      if constexpr (!BF16) g.norms[row] = norm;
     }
   }
   if constexpr (!BF16) {
     // (a maximum a block, and not one for the call by an atomic, which something would have to set to 0 first: a
     // launch of some 4 us)
-    __shared__ uint32_t tops[kRowThreads / 32];
-    const uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));
-    if (threadIdx.x % 32 == 0) tops[threadIdx.x / 32] = bits;
-    __syncthreads();
-    if (threadIdx.x < 32) {
-      const uint32_t all = __reduce_max_sync(0xffffffffu, threadIdx.x < kRowThreads / 32 ? tops[threadIdx.x] : 0u);
-      if (threadIdx.x == 0) g.maxima[static_cast<int64_t>(blockIdx.y) * (gridDim.x - few) + blockIdx.x - few] = __uint_as_float(all);
-    }
+    const float top = block_max(most);
+    if (threadIdx.x == 0) g.maxima[static_cast<int64_t>(blockIdx.y) * g.q_blocks + blockIdx.x - few] = top;
   }
 }
 
@@ -416,6 +454,14 @@ struct DqBars {
   __device__ __forceinline__ uint32_t item_read() const { return one(kRest + 14 + kDqItems); }
 };
 
+// The largest of n values, none negative, by a whole warp.
+__device__ __forceinline__ float warp_max(const float* from, int64_t n) {
+  uint32_t top = 0;
+#pragma unroll 8
+  for (int64_t i = threadIdx.x % 32; i < n; i += 32) top = max(top, __float_as_uint(from[i]));
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+}
+
 // A place in a ring, and how often the ring has been gone through before it.
 template <int SLOTS>
 struct Place {
@@ -496,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / p.q_per_tile;
     };
     Finder finder(p.B, !p.causal, pieces);
+    const float values = BF16 ? 0.f : warp_max(gp.v_maxima, gp.num_v_maxima);
     int tiles = 0, tails = 0;          // key tiles of the items so far; K tiles cleared
     int clear_at = -1, clear_row = 0;  // the item before: its last key tile, first row to clear
     bool ok = true, more = true;
@@ -514,6 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           item.seq = load_seq(p, b);
           item.at = t * p.q_per_tile;
           item.head = w % p.Hkv;
+          item.bound = values;
         }
         if (k >= kDqItems)
           ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kDqItems), (k / kDqItems - 1) & 1, p.status));
@@ -693,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t row = item.seq.q0 + i;
       const int64_t at = (item.head * static_cast<int64_t>(p.total_q) + row) * p.G + row_head;
       const float2 rd = valid ? gp.rows[at] : make_float2(-INFINITY, 0.f);
-      const float f = !BF16 && valid ? gp.powers[at] : 1.f;
+      const float f = !BF16 && valid ? power_for(gp.norms[at] * item.bound) : 1.f;
       // (a row of no query is not looked at by anyone: it may see everything)
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
       const float delta = key_lim >= 1 && key_lim <= kFew ? gp.few[at] : rd.y, fd = key_lim == 1 ? 0.f : f;
@@ -816,8 +864,8 @@ struct DkvLayout {
   static constexpr int kShared = kBars + kNumBars * 8;       // work items, turns, tensor memory's address
   // No room is left to align the base by hand: the kernel has no static shared memory, and its dynamic
   // one is declared with this alignment.
-  static constexpr int kTops = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;  // fp16: largest |dout|, a warp each
-  static constexpr int kAlloc = kTops + kThreads / 32 * 4;
+  static constexpr int kTops = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;  // fp16: the largest norm and |v|, a warp each
+  static constexpr int kAlloc = kTops + 2 * kThreads / 32 * 4;
   static constexpr bool kApart = D == 64;
   static constexpr int kDv = 0, kDk = D, kS = 2 * D, kDp = kS + kRows;
   static constexpr int kP = kApart ? kDp + kRows : kS, kDs = kApart ? kP + kRows / 2 : kDp;
@@ -976,11 +1024,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if constexpr (!BF16) {
     wait_for_previous();  // row_kernel
-    uint32_t top = 0;
+    auto most = [&](const float* from, int n, int place) {
+      uint32_t top = 0;
 #pragma unroll 8
-    for (int i = threadIdx.x; i < gp.num_maxima; i += kThreads) top = max(top, __float_as_uint(gp.maxima[i]));
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::kTops)[warp] = top;
+      for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, __float_as_uint(from[i]));
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::kTops)[place] = top;
+    };
+    most(gp.maxima, gp.num_maxima, warp);
+    most(gp.v_maxima, gp.num_v_maxima, kThreads / 32 + warp);
   }
   tc_fence_before();
   __syncthreads();
@@ -988,10 +1040,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = tmem_slot;
   float power = 1.f;  // that dS is held times
   if constexpr (!BF16) {
-    uint32_t top = 0;
+    uint32_t norm = 0, value = 0;
 #pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) top = max(top, reinterpret_cast<const uint32_t*>(smem + L::kTops)[i]);
-    power = power_for(__uint_as_float(top));
+    for (int i = 0; i < kThreads / 32; ++i) {
+      norm = max(norm, reinterpret_cast<const uint32_t*>(smem + L::kTops)[i]);
+      value = max(value, reinterpret_cast<const uint32_t*>(smem + L::kTops)[kThreads / 32 + i]);
+    }
+    power = power_for(__uint_as_float(norm) * __uint_as_float(value));
   }
   if (warp == 11) {
     // --------------- work items; lse and delta of each query row; rows past the end ----------------
@@ -1257,7 +1312,7 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   const int64_t sms = num_sms() > 0 ? num_sms() : 152;
   auto blocks = [&](int64_t items) { return static_cast<unsigned>(items * g.f.Hkv < sms ? items * g.f.Hkv : sms); };
   if (q_items > 0) {
-    row_kernel<D, BF16><<<dim3(g.few_blocks + row_blocks(g.f.total_q, g.f.G, D), g.f.Hkv), kRowThreads, 0, st>>>(g);
+    row_kernel<D, BF16><<<dim3(g.few_blocks + g.q_blocks + (BF16 ? 0 : row_blocks(g.f.total_k, 1, D)), g.f.Hkv), kRowThreads, 0, st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // dq_kernel reads nothing of dkv_kernel's, whose blocks let it start once row_kernel has ended: it takes
@@ -1275,8 +1330,6 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   return cudaGetLastError();
 }
 
-constexpr size_t kWordBytes = 256;  // in front: the items taken
-
 size_t round_up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 size_t row_bytes(const fa_packed_backward_args* a) {
@@ -1287,8 +1340,15 @@ size_t num_maxima(const fa_packed_backward_args* a) {
   return static_cast<size_t>(row_blocks(a->total_q, a->Hq / a->Hkv, a->D)) * a->Hkv;
 }
 
+size_t num_v_maxima(const fa_packed_backward_args* a) {
+  return a->dtype == FA_FP16 ? static_cast<size_t>(row_blocks(a->total_k, 1, a->D)) * a->Hkv : 0;
+}
+
+// In front: the items taken; fp16: the largest |v| of each block of keys.
+size_t front_bytes(const fa_packed_backward_args* a) { return round_up(sizeof(int) + num_v_maxima(a) * sizeof(float)); }
+
 size_t workspace_bytes(const fa_packed_backward_args* a) {
-  return kWordBytes + row_bytes(a) + round_up(row_bytes(a) / 2) +
+  return front_bytes(a) + row_bytes(a) + round_up(row_bytes(a) / 2) +
          (a->dtype == FA_FP16 ? round_up(row_bytes(a) / 2) + round_up(num_maxima(a) * sizeof(float)) : 0);
 }
 
@@ -1366,9 +1426,10 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   memcpy(g.dv_strides, a->dv_strides, sizeof g.dv_strides);
   uint8_t* ws = static_cast<uint8_t*>(a->workspace);
   g.taken = reinterpret_cast<int*>(ws);
-  g.rows = reinterpret_cast<float2*>(ws + packed::kWordBytes);
+  g.q_blocks = static_cast<int>(packed::row_blocks(a->total_q, p.G, a->D));
+  g.rows = reinterpret_cast<float2*>(ws + packed::front_bytes(a));
   const size_t one = packed::round_up(packed::row_bytes(a) / 2) / sizeof(float);  // a float a row
-  g.few = reinterpret_cast<float*>(ws + packed::kWordBytes + packed::row_bytes(a));
+  g.few = reinterpret_cast<float*>(ws + packed::front_bytes(a) + packed::row_bytes(a));
   // pieces of 128 rows: causal, all that a sequence can have of few keys; else, the mean sequence's
   const int64_t rows = p.causal ? static_cast<int64_t>(packed::kFew) * p.G : (static_cast<int64_t>(a->total_q) * p.G + a->B - 1) / a->B;
   g.few_units = static_cast<int>((rows + 127) / 128 > 1 ? (rows + 127) / 128 : 1);
@@ -1381,9 +1442,11 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   memcpy(g.k_strides, a->k_strides, sizeof g.k_strides);
   memcpy(g.v_strides, a->v_strides, sizeof g.v_strides);
   if (a->dtype == FA_FP16) {
-    g.powers = g.few + one;
-    g.maxima = g.powers + one;
+    g.norms = g.few + one;
+    g.maxima = g.norms + one;
     g.num_maxima = static_cast<int>(packed::num_maxima(a));
+    g.v_maxima = reinterpret_cast<float*>(g.taken + 1);
+    g.num_v_maxima = static_cast<int>(packed::num_v_maxima(a));
   }
   const bool bf16 = a->dtype == FA_BF16;
   // Maps of an empty side are read by nothing; they get the workspace as their address.

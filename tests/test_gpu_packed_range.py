@@ -50,3 +50,61 @@ def test_backward_of_a_context_past_the_product_with_the_group(causal):
             value, bound = want[name]
             # (twice the bound: the exponent's rounding counts |lse|, and ln 2000 is not in it)
             ref.check(f"{name} of period {i}", got[at], value / reps, 2 * bound / reps)
+
+
+# ------------------------------------------------------------------ fp16 gradients
+def _check_half(got, q, k, v, dout, causal, scale):
+    """Gradients of one sequence.  dS is held times a power of two that brings the largest sum |dout_i| max |v| (of the
+    row for dq, of the sequence's rows for dk) to 2^14 or more: half the least subnormal over that power, 2^-25 / f
+    with f >= 2^14 / (sum |dout_i| max |v|), in place of the reference's, which knows |dout| alone."""
+    want = ref.attention(q, k, v, causal, scale, dout)
+    n, Hq, D = q.shape
+    m, Hkv = k.shape[:2]
+    G = Hq // Hkv
+    sums = dout.double().abs().sum(-1)                                              # [n,Hq]
+    top = v.double().abs().amax((0, 2)).repeat_interleave(G)                        # [Hq]
+    step = 2.0 ** -25 * sums * top / 2.0 ** 14                                      # of a row
+    seen = ref._visible(n, m, causal).double()
+    kk = k.double().abs().repeat_interleave(G, 1)
+    more = abs(scale) * step[..., None] * torch.einsum("ij,jhd->ihd", seen, kk)
+    value, bound = want["dq"]
+    ref.check("dq", got[0], value, bound + more)
+    of_all = step.view(n, Hkv, G).amax((0, 2))                                      # of the sequence and kv head
+    rows = torch.einsum("ij,ihd->jhd", seen, q.double().abs()).view(m, Hkv, G, D).sum(2)
+    value, bound = want["dk"]
+    ref.check("dk", got[1], value, bound + abs(scale) * of_all[None, :, None] * rows)
+    ref.check("dv", got[2], *want["dv"])
+
+
+@pytest.mark.parametrize("size,big", [(0.0019, 100.0), (1.0, 150.0), (1.0, 1000.0), (2.0 ** -20, 60000.0), (16.0, 0.01)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_half_gradients_of_large_values(D, size, big):
+    """Values aligned with dout: dP = +- D size big, whose products with the power of two have to stay in range.
+    (q and k are small, and so are the gradients.)"""
+    lens = [2, 40, 200]
+    c = Case(lens, 4, 2, D, HF, seed=5)
+    c.x[:, :6] *= 2.0 ** -6
+    sign = torch.where(torch.arange(c.x.shape[0]) % 2 == 0, 1.0, -1.0)[:, None, None]
+    c.x[:, 6:] = (sign * big * (1 + 0.1 * c.x[:, 6:].float().clamp(-0.9, 0.9))).to(HF)
+    c.do = torch.full_like(c.do, size)
+    scale = 1.0 / D
+    for causal in (True, False):
+        q, k, v = c.gpu()
+        out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), causal=causal, scale=scale)
+        got = fa.fa_prefill_packed_backward(c.do.cuda(), q, k, v, out, lse, *c.offsets(), causal=causal,
+                                            scale=scale, workspace=_nan_workspace())
+        for a, b in zip(c.cu, c.cu[1:]):
+            _check_half([t[a:b] for t in got], *(t[a:b] for t in c.cpu()), c.do[a:b], causal, scale)
+
+
+def test_half_gradient_of_two_keys():
+    """The smallest such call: one query, two keys of equal weight, v = +100 and -100, dout 0.0019 in every column."""
+    D = 128
+    q = torch.full((1, 1, D), 2.0 ** -7, dtype=HF)
+    k = torch.full((2, 1, D), 2.0 ** -7, dtype=HF)
+    v = torch.tensor([100.0, -100.0]).view(2, 1, 1).expand(2, 1, D).to(HF).contiguous()
+    do = torch.full((1, 1, D), 0.0019, dtype=HF)
+    cu, cuk = torch.tensor([0, 1], dtype=torch.int32).cuda(), torch.tensor([0, 2], dtype=torch.int32).cuda()
+    out, lse = fa.fa_prefill_packed(q.cuda(), k.cuda(), v.cuda(), cu, cuk, causal=False, scale=0.1)
+    got = fa.fa_prefill_packed_backward(do.cuda(), q.cuda(), k.cuda(), v.cuda(), out, lse, cu, cuk, causal=False, scale=0.1)
+    _check_half(got, q, k, v, do, False, 0.1)
