@@ -716,8 +716,9 @@ size_t fa_packed_workspace_size(const fa_packed_args* args);
  * would show where dP and delta nearly cancel (of one that sees one key dq is 0).
  * dS is rounded to dtype on its way to the products.  FA_FP16: it is held there times a power of two
  * that brings sum_d |dout_id| max |v|, which no |dP_ij| passes, to [2^14, 2^15) (of the row for dq, the
- * largest of all rows for dk and dv; max |v| over all keys), so that it stays in range whatever q, k, v and
- * dout are, and gradients far below 1 keep their bits: what is 2^-39 of that bound, or less, is lost.
+ * largest of the sequence's rows for dk; max |v| over the sequence's keys, or fewer), so that it stays in
+ * range whatever q, k, v and dout are, and gradients far below 1 keep their bits: what is 2^-39 of that
+ * bound, or less, is lost.  What a sequence gets does not depend on the others.
  * (Within a sequence values of q, k, v or dout that are not finite may reach gradients that they have
  * no part in, as 0 times them.)
  * Every row of dq, dk and dv that belongs to a sequence is written (zeros where nothing is seen),

@@ -164,7 +164,7 @@ struct Item {
   int at;    // first query, or key, of the piece in its sequence; -1: no more work
   int head;  // kv head
   int split; // forward: part of the keys
-  float bound; // fp16 gradients: of what the products are held within range by (packed_grad.cu)
+  float value; // dq, fp16: the largest finite |v| of its keys
 };
 
 // A value that is the same in every lane, in a form that the compiler knows to be: the operands of

@@ -28,7 +28,8 @@
 // fp16: dS is held times a power of two, f, so that the small values that gradients have keep their
 // bits (its smallest normal number is 2^-14) and the large ones stay below its largest, 65504.  No |dP_ij| passes
 // b_i = sum_d |dout_id| max |v|, and no |dS_ij|, with delta_i a mean of dP_ij over j by P_ij, b_i / 2: f brings b_i to
-// [2^14, 2^15), of the row in dq_kernel, the largest of the whole call in dkv_kernel, whose sums run over rows.
+// [2^14, 2^15), of the row and the keys that its tile sees in dq_kernel, of the key tile and the largest row that may see it
+// in dkv_kernel, whose sums run over rows; another sequence has no part in either.
 // (What |dout| alone would give, dS of values of 100 can pass.)  P is held times 2^7 there.  bf16 has fp32's
 // exponents, and f = 1.
 #include <math.h>
@@ -65,11 +66,10 @@ struct GradParams {
   float* norms;          // fp16: sum of |dout| of the row; 0 where that is no number, or infinite
   float* few;            // delta of the rows that see few keys, likewise
   int few_units, few_blocks;  // row_kernel: pieces of such rows of a sequence; blocks for them, in front
-  float* maxima;         // fp16: the largest of `norms` in each block of row_kernel (num_maxima of them)
-  int num_maxima;
-  float* v_maxima;       // fp16: the largest finite |v| of each of its blocks for values (num_v_maxima of them)
-  int num_v_maxima;
-  int q_blocks;          // row_kernel: blocks for the rows of a kv head, behind which those for its values come
+  float* maxima;         // fp16: the largest of `norms` in each block of row_kernel, [Hkv, q_blocks]
+  float* v_norms;        // fp16: the largest finite |v| of each key, [Hkv, total_k]
+  float* v_maxima;       // fp16: and of each of its blocks for values, [Hkv, k_blocks]
+  int q_blocks, k_blocks;  // row_kernel: blocks for the rows of a kv head, behind which those for its values come
   int* taken;            // dq_kernel: work items taken so far, beyond each block's first
 };
 
@@ -152,9 +152,11 @@ __device__ __forceinline__ void product_ts(uint32_t d, uint32_t a, uint32_t half
 constexpr int kRowThreads = 256;
 constexpr int kRowBatch = 4;
 
+constexpr int row_block(int D) { return kRowThreads / (D / 8) * kRowBatch; }  // rows of a block
+
 // Blocks for the rows of a kv head.
 unsigned row_blocks(int total_q, int G, int D) {
-  const int64_t per = kRowThreads / (D / 8) * kRowBatch;
+  const int64_t per = row_block(D);
   return static_cast<unsigned>((static_cast<int64_t>(total_q) * G + per - 1) / per);
 }
 
@@ -273,27 +275,41 @@ __device__ __forceinline__ float block_max(float v) {
   return __uint_as_float(threadIdx.x < 32 ? __reduce_max_sync(0xffffffffu, threadIdx.x < kRowThreads / 32 ? tops[threadIdx.x] : 0u) : 0u);
 }
 
-// fp16: the largest finite |v| of a block of keys of a kv head.  (With all that the bound takes: three
-// short samples 17.2 us for 16.3 without, 8 of 693 to 2005 tokens 405 for 395.)
+// fp16: the largest finite |v| of each key of a kv head, and of the block.  (With all that the bound takes: three short
+// samples 17.3 us for 16.7 without, 8 of 693 to 2005 tokens 404 for 393.)
 template <int D>
 __device__ __forceinline__ void value_rows(const GradParams& g, int block, int hk) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
   const int from = max(0, __ldg(g.f.cu_k)), to = min(g.f.total_k, __ldg(g.f.cu_k + g.f.B));
-  uint32_t most = 0;
+  const int lane = threadIdx.x % kLanes;
+  const int64_t key0 = static_cast<int64_t>(block) * (kPerPass * kRowBatch) + threadIdx.x / kLanes;
+  uint4 x[kRowBatch];
 #pragma unroll
   for (int i = 0; i < kRowBatch; ++i) {
-    const int64_t key = (static_cast<int64_t>(block) * kRowBatch + i) * kPerPass + threadIdx.x / kLanes;
-    if (key < from || key >= to) continue;
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.v) + key * g.v_strides[0] + hk * g.v_strides[1]) + threadIdx.x % kLanes);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    const int64_t key = key0 + i * kPerPass;
+    x[i] = make_uint4(0, 0, 0, 0);
+    if (key >= from && key < to)
+      x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.v) + key * g.v_strides[0] + hk * g.v_strides[1]) + lane);
+  }
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < kRowBatch; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t top = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t lo = w[e] & 0x7fffu, hi = (w[e] >> 16) & 0x7fffu;  // magnitudes: 0x7c00 and up are no numbers
-      most = max(most, max(lo < 0x7c00u ? lo : 0u, hi < 0x7c00u ? hi : 0u));
+      top = max(top, max(lo < 0x7c00u ? lo : 0u, hi < 0x7c00u ? hi : 0u));
     }
+#pragma unroll
+    for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(top)));
+    const int64_t key = key0 + i * kPerPass;
+    if (lane == 0 && key >= from && key < to) g.v_norms[static_cast<int64_t>(hk) * g.f.total_k + key] = v;
+    most = fmaxf(most, v);
   }
-  const float top = block_max(__half2float(__ushort_as_half(static_cast<unsigned short>(most))));
-  if (threadIdx.x == 0) g.v_maxima[static_cast<int64_t>(hk) * (gridDim.x - g.few_blocks - g.q_blocks) + block] = top;
+  most = block_max(most);
+  if (threadIdx.x == 0) g.v_maxima[static_cast<int64_t>(hk) * g.k_blocks + block] = most;
 }
 
 template <int D, bool BF16>
@@ -454,12 +470,48 @@ struct DqBars {
   __device__ __forceinline__ uint32_t item_read() const { return one(kRest + 14 + kDqItems); }
 };
 
-// The largest of n values, none negative, by a whole warp.
-__device__ __forceinline__ float warp_max(const float* from, int64_t n) {
-  uint32_t top = 0;
+// The largest of the values first .. end - 1, none negative, by a whole warp: of blocks of PER by their own
+// largest, of those at either end that reach beyond, one by one.  The loads start with it; the answer may be
+// asked for later.
+template <int PER>
+class Largest {
+ public:
+  __device__ __forceinline__ Largest(const float* each, const float* blocks, int64_t first, int64_t end)
+      : blocks_(blocks), next_((first + PER - 1) / PER + threadIdx.x % 32), end_(end / PER) {
+    const int lane = threadIdx.x % 32;
+    const int64_t head = min(end, (first + PER - 1) / PER * PER), tail = max(head, end_ * PER);
+#pragma unroll
+    for (int i = 0; i < kEdge; ++i) {
+      held_[2 * i] = first + 32 * i + lane < head ? each[first + 32 * i + lane] : 0.f;
+      held_[2 * i + 1] = tail + 32 * i + lane < end ? each[tail + 32 * i + lane] : 0.f;
+    }
+    held_[2 * kEdge] = next_ < end_ ? blocks[next_] : 0.f;
+  }
+
+  __device__ __forceinline__ float get() {
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i <= 2 * kEdge; ++i) top = fmaxf(top, held_[i]);
 #pragma unroll 8
-  for (int64_t i = threadIdx.x % 32; i < n; i += 32) top = max(top, __float_as_uint(from[i]));
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+    for (int64_t b = next_ + 32; b < end_; b += 32) top = fmaxf(top, blocks_[b]);
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+  }
+
+ private:
+  static constexpr int kEdge = PER / 32;
+  const float* blocks_;
+  int64_t next_, end_;
+  float held_[2 * kEdge + 1];
+};
+
+// fp16: of a kv head's keys, or rows.
+template <int D>
+__device__ __forceinline__ Largest<row_block(D)> largest_value(const GradParams& g, int hk, int64_t first, int64_t end) {
+  return {g.v_norms + static_cast<int64_t>(hk) * g.f.total_k, g.v_maxima + static_cast<int64_t>(hk) * g.k_blocks, first, end};
+}
+template <int D>
+__device__ __forceinline__ Largest<row_block(D)> largest_norm(const GradParams& g, int hk, int64_t first, int64_t end) {
+  return {g.norms + static_cast<int64_t>(hk) * g.f.total_q * g.f.G, g.maxima + static_cast<int64_t>(hk) * g.q_blocks, first, end};
 }
 
 // A place in a ring, and how often the ring has been gone through before it.
@@ -479,6 +531,13 @@ __device__ __forceinline__ int key_tiles(const Params& p, const Seq& s, int q0) 
   const int last = min(s.nq, q0 + p.q_per_tile) - 1;
   const int end = p.causal ? min(s.nk, max(0, last + s.nk - s.nq + 1)) : s.nk;
   return (end + kKeys - 1) / kKeys;
+}
+
+// fp16: the largest finite |v| of the keys that dq_kernel's item walks over.
+template <int D>
+__device__ __forceinline__ float largest_seen(const GradParams& g, const Item& item) {
+  const int64_t n = min(item.seq.nk, key_tiles(g.f, item.seq, item.at) * kKeys);
+  return largest_value<D>(g, item.head, item.seq.k0, item.seq.k0 + n).get();
 }
 
 template <int D, bool BF16>
@@ -542,7 +601,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       first = (p.causal ? max(0, q.nk - q.nq) : q.nk) / p.q_per_tile;
     };
     Finder finder(p.B, !p.causal, pieces);
-    const float values = BF16 ? 0.f : warp_max(gp.v_maxima, gp.num_v_maxima);
     int tiles = 0, tails = 0;          // key tiles of the items so far; K tiles cleared
     int clear_at = -1, clear_row = 0;  // the item before: its last key tile, first row to clear
     bool ok = true, more = true;
@@ -561,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           item.seq = load_seq(p, b);
           item.at = t * p.q_per_tile;
           item.head = w % p.Hkv;
-          item.bound = values;
+          if constexpr (!BF16) item.value = largest_seen<D>(gp, item);
         }
         if (k >= kDqItems)
           ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kDqItems), (k / kDqItems - 1) & 1, p.status));
@@ -741,10 +799,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t row = item.seq.q0 + i;
       const int64_t at = (item.head * static_cast<int64_t>(p.total_q) + row) * p.G + row_head;
       const float2 rd = valid ? gp.rows[at] : make_float2(-INFINITY, 0.f);
-      const float f = !BF16 && valid ? power_for(gp.norms[at] * item.bound) : 1.f;
+      const float norm = !BF16 && valid ? gp.norms[at] : 0.f;
       // (a row of no query is not looked at by anyone: it may see everything)
       const int key_lim = !valid ? 0x7fffffff : p.causal ? min(item.seq.nk, i + item.seq.nk - item.seq.nq + 1) : item.seq.nk;
-      const float delta = key_lim >= 1 && key_lim <= kFew ? gp.few[at] : rd.y, fd = key_lim == 1 ? 0.f : f;
+      const float delta = key_lim >= 1 && key_lim <= kFew ? gp.few[at] : rd.y;
+      const float f = BF16 ? 1.f : power_for(norm * item.value);
+      const float fd = key_lim == 1 ? 0.f : f;
       const float2 nl2 = make_float2(rd.x, rd.x), f2 = make_float2(fd, fd), nd2 = make_float2(-delta * fd, -delta * fd);
       for (int j = -1; j < n; ++j) {
         if (j >= 0) {
@@ -864,8 +924,8 @@ struct DkvLayout {
   static constexpr int kShared = kBars + kNumBars * 8;       // work items, turns, tensor memory's address
   // No room is left to align the base by hand: the kernel has no static shared memory, and its dynamic
   // one is declared with this alignment.
-  static constexpr int kTops = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;  // fp16: the largest norm and |v|, a warp each
-  static constexpr int kAlloc = kTops + 2 * kThreads / 32 * 4;
+  static constexpr int kPowers = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;  // fp16: [2], beside the row data
+  static constexpr int kAlloc = kPowers + 2 * 4;
   static constexpr bool kApart = D == 64;
   static constexpr int kDv = 0, kDk = D, kS = 2 * D, kDp = kS + kRows;
   static constexpr int kP = kApart ? kDp + kRows : kS, kDs = kApart ? kP + kRows / 2 : kDp;
@@ -1022,32 +1082,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       clear_rows<D>(smem + L::kRing + s * L::kTile, used, threadIdx.x, kThreads);
     fence_proxy_async_smem();
   }
-  if constexpr (!BF16) {
-    wait_for_previous();  // row_kernel
-    auto most = [&](const float* from, int n, int place) {
-      uint32_t top = 0;
-#pragma unroll 8
-      for (int i = threadIdx.x; i < n; i += kThreads) top = max(top, __float_as_uint(from[i]));
-      top = __reduce_max_sync(0xffffffffu, top);
-      if (lane == 0) reinterpret_cast<uint32_t*>(smem + L::kTops)[place] = top;
-    };
-    most(gp.maxima, gp.num_maxima, warp);
-    most(gp.v_maxima, gp.num_v_maxima, kThreads / 32 + warp);
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  float power = 1.f;  // that dS is held times
-  if constexpr (!BF16) {
-    uint32_t norm = 0, value = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      norm = max(norm, reinterpret_cast<const uint32_t*>(smem + L::kTops)[i]);
-      value = max(value, reinterpret_cast<const uint32_t*>(smem + L::kTops)[kThreads / 32 + i]);
-    }
-    power = power_for(__uint_as_float(norm) * __uint_as_float(value));
-  }
   if (warp == 11) {
     // --------------- work items; lse and delta of each query row; rows past the end ----------------
     wait_for_previous();  // row_kernel
@@ -1081,7 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bars.item() + 8u * (k % kItems));
       }
     };
-    const float f = kUnpower * power;
+    float power = 1.f;  // that the item's dS is held times
     int step = 0, tails = 0;
     int token[4];  // of the tile's, of the lane's rows
 #pragma unroll
@@ -1089,10 +1127,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item item = find(0);
     publish(0, item);
     for (int k = 0; ok && item.at >= 0; ++k) {
-      const Item ahead = find(k + 1);
-      publish(k + 1, ahead);
       int first_tile;
       const int n = query_tiles(p, item.seq, item.at, first_tile);
+      Item ahead;
+      auto look_ahead = [&]() {
+        ahead = find(k + 1);
+        publish(k + 1, ahead);
+      };
+      if constexpr (BF16) {
+        look_ahead();
+      } else {
+        // The item's power goes with the row data and not with the item, so that the first tiles' copies and products do not
+        // wait for it, and what it is found from loads beside the search (three short samples: 18.1 us without that, 17.3 with it).
+        const int64_t key = item.seq.k0 + static_cast<int64_t>(item.at), row = item.seq.q0 + static_cast<int64_t>(first_tile) * p.q_per_tile;
+        auto value = largest_value<D>(gp, item.head, key, n > 0 ? key + min(kKeys, item.seq.nk - item.at) : key);
+        auto norm = largest_norm<D>(gp, item.head, row * p.G, n > 0 ? (item.seq.q0 + static_cast<int64_t>(item.seq.nq)) * p.G : row * p.G);
+        look_ahead();
+        power = power_for(value.get() * norm.get());
+      }
       const int last_rows = n > 0 ? (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G : used;
       for (int i = 0; ok && i < n; ++i, ++step) {
         const int q0 = (first_tile + i) * p.q_per_tile;
@@ -1107,15 +1159,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 rd = gp.rows[at + e];
             const int sees = p.causal ? q0 + token[e] + item.seq.nk - item.seq.nq + 1 : item.seq.nk;
             nl[e] = rd.x + kPower;
-            nd[e] = -f * (sees >= 1 && sees <= kFew ? gp.few[at + e] : rd.y);
+            nd[e] = sees >= 1 && sees <= kFew ? gp.few[at + e] : rd.y;
           }
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) nd[e] *= -kUnpower * power;
         if (step >= 2)
           ok = __all_sync(0xffffffffu, mbar_wait(bars.rows_read(step & 1), (step / 2 - 1) & 1, p.status));
         float* to = reinterpret_cast<float*>(smem + L::kRowData) + (step & 1) * 2 * kRows + lane * 4;
         if (ok) {
           *reinterpret_cast<float4*>(to) = make_float4(nl[0], nl[1], nl[2], nl[3]);
           *reinterpret_cast<float4*>(to + kRows) = make_float4(nd[0], nd[1], nd[2], nd[3]);
+          if (!BF16 && lane == 0) reinterpret_cast<float*>(smem + L::kPowers)[step & 1] = power;
           mbar_arrive(bars.rows(step & 1));
         }
         if (ok && i == n - 1 && last_rows < used) {
@@ -1189,8 +1244,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t tm_s = tmem + L::kS + w * kHalf + lanes, tm_dp = tmem + L::kDp + w * kHalf + lanes;
     const uint32_t tm_p = tmem + L::kP + w * L::kStep + lanes, tm_ds = tmem + L::kDs + w * L::kStep + lanes;
-    const float f = power;
-    const float2 a2 = make_float2(p.scale_log2, p.scale_log2), f2 = make_float2(f * kUnpower, f * kUnpower);
+    float f = 1.f;  // that the item's dS is held times
+    float2 f2 = make_float2(kUnpower, kUnpower);
+    const float2 a2 = make_float2(p.scale_log2, p.scale_log2);
     bool ok = true;
     int step = 0;
     Item item;
@@ -1209,6 +1265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 nl[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) nl[c] = row_data[c];
+        if (!BF16 && i == 0) {
+          f = reinterpret_cast<const float*>(smem + L::kPowers)[step & 1];
+          f2 = make_float2(f * kUnpower, f * kUnpower);
+        }
         ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.first(0), step & 1, p.status));
         if (!ok) break;
         tc_fence_after();
@@ -1312,7 +1372,7 @@ cudaError_t launch(const GradParams& g, const CUtensorMap (&maps)[4], int64_t q_
   const int64_t sms = num_sms() > 0 ? num_sms() : 152;
   auto blocks = [&](int64_t items) { return static_cast<unsigned>(items * g.f.Hkv < sms ? items * g.f.Hkv : sms); };
   if (q_items > 0) {
-    row_kernel<D, BF16><<<dim3(g.few_blocks + g.q_blocks + (BF16 ? 0 : row_blocks(g.f.total_k, 1, D)), g.f.Hkv), kRowThreads, 0, st>>>(g);
+    row_kernel<D, BF16><<<dim3(g.few_blocks + g.q_blocks + g.k_blocks, g.f.Hkv), kRowThreads, 0, st>>>(g);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // dq_kernel reads nothing of dkv_kernel's, whose blocks let it start once row_kernel has ended: it takes
@@ -1340,12 +1400,11 @@ size_t num_maxima(const fa_packed_backward_args* a) {
   return static_cast<size_t>(row_blocks(a->total_q, a->Hq / a->Hkv, a->D)) * a->Hkv;
 }
 
-size_t num_v_maxima(const fa_packed_backward_args* a) {
-  return a->dtype == FA_FP16 ? static_cast<size_t>(row_blocks(a->total_k, 1, a->D)) * a->Hkv : 0;
+// In front: the items taken; fp16: the largest |v| of each block of keys and of each key.
+size_t front_bytes(const fa_packed_backward_args* a) {
+  const size_t values = a->dtype == FA_FP16 ? (static_cast<size_t>(row_blocks(a->total_k, 1, a->D)) + a->total_k) * a->Hkv : 0;
+  return round_up(sizeof(int) + values * sizeof(float));
 }
-
-// In front: the items taken; fp16: the largest |v| of each block of keys.
-size_t front_bytes(const fa_packed_backward_args* a) { return round_up(sizeof(int) + num_v_maxima(a) * sizeof(float)); }
 
 size_t workspace_bytes(const fa_packed_backward_args* a) {
   return front_bytes(a) + row_bytes(a) + round_up(row_bytes(a) / 2) +
@@ -1444,9 +1503,9 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   if (a->dtype == FA_FP16) {
     g.norms = g.few + one;
     g.maxima = g.norms + one;
-    g.num_maxima = static_cast<int>(packed::num_maxima(a));
+    g.k_blocks = static_cast<int>(packed::row_blocks(a->total_k, 1, a->D));
     g.v_maxima = reinterpret_cast<float*>(g.taken + 1);
-    g.num_v_maxima = static_cast<int>(packed::num_v_maxima(a));
+    g.v_norms = g.v_maxima + static_cast<size_t>(g.k_blocks) * a->Hkv;
   }
   const bool bf16 = a->dtype == FA_BF16;
   // Maps of an empty side are read by nothing; they get the workspace as their address.

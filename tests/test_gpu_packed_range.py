@@ -108,3 +108,33 @@ def test_half_gradient_of_two_keys():
     out, lse = fa.fa_prefill_packed(q.cuda(), k.cuda(), v.cuda(), cu, cuk, causal=False, scale=0.1)
     got = fa.fa_prefill_packed_backward(do.cuda(), q.cuda(), k.cuda(), v.cuda(), out, lse, cu, cuk, causal=False, scale=0.1)
     _check_half(got, q, k, v, do, False, 0.1)
+
+
+# ------------------------------------------------------------------ samples of a pack
+@pytest.mark.parametrize("lens", [[150, 150], [70, 1, 133, 40], [64, 128, 5]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_half_gradients_of_a_sample_are_its_own(D, lens):
+    """Samples whose dout, and whose values, are powers of two apart, and one of infinities: each has the bits of the same sample
+    packed alone, and is inside bounds that know nothing of the others."""
+    c = Case(lens, 8, 2, D, HF, seed=23)
+    sizes = [2.0 ** 12, 2.0 ** -8, 1.0, 2.0 ** -12]
+    for i, (a, b) in enumerate(zip(c.cu, c.cu[1:])):
+        c.do[a:b] = (c.do[a:b].float() * sizes[i % 4]).to(HF)
+        c.x[a:b, 10:] = (c.x[a:b, 10:].float() * sizes[(i + 1) % 4]).to(HF)
+    scale = 1.0 / math.sqrt(D)
+    for infinite in (False, True):
+        do = c.do.clone()
+        if infinite:
+            do[c.cu[1] - 1, 0, 0] = INF  # of the first sample
+        q, k, v = c.gpu()
+        out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), scale=scale)
+        got = fa.fa_prefill_packed_backward(do.cuda(), q, k, v, out, lse, *c.offsets(), scale=scale)
+        for i, (a, b) in enumerate(zip(c.cu, c.cu[1:])):
+            if infinite and i == 0:
+                continue
+            one = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+            alone = fa.fa_prefill_packed_backward(do[a:b].cuda(), q[a:b], k[a:b], v[a:b], out[a:b], lse[a:b], one,
+                                                  scale=scale)
+            for name, x, y in zip(("dq", "dk", "dv"), got, alone):
+                assert torch.equal(x[a:b], y), (name, i)
+            _check_half([t[a:b] for t in got], *(t[a:b] for t in c.cpu()), do[a:b], True, scale)
