@@ -266,6 +266,19 @@ __device__ __forceinline__ void few_rows(const GradParams& g, int b, int piece, 
   }
 }
 
+// Whether tokens t0 .. t1, a block's, are to be looked at: all between the first offset and the last are (if
+// offsets are broken there, nobody asks for what stands beside them); of others, padding as a rule, those of a
+// sequence, by the rule that the other kernels have, for it may lie outside where those two are the broken ones.
+__device__ __forceinline__ bool wanted(const int32_t* cu, int B, int total, int64_t t0, int64_t t1) {
+  if (t0 >= __ldg(cu) && t1 < __ldg(cu + B)) return true;
+  bool mine = false;
+  for (int b = threadIdx.x; b < B; b += kRowThreads) {
+    const int first = __ldg(cu + b), end = __ldg(cu + b + 1);
+    mine = mine || (first >= 0 && first < end && end <= total && first <= t1 && t0 < end);
+  }
+  return __syncthreads_or(mine);
+}
+
 // The largest of `v`, not negative, of a block's threads, in its first one.
 __device__ __forceinline__ float block_max(float v) {
   __shared__ uint32_t tops[kRowThreads / 32];
@@ -280,15 +293,15 @@ __device__ __forceinline__ float block_max(float v) {
 template <int D>
 __device__ __forceinline__ void value_rows(const GradParams& g, int block, int hk) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
-  const int from = max(0, __ldg(g.f.cu_k)), to = min(g.f.total_k, __ldg(g.f.cu_k + g.f.B));
-  const int lane = threadIdx.x % kLanes;
-  const int64_t key0 = static_cast<int64_t>(block) * (kPerPass * kRowBatch) + threadIdx.x / kLanes;
+  const int lane = threadIdx.x % kLanes, end = g.f.total_k;
+  const int64_t start = static_cast<int64_t>(block) * row_block(D), key0 = start + threadIdx.x / kLanes;
+  if (!wanted(g.f.cu_k, g.f.B, end, start, min(start + row_block(D), static_cast<int64_t>(end)) - 1)) return;
   uint4 x[kRowBatch];
 #pragma unroll
   for (int i = 0; i < kRowBatch; ++i) {
     const int64_t key = key0 + i * kPerPass;
     x[i] = make_uint4(0, 0, 0, 0);
-    if (key >= from && key < to)
+    if (key < end)
       x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.v) + key * g.v_strides[0] + hk * g.v_strides[1]) + lane);
   }
   float most = 0.f;
@@ -305,7 +318,7 @@ __device__ __forceinline__ void value_rows(const GradParams& g, int block, int h
     for (int o = kLanes / 2; o >= 1; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float v = __half2float(__ushort_as_half(static_cast<unsigned short>(top)));
     const int64_t key = key0 + i * kPerPass;
-    if (lane == 0 && key >= from && key < to) g.v_norms[static_cast<int64_t>(hk) * g.f.total_k + key] = v;
+    if (lane == 0 && key < end) g.v_norms[static_cast<int64_t>(hk) * g.f.total_k + key] = v;
     most = fmaxf(most, v);
   }
   most = block_max(most);
@@ -330,10 +343,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g)
       return;
     }
   }
-  // rows in front of the first sequence and behind the last take no part
-  const int from = max(0, __ldg(p.cu_q)), to = min(p.total_q, __ldg(p.cu_q + p.B));
+  const uint32_t start = (blockIdx.x - few) * row_block(D);  // of the kv head's rows
+  if (!wanted(p.cu_q, p.B, p.total_q, start / p.G, min((start + row_block(D) - 1) / p.G, p.total_q - 1u))) return;
   const int lane = threadIdx.x % kLanes;
-  const uint32_t row0 = (blockIdx.x - few) * (kPerPass * kRowBatch) + threadIdx.x / kLanes;  // of the kv head's
+  const uint32_t row0 = start + threadIdx.x / kLanes;
   const int hk = blockIdx.y;
   uint4 a[kRowBatch], c[kRowBatch];
   int token[kRowBatch], head[kRowBatch];
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g)
     token[i] = static_cast<int>(row / static_cast<uint32_t>(p.G));
     head[i] = hk * p.G + static_cast<int>(row - token[i] * p.G);
     a[i] = c[i] = make_uint4(0, 0, 0, 0);
-    if (token[i] < from || token[i] >= to) token[i] = -1;
+    if (token[i] >= p.total_q) token[i] = -1;
     if (token[i] < 0) continue;
     a[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.dout) + token[i] * g.dout_strides[0] + head[i] * g.dout_strides[1]) + lane);
     c[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g.o) + token[i] * g.o_strides[0] + head[i] * g.o_strides[1]) + lane);

@@ -52,6 +52,33 @@ def test_backward_of_a_context_past_the_product_with_the_group(causal):
             ref.check(f"{name} of period {i}", got[at], value / reps, 2 * bound / reps)
 
 
+# ------------------------------------------------------------------ broken offsets
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("offsets,first,end", [
+    ([0, 64, 32], 0, 64), ([-5, 64, 128], 64, 128), ([0, 64, 129], 0, 64), ([100, 0, 64], 0, 64),
+    ([0, 90, 3, 2], 0, 90), ([0, 100, 2 ** 31 - 1], 0, 100), ([128, 128, 5, 100, 0], 5, 100)])
+def test_gradients_beside_broken_offsets(offsets, first, end, dtype):
+    """A sequence whose offsets hold has its gradients, whatever stands beside it; other rows stay as they were."""
+    c = Case([128], 4, 2, 64, dtype, seed=17)
+    q, k, v = c.gpu()
+    cu = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    out = torch.full((128, 4, 64), NAN, dtype=dtype, device="cuda")
+    lse = torch.full((128, 4), NAN, device="cuda")
+    fa.fa_prefill_packed(q, k, v, cu, scale=0.125, out=out, lse=lse)
+    dq = torch.full_like(out, 7.0)
+    dk, dv = (torch.full((128, 2, 64), 7.0, dtype=dtype, device="cuda") for _ in range(2))
+    do = c.do.clone()
+    do[:first], do[end:] = NAN, NAN
+    fa.fa_prefill_packed_backward(do.cuda(), q, k, v, out, lse, cu, scale=0.125, dq=dq, dk=dk, dv=dv,
+                                  workspace=_nan_workspace())
+    assert fa.fa_get_device_status() == fa.FA_ERR_BOUNDS
+    at = slice(first, end)
+    want = ref.attention(*(t[at] for t in c.cpu()), True, 0.125, c.do[at])
+    for name, t in (("dq", dq), ("dk", dk), ("dv", dv)):
+        ref.check(name, t[at], *want[name])
+        assert (t[:first] == 7).all() and (t[end:] == 7).all()
+
+
 # ------------------------------------------------------------------ fp16 gradients
 def _check_half(got, q, k, v, dout, causal, scale):
     """Gradients of one sequence.  dS is held times a power of two that brings the largest sum |dout_i| max |v| (of the
