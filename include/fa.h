@@ -669,9 +669,9 @@ size_t fa_tree_workspace_size(const fa_tree_args* args);
  *   cu_seqlens_q, cu_seqlens_k [B + 1] int32 (device), not decreasing
  *   D in {64, 128}; Hq % Hkv == 0, Hq / Hkv <= 128, Hkv <= 65535; total_q * Hq and total_k * Hkv
  *   below 2^31 - 2^16.  out must not overlap an input.
- * A row that sees no key gets out = 0 and lse = -inf.  Rows of out and lse in front of the first
- * sequence and behind the last are left as they were, and what q, k and v hold there, or in other
- * sequences, takes no part.  (Within a sequence a value of v that is not finite may reach
+ * A row that sees no key gets out = 0 and lse = -inf, one with a NaN among its scores NaN in both.
+ * Rows of out and lse in front of the first sequence and behind the last are left as they were, and
+ * what q, k and v hold there, or in other sequences, takes no part.  (Within a sequence a value of v that is not finite may reach
  * rows that do not see it, as 0 times it.)
  * Sequences whose offsets decrease or reach out of the tensor set FA_ERR_BOUNDS in the device
  * status word and are taken as empty.

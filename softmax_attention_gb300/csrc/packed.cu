@@ -615,7 +615,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
           }
-          if (lse_row) *lse_row = prefill::row_lse(out_m, out_l);
+          // (no key seen: -inf; a NaN among the scores: l is NaN, and so is lse)
+          if (lse_row) *lse_row = out_l == 0.f ? -INFINITY : (out_m + log2f(out_l)) * kLn2;
         }
       }
       if (!ok || !more) break;

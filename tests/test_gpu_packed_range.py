@@ -1,5 +1,5 @@
 """Packed prompts at the ends of their range: long contexts, offsets that are broken beside ones that are
-not, fp16 gradients over all of fp16's range, scores that are no number.  Against the plain 64-bit
+not, fp16 gradients over all of fp16's range, scores that are no number or infinite.  Against the plain 64-bit
 references with derived bounds (tests/_packed_ref.py)."""
 import math
 
@@ -165,3 +165,21 @@ def test_half_gradients_of_a_sample_are_its_own(D, lens):
             for name, x, y in zip(("dq", "dk", "dv"), got, alone):
                 assert torch.equal(x[a:b], y), (name, i)
             _check_half([t[a:b] for t in got], *(t[a:b] for t in c.cpu()), do[a:b], True, scale)
+
+
+# ------------------------------------------------------------------ scores that are no number
+@pytest.mark.parametrize("D,dtype", [(64, HF), (128, BF)])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_a_nan_score_reaches_lse(D, dtype, splits):
+    """A NaN in a key: out and lse of every row that sees it are NaN, the others' as ever."""
+    for at in (0, 37, 200, 389):
+        c = Case([90], 4, 2, D, dtype, klens=[390], seed=19)
+        c.y[at, :2, 5] = NAN
+        q, k, v = c.gpu()
+        out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), scale=0.1, num_splits=splits)
+        clean = Case([90], 4, 2, D, dtype, klens=[390], seed=19)
+        want = next(clean.want(True, 0.1))[2]
+        n = max(0, min(90, at - 300))  # rows in front of the key
+        assert out[n:].isnan().all() and lse[n:].isnan().all()
+        ref.check("out", out[:n], *(t[:n] for t in want["out"]))
+        ref.check("lse", lse[:n], *(t[:n] for t in want["lse"]))
