@@ -671,8 +671,8 @@ size_t fa_tree_workspace_size(const fa_tree_args* args);
  *   below 2^31 - 2^16.  out must not overlap an input.
  * A row that sees no key gets out = 0 and lse = -inf, one with a NaN among its scores NaN in both.
  * Rows of out and lse in front of the first sequence and behind the last are left as they were, and
- * what q, k and v hold there, or in other sequences, takes no part.  (Within a sequence a value of v that is not finite may reach
- * rows that do not see it, as 0 times it.)
+ * what q, k and v hold there, or in other sequences, takes no part.  (Within a sequence a value of v
+ * that is not finite may reach rows that do not see it, as 0 times it.)
  * Sequences whose offsets decrease or reach out of the tensor set FA_ERR_BOUNDS in the device
  * status word and are taken as empty.
  * num_splits: parts that each sequence's keys are split into, 0 (the library's choice: more than one

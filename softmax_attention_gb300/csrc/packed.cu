@@ -512,14 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (a > 0.f) {
             const bool masked = __any_sync(0xffffffffu, left < kKeys);
             if (j == 0) {
-              // a first guess at the maximum: that of the first 32 scores
+              // A first guess at the maximum: that of the first 32 scores.  Where all of them are hidden or -inf, one
+              // below every score: the first that is finite then takes the slow path, however small it is.
               uint32_t raw[32];
               tmem_ld32(tm_s, raw);
               prefill::tmem_ld_wait_tied(raw);
               float top = -INFINITY;
   #pragma unroll
               for (int e = 0; e < 32; ++e) top = fmaxf(top, e < left ? __uint_as_float(raw[e]) : -INFINITY);
-              m = top > -INFINITY ? top * a : 0.f;
+              m = top > -INFINITY ? top * a : -1e37f;
             }
             uint32_t pk[kKeys / 2];
             float2 sum = make_float2(0.f, 0.f);

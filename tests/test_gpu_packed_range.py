@@ -183,3 +183,24 @@ def test_a_nan_score_reaches_lse(D, dtype, splits):
         assert out[n:].isnan().all() and lse[n:].isnan().all()
         ref.check("out", out[:n], *(t[:n] for t in want["out"]))
         ref.check("lse", lse[:n], *(t[:n] for t in want["lse"]))
+
+
+# ------------------------------------------------------------------ infinite scores
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("hidden", [20, 40, 150])
+def test_scores_of_minus_infinity(hidden, splits, causal):
+    """Keys of which a column is -inf, in front of keys with scores far below 0: weights of 0, and no bearing on the rest."""
+    L, D = 400, 64
+    c = Case([L], 2, 1, D, HF, seed=6)
+    c.x[:, :2, 0] = 8.0
+    c.x[:, 2, 0] = -100.0
+    clean = c.x.clone()
+    c.x[:hidden, 2, 0] = -INF
+    q, k, v = c.gpu()
+    out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), causal=causal, scale=1.0, num_splits=splits)
+    # rows from `hidden` on: what the other keys alone give
+    q, k, v = c.views(clean[hidden:], None)
+    want = ref.attention(q, k, v, causal, 1.0)
+    for name, got in (("out", out), ("lse", lse)):
+        ref.check(name, got[hidden:], *want[name])
