@@ -181,8 +181,8 @@ struct Bars {
 
 // The k-th item, copied from its place in shared memory; false: no more, or a wait ran out.
 template <int D>
-__device__ __forceinline__ bool next_item(const Bars<D>& bars, const Item* items, int k, Item& item, uint32_t* status) {
-  if (!mbar_wait(bars.item(k % kItems), (k / kItems) & 1, status)) return false;
+__device__ __forceinline__ bool next_item(const Bars<D>& bars, const Item* items, int k, Item& item, const Params& p) {
+  if (!mbar_wait(bars.item(k % kItems), (k / kItems) & 1, p)) return false;
   item = items[k % kItems];
   mbar_arrive(bars.item_read(k % kItems));
   return item.at >= 0;
@@ -204,7 +204,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
   const uint32_t tm_o = tmem + X * D, tm_s = tmem + L::kS + X * kKeys, tm_p = tmem + L::kP + X * L::kPStep;
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase) {
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p));
     return ok;
   };
   auto issue_s = [&](int slot) {
@@ -226,7 +226,7 @@ __device__ __forceinline__ void issue(const Params& p, uint32_t s_base, uint32_t
   for (int k = 0; ok; ++k) {
     Item got{};
     bool more = false;
-    if (__all_sync(0xffffffffu, mbar_wait(bars.item(k % kItems), (k / kItems) & 1, p.status))) {
+    if (__all_sync(0xffffffffu, mbar_wait(bars.item(k % kItems), (k / kItems) & 1, p))) {
       got = items[k % kItems];
       __syncwarp();
       if (elected()) mbar_arrive(bars.item_read(k % kItems));
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           item.head = SPLIT ? w / p.splits % p.Hkv : w % p.Hkv;
           item.split = SPLIT ? w % p.splits : 0;
         }
-        if (k >= kItems) ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read(k % kItems), (k / kItems - 1) & 1, p.status));
+        if (k >= kItems) ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read(k % kItems), (k / kItems - 1) & 1, p));
         if (ok && lane == 0) {
           items[k % kItems] = item;
           mbar_arrive(bars.item(k % kItems));
@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Rows past the sequence's end hold another sequence's values, or none: P is 0 there, but 0
         // times an infinity or NaN would spoil O.
         const int slot = clear_at % L::kSlots;
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(slot), (tail_phase >> slot) & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(slot), (tail_phase >> slot) & 1, p));
         tail_phase ^= 1u << slot;
         uint8_t* v = smem + L::kRing + slot * L::kTile;
         const int per = (kKeys - clear_row) * 8;
@@ -420,14 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // each slot: the last V of a short item may still be on its way when the next item's is copied.)
       uint32_t tail_phase = 0, to_tail = 0;
       Item item;
-      for (int k = 0; ok && next_item(bars, items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item(bars, items, k, item, p); ++k) {
         const Work<SPLIT> work(p, item);
         const int n = work.n;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const Tile tile = x ? work.b : work.a;
           if (!ok || tile.n == 0) continue;
-          if (q_uses[x] > 0 && !(ok = mbar_wait(bars.q_free(x), (q_uses[x] - 1) & 1, p.status))) continue;
+          if (q_uses[x] > 0 && !(ok = mbar_wait(bars.q_free(x), (q_uses[x] - 1) & 1, p))) continue;
           mbar_arrive_expect_tx(bars.q(x), static_cast<uint32_t>(128 * (D / 64) * p.G * p.q_per_tile));
           for (int kb = 0; kb < D / 64; ++kb)
             tma_load_3d(s_base + x * L::kTile + kb * L::kBlock, &tm_q, bars.q(x), kb * 64, item.head * p.G,
@@ -437,7 +437,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool tail = work.tail(item);
         for (int i = 0; ok && i < 2 * n; ++i, ++entry) {      // K_0, V_0, K_1, V_1, ...
           const int slot = entry % L::kSlots;
-          if (entry >= L::kSlots && !(ok = mbar_wait(bars.empty(slot), (entry / L::kSlots - 1) & 1, p.status))) break;
+          if (entry >= L::kSlots && !(ok = mbar_wait(bars.empty(slot), (entry / L::kSlots - 1) & 1, p))) break;
           uint32_t bar = bars.full(slot);
           to_tail &= ~(1u << slot);
           if (tail && i == 2 * n - 1) {
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = true;
     for (int k = 0; ok && more; ++k) {
       Item item{};
-      more = __all_sync(0xffffffffu, next_item(bars, items, k, item, p.status));
+      more = __all_sync(0xffffffffu, next_item(bars, items, k, item, p));
       int first = 0;
       Tile tile;
       if (SPLIT) {
@@ -504,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int j = -1; j < nx; ++j) {
         if (j >= 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.s(x), steps & 1, p));
           if (!ok) break;
           tc_fence_after();
           const int left = key_lim - first - j * kKeys;  // keys of the tile that the row sees
@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (j > 0) {
               // P_{j-1} V_{j-1} has to be in O before O is rescaled, and P_{j-1} read before P_j
-              ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p.status));
+              ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), (steps - 1) & 1, p));
               if (!ok) break;
               tc_fence_after();
               if (__any_sync(0xffffffffu, need)) prefill::rescale_o<D>(tm_o, alpha);
@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (pending && (j == 0 || nx == 0 || !__all_sync(0xffffffffu, mbar_test_wait(bars.s(x), steps & 1)))) {
           pending = false;
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), out_step & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.pv(x), out_step & 1, p));
           if (!ok) break;
           tc_fence_after();
           const float inv = out_l > 0.f ? 1.f / out_l : 0.f;
@@ -880,6 +880,7 @@ extern "C" int fa_prefill_packed(const fa_packed_args* a, void* stream) {
   memcpy(p.out_strides, a->out_strides, sizeof p.out_strides);
   p.lse = a->lse;
   p.status = status;
+  p.wait_ns = packed::wait_limit(a->total_q, a->total_k, p.q_per_tile);
   p.splits = splits;
   if (splits > 1) {
     uint8_t* ws = static_cast<uint8_t*>(a->workspace);

@@ -30,7 +30,22 @@ struct Params {
   float* o_part;
   float* lse_part;
   uint32_t* status;
+  uint64_t wait_ns;      // see mbar_wait below
 };
+
+// Waits of these kernels.  Some last as long as a work item: for its last tile, or until the next one is
+// asked for.  An item walks over all of a sequence's tiles, so with the longest sequences it takes seconds (a query
+// tile over 400,000,000 keys: 3), and the limit grows with the tiles that there can be: 20 us each, where one takes
+// 1 to 3.
+using fa::mbar_wait;
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const Params& p) {
+  return fa::mbar_wait(bar, parity, p.status, p.wait_ns);
+}
+
+inline uint64_t wait_limit(int total_q, int total_k, int q_per_tile) {
+  const uint64_t q = static_cast<uint64_t>(total_q) / q_per_tile, k = static_cast<uint64_t>(total_k) / kKeys;
+  return kWaitLimitNs + 20000 * (q > k ? q : k);
+}
 
 // One sequence: its first rows and lengths.
 struct Seq {
@@ -174,9 +189,9 @@ __device__ __forceinline__ int uniform(int v) { return __reduce_max_sync(0xfffff
 
 // Waits of a whole warp for two barriers.  A look at a barrier takes some 150 clocks even when it has come
 // true: both looks are on their way together.
-__device__ __forceinline__ bool warp_wait(uint32_t a, int phase_a, uint32_t b, int phase_b, uint32_t* status) {
+__device__ __forceinline__ bool warp_wait(uint32_t a, int phase_a, uint32_t b, int phase_b, const Params& p) {
   const bool first = mbar_test_wait(a, phase_a & 1), second = mbar_test_wait(b, phase_b & 1);
-  return __all_sync(0xffffffffu, (first || mbar_wait(a, phase_a & 1, status)) && (second || mbar_wait(b, phase_b & 1, status)));
+  return __all_sync(0xffffffffu, (first || mbar_wait(a, phase_a & 1, p)) && (second || mbar_wait(b, phase_b & 1, p)));
 }
 
 // True in one lane of the warp, always the same.  (An election, not a lane's number: the compiler then

@@ -411,8 +411,8 @@ constexpr int kItems = 4;
 // The k-th item, copied from its place (of PLACES) in shared memory; false: no more, or a wait ran out.
 template <int PLACES>
 __device__ __forceinline__ bool next_item(uint32_t bar_item, uint32_t bar_item_read, const Item* items, int k, Item& item,
-                                          uint32_t* status) {
-  if (!mbar_wait(bar_item + 8u * (k % PLACES), (k / PLACES) & 1, status)) return false;
+                                          const Params& p) {
+  if (!mbar_wait(bar_item + 8u * (k % PLACES), (k / PLACES) & 1, p)) return false;
   item = items[k % PLACES];
   mbar_arrive(bar_item_read + 8u * (k % PLACES));
   return item.at >= 0;
@@ -421,8 +421,8 @@ __device__ __forceinline__ bool next_item(uint32_t bar_item, uint32_t bar_item_r
 // The same by a whole issuing warp, one arrival for all lanes.
 template <int PLACES>
 __device__ __forceinline__ bool next_item_warp(uint32_t bar_item, uint32_t bar_item_read, const Item* items, int k,
-                                               Item& item, uint32_t* status) {
-  if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8u * (k % PLACES), (k / PLACES) & 1, status))) return false;
+                                               Item& item, const Params& p) {
+  if (!__all_sync(0xffffffffu, mbar_wait(bar_item + 8u * (k % PLACES), (k / PLACES) & 1, p))) return false;
   item = items[k % PLACES];
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(bar_item_read + 8u * (k % PLACES));
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (!BF16) item.value = largest_seen<D>(gp, item);
         }
         if (k >= kDqItems)
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kDqItems), (k / kDqItems - 1) & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kDqItems), (k / kDqItems - 1) & 1, p));
         if (ok && lane == 0) {
           items[k % kDqItems] = item;
           mbar_arrive(bars.item() + 8u * (k % kDqItems));
@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok && clear_at >= 0) {
         // K rows past the sequence's end: dS is 0 there, but 0 times an infinity or NaN is not
         const int slot = clear_at % L::kKeep;
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p));
         ++tails;
         if (ok) clear_rows<D>(smem + L::kK + slot * L::kTile, clear_row, lane, 32);
         fence_proxy_async_smem();
@@ -669,10 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tile = 0, uses = 0, tails = 0;  // key tiles; items with any; K tiles that land on the tail's barrier
       int tail_at = -1, k_only = -1;
       Item item;
-      for (int k = 0; ok && next_item<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item<kDqItems>(bars.item(), bars.item_read(), items, k, item, p); ++k) {
         const int n = key_tiles(p, item.seq, item.at);
         if (n == 0) continue;
-        if (uses > 0 && !(ok = mbar_wait(bars.q_free(), (uses - 1) & 1, p.status))) break;
+        if (uses > 0 && !(ok = mbar_wait(bars.q_free(), (uses - 1) & 1, p))) break;
         ++uses;
         mbar_arrive_expect_tx(bars.q(), static_cast<uint32_t>(2 * 128 * (D / 64) * p.G * p.q_per_tile));
         for (int kb = 0; kb < D / 64; ++kb) {
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool tail = n * kKeys > item.seq.nk;  // the last K tile reaches past the sequence
         for (int j = 0; j < n; ++j, ++tile) {
           const int kp = tile % L::kKeep, vp = tile % L::kPass;
-          if (tile >= L::kKeep && !(ok = mbar_wait(bars.k_empty(kp), (tile / L::kKeep - 1) & 1, p.status))) break;
+          if (tile >= L::kKeep && !(ok = mbar_wait(bars.k_empty(kp), (tile / L::kKeep - 1) & 1, p))) break;
           uint32_t bar = bars.k_full(kp);
           if (tail && j == n - 1) {
             bar = bars.tail();
@@ -693,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kb = 0; kb < D / 64; ++kb)
             tma_load_3d(s_base + L::kK + kp * L::kTile + kb * kBlock, &tm_k, bar, kb * 64, item.head, item.seq.k0 + j * kKeys);
           k_only = tile;
-          if (tile >= L::kPass && !(ok = mbar_wait(bars.v_empty(vp), (tile / L::kPass - 1) & 1, p.status))) break;
+          if (tile >= L::kPass && !(ok = mbar_wait(bars.v_empty(vp), (tile / L::kPass - 1) & 1, p))) break;
           mbar_arrive_expect_tx(bars.v_full(vp), L::kTile);
           for (int kb = 0; kb < D / 64; ++kb)
             tma_load_3d(s_base + L::kV + vp * L::kTile + kb * kBlock, &tm_v, bars.v_full(vp), kb * 64, item.head,
@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = static_cast<uint32_t>(uniform(static_cast<int>(tmem)));
     bool ok = true;
     auto wait = [&](uint32_t bar, int phase) {
-      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p));
       return ok;
     };
     Place<L::kKeep> kp;
@@ -730,13 +730,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = sdesc_sw128(s_base + L::kQ, 16, 1024), do_desc = sdesc_sw128(s_base + L::kDo, 16, 1024);
       const uint64_t k_desc = sdesc_sw128(s_base + L::kK, 16, 1024), v_desc = sdesc_sw128(s_base + L::kV, 16, 1024);
       Place<L::kPass> vp;
-      for (int k = 0; ok && next_item_warp<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item_warp<kDqItems>(bars.item(), bars.item_read(), items, k, item, p); ++k) {
         const int n = uniform(key_tiles(p, item.seq, item.at));
         if (n == 0) continue;
         if (!wait(bars.q(), uses++)) break;
         for (int j = 0; j < n; ++j, ++step) {
           ok = step == 0 ? wait(bars.k_full(kp.slot), kp.lap)
-                         : warp_wait(bars.k_full(kp.slot), kp.lap, bars.s_read(), step - 1, p.status);
+                         : warp_wait(bars.k_full(kp.slot), kp.lap, bars.s_read(), step - 1, p);
           if (!ok) break;
           tc_fence_after();
           if (elected()) {
@@ -745,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
           ok = step == 0 ? wait(bars.v_full(vp.slot), vp.lap)
-                         : warp_wait(bars.v_full(vp.slot), vp.lap, bars.dp_read(), step - 1, p.status);
+                         : warp_wait(bars.v_full(vp.slot), vp.lap, bars.dp_read(), step - 1, p);
           if (!ok) break;
           tc_fence_after();
           if (elected()) {
@@ -762,14 +762,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       constexpr uint32_t idesc = idesc_f16(BF16, kRows, D, false, true);
       const uint64_t k_desc = sdesc_sw128(s_base + L::kK, kBlock, 1024);
-      for (int k = 0; ok && next_item_warp<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item_warp<kDqItems>(bars.item(), bars.item_read(), items, k, item, p); ++k) {
         const int n = uniform(key_tiles(p, item.seq, item.at));
         if (n == 0) continue;
         // dQ of the item before has to be read before the first product overwrites it
         if (uses > 0 && !wait(bars.o_free(), uses - 1)) break;
         ++uses;
         for (int j = 0; j < n; ++j, ++step) {
-          ok = warp_wait(bars.k_full(kp.slot), kp.lap, bars.ds(step & 1), step / 2, p.status);
+          ok = warp_wait(bars.k_full(kp.slot), kp.lap, bars.ds(step & 1), step / 2, p);
           if (!ok) break;
           tc_fence_after();
           if (elected()) {
@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool more = true;
     for (int k = 0; ok && more; ++k) {
       Item item{};
-      more = __all_sync(0xffffffffu, next_item<kDqItems>(bars.item(), bars.item_read(), items, k, item, p.status));
+      more = __all_sync(0xffffffffu, next_item<kDqItems>(bars.item(), bars.item_read(), items, k, item, p));
       const int n = more ? key_tiles(p, item.seq, item.at) : 0;
       const int i = item.at + row_token, h = item.head * p.G + row_head;
       const bool valid = more && r < p.G * p.q_per_tile && i < item.seq.nq;
@@ -822,8 +822,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = -1; j < n; ++j) {
         if (j >= 0) {
           // S_step; and dS_{step-2} read, before dS_step takes its place
-          ok = step < 2 ? __all_sync(0xffffffffu, mbar_wait(bars.s(), step & 1, p.status))
-                        : warp_wait(bars.dq(step & 1), step / 2 - 1, bars.s(), step, p.status);
+          ok = step < 2 ? __all_sync(0xffffffffu, mbar_wait(bars.s(), step & 1, p))
+                        : warp_wait(bars.dq(step & 1), step / 2 - 1, bars.s(), step, p);
           if (!ok) break;
           tc_fence_after();
           const int left = key_lim - (j * kKeys + w * kHalf);  // columns that the row sees
@@ -842,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     __uint_as_float(raw[c / 16][(2 * c) % 32 + 1])), a2, nl2);
             x[c] = make_float2(exp2_approx(t.x), exp2_approx(t.y));
           }
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.dp(), step & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.dp(), step & 1, p));
           if (!ok) break;
           tc_fence_after();
           uint32_t dp[2][32], ds[32];
@@ -876,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (pending && (j == 0 || n == 0 || !__all_sync(0xffffffffu, mbar_test_wait(bars.s(), step & 1)))) {
           pending = false;
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.dq(out_step & 1), (out_step / 2) & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.dq(out_step & 1), (out_step / 2) & 1, p));
           if (!ok) break;
           tc_fence_after();
           uint32_t o[D / 64][32];
@@ -988,13 +988,13 @@ __device__ __forceinline__ void issue_pair(const Params& p, uint32_t s_base, uin
   const uint32_t tm1 = tmem + (X ? L::kDp : L::kS), tm2 = tmem + (X ? L::kDk : L::kDv), tm_a = tmem + (X ? L::kDs : L::kP);
   bool ok = true;
   auto wait = [&](uint32_t bar, int phase) {
-    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p.status));
+    ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, phase & 1, p));
     return ok;
   };
   Place<L::kSlots> q;  // of the tile's Q; its dO is the next
   int step = 0, uses = 0;
   Item item;
-  for (int k = 0; ok && next_item_warp<kItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+  for (int k = 0; ok && next_item_warp<kItems>(bars.item(), bars.item_read(), items, k, item, p); ++k) {
     int first_tile;
     const int n = uniform(query_tiles(p, item.seq, item.at, first_tile));
     if (n == 0) continue;
@@ -1126,7 +1126,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto publish = [&](int k, const Item& item) {
       if (k >= kItems)
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kItems), (k / kItems - 1) & 1, p.status));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.item_read() + 8u * (k % kItems), (k / kItems - 1) & 1, p));
       if (ok && lane == 0) {
         items[k % kItems] = item;
         mbar_arrive(bars.item() + 8u * (k % kItems));
@@ -1178,7 +1178,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) nd[e] *= -kUnpower * power;
         if (step >= 2)
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.rows_read(step & 1), (step / 2 - 1) & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.rows_read(step & 1), (step / 2 - 1) & 1, p));
         float* to = reinterpret_cast<float*>(smem + L::kRowData) + (step & 1) * 2 * kRows + lane * 4;
         if (ok) {
           *reinterpret_cast<float4*>(to) = make_float4(nl[0], nl[1], nl[2], nl[3]);
@@ -1188,7 +1188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (ok && i == n - 1 && last_rows < used) {
           // query rows past the sequence's end, which the sums over rows must not see
-          ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p.status));
+          ok = __all_sync(0xffffffffu, mbar_wait(bars.tail(), tails & 1, p));
           ++tails;
           for (int x = 0; ok && x < 2; ++x)
             clear_rows<D>(smem + L::kRing + (2 * step + x) % L::kSlots * L::kTile, last_rows, lane, 32);
@@ -1206,11 +1206,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       int entry = 0, uses = 0, tails = 0, tail_at = -1;
       const uint32_t bytes = static_cast<uint32_t>(128 * (D / 64) * used);
       Item item;
-      for (int k = 0; ok && next_item<kItems>(bars.item(), bars.item_read(), items, k, item, p.status); ++k) {
+      for (int k = 0; ok && next_item<kItems>(bars.item(), bars.item_read(), items, k, item, p); ++k) {
         int first_tile;
         const int n = query_tiles(p, item.seq, item.at, first_tile);
         if (n == 0) continue;
-        if (uses > 0 && !(ok = mbar_wait(bars.kv_free(), (uses - 1) & 1, p.status))) break;
+        if (uses > 0 && !(ok = mbar_wait(bars.kv_free(), (uses - 1) & 1, p))) break;
         ++uses;
         mbar_arrive_expect_tx(bars.kv(), 2 * L::kTile);
         for (int kb = 0; kb < D / 64; ++kb) {
@@ -1220,7 +1220,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool tail = (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G < used;
         for (int i = 0; ok && i < 2 * n; ++i, ++entry) {  // Q, dO, Q, dO, ...
           const int slot = entry % L::kSlots, lap = entry / L::kSlots;
-          if (lap > 0 && !(ok = mbar_wait(bars.empty(slot), (lap - 1) & 1, p.status))) break;
+          if (lap > 0 && !(ok = mbar_wait(bars.empty(slot), (lap - 1) & 1, p))) break;
           const bool in_tail = tail && i >= 2 * n - 2;
           const uint32_t bar = in_tail ? bars.tail() : bars.full(slot);
           // (the tail's barrier counts one arrival, for both of its copies)
@@ -1263,7 +1263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int step = 0;
     Item item;
-    for (int k = 0; ok && __all_sync(0xffffffffu, next_item<kItems>(bars.item(), bars.item_read(), items, k, item, p.status)); ++k) {
+    for (int k = 0; ok && __all_sync(0xffffffffu, next_item<kItems>(bars.item(), bars.item_read(), items, k, item, p)); ++k) {
       int first_tile;
       const int n = query_tiles(p, item.seq, item.at, first_tile);
       const int key = item.at + r;
@@ -1272,7 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int from = p.causal ? max(0, key - (item.seq.nk - item.seq.nq) - first_tile * p.q_per_tile) * p.G - w * kHalf : 0;
       for (int i = 0; i < n; ++i, ++step, from -= used) {
         const float4* row_data = reinterpret_cast<const float4*>(smem + L::kRowData) + (step & 1) * 64 + w * 16;
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.rows(step & 1), (step / 2) & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.rows(step & 1), (step / 2) & 1, p));
         // (read before S^T is waited for: beside the products, which take all of shared memory's bandwidth,
         // these reads cost 250 clocks)
         float4 nl[16];
@@ -1282,7 +1282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f = reinterpret_cast<const float*>(smem + L::kPowers)[step & 1];
           f2 = make_float2(f * kUnpower, f * kUnpower);
         }
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.first(0), step & 1, p.status));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(bars.first(0), step & 1, p));
         if (!ok) break;
         tc_fence_after();
         const bool whole = !p.causal || __all_sync(0xffffffffu, from <= 0);
@@ -1313,7 +1313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bars.packed(0));
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.first(1), step & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.first(1), step & 1, p));
         if (!ok) break;
         tc_fence_after();
         uint32_t dp[2][32], ds[32];
@@ -1341,7 +1341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bars.packed(1));
       }
       if (ok && n > 0) {
-        ok = __all_sync(0xffffffffu, mbar_wait(bars.second(w), (step - 1) & 1, p.status));
+        ok = __all_sync(0xffffffffu, mbar_wait(bars.second(w), (step - 1) & 1, p));
         tc_fence_after();
       }
       if (!ok) break;
@@ -1485,6 +1485,7 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   p.scale = a->scale;
   p.scale_log2 = a->scale * prefill::kLog2e;
   p.status = status;
+  p.wait_ns = packed::wait_limit(a->total_q, a->total_k, p.q_per_tile);
   g.dout = a->dout;
   g.o = a->out;
   g.lse = a->lse;

@@ -52,6 +52,25 @@ def test_backward_of_a_context_past_the_product_with_the_group(causal):
             ref.check(f"{name} of period {i}", got[at], value / reps, 2 * bound / reps)
 
 
+def test_a_work_item_of_seconds():
+    """One query over 400,000,007 keys, unsplit: the waits for its last tile are longer than those of a pipeline that has
+    stopped.  All scores are 0 but the last 128, of about 40 each: they alone count, as e^-40 x 4e8 is 1.7e-9."""
+    D, n = 64, 400_000_007
+    g = torch.Generator().manual_seed(7)
+    last = (0.625 + 0.02 * torch.randn(128, 1, D, generator=g)).to(BF)
+    kv = torch.zeros(n, 1, D, dtype=BF, device="cuda")
+    kv[-128:] = last.cuda()
+    q = torch.ones(1, 1, D, dtype=BF)
+    cu, cuk = (torch.tensor([0, m], dtype=torch.int32, device="cuda") for m in (1, n))
+    out, lse = fa.fa_prefill_packed(q.cuda(), kv, kv, cu, cuk, scale=1.0, num_splits=1)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == fa.FA_OK, fa.fa_last_error()
+    want = ref.attention(q, last, last, False, 1.0)
+    for name, got in (("out", out), ("lse", lse)):
+        value, bound = want[name]
+        ref.check(name, got, value, bound + 2e-9)
+
+
 # ------------------------------------------------------------------ broken offsets
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("offsets,first,end", [
