@@ -789,6 +789,13 @@ int check_sizes(const char* who, int B, int Hq, int Hkv, int D, int total_q, int
   return FA_OK;
 }
 
+int check_offsets(const char* who, const int32_t* cu_q, const int32_t* cu_k) {
+  if (!cu_q || !cu_k) return fail(FA_ERR_INVALID_ARG, "%s: null cu_seqlens pointer", who);
+  if (((reinterpret_cast<uintptr_t>(cu_q) | reinterpret_cast<uintptr_t>(cu_k)) & 3u) != 0)
+    return fail(FA_ERR_INVALID_ARG, "%s: misaligned cu_seqlens pointer", who);
+  return FA_OK;
+}
+
 int check_tensor(const char* who, const char* name, const void* base, const int64_t* strides, int tokens, int heads,
                  int D) {
   char msg[200];
@@ -843,8 +850,8 @@ extern "C" int fa_prefill_packed(const fa_packed_args* a, void* stream) {
   if (a->num_splits > 1 && packed::most_items(a->total_q, a->B, 2 * (packed::kRows / (a->Hq / a->Hkv))) * a->Hkv *
                                    a->num_splits > (1LL << 30))
     return set_error(FA_ERR_UNSUPPORTED, "fa_prefill_packed: too many tiles for that many parts");
-  if (!a->cu_seqlens_q || !a->cu_seqlens_k)
-    return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed: null cu_seqlens pointer");
+  if ((rc = packed::check_offsets(who, a->cu_seqlens_q, a->cu_seqlens_k)) != FA_OK) return rc;
+  if ((reinterpret_cast<uintptr_t>(a->lse) & 3u) != 0) return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed: misaligned lse");
   if ((rc = packed::check_tensor(who, "q", a->q, a->q_strides, a->total_q, a->Hq, a->D)) != FA_OK) return rc;
   if ((rc = packed::check_tensor(who, "out", a->out, a->out_strides, a->total_q, a->Hq, a->D)) != FA_OK) return rc;
   if (a->total_k > 0 &&

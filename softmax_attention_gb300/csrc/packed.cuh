@@ -210,6 +210,7 @@ inline int64_t most_items(int64_t total, int64_t B, int64_t width) {
 // Host: the checks that the calls share (argument struct fields as in fa.h).
 int check_sizes(const char* who, int B, int Hq, int Hkv, int D, int total_q, int total_k, fa_dtype dtype,
                 float scale);
+int check_offsets(const char* who, const int32_t* cu_q, const int32_t* cu_k);
 // A [tokens, heads, D] tensor's address and strides (token, head; elements), for 16-byte accesses.
 int check_tensor(const char* who, const char* name, const void* base, const int64_t* strides, int tokens,
                  int heads, int D);

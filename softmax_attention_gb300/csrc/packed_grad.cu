@@ -1444,8 +1444,7 @@ int fa_prefill_packed_backward(const fa_packed_backward_args* a, void* stream) {
   if (!a) return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed_backward: null argument struct");
   int rc = packed::check_sizes(who, a->B, a->Hq, a->Hkv, a->D, a->total_q, a->total_k, a->dtype, a->scale);
   if (rc != FA_OK || a->B == 0 || a->total_q + static_cast<int64_t>(a->total_k) == 0) return rc;
-  if (!a->cu_seqlens_q || !a->cu_seqlens_k)
-    return set_error(FA_ERR_INVALID_ARG, "fa_prefill_packed_backward: null cu_seqlens pointer");
+  if ((rc = packed::check_offsets(who, a->cu_seqlens_q, a->cu_seqlens_k)) != FA_OK) return rc;
   const struct {
     const char* name;
     const void* base;
