@@ -1268,7 +1268,8 @@ def fa_prefill_packed(q, k, v, cu_seqlens_q, cu_seqlens_k=None, *, causal: bool 
                   _flat(dev, torch.float32, rows, "lse", lse), *strides,
                   *_strided(dev, dtype, qs, "out", out), *fields, num_splits)
         a = _pack_packed(*fields, 0, 0)
-        # (keys of fewer than 2048 a sequence are in parts only where the caller asks for it)
+        # (keys of fewer than 2048 a sequence are in parts only where the caller asks for it: twice the eight tiles of
+        # 128 keys that a part of the library's own choice has at least)
         if num_splits > 1 or (num_splits == 0 and ks[0] >= 2048 * (len(cu_seqlens_q) - 1)):
             need = lib.fa_packed_workspace_size(a)
             if need:

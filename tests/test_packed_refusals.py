@@ -1,5 +1,6 @@
 """Packed prompts without a device: pointers that no access may have, and the plan that the binding counts on."""
 import ctypes
+import random
 
 import pytest
 
@@ -17,3 +18,17 @@ def test_misaligned(lib, name, make, field, off):  # noqa: F811
     """Offsets and lse are read and written four bytes at a time."""
     assert getattr(lib, name)(ctypes.byref(make(**{field: P + off})), None) == INV
     assert b"align" in lib.fa_last_error()
+
+
+def test_parts_only_where_the_binding_looks_for_them(lib):  # noqa: F811
+    """The binding asks for a workspace by itself only where the keys are 2048 a sequence or more: the plan has parts nowhere else."""
+    rng = random.Random(5)
+    parts = 0
+    for _ in range(20000):
+        Hkv, B = rng.choice([1, 2, 4, 8]), int(2 ** rng.uniform(0, 10))
+        kw = dict(B=B, Hkv=Hkv, Hq=Hkv * rng.choice([1, 2, 3, 8, 16, 128]), D=rng.choice([64, 128]),
+                  total_q=int(2 ** rng.uniform(0, 17)), total_k=rng.choice([2048 * B - 1, 2048 * B, int(2 ** rng.uniform(0, 21))]))
+        need = lib.fa_packed_workspace_size(ctypes.byref(_packed(num_splits=0, **kw)))
+        assert need == 0 or kw["total_k"] >= 2048 * B, kw
+        parts += need > 0
+    assert parts > 1000
