@@ -22,15 +22,16 @@
 //
 // The softmax works on a row 32 scores at a time against the maximum so far (of the first 32 scores
 // to begin with), and looks for a larger one on the way; only if a row's maximum turns out to be more
-// than 2^8 times larger is the tile done again in two passes.  So no more than 64 scores and the 64
+// than 2^8 times larger is the tile done again in two passes (scores of standard deviation 1: hardly ever; of 2, 4 and 8:
+// a 16K-token prompt takes 760, 1190 and 1298 us for 638).  So no more than 64 scores and the 64
 // registers of packed P are held, and the maximum is not in the way of the first exponential.
 //
 // A block stays for all of its work items: while one ends, the copies and the first scores of the
 // next are under way, so that only its first item pays for set-up and an empty pipe (packed.cuh
 // says how the items are dealt out).
 //
-// Bound by the tensor cores: that prompt takes 620 to 660 us, from board to board (1670 to 1770 TFLOP/s of its
-// unmasked half, 0.87 to 0.92 of the measured bf16 rate), three quarters of all clocks with a product in the pipe and
+// Bound by the tensor cores: that prompt takes 616 to 671 us, from board to board (1640 to 1790 TFLOP/s of its
+// unmasked half, 0.85 to 0.92 of the measured bf16 rate), three quarters of all clocks with a product in the pipe and
 // the exponentials' pipe busy in 38 % (counters of four sequences of 8192 tokens).  At D = 64 by the softmax instead,
 // which is the same per score for half the products (four sequences of 4096 tokens: 150 us, 920 TFLOP/s).  Short
 // sequences pay some 3.5 us a work item for its first and last tiles (512 to 2048 tokens: 180 us, 1100 TFLOP/s).

@@ -7,7 +7,7 @@
 // Three kernels; the sums that a block owns stay in tensor memory, so that nothing is added by atomics
 // and the same call gives the same bits:
 //   - row_kernel: delta and -lse, in the form that the others use them, a pass over dout and out (and, of rows that see
-//     few keys, the products themselves);
+//     few keys, the products themselves; fp16: what bounds dP, with a pass over v);
 //   - dkv_kernel: a block holds a tile of 128 keys and walks over the query tiles that see it, all
 //     heads of the group: S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  With the
 //     products turned, P^T and dS^T have keys as rows and go back to tensor memory as the
@@ -17,7 +17,8 @@
 // S and dP are computed in both, seven products for the five of a form that adds dq by atomics.
 //
 // Bound by the tensor cores where sequences are long: 8192 tokens of 16 heads in 4 groups (bf16, D = 128, causal) take
-// 555 us, 1240 TFLOP/s counting five products and 1740 counting the seven, 0.90 of the measured bf16 rate.
+// 555 to 590 us, from board to board, 1170 to 1240 TFLOP/s counting five products and 1640 to 1740 counting the seven,
+// 0.85 to 0.90 of the measured bf16 rate.
 // Samples of 512 to 2048 tokens: 380 us (850 and 1190); there a work item's first tile, which waits for its loads
 // and meets an empty pipe, costs some 3 us of the 7 to 20 that the item takes, and shared memory has no room to
 // hold the next item's Q and dO (K and V) beside this one's.  (Loading them to L2 ahead of time: no change.)
@@ -165,7 +166,8 @@ unsigned row_blocks(int total_q, int G, int D) {
 // delta is sum_j P_j dP_j / sum_j P_j, from the products themselves; and of a row that sees one key dS is 0,
 // exactly, which dq_kernel sees to for the row and dkv_kernel for a sequence's only key.  (Costs 1 us of 15 for three
 // short samples, 4 of 380 for samples of 512 to 2048 tokens.  Such rows' columns masked out of dS in dkv_kernel's loop:
-// 18 us of 555.  32 keys, two passes: 2 us more for the short ones, and registers that slow the others.)
+// 18 us of 555.  32 keys, two passes: 2 us more for the short ones, and registers that slow the others.  The products
+// share row_kernel's 64 registers, and spill 100 to 192 bytes.)
 constexpr int kFew = 16;
 
 // C (16 x 8, fp32) += A (16 x 16) B (16 x 8).  With g = lane / 4, t = lane % 4: a0 (row g, k 2t..), a1 (g + 8, 2t..),
@@ -394,8 +396,8 @@ __global__ void __launch_bounds__(kRowThreads, 4) row_kernel(const GradParams g)
     }
   }
   if constexpr (!BF16) {
-    // (a maximum a block, and not one for the call by an atomic, which something would have to set to 0 first: a
-    // launch of some 4 us)
+    // (a maximum a block, which the other kernels join as they need it: one of a sequence by an atomic would have to be
+    // set to 0 first, by a launch of some 4 us)
     const float top = block_max(most);
     if (threadIdx.x == 0) g.maxima[static_cast<int64_t>(blockIdx.y) * g.q_blocks + blockIdx.x - few] = top;
   }
