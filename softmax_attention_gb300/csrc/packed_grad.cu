@@ -29,8 +29,8 @@
 // fp16: dS is held times a power of two, f, so that the small values that gradients have keep their
 // bits (its smallest normal number is 2^-14) and the large ones stay below its largest, 65504.  No |dP_ij| passes
 // b_i = sum_d |dout_id| max |v|, and no |dS_ij|, with delta_i a mean of dP_ij over j by P_ij, b_i / 2: f brings b_i to
-// [2^14, 2^15), of the row and the keys that its tile sees in dq_kernel, of the key tile and the largest row that may see it
-// in dkv_kernel, whose sums run over rows; another sequence has no part in either.
+// [2^14, 2^15), of the row and the keys that its tile sees in dq_kernel, of the sequence's keys and the largest row that may see
+// the key tile in dkv_kernel, whose sums run over rows; another sequence has no part in either.
 // (What |dout| alone would give, dS of values of 100 can pass.)  P is held times 2^7 there.  bf16 has fp32's
 // exponents, and f = 1.
 #include <math.h>
@@ -291,7 +291,7 @@ __device__ __forceinline__ float block_max(float v) {
 }
 
 // fp16: the largest finite |v| of each key of a kv head, and of the block.  (With all that the bound takes: three short
-// samples 17.3 us for 16.7 without, 8 of 693 to 2005 tokens 404 for 393.)
+// samples 17.8 us for 16.6 without, 8 of 693 to 2005 tokens 407 for 396.)
 template <int D>
 __device__ __forceinline__ void value_rows(const GradParams& g, int block, int hk) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
@@ -1135,6 +1135,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     float power = 1.f;  // that the item's dS is held times
+    // fp16: the largest |v| of an item's sequence and head, kept for the next item of both: blocks deal out
+    // heads by turns, as a rule two, so that of the item before the last is kept beside the last one's
+    struct Values {
+      int k0, nk, head;
+      float value;
+    } now{0, 0, -1, 0.f}, before{0, 0, -1, 0.f};
     int step = 0, tails = 0;
     int token[4];  // of the tile's, of the lane's rows
 #pragma unroll
@@ -1153,12 +1159,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         look_ahead();
       } else {
         // The item's power goes with the row data and not with the item, so that the first tiles' copies and products do not
-        // wait for it, and what it is found from loads beside the search (three short samples: 18.1 us without that, 17.3 with it).
-        const int64_t key = item.seq.k0 + static_cast<int64_t>(item.at), row = item.seq.q0 + static_cast<int64_t>(first_tile) * p.q_per_tile;
-        auto value = largest_value<D>(gp, item.head, key, n > 0 ? key + min(kKeys, item.seq.nk - item.at) : key);
+        // wait for it, and what it is found from loads beside the search (after it, three short samples took 0.8 us more).
+        // |v| is of all of the sequence's keys, for delta is a mean over them.
+        const int64_t key = item.seq.k0, row = item.seq.q0 + static_cast<int64_t>(first_tile) * p.q_per_tile;
+        const bool known = n == 0 || (now.head == item.head && now.k0 == item.seq.k0 && now.nk == item.seq.nk);
+        auto value = largest_value<D>(gp, item.head, key, known ? key : key + item.seq.nk);
         auto norm = largest_norm<D>(gp, item.head, row * p.G, n > 0 ? (item.seq.q0 + static_cast<int64_t>(item.seq.nq)) * p.G : row * p.G);
         look_ahead();
-        power = power_for(value.get() * norm.get());
+        if (!known) now = {item.seq.k0, item.seq.nk, item.head, value.get()};
+        power = power_for(now.value * norm.get());
+        const Values other = before;
+        before = now;
+        now = other;
       }
       const int last_rows = n > 0 ? (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G : used;
       for (int i = 0; ok && i < n; ++i, ++step) {

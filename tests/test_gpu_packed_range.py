@@ -156,6 +156,27 @@ def test_half_gradient_of_two_keys():
     _check_half(got, q, k, v, do, False, 0.1)
 
 
+@pytest.mark.parametrize("small,large", [(0.01, 1000.0), (0.0, 60000.0), (1.0, 300.0)])
+@pytest.mark.parametrize("D,G,causal", [(64, 2, True), (128, 1, False), (128, 4, True)])
+def test_half_gradients_of_values_that_differ_by_tile(D, G, causal, small, large):
+    """Keys of small values in one tile, of large ones in others: delta, a mean over all of them, is far larger than the
+    dP of the small ones, in their dS too."""
+    L = 500
+    c = Case([L, 40], 2 * G, 2, D, HF, seed=29)
+    c.x[:, :2 * G + 2] *= 2.0 ** -6
+    size = torch.full((c.x.shape[0], 1, 1), large)
+    size[:100], size[200:390] = small, small
+    c.x[:, 2 * G + 2:] = (size * (1 + 0.1 * c.x[:, 2 * G + 2:].float().clamp(-0.9, 0.9))).to(HF)
+    c.do = torch.full_like(c.do, 2.0 ** -6)
+    scale = 1.0 / D
+    q, k, v = c.gpu()
+    out, lse = fa.fa_prefill_packed(q, k, v, *c.offsets(), causal=causal, scale=scale)
+    got = fa.fa_prefill_packed_backward(c.do.cuda(), q, k, v, out, lse, *c.offsets(), causal=causal, scale=scale,
+                                        workspace=_nan_workspace())
+    for a, b in zip(c.cu, c.cu[1:]):
+        _check_half([t[a:b] for t in got], *(t[a:b] for t in c.cpu()), c.do[a:b], causal, scale)
+
+
 # ------------------------------------------------------------------ samples of a pack
 @pytest.mark.parametrize("lens", [[150, 150], [70, 1, 133, 40], [64, 128, 5]])
 @pytest.mark.parametrize("D", [64, 128])
