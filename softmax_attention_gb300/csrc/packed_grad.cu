@@ -291,7 +291,7 @@ __device__ __forceinline__ float block_max(float v) {
 }
 
 // fp16: the largest finite |v| of each key of a kv head, and of the block.  (With all that the bound takes: three short
-// samples 17.8 us for 16.6 without, 8 of 693 to 2005 tokens 407 for 396.)
+// samples 17.6 us for 16.3 without, 8 of 693 to 2005 tokens 407 for 396.)
 template <int D>
 __device__ __forceinline__ void value_rows(const GradParams& g, int block, int hk) {
   constexpr int kLanes = D / 8, kPerPass = kRowThreads / kLanes;
@@ -926,6 +926,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 // given earlier 594, after the commits 602.  At D = 64, where the shapes differ, P^T and dS^T have columns of
 // their own.
 // ------------------------------------------------------------------------------------------
+// fp16: the largest |v| of a sequence and head, kept from one work item to the next of both, by head.  (Found anew by
+// every item: 16 queries of 24 heads in 3 groups over 2^20 keys 7977 us for 6918.)
+struct Values {
+  int k0, nk, head;
+  float value;
+};
+constexpr int kKept = 16;
+
 template <int D>
 struct DkvLayout {
   // Ring of Q and dO tiles by turns.  Q_{i+1} is needed as soon as dK_{i-1}, the last to read Q_{i-1}, is
@@ -940,7 +948,8 @@ struct DkvLayout {
   // No room is left to align the base by hand: the kernel has no static shared memory, and its dynamic
   // one is declared with this alignment.
   static constexpr int kPowers = kShared + static_cast<int>(kItems * sizeof(Item)) + 16;  // fp16: [2], beside the row data
-  static constexpr int kAlloc = kPowers + 2 * 4;
+  static constexpr int kValues = (kPowers + 2 * 4 + 15) / 16 * 16;  // fp16: [kKept]
+  static constexpr int kAlloc = kValues + kKept * 16;
   static constexpr bool kApart = D == 64;
   static constexpr int kDv = 0, kDk = D, kS = 2 * D, kDp = kS + kRows;
   static constexpr int kP = kApart ? kDp + kRows : kS, kDs = kApart ? kP + kRows / 2 : kDp;
@@ -1135,12 +1144,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     float power = 1.f;  // that the item's dS is held times
-    // fp16: the largest |v| of an item's sequence and head, kept for the next item of both: blocks deal out
-    // heads by turns, as a rule two, so that of the item before the last is kept beside the last one's
-    struct Values {
-      int k0, nk, head;
-      float value;
-    } now{0, 0, -1, 0.f}, before{0, 0, -1, 0.f};
+    Values* kept = reinterpret_cast<Values*>(smem + L::kValues);
+    if (!BF16 && lane < kKept) kept[lane].head = -1;
+    __syncwarp();
     int step = 0, tails = 0;
     int token[4];  // of the tile's, of the lane's rows
 #pragma unroll
@@ -1162,15 +1168,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         // wait for it, and what it is found from loads beside the search (after it, three short samples took 0.8 us more).
         // |v| is of all of the sequence's keys, for delta is a mean over them.
         const int64_t key = item.seq.k0, row = item.seq.q0 + static_cast<int64_t>(first_tile) * p.q_per_tile;
+        Values now = kept[item.head % kKept];
         const bool known = n == 0 || (now.head == item.head && now.k0 == item.seq.k0 && now.nk == item.seq.nk);
         auto value = largest_value<D>(gp, item.head, key, known ? key : key + item.seq.nk);
         auto norm = largest_norm<D>(gp, item.head, row * p.G, n > 0 ? (item.seq.q0 + static_cast<int64_t>(item.seq.nq)) * p.G : row * p.G);
         look_ahead();
-        if (!known) now = {item.seq.k0, item.seq.nk, item.head, value.get()};
+        if (!known) {
+          now = {item.seq.k0, item.seq.nk, item.head, value.get()};
+          if (lane == 0) kept[item.head % kKept] = now;
+          __syncwarp();
+        }
         power = power_for(now.value * norm.get());
-        const Values other = before;
-        before = now;
-        now = other;
       }
       const int last_rows = n > 0 ? (item.seq.nq - (first_tile + n - 1) * p.q_per_tile) * p.G : used;
       for (int i = 0; ok && i < n; ++i, ++step) {
